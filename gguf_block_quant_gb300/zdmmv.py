@@ -28,6 +28,9 @@ BLOCK_BYTES = {Q4_0: 18, Q8_0: 34}
 FAULT_WAIT_TIMEOUT = 1
 FAULT_SMEM_ALIGN = 2
 ARGMAX_WORKSPACE_BYTES = 16384
+ROPE_PAIRS = 0
+ROPE_HALVES = 1
+KV_SLAB = 16
 
 STATUS = {0: "ok", 1: "null pointer", 2: "bad shape", 3: "misaligned pointer or stride",
           4: "unknown layout", 5: "unknown block format", 6: "buffer too small",
@@ -46,6 +49,32 @@ _lib = None
 _vp = ctypes.c_void_p
 _i64 = ctypes.c_int64
 _int = ctypes.c_int
+
+
+class _RmsnormArgs(ctypes.Structure):
+    _fields_ = [("x", _vp), ("residual", _vp), ("weight", _vp), ("out", _vp), ("xq", _vp), ("y", _vp),
+                ("rows", _i64), ("cols", _i64), ("x_stride", _i64), ("residual_stride", _i64),
+                ("eps", ctypes.c_float)]
+
+
+class _KvCache(ctypes.Structure):
+    _fields_ = [("pages", _vp), ("page_table", _vp), ("n_pages", _i64)] + [
+        (n, ctypes.c_int32) for n in ("n_seq", "max_pages", "page_tokens", "n_kv_heads", "head_dim")]
+
+
+class _KvAppendArgs(ctypes.Structure):
+    _fields_ = [(n, _vp) for n in ("k", "v", "q", "seq", "pos", "rope", "q_out", "k_val", "v_val", "status_dev")] + [
+        (n, _i64) for n in ("k_stride", "v_stride", "q_stride", "rope_rows")] + [
+        (n, ctypes.c_int32) for n in ("n_tok", "n_q_heads", "rot_dim", "rope_style")]
+
+
+class _AttnArgs(ctypes.Structure):
+    _fields_ = [(n, _vp) for n in ("q", "q_start", "kv_len", "out", "workspace", "status_dev")] + [
+        ("workspace_bytes", ctypes.c_size_t), ("q_stride", _i64)] + [
+        (n, ctypes.c_int32) for n in ("n_tok", "n_q_heads", "max_q_len", "max_kv_len", "window")] + [
+        ("scale", ctypes.c_float)]
+
+
 _SIGS = {
     "zdmmv_status_str": ([_int], ctypes.c_char_p),
     "zdmmv_version": ([], ctypes.c_char_p),
@@ -81,6 +110,11 @@ _SIGS = {
     "zdmmv_selftest_dp4a": ([_vp, _vp, _vp, _vp, _int, _vp], _int),
     "zdmmv_selftest_wait_timeout": ([_vp, _vp], _int),
     "zdmmv_device_status": ([ctypes.POINTER(ctypes.c_uint32), _int], _int),
+    "zdmmv_add_rmsnorm_q8_0": ([ctypes.POINTER(_RmsnormArgs), _vp], _int),
+    "zdmmv_kv_page_bytes": ([_int, _int, _int], ctypes.c_size_t),
+    "zdmmv_kv_append_q4_0": ([ctypes.POINTER(_KvCache), ctypes.POINTER(_KvAppendArgs), _vp], _int),
+    "zdmmv_attn_q4_0_workspace_bytes": ([ctypes.POINTER(_KvCache), _int, _int, _int], ctypes.c_size_t),
+    "zdmmv_attn_q4_0": ([ctypes.POINTER(_KvCache), ctypes.POINTER(_AttnArgs), _vp], _int),
 }
 
 
@@ -371,3 +405,155 @@ def device_status(clear: bool = False) -> int:
     v = ctypes.c_uint32(0)
     _call("zdmmv_device_status", ctypes.byref(v), 1 if clear else 0)
     return int(v.value)
+
+
+# ------------------------------------------- the attention half of a decode layer
+def _check(ok: bool, what: str):
+    if not ok:
+        raise ValueError(what)
+
+
+def _rows_of(t: torch.Tensor, width: int, what: str) -> int:
+    """Data pointer of fp32 rows of `width` values; any even distance between rows (view the
+    token's heads as one row or as [heads][head_dim]), the values of a row side by side."""
+    _check(t.is_cuda and t.dtype == torch.float32, f"{what}: expected a float32 CUDA tensor")
+    n = t.dim()
+    _check(n >= 2 and t.stride(n - 1) == 1 and t[0].is_contiguous() if t.shape[0] else n >= 2,
+           f"{what}: the values of a row have to lie side by side")
+    _check(t.shape[0] == 0 or t[0].numel() == width, f"{what}: rows of {width} values expected")
+    return t.data_ptr()
+
+
+def _stride_of(t: torch.Tensor, width: int) -> int:
+    """Floats between rows (a single row's distance to nothing is its width)."""
+    return t.stride(0) if t.shape[0] > 1 else width
+
+
+def _i32(t: torch.Tensor, n: int, what: str) -> int:
+    _check(t.dtype == torch.int32 and t.numel() >= n, f"{what}: expected int32 [{n}]")
+    return _ptr(t)
+
+
+def _make(shape, dtype, device, stream):
+    """An empty tensor for a call on `stream`: of that stream's memory, so that it is not
+    handed out again while the call may still be using it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def add_rmsnorm_q8_0(x, weight, eps: float, residual=None, out=None, xq=None, y=None, stream=None):
+    """s = x + residual; the Q8_0 blocks (uint8 tensor, returned) of s / sqrt(mean(s^2) + eps) * weight, per row of
+    x (fp32 [rows][cols]; rows may be strided). out: s (may be x or residual); y: fp16, the blocks' values."""
+    _check(x.dim() == 2, "add_rmsnorm_q8_0: x must be [rows][cols]")
+    rows, cols = x.shape
+    a = _RmsnormArgs(x=_rows_of(x, cols, "x"), rows=rows, cols=cols, x_stride=_stride_of(x, cols), eps=eps)
+    if residual is not None:
+        _check(residual.shape == x.shape, "add_rmsnorm_q8_0: residual must have x's shape")
+        a.residual, a.residual_stride = _rows_of(residual, cols, "residual"), _stride_of(residual, cols)
+    if weight is not None:
+        _check(weight.dtype == torch.float32 and weight.numel() == cols, "add_rmsnorm_q8_0: weight must be float32 [cols]")
+        a.weight = _ptr(weight)
+    if out is not None:
+        _check(out.dtype == torch.float32 and out.numel() == rows * cols, "add_rmsnorm_q8_0: out must be float32 [rows][cols]")
+        a.out = _ptr(out)
+    if xq is None:
+        xq = _make(rows * (cols // QK) * 34, torch.uint8, x.device, stream)
+    _check(_nbytes(xq) >= rows * (cols // QK) * 34, "add_rmsnorm_q8_0: xq too small")
+    a.xq = _ptr(xq)
+    if y is not None:
+        _check(y.dtype == torch.float16 and y.numel() == rows * cols, "add_rmsnorm_q8_0: y must be float16 [rows][cols]")
+        a.y = _ptr(y)
+    _call("zdmmv_add_rmsnorm_q8_0", ctypes.byref(a), _stream(stream))
+    return xq
+
+
+def kv_page_bytes(page_tokens: int, n_kv_heads: int, head_dim: int) -> int:
+    return int(lib().zdmmv_kv_page_bytes(page_tokens, n_kv_heads, head_dim))
+
+
+class KVCache:
+    """A paged key/value cache in Q4_0 (zdmmv_kv_cache): `pages` is a uint8 tensor of whole pages (see
+    kv_page_bytes), `page_table` int32 [sequences][pages of a sequence]. Both stay the caller's: the table's
+    contents may change between calls."""
+
+    def __init__(self, pages, page_tokens: int, n_kv_heads: int, head_dim: int, page_table):
+        per = kv_page_bytes(page_tokens, n_kv_heads, head_dim)
+        _check(per > 0, "KVCache: page_tokens must be a multiple of 16 up to 1024, head_dim 64, 96, 128, 192 or 256")
+        _check(page_table.dim() == 2 and page_table.dtype == torch.int32, "KVCache: page_table must be int32 [n_seq][max_pages]")
+        _check(pages.dtype == torch.uint8, "KVCache: pages must be uint8")
+        self.pages, self.page_table = pages, page_table
+        self.page_tokens, self.n_kv_heads, self.head_dim = page_tokens, n_kv_heads, head_dim
+        self.n_pages, (self.n_seq, self.max_pages) = _nbytes(pages) // per, page_table.shape
+        self.c = _KvCache(_ptr(pages), _ptr(page_table), self.n_pages, self.n_seq, self.max_pages, page_tokens,
+                          n_kv_heads, head_dim)
+
+
+def kv_append_q4_0(cache: KVCache, k, v, seq, pos, q=None, q_out=None, rope=None, rope_style: int = ROPE_HALVES,
+                   k_val=None, v_val=None, status=None, stream=None):
+    """Append tokens (fp32 k and v, [n_tok][heads * head_dim] or [n_tok][heads][head_dim], tokens may be strided) to
+    their sequences' pages, rotated by rope (fp32 [positions][rot_dim]: cosines, then sines) and quantized to Q4_0.
+    With q, returns it rotated (q_out). k_val, v_val: fp16, the values the cache then holds."""
+    n_tok, dim = k.shape[0], cache.head_dim
+    kv = cache.n_kv_heads * dim
+    _check(v.shape[0] == n_tok, "kv_append_q4_0: k and v must have the same tokens")
+    a = _KvAppendArgs(k=_rows_of(k, kv, "k"), v=_rows_of(v, kv, "v"), seq=_i32(seq, n_tok, "seq"),
+                      pos=_i32(pos, n_tok, "pos"), k_stride=_stride_of(k, kv), v_stride=_stride_of(v, kv), n_tok=n_tok,
+                      rope_style=rope_style)
+    if q is not None:
+        width = q[0].numel() if n_tok else dim
+        _check(q.shape[0] == n_tok and width % dim == 0, "kv_append_q4_0: q must be [n_tok][heads * head_dim]")
+        a.q, a.q_stride, a.n_q_heads = _rows_of(q, width, "q"), _stride_of(q, width), width // dim
+        if q_out is None:
+            q_out = _make((n_tok, width // dim, dim), torch.float32, q.device, stream)
+        _check(q_out.dtype == torch.float32 and q_out.numel() == n_tok * width, "kv_append_q4_0: q_out must be float32, q's size")
+        a.q_out = _ptr(q_out)
+    if rope is not None:
+        _check(rope.dim() == 2 and rope.dtype == torch.float32, "kv_append_q4_0: rope must be float32 [positions][rot_dim]")
+        a.rope, (a.rope_rows, a.rot_dim) = _ptr(rope), rope.shape
+    for name, t in (("k_val", k_val), ("v_val", v_val)):
+        if t is not None:
+            _check(t.dtype == torch.float16 and t.numel() == n_tok * kv, f"kv_append_q4_0: {name} must be float16, k's size")
+            setattr(a, name, _ptr(t))
+    if status is not None:
+        a.status_dev = _i32(status, 1, "status")
+    _call("zdmmv_kv_append_q4_0", ctypes.byref(cache.c), ctypes.byref(a), _stream(stream))
+    return q_out
+
+
+def attn_q4_0_workspace_bytes(cache: KVCache, n_q_heads: int, max_q_len: int, max_kv_len: int) -> int:
+    return int(lib().zdmmv_attn_q4_0_workspace_bytes(ctypes.byref(cache.c), n_q_heads, max_q_len, max_kv_len))
+
+
+def attn_q4_0_workspace(cache: KVCache, n_q_heads: int, max_q_len: int, max_kv_len: int):
+    """A workspace for attn_q4_0 calls of these bounds (one call in flight at a time)."""
+    n = attn_q4_0_workspace_bytes(cache, n_q_heads, max_q_len, max_kv_len)
+    return torch.empty(n, dtype=torch.uint8, device=cache.pages.device)
+
+
+def attn_q4_0(cache: KVCache, q, q_start, kv_len, max_q_len: int, max_kv_len: int, scale: float | None = None,
+              window: int = 0, out=None, workspace=None, status=None, stream=None):
+    """Attention of the new tokens q (fp32 [n_tok][heads][head_dim] or [n_tok][heads * head_dim]) over the cache;
+    sequence s has the rows q_start[s] .. q_start[s+1]-1 and kv_len[s] tokens in the cache. scale: default
+    1/sqrt(head_dim). Returns out, fp32 [n_tok][heads][head_dim]."""
+    n_tok, dim = q.shape[0], cache.head_dim
+    width = q[0].numel() if n_tok else dim * cache.n_kv_heads
+    heads = width // dim
+    _check(width % dim == 0, "attn_q4_0: q must be [n_tok][heads * head_dim]")
+    if out is None:
+        out = _make((n_tok, heads, dim), torch.float32, q.device, stream)
+    _check(out.dtype == torch.float32 and out.numel() == n_tok * width, "attn_q4_0: out must be float32, q's size")
+    if workspace is None:
+        workspace = _make(attn_q4_0_workspace_bytes(cache, heads, max_q_len, max_kv_len), torch.uint8, q.device, stream)
+    a = _AttnArgs(q=_rows_of(q, width, "q"), q_start=_i32(q_start, cache.n_seq + 1, "q_start"),
+                  kv_len=_i32(kv_len, cache.n_seq, "kv_len"), out=_ptr(out), workspace=_ptr(workspace),
+                  workspace_bytes=_nbytes(workspace), q_stride=_stride_of(q, width), n_tok=n_tok, n_q_heads=heads,
+                  max_q_len=max_q_len, max_kv_len=max_kv_len, window=window,
+                  scale=dim ** -0.5 if scale is None else scale)
+    if status is not None:
+        a.status_dev = _i32(status, 1, "status")
+    _call("zdmmv_attn_q4_0", ctypes.byref(cache.c), ctypes.byref(a), _stream(stream))
+    return out

@@ -522,6 +522,156 @@ zdmmv_status zdmmv_selftest_wait_timeout(int32_t *result, zdmmv_stream_t stream)
  * has reported a fault. Errors: ERR_NULL, ERR_CUDA. */
 zdmmv_status zdmmv_device_status(uint32_t *bits_out, int clear);
 
+/* ---------------------------------------------------------------------------
+ * The attention half of a decode layer: the operators between the products
+ * (norm, cache append with the position rotation, attention over the cache).
+ * Their arguments are plain structs of pointers and sizes, read on the host
+ * during the call; zero a struct before filling it.
+ * ------------------------------------------------------------------------ */
+
+/* Root-mean-square norm with the residual's addition and a Q8_0 output, per row
+ * of `cols` values:
+ *   s = x + residual                        (s = x where residual is NULL)
+ *   y = (s * (1 / sqrt(sum(s^2) / cols + eps))) * weight
+ *   xq = the Q8_0 blocks of y, as zdmmv_quantize_act_q8_0 forms them
+ * in fp32 throughout, in ONE launch: xq is what the DMMV entry points read. */
+typedef struct {
+    const float *x;          /* device fp32, row r at x + r*x_stride, 16-byte aligned */
+    const float *residual;   /* nullable; device fp32, row r at residual + r*residual_stride */
+    const float *weight;     /* nullable (all ones); device fp32 [cols], 16-byte aligned */
+    float *out;              /* nullable; device fp32 [rows][cols], s; may be x or residual
+                                themselves where their stride is cols */
+    void *xq;                /* nullable; device, rows*cols/32 Q8_0 blocks (34 B each), 16-byte aligned */
+    void *y;                 /* nullable; device fp16 [rows][cols], the values the blocks stand
+                                for (fp16(d)*q rounded to fp16), for consumers in half
+                                precision that should see what the DMMVs see; 8-byte aligned */
+    int64_t rows;            /* >= 0 (0 is a no-op) */
+    int64_t cols;            /* a multiple of 32, 32 .. 32768 */
+    int64_t x_stride;        /* floats between rows, a multiple of 4, >= cols */
+    int64_t residual_stride; /* the same for residual (ignored where it is NULL) */
+    float eps;               /* finite, > 0 */
+} zdmmv_rmsnorm_args;
+
+/* At least one of out, xq and y is not NULL. The outputs overlap no input but
+ * as stated. Errors: ERR_NULL, ERR_SHAPE (eps too), ERR_ALIGN, ERR_CUDA. */
+zdmmv_status zdmmv_add_rmsnorm_q8_0(const zdmmv_rmsnorm_args *args, zdmmv_stream_t stream);
+
+/* A paged key/value cache in 4 bits: Q4_0 blocks of 32 of a head's dimensions
+ * (fp16 scale d, codes 0..15, value d*(code - 8)), 18 bytes for 32 values.
+ *
+ * Sequence s keeps its token t in page page_table[s*max_pages + t/page_tokens].
+ * A page holds, head by head, page_tokens/16 TILES of 16 tokens of one head,
+ * 18*head_dim bytes each: the K codes (8*head_dim bytes), the V codes (the
+ * same), the K scales (head_dim bytes), the V scales. Inside a tile the codes
+ * lie in the order in which the lanes of a warp feed them to the tensor cores,
+ * so that attention reads them with 128-bit loads and unpacks them with masks
+ * alone. With nb = head_dim/32 and W = 4, 2 or 1 (the largest that divides nb),
+ * token r (0..15) of the tile and dimension e = 32*b + f (f < 32):
+ *   K code: bits 4*(f%8) of the 32-bit word
+ *     (((r/8)*(nb/W) + b/W)*32 + (r%8)*4 + f/8)*W + b%W
+ *   V code: bits 16*(r%2) + 4*(f%4) of the word
+ *     (((r/8)*(nb/W) + b/W)*32 + (f/4)*4 + (r%8)/2)*W + b%W
+ *   scale of block b (K or V): fp16 number ((r/2)*nb + b)*2 + r%2
+ * A V code's 16-bit half holds one token alone and so does a K code's word:
+ * appending a token writes no byte of another one. */
+typedef struct {
+    void *pages;               /* device, n_pages pages of zdmmv_kv_page_bytes, 16-byte aligned */
+    const int32_t *page_table; /* device int32 [n_seq][max_pages] */
+    int64_t n_pages;           /* valid page numbers are 0 .. n_pages-1 */
+    int32_t n_seq;
+    int32_t max_pages;         /* pages a sequence can have */
+    int32_t page_tokens;       /* a multiple of 16, 16 .. 1024 */
+    int32_t n_kv_heads;        /* 1 .. 1024 */
+    int32_t head_dim;          /* 64, 96, 128, 192 or 256 */
+} zdmmv_kv_cache;
+
+/* Bytes of one page; 0 for a geometry that zdmmv_kv_cache does not take. */
+size_t zdmmv_kv_page_bytes(int page_tokens, int n_kv_heads, int head_dim);
+
+#define ZDMMV_ROPE_PAIRS  0 /* dimensions 2i and 2i+1 are turned together */
+#define ZDMMV_ROPE_HALVES 1 /* dimensions i and i + rot_dim/2 */
+
+/* Append n_tok tokens' keys and values to the cache, in ONE launch. Of each
+ * head's vector of q and k the first rot_dim dimensions are rotated, pair
+ * (a, b) of angle i by  a' = a*cos - b*sin,  b' = a*sin + b*cos  (fp32, every
+ * product and sum rounded); then k and v are quantized to Q4_0 blocks: d = (the
+ * first value of the largest magnitude)/-8, id = d ? 1/d : 0, code =
+ * min(15, trunc(x*id + 8.5)), the scale stored as fp16(d). */
+typedef struct {
+    const float *k, *v;      /* device fp32 [n_tok][n_kv_heads][head_dim], tokens k_stride / v_stride apart */
+    const float *q;          /* nullable; device fp32 [n_tok][n_q_heads][head_dim], tokens q_stride apart */
+    const int32_t *seq;      /* device int32 [n_tok]: the token's sequence */
+    const int32_t *pos;      /* device int32 [n_tok]: its position, in the sequence's pages and
+                                in rope; < 0: no token (a padded batch): nothing is written to
+                                the cache, q_out, k_val and v_val get zeros there */
+    const float *rope;       /* device fp32 [rope_rows][rot_dim]: of each position the cosines of
+                                the rot_dim/2 angles, then the sines; NULL with rot_dim 0 */
+    float *q_out;            /* device fp32 [n_tok][n_q_heads][head_dim], contiguous: q rotated;
+                                NULL with q NULL; may be q itself where q_stride is
+                                n_q_heads*head_dim */
+    void *k_val, *v_val;     /* nullable; device fp16 [n_tok][n_kv_heads][head_dim]: the values the
+                                stored blocks stand for (d*(code-8) rounded to fp16), e.g. for a
+                                prompt's own attention in half precision */
+    int32_t *status_dev;     /* nullable device int32: 1 is stored for a bad token (below) */
+    int64_t k_stride, v_stride, q_stride; /* floats, multiples of 4, >= heads*head_dim */
+    int64_t rope_rows;
+    int32_t n_tok;           /* >= 0 (0 is a no-op) */
+    int32_t n_q_heads;       /* 1 .. 65535 (0 with q NULL) */
+    int32_t rot_dim;         /* even, 0 .. head_dim; 0: no rotation */
+    int32_t rope_style;      /* ZDMMV_ROPE_PAIRS or ZDMMV_ROPE_HALVES */
+} zdmmv_kv_append_args;
+
+/* k, v, q, q_out and rope are 16-byte aligned, k_val and v_val 8-byte. A token
+ * whose sequence is outside 0..n_seq-1, whose position is past the sequence's
+ * max_pages pages or past rope_rows, or whose page number is outside
+ * 0..n_pages-1 is bad: nothing is written to the cache for it, its q_out, k_val
+ * and v_val are NaN. Two tokens of one call with the same sequence and position:
+ * either may win, block by block.
+ * Errors: ERR_NULL, ERR_SHAPE, ERR_ALIGN, ERR_CUDA. */
+zdmmv_status zdmmv_kv_append_q4_0(const zdmmv_kv_cache *cache, const zdmmv_kv_append_args *args,
+                                  zdmmv_stream_t stream);
+
+/* Attention over the cache. Sequence s has kv_len[s] tokens in the cache, the
+ * last q_start[s+1] - q_start[s] of which are the new ones that q holds, in
+ * order; new token i of n sees the tokens t < kv_len[s] - (n-1-i), and of those
+ * the last `window` ones where window > 0. Query head h uses kv head
+ * h / (n_q_heads/n_kv_heads):
+ *   out = sum_t p_t v_t / sum_t p_t,   p_t = exp(scale * (q . k_t))
+ * over the tokens seen; a row that sees none is zero. q and every p are split
+ * into two fp16 parts for the tensor cores (22 bits), the codes of K and V are
+ * exact there, the blocks' scales, all sums and the softmax's statistics are
+ * fp32: the result is that of fp32 arithmetic on the cache's values. */
+typedef struct {
+    const float *q;          /* device fp32 [n_tok][n_q_heads][head_dim], tokens q_stride apart (rotated) */
+    const int32_t *q_start;  /* device int32 [n_seq+1], rising from 0 to n_tok */
+    const int32_t *kv_len;   /* device int32 [n_seq], the new tokens included */
+    float *out;              /* device fp32 [n_tok][n_q_heads][head_dim], contiguous */
+    void *workspace;         /* device, 16-byte aligned, >= zdmmv_attn_q4_0_workspace_bytes; NULL
+                                where that is 0; needs no initial contents; one per call in flight */
+    int32_t *status_dev;     /* nullable device int32: 1 is stored for a bad sequence (below) */
+    size_t workspace_bytes;
+    int64_t q_stride;        /* floats, a multiple of 4, >= n_q_heads*head_dim */
+    int32_t n_tok;           /* rows of q and out, >= 0 (0 is a no-op) */
+    int32_t n_q_heads;       /* a multiple of n_kv_heads, at most 65535 */
+    int32_t max_q_len;       /* the most new tokens of a sequence, >= 1: bounds the grid */
+    int32_t max_kv_len;      /* the longest kv_len (an upper bound will do): bounds the grid */
+    int32_t window;          /* 0: no window */
+    float scale;             /* finite; usually 1/sqrt(head_dim) */
+} zdmmv_attn_args;
+
+/* The lengths and the page table are read on the device (a captured graph
+ * replays with new ones, within max_q_len and max_kv_len). A sequence with
+ * kv_len < 0, kv_len > max_kv_len or past its max_pages pages, with a page
+ * number outside 0..n_pages-1 where it would read, or with more new tokens than
+ * max_q_len is bad: the rows of it that the grid covers are NaN, nothing is read
+ * out of range. Tokens at and past kv_len may hold anything. Deterministic from
+ * call to call with the same max_q_len and max_kv_len.
+ * Errors: ERR_NULL, ERR_SHAPE, ERR_ALIGN, ERR_SIZE, ERR_CUDA. */
+size_t zdmmv_attn_q4_0_workspace_bytes(const zdmmv_kv_cache *cache, int n_q_heads, int max_q_len,
+                                       int max_kv_len);
+zdmmv_status zdmmv_attn_q4_0(const zdmmv_kv_cache *cache, const zdmmv_attn_args *args,
+                             zdmmv_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
