@@ -1,110 +1,50 @@
-// zdmmv_attn.cu -- zdmmv_attn_q4_0: attention over the paged 4-bit cache.
-//
-//   out = sum_t p_t v_t / sum_t p_t,  p_t = exp(scale * (q . k_t) - m),  m the running maximum
-//
-// One CTA per (new token, query head): tile by tile, the warps form the tile's 16
-// scores, then every thread updates its dimensions of the sum over V.
+// zdmmv_attn.cu -- zdmmv_attn_q4_0: argument checks and the plan of the launch
+// (the kernels: zdmmv_attn.cuh).
+#include <algorithm>
 #include <cmath>
 
-#include "zdmmv_kv.cuh"
+#include "zdmmv_attn.cuh"
+#include "zdmmv_internal.h"
 
 namespace zdmmv {
 namespace {
 
-struct AttnArgs {
-    KvView c;
-    const float *q;
-    const int32_t *q_start, *kv_len;
-    float *out;
-    int32_t *status;
-    int64_t q_stride;
-    int32_t n_tok, n_q_heads, max_q_len, max_kv_len, window;
-    float scale;
-};
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-constexpr int kThreads = 128;
-
-template <int NB> __global__ void __launch_bounds__(kThreads) attn_kernel(AttnArgs a) {
-    using G = KvGeom<NB>;
-    __shared__ float q[G::kDim];
-    __shared__ float score[kKvSlab];
-    block_op_wait();
-    block_op_release();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int head = blockIdx.x % a.n_q_heads;
-    const int item = blockIdx.x / a.n_q_heads;
-    const int seq = item / a.max_q_len, i = item % a.max_q_len;
-    int q0 = a.q_start[seq], q1 = a.q_start[seq + 1];
-    const int len = a.kv_len[seq];
-    bool bad = q0 < 0 || q1 < q0 || q1 > a.n_tok || q1 - q0 > a.max_q_len || len < 0 || len > a.max_kv_len ||
-               len > static_cast<int64_t>(a.c.max_pages) * a.c.page_tokens;
-    q0 = max(q0, 0);
-    q1 = min(q1, a.n_tok);
-    if (i >= q1 - q0) return;
-    const int64_t row = q0 + i;
-    const int end = bad ? 0 : max(0, len - (q1 - q0 - 1 - i));
-    const int low = a.window > 0 ? max(0, end - a.window) : 0;
-    const int kvh = head / (a.n_q_heads / a.c.n_kv_heads);
-    for (int e = tid; e < G::kDim; e += kThreads) q[e] = a.q[row * a.q_stride + static_cast<int64_t>(head) * G::kDim + e];
-    __syncthreads();
-    float m = -INFINITY, l = 0.0f, o[2] = {0.0f, 0.0f};
-    for (int t0 = low / kKvSlab * kKvSlab; t0 < end; t0 += kKvSlab) {
-        const int page = a.c.table[static_cast<int64_t>(seq) * a.c.max_pages + t0 / a.c.page_tokens];
-        if (page < 0 || page >= a.c.n_pages) {
-            bad = true;
-            break;
-        }
-        const uint8_t *tile = a.c.pages + page * a.c.page_bytes +
-                              static_cast<int64_t>(kvh * (a.c.page_tokens / kKvSlab) + t0 % a.c.page_tokens / kKvSlab) * G::kTileBytes;
-        const __half *ks = reinterpret_cast<const __half *>(tile + G::kKScaleAt);
-        const __half *vs = reinterpret_cast<const __half *>(tile + G::kVScaleAt);
-        for (int r = warp; r < kKvSlab; r += kThreads / 32) {
-            float s = 0.0f;
-            for (int w = lane; w < NB * 4; w += 32) {
-                const uint32_t code = reinterpret_cast<const uint32_t *>(tile)[G::k_word(r, w / 4, w % 4)];
-                const float d = __half2float(ks[G::scale_half(r, w / 4)]);
-                float part = 0.0f;
-                for (int j = 0; j < 8; ++j) part += q[w * 8 + j] * (static_cast<float>((code >> (4 * j)) & 15) - 8.0f);
-                s += d * part;
-            }
-            for (int k = 16; k > 0; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
-            if (lane == 0) score[r] = t0 + r >= low && t0 + r < end ? s * a.scale : -INFINITY;
-        }
-        __syncthreads();
-        float top = m;
-        for (int r = 0; r < kKvSlab; ++r) top = fmaxf(top, score[r]);
-        const float keep = m == -INFINITY ? 0.0f : expf(m - top);
-        m = top;
-        l *= keep;
-        o[0] *= keep;
-        o[1] *= keep;
-        for (int r = 0; r < kKvSlab; ++r) {
-            if (score[r] == -INFINITY) continue;
-            const float p = expf(score[r] - m);
-            l += p;
-            for (int k = 0; k < 2; ++k) {
-                const int e = tid + k * kThreads;
-                if (e >= G::kDim) continue;
-                const uint32_t code = reinterpret_cast<const uint16_t *>(tile + G::kVAt)[G::v_half(r, e / kQK, e % kQK / 4)];
-                const float v = __half2float(vs[G::scale_half(r, e / kQK)]) *
-                                (static_cast<float>((code >> (4 * (e % 4))) & 15) - 8.0f);
-                o[k] += p * v;
-            }
-        }
-        __syncthreads();
-    }
-    if (bad && tid == 0 && a.status) *a.status = 1;
-    for (int k = 0; k < 2; ++k) {
-        const int e = tid + k * kThreads;
-        if (e < G::kDim)
-            a.out[(row * a.n_q_heads + head) * G::kDim + e] = bad ? __int_as_float(0x7fffffff) : (l > 0.0f ? o[k] / l : 0.0f);
-    }
+// Column tiles and splits. A warp takes 8 columns, or 16 where a kv head of a sequence has more; from 17 on the
+// warps share the columns among them. The splits: enough for a few CTAs per SM, each of kMinChunk tiles or more.
+constexpr int kMinChunk = 8;
+constexpr int kCtasWanted = 4;  // per SM
+bool attn_plan(const KvView &c, int head_dim, int n_q_heads, int max_q_len, int64_t max_tokens, AttnPlan *out) {
+    (void)head_dim;
+    static const int sms = [] {
+        int dev = 0, n = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+            return 152;
+        return n;
+    }();
+    AttnPlan p{};
+    const int64_t columns = static_cast<int64_t>(max_q_len) * (n_q_heads / c.n_kv_heads);
+    p.nt = columns <= 8 ? 1 : 2;
+    p.wc = columns <= 16 ? 1 : (columns <= 32 ? 2 : 4);
+    p.cols = 8 * p.nt * p.wc;
+    const int64_t n_ct = ceil_div(columns, p.cols);
+    p.items = static_cast<int64_t>(c.n_seq) * c.n_kv_heads * n_ct;
+    if (p.items > 0x7fffffff) return false;
+    p.n_ct = static_cast<int>(n_ct);
+    const int64_t tiles = std::max<int64_t>(1, ceil_div(max_tokens, kKvSlab));
+    const int64_t wanted = std::max<int64_t>(1, ceil_div(static_cast<int64_t>(sms) * kCtasWanted, p.items));
+    p.max_split = static_cast<int>(std::min(wanted, ceil_div(tiles, kMinChunk)));
+    p.chunk = static_cast<int>(ceil_div(tiles, p.max_split));
+    p.n_split = static_cast<int>(ceil_div(tiles, p.chunk));
+    *out = p;
+    return true;
 }
 
-template <int NB> cudaError_t launch_attn(const AttnArgs &a, cudaStream_t st) {
-    const int64_t ctas = static_cast<int64_t>(a.c.n_seq) * a.max_q_len * a.n_q_heads;
-    if (ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    return launch_block_op(attn_kernel<NB>, dim3(static_cast<unsigned>(ctas)), kThreads, 0, st, a);
+size_t attn_workspace(const AttnPlan &p, int head_dim) {
+    if (p.max_split <= 1) return 0;
+    return static_cast<size_t>(p.items) * p.max_split * p.cols * (head_dim + 2) * 4;
 }
 
 }  // namespace
@@ -115,8 +55,12 @@ using namespace zdmmv;
 extern "C" {
 
 size_t zdmmv_attn_q4_0_workspace_bytes(const zdmmv_kv_cache *cache, int n_q_heads, int max_q_len, int max_kv_len) {
-    (void)cache; (void)n_q_heads; (void)max_q_len; (void)max_kv_len;
-    return 0;
+    KvView c{};
+    AttnPlan p{};
+    if (kv_check(cache, &c) != ZDMMV_OK || n_q_heads < 1 || n_q_heads > 65535 || n_q_heads % c.n_kv_heads ||
+        max_q_len < 1 || max_kv_len < 0 || !attn_plan(c, cache->head_dim, n_q_heads, max_q_len, max_kv_len, &p))
+        return 0;
+    return attn_workspace(p, cache->head_dim);
 }
 
 zdmmv_status zdmmv_attn_q4_0(const zdmmv_kv_cache *cache, const zdmmv_attn_args *args, zdmmv_stream_t stream) {
@@ -125,8 +69,15 @@ zdmmv_status zdmmv_attn_q4_0(const zdmmv_kv_cache *cache, const zdmmv_attn_args 
     const zdmmv_status st = kv_check(cache, &a.c);
     if (st != ZDMMV_OK) return st;
     const zdmmv_attn_args &g = *args;
+    AttnPlan p{}, whole{};
     if (g.n_tok < 0 || g.n_q_heads < 1 || g.n_q_heads > 65535 || g.n_q_heads % cache->n_kv_heads || g.max_q_len < 1 ||
         g.max_kv_len < 0 || g.window < 0 || !std::isfinite(g.scale))
+        return ZDMMV_ERR_SHAPE;
+    // with a window, no column tile sees more than the window and its own new tokens
+    const int64_t seen = g.window > 0 ? std::min<int64_t>(g.max_kv_len, static_cast<int64_t>(g.window) + g.max_q_len + kKvSlab)
+                                      : g.max_kv_len;
+    if (!attn_plan(a.c, cache->head_dim, g.n_q_heads, g.max_q_len, g.max_kv_len, &whole) ||
+        !attn_plan(a.c, cache->head_dim, g.n_q_heads, g.max_q_len, seen, &p))
         return ZDMMV_ERR_SHAPE;
     if (g.n_tok == 0) return ZDMMV_OK;
     if (!g.q || !g.q_start || !g.kv_len || !g.out) return ZDMMV_ERR_NULL;
@@ -134,21 +85,27 @@ zdmmv_status zdmmv_attn_q4_0(const zdmmv_kv_cache *cache, const zdmmv_attn_args 
     if (kv_misaligned(g.q, 16) || kv_misaligned(g.out, 16) || kv_misaligned(g.workspace, 16) ||
         kv_misaligned(g.q_start, 4) || kv_misaligned(g.kv_len, 4) || kv_misaligned(g.status_dev, 4) || g.q_stride % 4)
         return ZDMMV_ERR_ALIGN;
-    const size_t need = zdmmv_attn_q4_0_workspace_bytes(cache, g.n_q_heads, g.max_q_len, g.max_kv_len);
+    const size_t need = attn_workspace(whole, cache->head_dim);
     if (need && !g.workspace) return ZDMMV_ERR_NULL;
     if (g.workspace_bytes < need) return ZDMMV_ERR_SIZE;
     a.q = g.q; a.q_start = g.q_start; a.kv_len = g.kv_len; a.out = g.out; a.status = g.status_dev;
+    a.fault = current_fault_word();
+    if (!a.fault) return ZDMMV_ERR_CUDA;
     a.q_stride = g.q_stride;
-    a.n_tok = g.n_tok; a.n_q_heads = g.n_q_heads; a.max_q_len = g.max_q_len; a.max_kv_len = g.max_kv_len;
-    a.window = g.window; a.scale = g.scale;
+    a.n_tok = g.n_tok; a.n_q_heads = g.n_q_heads; a.group = g.n_q_heads / cache->n_kv_heads;
+    a.max_q_len = g.max_q_len; a.max_kv_len = g.max_kv_len; a.window = g.window;
+    a.scale_log2 = g.scale * 1.44269504088896340736f;
+    a.n_ct = p.n_ct; a.n_split = p.n_split; a.chunk = p.chunk; a.wc = p.wc;
+    a.part = static_cast<float *>(g.workspace);
+    a.part_ml = reinterpret_cast<float2 *>(a.part + p.items * p.n_split * p.cols * cache->head_dim);
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e = cudaErrorInvalidValue;
     switch (kv_blocks(cache->head_dim)) {
-    case 2: e = launch_attn<2>(a, s); break;
-    case 3: e = launch_attn<3>(a, s); break;
-    case 4: e = launch_attn<4>(a, s); break;
-    case 6: e = launch_attn<6>(a, s); break;
-    case 8: e = launch_attn<8>(a, s); break;
+    case 2: e = launch_attn<2>(a, p, s); break;
+    case 3: e = launch_attn<3>(a, p, s); break;
+    case 4: e = launch_attn<4>(a, p, s); break;
+    case 6: e = launch_attn<6>(a, p, s); break;
+    case 8: e = launch_attn<8>(a, p, s); break;
     }
     return e == cudaSuccess ? ZDMMV_OK : ZDMMV_ERR_CUDA;
 }
