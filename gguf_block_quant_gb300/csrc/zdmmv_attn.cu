@@ -36,7 +36,7 @@ bool attn_plan(const KvView &c, int head_dim, int n_q_heads, int max_q_len, int6
     const int64_t tiles = std::max<int64_t>(1, ceil_div(max_tokens, kKvSlab));
     const int64_t wanted = std::max<int64_t>(1, ceil_div(static_cast<int64_t>(sms) * kCtasWanted, p.items));
     p.max_split = static_cast<int>(std::min(wanted, ceil_div(tiles, kMinChunk)));
-    p.chunk = static_cast<int>(ceil_div(tiles, p.max_split));
+    p.chunk = static_cast<int>(ceil_div(ceil_div(tiles, p.max_split), 2) * 2);  // whole ring slots
     p.n_split = static_cast<int>(ceil_div(tiles, p.chunk));
     *out = p;
     return true;

@@ -51,21 +51,15 @@ struct AttnArgs {
     int32_t n_tok, n_q_heads, group, max_q_len, max_kv_len, window;
     int32_t n_ct;       // column tiles of a kv head of a sequence
     int32_t n_split, chunk;  // most splits, tiles of a split
-    int32_t stages;
+    int32_t slots;      // ring slots
     int32_t wc;         // warps that split the columns (the others split the tokens)
     float scale_log2;
 };
 
 constexpr int kAttnWarps = 4;
 constexpr int kAttnThreads = kAttnWarps * 32 + 32;
-constexpr int kAttnBarBytes = 256;
-constexpr int kAttnMaxStages = 8;
-
-// Tiles of a pipeline stage: about 18 KB.
-template <int NB> struct AttnStage {
-    static constexpr int kTiles = NB <= 2 ? 16 : (NB <= 4 ? 8 : 4);
-    static constexpr int kBytes = kTiles * KvGeom<NB>::kTileBytes;
-};
+constexpr int kAttnBarBytes = 512;
+constexpr int kAttnMaxSlots = 32;  // ring slots (two barriers each), a pair of tiles in each
 
 // What a CTA (and the join) works on, from the lengths on the device.
 struct AttnRange {
@@ -145,6 +139,41 @@ template <int NB, int W> __device__ __forceinline__ void lds_words(uint32_t at, 
     }
 }
 
+// Two fp32 operations in one instruction (each half rounded as the scalar one).
+__device__ __forceinline__ uint64_t f2(float x, float y) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(x), "f"(y));
+    return d;
+}
+__device__ __forceinline__ float2 f2_parts(uint64_t v) {
+    float2 d;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(v));
+    return d;
+}
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t f2_half2(uint32_t w) { return f2(half_lo(w), half_hi(w)); }
+// hi + lo = x to 22 bits, as two fp16 pairs
+__device__ __forceinline__ void split_f2(uint64_t x, uint32_t &hi, uint32_t &lo) {
+    const float2 v = f2_parts(x);
+    hi = pack_h2(v.x, v.y);
+    const float2 r = f2_parts(f2_add(x, f2(-half_lo(hi), -half_hi(hi))));
+    lo = pack_h2(r.x, r.y);
+}
+
 __device__ __forceinline__ void attn_consumer_barrier() {
     asm volatile("bar.sync 1, %0;" ::"n"(kAttnWarps * 32) : "memory");
 }
@@ -152,22 +181,21 @@ __device__ __forceinline__ void attn_consumer_barrier() {
 template <int NB, int NT>
 __global__ void __launch_bounds__(kAttnThreads, NB * NT <= 4 ? 3 : (NB * NT <= 8 ? 2 : 1)) attn_kernel(AttnArgs a) {
     using G = KvGeom<NB>;
-    using S = AttnStage<NB>;
     constexpr int D = G::kDim;
-    constexpr bool kQReg = NB * NT <= 8;  // q's fragments in registers, else in shared memory
+    constexpr int kSlotBytes = 2 * G::kTileBytes;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ float sh_m[kAttnWarps][NT * 8], sh_l[kAttnWarps][NT * 8];
+    __shared__ float sh_m[kAttnWarps][NT * 8], sh_l[kAttnWarps][NT * 8], sh_qs[kAttnWarps][NT * 8];
     __shared__ int sh_bad;
     uint64_t *full = reinterpret_cast<uint64_t *>(smem);
-    uint64_t *empty = full + kAttnMaxStages;
+    uint64_t *empty = full + kAttnMaxSlots;
     uint8_t *ring = smem + kAttnBarBytes;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int cols = 8 * NT * a.wc;  // columns of the CTA
     if (tid == 0) {
-        for (int s = 0; s < a.stages; ++s) {
+        for (int s = 0; s < a.slots; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&empty[s], kAttnWarps);
+            mbar_init(&empty[s], a.wc);
         }
         sh_bad = 0;
         fence_barrier_init();
@@ -184,52 +212,55 @@ __global__ void __launch_bounds__(kAttnThreads, NB * NT <= 4 ? 3 : (NB * NT <= 8
     if (ct * cols >= r.n * a.group) return;
     const int n_splits = r.splits(a.chunk);
     if (split >= n_splits) return;
-    const int first = r.slab0 + split * a.chunk;                        // tiles first .. last-1
+    const int first = r.slab0 + split * a.chunk;  // tiles first .. last-1
     const int last = min(r.slab0 + r.slabs, first + a.chunk);
-    const int n_stages = (last - first + S::kTiles - 1) / S::kTiles;
+    const int n_units = (last - first + 1) / 2;   // pairs of tiles, a ring slot each
 
     if (warp == kAttnWarps) {
         // ------------------------------------------------------- producer
         const uint64_t policy = l2_evict_first_policy();
         const int page_tiles = a.c.page_tokens / kKvSlab;
         const int32_t *table = a.c.table + static_cast<int64_t>(seq) * a.c.max_pages;
-        const int64_t head_at = static_cast<int64_t>(kvh) * page_tiles * G::kTileBytes;
-        int slab = first + lane;  // the lane's tile of the stage
-        int page = lane < S::kTiles && slab < last ? table[slab / page_tiles] : 0;
+        const uint8_t *base = a.c.pages + static_cast<int64_t>(kvh) * page_tiles * G::kTileBytes;
         bool ok = true;
-        int st = 0;
-        for (; st < n_stages; ++st) {
-            const int s = st % a.stages;
-            const bool mine = lane < S::kTiles && slab < last;
-            const bool bad_page = mine && (page < 0 || page >= a.c.n_pages);
-            const int use = bad_page ? 0 : page;
-            const uint8_t *src = a.c.pages + use * a.c.page_bytes + head_at +
-                                 static_cast<int64_t>(slab % page_tiles) * G::kTileBytes;
-            slab += S::kTiles;
-            page = lane < S::kTiles && slab < last ? table[slab / page_tiles] : 0;  // the next stage's, ahead of time
-            if (st >= a.stages) {
-                if (!__all_sync(0xffffffffu, mbar_wait(&empty[s], static_cast<uint32_t>(st / a.stages - 1) & 1u))) {
-                    ok = false;
-                    break;
-                }
-                fence_proxy_async_smem();
+        int u = 0, slot = 0;
+        uint32_t phase = 1;  // the parity of a wait that passes at once on a fresh barrier
+        for (int u0 = 0; u0 < n_units && ok; u0 += 16) {
+            // 32 tiles' pages at a time, one a lane
+            const int tile = first + 2 * u0 + lane;
+            const bool in = tile < last;
+            int page = in ? table[tile / page_tiles] : 0;
+            const bool wrong = in && (page < 0 || page >= a.c.n_pages);
+            if (wrong) page = 0;
+            if (__any_sync(0xffffffffu, wrong) && lane == 0) {
+                sh_bad = 1;  // before the arrival below, so before any consumer is through
+                if (a.status) *a.status = 1;
             }
-            const bool any_bad = __any_sync(0xffffffffu, bad_page);
-            if (lane == 0) {
-                if (any_bad) {
-                    sh_bad = 1;
-                    if (a.status) *a.status = 1;
+            const uint8_t *src = base + page * a.c.page_bytes + static_cast<int64_t>(tile % page_tiles) * G::kTileBytes;
+            const int end = min(n_units, u0 + 16);
+            for (; u < end; ++u) {
+                if (u >= a.slots) {
+                    if (!__all_sync(0xffffffffu, mbar_wait(&empty[slot], phase))) {
+                        ok = false;
+                        break;
+                    }
+                    fence_proxy_async_smem();
                 }
-                const int n = min(S::kTiles, last - first - st * S::kTiles);
-                mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(n) * G::kTileBytes);
+                const int at = 2 * (u - u0);  // the lanes that copy
+                if (lane == at) mbar_arrive_expect_tx(&full[slot], first + 2 * u + 1 < last ? kSlotBytes : G::kTileBytes);
+                __syncwarp();
+                if ((lane == at || lane == at + 1) && in)
+                    bulk_copy_g2s(ring + slot * kSlotBytes + (lane & 1) * G::kTileBytes, src, G::kTileBytes, &full[slot], policy);
+                if (++slot == a.slots) {
+                    slot = 0;
+                    phase ^= 1;
+                }
             }
-            __syncwarp();
-            if (mine) bulk_copy_g2s(ring + s * S::kBytes + lane * G::kTileBytes, src, G::kTileBytes, &full[s], policy);
         }
         if (!ok && lane == 0) atomicOr(a.fault, 1u);
         // leave only when the copies into this CTA's shared memory have landed
-        for (int k = max(0, st - a.stages); k < st; ++k)
-            (void)mbar_wait(&full[k % a.stages], static_cast<uint32_t>(k / a.stages) & 1u);
+        for (int k = max(0, u - a.slots); k < u; ++k)
+            (void)mbar_wait(&full[k % a.slots], static_cast<uint32_t>(k / a.slots) & 1u);
         return;
     }
 
@@ -237,238 +268,269 @@ __global__ void __launch_bounds__(kAttnThreads, NB * NT <= 4 ? 3 : (NB * NT <= 8
     const int g = lane >> 2, t = lane & 3;
     const int wc = warp % a.wc, wt = warp / a.wc, n_wt = kAttnWarps / a.wc;
     const int col0 = ct * cols + wc * 8 * NT;  // the warp's first column
-
-    // q's fragments: column g of each group of 8, this lane's 8 dimensions 8t.. of every block
-    uint32_t qf[kQReg ? NT : 1][kQReg ? 2 * NB : 1][4];
-    uint4 *q_sm = reinterpret_cast<uint4 *>(ring + a.stages * S::kBytes) + warp * (NT * 2 * NB * 32) + lane;
-    float qs[NT];
-    int end[NT], low[NT];
-    int end_min = r.len, low_max = 0, len = r.len;
+    uint4 *q_sm = reinterpret_cast<uint4 *>(ring + a.slots * kSlotBytes) + wc * (NT * 2 * NB * 32) + lane;
+    if (wt == 0) {
+        // q's fragments: column g of each group of 8, this lane's 8 dimensions 8t.. of every block
+#pragma unroll 1
+        for (int nt = 0; nt < NT; ++nt) {
+            const int col = col0 + 8 * nt + g;
+            const int i = col / a.group;
+            const bool valid = i < r.n;
+            const float *q = a.q + static_cast<int64_t>(r.q0 + (valid ? i : 0)) * a.q_stride +
+                             static_cast<int64_t>(kvh * a.group + (valid ? col - i * a.group : 0)) * D + 8 * t;
+            float v[NB][8];
+            float top = 0.0f;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        const int col = col0 + 8 * nt + g;
-        const int i = col / a.group;
-        const bool valid = i < r.n;
-        end[nt] = valid ? max(0, r.len - (r.n - 1 - i)) : r.len;
-        low[nt] = valid && a.window > 0 ? max(0, end[nt] - a.window) : 0;
-        end_min = min(end_min, end[nt]);
-        low_max = max(low_max, low[nt]);
-        const float *q = a.q + static_cast<int64_t>(r.q0 + (valid ? i : 0)) * a.q_stride +
-                         static_cast<int64_t>(kvh * a.group + (valid ? col - i * a.group : 0)) * D + 8 * t;
-        float v[NB][8];
-        float top = 0.0f;
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-            float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
-            if (valid) {
-                x = *reinterpret_cast<const float4 *>(q + b * kQK);
-                y = *reinterpret_cast<const float4 *>(q + b * kQK + 4);
+            for (int b = 0; b < NB; ++b) {
+                float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+                if (valid) {
+                    x = *reinterpret_cast<const float4 *>(q + b * kQK);
+                    y = *reinterpret_cast<const float4 *>(q + b * kQK + 4);
+                }
+                v[b][0] = x.x; v[b][1] = x.y; v[b][2] = x.z; v[b][3] = x.w;
+                v[b][4] = y.x; v[b][5] = y.y; v[b][6] = y.z; v[b][7] = y.w;
             }
-            v[b][0] = x.x; v[b][1] = x.y; v[b][2] = x.z; v[b][3] = x.w;
-            v[b][4] = y.x; v[b][5] = y.y; v[b][6] = y.z; v[b][7] = y.w;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(v[b][k]));
-        }
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        // 2^e brings the column's largest magnitude into [2^13, 2^14)
-        int e = 13 - (static_cast<int>(__float_as_uint(top) >> 23) - 127);
-        e = min(100, max(-100, e));
-        const float up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
-        const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-        qs[nt] = a.scale_log2 * down;
+            for (int b = 0; b < NB; ++b)
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
+                for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(v[b][k]));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            // 2^e brings the column's largest magnitude into [2^13, 2^14); the scale's sign goes into q
+            int e = 13 - (static_cast<int>(__float_as_uint(top) >> 23) - 127);
+            e = min(100, max(-100, e));
+            const float up = __uint_as_float((static_cast<uint32_t>(e + 127) << 23) | (a.scale_log2 < 0.0f ? 0x80000000u : 0u));
+            const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+            if (t == 0) sh_qs[wc][8 * nt + g] = fmaxf(fabsf(a.scale_log2) * down, 1e-37f);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v[b][k] *= up;
+            for (int b = 0; b < NB; ++b) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                // k slots: the codes at bits 0 and 16 of the (shifted) word, then those at bits 4 and 20
-                uint4 f;
-                split_h2(v[b][2 * h], v[b][2 * h + 4], f.x, f.y);
-                split_h2(v[b][2 * h + 1] * 0.0625f, v[b][2 * h + 5] * 0.0625f, f.z, f.w);
-                if constexpr (kQReg) {
-                    qf[nt][2 * b + h][0] = f.x; qf[nt][2 * b + h][1] = f.y;
-                    qf[nt][2 * b + h][2] = f.z; qf[nt][2 * b + h][3] = f.w;
-                } else {
+                for (int h = 0; h < 2; ++h) {
+                    // k slots: the codes at bits 0 and 16 of the (shifted) word, then those at bits 4 and 20
+                    uint4 f;
+                    split_h2(v[b][2 * h] * up, v[b][2 * h + 4] * up, f.x, f.y);
+                    split_h2(v[b][2 * h + 1] * up * 0.0625f, v[b][2 * h + 5] * up * 0.0625f, f.z, f.w);
                     q_sm[(nt * 2 * NB + 2 * b + h) * 32] = f;
                 }
             }
         }
     }
-    // tiles outside low_max .. end_min need masks (warp-uniform)
+    // what each column sees, of this split's tiles
+    int end[NT], low[NT];
+    const int limit = min(r.len, last * kKvSlab);
+    int end_min = limit, low_max = 0;
 #pragma unroll
-    for (int o = 4; o < 32; o <<= 1) {
-        end_min = min(end_min, __shfl_xor_sync(0xffffffffu, end_min, o));
-        low_max = max(low_max, __shfl_xor_sync(0xffffffffu, low_max, o));
+    for (int nt = 0; nt < NT; ++nt) {
+        const int i = (col0 + 8 * nt + g) / a.group;
+        const bool valid = i < r.n;
+        end[nt] = valid ? min(limit, max(0, r.len - (r.n - 1 - i))) : limit;
+        low[nt] = valid && a.window > 0 ? max(0, r.len - (r.n - 1 - i) - a.window) : 0;
+        end_min = min(end_min, end[nt]);
+        low_max = max(low_max, low[nt]);
     }
-    __syncwarp();
+    // units outside low_max .. end_min need masks (warp-uniform)
+    end_min = __reduce_min_sync(0xffffffffu, end_min);
+    low_max = __reduce_max_sync(0xffffffffu, low_max);
+    attn_consumer_barrier();
 
-    float o[NT][2 * NB][4], m[NT], l[NT];
+    float m[NT], l[NT], qs[NT];
+    uint64_t o[NT][2 * NB][2];  // columns 2t, 2t+1: dimension pairs' first and second
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         m[nt] = -INFINITY;
         l[nt] = 0.0f;
+        qs[nt] = sh_qs[wc][8 * nt + g];
 #pragma unroll
-        for (int k = 0; k < 2 * NB; ++k) o[nt][k][0] = o[nt][k][1] = o[nt][k][2] = o[nt][k][3] = 0.0f;
+        for (int k = 0; k < 2 * NB; ++k) o[nt][k][0] = o[nt][k][1] = 0;
     }
-    int sx = 38;           // p is in units of 2^sx ...
-    uint32_t cap = 0x0001;  // ... |d_v| <= 2^(14 - sx), as an fp16 number: here 2^-24
+    int sx = 38;                          // p is in units of 2^sx ...
+    __half cap = __ushort_as_half(0x0001);  // ... |d_v| <= 2^(14 - sx), here 2^-24
     bool dead = false;
 
-    for (int st = 0; st < n_stages; ++st) {
-        const int s = st % a.stages;
-        if (!__all_sync(0xffffffffu, mbar_wait(&full[s], static_cast<uint32_t>(st / a.stages) & 1u))) {
+    int slot = wt;
+    uint32_t phase = 0;
+    for (int u = wt; u < n_units; u += n_wt) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&full[slot], phase))) {
             if (lane == 0) atomicOr(a.fault, 1u);
             dead = true;
             break;
         }
-        const int n_tiles = min(S::kTiles, last - first - st * S::kTiles);
-        for (int k = wt; k < n_tiles; k += n_wt) {
-            const int t0 = (first + st * S::kTiles + k) * kKvSlab;
-            const uint32_t tile = smem_addr(ring + s * S::kBytes + k * G::kTileBytes);
-            // ------------------------------------------------ scores
-            float sc[NT][4];  // column g, tokens 2t, 2t+1, 8+2t, 8+2t+1
+        const uint32_t tile = smem_addr(ring) + slot * kSlotBytes;
+        const int t0 = (first + 2 * u) * kKvSlab;
+        // ------------------------------------------------ scores: column g, tokens 8h + 2t, 8h + 2t + 1
+        uint64_t acc[NT][4];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                uint32_t kw[NB], dk[NB];
-                lds_words<NB, G::kVec>(tile + (h * NB * 32 + lane * G::kVec) * 4, 128 * G::kVec, kw);
-                lds_words<NB, G::kVec>(tile + G::kKScaleAt + (t + 4 * h) * NB * 4, 4 * G::kVec, dk);
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) sc[nt][2 * h] = sc[nt][2 * h + 1] = 0.0f;
+            for (int h = 0; h < 4; ++h) acc[nt][h] = 0;
+        {
+            uint32_t kw[4][NB], dk[4][NB];
 #pragma unroll
-                for (int b = 0; b < NB; ++b) {
+            for (int h = 0; h < 4; ++h) {
+                const uint32_t at = tile + (h >> 1) * G::kTileBytes;
+                lds_words<NB, G::kVec>(at + ((h & 1) * NB * 32 + lane * G::kVec) * 4, 128 * G::kVec, kw[h]);
+                lds_words<NB, G::kVec>(at + G::kKScaleAt + (t + 4 * (h & 1)) * NB * 4, 4 * G::kVec, dk[h]);
+            }
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                uint32_t qa[NT][2][4];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+                        const uint4 f = q_sm[(nt * 2 * NB + 2 * b + s) * 32];
+                        qa[nt][s][0] = f.x; qa[nt][s][1] = f.y; qa[nt][s][2] = f.z; qa[nt][s][3] = f.w;
+                    }
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
                     uint32_t kc[4];
-                    code_pairs(kw[b], kc);
-                    const float d0 = half_lo(dk[b]), d1 = half_hi(dk[b]);
+                    code_pairs(kw[h][b], kc);
+                    const uint64_t d = f2_half2(dk[h][b]);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                        if constexpr (kQReg) {
-                            mma_acc(c, qf[nt][2 * b], kc[0], kc[1]);
-                            mma_acc(c, qf[nt][2 * b + 1], kc[2], kc[3]);
-                        } else {
-                            const uint4 f0 = q_sm[(nt * 2 * NB + 2 * b) * 32], f1 = q_sm[(nt * 2 * NB + 2 * b + 1) * 32];
-                            const uint32_t a0[4] = {f0.x, f0.y, f0.z, f0.w}, a1[4] = {f1.x, f1.y, f1.z, f1.w};
-                            mma_acc(c, a0, kc[0], kc[1]);
-                            mma_acc(c, a1, kc[2], kc[3]);
-                        }
-                        sc[nt][2 * h] = fmaf(d0, c[0] + c[2], sc[nt][2 * h]);
-                        sc[nt][2 * h + 1] = fmaf(d1, c[1] + c[3], sc[nt][2 * h + 1]);
+                        mma_acc(c, qa[nt][0], kc[0], kc[1]);
+                        mma_acc(c, qa[nt][1], kc[2], kc[3]);
+                        acc[nt][h] = f2_fma(d, f2_add(f2(c[0], c[1]), f2(c[2], c[3])), acc[nt][h]);
                     }
                 }
             }
-            // ------------------------------------------------ V's scales, masks
-            uint32_t dv[2][NB];
-            lds_words<NB, G::kVec>(tile + G::kVScaleAt + t * NB * 4, 4 * G::kVec, dv[0]);
-            lds_words<NB, G::kVec>(tile + G::kVScaleAt + (t + 4) * NB * 4, 4 * G::kVec, dv[1]);
+        }
+        uint32_t dv[4][NB];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+        for (int h = 0; h < 4; ++h)
+            lds_words<NB, G::kVec>(tile + (h >> 1) * G::kTileBytes + G::kVScaleAt + (t + 4 * (h & 1)) * NB * 4, 4 * G::kVec, dv[h]);
+        float sc[NT][8];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) sc[nt][i] *= qs[nt];
-            if (t0 + kKvSlab > end_min || t0 < low_max) {
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int tok = t0 + 2 * t + (i & 1) + 8 * (i >> 1);
+            for (int h = 0; h < 4; ++h) {
+                const float2 v = f2_parts(acc[nt][h]);
+                sc[nt][2 * h] = v.x;
+                sc[nt][2 * h + 1] = v.y;
+            }
+        if (t0 + 2 * kKvSlab > end_min || t0 < low_max) {
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                        if (tok < low[nt] || tok >= end[nt]) sc[nt][i] = -INFINITY;
-                    // a token past the sequence's may hold anything, NaN among it: its V counts for nothing
-                    if (tok >= len) {
+            for (int i = 0; i < 8; ++i) {
+                const int tok = t0 + 2 * t + (i & 1) + 8 * (i >> 1);
 #pragma unroll
-                        for (int b = 0; b < NB; ++b) dv[i >> 1][b] &= (i & 1) ? 0x0000ffffu : 0xffff0000u;
-                    }
+                for (int nt = 0; nt < NT; ++nt)
+                    if (tok < low[nt] || tok >= end[nt]) sc[nt][i] = -INFINITY;
+                // a token past the sequence's (or a stale half slot) may hold anything, NaN among it: its V
+                // counts for nothing
+                if (tok >= limit) {
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) dv[i >> 1][b] &= (i & 1) ? 0x0000ffffu : 0xffff0000u;
                 }
             }
-            // ------------------------------------------------ the unit of p: largest |d_v| so far
-            uint32_t big = 0;
+        }
+        // ------------------------------------------------ the unit of p: the largest |d_v| so far
+        {
+            __half2 big = __half2half2(__ushort_as_half(0));
 #pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                // magnitudes of fp16 numbers order like their bits
-                big = __vmaxu2(big, dv[0][b] & 0x7fff7fffu);
-                big = __vmaxu2(big, dv[1][b] & 0x7fff7fffu);
-            }
-            big = max(big & 0xffffu, big >> 16);
-            if (__any_sync(0xffffffffu, big > cap)) {
-                big = __reduce_max_sync(0xffffffffu, big);
+            for (int h = 0; h < 4; ++h)
+#pragma unroll
+                for (int b = 0; b < NB; ++b) big = __hmax2(big, __habs2(*reinterpret_cast<const __half2 *>(&dv[h][b])));
+            const __half one = __hmax(__low2half(big), __high2half(big));
+            if (__any_sync(0xffffffffu, __hgt(one, cap))) {
+                const uint32_t bits = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(__half_as_ushort(one)));
                 // the power of two at or above it
-                const float f = half_lo(min(big, 0x7bffu));
+                const float f = half_lo(min(bits, 0x7bffu));
                 const int ex = static_cast<int>((__float_as_uint(f) + 0x7fffffu) >> 23) - 127;
                 const int to = 14 - ex;
                 const float keep = __uint_as_float(static_cast<uint32_t>(max(0, to - sx + 127)) << 23);
                 sx = to;
-                cap = ex >= 16 ? 0x7fffu : __half_as_ushort(__float2half_rn(__uint_as_float(static_cast<uint32_t>(ex + 127) << 23)));
+                cap = ex >= 16 ? __ushort_as_half(0x7c00) : __float2half_rn(__uint_as_float(static_cast<uint32_t>(ex + 127) << 23));
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     l[nt] *= keep;
 #pragma unroll
                     for (int j = 0; j < 2 * NB; ++j)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) o[nt][j][i] *= keep;
+                        for (int i = 0; i < 2; ++i) o[nt][j][i] = f2_mul(o[nt][j][i], f2(keep, keep));
                 }
             }
-            // ------------------------------------------------ softmax
-            bool grow = false;
-            float top[NT];
+        }
+        // ------------------------------------------------ softmax
+        bool grow = false;
+        float top[NT];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            float x = sc[nt][0];
+#pragma unroll
+            for (int i = 1; i < 8; ++i) x = fmaxf(x, sc[nt][i]);
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+            top[nt] = x * qs[nt];
+            grow |= top[nt] > m[nt];
+        }
+        if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                top[nt] = fmaxf(fmaxf(sc[nt][0], sc[nt][1]), fmaxf(sc[nt][2], sc[nt][3]));
-                top[nt] = fmaxf(top[nt], __shfl_xor_sync(0xffffffffu, top[nt], 1));
-                top[nt] = fmaxf(top[nt], __shfl_xor_sync(0xffffffffu, top[nt], 2));
-                grow |= top[nt] > m[nt];
-            }
-            if (__any_sync(0xffffffffu, grow)) {
+                const float to = fmaxf(m[nt], top[nt]);
+                const float keep = to > m[nt] ? exp2_approx(m[nt] - to) : 1.0f;  // 0 where nothing was seen before
+                m[nt] = to;
+                l[nt] *= keep;
+                const uint64_t k01 = f2(__shfl_sync(0xffffffffu, keep, 8 * t), __shfl_sync(0xffffffffu, keep, 8 * t + 4));
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    const float to = fmaxf(m[nt], top[nt]);
-                    const float keep = to > m[nt] ? exp2_approx(m[nt] - to) : 1.0f;  // 0 where nothing was seen before
-                    m[nt] = to;
-                    l[nt] *= keep;
-                    const float k0 = __shfl_sync(0xffffffffu, keep, 8 * t), k1 = __shfl_sync(0xffffffffu, keep, 8 * t + 4);
-#pragma unroll
-                    for (int j = 0; j < 2 * NB; ++j) {
-                        o[nt][j][0] *= k0; o[nt][j][2] *= k0;
-                        o[nt][j][1] *= k1; o[nt][j][3] *= k1;
-                    }
+                for (int j = 0; j < 2 * NB; ++j) {
+                    o[nt][j][0] = f2_mul(o[nt][j][0], k01);
+                    o[nt][j][1] = f2_mul(o[nt][j][1], k01);
                 }
             }
-            float p[NT][4];
+        }
+        uint64_t p[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const float base = m[nt] == -INFINITY ? 0.0f : m[nt] - static_cast<float>(sx);
+            float e[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) e[i] = exp2_approx(fmaf(sc[nt][i], qs[nt], -base));
+            l[nt] += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+#pragma unroll
+            for (int h = 0; h < 4; ++h) p[nt][h] = f2(e[2 * h], e[2 * h + 1]);
+        }
+        // ------------------------------------------------ product with V
+        uint32_t vw[4][NB];
+#pragma unroll
+        for (int h = 0; h < 4; ++h)
+            lds_words<NB, G::kVec>(tile + (h >> 1) * G::kTileBytes + G::kVAt + ((h & 1) * NB * 32 + lane * G::kVec) * 4,
+                                   128 * G::kVec, vw[h]);
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+            uint32_t f[2][2][4];  // [tile][dimensions 4g, 4g+1 / 4g+2, 4g+3 of the block]
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                uint32_t vc[4];
+                code_pairs(vw[h][j], vc);
+                f[h >> 1][0][2 * (h & 1)] = vc[0]; f[h >> 1][0][2 * (h & 1) + 1] = vc[1];
+                f[h >> 1][1][2 * (h & 1)] = vc[2]; f[h >> 1][1][2 * (h & 1) + 1] = vc[3];
+            }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                const float base = m[nt] == -INFINITY ? 0.0f : m[nt] - static_cast<float>(sx);
+                uint32_t hi[4], lo[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) p[nt][i] = exp2_approx(sc[nt][i] - base);
-                l[nt] += (p[nt][0] + p[nt][1]) + (p[nt][2] + p[nt][3]);
-            }
-            // ------------------------------------------------ product with V
-            uint32_t vw[2][NB];
-            lds_words<NB, G::kVec>(tile + G::kVAt + lane * G::kVec * 4, 128 * G::kVec, vw[0]);
-            lds_words<NB, G::kVec>(tile + G::kVAt + (NB * 32 + lane * G::kVec) * 4, 128 * G::kVec, vw[1]);
+                for (int h = 0; h < 4; ++h) split_f2(f2_mul(p[nt][h], f2_half2(dv[h][j])), hi[h], lo[h]);
+                // summed over the unit by the tensor cores (they truncate), over the units in fp32
 #pragma unroll
-            for (int j = 0; j < NB; ++j) {
-                uint32_t f0[4], f1[4];  // dimensions 4g, 4g+1 and 4g+2, 4g+3 of the block
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t vc[4];
-                    code_pairs(vw[h][j], vc);
-                    f0[2 * h] = vc[0]; f0[2 * h + 1] = vc[1];
-                    f1[2 * h] = vc[2]; f1[2 * h + 1] = vc[3];
-                }
-                const float d0 = half_lo(dv[0][j]), d1 = half_hi(dv[0][j]), d2 = half_lo(dv[1][j]), d3 = half_hi(dv[1][j]);
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    uint32_t hi0, lo0, hi1, lo1;
-                    split_h2(p[nt][0] * d0, p[nt][1] * d1, hi0, lo0);
-                    split_h2(p[nt][2] * d2, p[nt][3] * d3, hi1, lo1);
-                    mma_acc(o[nt][2 * j], f0, hi0, hi1);
-                    mma_acc(o[nt][2 * j + 1], f1, hi0, hi1);
-                    mma_acc(o[nt][2 * j], f0, lo0, lo1);
-                    mma_acc(o[nt][2 * j + 1], f1, lo0, lo1);
+                for (int s = 0; s < 2; ++s) {
+                    float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    mma_acc(c, f[0][s], lo[0], lo[1]);
+                    mma_acc(c, f[1][s], lo[2], lo[3]);
+                    mma_acc(c, f[0][s], hi[0], hi[1]);
+                    mma_acc(c, f[1][s], hi[2], hi[3]);
+                    o[nt][2 * j + s][0] = f2_add(o[nt][2 * j + s][0], f2(c[0], c[1]));
+                    o[nt][2 * j + s][1] = f2_add(o[nt][2 * j + s][1], f2(c[2], c[3]));
                 }
             }
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&empty[s]);
+        if (lane == 0) mbar_arrive(&empty[slot]);
+        slot += n_wt;
+        if (slot >= a.slots) {
+            slot -= a.slots;
+            phase ^= 1;
+        }
     }
 
     // ------------------------------------------------ join the warps
@@ -495,14 +557,13 @@ __global__ void __launch_bounds__(kAttnThreads, NB * NT <= 4 ? 3 : (NB * NT <= 8
             f[h] = top == -INFINITY ? 0.0f : exp2_approx(sh_m[warp][c] - top);
         }
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            float *dst = sum + (warp * NT * 8 + 8 * nt + 2 * t + h) * D + 4 * g;
-            const float one = f[h], sixteenth = f[h] * 0.0625f;
-#pragma unroll
-            for (int j = 0; j < NB; ++j)
-                *reinterpret_cast<float4 *>(dst + j * kQK) =
-                    make_float4(o[nt][2 * j][h] * one, o[nt][2 * j][2 + h] * sixteenth, o[nt][2 * j + 1][h] * one,
-                                o[nt][2 * j + 1][2 + h] * sixteenth);
+        for (int j = 0; j < NB; ++j) {
+            const float2 x0 = f2_parts(o[nt][2 * j][0]), x1 = f2_parts(o[nt][2 * j][1]);
+            const float2 x2 = f2_parts(o[nt][2 * j + 1][0]), x3 = f2_parts(o[nt][2 * j + 1][1]);
+            float *dst = sum + (warp * NT * 8 + 8 * nt + 2 * t) * D + 4 * g + j * kQK;
+            const float s0 = f[0] * 0.0625f, s1 = f[1] * 0.0625f;  // the second of each pair is 16 times too large
+            *reinterpret_cast<float4 *>(dst) = make_float4(x0.x * f[0], x1.x * s0, x2.x * f[0], x3.x * s0);
+            *reinterpret_cast<float4 *>(dst + D) = make_float4(x0.y * f[1], x1.y * s1, x2.y * f[1], x3.y * s1);
         }
     }
     attn_consumer_barrier();
@@ -543,7 +604,7 @@ constexpr int kJoinThreads = 128;
 template <int NB> __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(AttnArgs a, int cols) {
     constexpr int D = NB * kQK, kQuads = D / 4, kGroups = kJoinThreads / kQuads;
     __shared__ float4 sum[kGroups][kQuads];
-    __shared__ float sum_l[kGroups];
+    __shared__ float sum_l[kGroups], tops[kJoinThreads / 32];
     block_op_wait();
     block_op_release();
     const int item = blockIdx.x, c = blockIdx.y;
@@ -556,11 +617,16 @@ template <int NB> __global__ void __launch_bounds__(kJoinThreads) attn_join_kern
     if (n == 1 || col >= r.n * a.group) return;
     const int64_t at = static_cast<int64_t>(item) * a.n_split * cols + c;
     float top = -INFINITY;
-    for (int s = 0; s < n; ++s) top = fmaxf(top, a.part_ml[at + static_cast<int64_t>(s) * cols].x);
+    for (int s = threadIdx.x; s < n; s += kJoinThreads) top = fmaxf(top, a.part_ml[at + static_cast<int64_t>(s) * cols].x);
+    for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+    if ((threadIdx.x & 31) == 0) tops[threadIdx.x >> 5] = top;
+    __syncthreads();
+    for (int k = 0; k < kJoinThreads / 32; ++k) top = fmaxf(top, tops[k]);
     const int grp = threadIdx.x / kQuads, e = threadIdx.x % kQuads;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float ls = 0.0f;
     if (grp < kGroups) {
+#pragma unroll 4
         for (int s = grp; s < n; s += kGroups) {
             const int64_t p = at + static_cast<int64_t>(s) * cols;
             const float2 ml = a.part_ml[p];
@@ -602,9 +668,12 @@ extern template cudaError_t launch_attn<6>(AttnArgs, const AttnPlan &, cudaStrea
 extern template cudaError_t launch_attn<8>(AttnArgs, const AttnPlan &, cudaStream_t);
 
 #ifdef ZDMMV_ATTN_INSTANTIATE
-template <int NB, int NT> cudaError_t launch_attn_nt(const AttnArgs &a, const AttnPlan &p, cudaStream_t st) {
-    constexpr bool kQReg = NB * NT <= 8;
-    const size_t ring = static_cast<size_t>(a.stages) * AttnStage<NB>::kBytes + (kQReg ? 0 : kAttnWarps * NT * 2 * NB * 512);
+template <int NB, int NT> cudaError_t launch_attn_nt(AttnArgs a, const AttnPlan &p, cudaStream_t st) {
+    constexpr size_t kSlot = 2 * KvGeom<NB>::kTileBytes;
+    // a ring of about 55 KB, at least two slots a warp; the join's sums lie over it
+    a.slots = static_cast<int32_t>(55 * 1024 / kSlot / kAttnWarps * kAttnWarps);
+    a.slots = a.slots < 2 * kAttnWarps ? 2 * kAttnWarps : (a.slots > kAttnMaxSlots ? kAttnMaxSlots : a.slots);
+    const size_t ring = a.slots * kSlot + static_cast<size_t>(p.wc) * NT * 2 * NB * 512;
     const size_t join = static_cast<size_t>(kAttnWarps) * NT * 8 * NB * kQK * 4;
     const size_t smem = kAttnBarBytes + (ring > join ? ring : join);
     cudaError_t e = cudaFuncSetAttribute(attn_kernel<NB, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -616,7 +685,6 @@ template <int NB, int NT> cudaError_t launch_attn_nt(const AttnArgs &a, const At
                            p.cols);
 }
 template <int NB> cudaError_t launch_attn(AttnArgs a, const AttnPlan &p, cudaStream_t st) {
-    a.stages = 3;
     return p.nt == 1 ? launch_attn_nt<NB, 1>(a, p, st) : launch_attn_nt<NB, 2>(a, p, st);
 }
 #endif
