@@ -27,8 +27,8 @@ bool attn_plan(const KvView &c, int head_dim, int n_q_heads, int max_q_len, int6
     AttnPlan p{};
     const int64_t columns = static_cast<int64_t>(max_q_len) * (n_q_heads / c.n_kv_heads);
     p.nt = columns <= 8 ? 1 : 2;
-    p.wc = columns <= 16 ? 1 : (columns <= 32 ? 2 : 4);
-    p.cols = 8 * p.nt * p.wc;
+    p.wc = columns <= 16 ? 1 : (columns <= 32 ? 2 : (columns <= 64 ? 4 : 8));
+    p.cols = columns <= kNarrowCols ? kNarrowCols : 8 * p.nt * p.wc;
     const int64_t n_ct = ceil_div(columns, p.cols);
     p.items = static_cast<int64_t>(c.n_seq) * c.n_kv_heads * n_ct;
     if (p.items > 0x7fffffff) return false;

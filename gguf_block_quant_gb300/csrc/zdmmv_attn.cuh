@@ -21,11 +21,13 @@
 //  * The C fragment of the scores holds, per lane, a column's two neighbouring
 //    tokens: exactly the B fragment of the product with V (columns x tokens), so
 //    p goes from one MMA to the next in its registers.
-//  * Product with V: A = the codes' dimensions x 16 tokens. V's scales are per
-//    (token, block): x = p * d_v, split into two
-//    fp16 parts again. p is kept in units of 2^sx, sx such that x <= 2^14 for the
-//    largest |d_v| met: with fp16's lowest unit at 2^-24 every x is then exact to
-//    2^-38 of the largest.
+//  * Product with V: A = the codes' dimensions x 16 tokens, B = x = p * d_v (V's
+//    scales are per token and block) in two fp16 parts, formed in fp16: with p =
+//    ph + pl, xh = ph * d_v rounded, xl = pl * d_v + (ph * d_v - xh), whose bracket
+//    one fma gives exactly. p is kept in units of 2^sx, sx such that p and x stay
+//    below 2^15 for the largest |d_v| met: fp16's lowest unit of 2^-24 is then
+//    below 2^-38 of the largest p, and below 2^-26 of the largest x while d_v is a
+//    normal fp16 number.
 //
 // Work: grid (kv head of a sequence and column tile) x (split of its tokens); a
 // producer warp copies tiles (one bulk copy each) into a ring, the consumer warps
@@ -51,15 +53,19 @@ struct AttnArgs {
     int32_t n_tok, n_q_heads, group, max_q_len, max_kv_len, window;
     int32_t n_ct;       // column tiles of a kv head of a sequence
     int32_t n_split, chunk;  // most splits, tiles of a split
-    int32_t slots;      // ring slots
     int32_t wc;         // warps that split the columns (the others split the tokens)
     float scale_log2;
 };
 
-constexpr int kAttnWarps = 4;
-constexpr int kAttnThreads = kAttnWarps * 32 + 32;
-constexpr int kAttnBarBytes = 512;
-constexpr int kAttnMaxSlots = 32;  // ring slots (two barriers each), a pair of tiles in each
+// The kernel's two forms. Own rings (wc = 1): each of 4 warps copies its own tiles into two slots of its own and waits
+// for nobody. Shared ring (wc > 1): 8 warps split the columns (and the slots among groups of them), a ninth copies.
+template <int NB, bool SHARED> struct AttnForm {
+    static constexpr int kWarps = SHARED ? 8 : 4;
+    static constexpr int kThreads = kWarps * 32 + (SHARED ? 32 : 0);
+    static constexpr int kSlots = SHARED ? (NB >= 8 ? 8 : 16) : 2 * kWarps;  // ring slots, a pair of tiles in each
+};
+constexpr int kAttnBarBytes = 256;  // two barriers a slot
+constexpr int kAttnUnit = 13;
 
 // What a CTA (and the join) works on, from the lengths on the device.
 struct AttnRange {
@@ -91,9 +97,30 @@ __device__ __forceinline__ void mma_acc(float (&d)[4], const uint32_t (&a)[4], u
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void mma_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+}
 __device__ __forceinline__ uint32_t h2_add(uint32_t a, uint32_t b) {
     uint32_t d;
     asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ uint32_t h2_mul(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ uint32_t h2_fma(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t d;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
+__device__ __forceinline__ uint32_t h2_neg(uint32_t a) {
+    uint32_t d;
+    asm("neg.f16x2 %0, %1;" : "=r"(d) : "r"(a));
     return d;
 }
 __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
@@ -113,14 +140,16 @@ __device__ __forceinline__ void split_h2(float x, float y, uint32_t &hi, uint32_
 }
 
 // The 8 codes of a word as exact fp16 pairs: n - 8 of the nibbles 0 and 4, 16 (n - 8) of 1 and 5, n - 8 of 2 and 6,
-// 16 (n - 8) of 3 and 7.
-__device__ __forceinline__ void code_pairs(uint32_t w, uint32_t (&f)[4]) {
-    constexpr uint32_t kMagic = 0x64006400u, kM1032 = 0xE408E408u, kM1152 = 0xE480E480u;
+// 16 (n - 8) of 3 and 7. `magic` is 1024 in both halves, loaded from shared memory so that it stays in a register: the
+// mask is then the one immediate of a three-input logic operation (two constants take two operations).
+constexpr uint32_t kCodeMagic = 0x64006400u;
+__device__ __forceinline__ void code_pairs(uint32_t w, uint32_t magic, uint32_t (&f)[4]) {
+    constexpr uint32_t kM1032 = 0xE408E408u, kM1152 = 0xE480E480u;
     const uint32_t w8 = w >> 8;
-    f[0] = h2_add((w & 0x000F000Fu) | kMagic, kM1032);
-    f[1] = h2_add((w & 0x00F000F0u) | kMagic, kM1152);
-    f[2] = h2_add((w8 & 0x000F000Fu) | kMagic, kM1032);
-    f[3] = h2_add((w8 & 0x00F000F0u) | kMagic, kM1152);
+    f[0] = h2_add((w & 0x000F000Fu) | magic, kM1032);
+    f[1] = h2_add((w & 0x00F000F0u) | magic, kM1152);
+    f[2] = h2_add((w8 & 0x000F000Fu) | magic, kM1032);
+    f[3] = h2_add((w8 & 0x00F000F0u) | magic, kM1152);
 }
 
 // NB words of a lane: NB / W vectors of W words, `step` bytes apart.
@@ -165,39 +194,422 @@ __device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
     return d;
 }
-__device__ __forceinline__ uint64_t f2_half2(uint32_t w) { return f2(half_lo(w), half_hi(w)); }
+__device__ __forceinline__ uint64_t f2_half2(uint32_t w) {
+    uint64_t d;
+    asm("{\n\t.reg .b16 a, b;\n\t.reg .f32 x, y;\n\t"
+        "mov.b32 {a, b}, %1;\n\tcvt.f32.f16 x, a;\n\tcvt.f32.f16 y, b;\n\tmov.b64 %0, {x, y};\n\t}"
+        : "=l"(d)
+        : "r"(w));
+    return d;
+}
 // hi + lo = x to 22 bits, as two fp16 pairs
 __device__ __forceinline__ void split_f2(uint64_t x, uint32_t &hi, uint32_t &lo) {
     const float2 v = f2_parts(x);
     hi = pack_h2(v.x, v.y);
-    const float2 r = f2_parts(f2_add(x, f2(-half_lo(hi), -half_hi(hi))));
+    const float2 r = f2_parts(f2_fma(f2_half2(hi), f2(-1.0f, -1.0f), x));
     lo = pack_h2(r.x, r.y);
 }
 
-__device__ __forceinline__ void attn_consumer_barrier() {
-    asm volatile("bar.sync 1, %0;" ::"n"(kAttnWarps * 32) : "memory");
+template <int WARPS> __device__ __forceinline__ void attn_consumer_barrier() {
+    asm volatile("bar.sync 1, %0;" ::"n"(WARPS * 32) : "memory");
 }
 
-template <int NB, int NT>
-__global__ void __launch_bounds__(kAttnThreads, NB * NT <= 4 ? 3 : (NB * NT <= 8 ? 2 : 1)) attn_kernel(AttnArgs a) {
+// 2^e that brings a column's largest magnitude into [2^13, 2^14), with the scale's sign (up), and 2^-e (down).
+__device__ __forceinline__ void q_unit(float top, float scale, float &up, float &down) {
+    int e = 13 - (static_cast<int>(__float_as_uint(top) >> 23) - 127);
+    e = min(100, max(-100, e));
+    up = __uint_as_float((static_cast<uint32_t>(e + 127) << 23) | (scale < 0.0f ? 0x80000000u : 0u));
+    down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+}
+// The unit of p for a largest |d_v| (fp16 bits) of 2 or more: 2^(unit - kAttnUnit) |d_v| < 2.
+__device__ __forceinline__ int unit_for(uint32_t bits) { return kAttnUnit + 15 - static_cast<int>(bits >> 10); }
+
+// The copies of a stretch of units (pairs of tiles, a ring slot each): unit first_unit + k * step, k = 0, 1, ...; a warp's
+// lanes look up the pages of 16 units at a time, lanes 2j and 2j + 1 copy unit j's tiles.
+template <int NB> struct TileFeed {
+    const uint8_t *src = nullptr;  // this lane's tile
+    bool in = false;               // ... is one of the split's
+    __device__ void look(const AttnArgs &a, const uint8_t *head, const int32_t *table, int tile, int last, int *sh_bad) {
+        const int page_tiles = a.c.page_tokens / kKvSlab;
+        in = tile < last;
+        int page = in ? table[tile / page_tiles] : 0;
+        const bool wrong = in && (page < 0 || page >= a.c.n_pages);
+        if (wrong) {  // seen by whoever waits for the copy that follows
+            page = 0;
+            *sh_bad = 1;
+            if (a.status) *a.status = 1;
+        }
+        __syncwarp();
+        src = head + page * a.c.page_bytes + static_cast<int64_t>(tile % page_tiles) * KvGeom<NB>::kTileBytes;
+    }
+    // unit j of the stretch into `slot`
+    __device__ void copy(int j, int lane, uint8_t *slot, uint64_t *full, uint64_t policy) const {
+        constexpr uint32_t kBytes = KvGeom<NB>::kTileBytes;
+        const uint32_t both = __ballot_sync(0xffffffffu, in) >> (2 * j + 1) & 1u;
+        if (lane == 2 * j) mbar_arrive_expect_tx(full, kBytes << both);
+        __syncwarp();
+        if (lane >> 1 == j && in) bulk_copy_g2s(slot + (lane & 1) * kBytes, src, kBytes, full, policy);
+    }
+};
+
+// The CTA's end: the warps' sums (already in the unit of their common maximum) added up, and stored as the result or,
+// where the sequence's tokens are split, as a partial one. `sum`: [warp][WCOLS][D]; m, l: [warp][WCOLS].
+template <int D, int WCOLS, int WARPS>
+__device__ __forceinline__ void attn_store(const AttnArgs &a, const AttnRange &r, int item, int split, int n_splits,
+                                           int cols, int wc, const float *sum, const float *m, const float *l, bool bad) {
+    const int ct = item % a.n_ct, kvh = item / a.n_ct % a.c.n_kv_heads;
+    const int n_wt = WARPS / wc;
+    if (r.bad && threadIdx.x == 0 && a.status) *a.status = 1;
+    constexpr int kQuads = D / 4;
+    for (int k = threadIdx.x; k < cols * kQuads; k += WARPS * 32) {
+        const int c = k / kQuads, e = 4 * (k % kQuads);
+        const int w0 = c / WCOLS, wcol = c % WCOLS;
+        const int col = ct * cols + c;
+        if (col >= r.n * a.group) break;
+        float top = -INFINITY, ls = 0.0f;
+        for (int w = 0; w < n_wt; ++w) top = fmaxf(top, m[(w * wc + w0) * WCOLS + wcol]);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int w = 0; w < n_wt; ++w) {
+            const int at = (w * wc + w0) * WCOLS + wcol;
+            ls += l[at] * (top == -INFINITY ? 1.0f : exp2_approx(m[at] - top));
+            const float4 x = *reinterpret_cast<const float4 *>(sum + at * D + e);
+            acc.x += x.x; acc.y += x.y; acc.z += x.z; acc.w += x.w;
+        }
+        if (bad) ls = __int_as_float(0x7fffffff);
+        if (n_splits == 1) {
+            const float inv = ls == 0.0f ? 0.0f : 1.0f / ls;
+            const int i = col / a.group;
+            float *dst = a.out + (static_cast<int64_t>(r.q0 + i) * a.n_q_heads + kvh * a.group + (col - i * a.group)) * D + e;
+            *reinterpret_cast<float4 *>(dst) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+        } else {
+            const int64_t at = (static_cast<int64_t>(item) * a.n_split + split) * cols + c;
+            *reinterpret_cast<float4 *>(a.part + at * D + e) = acc;
+            if (e == 0) a.part_ml[at] = make_float2(top, ls);
+        }
+    }
+}
+
+// The narrow form: up to 4 columns, each as two neighbouring columns (upper and lower part) of the MMAs' 8.
+//  * Scores: A = 16 tokens' codes, B = q's parts: C holds, per lane (g, t), column t's upper and lower sum for the
+//    tokens g and g + 8, so a score is d_k * (c0 + c1) and nothing is computed twice (the wide form with 4 columns
+//    spends twice the MMAs, scales and exponentials).
+//  * p's parts go to the B fragment of the product with V (tokens x parts) by a transpose of 8 x 8 fp16 pairs
+//    (movmatrix): the pairs (0, ph) and (ph, pl), whose rows are then 0 or ph, and ph or pl, so that one formula
+//    x = fma(second, d_v, fma(first, d_v, -(first * d_v))) is xh on a row of ph and xl on a row of pl.
+//  * The product's C holds column t's two parts side by side again: they are one sum of fp32 pairs.
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+constexpr int kNarrowWarps = 4, kNarrowCols = 4;
+template <int NB> __global__ void __launch_bounds__(kNarrowWarps * 32, NB <= 4 ? 4 : 3) attn_narrow_kernel(AttnArgs a) {
     using G = KvGeom<NB>;
+    constexpr int D = G::kDim, kWarps = kNarrowWarps;
+    constexpr int kSlotBytes = 2 * G::kTileBytes;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ float sh_m[kWarps][kNarrowCols], sh_l[kWarps][kNarrowCols];
+    __shared__ int sh_bad;
+    __shared__ uint32_t sh_magic;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem) + 2 * warp;  // the warp's two slots
+    uint8_t *ring = smem + kAttnBarBytes + 2 * warp * kSlotBytes;
+    if (lane == 0) {
+        mbar_init(&full[0], 1);
+        mbar_init(&full[1], 1);
+        fence_barrier_init();
+    }
+    if (tid == 0) {
+        sh_bad = 0;
+        sh_magic = kCodeMagic;
+    }
+    __syncthreads();
+    block_op_wait();
+    block_op_release();
+
+    const int item = blockIdx.x, split = blockIdx.y;
+    const int ct = item % a.n_ct;
+    const int kvh = item / a.n_ct % a.c.n_kv_heads;
+    const int seq = item / a.n_ct / a.c.n_kv_heads;
+    const AttnRange r = attn_range(a, seq, ct, kNarrowCols);
+    if (ct * kNarrowCols >= r.n * a.group) return;
+    const int n_splits = r.splits(a.chunk);
+    if (split >= n_splits) return;
+    const int first = r.slab0 + split * a.chunk;  // tiles first .. last-1
+    const int last = min(r.slab0 + r.slabs, first + a.chunk);
+    const int n_units = (last - first + 1) / 2;   // pairs of tiles
+
+    const uint8_t *head = a.c.pages + static_cast<int64_t>(kvh) * (a.c.page_tokens / kKvSlab) * G::kTileBytes;
+    const int32_t *table = a.c.table + static_cast<int64_t>(seq) * a.c.max_pages;
+    const uint64_t policy = l2_evict_first_policy();
+    TileFeed<NB> feed;
+    feed.look(a, head, table, first + 2 * (warp + (lane >> 1) * kWarps) + (lane & 1), last, &sh_bad);
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+        if (warp + j * kWarps < n_units) feed.copy(j, lane, ring + j * kSlotBytes, &full[j], policy);
+
+    const int g = lane >> 2, t = lane & 3;
+    // q's B fragments: column g / 2, its upper (g even) or lower part; this lane's dimensions 8t .. 8t+7 of every block
+    uint32_t qf[NB][4];
+    float qs;
+    {
+        const int col = ct * kNarrowCols + g / 2;
+        const int i = col / a.group;
+        const bool valid = i < r.n;
+        const float *q = a.q + static_cast<int64_t>(r.q0 + (valid ? i : 0)) * a.q_stride +
+                         static_cast<int64_t>(kvh * a.group + (valid ? col - i * a.group : 0)) * D + 8 * t;
+        float v[NB][8];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+            if (valid) {
+                x = *reinterpret_cast<const float4 *>(q + b * kQK);
+                y = *reinterpret_cast<const float4 *>(q + b * kQK + 4);
+            }
+            v[b][0] = x.x; v[b][1] = x.y; v[b][2] = x.z; v[b][3] = x.w;
+            v[b][4] = y.x; v[b][5] = y.y; v[b][6] = y.z; v[b][7] = y.w;
+        }
+        float top = 0.0f;
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(v[b][k]));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        float up, down;
+        q_unit(top, a.scale_log2, up, down);
+        qs = __shfl_sync(0xffffffffu, fmaxf(fabsf(a.scale_log2) * down, 1e-37f), 8 * t);  // column t's
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t f[4];
+                split_h2(v[b][2 * h] * up, v[b][2 * h + 4] * up, f[0], f[1]);
+                split_h2(v[b][2 * h + 1] * up * 0.0625f, v[b][2 * h + 5] * up * 0.0625f, f[2], f[3]);
+                qf[b][2 * h] = (g & 1) ? f[1] : f[0];
+                qf[b][2 * h + 1] = (g & 1) ? f[3] : f[2];
+            }
+    }
+    // what column t sees, of this split's tiles
+    const int limit = min(r.len, last * kKvSlab);
+    const int ti = (ct * kNarrowCols + t) / a.group;
+    const int end = ti < r.n ? min(limit, max(0, r.len - (r.n - 1 - ti))) : limit;
+    const int low = ti < r.n && a.window > 0 ? max(0, r.len - (r.n - 1 - ti) - a.window) : 0;
+    const int end_min = __reduce_min_sync(0xffffffffu, end), low_max = __reduce_max_sync(0xffffffffu, low);
+
+    const uint32_t magic = lds32(smem_addr(&sh_magic));
+    const uint32_t pick = (g & 1) ? 0x7632u : 0x5410u;  // the token's half of two words of scales
+    float m = -INFINITY, l = 0.0f;
+    uint64_t o[2 * NB][2];  // dimensions 4g (4g + 2) and 4g + 1 (4g + 3) of the block, upper and lower part
+#pragma unroll
+    for (int k = 0; k < 2 * NB; ++k) o[k][0] = o[k][1] = 0;
+    int sx = kAttnUnit;  // p is in units of 2^sx
+    bool dead = false;
+
+    int slot = 0;
+    uint32_t phase = 0;
+    for (int u = warp, j_next = 2; u < n_units; u += kWarps) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&full[slot], phase))) {
+            if (lane == 0) atomicOr(a.fault, 1u);
+            dead = true;
+            break;
+        }
+        const uint32_t tile = smem_addr(ring) + slot * kSlotBytes;
+        const int t0 = (first + 2 * u) * kKvSlab;
+        // ------------------------------------------------ scores of column t: tokens 8h + g
+        float sc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            uint32_t kw[2][NB], dk[2][NB];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                lds_words<NB, G::kVec>(tile + s * G::kTileBytes + (h * NB * 32 + lane * G::kVec) * 4, 128 * G::kVec, kw[h]);
+                lds_words<NB, G::kVec>(tile + s * G::kTileBytes + G::kKScaleAt + (g / 2 + 4 * h) * NB * 4, 4 * G::kVec, dk[h]);
+            }
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                uint32_t k0[4], k1[4];
+                code_pairs(kw[0][b], magic, k0);
+                code_pairs(kw[1][b], magic, k1);
+                const uint32_t a0[4] = {k0[0], k1[0], k0[1], k1[1]}, a1[4] = {k0[2], k1[2], k0[3], k1[3]};
+                float c[4];
+                mma_first(c, a0, qf[b][0], qf[b][1]);
+                mma_acc(c, a1, qf[b][2], qf[b][3]);
+                const uint64_t d = f2_half2(__byte_perm(dk[0][b], dk[1][b], pick));  // tokens g, g + 8
+                const float2 dd = f2_parts(d);
+                sc[2 * s] = fmaf(dd.x, c[0] + c[1], sc[2 * s]);
+                sc[2 * s + 1] = fmaf(dd.y, c[2] + c[3], sc[2 * s + 1]);
+            }
+        }
+        uint32_t dv[4][NB];
+#pragma unroll
+        for (int h = 0; h < 4; ++h)
+            lds_words<NB, G::kVec>(tile + (h >> 1) * G::kTileBytes + G::kVScaleAt + (t + 4 * (h & 1)) * NB * 4, 4 * G::kVec, dv[h]);
+        if (t0 + 2 * kKvSlab > end_min || t0 < low_max) {
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                const int tok = t0 + 8 * h + g;
+                if (tok < low || tok >= end) sc[h] = -INFINITY;
+                // a token past the sequence's (or a stale half slot) may hold anything, NaN among it: its V
+                // counts for nothing
+                const int pair = t0 + 8 * h + 2 * t;
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    if (pair >= limit) dv[h][b] = 0;
+                    else if (pair + 1 >= limit) dv[h][b] &= 0xffffu;
+                }
+            }
+        }
+        // ------------------------------------------------ the unit of p: 2^kAttnUnit while every |d_v| < 2
+        {
+            uint32_t any = 0;
+#pragma unroll
+            for (int h = 0; h < 4; ++h)
+#pragma unroll
+                for (int b = 0; b < NB; ++b) any |= dv[h][b];
+            if (__any_sync(0xffffffffu, (any & 0x40004000u) != 0)) {
+                uint32_t big = 0;
+#pragma unroll
+                for (int h = 0; h < 4; ++h)
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) big = max(big, max(dv[h][b] & 0x7fffu, (dv[h][b] >> 16) & 0x7fffu));
+                const int to = unit_for(__reduce_max_sync(0xffffffffu, big));
+                if (to < sx) {
+                    const float keep = __uint_as_float(static_cast<uint32_t>(to - sx + 127) << 23);
+                    sx = to;
+                    l *= keep;
+#pragma unroll
+                    for (int k = 0; k < 2 * NB; ++k) {
+                        o[k][0] = f2_mul(o[k][0], f2(keep, keep));
+                        o[k][1] = f2_mul(o[k][1], f2(keep, keep));
+                    }
+                }
+            }
+        }
+        // ------------------------------------------------ softmax
+        float top = fmaxf(fmaxf(sc[0], sc[1]), fmaxf(sc[2], sc[3]));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+        top *= qs;
+        if (__any_sync(0xffffffffu, top > m)) {
+            const float to = fmaxf(m, top);
+            const float keep = to > m ? exp2_approx(m - to) : 1.0f;  // 0 where nothing was seen before
+            m = to;
+            l *= keep;
+#pragma unroll
+            for (int k = 0; k < 2 * NB; ++k) {
+                o[k][0] = f2_mul(o[k][0], f2(keep, keep));
+                o[k][1] = f2_mul(o[k][1], f2(keep, keep));
+            }
+        }
+        const float base = m == -INFINITY ? 0.0f : m - static_cast<float>(sx);
+        uint32_t p0[4], p1[4];  // rows 0 or ph, and ph or pl, of tokens 8h + 2t, + 1
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+            const float p = exp2_approx(fmaf(sc[h], qs, -base));
+            l += p;
+            const uint32_t w = pack_h2(0.0f, p);
+            p0[h] = transpose_8x8(w);
+            p1[h] = transpose_8x8(pack_h2(p, p - f2_parts(f2_half2(w)).y));
+        }
+        // ------------------------------------------------ product with V
+        uint32_t vw[4][NB];
+#pragma unroll
+        for (int h = 0; h < 4; ++h)
+            lds_words<NB, G::kVec>(tile + (h >> 1) * G::kTileBytes + G::kVAt + ((h & 1) * NB * 32 + lane * G::kVec) * 4,
+                                   128 * G::kVec, vw[h]);
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+            uint32_t f[2][2][4], x[4];
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                uint32_t vc[4];
+                code_pairs(vw[h][j], magic, vc);
+                f[h >> 1][0][2 * (h & 1)] = vc[0]; f[h >> 1][0][2 * (h & 1) + 1] = vc[1];
+                f[h >> 1][1][2 * (h & 1)] = vc[2]; f[h >> 1][1][2 * (h & 1) + 1] = vc[3];
+                x[h] = h2_fma(p1[h], dv[h][j], h2_fma(p0[h], dv[h][j], h2_neg(h2_mul(p0[h], dv[h][j]))));
+            }
+            // summed over the unit by the tensor cores (they truncate), over the units in fp32
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float c[4];
+                mma_first(c, f[0][i], x[0], x[1]);
+                mma_acc(c, f[1][i], x[2], x[3]);
+                o[2 * j + i][0] = f2_add(o[2 * j + i][0], f2(c[0], c[1]));
+                o[2 * j + i][1] = f2_add(o[2 * j + i][1], f2(c[2], c[3]));
+            }
+        }
+        __syncwarp();
+        if (u + 2 * kWarps < n_units) {  // the warp's unit after next takes the slot's place
+            if (j_next == 16) {
+                j_next = 0;
+                feed.look(a, head, table, first + 2 * (u + 2 * kWarps + (lane >> 1) * kWarps) + (lane & 1), last, &sh_bad);
+            }
+            fence_proxy_async_smem();
+            feed.copy(j_next++, lane, ring + slot * kSlotBytes, &full[slot], policy);
+        }
+        phase ^= static_cast<uint32_t>(slot);
+        slot ^= 1;
+    }
+    if (dead) {
+        // leave only when the warp's copies have landed: the one that failed and the one behind it
+        (void)mbar_wait(&full[slot], phase);
+        if (warp + kWarps < n_units) (void)mbar_wait(&full[slot ^ 1], phase ^ static_cast<uint32_t>(slot));
+    }
+
+    // ------------------------------------------------ join the warps
+    l += __shfl_xor_sync(0xffffffffu, l, 4);
+    l += __shfl_xor_sync(0xffffffffu, l, 8);
+    l += __shfl_xor_sync(0xffffffffu, l, 16);
+    m -= static_cast<float>(sx);  // the maximum in p's unit
+    if (g == 0) {
+        sh_m[warp][t] = m;
+        sh_l[warp][t] = dead ? __int_as_float(0x7fffffff) : l;
+    }
+    __syncthreads();  // every warp is done with its ring
+    float top = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sh_m[w][t]);
+    const float f0 = top == -INFINITY ? 0.0f : exp2_approx(m - top), f1 = f0 * 0.0625f;
+    float *sum = reinterpret_cast<float *>(smem + kAttnBarBytes);  // [warp][column][D]
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+        const float2 x0 = f2_parts(o[2 * j][0]), x1 = f2_parts(o[2 * j][1]);
+        const float2 x2 = f2_parts(o[2 * j + 1][0]), x3 = f2_parts(o[2 * j + 1][1]);
+        // the second of each pair is 16 times too large
+        *reinterpret_cast<float4 *>(sum + (warp * kNarrowCols + t) * D + 4 * g + j * kQK) =
+            make_float4((x0.x + x0.y) * f0, (x1.x + x1.y) * f1, (x2.x + x2.y) * f0, (x3.x + x3.y) * f1);
+    }
+    __syncthreads();
+    attn_store<D, kNarrowCols, kWarps>(a, r, item, split, n_splits, kNarrowCols, 1, sum, &sh_m[0][0], &sh_l[0][0],
+                                       r.bad || sh_bad);
+}
+
+template <int NB, int NT, bool SHARED>
+__global__ void __launch_bounds__(AttnForm<NB, SHARED>::kThreads, SHARED ? 1 : (NB * NT <= 4 ? 4 : 2)) attn_kernel(AttnArgs a) {
+    using G = KvGeom<NB>;
+    using F = AttnForm<NB, SHARED>;
+    constexpr int kWarps = F::kWarps, kSlots = F::kSlots;
     constexpr int D = G::kDim;
     constexpr int kSlotBytes = 2 * G::kTileBytes;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ float sh_m[kAttnWarps][NT * 8], sh_l[kAttnWarps][NT * 8], sh_qs[kAttnWarps][NT * 8];
+    __shared__ float sh_m[kWarps][NT * 8], sh_l[kWarps][NT * 8], sh_qs[kWarps][NT * 8];
     __shared__ int sh_bad;
+    __shared__ uint32_t sh_magic;
     uint64_t *full = reinterpret_cast<uint64_t *>(smem);
-    uint64_t *empty = full + kAttnMaxSlots;
+    uint64_t *empty = full + kSlots;
     uint8_t *ring = smem + kAttnBarBytes;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int cols = 8 * NT * a.wc;  // columns of the CTA
     if (tid == 0) {
-        for (int s = 0; s < a.slots; ++s) {
+        for (int s = 0; s < kSlots; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], a.wc);
         }
         sh_bad = 0;
+        sh_magic = kCodeMagic;
         fence_barrier_init();
     }
     __syncthreads();
@@ -216,59 +628,48 @@ __global__ void __launch_bounds__(kAttnThreads, NB * NT <= 4 ? 3 : (NB * NT <= 8
     const int last = min(r.slab0 + r.slabs, first + a.chunk);
     const int n_units = (last - first + 1) / 2;   // pairs of tiles, a ring slot each
 
-    if (warp == kAttnWarps) {
+    const uint8_t *head = a.c.pages + static_cast<int64_t>(kvh) * (a.c.page_tokens / kKvSlab) * G::kTileBytes;
+    const int32_t *table = a.c.table + static_cast<int64_t>(seq) * a.c.max_pages;
+    const uint64_t policy = l2_evict_first_policy();
+    TileFeed<NB> feed;
+
+    if (SHARED && warp == kWarps) {
         // ------------------------------------------------------- producer
-        const uint64_t policy = l2_evict_first_policy();
-        const int page_tiles = a.c.page_tokens / kKvSlab;
-        const int32_t *table = a.c.table + static_cast<int64_t>(seq) * a.c.max_pages;
-        const uint8_t *base = a.c.pages + static_cast<int64_t>(kvh) * page_tiles * G::kTileBytes;
         bool ok = true;
-        int u = 0, slot = 0;
-        uint32_t phase = 1;  // the parity of a wait that passes at once on a fresh barrier
+        int u = 0;
         for (int u0 = 0; u0 < n_units && ok; u0 += 16) {
-            // 32 tiles' pages at a time, one a lane
-            const int tile = first + 2 * u0 + lane;
-            const bool in = tile < last;
-            int page = in ? table[tile / page_tiles] : 0;
-            const bool wrong = in && (page < 0 || page >= a.c.n_pages);
-            if (wrong) page = 0;
-            if (__any_sync(0xffffffffu, wrong) && lane == 0) {
-                sh_bad = 1;  // before the arrival below, so before any consumer is through
-                if (a.status) *a.status = 1;
-            }
-            const uint8_t *src = base + page * a.c.page_bytes + static_cast<int64_t>(tile % page_tiles) * G::kTileBytes;
-            const int end = min(n_units, u0 + 16);
-            for (; u < end; ++u) {
-                if (u >= a.slots) {
-                    if (!__all_sync(0xffffffffu, mbar_wait(&empty[slot], phase))) {
+            feed.look(a, head, table, first + 2 * u0 + lane, last, &sh_bad);
+            for (; u < min(n_units, u0 + 16); ++u) {
+                const int s = u % kSlots;
+                if (u >= kSlots) {
+                    if (!__all_sync(0xffffffffu, mbar_wait(&empty[s], static_cast<uint32_t>(u / kSlots - 1) & 1u))) {
                         ok = false;
                         break;
                     }
                     fence_proxy_async_smem();
                 }
-                const int at = 2 * (u - u0);  // the lanes that copy
-                if (lane == at) mbar_arrive_expect_tx(&full[slot], first + 2 * u + 1 < last ? kSlotBytes : G::kTileBytes);
-                __syncwarp();
-                if ((lane == at || lane == at + 1) && in)
-                    bulk_copy_g2s(ring + slot * kSlotBytes + (lane & 1) * G::kTileBytes, src, G::kTileBytes, &full[slot], policy);
-                if (++slot == a.slots) {
-                    slot = 0;
-                    phase ^= 1;
-                }
+                feed.copy(u - u0, lane, ring + s * kSlotBytes, &full[s], policy);
             }
         }
         if (!ok && lane == 0) atomicOr(a.fault, 1u);
         // leave only when the copies into this CTA's shared memory have landed
-        for (int k = max(0, u - a.slots); k < u; ++k)
-            (void)mbar_wait(&full[k % a.slots], static_cast<uint32_t>(k / a.slots) & 1u);
+        for (int k = max(0, u - kSlots); k < u; ++k)
+            (void)mbar_wait(&full[k % kSlots], static_cast<uint32_t>(k / kSlots) & 1u);
         return;
     }
 
     // ---------------------------------------------------------- consumers
     const int g = lane >> 2, t = lane & 3;
-    const int wc = warp % a.wc, wt = warp / a.wc, n_wt = kAttnWarps / a.wc;
+    const int wc = warp % a.wc, wt = warp / a.wc, n_wt = kWarps / a.wc;
     const int col0 = ct * cols + wc * 8 * NT;  // the warp's first column
-    uint4 *q_sm = reinterpret_cast<uint4 *>(ring + a.slots * kSlotBytes) + wc * (NT * 2 * NB * 32) + lane;
+    uint4 *q_sm = reinterpret_cast<uint4 *>(ring + kSlots * kSlotBytes) + wc * (NT * 2 * NB * 32) + lane;
+    if constexpr (!SHARED) {
+        feed.look(a, head, table, first + 2 * (warp + (lane >> 1) * kWarps) + (lane & 1), last, &sh_bad);
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            if (warp + j * kWarps < n_units)
+                feed.copy(j, lane, ring + (warp + j * kWarps) * kSlotBytes, &full[warp + j * kWarps], policy);
+    }
     if (wt == 0) {
         // q's fragments: column g of each group of 8, this lane's 8 dimensions 8t.. of every block
 #pragma unroll 1
@@ -296,11 +697,8 @@ __global__ void __launch_bounds__(kAttnThreads, NB * NT <= 4 ? 3 : (NB * NT <= 8
                 for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(v[b][k]));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            // 2^e brings the column's largest magnitude into [2^13, 2^14); the scale's sign goes into q
-            int e = 13 - (static_cast<int>(__float_as_uint(top) >> 23) - 127);
-            e = min(100, max(-100, e));
-            const float up = __uint_as_float((static_cast<uint32_t>(e + 127) << 23) | (a.scale_log2 < 0.0f ? 0x80000000u : 0u));
-            const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+            float up, down;
+            q_unit(top, a.scale_log2, up, down);
             if (t == 0) sh_qs[wc][8 * nt + g] = fmaxf(fabsf(a.scale_log2) * down, 1e-37f);
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
@@ -331,7 +729,7 @@ __global__ void __launch_bounds__(kAttnThreads, NB * NT <= 4 ? 3 : (NB * NT <= 8
     // units outside low_max .. end_min need masks (warp-uniform)
     end_min = __reduce_min_sync(0xffffffffu, end_min);
     low_max = __reduce_max_sync(0xffffffffu, low_max);
-    attn_consumer_barrier();
+    attn_consumer_barrier<kWarps>();
 
     float m[NT], l[NT], qs[NT];
     uint64_t o[NT][2 * NB][2];  // columns 2t, 2t+1: dimension pairs' first and second
@@ -343,13 +741,14 @@ __global__ void __launch_bounds__(kAttnThreads, NB * NT <= 4 ? 3 : (NB * NT <= 8
 #pragma unroll
         for (int k = 0; k < 2 * NB; ++k) o[nt][k][0] = o[nt][k][1] = 0;
     }
-    int sx = 38;                          // p is in units of 2^sx ...
-    __half cap = __ushort_as_half(0x0001);  // ... |d_v| <= 2^(14 - sx), here 2^-24
+    int sx = kAttnUnit;  // p is in units of 2^sx
     bool dead = false;
+    const uint32_t magic = lds32(smem_addr(&sh_magic));
+    const uint32_t q_at = smem_addr(q_sm);
 
     int slot = wt;
     uint32_t phase = 0;
-    for (int u = wt; u < n_units; u += n_wt) {
+    for (int u = wt, j = 2; u < n_units; u += n_wt) {
         if (!__all_sync(0xffffffffu, mbar_wait(&full[slot], phase))) {
             if (lane == 0) atomicOr(a.fault, 1u);
             dead = true;
@@ -363,13 +762,13 @@ __global__ void __launch_bounds__(kAttnThreads, NB * NT <= 4 ? 3 : (NB * NT <= 8
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int h = 0; h < 4; ++h) acc[nt][h] = 0;
-        {
-            uint32_t kw[4][NB], dk[4][NB];
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {
-                const uint32_t at = tile + (h >> 1) * G::kTileBytes;
-                lds_words<NB, G::kVec>(at + ((h & 1) * NB * 32 + lane * G::kVec) * 4, 128 * G::kVec, kw[h]);
-                lds_words<NB, G::kVec>(at + G::kKScaleAt + (t + 4 * (h & 1)) * NB * 4, 4 * G::kVec, dk[h]);
+        for (int s = 0; s < 2; ++s) {
+            uint32_t kw[2][NB], dk[2][NB];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                lds_words<NB, G::kVec>(tile + s * G::kTileBytes + (h * NB * 32 + lane * G::kVec) * 4, 128 * G::kVec, kw[h]);
+                lds_words<NB, G::kVec>(tile + s * G::kTileBytes + G::kKScaleAt + (t + 4 * h) * NB * 4, 4 * G::kVec, dk[h]);
             }
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
@@ -377,21 +776,21 @@ __global__ void __launch_bounds__(kAttnThreads, NB * NT <= 4 ? 3 : (NB * NT <= 8
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int s = 0; s < 2; ++s) {
-                        const uint4 f = q_sm[(nt * 2 * NB + 2 * b + s) * 32];
-                        qa[nt][s][0] = f.x; qa[nt][s][1] = f.y; qa[nt][s][2] = f.z; qa[nt][s][3] = f.w;
+                    for (int k = 0; k < 2; ++k) {
+                        const uint4 f = lds128(q_at + (nt * 2 * NB + 2 * b + k) * 512);
+                        qa[nt][k][0] = f.x; qa[nt][k][1] = f.y; qa[nt][k][2] = f.z; qa[nt][k][3] = f.w;
                     }
 #pragma unroll
-                for (int h = 0; h < 4; ++h) {
+                for (int h = 0; h < 2; ++h) {
                     uint32_t kc[4];
-                    code_pairs(kw[h][b], kc);
+                    code_pairs(kw[h][b], magic, kc);
                     const uint64_t d = f2_half2(dk[h][b]);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                        mma_acc(c, qa[nt][0], kc[0], kc[1]);
+                        float c[4];
+                        mma_first(c, qa[nt][0], kc[0], kc[1]);
                         mma_acc(c, qa[nt][1], kc[2], kc[3]);
-                        acc[nt][h] = f2_fma(d, f2_add(f2(c[0], c[1]), f2(c[2], c[3])), acc[nt][h]);
+                        acc[nt][2 * s + h] = f2_fma(d, f2_add(f2(c[0], c[1]), f2(c[2], c[3])), acc[nt][2 * s + h]);
                     }
                 }
             }
@@ -424,30 +823,32 @@ __global__ void __launch_bounds__(kAttnThreads, NB * NT <= 4 ? 3 : (NB * NT <= 8
                 }
             }
         }
-        // ------------------------------------------------ the unit of p: the largest |d_v| so far
+        // ------------------------------------------------ the unit of p: 2^kAttnUnit while every |d_v| < 2
         {
-            __half2 big = __half2half2(__ushort_as_half(0));
+            uint32_t any = 0;
 #pragma unroll
             for (int h = 0; h < 4; ++h)
 #pragma unroll
-                for (int b = 0; b < NB; ++b) big = __hmax2(big, __habs2(*reinterpret_cast<const __half2 *>(&dv[h][b])));
-            const __half one = __hmax(__low2half(big), __high2half(big));
-            if (__any_sync(0xffffffffu, __hgt(one, cap))) {
-                const uint32_t bits = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(__half_as_ushort(one)));
-                // the power of two at or above it
-                const float f = half_lo(min(bits, 0x7bffu));
-                const int ex = static_cast<int>((__float_as_uint(f) + 0x7fffffu) >> 23) - 127;
-                const int to = 14 - ex;
-                const float keep = __uint_as_float(static_cast<uint32_t>(max(0, to - sx + 127)) << 23);
-                sx = to;
-                cap = ex >= 16 ? __ushort_as_half(0x7c00) : __float2half_rn(__uint_as_float(static_cast<uint32_t>(ex + 127) << 23));
+                for (int b = 0; b < NB; ++b) any |= dv[h][b];
+            if (__any_sync(0xffffffffu, (any & 0x40004000u) != 0)) {  // bit 14 of an fp16 number: 2 and above
+                uint32_t big = 0;
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    l[nt] *= keep;
+                for (int h = 0; h < 4; ++h)
 #pragma unroll
-                    for (int j = 0; j < 2 * NB; ++j)
+                    for (int b = 0; b < NB; ++b) big = max(big, max(dv[h][b] & 0x7fffu, (dv[h][b] >> 16) & 0x7fffu));
+                big = __reduce_max_sync(0xffffffffu, big);
+                const int to = unit_for(big);
+                if (to < sx) {
+                    const float keep = __uint_as_float(static_cast<uint32_t>(to - sx + 127) << 23);
+                    sx = to;
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) o[nt][j][i] = f2_mul(o[nt][j][i], f2(keep, keep));
+                    for (int nt = 0; nt < NT; ++nt) {
+                        l[nt] *= keep;
+#pragma unroll
+                        for (int j = 0; j < 2 * NB; ++j)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) o[nt][j][i] = f2_mul(o[nt][j][i], f2(keep, keep));
+                    }
                 }
             }
         }
@@ -479,7 +880,7 @@ __global__ void __launch_bounds__(kAttnThreads, NB * NT <= 4 ? 3 : (NB * NT <= 8
                 }
             }
         }
-        uint64_t p[NT][4];
+        uint32_t ph[NT][4], pl[NT][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const float base = m[nt] == -INFINITY ? 0.0f : m[nt] - static_cast<float>(sx);
@@ -488,7 +889,7 @@ __global__ void __launch_bounds__(kAttnThreads, NB * NT <= 4 ? 3 : (NB * NT <= 8
             for (int i = 0; i < 8; ++i) e[i] = exp2_approx(fmaf(sc[nt][i], qs[nt], -base));
             l[nt] += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
 #pragma unroll
-            for (int h = 0; h < 4; ++h) p[nt][h] = f2(e[2 * h], e[2 * h + 1]);
+            for (int h = 0; h < 4; ++h) split_f2(f2(e[2 * h], e[2 * h + 1]), ph[nt][h], pl[nt][h]);
         }
         // ------------------------------------------------ product with V
         uint32_t vw[4][NB];
@@ -502,7 +903,7 @@ __global__ void __launch_bounds__(kAttnThreads, NB * NT <= 4 ? 3 : (NB * NT <= 8
 #pragma unroll
             for (int h = 0; h < 4; ++h) {
                 uint32_t vc[4];
-                code_pairs(vw[h][j], vc);
+                code_pairs(vw[h][j], magic, vc);
                 f[h >> 1][0][2 * (h & 1)] = vc[0]; f[h >> 1][0][2 * (h & 1) + 1] = vc[1];
                 f[h >> 1][1][2 * (h & 1)] = vc[2]; f[h >> 1][1][2 * (h & 1) + 1] = vc[3];
             }
@@ -510,12 +911,15 @@ __global__ void __launch_bounds__(kAttnThreads, NB * NT <= 4 ? 3 : (NB * NT <= 8
             for (int nt = 0; nt < NT; ++nt) {
                 uint32_t hi[4], lo[4];
 #pragma unroll
-                for (int h = 0; h < 4; ++h) split_f2(f2_mul(p[nt][h], f2_half2(dv[h][j])), hi[h], lo[h]);
+                for (int h = 0; h < 4; ++h) {
+                    hi[h] = h2_mul(ph[nt][h], dv[h][j]);
+                    lo[h] = h2_fma(pl[nt][h], dv[h][j], h2_fma(ph[nt][h], dv[h][j], h2_neg(hi[h])));
+                }
                 // summed over the unit by the tensor cores (they truncate), over the units in fp32
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {
-                    float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                    mma_acc(c, f[0][s], lo[0], lo[1]);
+                    float c[4];
+                    mma_first(c, f[0][s], lo[0], lo[1]);
                     mma_acc(c, f[1][s], lo[2], lo[3]);
                     mma_acc(c, f[0][s], hi[0], hi[1]);
                     mma_acc(c, f[1][s], hi[2], hi[3]);
@@ -525,12 +929,27 @@ __global__ void __launch_bounds__(kAttnThreads, NB * NT <= 4 ? 3 : (NB * NT <= 8
             }
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&empty[slot]);
+        if constexpr (SHARED) {
+            if (lane == 0) mbar_arrive(&empty[slot]);
+        } else if (u + 2 * kWarps < n_units) {  // the warp's unit after next takes the slot's place
+            if (j == 16) {
+                j = 0;
+                feed.look(a, head, table, first + 2 * (u + 2 * kWarps + (lane >> 1) * kWarps) + (lane & 1), last, &sh_bad);
+            }
+            fence_proxy_async_smem();
+            feed.copy(j++, lane, ring + slot * kSlotBytes, &full[slot], policy);
+        }
         slot += n_wt;
-        if (slot >= a.slots) {
-            slot -= a.slots;
+        if (slot >= kSlots) {
+            slot -= kSlots;
             phase ^= 1;
         }
+    }
+
+    if (!SHARED && dead) {
+        // leave only when the warp's copies have landed (both slots: the one that failed, the one behind it)
+        for (int k = 0; k < 2; ++k)
+            if (warp + k * kWarps < n_units) (void)mbar_wait(&full[warp + k * kWarps], slot == warp + k * kWarps ? phase : phase ^ (k == 0));
     }
 
     // ------------------------------------------------ join the warps
@@ -544,7 +963,7 @@ __global__ void __launch_bounds__(kAttnThreads, NB * NT <= 4 ? 3 : (NB * NT <= 8
             sh_l[warp][8 * nt + g] = dead ? __int_as_float(0x7fffffff) : l[nt];
         }
     }
-    attn_consumer_barrier();  // every warp is done with the ring
+    attn_consumer_barrier<kWarps>();  // every warp is done with the ring
     float *sum = reinterpret_cast<float *>(ring);  // [warp][column of the warp][D]
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -566,36 +985,8 @@ __global__ void __launch_bounds__(kAttnThreads, NB * NT <= 4 ? 3 : (NB * NT <= 8
             *reinterpret_cast<float4 *>(dst + D) = make_float4(x0.y * f[1], x1.y * s1, x2.y * f[1], x3.y * s1);
         }
     }
-    attn_consumer_barrier();
-    const bool bad = r.bad || sh_bad;
-    if (r.bad && tid == 0 && a.status) *a.status = 1;
-    constexpr int kQuads = D / 4;
-    for (int k = tid; k < cols * kQuads; k += kAttnWarps * 32) {
-        const int c = k / kQuads, e = 4 * (k % kQuads);
-        const int w0 = c / (8 * NT), wcol = c % (8 * NT);
-        const int col = ct * cols + c;
-        if (col >= r.n * a.group) break;
-        float top = -INFINITY, ls = 0.0f;
-        for (int w = 0; w < n_wt; ++w) top = fmaxf(top, sh_m[w * a.wc + w0][wcol]);
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int w = 0; w < n_wt; ++w) {
-            const int ww = w * a.wc + w0;
-            ls += sh_l[ww][wcol] * (top == -INFINITY ? 1.0f : exp2_approx(sh_m[ww][wcol] - top));
-            const float4 x = *reinterpret_cast<const float4 *>(sum + (ww * NT * 8 + wcol) * D + e);
-            acc.x += x.x; acc.y += x.y; acc.z += x.z; acc.w += x.w;
-        }
-        if (bad) ls = __int_as_float(0x7fffffff);
-        if (n_splits == 1) {
-            const float inv = ls == 0.0f ? 0.0f : 1.0f / ls;
-            const int i = col / a.group;
-            float *dst = a.out + (static_cast<int64_t>(r.q0 + i) * a.n_q_heads + kvh * a.group + (col - i * a.group)) * D + e;
-            *reinterpret_cast<float4 *>(dst) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-        } else {
-            const int64_t at = (static_cast<int64_t>(item) * a.n_split + split) * cols + c;
-            *reinterpret_cast<float4 *>(a.part + at * D + e) = acc;
-            if (e == 0) a.part_ml[at] = make_float2(top, ls);
-        }
-    }
+    attn_consumer_barrier<kWarps>();
+    attn_store<D, 8 * NT, kWarps>(a, r, item, split, n_splits, cols, a.wc, sum, &sh_m[0][0], &sh_l[0][0], r.bad || sh_bad);
 }
 
 // Joins the splits of a column: out = sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s, in the splits' order. One CTA
@@ -668,24 +1059,32 @@ extern template cudaError_t launch_attn<6>(AttnArgs, const AttnPlan &, cudaStrea
 extern template cudaError_t launch_attn<8>(AttnArgs, const AttnPlan &, cudaStream_t);
 
 #ifdef ZDMMV_ATTN_INSTANTIATE
-template <int NB, int NT> cudaError_t launch_attn_nt(AttnArgs a, const AttnPlan &p, cudaStream_t st) {
-    constexpr size_t kSlot = 2 * KvGeom<NB>::kTileBytes;
-    // a ring of about 55 KB, at least two slots a warp; the join's sums lie over it
-    a.slots = static_cast<int32_t>(55 * 1024 / kSlot / kAttnWarps * kAttnWarps);
-    a.slots = a.slots < 2 * kAttnWarps ? 2 * kAttnWarps : (a.slots > kAttnMaxSlots ? kAttnMaxSlots : a.slots);
-    const size_t ring = a.slots * kSlot + static_cast<size_t>(p.wc) * NT * 2 * NB * 512;
-    const size_t join = static_cast<size_t>(kAttnWarps) * NT * 8 * NB * kQK * 4;
-    const size_t smem = kAttnBarBytes + (ring > join ? ring : join);
-    cudaError_t e = cudaFuncSetAttribute(attn_kernel<NB, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(smem));
+template <int NB>
+cudaError_t launch_attn_kernel(void (*kernel)(AttnArgs), int threads, size_t smem, const AttnArgs &a, const AttnPlan &p,
+                               cudaStream_t st) {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
-    e = launch_block_op(attn_kernel<NB, NT>, dim3(static_cast<unsigned>(p.items), p.n_split), kAttnThreads, smem, st, a);
+    e = launch_block_op(kernel, dim3(static_cast<unsigned>(p.items), p.n_split), threads, smem, st, a);
     if (e != cudaSuccess || p.n_split == 1) return e;
     return launch_block_op(attn_join_kernel<NB>, dim3(static_cast<unsigned>(p.items), p.cols), kJoinThreads, 0, st, a,
                            p.cols);
 }
+template <int NB, int NT, bool SHARED> cudaError_t launch_attn_form(const AttnArgs &a, const AttnPlan &p, cudaStream_t st) {
+    using F = AttnForm<NB, SHARED>;
+    // the join's sums lie over the ring
+    const size_t ring = F::kSlots * 2 * KvGeom<NB>::kTileBytes + static_cast<size_t>(p.wc) * NT * 2 * NB * 512;
+    const size_t join = static_cast<size_t>(F::kWarps) * NT * 8 * NB * kQK * 4;
+    return launch_attn_kernel<NB>(attn_kernel<NB, NT, SHARED>, F::kThreads, kAttnBarBytes + (ring > join ? ring : join), a,
+                                  p, st);
+}
 template <int NB> cudaError_t launch_attn(AttnArgs a, const AttnPlan &p, cudaStream_t st) {
-    return p.nt == 1 ? launch_attn_nt<NB, 1>(a, p, st) : launch_attn_nt<NB, 2>(a, p, st);
+    if (p.cols == kNarrowCols) {
+        constexpr size_t kRing = 2 * kNarrowWarps * 2 * KvGeom<NB>::kTileBytes;
+        static_assert(kRing >= kNarrowWarps * kNarrowCols * NB * kQK * 4, "the warps' sums lie over the ring");
+        return launch_attn_kernel<NB>(attn_narrow_kernel<NB>, kNarrowWarps * 32, kAttnBarBytes + kRing, a, p, st);
+    }
+    if (p.wc > 1) return launch_attn_form<NB, 2, true>(a, p, st);
+    return p.nt == 1 ? launch_attn_form<NB, 1, false>(a, p, st) : launch_attn_form<NB, 2, false>(a, p, st);
 }
 #endif
 
