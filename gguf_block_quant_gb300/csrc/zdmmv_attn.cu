@@ -11,12 +11,13 @@ namespace {
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Column tiles and splits. A warp takes 8 columns, or 16 where a kv head of a sequence has more; from 17 on the
-// warps share the columns among them. The splits: enough for a few CTAs per SM, each of kMinChunk tiles or more.
-constexpr int kMinChunk = 8;
-constexpr int kCtasWanted = 4;  // per SM
+// Column tiles and splits. Four columns or fewer take the narrow form; else a warp takes 8, or 16 where a kv head of a
+// sequence has more, and from 17 on the warps share the columns among them. The splits: with one sequence as many as
+// fill the device once; with more, whose lengths may differ, up to four times that while a split has kRaggedChunk tiles.
+constexpr int kMinChunk = 16;      // tiles: a ring slot for each of 8 warps
+constexpr int kRaggedChunk = 128;
+constexpr int kMaxSplitItems = ZDMMV_ATTN_COUNTER_BYTES / 4;  // counters of the join; more items fill the device anyway
 bool attn_plan(const KvView &c, int head_dim, int n_q_heads, int max_q_len, int64_t max_tokens, AttnPlan *out) {
-    (void)head_dim;
     static const int sms = [] {
         int dev = 0, n = 0;
         if (cudaGetDevice(&dev) != cudaSuccess ||
@@ -34,8 +35,13 @@ bool attn_plan(const KvView &c, int head_dim, int n_q_heads, int max_q_len, int6
     if (p.items > 0x7fffffff) return false;
     p.n_ct = static_cast<int>(n_ct);
     const int64_t tiles = std::max<int64_t>(1, ceil_div(max_tokens, kKvSlab));
-    const int64_t wanted = std::max<int64_t>(1, ceil_div(static_cast<int64_t>(sms) * kCtasWanted, p.items));
-    p.max_split = static_cast<int>(std::min(wanted, ceil_div(tiles, kMinChunk)));
+    // CTAs that run at once
+    const int64_t slots = static_cast<int64_t>(sms) * (p.wc > 1 ? 1 : attn_ctas_per_sm(kv_blocks(head_dim), p.nt));
+    const int64_t once = std::max<int64_t>(1, slots / p.items);
+    int64_t splits = once;
+    if (c.n_seq > 1) splits = std::max(once, std::min(ceil_div(4 * slots, p.items), ceil_div(tiles, kRaggedChunk)));
+    if (p.items > kMaxSplitItems) splits = 1;
+    p.max_split = static_cast<int>(std::min(splits, ceil_div(tiles, kMinChunk)));
     p.chunk = static_cast<int>(ceil_div(ceil_div(tiles, p.max_split), 2) * 2);  // whole ring slots
     p.n_split = static_cast<int>(ceil_div(tiles, p.chunk));
     *out = p;
@@ -44,7 +50,7 @@ bool attn_plan(const KvView &c, int head_dim, int n_q_heads, int max_q_len, int6
 
 size_t attn_workspace(const AttnPlan &p, int head_dim) {
     if (p.max_split <= 1) return 0;
-    return static_cast<size_t>(p.items) * p.max_split * p.cols * (head_dim + 2) * 4;
+    return ZDMMV_ATTN_COUNTER_BYTES + static_cast<size_t>(p.items) * p.max_split * p.cols * (head_dim + 2) * 4;
 }
 
 }  // namespace
@@ -96,7 +102,8 @@ zdmmv_status zdmmv_attn_q4_0(const zdmmv_kv_cache *cache, const zdmmv_attn_args 
     a.max_q_len = g.max_q_len; a.max_kv_len = g.max_kv_len; a.window = g.window;
     a.scale_log2 = g.scale * 1.44269504088896340736f;
     a.n_ct = p.n_ct; a.n_split = p.n_split; a.chunk = p.chunk; a.wc = p.wc;
-    a.part = static_cast<float *>(g.workspace);
+    a.count = static_cast<uint32_t *>(g.workspace);
+    a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(g.workspace) + ZDMMV_ATTN_COUNTER_BYTES);
     a.part_ml = reinterpret_cast<float2 *>(a.part + p.items * p.n_split * p.cols * cache->head_dim);
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e = cudaErrorInvalidValue;

@@ -33,7 +33,7 @@
 // producer warp copies tiles (one bulk copy each) into a ring, the consumer warps
 // split a stage's tiles among them (WC = 1) or the columns (WC = 4). Each warp has
 // its own running maximum and sums; they are joined once, at the end, through
-// shared memory, and the splits by attn_join_kernel.
+// shared memory, and the splits by the CTA of an item that finishes last.
 #pragma once
 
 #include "zdmmv_kv.cuh"
@@ -45,6 +45,7 @@ struct AttnArgs {
     const float *q;
     const int32_t *q_start, *kv_len;
     float *out;
+    uint32_t *count;    // [item]: splits that have stored their partial sums (0 between calls)
     float *part;        // partial sums [item][split][column][dim], then float2 (max, sum) [item][split][column]
     float2 *part_ml;
     int32_t *status;
@@ -57,13 +58,15 @@ struct AttnArgs {
     float scale_log2;
 };
 
-// The kernel's two forms. Own rings (wc = 1): each of 4 warps copies its own tiles into two slots of its own and waits
-// for nobody. Shared ring (wc > 1): 8 warps split the columns (and the slots among groups of them), a ninth copies.
+// The wide kernel's two forms. Own rings (wc = 1): each of 8 warps copies its own tiles into two slots of its own and
+// waits for nobody. Shared ring (wc > 1): 8 warps split the columns (and the slots among groups of them), a ninth copies.
+constexpr int kAttnWarps = 8;
 template <int NB, bool SHARED> struct AttnForm {
-    static constexpr int kWarps = SHARED ? 8 : 4;
-    static constexpr int kThreads = kWarps * 32 + (SHARED ? 32 : 0);
-    static constexpr int kSlots = SHARED ? (NB >= 8 ? 8 : 16) : 2 * kWarps;  // ring slots, a pair of tiles in each
+    static constexpr int kThreads = kAttnWarps * 32 + (SHARED ? 32 : 0);
+    static constexpr int kSlots = SHARED && NB >= 8 ? 8 : 16;  // ring slots, a pair of tiles in each
 };
+// CTAs of the forms without a shared ring that run on an SM at once.
+__host__ __device__ constexpr int attn_ctas_per_sm(int nb, int nt) { return nb * nt <= 4 ? 2 : 1; }
 constexpr int kAttnBarBytes = 256;  // two barriers a slot
 constexpr int kAttnUnit = 13;
 
@@ -210,6 +213,26 @@ __device__ __forceinline__ void split_f2(uint64_t x, uint32_t &hi, uint32_t &lo)
     lo = pack_h2(r.x, r.y);
 }
 
+// The fp32 values of a query row (column `col` of the kv head) that a lane of index t holds: dimensions 8t .. 8t+7 of
+// every block; zeros where the column is none.
+template <int NB>
+__device__ __forceinline__ void load_q(const AttnArgs &a, const AttnRange &r, int kvh, int col, int t, float (&v)[NB][8]) {
+    const int i = col / a.group;
+    const bool valid = i < r.n;
+    const float *q = a.q + static_cast<int64_t>(r.q0 + (valid ? i : 0)) * a.q_stride +
+                     static_cast<int64_t>(kvh * a.group + (valid ? col - i * a.group : 0)) * (NB * kQK) + 8 * t;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+        if (valid) {
+            x = *reinterpret_cast<const float4 *>(q + b * kQK);
+            y = *reinterpret_cast<const float4 *>(q + b * kQK + 4);
+        }
+        v[b][0] = x.x; v[b][1] = x.y; v[b][2] = x.z; v[b][3] = x.w;
+        v[b][4] = y.x; v[b][5] = y.y; v[b][6] = y.z; v[b][7] = y.w;
+    }
+}
+
 template <int WARPS> __device__ __forceinline__ void attn_consumer_barrier() {
     asm volatile("bar.sync 1, %0;" ::"n"(WARPS * 32) : "memory");
 }
@@ -229,18 +252,20 @@ __device__ __forceinline__ int unit_for(uint32_t bits) { return kAttnUnit + 15 -
 template <int NB> struct TileFeed {
     const uint8_t *src = nullptr;  // this lane's tile
     bool in = false;               // ... is one of the split's
-    __device__ void look(const AttnArgs &a, const uint8_t *head, const int32_t *table, int tile, int last, int *sh_bad) {
-        const int page_tiles = a.c.page_tokens / kKvSlab;
+    __device__ static int page_at(const AttnArgs &a, const int32_t *table, int tile) {
+        const int slot = tile / (a.c.page_tokens / kKvSlab);
+        return slot < a.c.max_pages ? table[slot] : 0;
+    }
+    __device__ void look(const AttnArgs &a, const uint8_t *head, int page, int tile, int last, int *sh_bad) {
         in = tile < last;
-        int page = in ? table[tile / page_tiles] : 0;
         const bool wrong = in && (page < 0 || page >= a.c.n_pages);
         if (wrong) {  // seen by whoever waits for the copy that follows
-            page = 0;
             *sh_bad = 1;
             if (a.status) *a.status = 1;
         }
+        if (wrong || !in) page = 0;
         __syncwarp();
-        src = head + page * a.c.page_bytes + static_cast<int64_t>(tile % page_tiles) * KvGeom<NB>::kTileBytes;
+        src = head + page * a.c.page_bytes + static_cast<int64_t>(tile % (a.c.page_tokens / kKvSlab)) * KvGeom<NB>::kTileBytes;
     }
     // unit j of the stretch into `slot`
     __device__ void copy(int j, int lane, uint8_t *slot, uint64_t *full, uint64_t policy) const {
@@ -253,38 +278,119 @@ template <int NB> struct TileFeed {
 };
 
 // The CTA's end: the warps' sums (already in the unit of their common maximum) added up, and stored as the result or,
-// where the sequence's tokens are split, as a partial one. `sum`: [warp][WCOLS][D]; m, l: [warp][WCOLS].
+// where the sequence's tokens are split, as a partial one; the split that comes last joins them all, in the splits'
+// order: out = sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s. `sum`: [warp][WCOLS][D]; m, l: [warp][WCOLS], l in the
+// common unit too.
 template <int D, int WCOLS, int WARPS>
 __device__ __forceinline__ void attn_store(const AttnArgs &a, const AttnRange &r, int item, int split, int n_splits,
-                                           int cols, int wc, const float *sum, const float *m, const float *l, bool bad) {
+                                           int cols, int wc, float *sum, const float *m, const float *l, bool bad,
+                                           int *sh_last) {
+    constexpr int kThreads = WARPS * 32, kQuads = D / 4;
+    const int tid = threadIdx.x;
     const int ct = item % a.n_ct, kvh = item / a.n_ct % a.c.n_kv_heads;
     const int n_wt = WARPS / wc;
-    if (r.bad && threadIdx.x == 0 && a.status) *a.status = 1;
-    constexpr int kQuads = D / 4;
-    for (int k = threadIdx.x; k < cols * kQuads; k += WARPS * 32) {
+    const int live = min(cols, r.n * a.group - ct * cols);  // columns that are query rows
+    if (r.bad && tid == 0 && a.status) *a.status = 1;
+    const auto row = [&](int col) {
+        const int i = col / a.group;
+        return a.out + (static_cast<int64_t>(r.q0 + i) * a.n_q_heads + kvh * a.group + (col - i * a.group)) * D;
+    };
+    const int64_t part0 = static_cast<int64_t>(item) * a.n_split * cols;
+    for (int k = tid; k < live * kQuads; k += kThreads) {
         const int c = k / kQuads, e = 4 * (k % kQuads);
         const int w0 = c / WCOLS, wcol = c % WCOLS;
-        const int col = ct * cols + c;
-        if (col >= r.n * a.group) break;
-        float top = -INFINITY, ls = 0.0f;
-        for (int w = 0; w < n_wt; ++w) top = fmaxf(top, m[(w * wc + w0) * WCOLS + wcol]);
+        float ls = 0.0f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int w = 0; w < n_wt; ++w) {
             const int at = (w * wc + w0) * WCOLS + wcol;
-            ls += l[at] * (top == -INFINITY ? 1.0f : exp2_approx(m[at] - top));
+            ls += l[at];
             const float4 x = *reinterpret_cast<const float4 *>(sum + at * D + e);
             acc.x += x.x; acc.y += x.y; acc.z += x.z; acc.w += x.w;
         }
         if (bad) ls = __int_as_float(0x7fffffff);
         if (n_splits == 1) {
             const float inv = ls == 0.0f ? 0.0f : 1.0f / ls;
-            const int i = col / a.group;
-            float *dst = a.out + (static_cast<int64_t>(r.q0 + i) * a.n_q_heads + kvh * a.group + (col - i * a.group)) * D + e;
-            *reinterpret_cast<float4 *>(dst) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+            *reinterpret_cast<float4 *>(row(ct * cols + c) + e) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
         } else {
-            const int64_t at = (static_cast<int64_t>(item) * a.n_split + split) * cols + c;
-            *reinterpret_cast<float4 *>(a.part + at * D + e) = acc;
-            if (e == 0) a.part_ml[at] = make_float2(top, ls);
+            const int64_t at = part0 + static_cast<int64_t>(split) * cols + c;
+            __stcg(reinterpret_cast<float4 *>(a.part + at * D + e), acc);
+            if (e == 0) {
+                float top = -INFINITY;
+                for (int w = 0; w < n_wt; ++w) top = fmaxf(top, m[(w * wc + w0) * WCOLS + wcol]);
+                __stcg(&a.part_ml[at], make_float2(top, ls));
+            }
+        }
+    }
+    if (n_splits == 1) return;
+    attn_consumer_barrier<WARPS>();
+    if (tid == 0) {
+        __threadfence();  // the CTA's partial sums (the barrier orders them before this) before the count
+        const bool is_last = atomicAdd(&a.count[item], 1u) == static_cast<uint32_t>(n_splits) - 1u;
+        if (is_last) a.count[item] = 0;
+        __threadfence();
+        *sh_last = is_last;
+    }
+    attn_consumer_barrier<WARPS>();
+    if (!*sh_last) return;
+    // a thread for four dimensions of a column, 8 splits' loads in flight; where that leaves threads over, groups of
+    // them share the splits
+    const int quads = live * kQuads, groups = max(1, kThreads / quads);
+    float4 *grp_sum = reinterpret_cast<float4 *>(sum);  // [group][quads], then their maxima and sums of p
+    float2 *grp_ml = reinterpret_cast<float2 *>(grp_sum + kThreads);
+    for (int k0 = 0; k0 < quads; k0 += kThreads) {
+        const int grp = groups > 1 ? tid / quads : 0, k = k0 + tid - grp * quads;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        float top = -INFINITY, ls = 0.0f;
+        const int c = k / kQuads, e = 4 * (k % kQuads);
+        if (k < quads && grp < groups) {
+            for (int s0 = grp; s0 < n_splits; s0 += 8 * groups) {
+                float2 ml[8];
+                float4 x[8];
+                float to = top;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int s = s0 + i * groups;
+                    const int64_t p = part0 + static_cast<int64_t>(s) * cols + c;
+                    ml[i] = s < n_splits ? __ldcg(&a.part_ml[p]) : make_float2(-INFINITY, 0.0f);
+                    x[i] = s < n_splits ? __ldcg(reinterpret_cast<const float4 *>(a.part + p * D + e)) : make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) to = fmaxf(to, ml[i].x);
+                const float keep = top == -INFINITY ? 0.0f : exp2_approx(top - to);
+                top = to;
+                ls *= keep;
+                acc.x *= keep; acc.y *= keep; acc.z *= keep; acc.w *= keep;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float f = ml[i].x == -INFINITY ? 0.0f : exp2_approx(ml[i].x - top);
+                    ls += f * ml[i].y;  // NaN where a split is bad, whatever its weight
+                    acc.x += f * x[i].x; acc.y += f * x[i].y; acc.z += f * x[i].z; acc.w += f * x[i].w;
+                }
+            }
+        }
+        if (groups > 1) {  // one round
+            if (grp < groups) {
+                grp_sum[tid] = acc;
+                grp_ml[tid] = make_float2(top, ls);
+            }
+            attn_consumer_barrier<WARPS>();
+            if (grp != 0) return;
+            float to = top;
+            for (int q = 1; q < groups; ++q) to = fmaxf(to, grp_ml[q * quads + k].x);
+            const float keep = top == -INFINITY ? 0.0f : exp2_approx(top - to);
+            ls *= keep;
+            acc.x *= keep; acc.y *= keep; acc.z *= keep; acc.w *= keep;
+            for (int q = 1; q < groups; ++q) {
+                const float2 ml = grp_ml[q * quads + k];
+                const float f = ml.x == -INFINITY ? 0.0f : exp2_approx(ml.x - to);
+                const float4 x = grp_sum[q * quads + k];
+                ls += f * ml.y;
+                acc.x += f * x.x; acc.y += f * x.y; acc.z += f * x.z; acc.w += f * x.w;
+            }
+        }
+        if (k < quads) {
+            const float inv = ls == 0.0f ? 0.0f : 1.0f / ls;
+            *reinterpret_cast<float4 *>(row(ct * cols + c) + e) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
         }
     }
 }
@@ -302,14 +408,14 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
-constexpr int kNarrowWarps = 4, kNarrowCols = 4;
-template <int NB> __global__ void __launch_bounds__(kNarrowWarps * 32, NB <= 4 ? 4 : 3) attn_narrow_kernel(AttnArgs a) {
+constexpr int kNarrowCols = 4;
+template <int NB> __global__ void __launch_bounds__(kAttnWarps * 32, attn_ctas_per_sm(NB, 1)) attn_narrow_kernel(AttnArgs a) {
     using G = KvGeom<NB>;
-    constexpr int D = G::kDim, kWarps = kNarrowWarps;
+    constexpr int D = G::kDim, kWarps = kAttnWarps;
     constexpr int kSlotBytes = 2 * G::kTileBytes;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float sh_m[kWarps][kNarrowCols], sh_l[kWarps][kNarrowCols];
-    __shared__ int sh_bad;
+    __shared__ int sh_bad, sh_last;
     __shared__ uint32_t sh_magic;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     uint64_t *full = reinterpret_cast<uint64_t *>(smem) + 2 * warp;  // the warp's two slots
@@ -331,6 +437,10 @@ template <int NB> __global__ void __launch_bounds__(kNarrowWarps * 32, NB <= 4 ?
     const int ct = item % a.n_ct;
     const int kvh = item / a.n_ct % a.c.n_kv_heads;
     const int seq = item / a.n_ct / a.c.n_kv_heads;
+    const int32_t *table = a.c.table + static_cast<int64_t>(seq) * a.c.max_pages;
+    // without a window the split's first tile does not hang on the lengths: the pages are looked up beside them
+    const int tile_off = split * a.chunk + 2 * (warp + (lane >> 1) * kWarps) + (lane & 1);
+    int page = a.window == 0 ? TileFeed<NB>::page_at(a, table, tile_off) : 0;
     const AttnRange r = attn_range(a, seq, ct, kNarrowCols);
     if (ct * kNarrowCols >= r.n * a.group) return;
     const int n_splits = r.splits(a.chunk);
@@ -340,35 +450,23 @@ template <int NB> __global__ void __launch_bounds__(kNarrowWarps * 32, NB <= 4 ?
     const int n_units = (last - first + 1) / 2;   // pairs of tiles
 
     const uint8_t *head = a.c.pages + static_cast<int64_t>(kvh) * (a.c.page_tokens / kKvSlab) * G::kTileBytes;
-    const int32_t *table = a.c.table + static_cast<int64_t>(seq) * a.c.max_pages;
+    const int g = lane >> 2, t = lane & 3;
+    // q: column g / 2, this lane's dimensions 8t .. 8t+7 of every block; asked for before the tiles' copies, which it
+    // would otherwise wait behind
+    float v[NB][8];
+    load_q<NB>(a, r, kvh, ct * kNarrowCols + g / 2, t, v);
     const uint64_t policy = l2_evict_first_policy();
     TileFeed<NB> feed;
-    feed.look(a, head, table, first + 2 * (warp + (lane >> 1) * kWarps) + (lane & 1), last, &sh_bad);
+    if (a.window != 0 && r.slab0 + tile_off < last) page = feed.page_at(a, table, r.slab0 + tile_off);
+    feed.look(a, head, page, r.slab0 + tile_off, last, &sh_bad);
 #pragma unroll
     for (int j = 0; j < 2; ++j)
         if (warp + j * kWarps < n_units) feed.copy(j, lane, ring + j * kSlotBytes, &full[j], policy);
 
-    const int g = lane >> 2, t = lane & 3;
-    // q's B fragments: column g / 2, its upper (g even) or lower part; this lane's dimensions 8t .. 8t+7 of every block
+    // its B fragments: the upper (g even) or lower part
     uint32_t qf[NB][4];
     float qs;
     {
-        const int col = ct * kNarrowCols + g / 2;
-        const int i = col / a.group;
-        const bool valid = i < r.n;
-        const float *q = a.q + static_cast<int64_t>(r.q0 + (valid ? i : 0)) * a.q_stride +
-                         static_cast<int64_t>(kvh * a.group + (valid ? col - i * a.group : 0)) * D + 8 * t;
-        float v[NB][8];
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-            float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
-            if (valid) {
-                x = *reinterpret_cast<const float4 *>(q + b * kQK);
-                y = *reinterpret_cast<const float4 *>(q + b * kQK + 4);
-            }
-            v[b][0] = x.x; v[b][1] = x.y; v[b][2] = x.z; v[b][3] = x.w;
-            v[b][4] = y.x; v[b][5] = y.y; v[b][6] = y.z; v[b][7] = y.w;
-        }
         float top = 0.0f;
 #pragma unroll
         for (int b = 0; b < NB; ++b)
@@ -400,9 +498,9 @@ template <int NB> __global__ void __launch_bounds__(kNarrowWarps * 32, NB <= 4 ?
     const uint32_t magic = lds32(smem_addr(&sh_magic));
     const uint32_t pick = (g & 1) ? 0x7632u : 0x5410u;  // the token's half of two words of scales
     float m = -INFINITY, l = 0.0f;
-    uint64_t o[2 * NB][2];  // dimensions 4g (4g + 2) and 4g + 1 (4g + 3) of the block, upper and lower part
+    uint64_t o[2 * NB];  // column t, dimensions 4g and 4g + 1, or 4g + 2 and 4g + 3, of the block
 #pragma unroll
-    for (int k = 0; k < 2 * NB; ++k) o[k][0] = o[k][1] = 0;
+    for (int k = 0; k < 2 * NB; ++k) o[k] = 0;
     int sx = kAttnUnit;  // p is in units of 2^sx
     bool dead = false;
 
@@ -479,10 +577,7 @@ template <int NB> __global__ void __launch_bounds__(kNarrowWarps * 32, NB <= 4 ?
                     sx = to;
                     l *= keep;
 #pragma unroll
-                    for (int k = 0; k < 2 * NB; ++k) {
-                        o[k][0] = f2_mul(o[k][0], f2(keep, keep));
-                        o[k][1] = f2_mul(o[k][1], f2(keep, keep));
-                    }
+                    for (int k = 0; k < 2 * NB; ++k) o[k] = f2_mul(o[k], f2(keep, keep));
                 }
             }
         }
@@ -498,10 +593,7 @@ template <int NB> __global__ void __launch_bounds__(kNarrowWarps * 32, NB <= 4 ?
             m = to;
             l *= keep;
 #pragma unroll
-            for (int k = 0; k < 2 * NB; ++k) {
-                o[k][0] = f2_mul(o[k][0], f2(keep, keep));
-                o[k][1] = f2_mul(o[k][1], f2(keep, keep));
-            }
+            for (int k = 0; k < 2 * NB; ++k) o[k] = f2_mul(o[k], f2(keep, keep));
         }
         const float base = m == -INFINITY ? 0.0f : m - static_cast<float>(sx);
         uint32_t p0[4], p1[4];  // rows 0 or ph, and ph or pl, of tokens 8h + 2t, + 1
@@ -536,15 +628,15 @@ template <int NB> __global__ void __launch_bounds__(kNarrowWarps * 32, NB <= 4 ?
                 float c[4];
                 mma_first(c, f[0][i], x[0], x[1]);
                 mma_acc(c, f[1][i], x[2], x[3]);
-                o[2 * j + i][0] = f2_add(o[2 * j + i][0], f2(c[0], c[1]));
-                o[2 * j + i][1] = f2_add(o[2 * j + i][1], f2(c[2], c[3]));
+                o[2 * j + i] = f2_add(o[2 * j + i], f2(c[0] + c[1], c[2] + c[3]));
             }
         }
         __syncwarp();
         if (u + 2 * kWarps < n_units) {  // the warp's unit after next takes the slot's place
             if (j_next == 16) {
                 j_next = 0;
-                feed.look(a, head, table, first + 2 * (u + 2 * kWarps + (lane >> 1) * kWarps) + (lane & 1), last, &sh_bad);
+                const int next = first + 2 * (u + 2 * kWarps + (lane >> 1) * kWarps) + (lane & 1);
+                feed.look(a, head, next < last ? feed.page_at(a, table, next) : 0, next, last, &sh_bad);
             }
             fence_proxy_async_smem();
             feed.copy(j_next++, lane, ring + slot * kSlotBytes, &full[slot], policy);
@@ -563,39 +655,36 @@ template <int NB> __global__ void __launch_bounds__(kNarrowWarps * 32, NB <= 4 ?
     l += __shfl_xor_sync(0xffffffffu, l, 8);
     l += __shfl_xor_sync(0xffffffffu, l, 16);
     m -= static_cast<float>(sx);  // the maximum in p's unit
-    if (g == 0) {
-        sh_m[warp][t] = m;
-        sh_l[warp][t] = dead ? __int_as_float(0x7fffffff) : l;
-    }
+    if (g == 0) sh_m[warp][t] = m;
     __syncthreads();  // every warp is done with its ring
     float top = -INFINITY;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sh_m[w][t]);
     const float f0 = top == -INFINITY ? 0.0f : exp2_approx(m - top), f1 = f0 * 0.0625f;
+    if (g == 0) sh_l[warp][t] = dead ? __int_as_float(0x7fffffff) : l * f0;
     float *sum = reinterpret_cast<float *>(smem + kAttnBarBytes);  // [warp][column][D]
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
-        const float2 x0 = f2_parts(o[2 * j][0]), x1 = f2_parts(o[2 * j][1]);
-        const float2 x2 = f2_parts(o[2 * j + 1][0]), x3 = f2_parts(o[2 * j + 1][1]);
+        const float2 x = f2_parts(o[2 * j]), y = f2_parts(o[2 * j + 1]);
         // the second of each pair is 16 times too large
         *reinterpret_cast<float4 *>(sum + (warp * kNarrowCols + t) * D + 4 * g + j * kQK) =
-            make_float4((x0.x + x0.y) * f0, (x1.x + x1.y) * f1, (x2.x + x2.y) * f0, (x3.x + x3.y) * f1);
+            make_float4(x.x * f0, x.y * f1, y.x * f0, y.y * f1);
     }
     __syncthreads();
     attn_store<D, kNarrowCols, kWarps>(a, r, item, split, n_splits, kNarrowCols, 1, sum, &sh_m[0][0], &sh_l[0][0],
-                                       r.bad || sh_bad);
+                                       r.bad || sh_bad, &sh_last);
 }
 
 template <int NB, int NT, bool SHARED>
-__global__ void __launch_bounds__(AttnForm<NB, SHARED>::kThreads, SHARED ? 1 : (NB * NT <= 4 ? 4 : 2)) attn_kernel(AttnArgs a) {
+__global__ void __launch_bounds__(AttnForm<NB, SHARED>::kThreads, SHARED ? 1 : attn_ctas_per_sm(NB, NT)) attn_kernel(AttnArgs a) {
     using G = KvGeom<NB>;
     using F = AttnForm<NB, SHARED>;
-    constexpr int kWarps = F::kWarps, kSlots = F::kSlots;
+    constexpr int kWarps = kAttnWarps, kSlots = F::kSlots;
     constexpr int D = G::kDim;
     constexpr int kSlotBytes = 2 * G::kTileBytes;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float sh_m[kWarps][NT * 8], sh_l[kWarps][NT * 8], sh_qs[kWarps][NT * 8];
-    __shared__ int sh_bad;
+    __shared__ int sh_bad, sh_last;
     __shared__ uint32_t sh_magic;
     uint64_t *full = reinterpret_cast<uint64_t *>(smem);
     uint64_t *empty = full + kSlots;
@@ -638,7 +727,8 @@ __global__ void __launch_bounds__(AttnForm<NB, SHARED>::kThreads, SHARED ? 1 : (
         bool ok = true;
         int u = 0;
         for (int u0 = 0; u0 < n_units && ok; u0 += 16) {
-            feed.look(a, head, table, first + 2 * u0 + lane, last, &sh_bad);
+            const int tile = first + 2 * u0 + lane;
+            feed.look(a, head, tile < last ? feed.page_at(a, table, tile) : 0, tile, last, &sh_bad);
             for (; u < min(n_units, u0 + 16); ++u) {
                 const int s = u % kSlots;
                 if (u >= kSlots) {
@@ -663,55 +753,40 @@ __global__ void __launch_bounds__(AttnForm<NB, SHARED>::kThreads, SHARED ? 1 : (
     const int wc = warp % a.wc, wt = warp / a.wc, n_wt = kWarps / a.wc;
     const int col0 = ct * cols + wc * 8 * NT;  // the warp's first column
     uint4 *q_sm = reinterpret_cast<uint4 *>(ring + kSlots * kSlotBytes) + wc * (NT * 2 * NB * 32) + lane;
+    // q's fragments: column g of each group of 8, this lane's 8 dimensions 8t.. of every block
+#pragma unroll 1
+    for (int nt = wt; nt < NT; nt += n_wt) {
+        float v[NB][8];
+        load_q<NB>(a, r, kvh, col0 + 8 * nt + g, t, v);
+        float top = 0.0f;
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(v[b][k]));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        float up, down;
+        q_unit(top, a.scale_log2, up, down);
+        if (t == 0) sh_qs[wc][8 * nt + g] = fmaxf(fabsf(a.scale_log2) * down, 1e-37f);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                // k slots: the codes at bits 0 and 16 of the (shifted) word, then those at bits 4 and 20
+                uint4 f;
+                split_h2(v[b][2 * h] * up, v[b][2 * h + 4] * up, f.x, f.y);
+                split_h2(v[b][2 * h + 1] * up * 0.0625f, v[b][2 * h + 5] * up * 0.0625f, f.z, f.w);
+                q_sm[(nt * 2 * NB + 2 * b + h) * 32] = f;
+            }
+        }
+    }
     if constexpr (!SHARED) {
-        feed.look(a, head, table, first + 2 * (warp + (lane >> 1) * kWarps) + (lane & 1), last, &sh_bad);
+        const int tile = first + 2 * (warp + (lane >> 1) * kWarps) + (lane & 1);
+        feed.look(a, head, tile < last ? feed.page_at(a, table, tile) : 0, tile, last, &sh_bad);
 #pragma unroll
         for (int j = 0; j < 2; ++j)
             if (warp + j * kWarps < n_units)
                 feed.copy(j, lane, ring + (warp + j * kWarps) * kSlotBytes, &full[warp + j * kWarps], policy);
-    }
-    if (wt == 0) {
-        // q's fragments: column g of each group of 8, this lane's 8 dimensions 8t.. of every block
-#pragma unroll 1
-        for (int nt = 0; nt < NT; ++nt) {
-            const int col = col0 + 8 * nt + g;
-            const int i = col / a.group;
-            const bool valid = i < r.n;
-            const float *q = a.q + static_cast<int64_t>(r.q0 + (valid ? i : 0)) * a.q_stride +
-                             static_cast<int64_t>(kvh * a.group + (valid ? col - i * a.group : 0)) * D + 8 * t;
-            float v[NB][8];
-            float top = 0.0f;
-#pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
-                if (valid) {
-                    x = *reinterpret_cast<const float4 *>(q + b * kQK);
-                    y = *reinterpret_cast<const float4 *>(q + b * kQK + 4);
-                }
-                v[b][0] = x.x; v[b][1] = x.y; v[b][2] = x.z; v[b][3] = x.w;
-                v[b][4] = y.x; v[b][5] = y.y; v[b][6] = y.z; v[b][7] = y.w;
-            }
-#pragma unroll
-            for (int b = 0; b < NB; ++b)
-#pragma unroll
-                for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(v[b][k]));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            float up, down;
-            q_unit(top, a.scale_log2, up, down);
-            if (t == 0) sh_qs[wc][8 * nt + g] = fmaxf(fabsf(a.scale_log2) * down, 1e-37f);
-#pragma unroll
-            for (int b = 0; b < NB; ++b) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    // k slots: the codes at bits 0 and 16 of the (shifted) word, then those at bits 4 and 20
-                    uint4 f;
-                    split_h2(v[b][2 * h] * up, v[b][2 * h + 4] * up, f.x, f.y);
-                    split_h2(v[b][2 * h + 1] * up * 0.0625f, v[b][2 * h + 5] * up * 0.0625f, f.z, f.w);
-                    q_sm[(nt * 2 * NB + 2 * b + h) * 32] = f;
-                }
-            }
-        }
     }
     // what each column sees, of this split's tiles
     int end[NT], low[NT];
@@ -748,7 +823,7 @@ __global__ void __launch_bounds__(AttnForm<NB, SHARED>::kThreads, SHARED ? 1 : (
 
     int slot = wt;
     uint32_t phase = 0;
-    for (int u = wt, j = 2; u < n_units; u += n_wt) {
+    for (int u = wt, j_next = 2; u < n_units; u += n_wt) {
         if (!__all_sync(0xffffffffu, mbar_wait(&full[slot], phase))) {
             if (lane == 0) atomicOr(a.fault, 1u);
             dead = true;
@@ -932,12 +1007,13 @@ __global__ void __launch_bounds__(AttnForm<NB, SHARED>::kThreads, SHARED ? 1 : (
         if constexpr (SHARED) {
             if (lane == 0) mbar_arrive(&empty[slot]);
         } else if (u + 2 * kWarps < n_units) {  // the warp's unit after next takes the slot's place
-            if (j == 16) {
-                j = 0;
-                feed.look(a, head, table, first + 2 * (u + 2 * kWarps + (lane >> 1) * kWarps) + (lane & 1), last, &sh_bad);
+            if (j_next == 16) {
+                j_next = 0;
+                const int next = first + 2 * (u + 2 * kWarps + (lane >> 1) * kWarps) + (lane & 1);
+                feed.look(a, head, next < last ? feed.page_at(a, table, next) : 0, next, last, &sh_bad);
             }
             fence_proxy_async_smem();
-            feed.copy(j++, lane, ring + slot * kSlotBytes, &full[slot], policy);
+            feed.copy(j_next++, lane, ring + slot * kSlotBytes, &full[slot], policy);
         }
         slot += n_wt;
         if (slot >= kSlots) {
@@ -958,23 +1034,18 @@ __global__ void __launch_bounds__(AttnForm<NB, SHARED>::kThreads, SHARED ? 1 : (
         l[nt] += __shfl_xor_sync(0xffffffffu, l[nt], 1);
         l[nt] += __shfl_xor_sync(0xffffffffu, l[nt], 2);
         m[nt] -= static_cast<float>(sx);  // the maximum in p's unit
-        if (t == 0) {
-            sh_m[warp][8 * nt + g] = m[nt];
-            sh_l[warp][8 * nt + g] = dead ? __int_as_float(0x7fffffff) : l[nt];
-        }
+        if (t == 0) sh_m[warp][8 * nt + g] = m[nt];
     }
     attn_consumer_barrier<kWarps>();  // every warp is done with the ring
     float *sum = reinterpret_cast<float *>(ring);  // [warp][column of the warp][D]
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-        float f[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int c = 8 * nt + 2 * t + h;
-            float top = -INFINITY;
-            for (int w = 0; w < n_wt; ++w) top = fmaxf(top, sh_m[w * a.wc + wc][c]);
-            f[h] = top == -INFINITY ? 0.0f : exp2_approx(sh_m[warp][c] - top);
-        }
+        // this warp's sums in the unit of the warps' common maximum: the lane's column g, columns 2t and 2t + 1 of o
+        float top = -INFINITY;
+        for (int w = 0; w < n_wt; ++w) top = fmaxf(top, sh_m[w * a.wc + wc][8 * nt + g]);
+        const float fg = top == -INFINITY ? 0.0f : exp2_approx(m[nt] - top);
+        if (t == 0) sh_l[warp][8 * nt + g] = dead ? __int_as_float(0x7fffffff) : l[nt] * fg;
+        const float f[2] = {__shfl_sync(0xffffffffu, fg, 8 * t), __shfl_sync(0xffffffffu, fg, 8 * t + 4)};
 #pragma unroll
         for (int j = 0; j < NB; ++j) {
             const float2 x0 = f2_parts(o[nt][2 * j][0]), x1 = f2_parts(o[nt][2 * j][1]);
@@ -986,60 +1057,8 @@ __global__ void __launch_bounds__(AttnForm<NB, SHARED>::kThreads, SHARED ? 1 : (
         }
     }
     attn_consumer_barrier<kWarps>();
-    attn_store<D, 8 * NT, kWarps>(a, r, item, split, n_splits, cols, a.wc, sum, &sh_m[0][0], &sh_l[0][0], r.bad || sh_bad);
-}
-
-// Joins the splits of a column: out = sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s, in the splits' order. One CTA
-// a column; groups of D/4 threads take every n-th split.
-constexpr int kJoinThreads = 128;
-template <int NB> __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(AttnArgs a, int cols) {
-    constexpr int D = NB * kQK, kQuads = D / 4, kGroups = kJoinThreads / kQuads;
-    __shared__ float4 sum[kGroups][kQuads];
-    __shared__ float sum_l[kGroups], tops[kJoinThreads / 32];
-    block_op_wait();
-    block_op_release();
-    const int item = blockIdx.x, c = blockIdx.y;
-    const int ct = item % a.n_ct;
-    const int kvh = item / a.n_ct % a.c.n_kv_heads;
-    const int seq = item / a.n_ct / a.c.n_kv_heads;
-    const AttnRange r = attn_range(a, seq, ct, cols);
-    const int col = ct * cols + c;
-    const int n = r.splits(a.chunk);
-    if (n == 1 || col >= r.n * a.group) return;
-    const int64_t at = static_cast<int64_t>(item) * a.n_split * cols + c;
-    float top = -INFINITY;
-    for (int s = threadIdx.x; s < n; s += kJoinThreads) top = fmaxf(top, a.part_ml[at + static_cast<int64_t>(s) * cols].x);
-    for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
-    if ((threadIdx.x & 31) == 0) tops[threadIdx.x >> 5] = top;
-    __syncthreads();
-    for (int k = 0; k < kJoinThreads / 32; ++k) top = fmaxf(top, tops[k]);
-    const int grp = threadIdx.x / kQuads, e = threadIdx.x % kQuads;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float ls = 0.0f;
-    if (grp < kGroups) {
-#pragma unroll 4
-        for (int s = grp; s < n; s += kGroups) {
-            const int64_t p = at + static_cast<int64_t>(s) * cols;
-            const float2 ml = a.part_ml[p];
-            const float f = top == -INFINITY ? 0.0f : exp2_approx(ml.x - top);
-            const float4 x = *reinterpret_cast<const float4 *>(a.part + p * D + 4 * e);
-            ls += f * ml.y;
-            acc.x += f * x.x; acc.y += f * x.y; acc.z += f * x.z; acc.w += f * x.w;
-        }
-        sum[grp][e] = acc;
-        if (e == 0) sum_l[grp] = ls;
-    }
-    __syncthreads();
-    if (grp != 0) return;
-    for (int k = 1; k < kGroups; ++k) {
-        const float4 x = sum[k][e];
-        acc.x += x.x; acc.y += x.y; acc.z += x.z; acc.w += x.w;
-        ls += sum_l[k];
-    }
-    const float inv = ls == 0.0f ? 0.0f : 1.0f / ls;
-    const int i = col / a.group;
-    float *dst = a.out + (static_cast<int64_t>(r.q0 + i) * a.n_q_heads + kvh * a.group + (col - i * a.group)) * D + 4 * e;
-    *reinterpret_cast<float4 *>(dst) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+    attn_store<D, 8 * NT, kWarps>(a, r, item, split, n_splits, cols, a.wc, sum, &sh_m[0][0], &sh_l[0][0], r.bad || sh_bad,
+                                  &sh_last);
 }
 
 // ------------------------------------------------------------------ host side
@@ -1064,24 +1083,21 @@ cudaError_t launch_attn_kernel(void (*kernel)(AttnArgs), int threads, size_t sme
                                cudaStream_t st) {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
-    e = launch_block_op(kernel, dim3(static_cast<unsigned>(p.items), p.n_split), threads, smem, st, a);
-    if (e != cudaSuccess || p.n_split == 1) return e;
-    return launch_block_op(attn_join_kernel<NB>, dim3(static_cast<unsigned>(p.items), p.cols), kJoinThreads, 0, st, a,
-                           p.cols);
+    return launch_block_op(kernel, dim3(static_cast<unsigned>(p.items), p.n_split), threads, smem, st, a);
 }
 template <int NB, int NT, bool SHARED> cudaError_t launch_attn_form(const AttnArgs &a, const AttnPlan &p, cudaStream_t st) {
     using F = AttnForm<NB, SHARED>;
     // the join's sums lie over the ring
     const size_t ring = F::kSlots * 2 * KvGeom<NB>::kTileBytes + static_cast<size_t>(p.wc) * NT * 2 * NB * 512;
-    const size_t join = static_cast<size_t>(F::kWarps) * NT * 8 * NB * kQK * 4;
+    const size_t join = static_cast<size_t>(kAttnWarps) * NT * 8 * NB * kQK * 4;
     return launch_attn_kernel<NB>(attn_kernel<NB, NT, SHARED>, F::kThreads, kAttnBarBytes + (ring > join ? ring : join), a,
                                   p, st);
 }
 template <int NB> cudaError_t launch_attn(AttnArgs a, const AttnPlan &p, cudaStream_t st) {
     if (p.cols == kNarrowCols) {
-        constexpr size_t kRing = 2 * kNarrowWarps * 2 * KvGeom<NB>::kTileBytes;
-        static_assert(kRing >= kNarrowWarps * kNarrowCols * NB * kQK * 4, "the warps' sums lie over the ring");
-        return launch_attn_kernel<NB>(attn_narrow_kernel<NB>, kNarrowWarps * 32, kAttnBarBytes + kRing, a, p, st);
+        constexpr size_t kRing = 2 * kAttnWarps * 2 * KvGeom<NB>::kTileBytes;
+        static_assert(kRing >= kAttnWarps * kNarrowCols * NB * kQK * 4, "the warps' sums lie over the ring");
+        return launch_attn_kernel<NB>(attn_narrow_kernel<NB>, kAttnWarps * 32, kAttnBarBytes + kRing, a, p, st);
     }
     if (p.wc > 1) return launch_attn_form<NB, 2, true>(a, p, st);
     return p.nt == 1 ? launch_attn_form<NB, 1, false>(a, p, st) : launch_attn_form<NB, 2, false>(a, p, st);

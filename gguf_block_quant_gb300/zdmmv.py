@@ -434,15 +434,15 @@ def _i32(t: torch.Tensor, n: int, what: str) -> int:
     return _ptr(t)
 
 
-def _make(shape, dtype, device, stream):
-    """An empty tensor for a call on `stream`: of that stream's memory, so that it is not
+def _make(shape, dtype, device, stream, how=torch.empty):
+    """A tensor for a call on `stream`: of that stream's memory, so that it is not
     handed out again while the call may still be using it."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return how(shape, dtype=dtype, device=device)
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return how(shape, dtype=dtype, device=device)
 
 
 def add_rmsnorm_q8_0(x, weight, eps: float, residual=None, out=None, xq=None, y=None, stream=None):
@@ -529,9 +529,10 @@ def attn_q4_0_workspace_bytes(cache: KVCache, n_q_heads: int, max_q_len: int, ma
 
 
 def attn_q4_0_workspace(cache: KVCache, n_q_heads: int, max_q_len: int, max_kv_len: int):
-    """A workspace for attn_q4_0 calls of these bounds (one call in flight at a time)."""
+    """A workspace for attn_q4_0 calls of these bounds or smaller ones, one in flight at a time (zeros: its counters
+    start at zero, and every call leaves them so)."""
     n = attn_q4_0_workspace_bytes(cache, n_q_heads, max_q_len, max_kv_len)
-    return torch.empty(n, dtype=torch.uint8, device=cache.pages.device)
+    return torch.zeros(n, dtype=torch.uint8, device=cache.pages.device)
 
 
 def attn_q4_0(cache: KVCache, q, q_start, kv_len, max_q_len: int, max_kv_len: int, scale: float | None = None,
@@ -547,7 +548,8 @@ def attn_q4_0(cache: KVCache, q, q_start, kv_len, max_q_len: int, max_kv_len: in
         out = _make((n_tok, heads, dim), torch.float32, q.device, stream)
     _check(out.dtype == torch.float32 and out.numel() == n_tok * width, "attn_q4_0: out must be float32, q's size")
     if workspace is None:
-        workspace = _make(attn_q4_0_workspace_bytes(cache, heads, max_q_len, max_kv_len), torch.uint8, q.device, stream)
+        workspace = _make(attn_q4_0_workspace_bytes(cache, heads, max_q_len, max_kv_len), torch.uint8, q.device, stream,
+                          torch.zeros)
     a = _AttnArgs(q=_rows_of(q, width, "q"), q_start=_i32(q_start, cache.n_seq + 1, "q_start"),
                   kv_len=_i32(kv_len, cache.n_seq, "kv_len"), out=_ptr(out), workspace=_ptr(workspace),
                   workspace_bytes=_nbytes(workspace), q_stride=_stride_of(q, width), n_tok=n_tok, n_q_heads=heads,

@@ -646,8 +646,12 @@ typedef struct {
     const int32_t *q_start;  /* device int32 [n_seq+1], rising from 0 to n_tok */
     const int32_t *kv_len;   /* device int32 [n_seq], the new tokens included */
     float *out;              /* device fp32 [n_tok][n_q_heads][head_dim], contiguous */
-    void *workspace;         /* device, 16-byte aligned, >= zdmmv_attn_q4_0_workspace_bytes; NULL
-                                where that is 0; needs no initial contents; one per call in flight */
+    void *workspace;         /* device, 16-byte aligned, >= zdmmv_attn_q4_0_workspace_bytes, its first
+                                ZDMMV_ATTN_COUNTER_BYTES bytes ZERO before its first use (every
+                                call leaves them zero again); NULL where that size is 0. One
+                                workspace per call in flight; calls of any sizes may follow one
+                                another on it. After a call that reported
+                                ZDMMV_FAULT_WAIT_TIMEOUT, zero them again */
     int32_t *status_dev;     /* nullable device int32: 1 is stored for a bad sequence (below) */
     size_t workspace_bytes;
     int64_t q_stride;        /* floats, a multiple of 4, >= n_q_heads*head_dim */
@@ -667,6 +671,7 @@ typedef struct {
  * out of range. Tokens at and past kv_len may hold anything. Deterministic from
  * call to call with the same max_q_len and max_kv_len.
  * Errors: ERR_NULL, ERR_SHAPE, ERR_ALIGN, ERR_SIZE, ERR_CUDA. */
+#define ZDMMV_ATTN_COUNTER_BYTES 8192
 size_t zdmmv_attn_q4_0_workspace_bytes(const zdmmv_kv_cache *cache, int n_q_heads, int max_q_len,
                                        int max_kv_len);
 zdmmv_status zdmmv_attn_q4_0(const zdmmv_kv_cache *cache, const zdmmv_attn_args *args,

@@ -86,10 +86,23 @@ def test_append_checks(L, code, change):
     (1, dict(q=None)), (1, dict(q_start=None)), (1, dict(kv_len=None)), (1, dict(out=None)),
     (3, dict(q=FAKE + 4)), (3, dict(out=FAKE + 8)), (3, dict(q_start=FAKE + 1)), (3, dict(kv_len=FAKE + 2)),
     (3, dict(workspace=FAKE + 8)), (3, dict(status_dev=FAKE + 2)), (3, dict(q_stride=1026)),
+    (1, dict(workspace=None, max_kv_len=100000)), (6, dict(workspace_bytes=8192, max_kv_len=100000)),
     (0, dict(n_tok=0, q=None)),
 ])
 def test_attention_checks(L, code, change):
     assert L.zdmmv_attn_q4_0(ctypes.byref(_cache()), ctypes.byref(_attn(**change)), None) == code
+
+
+def test_attention_workspace_grows_with_the_bounds(L):
+    c = _cache(max_pages=1 << 16)
+    size = lambda heads, new, most: L.zdmmv_attn_q4_0_workspace_bytes(ctypes.byref(c), heads, new, most)  # noqa: E731
+    assert size(8, 1, 16) == 0                                   # one split: none needed
+    last = 0
+    for most in (1000, 1001, 5000, 20000, 20016, 65536, 1 << 20):
+        assert size(8, 1, most) >= last >= 0
+        last = size(8, 1, most)
+    assert last > 8192
+    assert size(7, 1, 1000) == 0 and size(8, 0, 1000) == 0       # refused shapes
 
 
 def test_null_structs(L):

@@ -359,6 +359,27 @@ def test_attention_strides_streams_graphs_and_repeats():
         assert torch.equal(o2, Z.attn_q4_0(cache, q2, qs, kv, 1, 900))
 
 
+def test_attention_workspace_is_shared_by_calls_of_any_size():
+    """One workspace, garbage behind its counters, calls of different shapes one after another: each as on its own."""
+    rng = np.random.default_rng(12)
+    shapes = [([5000], [1], 2, 4, 128, 0), ([900, 40, 2500], [1, 1, 1], 1, 8, 64, 0), ([3000, 700], [9, 40], 2, 4, 128, 0),
+              ([6000], [1], 1, 2, 256, 1500), ([2000, 2100], [3, 1], 1, 5, 96, 0)]
+    cases = []
+    for lens, new, heads, group, dim, window in shapes:
+        cache, _, _ = random_cache(rng, lens, 64, heads, dim)
+        q_start = dev(np.concatenate(([0], np.cumsum(new))).astype(np.int32))
+        q = torch.randn(sum(new), heads * group, dim, device="cuda", generator=torch.Generator("cuda").manual_seed(len(cases)))
+        cases.append((cache, q, q_start, dev(np.array(lens, np.int32)), max(new), max(lens), window))
+    alone = [Z.attn_q4_0(c, q, s, n, a, b, window=w) for c, q, s, n, a, b, w in cases]
+    size = max(Z.attn_q4_0_workspace_bytes(c, q.shape[1], a, b) for c, q, s, n, a, b, w in cases)
+    ws = torch.full((size,), 0xFF, dtype=torch.uint8, device="cuda")
+    ws[:8192] = 0
+    for _ in range(2):
+        for (c, q, s, n, a, b, w), want in zip(cases, alone):
+            assert torch.equal(Z.attn_q4_0(c, q, s, n, a, b, window=w, workspace=ws), want)
+    assert not ws[:8192].any()
+
+
 def test_caches_past_four_gigabytes():
     page, heads, dim = 1024, 4, 256
     per = Z.kv_page_bytes(page, heads, dim)
