@@ -32,7 +32,7 @@ bool attn_plan(const KvView &c, int head_dim, int n_q_heads, int max_q_len, int6
     p.cols = columns <= kNarrowCols ? kNarrowCols : 8 * p.nt * p.wc;
     const int64_t n_ct = ceil_div(columns, p.cols);
     p.items = static_cast<int64_t>(c.n_seq) * c.n_kv_heads * n_ct;
-    if (p.items > 0x7fffffff) return false;
+    if (p.items > 0x7fffffff || columns > 0x7fffff00) return false;
     p.n_ct = static_cast<int>(n_ct);
     const int64_t tiles = std::max<int64_t>(1, ceil_div(max_tokens, kKvSlab));
     // CTAs that run at once
@@ -101,6 +101,10 @@ zdmmv_status zdmmv_attn_q4_0(const zdmmv_kv_cache *cache, const zdmmv_attn_args 
     a.n_tok = g.n_tok; a.n_q_heads = g.n_q_heads; a.group = g.n_q_heads / cache->n_kv_heads;
     a.max_q_len = g.max_q_len; a.max_kv_len = g.max_kv_len; a.window = g.window;
     a.scale_log2 = g.scale * 1.44269504088896340736f;
+    a.by_ct = FastDiv::of(p.n_ct);
+    a.by_heads = FastDiv::of(cache->n_kv_heads);
+    a.by_group = FastDiv::of(a.group);
+    a.by_page_tiles = FastDiv::of(cache->page_tokens / kKvSlab);
     a.n_ct = p.n_ct; a.n_split = p.n_split; a.chunk = p.chunk; a.wc = p.wc;
     a.count = static_cast<uint32_t *>(g.workspace);
     a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(g.workspace) + ZDMMV_ATTN_COUNTER_BYTES);

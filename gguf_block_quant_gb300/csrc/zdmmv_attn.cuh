@@ -40,8 +40,25 @@
 
 namespace zdmmv {
 
+// n / d and n % d for 0 <= n < 2^31 by a multiplication: q = n * ceil(2^p / d) >> p with p = 31 + ceil(log2 d), exact
+// there (the product's error is below n / 2^p <= 1 / d).
+struct FastDiv {
+    uint32_t d, m, p;
+    __host__ static FastDiv of(int32_t d) {
+        FastDiv f{static_cast<uint32_t>(d), 0, 31};
+        while ((1ull << (f.p - 31)) < f.d) ++f.p;
+        f.m = static_cast<uint32_t>(((1ull << f.p) + f.d - 1) / f.d);
+        return f;
+    }
+    __device__ __forceinline__ int div(int n) const {
+        return static_cast<int>(static_cast<uint64_t>(static_cast<uint32_t>(n)) * m >> p);
+    }
+    __device__ __forceinline__ int mod(int n, int q) const { return n - q * static_cast<int>(d); }
+};
+
 struct AttnArgs {
     KvView c;
+    FastDiv by_ct, by_heads, by_group, by_page_tiles;
     const float *q;
     const int32_t *q_start, *kv_len;
     float *out;
@@ -69,6 +86,7 @@ template <int NB, bool SHARED> struct AttnForm {
 __host__ __device__ constexpr int attn_ctas_per_sm(int nb, int nt) { return nb * nt <= 4 ? 2 : 1; }
 constexpr int kAttnBarBytes = 256;  // two barriers a slot
 constexpr int kAttnUnit = 13;
+constexpr int kJoinAhead = 16;
 
 // What a CTA (and the join) works on, from the lengths on the device.
 struct AttnRange {
@@ -86,7 +104,7 @@ __device__ __forceinline__ AttnRange attn_range(const AttnArgs &a, int seq, int 
             r.len > static_cast<int64_t>(a.c.max_pages) * a.c.page_tokens;
     r.q0 = min(max(q0, 0), a.n_tok);
     r.n = max(0, min(q1, a.n_tok) - r.q0);
-    const int i0 = ct * cols / a.group, i1 = min(r.n - 1, (ct * cols + cols - 1) / a.group);
+    const int i0 = a.by_group.div(ct * cols), i1 = min(r.n - 1, a.by_group.div(ct * cols + cols - 1));
     const int end = max(0, r.len - (r.n - 1 - i1));
     const int low = a.window > 0 ? max(0, r.len - (r.n - 1 - i0) - a.window) : 0;
     r.slab0 = low / kKvSlab;
@@ -217,7 +235,7 @@ __device__ __forceinline__ void split_f2(uint64_t x, uint32_t &hi, uint32_t &lo)
 // every block; zeros where the column is none.
 template <int NB>
 __device__ __forceinline__ void load_q(const AttnArgs &a, const AttnRange &r, int kvh, int col, int t, float (&v)[NB][8]) {
-    const int i = col / a.group;
+    const int i = a.by_group.div(col);
     const bool valid = i < r.n;
     const float *q = a.q + static_cast<int64_t>(r.q0 + (valid ? i : 0)) * a.q_stride +
                      static_cast<int64_t>(kvh * a.group + (valid ? col - i * a.group : 0)) * (NB * kQK) + 8 * t;
@@ -253,7 +271,7 @@ template <int NB> struct TileFeed {
     const uint8_t *src = nullptr;  // this lane's tile
     bool in = false;               // ... is one of the split's
     __device__ static int page_at(const AttnArgs &a, const int32_t *table, int tile) {
-        const int slot = tile / (a.c.page_tokens / kKvSlab);
+        const int slot = a.by_page_tiles.div(tile);
         return slot < a.c.max_pages ? table[slot] : 0;
     }
     __device__ void look(const AttnArgs &a, const uint8_t *head, int page, int tile, int last, int *sh_bad) {
@@ -265,7 +283,8 @@ template <int NB> struct TileFeed {
         }
         if (wrong || !in) page = 0;
         __syncwarp();
-        src = head + page * a.c.page_bytes + static_cast<int64_t>(tile % (a.c.page_tokens / kKvSlab)) * KvGeom<NB>::kTileBytes;
+        src = head + page * a.c.page_bytes +
+              static_cast<int64_t>(a.by_page_tiles.mod(tile, a.by_page_tiles.div(tile))) * KvGeom<NB>::kTileBytes;
     }
     // unit j of the stretch into `slot`
     __device__ void copy(int j, int lane, uint8_t *slot, uint64_t *full, uint64_t policy) const {
@@ -287,12 +306,13 @@ __device__ __forceinline__ void attn_store(const AttnArgs &a, const AttnRange &r
                                            int *sh_last) {
     constexpr int kThreads = WARPS * 32, kQuads = D / 4;
     const int tid = threadIdx.x;
-    const int ct = item % a.n_ct, kvh = item / a.n_ct % a.c.n_kv_heads;
+    const int sh = a.by_ct.div(item), ct = a.by_ct.mod(item, sh);
+    const int kvh = a.by_heads.mod(sh, a.by_heads.div(sh));
     const int n_wt = WARPS / wc;
     const int live = min(cols, r.n * a.group - ct * cols);  // columns that are query rows
     if (r.bad && tid == 0 && a.status) *a.status = 1;
     const auto row = [&](int col) {
-        const int i = col / a.group;
+        const int i = a.by_group.div(col);
         return a.out + (static_cast<int64_t>(r.q0 + i) * a.n_q_heads + kvh * a.group + (col - i * a.group)) * D;
     };
     const int64_t part0 = static_cast<int64_t>(item) * a.n_split * cols;
@@ -324,15 +344,16 @@ __device__ __forceinline__ void attn_store(const AttnArgs &a, const AttnRange &r
     if (n_splits == 1) return;
     attn_consumer_barrier<WARPS>();
     if (tid == 0) {
-        __threadfence();  // the CTA's partial sums (the barrier orders them before this) before the count
-        const bool is_last = atomicAdd(&a.count[item], 1u) == static_cast<uint32_t>(n_splits) - 1u;
+        // releases the CTA's partial sums (which the barrier orders before it), acquires the others'
+        uint32_t before;
+        asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(before) : "l"(a.count + item) : "memory");
+        const bool is_last = before == static_cast<uint32_t>(n_splits) - 1u;
         if (is_last) a.count[item] = 0;
-        __threadfence();
         *sh_last = is_last;
     }
     attn_consumer_barrier<WARPS>();
     if (!*sh_last) return;
-    // a thread for four dimensions of a column, 8 splits' loads in flight; where that leaves threads over, groups of
+    // a thread for four dimensions of a column, kJoinAhead splits' loads in flight; where that leaves threads over, groups of
     // them share the splits
     const int quads = live * kQuads, groups = max(1, kThreads / quads);
     float4 *grp_sum = reinterpret_cast<float4 *>(sum);  // [group][quads], then their maxima and sums of p
@@ -343,25 +364,25 @@ __device__ __forceinline__ void attn_store(const AttnArgs &a, const AttnRange &r
         float top = -INFINITY, ls = 0.0f;
         const int c = k / kQuads, e = 4 * (k % kQuads);
         if (k < quads && grp < groups) {
-            for (int s0 = grp; s0 < n_splits; s0 += 8 * groups) {
-                float2 ml[8];
-                float4 x[8];
+            for (int s0 = grp; s0 < n_splits; s0 += kJoinAhead * groups) {
+                float2 ml[kJoinAhead];
+                float4 x[kJoinAhead];
                 float to = top;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
+                for (int i = 0; i < kJoinAhead; ++i) {
                     const int s = s0 + i * groups;
                     const int64_t p = part0 + static_cast<int64_t>(s) * cols + c;
                     ml[i] = s < n_splits ? __ldcg(&a.part_ml[p]) : make_float2(-INFINITY, 0.0f);
                     x[i] = s < n_splits ? __ldcg(reinterpret_cast<const float4 *>(a.part + p * D + e)) : make_float4(0.f, 0.f, 0.f, 0.f);
                 }
 #pragma unroll
-                for (int i = 0; i < 8; ++i) to = fmaxf(to, ml[i].x);
+                for (int i = 0; i < kJoinAhead; ++i) to = fmaxf(to, ml[i].x);
                 const float keep = top == -INFINITY ? 0.0f : exp2_approx(top - to);
                 top = to;
                 ls *= keep;
                 acc.x *= keep; acc.y *= keep; acc.z *= keep; acc.w *= keep;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
+                for (int i = 0; i < kJoinAhead; ++i) {
                     const float f = ml[i].x == -INFINITY ? 0.0f : exp2_approx(ml[i].x - top);
                     ls += f * ml[i].y;  // NaN where a split is bad, whatever its weight
                     acc.x += f * x[i].x; acc.y += f * x[i].y; acc.z += f * x[i].z; acc.w += f * x[i].w;
@@ -434,9 +455,8 @@ template <int NB> __global__ void __launch_bounds__(kAttnWarps * 32, attn_ctas_p
     block_op_release();
 
     const int item = blockIdx.x, split = blockIdx.y;
-    const int ct = item % a.n_ct;
-    const int kvh = item / a.n_ct % a.c.n_kv_heads;
-    const int seq = item / a.n_ct / a.c.n_kv_heads;
+    const int sh = a.by_ct.div(item), ct = a.by_ct.mod(item, sh);
+    const int seq = a.by_heads.div(sh), kvh = a.by_heads.mod(sh, seq);
     const int32_t *table = a.c.table + static_cast<int64_t>(seq) * a.c.max_pages;
     // without a window the split's first tile does not hang on the lengths: the pages are looked up beside them
     const int tile_off = split * a.chunk + 2 * (warp + (lane >> 1) * kWarps) + (lane & 1);
@@ -463,7 +483,7 @@ template <int NB> __global__ void __launch_bounds__(kAttnWarps * 32, attn_ctas_p
     for (int j = 0; j < 2; ++j)
         if (warp + j * kWarps < n_units) feed.copy(j, lane, ring + j * kSlotBytes, &full[j], policy);
 
-    // its B fragments: the upper (g even) or lower part
+    // its B fragments, the upper (g even) or lower part: each warp makes an eighth of them for all
     uint32_t qf[NB][4];
     float qs;
     {
@@ -477,20 +497,27 @@ template <int NB> __global__ void __launch_bounds__(kAttnWarps * 32, attn_ctas_p
         float up, down;
         q_unit(top, a.scale_log2, up, down);
         qs = __shfl_sync(0xffffffffu, fmaxf(fabsf(a.scale_log2) * down, 1e-37f), 8 * t);  // column t's
+        uint2 *q_sm = reinterpret_cast<uint2 *>(smem + kAttnBarBytes + 2 * kWarps * kSlotBytes) + lane;
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
+        for (int k = 0; k < 2 * NB; ++k) {
+            if (k % kWarps != warp) continue;
+            const int b = k / 2, h = k % 2;
+            uint32_t f[4];
+            split_h2(v[b][2 * h] * up, v[b][2 * h + 4] * up, f[0], f[1]);
+            split_h2(v[b][2 * h + 1] * up * 0.0625f, v[b][2 * h + 5] * up * 0.0625f, f[2], f[3]);
+            q_sm[k * 32] = (g & 1) ? make_uint2(f[1], f[3]) : make_uint2(f[0], f[2]);
+        }
+        __syncthreads();
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                uint32_t f[4];
-                split_h2(v[b][2 * h] * up, v[b][2 * h + 4] * up, f[0], f[1]);
-                split_h2(v[b][2 * h + 1] * up * 0.0625f, v[b][2 * h + 5] * up * 0.0625f, f[2], f[3]);
-                qf[b][2 * h] = (g & 1) ? f[1] : f[0];
-                qf[b][2 * h + 1] = (g & 1) ? f[3] : f[2];
-            }
+        for (int k = 0; k < 2 * NB; ++k) {
+            const uint2 f = q_sm[k * 32];
+            qf[k / 2][2 * (k % 2)] = f.x;
+            qf[k / 2][2 * (k % 2) + 1] = f.y;
+        }
     }
     // what column t sees, of this split's tiles
     const int limit = min(r.len, last * kKvSlab);
-    const int ti = (ct * kNarrowCols + t) / a.group;
+    const int ti = a.by_group.div(ct * kNarrowCols + t);
     const int end = ti < r.n ? min(limit, max(0, r.len - (r.n - 1 - ti))) : limit;
     const int low = ti < r.n && a.window > 0 ? max(0, r.len - (r.n - 1 - ti) - a.window) : 0;
     const int end_min = __reduce_min_sync(0xffffffffu, end), low_max = __reduce_max_sync(0xffffffffu, low);
@@ -706,9 +733,8 @@ __global__ void __launch_bounds__(AttnForm<NB, SHARED>::kThreads, SHARED ? 1 : a
     block_op_release();
 
     const int item = blockIdx.x, split = blockIdx.y;
-    const int ct = item % a.n_ct;
-    const int kvh = item / a.n_ct % a.c.n_kv_heads;
-    const int seq = item / a.n_ct / a.c.n_kv_heads;
+    const int sh = a.by_ct.div(item), ct = a.by_ct.mod(item, sh);
+    const int seq = a.by_heads.div(sh), kvh = a.by_heads.mod(sh, seq);
     const AttnRange r = attn_range(a, seq, ct, cols);
     if (ct * cols >= r.n * a.group) return;
     const int n_splits = r.splits(a.chunk);
@@ -794,7 +820,7 @@ __global__ void __launch_bounds__(AttnForm<NB, SHARED>::kThreads, SHARED ? 1 : a
     int end_min = limit, low_max = 0;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-        const int i = (col0 + 8 * nt + g) / a.group;
+        const int i = a.by_group.div(col0 + 8 * nt + g);
         const bool valid = i < r.n;
         end[nt] = valid ? min(limit, max(0, r.len - (r.n - 1 - i))) : limit;
         low[nt] = valid && a.window > 0 ? max(0, r.len - (r.n - 1 - i) - a.window) : 0;
@@ -1095,9 +1121,9 @@ template <int NB, int NT, bool SHARED> cudaError_t launch_attn_form(const AttnAr
 }
 template <int NB> cudaError_t launch_attn(AttnArgs a, const AttnPlan &p, cudaStream_t st) {
     if (p.cols == kNarrowCols) {
-        constexpr size_t kRing = 2 * kAttnWarps * 2 * KvGeom<NB>::kTileBytes;
+        constexpr size_t kRing = 2 * kAttnWarps * 2 * KvGeom<NB>::kTileBytes, kQ = 2 * NB * 256;
         static_assert(kRing >= kAttnWarps * kNarrowCols * NB * kQK * 4, "the warps' sums lie over the ring");
-        return launch_attn_kernel<NB>(attn_narrow_kernel<NB>, kAttnWarps * 32, kAttnBarBytes + kRing, a, p, st);
+        return launch_attn_kernel<NB>(attn_narrow_kernel<NB>, kAttnWarps * 32, kAttnBarBytes + kRing + kQ, a, p, st);
     }
     if (p.wc > 1) return launch_attn_form<NB, 2, true>(a, p, st);
     return p.nt == 1 ? launch_attn_form<NB, 1, false>(a, p, st) : launch_attn_form<NB, 2, false>(a, p, st);
