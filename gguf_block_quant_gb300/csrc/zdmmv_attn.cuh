@@ -1104,26 +1104,24 @@ extern template cudaError_t launch_attn<6>(AttnArgs, const AttnPlan &, cudaStrea
 extern template cudaError_t launch_attn<8>(AttnArgs, const AttnPlan &, cudaStream_t);
 
 #ifdef ZDMMV_ATTN_INSTANTIATE
-template <int NB>
-cudaError_t launch_attn_kernel(void (*kernel)(AttnArgs), int threads, size_t smem, const AttnArgs &a, const AttnPlan &p,
-                               cudaStream_t st) {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+template <auto KERNEL>
+cudaError_t launch_attn_kernel(int threads, size_t smem, const AttnArgs &a, const AttnPlan &p, cudaStream_t st) {
+    const cudaError_t e = smem_limit_raised<KERNEL>();
     if (e != cudaSuccess) return e;
-    return launch_block_op(kernel, dim3(static_cast<unsigned>(p.items), p.n_split), threads, smem, st, a);
+    return launch_block_op(KERNEL, dim3(static_cast<unsigned>(p.items), p.n_split), threads, smem, st, a);
 }
 template <int NB, int NT, bool SHARED> cudaError_t launch_attn_form(const AttnArgs &a, const AttnPlan &p, cudaStream_t st) {
     using F = AttnForm<NB, SHARED>;
     // the join's sums lie over the ring
     const size_t ring = F::kSlots * 2 * KvGeom<NB>::kTileBytes + static_cast<size_t>(p.wc) * NT * 2 * NB * 512;
     const size_t join = static_cast<size_t>(kAttnWarps) * NT * 8 * NB * kQK * 4;
-    return launch_attn_kernel<NB>(attn_kernel<NB, NT, SHARED>, F::kThreads, kAttnBarBytes + (ring > join ? ring : join), a,
-                                  p, st);
+    return launch_attn_kernel<&attn_kernel<NB, NT, SHARED>>(F::kThreads, kAttnBarBytes + (ring > join ? ring : join), a, p, st);
 }
 template <int NB> cudaError_t launch_attn(AttnArgs a, const AttnPlan &p, cudaStream_t st) {
     if (p.cols == kNarrowCols) {
         constexpr size_t kRing = 2 * kAttnWarps * 2 * KvGeom<NB>::kTileBytes, kQ = 2 * NB * 256;
         static_assert(kRing >= kAttnWarps * kNarrowCols * NB * kQK * 4, "the warps' sums lie over the ring");
-        return launch_attn_kernel<NB>(attn_narrow_kernel<NB>, kAttnWarps * 32, kAttnBarBytes + kRing + kQ, a, p, st);
+        return launch_attn_kernel<&attn_narrow_kernel<NB>>(kAttnWarps * 32, kAttnBarBytes + kRing + kQ, a, p, st);
     }
     if (p.wc > 1) return launch_attn_form<NB, 2, true>(a, p, st);
     return p.nt == 1 ? launch_attn_form<NB, 1, false>(a, p, st) : launch_attn_form<NB, 2, false>(a, p, st);

@@ -50,134 +50,200 @@ struct AppendArgs {
     int32_t n_tok, n_q_heads, rot_dim, halves;
 };
 
+constexpr int64_t kManyWarps = 152 * 64;  // as many (token, head) pairs as the device holds warps
 constexpr int kAppendWarps = 4;
 
-// One warp per (token, head) of q, k and v: lane l holds the four dimensions
-// 4l .. 4l+3 of each pass of 128. All of a head is loaded before any of it is
-// stored, so q_out may be q.
-template <int NB>
-__global__ void __launch_bounds__(kAppendWarps * 32) kv_append_kernel(AppendArgs a) {
-    using G = KvGeom<NB>;
-    constexpr int kPass = (G::kDim + 127) / 128;
-    block_op_wait();
-    block_op_release();
-    const int lane = threadIdx.x & 31;
-    const int heads = a.n_q_heads + 2 * a.c.n_kv_heads;
-    const int64_t job = static_cast<int64_t>(blockIdx.x) * kAppendWarps + (threadIdx.x >> 5);
-    const int64_t tok = job / heads;
-    if (tok >= a.n_tok) return;
-    int head = static_cast<int>(job - tok * heads);
-    const int kind = head < a.n_q_heads ? 0 : (head < a.n_q_heads + a.c.n_kv_heads ? 1 : 2);  // q, k, v
-    head -= kind == 0 ? 0 : (kind == 1 ? a.n_q_heads : a.n_q_heads + a.c.n_kv_heads);
-    const int pos = a.pos[tok], seq = a.seq[tok];
-    // where the token goes; bad: outside what the cache and the rotation table have
-    bool bad = false;
-    uint8_t *tile = nullptr;
-    int r = 0;
-    if (pos >= 0) {
-        const int slot = pos / a.c.page_tokens, in = pos - slot * a.c.page_tokens;
-        bad = seq < 0 || seq >= a.c.n_seq || slot >= a.c.max_pages || (a.rot_dim > 0 && pos >= a.rope_rows);
-        if (!bad) {
-            const int page = a.c.table[static_cast<int64_t>(seq) * a.c.max_pages + slot];
-            bad = page < 0 || page >= a.c.n_pages;
-            r = in % kKvSlab;
-            tile = a.c.pages + page * a.c.page_bytes +
-                   static_cast<int64_t>(head * (a.c.page_tokens / kKvSlab) + in / kKvSlab) * G::kTileBytes;
+// The rotation of four neighbouring dimensions e0 .. e0+3 of a head at `src`: their cosines and sines, the partner
+// dimensions, and which half of its pair each is. Every product and sum is rounded by itself (no fused multiply-add), so
+// that the result is the same wherever it is computed.
+struct Turn {
+    float c[4], s[4];  // sign of s: minus for a pair's first dimension, whose result is x cos - partner sin
+};
+
+// FAST: four neighbouring dimensions are all rotated or none, and their partners and angles are neighbours too (pairs:
+// rot_dim a multiple of 4; halves: rot_dim a multiple of 8), so everything is 128-bit loads.
+template <bool FAST>
+__device__ __forceinline__ Turn load_turn(const AppendArgs &a, int pos, int e0) {
+    Turn t;
+    const int half = a.rot_dim / 2;
+    const float *row = a.rope + static_cast<int64_t>(pos) * a.rot_dim;
+    if constexpr (FAST) {
+        if (a.halves) {
+            const bool second = e0 >= half;
+            const int p = second ? e0 - half : e0;
+            const float4 c = *reinterpret_cast<const float4 *>(row + p), s = *reinterpret_cast<const float4 *>(row + half + p);
+            const float sign = second ? 1.0f : -1.0f;
+            t.c[0] = c.x; t.c[1] = c.y; t.c[2] = c.z; t.c[3] = c.w;
+            t.s[0] = sign * s.x; t.s[1] = sign * s.y; t.s[2] = sign * s.z; t.s[3] = sign * s.w;
+        } else {
+            const float2 c = *reinterpret_cast<const float2 *>(row + e0 / 2), s = *reinterpret_cast<const float2 *>(row + half + e0 / 2);
+            t.c[0] = t.c[1] = c.x; t.c[2] = t.c[3] = c.y;
+            t.s[0] = -s.x; t.s[1] = s.x; t.s[2] = -s.y; t.s[3] = s.y;
         }
-    }
-    if (bad && lane == 0 && a.status) *a.status = 1;
-    const float *src = kind == 0 ? a.q + tok * a.q_stride : (kind == 1 ? a.k + tok * a.k_stride : a.v + tok * a.v_stride);
-    src += static_cast<int64_t>(head) * G::kDim;
-    float v[kPass][4];
-#pragma unroll
-    for (int p = 0; p < kPass; ++p) {
-        const int e0 = p * 128 + 4 * lane;
+    } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int e = e0 + i;
-            v[p][i] = 0.0f;
-            if (e >= G::kDim) continue;
-            if (pos < 0 || bad) {
-                v[p][i] = bad ? __int_as_float(0x7fffffff) : 0.0f;
-            } else if (kind == 2 || e >= a.rot_dim) {
-                v[p][i] = src[e];
-            } else {
-                const int half = a.rot_dim / 2;
-                const bool second = a.halves ? e >= half : (e & 1) != 0;
-                const int pair = a.halves ? (second ? e - half : e) : e / 2;
-                const int other = a.halves ? (second ? e - half : e + half) : e ^ 1;
-                const float c = a.rope[static_cast<int64_t>(pos) * a.rot_dim + pair];
-                const float s = a.rope[static_cast<int64_t>(pos) * a.rot_dim + half + pair];
-                const float own = src[e], oth = src[other];
-                v[p][i] = second ? __fadd_rn(__fmul_rn(oth, s), __fmul_rn(own, c))
-                                 : __fsub_rn(__fmul_rn(own, c), __fmul_rn(oth, s));
-            }
+            t.c[i] = 1.0f;
+            t.s[i] = 0.0f;
+            if (e >= a.rot_dim) continue;
+            const bool second = a.halves ? e >= half : (e & 1) != 0;
+            const int p = a.halves ? (second ? e - half : e) : e / 2;
+            t.c[i] = row[p];
+            t.s[i] = second ? row[half + p] : -row[half + p];
         }
     }
-    __syncwarp();
-    if (kind == 0) {
-        float *dst = a.q_out + (tok * a.n_q_heads + head) * G::kDim;
-#pragma unroll
-        for (int p = 0; p < kPass; ++p) {
-            const int e0 = p * 128 + 4 * lane;
-            if (e0 < G::kDim) *reinterpret_cast<float4 *>(dst + e0) = make_float4(v[p][0], v[p][1], v[p][2], v[p][3]);
-        }
-        return;
-    }
-    __half *val = kind == 1 ? a.k_val : a.v_val;
-    if (val) val += (tok * a.c.n_kv_heads + head) * G::kDim;
-#pragma unroll
-    for (int p = 0; p < kPass; ++p) {
-        const int e0 = p * 128 + 4 * lane;
-        const bool in = e0 < G::kDim;
-        // the first value of the largest magnitude, over the block's 8 lanes
-        float m = v[p][0];
-        int at = e0;
-#pragma unroll
-        for (int i = 1; i < 4; ++i)
-            if (fabsf(v[p][i]) > fabsf(m)) { m = v[p][i]; at = e0 + i; }
-#pragma unroll
-        for (int o = 1; o < 8; o <<= 1) {
-            const float om = __shfl_xor_sync(0xffffffffu, m, o);
-            const int oat = __shfl_xor_sync(0xffffffffu, at, o);
-            if (fabsf(om) > fabsf(m) || (fabsf(om) == fabsf(m) && oat < at)) { m = om; at = oat; }
-        }
-        const float d = m / -8.0f;
-        const float id = d != 0.0f ? 1.0f / d : 0.0f;
-        const __half dh = __float2half_rn(d);
-        uint32_t code[4], packed = 0;
+    return t;
+}
+template <bool FAST>
+__device__ __forceinline__ void load_head(const AppendArgs &a, const float *src, int e0, bool turned, float (&v)[4], float (&o)[4]) {
+    const float4 x = *reinterpret_cast<const float4 *>(src + e0);
+    v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+    o[0] = v[1]; o[1] = v[0]; o[2] = v[3]; o[3] = v[2];
+    if (!turned || !a.halves) return;
+    const int half = a.rot_dim / 2;
+    if constexpr (FAST) {
+        const float4 y = *reinterpret_cast<const float4 *>(src + (e0 >= half ? e0 - half : e0 + half));
+        o[0] = y.x; o[1] = y.y; o[2] = y.z; o[3] = y.w;
+    } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int c = static_cast<int>(__fadd_rn(__fmul_rn(v[p][i], id), 8.5f));
-            code[i] = c < 0 ? 0 : (c > 15 ? 15 : c);
-            packed |= code[i] << (4 * i);
-        }
-        const int b = e0 / kQK, g = (e0 % kQK) / 4;
-        const uint32_t upper = __shfl_down_sync(0xffffffffu, packed, 1);
-        if (tile && !bad && in) {
-            __half *scales = reinterpret_cast<__half *>(tile + (kind == 1 ? G::kKScaleAt : G::kVScaleAt));
-            if (g == 0) scales[G::scale_half(r, b)] = dh;
-            if (kind == 1) {
-                if ((g & 1) == 0) reinterpret_cast<uint32_t *>(tile)[G::k_word(r, b, g / 2)] = packed | (upper << 16);
-            } else {
-                reinterpret_cast<uint16_t *>(tile + G::kVAt)[G::v_half(r, b, g)] = static_cast<uint16_t>(packed);
-            }
-        }
-        if (val && in) {
-            const float df = __half2float(dh);
-#pragma unroll
-            for (int i = 0; i < 4; i += 2)
-                *reinterpret_cast<__half2 *>(val + e0 + i) =
-                    __floats2half2_rn(df * (static_cast<float>(code[i]) - 8.0f), df * (static_cast<float>(code[i + 1]) - 8.0f));
+            const int e = e0 + i;
+            if (e < a.rot_dim) o[i] = src[e >= half ? e - half : e + half];
         }
     }
 }
 
-template <int NB> cudaError_t launch_append(const AppendArgs &a, cudaStream_t st) {
-    const int64_t jobs = static_cast<int64_t>(a.n_tok) * (a.n_q_heads + 2 * a.c.n_kv_heads);
+// One warp per token and HEADS neighbouring heads of its q, k and v: lane l holds the four dimensions 4l .. 4l+3 of each
+// pass of 128, loads them for all its heads before it stores any (so q_out may be q), and keeps the token's cosines and
+// sines for all of them. Bound by memory for prompts (HEADS = 4: four heads' loads in flight), by latency for a few
+// tokens (HEADS = 1: as many warps as heads).
+template <int NB, int HEADS, bool FAST>
+__global__ void __launch_bounds__(kAppendWarps * 32) kv_append_kernel(AppendArgs a) {
+    using G = KvGeom<NB>;
+    constexpr int kPass = (G::kDim + 127) / 128;
+    const int lane = threadIdx.x & 31;
+    const int heads = a.n_q_heads + 2 * a.c.n_kv_heads;
+    const int groups = (heads + HEADS - 1) / HEADS;
+    const int64_t job = static_cast<int64_t>(blockIdx.x) * kAppendWarps + (threadIdx.x >> 5);
+    const int64_t tok = job / groups;
+    const int h0 = static_cast<int>(job - tok * groups) * HEADS;
+    block_op_wait();
+    block_op_release();
+    if (tok >= a.n_tok) return;
+    const int pos = a.pos[tok], seq = a.seq[tok];
+    // where the token goes; bad: outside what the cache and the rotation table have
+    const int slot = pos / a.c.page_tokens, in = pos - slot * a.c.page_tokens;
+    const bool pad = pos < 0;
+    bool bad = !pad && (seq < 0 || seq >= a.c.n_seq || slot >= a.c.max_pages || (a.rot_dim > 0 && pos >= a.rope_rows));
+    const int page = pad || bad ? 0 : a.c.table[static_cast<int64_t>(seq) * a.c.max_pages + slot];
+    if (page < 0 || page >= a.c.n_pages) bad = true;
+    if (bad && lane == 0 && a.status) *a.status = 1;
+    const bool ok = !pad && !bad;
+    uint8_t *tiles = a.c.pages + (ok ? page : 0) * a.c.page_bytes + static_cast<int64_t>(in / kKvSlab) * G::kTileBytes;
+    const int64_t head_bytes = static_cast<int64_t>(a.c.page_tokens / kKvSlab) * G::kTileBytes;
+    const int r = in % kKvSlab;
+    const float fill = bad ? __int_as_float(0x7fffffff) : 0.0f;
+    float v[HEADS][kPass][4], o[HEADS][kPass][4];
+    Turn turn[kPass];
+#pragma unroll
+    for (int u = 0; u < HEADS; ++u)
+#pragma unroll
+        for (int p = 0; p < kPass; ++p) {
+            const int head = h0 + u, kvh = head - a.n_q_heads, e0 = p * 128 + 4 * lane;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[u][p][i] = fill;
+            if (!ok || e0 >= G::kDim || head >= heads) continue;
+            const float *src = kvh < 0 ? a.q + tok * a.q_stride + static_cast<int64_t>(head) * G::kDim
+                               : (kvh < a.c.n_kv_heads ? a.k + tok * a.k_stride + static_cast<int64_t>(kvh) * G::kDim
+                                                       : a.v + tok * a.v_stride + static_cast<int64_t>(kvh - a.c.n_kv_heads) * G::kDim);
+            load_head<FAST>(a, src, e0, e0 < a.rot_dim && kvh < a.c.n_kv_heads, v[u][p], o[u][p]);
+        }
+#pragma unroll
+    for (int p = 0; p < kPass; ++p)
+        if (ok && p * 128 + 4 * lane < a.rot_dim) turn[p] = load_turn<FAST>(a, pos, p * 128 + 4 * lane);
+    __syncwarp();
+#pragma unroll
+    for (int u = 0; u < HEADS; ++u) {
+        const int head = h0 + u, kvh = head - a.n_q_heads;
+        if (head >= heads) break;
+#pragma unroll
+        for (int p = 0; p < kPass; ++p) {
+            const int e0 = p * 128 + 4 * lane;
+            const bool inside = e0 < G::kDim;
+            float (&x)[4] = v[u][p];
+            if (ok && e0 < a.rot_dim && kvh < a.c.n_kv_heads) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (FAST || e0 + i < a.rot_dim) x[i] = __fadd_rn(__fmul_rn(x[i], turn[p].c[i]), __fmul_rn(o[u][p][i], turn[p].s[i]));
+            }
+            if (kvh < 0) {
+                if (inside)
+                    *reinterpret_cast<float4 *>(a.q_out + (tok * a.n_q_heads + head) * G::kDim + e0) = make_float4(x[0], x[1], x[2], x[3]);
+                continue;
+            }
+            const bool is_k = kvh < a.c.n_kv_heads;
+            const int h = is_k ? kvh : kvh - a.c.n_kv_heads;
+            // the first value of the largest magnitude, over the block's 8 lanes
+            float m = x[0];
+            int at = e0;
+#pragma unroll
+            for (int i = 1; i < 4; ++i)
+                if (fabsf(x[i]) > fabsf(m)) { m = x[i]; at = e0 + i; }
+#pragma unroll
+            for (int s = 1; s < 8; s <<= 1) {
+                const float om = __shfl_xor_sync(0xffffffffu, m, s);
+                const int oat = __shfl_xor_sync(0xffffffffu, at, s);
+                if (fabsf(om) > fabsf(m) || (fabsf(om) == fabsf(m) && oat < at)) { m = om; at = oat; }
+            }
+            const float d = m / -8.0f;
+            const float id = d != 0.0f ? 1.0f / d : 0.0f;
+            const __half dh = __float2half_rn(d);
+            uint32_t code[4], packed = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int c = static_cast<int>(__fadd_rn(__fmul_rn(x[i], id), 8.5f));
+                code[i] = c < 0 ? 0 : (c > 15 ? 15 : c);
+                packed |= code[i] << (4 * i);
+            }
+            const int b = e0 / kQK, g = (e0 % kQK) / 4;
+            const uint32_t upper = __shfl_down_sync(0xffffffffu, packed, 1);
+            if (!inside) continue;
+            if (ok) {
+                uint8_t *tile = tiles + h * head_bytes;
+                __half *scales = reinterpret_cast<__half *>(tile + (is_k ? G::kKScaleAt : G::kVScaleAt));
+                if (g == 0) scales[G::scale_half(r, b)] = dh;
+                if (is_k) {
+                    if ((g & 1) == 0) reinterpret_cast<uint32_t *>(tile)[G::k_word(r, b, g / 2)] = packed | (upper << 16);
+                } else {
+                    reinterpret_cast<uint16_t *>(tile + G::kVAt)[G::v_half(r, b, g)] = static_cast<uint16_t>(packed);
+                }
+            }
+            __half *val = is_k ? a.k_val : a.v_val;
+            if (val) {
+                const float df = __half2float(dh);
+                __half2 w[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    w[i] = __floats2half2_rn(df * (static_cast<float>(code[2 * i]) - 8.0f), df * (static_cast<float>(code[2 * i + 1]) - 8.0f));
+                *reinterpret_cast<uint2 *>(val + (tok * a.c.n_kv_heads + h) * G::kDim + e0) = *reinterpret_cast<uint2 *>(w);
+            }
+        }
+    }
+}
+
+template <int NB, int HEADS, bool FAST> cudaError_t launch_append_as(const AppendArgs &a, cudaStream_t st) {
+    const int heads = a.n_q_heads + 2 * a.c.n_kv_heads;
+    const int64_t jobs = static_cast<int64_t>(a.n_tok) * ((heads + HEADS - 1) / HEADS);
     const int64_t ctas = (jobs + kAppendWarps - 1) / kAppendWarps;
     if (ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    return launch_block_op(kv_append_kernel<NB>, dim3(static_cast<unsigned>(ctas)), kAppendWarps * 32, 0, st, a);
+    return launch_block_op(kv_append_kernel<NB, HEADS, FAST>, dim3(static_cast<unsigned>(ctas)), dim3(kAppendWarps * 32), 0, st, a);
+}
+template <int NB> cudaError_t launch_append(const AppendArgs &a, cudaStream_t st) {
+    const bool fast = a.rot_dim % (a.halves ? 8 : 4) == 0;
+    const int64_t warps = static_cast<int64_t>(a.n_tok) * (a.n_q_heads + 2 * a.c.n_kv_heads);
+    if (warps > kManyWarps) return fast ? launch_append_as<NB, 4, true>(a, st) : launch_append_as<NB, 4, false>(a, st);
+    return fast ? launch_append_as<NB, 1, true>(a, st) : launch_append_as<NB, 1, false>(a, st);
 }
 
 }  // namespace

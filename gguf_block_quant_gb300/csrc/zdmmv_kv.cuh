@@ -3,11 +3,13 @@
 // of the attention half's kernels.
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 #include <cuda_runtime.h>
 
 #include "zdmmv.h"
 #include "zdmmv_device.cuh"
+#include "zdmmv_internal.h"
 
 namespace zdmmv {
 
@@ -53,13 +55,12 @@ inline bool kv_misaligned(const void *p, uintptr_t a) { return (reinterpret_cast
 // One launch with the programmatic-dependent-launch attribute (unless ZDMMV_PDL=0).
 // Every kernel launched so waits (griddepcontrol.wait) before it reads or writes
 // global memory.
-bool pdl_enabled();
 template <typename... KArgs, typename... Args>
-cudaError_t launch_block_op(void (*kern)(KArgs...), dim3 grid, unsigned block, size_t smem, cudaStream_t st,
+cudaError_t launch_block_op(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
                             Args... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
-    cfg.blockDim = dim3(block, 1, 1);
+    cfg.blockDim = block;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
@@ -68,6 +69,18 @@ cudaError_t launch_block_op(void (*kern)(KArgs...), dim3 grid, unsigned block, s
     cfg.attrs = attr;
     cfg.numAttrs = pdl_enabled() ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+// Raises KERNEL's dynamic shared-memory limit to the device's, once per device.
+template <auto KERNEL> cudaError_t smem_limit_raised() {
+    static std::atomic<bool> done[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 64 && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+    e = raise_dynamic_smem_limit(reinterpret_cast<const void *>(KERNEL), dev);
+    if (e == cudaSuccess && dev < 64) done[dev].store(true, std::memory_order_release);
+    return e;
 }
 
 __device__ __forceinline__ void block_op_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }

@@ -3,7 +3,11 @@
 //
 //   s = x + r,  y = (s * (1 / sqrt(mean(s^2) + eps))) * w,  blocks of 32: d = max|y| / 127, q = round(y / d)
 //
-// One CTA per row; the sums are kept in shared memory between the two passes.
+// A row is read once and held in its threads' registers between the sum of
+// squares and the quantization: T threads (whole warps) with V float4 each, eight
+// neighbouring threads a block. Bound by memory with many rows (4 + 4 bytes in,
+// 4 + 34/32 out, 2 with y, a value), by latency with few: then V = 1, as many
+// threads as the row has float4.
 #include <cmath>
 
 #include "zdmmv_kv.cuh"
@@ -21,66 +25,127 @@ struct NormArgs {
     float eps;
 };
 
-constexpr int kNormThreads = 256;
 constexpr int kNormMaxCols = 32768;
+constexpr int kNormFewRows = 304;  // up to two rows an SM
 
-__global__ void __launch_bounds__(kNormThreads) add_rmsnorm_kernel(NormArgs a) {
-    extern __shared__ float4 s4[];
-    __shared__ float part[kNormThreads / 32];
+// blockDim.x = T threads a row; blockDim.y rows a CTA.
+template <int V> __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(NormArgs a) {
+    extern __shared__ __align__(16) uint8_t staged[];  // the rows' Q8_0 blocks
+    __shared__ float part[32];
+    const int tid = threadIdx.x, T = blockDim.x, lane = tid & 31, warps = T >> 5;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+    const bool live = row < a.rows;
+    const int n4 = a.cols / 4;
     block_op_wait();
     block_op_release();
-    const int64_t row = blockIdx.x;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const float4 *x = reinterpret_cast<const float4 *>(a.x + row * a.x_stride);
-    const float4 *r = a.r ? reinterpret_cast<const float4 *>(a.r + row * a.r_stride) : nullptr;
-    float4 *out = a.out ? reinterpret_cast<float4 *>(a.out + row * a.cols) : nullptr;
-    const int n4 = a.cols / 4;
-    float ss = 0.0f;
-    for (int i = tid; i < n4; i += kNormThreads) {
-        float4 v = x[i];
-        if (r) {
-            const float4 u = r[i];
-            v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
+    float4 s[V];
+    if (live) {
+        const float4 *x = reinterpret_cast<const float4 *>(a.x + row * a.x_stride);
+        const float4 *r = reinterpret_cast<const float4 *>(a.r + row * a.r_stride);
+        float4 u[V];
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            const int i = tid + k * T;
+            s[k] = u[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (i < n4) {
+                s[k] = x[i];
+                if (a.r) u[k] = r[i];
+            }
         }
-        if (out) out[i] = v;
-        s4[i] = v;
-        ss += v.x * v.x + v.y * v.y + v.z * v.z + v.w * v.w;
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            if (a.r) {
+                s[k].x += u[k].x; s[k].y += u[k].y; s[k].z += u[k].z; s[k].w += u[k].w;
+            }
+            const int i = tid + k * T;
+            if (a.out && i < n4) reinterpret_cast<float4 *>(a.out + row * a.cols)[i] = s[k];
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < V; ++k) s[k] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
+    // the weights' loads run beside the reduction (of 8 float4 they would cost spills, and wait)
+    const auto weight = [&](int i) {
+        return a.w && i < n4 ? reinterpret_cast<const float4 *>(a.w)[i] : make_float4(1.f, 1.f, 1.f, 1.f);
+    };
+    float4 ws[V <= 4 ? V : 1];
+    if constexpr (V <= 4) {
+#pragma unroll
+        for (int k = 0; k < V; ++k) ws[k] = weight(tid + k * T);
+    }
+    float ss = 0.0f;
+#pragma unroll
+    for (int k = 0; k < V; ++k) ss += (s[k].x * s[k].x + s[k].y * s[k].y) + (s[k].z * s[k].z + s[k].w * s[k].w);
+#pragma unroll
     for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    if (lane == 0) part[warp] = ss;
-    __syncthreads();
-    ss = 0.0f;
-    for (int k = 0; k < kNormThreads / 32; ++k) ss += part[k];
+    if (warps > 1) {  // uniform: T is the CTA's
+        const int first = threadIdx.y * warps;
+        if (lane == 0) part[first + (tid >> 5)] = ss;
+        __syncthreads();
+        ss = lane < warps ? part[first + lane] : 0.0f;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    }
     const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(ss, static_cast<float>(a.cols)), a.eps)));
-    // eight lanes a block of 32; the loop count is uniform over the warp
-    for (int i0 = warp * 32; i0 < n4; i0 += kNormThreads) {
-        const int i = i0 + lane;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (i < n4) {
-            v = s4[i];
-            const float4 w = a.w ? reinterpret_cast<const float4 *>(a.w)[i] : make_float4(1.f, 1.f, 1.f, 1.f);
-            v.x = __fmul_rn(__fmul_rn(v.x, rstd), w.x);
-            v.y = __fmul_rn(__fmul_rn(v.y, rstd), w.y);
-            v.z = __fmul_rn(__fmul_rn(v.z, rstd), w.z);
-            v.w = __fmul_rn(__fmul_rn(v.w, rstd), w.w);
-        }
+    const int row_bytes = a.cols / kQK * 34;
+    uint8_t *mine = staged + threadIdx.y * row_bytes;
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+        const int i = tid + k * T;
+        if ((i & ~31) >= n4) break;  // whole warps: the 8 lanes of a block exchange its maximum
+        float4 v = s[k], w;
+        if constexpr (V <= 4) w = ws[k];
+        else w = weight(i);
+        v.x = __fmul_rn(__fmul_rn(v.x, rstd), w.x);
+        v.y = __fmul_rn(__fmul_rn(v.y, rstd), w.y);
+        v.z = __fmul_rn(__fmul_rn(v.z, rstd), w.z);
+        v.w = __fmul_rn(__fmul_rn(v.w, rstd), w.w);
         unsigned short db;
         const uint32_t q = quantize_q8_0_quad(v, db);
-        if (i >= n4) continue;
+        if (i >= n4) break;
         if (a.xq) {
-            uint8_t *blk = a.xq + (row * (a.cols / kQK) + i / 8) * 34;
-            uint16_t *dst = reinterpret_cast<uint16_t *>(blk + 2 + 4 * (i & 7));
-            dst[0] = static_cast<uint16_t>(q);
-            dst[1] = static_cast<uint16_t>(q >> 16);
-            if ((i & 7) == 0) *reinterpret_cast<unsigned short *>(blk) = db;
+            uint16_t *blk = reinterpret_cast<uint16_t *>(mine + i / 8 * 34);
+            blk[1 + 2 * (i & 7)] = static_cast<uint16_t>(q);
+            blk[2 + 2 * (i & 7)] = static_cast<uint16_t>(q >> 16);
+            if ((i & 7) == 0) blk[0] = db;
         }
-        if (a.y) {
+        if (a.y && live) {
             const float d = __half2float(__ushort_as_half(db));
-            __half2 *y = reinterpret_cast<__half2 *>(a.y + row * a.cols + 4 * i);
-            y[0] = __floats2half2_rn(d * static_cast<int8_t>(q), d * static_cast<int8_t>(q >> 8));
-            y[1] = __floats2half2_rn(d * static_cast<int8_t>(q >> 16), d * static_cast<int8_t>(q >> 24));
+            const __half2 lo = __floats2half2_rn(d * static_cast<int8_t>(q), d * static_cast<int8_t>(q >> 8));
+            const __half2 hi = __floats2half2_rn(d * static_cast<int8_t>(q >> 16), d * static_cast<int8_t>(q >> 24));
+            uint2 both;
+            both.x = *reinterpret_cast<const uint32_t *>(&lo);
+            both.y = *reinterpret_cast<const uint32_t *>(&hi);
+            reinterpret_cast<uint2 *>(a.y + row * a.cols)[i] = both;
         }
     }
+    if (!a.xq) return;
+    // the CTA's rows are one stretch of bytes: out of shared memory in the widest words its start allows
+    __syncthreads();
+    const int64_t row0 = static_cast<int64_t>(blockIdx.x) * blockDim.y;
+    const int bytes = static_cast<int>(min(static_cast<int64_t>(blockDim.y), a.rows - row0)) * row_bytes;
+    uint8_t *dst = a.xq + row0 * row_bytes;
+    const int t = threadIdx.y * T + tid, n = T * blockDim.y;
+    const uint32_t align = static_cast<uint32_t>(row0 * row_bytes) & 15u;
+    if (align == 0) {
+        for (int i = t; i < bytes / 16; i += n) reinterpret_cast<uint4 *>(dst)[i] = reinterpret_cast<const uint4 *>(staged)[i];
+        for (int i = bytes / 16 * 8 + t; i < bytes / 2; i += n)
+            reinterpret_cast<uint16_t *>(dst)[i] = reinterpret_cast<const uint16_t *>(staged)[i];
+    } else if ((align & 3u) == 0) {
+        for (int i = t; i < bytes / 4; i += n) reinterpret_cast<uint32_t *>(dst)[i] = reinterpret_cast<const uint32_t *>(staged)[i];
+        if (t == 0 && (bytes & 2)) reinterpret_cast<uint16_t *>(dst)[bytes / 2 - 1] = reinterpret_cast<const uint16_t *>(staged)[bytes / 2 - 1];
+    } else {
+        for (int i = t; i < bytes / 2; i += n)
+            reinterpret_cast<uint16_t *>(dst)[i] = reinterpret_cast<const uint16_t *>(staged)[i];
+    }
+}
+
+template <int V> cudaError_t launch_norm(const NormArgs &a, int threads, int rows_per_cta, cudaStream_t st) {
+    const size_t smem = a.xq ? static_cast<size_t>(rows_per_cta) * (a.cols / kQK) * 34 : 0;
+    const cudaError_t e = smem_limit_raised<&add_rmsnorm_kernel<V>>();
+    if (e != cudaSuccess) return e;
+    const int64_t ctas = (a.rows + rows_per_cta - 1) / rows_per_cta;
+    return launch_block_op(add_rmsnorm_kernel<V>, dim3(static_cast<unsigned>(ctas)), dim3(threads, rows_per_cta), smem, st, a);
 }
 
 }  // namespace
@@ -106,13 +171,22 @@ extern "C" zdmmv_status zdmmv_add_rmsnorm_q8_0(const zdmmv_rmsnorm_args *args, z
         return ZDMMV_ERR_ALIGN;
     NormArgs a{g.x, g.residual, g.weight, g.out, static_cast<uint8_t *>(g.xq), static_cast<__half *>(g.y), g.rows,
                g.x_stride, g.residual_stride, static_cast<int32_t>(g.cols), g.eps};
-    const size_t smem = static_cast<size_t>(g.cols) * 4;
-    if (smem > 47 * 1024 &&
-        cudaFuncSetAttribute(add_rmsnorm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormMaxCols * 4) !=
-            cudaSuccess)
-        return ZDMMV_ERR_CUDA;
-    return launch_block_op(add_rmsnorm_kernel, dim3(static_cast<unsigned>(g.rows)), kNormThreads, smem,
-                           reinterpret_cast<cudaStream_t>(stream), a) == cudaSuccess
-               ? ZDMMV_OK
-               : ZDMMV_ERR_CUDA;
+    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    // Few rows: a thread a float4, up to 1024 of them. Many: up to four float4 a thread, so that a CTA of about 256
+    // threads holds enough loads in flight and several CTAs share an SM.
+    const int n4 = a.cols / 4;
+    const int most = a.rows <= kNormFewRows ? 1024 : 256;
+    int v = 1;
+    while (v < 4 && n4 > v * most) v *= 2;
+    if (n4 > v * 1024) v = 8;
+    const int threads = ((n4 + v - 1) / v + 31) / 32 * 32;
+    const int rows_per_cta = a.rows <= kNormFewRows ? 1 : (threads >= 256 ? 1 : 256 / threads);
+    cudaError_t e;
+    switch (v) {
+    case 1: e = launch_norm<1>(a, threads, rows_per_cta, st); break;
+    case 2: e = launch_norm<2>(a, threads, rows_per_cta, st); break;
+    case 4: e = launch_norm<4>(a, threads, rows_per_cta, st); break;
+    default: e = launch_norm<8>(a, threads, rows_per_cta, st); break;
+    }
+    return e == cudaSuccess ? ZDMMV_OK : ZDMMV_ERR_CUDA;
 }

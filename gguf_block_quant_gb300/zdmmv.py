@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import re
+import struct
 import threading
 
 import torch
@@ -50,31 +51,12 @@ _vp = ctypes.c_void_p
 _i64 = ctypes.c_int64
 _int = ctypes.c_int
 
-
-class _RmsnormArgs(ctypes.Structure):
-    _fields_ = [("x", _vp), ("residual", _vp), ("weight", _vp), ("out", _vp), ("xq", _vp), ("y", _vp),
-                ("rows", _i64), ("cols", _i64), ("x_stride", _i64), ("residual_stride", _i64),
-                ("eps", ctypes.c_float)]
-
-
-class _KvCache(ctypes.Structure):
-    _fields_ = [("pages", _vp), ("page_table", _vp), ("n_pages", _i64)] + [
-        (n, ctypes.c_int32) for n in ("n_seq", "max_pages", "page_tokens", "n_kv_heads", "head_dim")]
-
-
-class _KvAppendArgs(ctypes.Structure):
-    _fields_ = [(n, _vp) for n in ("k", "v", "q", "seq", "pos", "rope", "q_out", "k_val", "v_val", "status_dev")] + [
-        (n, _i64) for n in ("k_stride", "v_stride", "q_stride", "rope_rows")] + [
-        (n, ctypes.c_int32) for n in ("n_tok", "n_q_heads", "rot_dim", "rope_style")]
-
-
-class _AttnArgs(ctypes.Structure):
-    _fields_ = [(n, _vp) for n in ("q", "q_start", "kv_len", "out", "workspace", "status_dev")] + [
-        ("workspace_bytes", ctypes.c_size_t), ("q_stride", _i64)] + [
-        (n, ctypes.c_int32) for n in ("n_tok", "n_q_heads", "max_q_len", "max_kv_len", "window")] + [
-        ("scale", ctypes.c_float)]
-
-
+# The argument structs of the attention half's entry points, packed field by field (native alignment, as the C
+# compiler lays them out); a bytes object passes as a pointer.
+_RMSNORM_ARGS = struct.Struct("@6P4qf4x")
+_KV_CACHE = struct.Struct("@2Pq5i4x")
+_KV_APPEND_ARGS = struct.Struct("@10P4q4i")
+_ATTN_ARGS = struct.Struct("@6PNq5if")
 _SIGS = {
     "zdmmv_status_str": ([_int], ctypes.c_char_p),
     "zdmmv_version": ([], ctypes.c_char_p),
@@ -110,11 +92,11 @@ _SIGS = {
     "zdmmv_selftest_dp4a": ([_vp, _vp, _vp, _vp, _int, _vp], _int),
     "zdmmv_selftest_wait_timeout": ([_vp, _vp], _int),
     "zdmmv_device_status": ([ctypes.POINTER(ctypes.c_uint32), _int], _int),
-    "zdmmv_add_rmsnorm_q8_0": ([ctypes.POINTER(_RmsnormArgs), _vp], _int),
+    "zdmmv_add_rmsnorm_q8_0": ([_vp, _vp], _int),
     "zdmmv_kv_page_bytes": ([_int, _int, _int], ctypes.c_size_t),
-    "zdmmv_kv_append_q4_0": ([ctypes.POINTER(_KvCache), ctypes.POINTER(_KvAppendArgs), _vp], _int),
-    "zdmmv_attn_q4_0_workspace_bytes": ([ctypes.POINTER(_KvCache), _int, _int, _int], ctypes.c_size_t),
-    "zdmmv_attn_q4_0": ([ctypes.POINTER(_KvCache), ctypes.POINTER(_AttnArgs), _vp], _int),
+    "zdmmv_kv_append_q4_0": ([_vp, _vp, _vp], _int),
+    "zdmmv_attn_q4_0_workspace_bytes": ([_vp, _int, _int, _int], ctypes.c_size_t),
+    "zdmmv_attn_q4_0": ([_vp, _vp, _vp], _int),
 }
 
 
@@ -408,30 +390,54 @@ def device_status(clear: bool = False) -> int:
 
 
 # ------------------------------------------- the attention half of a decode layer
-def _check(ok: bool, what: str):
-    if not ok:
-        raise ValueError(what)
+# These calls are a few microseconds on the device: the arguments are checked with as few tensor queries as will do.
+_F32, _F16, _U8, _I32 = torch.float32, torch.float16, torch.uint8, torch.int32
+_entries: dict = {}
 
 
-def _rows_of(t: torch.Tensor, width: int, what: str) -> int:
-    """Data pointer of fp32 rows of `width` values; any even distance between rows (view the
-    token's heads as one row or as [heads][head_dim]), the values of a row side by side."""
-    _check(t.is_cuda and t.dtype == torch.float32, f"{what}: expected a float32 CUDA tensor")
-    n = t.dim()
-    _check(n >= 2 and t.stride(n - 1) == 1 and t[0].is_contiguous() if t.shape[0] else n >= 2,
-           f"{what}: the values of a row have to lie side by side")
-    _check(t.shape[0] == 0 or t[0].numel() == width, f"{what}: rows of {width} values expected")
+def _enter(name: str, *args):
+    fn = _entries.get(name)
+    if fn is None:
+        fn = _entries.setdefault(name, getattr(lib(), name))
+    rc = fn(*args)
+    if rc != 0:
+        raise ZdmmvError(name, rc)
+
+
+def _raw_stream(stream) -> int:
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _bad(what: str):
+    raise ValueError(what)
+
+
+def _rows(t: torch.Tensor, what: str) -> tuple[int, int, int, int]:
+    """(data pointer, rows, values of a row, floats between rows) of a float32 CUDA tensor [rows][values] or
+    [rows][heads][values of a head]; rows may be any distance apart, the values of a row lie side by side."""
+    if t.dtype is not _F32 or not t.is_cuda:
+        _bad(f"{what}: expected a float32 CUDA tensor")
+    shape, st = t.shape, t.stride()
+    if len(shape) == 2:
+        rows, width = shape
+        side_by_side = st[1] == 1 or width == 1
+    elif len(shape) == 3:
+        rows, width = shape[0], shape[1] * shape[2]
+        side_by_side = (st[2] == 1 or shape[2] == 1) and (st[1] == shape[2] or shape[1] == 1)
+    else:
+        _bad(f"{what}: expected [rows][values] or [rows][heads][values]")
+    if not side_by_side:
+        _bad(f"{what}: the values of a row have to lie side by side")
+    return t.data_ptr(), rows, width, st[0] if rows > 1 else width
+
+
+def _whole(t: torch.Tensor, dtype, n: int, what: str) -> int:
+    """Data pointer of a contiguous CUDA tensor of at least n values."""
+    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous() or t.numel() < n:
+        _bad(f"{what}: expected a contiguous CUDA tensor of {dtype} with {n} values")
     return t.data_ptr()
-
-
-def _stride_of(t: torch.Tensor, width: int) -> int:
-    """Floats between rows (a single row's distance to nothing is its width)."""
-    return t.stride(0) if t.shape[0] > 1 else width
-
-
-def _i32(t: torch.Tensor, n: int, what: str) -> int:
-    _check(t.dtype == torch.int32 and t.numel() >= n, f"{what}: expected int32 [{n}]")
-    return _ptr(t)
 
 
 def _make(shape, dtype, device, stream, how=torch.empty):
@@ -448,26 +454,24 @@ def _make(shape, dtype, device, stream, how=torch.empty):
 def add_rmsnorm_q8_0(x, weight, eps: float, residual=None, out=None, xq=None, y=None, stream=None):
     """s = x + residual; the Q8_0 blocks (uint8 tensor, returned) of s / sqrt(mean(s^2) + eps) * weight, per row of
     x (fp32 [rows][cols]; rows may be strided). out: s (may be x or residual); y: fp16, the blocks' values."""
-    _check(x.dim() == 2, "add_rmsnorm_q8_0: x must be [rows][cols]")
-    rows, cols = x.shape
-    a = _RmsnormArgs(x=_rows_of(x, cols, "x"), rows=rows, cols=cols, x_stride=_stride_of(x, cols), eps=eps)
+    px, rows, cols, sx = _rows(x, "x")
+    pr = sr = pw = po = py = 0
     if residual is not None:
-        _check(residual.shape == x.shape, "add_rmsnorm_q8_0: residual must have x's shape")
-        a.residual, a.residual_stride = _rows_of(residual, cols, "residual"), _stride_of(residual, cols)
+        pr, rrows, rcols, sr = _rows(residual, "residual")
+        if rrows != rows or rcols != cols:
+            _bad("add_rmsnorm_q8_0: residual must have x's shape")
     if weight is not None:
-        _check(weight.dtype == torch.float32 and weight.numel() == cols, "add_rmsnorm_q8_0: weight must be float32 [cols]")
-        a.weight = _ptr(weight)
+        pw = _whole(weight, _F32, cols, "weight")
     if out is not None:
-        _check(out.dtype == torch.float32 and out.numel() == rows * cols, "add_rmsnorm_q8_0: out must be float32 [rows][cols]")
-        a.out = _ptr(out)
+        po = _whole(out, _F32, rows * cols, "out")
+    nbytes = rows * (cols // QK) * 34
     if xq is None:
-        xq = _make(rows * (cols // QK) * 34, torch.uint8, x.device, stream)
-    _check(_nbytes(xq) >= rows * (cols // QK) * 34, "add_rmsnorm_q8_0: xq too small")
-    a.xq = _ptr(xq)
+        xq = _make(nbytes, _U8, x.device, stream)
+    pq = _whole(xq, _U8, nbytes, "xq")
     if y is not None:
-        _check(y.dtype == torch.float16 and y.numel() == rows * cols, "add_rmsnorm_q8_0: y must be float16 [rows][cols]")
-        a.y = _ptr(y)
-    _call("zdmmv_add_rmsnorm_q8_0", ctypes.byref(a), _stream(stream))
+        py = _whole(y, _F16, rows * cols, "y")
+    _enter("zdmmv_add_rmsnorm_q8_0", _RMSNORM_ARGS.pack(px, pr, pw, po, pq, py, rows, cols, sx, sr, eps),
+           _raw_stream(stream))
     return xq
 
 
@@ -482,14 +486,15 @@ class KVCache:
 
     def __init__(self, pages, page_tokens: int, n_kv_heads: int, head_dim: int, page_table):
         per = kv_page_bytes(page_tokens, n_kv_heads, head_dim)
-        _check(per > 0, "KVCache: page_tokens must be a multiple of 16 up to 1024, head_dim 64, 96, 128, 192 or 256")
-        _check(page_table.dim() == 2 and page_table.dtype == torch.int32, "KVCache: page_table must be int32 [n_seq][max_pages]")
-        _check(pages.dtype == torch.uint8, "KVCache: pages must be uint8")
+        if per == 0:
+            _bad("KVCache: page_tokens must be a multiple of 16 up to 1024, head_dim 64, 96, 128, 192 or 256")
+        if page_table.dim() != 2:
+            _bad("KVCache: page_table must be int32 [n_seq][max_pages]")
         self.pages, self.page_table = pages, page_table
         self.page_tokens, self.n_kv_heads, self.head_dim = page_tokens, n_kv_heads, head_dim
         self.n_pages, (self.n_seq, self.max_pages) = _nbytes(pages) // per, page_table.shape
-        self.c = _KvCache(_ptr(pages), _ptr(page_table), self.n_pages, self.n_seq, self.max_pages, page_tokens,
-                          n_kv_heads, head_dim)
+        self.c = _KV_CACHE.pack(_whole(pages, _U8, 0, "pages"), _whole(page_table, _I32, 0, "page_table"), self.n_pages,
+                                self.n_seq, self.max_pages, page_tokens, n_kv_heads, head_dim)
 
 
 def kv_append_q4_0(cache: KVCache, k, v, seq, pos, q=None, q_out=None, rope=None, rope_style: int = ROPE_HALVES,
@@ -497,42 +502,45 @@ def kv_append_q4_0(cache: KVCache, k, v, seq, pos, q=None, q_out=None, rope=None
     """Append tokens (fp32 k and v, [n_tok][heads * head_dim] or [n_tok][heads][head_dim], tokens may be strided) to
     their sequences' pages, rotated by rope (fp32 [positions][rot_dim]: cosines, then sines) and quantized to Q4_0.
     With q, returns it rotated (q_out). k_val, v_val: fp16, the values the cache then holds."""
-    n_tok, dim = k.shape[0], cache.head_dim
+    dim = cache.head_dim
     kv = cache.n_kv_heads * dim
-    _check(v.shape[0] == n_tok, "kv_append_q4_0: k and v must have the same tokens")
-    a = _KvAppendArgs(k=_rows_of(k, kv, "k"), v=_rows_of(v, kv, "v"), seq=_i32(seq, n_tok, "seq"),
-                      pos=_i32(pos, n_tok, "pos"), k_stride=_stride_of(k, kv), v_stride=_stride_of(v, kv), n_tok=n_tok,
-                      rope_style=rope_style)
+    pk, n_tok, wk, sk = _rows(k, "k")
+    pv, nv, wv, sv = _rows(v, "v")
+    if wk != kv or wv != kv or nv != n_tok:
+        _bad(f"kv_append_q4_0: k and v must be [n_tok][{kv}]")
+    pq = po = heads = sq = pr = rot = positions = pkv = pvv = ps = 0
     if q is not None:
-        width = q[0].numel() if n_tok else dim
-        _check(q.shape[0] == n_tok and width % dim == 0, "kv_append_q4_0: q must be [n_tok][heads * head_dim]")
-        a.q, a.q_stride, a.n_q_heads = _rows_of(q, width, "q"), _stride_of(q, width), width // dim
+        pq, nq, wq, sq = _rows(q, "q")
+        heads = wq // dim
+        if nq != n_tok or heads * dim != wq:
+            _bad("kv_append_q4_0: q must be [n_tok][heads * head_dim]")
         if q_out is None:
-            q_out = _make((n_tok, width // dim, dim), torch.float32, q.device, stream)
-        _check(q_out.dtype == torch.float32 and q_out.numel() == n_tok * width, "kv_append_q4_0: q_out must be float32, q's size")
-        a.q_out = _ptr(q_out)
+            q_out = _make((n_tok, heads, dim), _F32, q.device, stream)
+        po = _whole(q_out, _F32, n_tok * wq, "q_out")
     if rope is not None:
-        _check(rope.dim() == 2 and rope.dtype == torch.float32, "kv_append_q4_0: rope must be float32 [positions][rot_dim]")
-        a.rope, (a.rope_rows, a.rot_dim) = _ptr(rope), rope.shape
-    for name, t in (("k_val", k_val), ("v_val", v_val)):
-        if t is not None:
-            _check(t.dtype == torch.float16 and t.numel() == n_tok * kv, f"kv_append_q4_0: {name} must be float16, k's size")
-            setattr(a, name, _ptr(t))
+        positions, rot = rope.shape
+        pr = _whole(rope, _F32, 0, "rope")
+    if k_val is not None:
+        pkv = _whole(k_val, _F16, n_tok * kv, "k_val")
+    if v_val is not None:
+        pvv = _whole(v_val, _F16, n_tok * kv, "v_val")
     if status is not None:
-        a.status_dev = _i32(status, 1, "status")
-    _call("zdmmv_kv_append_q4_0", ctypes.byref(cache.c), ctypes.byref(a), _stream(stream))
+        ps = _whole(status, _I32, 1, "status")
+    args = _KV_APPEND_ARGS.pack(pk, pv, pq, _whole(seq, _I32, n_tok, "seq"), _whole(pos, _I32, n_tok, "pos"), pr, po, pkv,
+                                pvv, ps, sk, sv, sq, positions, n_tok, heads, rot, rope_style)
+    _enter("zdmmv_kv_append_q4_0", cache.c, args, _raw_stream(stream))
     return q_out
 
 
 def attn_q4_0_workspace_bytes(cache: KVCache, n_q_heads: int, max_q_len: int, max_kv_len: int) -> int:
-    return int(lib().zdmmv_attn_q4_0_workspace_bytes(ctypes.byref(cache.c), n_q_heads, max_q_len, max_kv_len))
+    return int(lib().zdmmv_attn_q4_0_workspace_bytes(cache.c, n_q_heads, max_q_len, max_kv_len))
 
 
 def attn_q4_0_workspace(cache: KVCache, n_q_heads: int, max_q_len: int, max_kv_len: int):
     """A workspace for attn_q4_0 calls of these bounds or smaller ones, one in flight at a time (zeros: its counters
     start at zero, and every call leaves them so)."""
     n = attn_q4_0_workspace_bytes(cache, n_q_heads, max_q_len, max_kv_len)
-    return torch.zeros(n, dtype=torch.uint8, device=cache.pages.device)
+    return torch.zeros(n, dtype=_U8, device=cache.pages.device)
 
 
 def attn_q4_0(cache: KVCache, q, q_start, kv_len, max_q_len: int, max_kv_len: int, scale: float | None = None,
@@ -540,22 +548,18 @@ def attn_q4_0(cache: KVCache, q, q_start, kv_len, max_q_len: int, max_kv_len: in
     """Attention of the new tokens q (fp32 [n_tok][heads][head_dim] or [n_tok][heads * head_dim]) over the cache;
     sequence s has the rows q_start[s] .. q_start[s+1]-1 and kv_len[s] tokens in the cache. scale: default
     1/sqrt(head_dim). Returns out, fp32 [n_tok][heads][head_dim]."""
-    n_tok, dim = q.shape[0], cache.head_dim
-    width = q[0].numel() if n_tok else dim * cache.n_kv_heads
+    dim, n_seq = cache.head_dim, cache.n_seq
+    pq, n_tok, width, sq = _rows(q, "q")
     heads = width // dim
-    _check(width % dim == 0, "attn_q4_0: q must be [n_tok][heads * head_dim]")
+    if heads * dim != width:
+        _bad("attn_q4_0: q must be [n_tok][heads * head_dim]")
     if out is None:
-        out = _make((n_tok, heads, dim), torch.float32, q.device, stream)
-    _check(out.dtype == torch.float32 and out.numel() == n_tok * width, "attn_q4_0: out must be float32, q's size")
+        out = _make((n_tok, heads, dim), _F32, q.device, stream)
     if workspace is None:
-        workspace = _make(attn_q4_0_workspace_bytes(cache, heads, max_q_len, max_kv_len), torch.uint8, q.device, stream,
-                          torch.zeros)
-    a = _AttnArgs(q=_rows_of(q, width, "q"), q_start=_i32(q_start, cache.n_seq + 1, "q_start"),
-                  kv_len=_i32(kv_len, cache.n_seq, "kv_len"), out=_ptr(out), workspace=_ptr(workspace),
-                  workspace_bytes=_nbytes(workspace), q_stride=_stride_of(q, width), n_tok=n_tok, n_q_heads=heads,
-                  max_q_len=max_q_len, max_kv_len=max_kv_len, window=window,
-                  scale=dim ** -0.5 if scale is None else scale)
-    if status is not None:
-        a.status_dev = _i32(status, 1, "status")
-    _call("zdmmv_attn_q4_0", ctypes.byref(cache.c), ctypes.byref(a), _stream(stream))
+        workspace = _make(attn_q4_0_workspace_bytes(cache, heads, max_q_len, max_kv_len), _U8, q.device, stream, torch.zeros)
+    args = _ATTN_ARGS.pack(pq, _whole(q_start, _I32, n_seq + 1, "q_start"), _whole(kv_len, _I32, n_seq, "kv_len"),
+                           _whole(out, _F32, n_tok * width, "out"), _whole(workspace, _U8, 0, "workspace"),
+                           0 if status is None else _whole(status, _I32, 1, "status"), workspace.numel(), sq, n_tok, heads,
+                           max_q_len, max_kv_len, window, dim ** -0.5 if scale is None else scale)
+    _enter("zdmmv_attn_q4_0", cache.c, args, _raw_stream(stream))
     return out

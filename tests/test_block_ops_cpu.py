@@ -16,28 +16,84 @@ def L():
     return Z.lib()
 
 
+class _RmsnormArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("x", "residual", "weight", "out", "xq", "y")] + [
+        (n, ctypes.c_int64) for n in ("rows", "cols", "x_stride", "residual_stride")] + [("eps", ctypes.c_float)]
+
+
+class _KvCache(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_void_p), ("page_table", ctypes.c_void_p), ("n_pages", ctypes.c_int64)] + [
+        (n, ctypes.c_int32) for n in ("n_seq", "max_pages", "page_tokens", "n_kv_heads", "head_dim")]
+
+
+class _KvAppendArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "q", "seq", "pos", "rope", "q_out", "k_val", "v_val",
+                                               "status_dev")] + [
+        (n, ctypes.c_int64) for n in ("k_stride", "v_stride", "q_stride", "rope_rows")] + [
+        (n, ctypes.c_int32) for n in ("n_tok", "n_q_heads", "rot_dim", "rope_style")]
+
+
+class _AttnArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("q", "q_start", "kv_len", "out", "workspace", "status_dev")] + [
+        ("workspace_bytes", ctypes.c_size_t), ("q_stride", ctypes.c_int64)] + [
+        (n, ctypes.c_int32) for n in ("n_tok", "n_q_heads", "max_q_len", "max_kv_len", "window")] + [
+        ("scale", ctypes.c_float)]
+
+
+def _header_fields(name):
+    """[(C type, field)] of a struct of include/zdmmv.h, in order."""
+    import os
+    import re
+    from gguf_block_quant_gb300 import _build
+    text = re.sub(r"/\*.*?\*/", "", open(os.path.join(_build.INCLUDE, "zdmmv.h")).read(), flags=re.S)
+    body = re.search(r"typedef struct \{([^}]*)\} " + name + ";", text).group(1)
+    out = []
+    for line in body.split(";"):
+        line = " ".join(line.split())
+        if line:
+            kind = re.match(r"(const )?(\w+)", line).group(2)
+            for f in line[line.index(kind) + len(kind):].split(","):
+                out.append(("ptr" if "*" in f else kind, f.replace("*", "").strip()))
+    return out
+
+
+@pytest.mark.parametrize("name, c, packed", [
+    ("zdmmv_rmsnorm_args", _RmsnormArgs, Z._RMSNORM_ARGS), ("zdmmv_kv_cache", _KvCache, Z._KV_CACHE),
+    ("zdmmv_kv_append_args", _KvAppendArgs, Z._KV_APPEND_ARGS), ("zdmmv_attn_args", _AttnArgs, Z._ATTN_ARGS)])
+def test_packed_structs_match_the_header(name, c, packed):
+    kinds = {"ptr": ctypes.c_void_p, "int64_t": ctypes.c_int64, "int32_t": ctypes.c_int32, "float": ctypes.c_float,
+             "size_t": ctypes.c_size_t}
+    want = _header_fields(name)
+    # pointers that share a line ("const float *k, *v") keep their star each
+    assert [(f, t) for f, t in c._fields_] == [(f, kinds[k]) for k, f in want]
+    assert packed.size == ctypes.sizeof(c)
+    values = [1000 + i for i in range(len(want))]
+    s = c.from_buffer_copy(packed.pack(*values))
+    assert [getattr(s, f) for _, f in want] == values
+
+
 def _cache(**k):
     d = dict(pages=FAKE, page_table=FAKE, n_pages=9, n_seq=2, max_pages=4, page_tokens=32, n_kv_heads=2, head_dim=128)
-    return Z._KvCache(**{**d, **k})
+    return _KvCache(**{**d, **k})
 
 
 def _norm(**k):
     d = dict(x=FAKE, residual=FAKE, weight=FAKE, out=FAKE, xq=FAKE, y=FAKE, rows=3, cols=64, x_stride=64,
              residual_stride=64, eps=1e-6)
-    return Z._RmsnormArgs(**{**d, **k})
+    return _RmsnormArgs(**{**d, **k})
 
 
 def _append(**k):
     d = dict(k=FAKE, v=FAKE, q=FAKE, seq=FAKE, pos=FAKE, rope=FAKE, q_out=FAKE, k_val=FAKE, v_val=FAKE,
              status_dev=FAKE, k_stride=256, v_stride=256, q_stride=1024, rope_rows=100, n_tok=3, n_q_heads=8,
              rot_dim=128, rope_style=0)
-    return Z._KvAppendArgs(**{**d, **k})
+    return _KvAppendArgs(**{**d, **k})
 
 
 def _attn(**k):
     d = dict(q=FAKE, q_start=FAKE, kv_len=FAKE, out=FAKE, workspace=FAKE, status_dev=FAKE, workspace_bytes=1 << 40,
              q_stride=1024, n_tok=3, n_q_heads=8, max_q_len=2, max_kv_len=100, window=0, scale=0.1)
-    return Z._AttnArgs(**{**d, **k})
+    return _AttnArgs(**{**d, **k})
 
 
 @pytest.mark.parametrize("code, change", [
