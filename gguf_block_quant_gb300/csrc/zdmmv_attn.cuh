@@ -40,22 +40,6 @@
 
 namespace zdmmv {
 
-// n / d and n % d for 0 <= n < 2^31 by a multiplication: q = n * ceil(2^p / d) >> p with p = 31 + ceil(log2 d), exact
-// there (the product's error is below n / 2^p <= 1 / d).
-struct FastDiv {
-    uint32_t d, m, p;
-    __host__ static FastDiv of(int32_t d) {
-        FastDiv f{static_cast<uint32_t>(d), 0, 31};
-        while ((1ull << (f.p - 31)) < f.d) ++f.p;
-        f.m = static_cast<uint32_t>(((1ull << f.p) + f.d - 1) / f.d);
-        return f;
-    }
-    __device__ __forceinline__ int div(int n) const {
-        return static_cast<int>(static_cast<uint64_t>(static_cast<uint32_t>(n)) * m >> p);
-    }
-    __device__ __forceinline__ int mod(int n, int q) const { return n - q * static_cast<int>(d); }
-};
-
 struct AttnArgs {
     KvView c;
     FastDiv by_ct, by_heads, by_group, by_page_tiles;

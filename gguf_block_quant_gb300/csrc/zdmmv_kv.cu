@@ -40,30 +40,28 @@ namespace {
 
 struct AppendArgs {
     KvView c;
+    FastDiv by_groups, by_page;
     const float *k, *v, *q;
     const int32_t *seq, *pos;
     const float *rope;
     float *q_out;
     __half *k_val, *v_val;
     int32_t *status;
+    uint32_t *fault;
     int64_t k_stride, v_stride, q_stride, rope_rows;
     int32_t n_tok, n_q_heads, rot_dim, halves;
 };
 
-constexpr int64_t kManyWarps = 152 * 64;  // as many (token, head) pairs as the device holds warps
-constexpr int kAppendWarps = 4;
-
-// The rotation of four neighbouring dimensions e0 .. e0+3 of a head at `src`: their cosines and sines, the partner
-// dimensions, and which half of its pair each is. Every product and sum is rounded by itself (no fused multiply-add), so
-// that the result is the same wherever it is computed.
+// The rotation of four neighbouring dimensions e0 .. e0+3 of a head: their cosines and sines, the sines of a pair's first
+// dimension negated (its result is x cos - partner sin). Every product and sum is rounded by itself (no fused
+// multiply-add), so that the result is the same wherever it is computed.
 struct Turn {
-    float c[4], s[4];  // sign of s: minus for a pair's first dimension, whose result is x cos - partner sin
+    float c[4], s[4];
 };
 
 // FAST: four neighbouring dimensions are all rotated or none, and their partners and angles are neighbours too (pairs:
 // rot_dim a multiple of 4; halves: rot_dim a multiple of 8), so everything is 128-bit loads.
-template <bool FAST>
-__device__ __forceinline__ Turn load_turn(const AppendArgs &a, int pos, int e0) {
+template <bool FAST> __device__ __forceinline__ Turn load_turn(const AppendArgs &a, int pos, int e0) {
     Turn t;
     const int half = a.rot_dim / 2;
     const float *row = a.rope + static_cast<int64_t>(pos) * a.rot_dim;
@@ -95,6 +93,7 @@ __device__ __forceinline__ Turn load_turn(const AppendArgs &a, int pos, int e0) 
     }
     return t;
 }
+// Four dimensions of a head at `src` (global or shared memory) and, where the head is turned, their partners.
 template <bool FAST>
 __device__ __forceinline__ void load_head(const AppendArgs &a, const float *src, int e0, bool turned, float (&v)[4], float (&o)[4]) {
     const float4 x = *reinterpret_cast<const float4 *>(src + e0);
@@ -113,137 +112,254 @@ __device__ __forceinline__ void load_head(const AppendArgs &a, const float *src,
         }
     }
 }
+template <bool FAST>
+__device__ __forceinline__ void turn_head(const AppendArgs &a, int e0, const Turn &t, const float (&o)[4], float (&x)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (FAST || e0 + i < a.rot_dim) x[i] = __fadd_rn(__fmul_rn(x[i], t.c[i]), __fmul_rn(o[i], t.s[i]));
+}
+// The head's row in the call's inputs: heads 0 .. of q, then those of k, then those of v.
+__device__ __forceinline__ const float *head_row(const AppendArgs &a, int tok, int head, int dim) {
+    const int kvh = head - a.n_q_heads;
+    if (kvh < 0) return a.q + tok * a.q_stride + static_cast<int64_t>(head) * dim;
+    if (kvh < a.c.n_kv_heads) return a.k + tok * a.k_stride + static_cast<int64_t>(kvh) * dim;
+    return a.v + tok * a.v_stride + static_cast<int64_t>(kvh - a.c.n_kv_heads) * dim;
+}
 
-// One warp per token and HEADS neighbouring heads of its q, k and v: lane l holds the four dimensions 4l .. 4l+3 of each
-// pass of 128, loads them for all its heads before it stores any (so q_out may be q), and keeps the token's cosines and
-// sines for all of them. Bound by memory for prompts (HEADS = 4: four heads' loads in flight), by latency for a few
-// tokens (HEADS = 1: as many warps as heads).
-template <int NB, int HEADS, bool FAST>
-__global__ void __launch_bounds__(kAppendWarps * 32) kv_append_kernel(AppendArgs a) {
+// Where a token goes in the cache.
+struct Place {
+    int page, in;   // page (0 where none is written), token of the page
+    bool ok, bad;   // written to the cache; outside what the cache and the rotation table have
+};
+// The page's look-up is the one load: place_check looks at what it brought.
+__device__ __forceinline__ Place place_of(const AppendArgs &a, int pos, int seq) {
+    Place w;
+    const bool pad = pos < 0;
+    const int slot = pad ? 0 : a.by_page.div(pos);
+    w.in = pad ? 0 : a.by_page.mod(pos, slot);
+    w.bad = !pad && (seq < 0 || seq >= a.c.n_seq || slot >= a.c.max_pages || (a.rot_dim > 0 && pos >= a.rope_rows));
+    w.ok = !pad && !w.bad;
+    w.page = w.ok ? a.c.table[static_cast<int64_t>(seq) * a.c.max_pages + slot] : 0;
+    return w;
+}
+__device__ __forceinline__ void place_check(const AppendArgs &a, Place &w, int lane) {
+    if (w.page < 0 || w.page >= a.c.n_pages) w.bad = true;
+    if (!w.bad) return;
+    w.ok = false;
+    w.page = 0;
+    if (lane == 0 && a.status) *a.status = 1;
+}
+__device__ __forceinline__ float place_fill(const Place &w) { return w.bad ? __int_as_float(0x7fffffff) : 0.0f; }
+
+// Four dimensions e0 .. e0+3 of a (rotated) head: q's are stored; k's and v's are quantized and stored in the cache and as
+// values. The whole warp calls it: a block's 8 lanes exchange its maximum.
+template <int NB>
+__device__ __forceinline__ void put_head(const AppendArgs &a, const Place &w, int tok, int head, int e0, int lane, const float (&x)[4]) {
+    using G = KvGeom<NB>;
+    const bool inside = e0 < G::kDim;
+    const int kvh = head - a.n_q_heads;
+    if (kvh < 0) {
+        if (inside)
+            *reinterpret_cast<float4 *>(a.q_out + (static_cast<int64_t>(tok) * a.n_q_heads + head) * G::kDim + e0) =
+                make_float4(x[0], x[1], x[2], x[3]);
+        return;
+    }
+    const bool is_k = kvh < a.c.n_kv_heads;
+    const int h = is_k ? kvh : kvh - a.c.n_kv_heads;
+    // the first value of the largest magnitude, over the block's 8 lanes
+    float big = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
+#pragma unroll
+    for (int s = 1; s < 8; s <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, s));
+    float m = x[3];
+#pragma unroll
+    for (int i = 2; i >= 0; --i)
+        if (fabsf(x[i]) == big) m = x[i];
+    const uint32_t has = __ballot_sync(0xffffffffu, fabsf(m) == big) >> (lane & 24) & 0xffu;
+    m = __shfl_sync(0xffffffffu, m, (lane & 24) + (has ? __ffs(has) - 1 : 0));
+    const float d = m * -0.125f;  // exactly m / -8
+    const float id = d != 0.0f ? __frcp_rn(d) : 0.0f;
+    const __half dh = __float2half_rn(d);
+    uint32_t code[4], packed = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int c = static_cast<int>(__fadd_rn(__fmul_rn(x[i], id), 8.5f));
+        code[i] = c < 0 ? 0 : (c > 15 ? 15 : c);
+        packed |= code[i] << (4 * i);
+    }
+    const uint32_t upper = __shfl_down_sync(0xffffffffu, packed, 1);
+    if (!inside) return;
+    const int b = e0 / kQK, g = (e0 % kQK) / 4, r = w.in % kKvSlab;
+    if (w.ok) {
+        uint8_t *tile = a.c.pages + w.page * a.c.page_bytes +
+                        static_cast<int64_t>(h * (a.c.page_tokens / kKvSlab) + w.in / kKvSlab) * G::kTileBytes;
+        __half *scales = reinterpret_cast<__half *>(tile + (is_k ? G::kKScaleAt : G::kVScaleAt));
+        if (g == 0) scales[G::scale_half(r, b)] = dh;
+        if (is_k) {
+            if ((g & 1) == 0) reinterpret_cast<uint32_t *>(tile)[G::k_word(r, b, g / 2)] = packed | (upper << 16);
+        } else {
+            reinterpret_cast<uint16_t *>(tile + G::kVAt)[G::v_half(r, b, g)] = static_cast<uint16_t>(packed);
+        }
+    }
+    __half *val = is_k ? a.k_val : a.v_val;
+    if (!val) return;
+    const float df = __half2float(dh);
+    __half2 y[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        y[i] = __floats2half2_rn(df * (static_cast<float>(code[2 * i]) - 8.0f), df * (static_cast<float>(code[2 * i + 1]) - 8.0f));
+    *reinterpret_cast<uint2 *>(val + (static_cast<int64_t>(tok) * a.c.n_kv_heads + h) * G::kDim + e0) = *reinterpret_cast<uint2 *>(y);
+}
+
+// Few tokens: one warp per token and head. Lane l holds the four dimensions 4l .. 4l+3 of each pass of 128 and loads all
+// of a head before it stores any (so q_out may be q); the look-up of the token's place runs beside the loads. Bound by
+// the latency of its three dependent loads (2.2 us for 48 tokens of 48 heads of 128).
+constexpr int kAppendWarps = 4;
+template <int NB, bool FAST> __global__ void __launch_bounds__(kAppendWarps * 32) kv_append_kernel(AppendArgs a) {
     using G = KvGeom<NB>;
     constexpr int kPass = (G::kDim + 127) / 128;
     const int lane = threadIdx.x & 31;
-    const int heads = a.n_q_heads + 2 * a.c.n_kv_heads;
-    const int groups = (heads + HEADS - 1) / HEADS;
-    const int64_t job = static_cast<int64_t>(blockIdx.x) * kAppendWarps + (threadIdx.x >> 5);
-    const int64_t tok = job / groups;
-    const int h0 = static_cast<int>(job - tok * groups) * HEADS;
+    const int job = static_cast<int>(blockIdx.x) * kAppendWarps + static_cast<int>(threadIdx.x >> 5);
+    const int tok = a.by_groups.div(job), head = a.by_groups.mod(job, tok);
     block_op_wait();
     block_op_release();
     if (tok >= a.n_tok) return;
+    const bool turned = head < a.n_q_heads + a.c.n_kv_heads;
     const int pos = a.pos[tok], seq = a.seq[tok];
-    // where the token goes; bad: outside what the cache and the rotation table have
-    const int slot = pos / a.c.page_tokens, in = pos - slot * a.c.page_tokens;
-    const bool pad = pos < 0;
-    bool bad = !pad && (seq < 0 || seq >= a.c.n_seq || slot >= a.c.max_pages || (a.rot_dim > 0 && pos >= a.rope_rows));
-    const int page = pad || bad ? 0 : a.c.table[static_cast<int64_t>(seq) * a.c.max_pages + slot];
-    if (page < 0 || page >= a.c.n_pages) bad = true;
-    if (bad && lane == 0 && a.status) *a.status = 1;
-    const bool ok = !pad && !bad;
-    uint8_t *tiles = a.c.pages + (ok ? page : 0) * a.c.page_bytes + static_cast<int64_t>(in / kKvSlab) * G::kTileBytes;
-    const int64_t head_bytes = static_cast<int64_t>(a.c.page_tokens / kKvSlab) * G::kTileBytes;
-    const int r = in % kKvSlab;
-    const float fill = bad ? __int_as_float(0x7fffffff) : 0.0f;
-    float v[HEADS][kPass][4], o[HEADS][kPass][4];
+    float v[kPass][4], o[kPass][4];
+#pragma unroll
+    for (int p = 0; p < kPass; ++p) {
+        const int e0 = p * 128 + 4 * lane;
+        v[p][0] = v[p][1] = v[p][2] = v[p][3] = 0.0f;
+        if (e0 < G::kDim) load_head<FAST>(a, head_row(a, tok, head, G::kDim), e0, turned && e0 < a.rot_dim, v[p], o[p]);
+    }
+    Place w = place_of(a, pos, seq);
     Turn turn[kPass];
 #pragma unroll
-    for (int u = 0; u < HEADS; ++u)
-#pragma unroll
-        for (int p = 0; p < kPass; ++p) {
-            const int head = h0 + u, kvh = head - a.n_q_heads, e0 = p * 128 + 4 * lane;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[u][p][i] = fill;
-            if (!ok || e0 >= G::kDim || head >= heads) continue;
-            const float *src = kvh < 0 ? a.q + tok * a.q_stride + static_cast<int64_t>(head) * G::kDim
-                               : (kvh < a.c.n_kv_heads ? a.k + tok * a.k_stride + static_cast<int64_t>(kvh) * G::kDim
-                                                       : a.v + tok * a.v_stride + static_cast<int64_t>(kvh - a.c.n_kv_heads) * G::kDim);
-            load_head<FAST>(a, src, e0, e0 < a.rot_dim && kvh < a.c.n_kv_heads, v[u][p], o[u][p]);
-        }
-#pragma unroll
     for (int p = 0; p < kPass; ++p)
-        if (ok && p * 128 + 4 * lane < a.rot_dim) turn[p] = load_turn<FAST>(a, pos, p * 128 + 4 * lane);
+        if (w.ok && turned && p * 128 + 4 * lane < a.rot_dim) turn[p] = load_turn<FAST>(a, pos, p * 128 + 4 * lane);
+    place_check(a, w, lane);
     __syncwarp();
 #pragma unroll
-    for (int u = 0; u < HEADS; ++u) {
-        const int head = h0 + u, kvh = head - a.n_q_heads;
-        if (head >= heads) break;
-#pragma unroll
-        for (int p = 0; p < kPass; ++p) {
-            const int e0 = p * 128 + 4 * lane;
-            const bool inside = e0 < G::kDim;
-            float (&x)[4] = v[u][p];
-            if (ok && e0 < a.rot_dim && kvh < a.c.n_kv_heads) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (FAST || e0 + i < a.rot_dim) x[i] = __fadd_rn(__fmul_rn(x[i], turn[p].c[i]), __fmul_rn(o[u][p][i], turn[p].s[i]));
-            }
-            if (kvh < 0) {
-                if (inside)
-                    *reinterpret_cast<float4 *>(a.q_out + (tok * a.n_q_heads + head) * G::kDim + e0) = make_float4(x[0], x[1], x[2], x[3]);
-                continue;
-            }
-            const bool is_k = kvh < a.c.n_kv_heads;
-            const int h = is_k ? kvh : kvh - a.c.n_kv_heads;
-            // the first value of the largest magnitude, over the block's 8 lanes
-            float m = x[0];
-            int at = e0;
-#pragma unroll
-            for (int i = 1; i < 4; ++i)
-                if (fabsf(x[i]) > fabsf(m)) { m = x[i]; at = e0 + i; }
-#pragma unroll
-            for (int s = 1; s < 8; s <<= 1) {
-                const float om = __shfl_xor_sync(0xffffffffu, m, s);
-                const int oat = __shfl_xor_sync(0xffffffffu, at, s);
-                if (fabsf(om) > fabsf(m) || (fabsf(om) == fabsf(m) && oat < at)) { m = om; at = oat; }
-            }
-            const float d = m / -8.0f;
-            const float id = d != 0.0f ? 1.0f / d : 0.0f;
-            const __half dh = __float2half_rn(d);
-            uint32_t code[4], packed = 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int c = static_cast<int>(__fadd_rn(__fmul_rn(x[i], id), 8.5f));
-                code[i] = c < 0 ? 0 : (c > 15 ? 15 : c);
-                packed |= code[i] << (4 * i);
-            }
-            const int b = e0 / kQK, g = (e0 % kQK) / 4;
-            const uint32_t upper = __shfl_down_sync(0xffffffffu, packed, 1);
-            if (!inside) continue;
-            if (ok) {
-                uint8_t *tile = tiles + h * head_bytes;
-                __half *scales = reinterpret_cast<__half *>(tile + (is_k ? G::kKScaleAt : G::kVScaleAt));
-                if (g == 0) scales[G::scale_half(r, b)] = dh;
-                if (is_k) {
-                    if ((g & 1) == 0) reinterpret_cast<uint32_t *>(tile)[G::k_word(r, b, g / 2)] = packed | (upper << 16);
-                } else {
-                    reinterpret_cast<uint16_t *>(tile + G::kVAt)[G::v_half(r, b, g)] = static_cast<uint16_t>(packed);
-                }
-            }
-            __half *val = is_k ? a.k_val : a.v_val;
-            if (val) {
-                const float df = __half2float(dh);
-                __half2 w[2];
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    w[i] = __floats2half2_rn(df * (static_cast<float>(code[2 * i]) - 8.0f), df * (static_cast<float>(code[2 * i + 1]) - 8.0f));
-                *reinterpret_cast<uint2 *>(val + (tok * a.c.n_kv_heads + h) * G::kDim + e0) = *reinterpret_cast<uint2 *>(w);
-            }
-        }
+    for (int p = 0; p < kPass; ++p) {
+        const int e0 = p * 128 + 4 * lane;
+        if (!w.ok) v[p][0] = v[p][1] = v[p][2] = v[p][3] = place_fill(w);
+        else if (turned && e0 < a.rot_dim) turn_head<FAST>(a, e0, turn[p], o[p], v[p]);
+        put_head<NB>(a, w, tok, head, e0, lane, v[p]);
     }
 }
 
-template <int NB, int HEADS, bool FAST> cudaError_t launch_append_as(const AppendArgs &a, cudaStream_t st) {
+// Prompts: bound by memory. Each warp takes a stretch of consecutive (token, group of kStreamHeads heads) pairs and keeps
+// the next kStreamSlots of them on their way into its own ring in shared memory (a bulk copy a head), so that the loads
+// wait neither for the token's look-up nor for the quantization; a token's place, cosines and sines are read once and
+// kept for all its heads. 4093 tokens of 48 heads of 128: one warp a head without the ring 49 us at best (48 warps an
+// SM, each with its loads in flight for half of its life), with it 38 us (74% of the copy rate).
+constexpr int kStreamWarps = 8, kStreamHeads = 4, kStreamSlots = 3;
+template <int NB, bool FAST> __global__ void __launch_bounds__(kStreamWarps * 32, NB <= 4 ? 3 : 2) kv_append_stream_kernel(AppendArgs a, int n_jobs) {
+    using G = KvGeom<NB>;
+    constexpr int kPass = (G::kDim + 127) / 128, kHeadBytes = G::kDim * 4, kSlotBytes = kStreamHeads * kHeadBytes;
+    extern __shared__ __align__(128) uint8_t smem[];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem) + warp * kStreamSlots;
+    uint8_t *ring = smem + 256 + warp * (kStreamSlots * kSlotBytes);
+    if (lane == 0) {
+        for (int s = 0; s < kStreamSlots; ++s) mbar_init(&full[s], 1);
+        fence_barrier_init();
+    }
+    __syncwarp();
+    block_op_wait();
+    block_op_release();
     const int heads = a.n_q_heads + 2 * a.c.n_kv_heads;
-    const int64_t jobs = static_cast<int64_t>(a.n_tok) * ((heads + HEADS - 1) / HEADS);
-    const int64_t ctas = (jobs + kAppendWarps - 1) / kAppendWarps;
-    if (ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    return launch_block_op(kv_append_kernel<NB, HEADS, FAST>, dim3(static_cast<unsigned>(ctas)), dim3(kAppendWarps * 32), 0, st, a);
+    const int64_t n_warps = static_cast<int64_t>(gridDim.x) * kStreamWarps, me = static_cast<int64_t>(blockIdx.x) * kStreamWarps + warp;
+    const int first = static_cast<int>(n_jobs * me / n_warps), last = static_cast<int>(n_jobs * (me + 1) / n_warps);
+    const uint64_t policy = l2_evict_first_policy();
+    const auto copy = [&](int job, int s) {
+        const int tok = a.by_groups.div(job), h0 = a.by_groups.mod(job, tok) * kStreamHeads;
+        const int n = min(kStreamHeads, heads - h0);
+        if (lane == 0) mbar_arrive_expect_tx(&full[s], n * kHeadBytes);
+        __syncwarp();
+        if (lane < n)
+            bulk_copy_g2s(ring + s * kSlotBytes + lane * kHeadBytes, head_row(a, tok, h0 + lane, G::kDim), kHeadBytes, &full[s], policy);
+    };
+    for (int s = 0; s < kStreamSlots; ++s)
+        if (first + s < last) copy(first + s, s);
+    int at = -1, s = 0;
+    uint32_t phase = 0;
+    Place w{};
+    Turn turn[kPass];
+    bool ok = true;
+    for (int job = first; job < last; ++job) {
+        const int tok = a.by_groups.div(job), h0 = a.by_groups.mod(job, tok) * kStreamHeads;
+        if (tok != at) {
+            at = tok;
+            const int pos = a.pos[tok];
+            w = place_of(a, pos, a.seq[tok]);
+#pragma unroll
+            for (int p = 0; p < kPass; ++p)
+                if (w.ok && p * 128 + 4 * lane < a.rot_dim) turn[p] = load_turn<FAST>(a, pos, p * 128 + 4 * lane);
+            place_check(a, w, lane);
+        }
+        if (!__all_sync(0xffffffffu, mbar_wait(&full[s], phase))) {
+            if (lane == 0) atomicOr(a.fault, 1u);
+            ok = false;
+        }
+        const float *rows = reinterpret_cast<const float *>(ring + s * kSlotBytes);
+#pragma unroll 2
+        for (int u = 0; u < min(kStreamHeads, heads - h0); ++u) {
+            const int head = h0 + u;
+            const bool turned = head < a.n_q_heads + a.c.n_kv_heads;
+#pragma unroll
+            for (int p = 0; p < kPass; ++p) {
+                const int e0 = p * 128 + 4 * lane;
+                float v[4] = {0.0f, 0.0f, 0.0f, 0.0f}, o[4];
+                if (!w.ok || !ok) {
+                    v[0] = v[1] = v[2] = v[3] = ok ? place_fill(w) : __int_as_float(0x7fffffff);
+                } else if (e0 < G::kDim) {
+                    const bool turn_it = turned && e0 < a.rot_dim;
+                    load_head<FAST>(a, rows + u * G::kDim, e0, turn_it, v, o);
+                    if (turn_it) turn_head<FAST>(a, e0, turn[p], o, v);
+                }
+                put_head<NB>(a, w, tok, head, e0, lane, v);
+            }
+        }
+        __syncwarp();
+        if (ok && job + kStreamSlots < last) {
+            fence_proxy_async_smem();
+            copy(job + kStreamSlots, s);
+        }
+        if (++s == kStreamSlots) {
+            s = 0;
+            phase ^= 1;
+        }
+    }
+    if (!ok) {  // leave only when the copies have landed, as far as they will
+        for (int k = 0; k < kStreamSlots; ++k) (void)mbar_wait(&full[k], 0);
+    }
+}
+
+template <int NB, bool FAST> cudaError_t launch_append_as(AppendArgs a, cudaStream_t st) {
+    const int heads = a.n_q_heads + 2 * a.c.n_kv_heads;
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    // the stream kernel from as many (token, head) pairs as the device holds warps
+    const int64_t pairs = static_cast<int64_t>(a.n_tok) * heads;
+    if (pairs <= static_cast<int64_t>(sms) * 64) {
+        a.by_groups = FastDiv::of(heads);
+        return launch_block_op(kv_append_kernel<NB, FAST>, dim3(static_cast<unsigned>((pairs + kAppendWarps - 1) / kAppendWarps)),
+                               dim3(kAppendWarps * 32), 0, st, a);
+    }
+    const int groups = (heads + kStreamHeads - 1) / kStreamHeads;
+    a.by_groups = FastDiv::of(groups);
+    const int n_jobs = a.n_tok * groups;
+    constexpr size_t kSmem = 256 + static_cast<size_t>(kStreamWarps) * kStreamSlots * kStreamHeads * NB * kQK * 4;
+    constexpr int kCtas = kSmem <= 55 * 1024 ? 3 : 2;  // per SM: as many as fit
+    e = smem_limit_raised<&kv_append_stream_kernel<NB, FAST>>();
+    if (e != cudaSuccess) return e;
+    return launch_block_op(kv_append_stream_kernel<NB, FAST>, dim3(sms * kCtas), dim3(kStreamWarps * 32), kSmem, st, a, n_jobs);
 }
 template <int NB> cudaError_t launch_append(const AppendArgs &a, cudaStream_t st) {
-    const bool fast = a.rot_dim % (a.halves ? 8 : 4) == 0;
-    const int64_t warps = static_cast<int64_t>(a.n_tok) * (a.n_q_heads + 2 * a.c.n_kv_heads);
-    if (warps > kManyWarps) return fast ? launch_append_as<NB, 4, true>(a, st) : launch_append_as<NB, 4, false>(a, st);
-    return fast ? launch_append_as<NB, 1, true>(a, st) : launch_append_as<NB, 1, false>(a, st);
+    return a.rot_dim % (a.halves ? 8 : 4) == 0 ? launch_append_as<NB, true>(a, st) : launch_append_as<NB, false>(a, st);
 }
 
 }  // namespace
@@ -269,7 +385,7 @@ zdmmv_status zdmmv_kv_append_q4_0(const zdmmv_kv_cache *cache, const zdmmv_kv_ap
     const int64_t qn = static_cast<int64_t>(g.n_q_heads) * cache->head_dim;
     if (g.n_tok < 0 || g.rot_dim < 0 || g.rot_dim % 2 || g.rot_dim > cache->head_dim ||
         (g.rope_style != ZDMMV_ROPE_PAIRS && g.rope_style != ZDMMV_ROPE_HALVES) ||
-        (g.rot_dim > 0 && g.rope_rows < 1) || g.n_q_heads < 0 || g.n_q_heads > 65535 || (g.q != nullptr) != (g.n_q_heads > 0))
+        (g.rot_dim > 0 && g.rope_rows < 1) || static_cast<int64_t>(g.n_tok) * (g.n_q_heads + 2 * cache->n_kv_heads) > 0x7fffff00 || g.n_q_heads < 0 || g.n_q_heads > 65535 || (g.q != nullptr) != (g.n_q_heads > 0))
         return ZDMMV_ERR_SHAPE;
     if (g.n_tok == 0) return ZDMMV_OK;
     if (!g.k || !g.v || !g.seq || !g.pos || (g.rot_dim > 0 && !g.rope) || (g.q && !g.q_out)) return ZDMMV_ERR_NULL;
@@ -280,12 +396,15 @@ zdmmv_status zdmmv_kv_append_q4_0(const zdmmv_kv_cache *cache, const zdmmv_kv_ap
         kv_misaligned(g.pos, 4) || kv_misaligned(g.status_dev, 4) || g.k_stride % 4 || g.v_stride % 4 ||
         (g.q && g.q_stride % 4))
         return ZDMMV_ERR_ALIGN;
+    a.by_page = FastDiv::of(cache->page_tokens);
     a.k = g.k; a.v = g.v; a.q = g.q;
     a.seq = g.seq; a.pos = g.pos; a.rope = g.rope;
     a.q_out = g.q_out;
     a.k_val = static_cast<__half *>(g.k_val);
     a.v_val = static_cast<__half *>(g.v_val);
     a.status = g.status_dev;
+    a.fault = current_fault_word();
+    if (!a.fault) return ZDMMV_ERR_CUDA;
     a.k_stride = g.k_stride; a.v_stride = g.v_stride; a.q_stride = g.q_stride; a.rope_rows = g.rope_rows;
     a.n_tok = g.n_tok; a.n_q_heads = g.n_q_heads; a.rot_dim = g.rot_dim; a.halves = g.rope_style == ZDMMV_ROPE_HALVES;
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

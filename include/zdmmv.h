@@ -615,7 +615,7 @@ typedef struct {
     int32_t *status_dev;     /* nullable device int32: 1 is stored for a bad token (below) */
     int64_t k_stride, v_stride, q_stride; /* floats, multiples of 4, >= heads*head_dim */
     int64_t rope_rows;
-    int32_t n_tok;           /* >= 0 (0 is a no-op) */
+    int32_t n_tok;           /* >= 0 (0 is a no-op); times all heads of q, k and v below 2^31 - 256 */
     int32_t n_q_heads;       /* 1 .. 65535 (0 with q NULL) */
     int32_t rot_dim;         /* even, 0 .. head_dim; 0: no rotation */
     int32_t rope_style;      /* ZDMMV_ROPE_PAIRS or ZDMMV_ROPE_HALVES */

@@ -146,6 +146,45 @@ def test_append(dim, rot, halves, page, heads, group):
     assert torch.equal(c2.pages, cache.pages)
 
 
+@pytest.mark.parametrize("dim, rot, halves", [(64, 64, True), (96, 50, True), (128, 128, True), (128, 64, False),
+                                              (192, 128, True), (256, 256, True), (256, 34, False)])
+@pytest.mark.parametrize("heads, group", [(2, 4), (1, 1), (3, 1)])
+def test_append_prompt(dim, rot, halves, heads, group):
+    """Many tokens at once (the kernel for prompts) are the same tokens a few at a time, byte for byte: two sequences, a
+    padded stretch, bad tokens among the good ones."""
+    n = -(-12000 // (heads * (group + 2)))
+    page, n_seq = 48, 2
+    max_pages = -(-n // page)
+    rng = np.random.default_rng(n + dim)
+    table = rng.permutation(2 * max_pages).reshape(n_seq, max_pages)
+    table[1, 3] = 1 << 28
+    seq = (np.arange(n) % 2).astype(np.int32)
+    pos = (np.arange(n) // 2).astype(np.int32)
+    pos[100:117] = -1
+    seq[200] = 2
+    hq = heads * group
+    g = torch.Generator("cuda").manual_seed(n)
+    joint = torch.randn(n, (hq + 2 * heads) * dim, device="cuda", generator=g)
+    q, k, v = joint[:, :hq * dim], joint[:, hq * dim:(hq + heads) * dim], joint[:, (hq + heads) * dim:]
+    rope, seq, pos = dev(R.rope_table(max_pages * page, rot)), dev(seq), dev(pos)
+    style = Z.ROPE_HALVES if halves else Z.ROPE_PAIRS
+
+    def run(step):
+        cache, _ = make_cache(2 * max_pages, page, heads, dim, table)
+        vals = [torch.empty(n, heads, dim, dtype=torch.float16, device="cuda") for _ in range(2)]
+        out, status = torch.empty(n, hq, dim, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+        for i in range(0, n, step):
+            s = slice(i, min(n, i + step))
+            Z.kv_append_q4_0(cache, k[s], v[s], seq[s], pos[s], q=q[s], q_out=out[s], rope=rope, rope_style=style,
+                             k_val=vals[0][s], v_val=vals[1][s], status=status)
+        return cache.pages, out, *vals, status
+    once, pieces = run(n), run(97)
+    assert once[4].item() == 1
+    for a, b in zip(once, pieces):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    assert Z.device_status() == 0
+
+
 def test_append_bad_tokens():
     page, heads, dim = 16, 2, 128
     table = np.array([[0, 1], [-1, 5], [2, 3]])
