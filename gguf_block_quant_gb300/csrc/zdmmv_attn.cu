@@ -11,12 +11,11 @@ namespace {
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Column tiles and splits. Four columns or fewer take the narrow form; else a warp takes 8, or 16 where a kv head of a
-// sequence has more, and from 17 on the warps share the columns among them. The splits: with one sequence as many as
-// fill the device once; with more, whose lengths may differ, up to four times that while a split has kRaggedChunk tiles.
-constexpr int kMinChunk = 16;      // tiles: a ring slot for each of 8 warps
-constexpr int kRaggedChunk = 128;
-constexpr int kMaxSplitItems = ZDMMV_ATTN_COUNTER_BYTES / 4;  // counters of the join; more items fill the device anyway
+// Up to four columns a kv head of a sequence take the narrow form, up to 16 the wide one, more a shared ring. The grid is
+// (items) x (splits of their tokens), as many as run at once -- but for several sequences' decoding with more steps than
+// CTAs, whose lengths decide (AttnWalk; 64 sequences of up to 16384 tokens: 109 us with the grid, WALK_US so).
+constexpr int kCounters = ZDMMV_ATTN_COUNTER_BYTES / 4;
+
 bool attn_plan(const KvView &c, int head_dim, int n_q_heads, int max_q_len, int64_t max_tokens, AttnPlan *out) {
     static const int sms = [] {
         int dev = 0, n = 0;
@@ -32,25 +31,28 @@ bool attn_plan(const KvView &c, int head_dim, int n_q_heads, int max_q_len, int6
     p.cols = columns <= kNarrowCols ? kNarrowCols : 8 * p.nt * p.wc;
     const int64_t n_ct = ceil_div(columns, p.cols);
     p.items = static_cast<int64_t>(c.n_seq) * c.n_kv_heads * n_ct;
-    if (p.items > 0x7fffffff || columns > 0x7fffff00) return false;
-    p.n_ct = static_cast<int>(n_ct);
     const int64_t tiles = std::max<int64_t>(1, ceil_div(max_tokens, kKvSlab));
-    // CTAs that run at once
+    const int64_t steps = p.items * ceil_div(tiles, kStepTiles);
+    if (steps > 0x7fffffff || columns > 0x7fffff00) return false;
+    p.n_ct = static_cast<int>(n_ct);
     const int64_t slots = static_cast<int64_t>(sms) * (p.wc > 1 ? 1 : attn_ctas_per_sm(kv_blocks(head_dim), p.nt));
-    const int64_t once = std::max<int64_t>(1, slots / p.items);
-    int64_t splits = once;
-    if (c.n_seq > 1) splits = std::max(once, std::min(ceil_div(4 * slots, p.items), ceil_div(tiles, kRaggedChunk)));
-    if (p.items > kMaxSplitItems) splits = 1;
-    p.max_split = static_cast<int>(std::min(splits, ceil_div(tiles, kMinChunk)));
-    p.chunk = static_cast<int>(ceil_div(ceil_div(tiles, p.max_split), 2) * 2);  // whole ring slots
-    p.n_split = static_cast<int>(ceil_div(tiles, p.chunk));
+    if (p.wc == 1 && c.n_seq > 1 && steps > slots) {
+        p.ctas = static_cast<int>(std::min<int64_t>(slots, kCounters));
+        p.parts = steps > p.items ? 2 * p.ctas : 0;  // an item of one step is never shared
+    } else {
+        const int64_t splits = p.items > kCounters ? 1 : std::max<int64_t>(1, slots / p.items);
+        const int64_t most = std::min(splits, ceil_div(tiles, kMinChunk));
+        p.chunk = static_cast<int>(std::max<int64_t>(kMinChunk, ceil_div(ceil_div(tiles, most), 2) * 2));  // whole ring slots
+        p.n_split = static_cast<int>(most);
+        p.parts = most > 1 ? p.items * most : 0;
+    }
     *out = p;
     return true;
 }
 
 size_t attn_workspace(const AttnPlan &p, int head_dim) {
-    if (p.max_split <= 1) return 0;
-    return ZDMMV_ATTN_COUNTER_BYTES + static_cast<size_t>(p.items) * p.max_split * p.cols * (head_dim + 2) * 4;
+    if (p.parts == 0) return 0;
+    return ZDMMV_ATTN_COUNTER_BYTES + static_cast<size_t>(p.parts) * p.cols * (head_dim + 2) * 4;
 }
 
 }  // namespace
@@ -105,10 +107,11 @@ zdmmv_status zdmmv_attn_q4_0(const zdmmv_kv_cache *cache, const zdmmv_attn_args 
     a.by_heads = FastDiv::of(cache->n_kv_heads);
     a.by_group = FastDiv::of(a.group);
     a.by_page_tiles = FastDiv::of(cache->page_tokens / kKvSlab);
+    a.by_split = FastDiv::of(std::max(1, p.n_split));
     a.n_ct = p.n_ct; a.n_split = p.n_split; a.chunk = p.chunk; a.wc = p.wc;
     a.count = static_cast<uint32_t *>(g.workspace);
     a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(g.workspace) + ZDMMV_ATTN_COUNTER_BYTES);
-    a.part_ml = reinterpret_cast<float2 *>(a.part + p.items * p.n_split * p.cols * cache->head_dim);
+    a.part_ml = reinterpret_cast<float2 *>(a.part + p.parts * p.cols * cache->head_dim);
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e = cudaErrorInvalidValue;
     switch (kv_blocks(cache->head_dim)) {

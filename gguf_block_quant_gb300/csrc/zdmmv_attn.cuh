@@ -29,11 +29,13 @@
 //    below 2^-38 of the largest p, and below 2^-26 of the largest x while d_v is a
 //    normal fp16 number.
 //
-// Work: grid (kv head of a sequence and column tile) x (split of its tokens); a
-// producer warp copies tiles (one bulk copy each) into a ring, the consumer warps
-// split a stage's tiles among them (WC = 1) or the columns (WC = 4). Each warp has
-// its own running maximum and sums; they are joined once, at the end, through
-// shared memory, and the splits by the CTA of an item that finishes last.
+// Work. Up to 16 columns a kv head of a sequence (decoding): the ITEMS (sequence, kv head) one after another are a row of
+// STEPS of 16 tiles (a pair for each of a CTA's 8 warps), and every CTA of a grid that fills the device once takes an
+// equal stretch of them, whatever the lengths: parts of an item at the stretch's ends, whole items between. Each warp has
+// its own ring of two slots (a pair of tiles each, one bulk copy a tile), its own running maximum and its own sums; they
+// are joined at the item's end through shared memory, and an item's parts by the CTA that finishes last (through the
+// workspace). More columns (prompts): the grid is (column tile of an item) x (split of its tokens), the warps split the
+// columns and share a ring.
 #pragma once
 
 #include "zdmmv_kv.cuh"
@@ -42,32 +44,32 @@ namespace zdmmv {
 
 struct AttnArgs {
     KvView c;
-    FastDiv by_ct, by_heads, by_group, by_page_tiles;
+    FastDiv by_ct, by_heads, by_group, by_page_tiles, by_split;
     const float *q;
     const int32_t *q_start, *kv_len;
     float *out;
-    uint32_t *count;    // [item]: splits that have stored their partial sums (0 between calls)
-    float *part;        // partial sums [item][split][column][dim], then float2 (max, sum) [item][split][column]
+    uint32_t *count;    // parts of an item that have stored their sums (0 between calls)
+    float *part;        // parts' sums [part][column][dim], then float2 (max, sum) [part][column]
     float2 *part_ml;
     int32_t *status;
     uint32_t *fault;
     int64_t q_stride;
     int32_t n_tok, n_q_heads, group, max_q_len, max_kv_len, window;
     int32_t n_ct;       // column tiles of a kv head of a sequence
-    int32_t n_split, chunk;  // most splits, tiles of a split
+    int32_t n_split, chunk;  // the grid's form: most splits, tiles of a split of the longest sequence; else 0
     int32_t wc;         // warps that split the columns (the others split the tokens)
     float scale_log2;
 };
 
-// The wide kernel's two forms. Own rings (wc = 1): each of 8 warps copies its own tiles into two slots of its own and
-// waits for nobody. Shared ring (wc > 1): 8 warps split the columns (and the slots among groups of them), a ninth copies.
-constexpr int kAttnWarps = 8;
-template <int NB, bool SHARED> struct AttnForm {
-    static constexpr int kThreads = kAttnWarps * 32 + (SHARED ? 32 : 0);
-    static constexpr int kSlots = SHARED && NB >= 8 ? 8 : 16;  // ring slots, a pair of tiles in each
-};
+constexpr int kAttnWarps = 8, kAttnThreads = kAttnWarps * 32;
+constexpr int kWalker = kAttnThreads - 1;    // the thread that finds the CTA's next segment
+constexpr int kStepTiles = 2 * kAttnWarps;  // tiles of a step: a ring slot for each warp
+// Ring slots (a pair of tiles) of a CTA: two a warp; the shared ring's, as many where they fit.
+template <int NB, bool SHARED> __host__ __device__ constexpr int attn_slots() { return SHARED && NB >= 8 ? 8 : 16; }
 // CTAs of the forms without a shared ring that run on an SM at once.
 __host__ __device__ constexpr int attn_ctas_per_sm(int nb, int nt) { return nb * nt <= 4 ? 2 : 1; }
+// Whether the warps' sums have shared memory of their own, so that the next item's tiles can come while they are joined.
+__host__ __device__ constexpr bool attn_sums_apart(int nb, int nt, bool shared) { return !shared && nb * nt < 16; }
 constexpr int kAttnBarBytes = 256;  // two barriers a slot
 constexpr int kAttnUnit = 13;
 constexpr int kJoinAhead = 16;
@@ -78,7 +80,6 @@ struct AttnRange {
     int len;
     bool bad;
     int slab0, slabs;  // tiles that any column of the column tile sees
-    __device__ int splits(int chunk) const { return slabs <= chunk ? 1 : (slabs + chunk - 1) / chunk; }
 };
 __device__ __forceinline__ AttnRange attn_range(const AttnArgs &a, int seq, int ct, int cols) {
     AttnRange r;
@@ -95,6 +96,204 @@ __device__ __forceinline__ AttnRange attn_range(const AttnArgs &a, int seq, int 
     r.slabs = r.bad ? 0 : max(0, (end + kKvSlab - 1) / kKvSlab - r.slab0);
     return r;
 }
+
+// One CTA's share of an item: tiles first .. last-1, and where its sums go where others share the item.
+struct AttnSeg {
+    AttnRange r;
+    int seq, kvh, ct;
+    int first, last;
+    int parts;           // CTAs that share the item
+    int counter;         // ... their counter
+    int mine, part0, part_step;  // this CTA's part; part s of the item is part0 (s = 0) or rest + s * part_step
+    int rest;
+    bool some;           // false: there is no such segment
+    __device__ int part(int s) const { return s == 0 ? part0 : rest + s * part_step; }
+};
+
+// The grid's form, (item) x (split): the CTA's part of its item, tiles in equal stretches of kMinChunk or more; false where
+// there is none.
+constexpr int kMinChunk = kStepTiles;
+__device__ __forceinline__ bool attn_grid_seg(const AttnArgs &a, int cols, AttnSeg &g) {
+    const int item = blockIdx.x, split = blockIdx.y;
+    const int sh = a.by_ct.div(item);
+    g.ct = a.by_ct.mod(item, sh);
+    g.seq = a.by_heads.div(sh);
+    g.kvh = a.by_heads.mod(sh, g.seq);
+    g.r = attn_range(a, g.seq, g.ct, cols);
+    if (g.ct * cols >= g.r.n * a.group) return false;
+    // the host's chunk is for the longest sequence that the call allows
+    const int chunk = max(kMinChunk, (a.by_split.div(g.r.slabs + a.n_split - 1) + 1) & ~1);
+    g.parts = max(1, (g.r.slabs + chunk - 1) / chunk);
+    if (split >= g.parts) return false;
+    g.first = g.r.slab0 + split * chunk;
+    g.last = min(g.r.slab0 + g.r.slabs, g.first + chunk);
+    g.counter = item;
+    g.part0 = g.rest = item * a.n_split;
+    g.part_step = 1;
+    g.mine = g.part0 + split;
+    return true;
+}
+
+// Decoding of several sequences: the CTA's stretch of the row of steps. It lies in shared memory, as the segments do (the main loop has no
+// registers to spare): begin() is for all threads, next() for one, between two barriers.
+struct AttnWalk {
+    int ctas, each, more;  // CTAs that have steps; `each` and in all `more` besides, evenly spread
+    float per_step;        // ctas / steps
+    int snap;              // a stretch's end this near an item's moves there: a part of so few steps costs more than it evens
+    int at, end;           // the CTA's steps
+    int seq, kvh, base, steps;  // the item that holds step `at`: its first step, its steps
+    AttnRange r;
+
+    __device__ static int steps_of(const AttnRange &r) { return r.n == 0 ? 0 : max(1, (r.slabs + kStepTiles - 1) / kStepTiles); }
+    __device__ int cut(int c) const { return c * each + c * more / ctas; }  // where CTA c's stretch begins, before snapping
+    // ... after it; a cut inside the item of steps first .. first + n - 1 may move
+    __device__ int snapped(int cut, int first, int n) const {
+        if (cut <= first || cut >= first + n) return cut;
+        return cut - first <= snap ? first : (first + n - cut <= snap ? first + n : cut);
+    }
+    __device__ int holder(int step) const {  // the CTA whose stretch holds a step, before snapping
+        int c = min(ctas - 1, static_cast<int>(static_cast<float>(step) * per_step));
+        while (cut(c) > step) --c;
+        while (cut(c + 1) <= step) ++c;
+        return c;
+    }
+
+    // False where the CTA has nothing to do. scan: shared memory for kAttnWarps + 3 ints.
+    __device__ bool begin(const AttnArgs &a, int cols, int *scan) {
+        const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, me = blockIdx.x;
+        const int heads = a.c.n_kv_heads, n_seq = a.c.n_seq;
+        int total = 0;
+        seq = base = 0;
+        if (n_seq == 1) {
+            r = attn_range(a, 0, 0, cols);
+            steps = steps_of(r);
+            total = steps * heads;
+        } else {
+            int mine = 0;
+            for (int s = tid; s < n_seq; s += kAttnThreads) mine += steps_of(attn_range(a, s, 0, cols)) * heads;
+            mine = __reduce_add_sync(0xffffffffu, mine);
+            if (lane == 0) scan[warp] = mine;
+            __syncthreads();
+#pragma unroll
+            for (int w = 0; w < kAttnWarps; ++w) total += scan[w];
+        }
+        ctas = min(static_cast<int>(gridDim.x), total);
+        if (me >= ctas) return false;
+        each = total / ctas;
+        more = total - each * ctas;
+        per_step = static_cast<float>(ctas) / static_cast<float>(total);
+        snap = min(3, each / 3);
+        at = cut(me);
+        end = cut(me + 1);
+        if (n_seq == 1) {
+            const int k0 = at / steps, k1 = (end - 1) / steps;
+            at = snapped(at, k0 * steps, steps);
+            end = snapped(end, k1 * steps, steps);
+        } else {
+            // the sequences whose steps hold both ends; each is snapped by the thread that finds it
+            for (int s0 = 0, before = 0;; s0 += kAttnThreads) {
+                const int s = s0 + tid;
+                const int n = s < n_seq ? steps_of(attn_range(a, s, 0, cols)) : 0, w = n * heads;
+                int upto = w;
+#pragma unroll
+                for (int k = 1; k < 32; k <<= 1) {
+                    const int o = __shfl_up_sync(0xffffffffu, upto, k);
+                    if (lane >= k) upto += o;
+                }
+                __syncthreads();
+                if (lane == 31) scan[warp] = upto;
+                __syncthreads();
+                int all = before;
+#pragma unroll
+                for (int k = 0; k < kAttnWarps; ++k) {
+                    if (k < warp) upto += scan[k];
+                    all += scan[k];
+                }
+                upto += before;
+                const int from = upto - w;
+                if (at >= from && at < upto) scan[kAttnWarps] = snapped(at, from + (at - from) / n * n, n);
+                if (end > from && end <= upto) scan[kAttnWarps + 1] = snapped(end, from + (end - 1 - from) / n * n, n);
+                if (end <= all) break;
+                before = all;
+            }
+            __syncthreads();
+            at = scan[kAttnWarps];
+            end = scan[kAttnWarps + 1];
+            if (at >= end) return false;
+            // the item that `at` begins or lies in
+            for (int s0 = 0, before = 0;; s0 += kAttnThreads) {
+                const int s = s0 + tid;
+                const int w = s < n_seq ? steps_of(attn_range(a, s, 0, cols)) * heads : 0;
+                int upto = w;
+#pragma unroll
+                for (int k = 1; k < 32; k <<= 1) {
+                    const int o = __shfl_up_sync(0xffffffffu, upto, k);
+                    if (lane >= k) upto += o;
+                }
+                __syncthreads();
+                if (lane == 31) scan[warp] = upto;
+                __syncthreads();
+                int all = before;
+#pragma unroll
+                for (int k = 0; k < kAttnWarps; ++k) {
+                    if (k < warp) upto += scan[k];
+                    all += scan[k];
+                }
+                upto += before;
+                if (at >= upto - w && at < upto) {
+                    scan[kAttnWarps] = s;
+                    scan[kAttnWarps + 1] = upto - w;
+                }
+                if (at < all) break;
+                before = all;
+            }
+            __syncthreads();
+            seq = scan[kAttnWarps];
+            base = scan[kAttnWarps + 1];
+            r = attn_range(a, seq, 0, cols);
+            steps = steps_of(r);
+        }
+        kvh = (at - base) / steps;
+        base += kvh * steps;
+        return at < end;
+    }
+    __device__ void next(const AttnArgs &a, int cols, AttnSeg &g) {
+        g.some = at < end;
+        if (!g.some) return;
+        if (at == base + steps) {
+            base = at;
+            if (++kvh == a.c.n_kv_heads) {
+                kvh = 0;
+                do {
+                    r = attn_range(a, ++seq, 0, cols);
+                    steps = steps_of(r);
+                } while (steps == 0);  // `end` is within the steps of all, so a sequence with some follows
+            }
+        }
+        const int k0 = at - base, k1 = min(steps, k0 + end - at);
+        g.r = r;
+        g.seq = seq;
+        g.kvh = kvh;
+        g.ct = 0;
+        g.first = r.slab0 + k0 * kStepTiles;
+        g.last = min(r.slab0 + r.slabs, r.slab0 + k1 * kStepTiles);
+        g.parts = 1;
+        if (k0 > 0 || k1 < steps) {
+            // the first and the last CTA that have a step of the item
+            int c0 = holder(base), c1 = holder(base + steps - 1);
+            while (snapped(cut(c0 + 1), base, steps) <= base) ++c0;
+            while (snapped(cut(c1), base, steps) >= base + steps) --c1;
+            // a CTA has at most two parts: of the item it starts with, and of the one that it leaves to the next CTA
+            g.parts = c1 - c0 + 1;
+            g.counter = c0;
+            g.part0 = 2 * c0 + 1;
+            g.rest = 2 * c0;
+            g.part_step = 2;
+            g.mine = g.part(static_cast<int>(blockIdx.x) - c0);
+        }
+        at += k1 - k0;
+    }
+};
 
 __device__ __forceinline__ void mma_acc(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
@@ -235,10 +434,6 @@ __device__ __forceinline__ void load_q(const AttnArgs &a, const AttnRange &r, in
     }
 }
 
-template <int WARPS> __device__ __forceinline__ void attn_consumer_barrier() {
-    asm volatile("bar.sync 1, %0;" ::"n"(WARPS * 32) : "memory");
-}
-
 // 2^e that brings a column's largest magnitude into [2^13, 2^14), with the scale's sign (up), and 2^-e (down).
 __device__ __forceinline__ void q_unit(float top, float scale, float &up, float &down) {
     int e = 13 - (static_cast<int>(__float_as_uint(top) >> 23) - 127);
@@ -270,6 +465,12 @@ template <int NB> struct TileFeed {
         src = head + page * a.c.page_bytes +
               static_cast<int64_t>(a.by_page_tiles.mod(tile, a.by_page_tiles.div(tile))) * KvGeom<NB>::kTileBytes;
     }
+    __device__ void start(const AttnArgs &a, const AttnSeg &s, int tile, int *sh_bad, int early_tile = -1, int early_page = 0) {
+        const int32_t *table = a.c.table + static_cast<int64_t>(s.seq) * a.c.max_pages;
+        const int page = tile >= s.last ? 0 : (tile == early_tile ? early_page : page_at(a, table, tile));
+        look(a, a.c.pages + static_cast<int64_t>(s.kvh) * static_cast<int>(a.by_page_tiles.d) * KvGeom<NB>::kTileBytes, page, tile,
+             s.last, sh_bad);
+    }
     // unit j of the stretch into `slot`
     __device__ void copy(int j, int lane, uint8_t *slot, uint64_t *full, uint64_t policy) const {
         constexpr uint32_t kBytes = KvGeom<NB>::kTileBytes;
@@ -281,25 +482,23 @@ template <int NB> struct TileFeed {
 };
 
 // The CTA's end: the warps' sums (already in the unit of their common maximum) added up, and stored as the result or,
-// where the sequence's tokens are split, as a partial one; the split that comes last joins them all, in the splits'
+// where CTAs share the item, as a part; the CTA that comes last joins the parts, in their
 // order: out = sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s. `sum`: [warp][WCOLS][D]; m, l: [warp][WCOLS], l in the
 // common unit too.
-template <int D, int WCOLS, int WARPS>
-__device__ __forceinline__ void attn_store(const AttnArgs &a, const AttnRange &r, int item, int split, int n_splits,
-                                           int cols, int wc, float *sum, const float *m, const float *l, bool bad,
-                                           int *sh_last) {
-    constexpr int kThreads = WARPS * 32, kQuads = D / 4;
+template <int D, int WCOLS>
+__device__ __forceinline__ void attn_store(const AttnArgs &a, const AttnSeg &seg, int cols, int wc, float *sum, const float *m,
+                                           const float *l, bool bad, int *sh_last) {
+    constexpr int kThreads = kAttnThreads, kQuads = D / 4;
     const int tid = threadIdx.x;
-    const int sh = a.by_ct.div(item), ct = a.by_ct.mod(item, sh);
-    const int kvh = a.by_heads.mod(sh, a.by_heads.div(sh));
-    const int n_wt = WARPS / wc;
+    const AttnRange &r = seg.r;
+    const int ct = seg.ct, kvh = seg.kvh, n_splits = seg.parts;
+    const int n_wt = kAttnWarps / wc;
     const int live = min(cols, r.n * a.group - ct * cols);  // columns that are query rows
     if (r.bad && tid == 0 && a.status) *a.status = 1;
     const auto row = [&](int col) {
         const int i = a.by_group.div(col);
         return a.out + (static_cast<int64_t>(r.q0 + i) * a.n_q_heads + kvh * a.group + (col - i * a.group)) * D;
     };
-    const int64_t part0 = static_cast<int64_t>(item) * a.n_split * cols;
     for (int k = tid; k < live * kQuads; k += kThreads) {
         const int c = k / kQuads, e = 4 * (k % kQuads);
         const int w0 = c / WCOLS, wcol = c % WCOLS;
@@ -316,7 +515,7 @@ __device__ __forceinline__ void attn_store(const AttnArgs &a, const AttnRange &r
             const float inv = ls == 0.0f ? 0.0f : 1.0f / ls;
             *reinterpret_cast<float4 *>(row(ct * cols + c) + e) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
         } else {
-            const int64_t at = part0 + static_cast<int64_t>(split) * cols + c;
+            const int64_t at = static_cast<int64_t>(seg.mine) * cols + c;
             __stcg(reinterpret_cast<float4 *>(a.part + at * D + e), acc);
             if (e == 0) {
                 float top = -INFINITY;
@@ -326,16 +525,16 @@ __device__ __forceinline__ void attn_store(const AttnArgs &a, const AttnRange &r
         }
     }
     if (n_splits == 1) return;
-    attn_consumer_barrier<WARPS>();
+    __syncthreads();
     if (tid == 0) {
         // releases the CTA's partial sums (which the barrier orders before it), acquires the others'
         uint32_t before;
-        asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(before) : "l"(a.count + item) : "memory");
+        asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(before) : "l"(a.count + seg.counter) : "memory");
         const bool is_last = before == static_cast<uint32_t>(n_splits) - 1u;
-        if (is_last) a.count[item] = 0;
+        if (is_last) a.count[seg.counter] = 0;
         *sh_last = is_last;
     }
-    attn_consumer_barrier<WARPS>();
+    __syncthreads();
     if (!*sh_last) return;
     // a thread for four dimensions of a column, kJoinAhead splits' loads in flight; where that leaves threads over, groups of
     // them share the splits
@@ -355,7 +554,7 @@ __device__ __forceinline__ void attn_store(const AttnArgs &a, const AttnRange &r
 #pragma unroll
                 for (int i = 0; i < kJoinAhead; ++i) {
                     const int s = s0 + i * groups;
-                    const int64_t p = part0 + static_cast<int64_t>(s) * cols + c;
+                    const int64_t p = static_cast<int64_t>(seg.part(s)) * cols + c;
                     ml[i] = s < n_splits ? __ldcg(&a.part_ml[p]) : make_float2(-INFINITY, 0.0f);
                     x[i] = s < n_splits ? __ldcg(reinterpret_cast<const float4 *>(a.part + p * D + e)) : make_float4(0.f, 0.f, 0.f, 0.f);
                 }
@@ -378,7 +577,7 @@ __device__ __forceinline__ void attn_store(const AttnArgs &a, const AttnRange &r
                 grp_sum[tid] = acc;
                 grp_ml[tid] = make_float2(top, ls);
             }
-            attn_consumer_barrier<WARPS>();
+            __syncthreads();
             if (grp != 0) return;
             float to = top;
             for (int q = 1; q < groups; ++q) to = fmaxf(to, grp_ml[q * quads + k].x);
@@ -414,59 +613,90 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
     return y;
 }
 constexpr int kNarrowCols = 4;
-template <int NB> __global__ void __launch_bounds__(kAttnWarps * 32, attn_ctas_per_sm(NB, 1)) attn_narrow_kernel(AttnArgs a) {
+template <int NB> __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(NB, 1)) attn_narrow_kernel(AttnArgs a) {
     using G = KvGeom<NB>;
     constexpr int D = G::kDim, kWarps = kAttnWarps;
     constexpr int kSlotBytes = 2 * G::kTileBytes;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float sh_m[kWarps][kNarrowCols], sh_l[kWarps][kNarrowCols];
-    __shared__ int sh_bad, sh_last;
+    __shared__ int sh_bad[2], sh_last, sh_scan[kWarps + 3];
     __shared__ uint32_t sh_magic;
+    __shared__ AttnSeg sh_seg[2];
+    __shared__ AttnWalk sh_walk;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     uint64_t *full = reinterpret_cast<uint64_t *>(smem) + 2 * warp;  // the warp's two slots
     uint8_t *ring = smem + kAttnBarBytes + 2 * warp * kSlotBytes;
+    uint2 *q_sm = reinterpret_cast<uint2 *>(smem + kAttnBarBytes + 2 * kWarps * kSlotBytes) + lane;
+    float *sum = reinterpret_cast<float *>(smem + kAttnBarBytes + 2 * kWarps * kSlotBytes + 2 * NB * 256);  // [warp][column][D]
     if (lane == 0) {
         mbar_init(&full[0], 1);
         mbar_init(&full[1], 1);
         fence_barrier_init();
     }
     if (tid == 0) {
-        sh_bad = 0;
+        sh_bad[0] = sh_bad[1] = 0;
         sh_magic = kCodeMagic;
     }
     __syncthreads();
     block_op_wait();
     block_op_release();
 
-    const int item = blockIdx.x, split = blockIdx.y;
-    const int sh = a.by_ct.div(item), ct = a.by_ct.mod(item, sh);
-    const int seq = a.by_heads.div(sh), kvh = a.by_heads.mod(sh, seq);
-    const int32_t *table = a.c.table + static_cast<int64_t>(seq) * a.c.max_pages;
-    // without a window the split's first tile does not hang on the lengths: the pages are looked up beside them
-    const int tile_off = split * a.chunk + 2 * (warp + (lane >> 1) * kWarps) + (lane & 1);
-    int page = a.window == 0 ? TileFeed<NB>::page_at(a, table, tile_off) : 0;
-    const AttnRange r = attn_range(a, seq, ct, kNarrowCols);
-    if (ct * kNarrowCols >= r.n * a.group) return;
-    const int n_splits = r.splits(a.chunk);
-    if (split >= n_splits) return;
-    const int first = r.slab0 + split * a.chunk;  // tiles first .. last-1
-    const int last = min(r.slab0 + r.slabs, first + a.chunk);
-    const int n_units = (last - first + 1) / 2;   // pairs of tiles
-
-    const uint8_t *head = a.c.pages + static_cast<int64_t>(kvh) * (a.c.page_tokens / kKvSlab) * G::kTileBytes;
+    // without a window a sequence of the full length has its split's pages here: looked up beside the lengths
+    const int tile_off = 2 * (warp + (lane >> 1) * kWarps) + (lane & 1);
+    int early_tile = -1, early_page = 0;
+    if (a.n_split > 0) {
+        AttnSeg seg;
+        if (a.window == 0) {
+            early_tile = blockIdx.y * a.chunk + tile_off;
+            const int seq = a.by_heads.div(a.by_ct.div(blockIdx.x));
+            early_page = TileFeed<NB>::page_at(a, a.c.table + static_cast<int64_t>(seq) * a.c.max_pages, early_tile);
+        }
+        if (!attn_grid_seg(a, kNarrowCols, seg)) return;
+        if (tid == kWalker) {
+            sh_seg[0] = seg;
+            sh_seg[1].some = false;
+        }
+    } else {
+        AttnWalk walk;
+        if (!walk.begin(a, kNarrowCols, sh_scan)) return;
+        if (tid == kWalker) {
+            walk.next(a, kNarrowCols, sh_seg[0]);
+            sh_walk = walk;
+        }
+    }
+    __syncthreads();
+    const uint64_t policy = l2_evict_first_policy();
+    TileFeed<NB> feed;
+    int slot = 0;
+    uint32_t phases = 0, pending = 0;  // by slot: the parity to wait for, copies not yet waited for
+    bool dead = false;
+    // the warp's first two units of a segment, on their way
+    const auto begin = [&](const AttnSeg &s, int *bad) {
+        feed.start(a, s, s.first + tile_off, bad, early_tile, early_page);
+        early_tile = -1;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            if (s.first + 2 * (warp + j * kWarps) < s.last) {
+                const int to = slot ^ j;
+                fence_proxy_async_smem();
+                feed.copy(j, lane, ring + to * kSlotBytes, &full[to], policy);
+                pending |= 1u << to;
+            }
+    };
     const int g = lane >> 2, t = lane & 3;
     // q: column g / 2, this lane's dimensions 8t .. 8t+7 of every block; asked for before the tiles' copies, which it
     // would otherwise wait behind
     float v[NB][8];
-    load_q<NB>(a, r, kvh, ct * kNarrowCols + g / 2, t, v);
-    const uint64_t policy = l2_evict_first_policy();
-    TileFeed<NB> feed;
-    if (a.window != 0 && r.slab0 + tile_off < last) page = feed.page_at(a, table, r.slab0 + tile_off);
-    feed.look(a, head, page, r.slab0 + tile_off, last, &sh_bad);
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-        if (warp + j * kWarps < n_units) feed.copy(j, lane, ring + j * kSlotBytes, &full[j], policy);
+    load_q<NB>(a, sh_seg[0].r, sh_seg[0].kvh, g / 2, t, v);
+    begin(sh_seg[0], &sh_bad[0]);
+    const uint32_t magic = lds32(smem_addr(&sh_magic));
+    const uint32_t pick = (g & 1) ? 0x7632u : 0x5410u;  // the token's half of two words of scales
 
+    for (int n_seg = 0;; ++n_seg) {
+    const AttnSeg &seg = sh_seg[n_seg & 1], &ahead = sh_seg[~n_seg & 1];
+    const AttnRange &r = seg.r;
+    const int first = seg.first, last = seg.last;
+    const int n_units = (last - first + 1) / 2;   // pairs of tiles
     // its B fragments, the upper (g even) or lower part: each warp makes an eighth of them for all
     uint32_t qf[NB][4];
     float qs;
@@ -481,7 +711,6 @@ template <int NB> __global__ void __launch_bounds__(kAttnWarps * 32, attn_ctas_p
         float up, down;
         q_unit(top, a.scale_log2, up, down);
         qs = __shfl_sync(0xffffffffu, fmaxf(fabsf(a.scale_log2) * down, 1e-37f), 8 * t);  // column t's
-        uint2 *q_sm = reinterpret_cast<uint2 *>(smem + kAttnBarBytes + 2 * kWarps * kSlotBytes) + lane;
 #pragma unroll
         for (int k = 0; k < 2 * NB; ++k) {
             if (k % kWarps != warp) continue;
@@ -499,30 +728,29 @@ template <int NB> __global__ void __launch_bounds__(kAttnWarps * 32, attn_ctas_p
             qf[k / 2][2 * (k % 2) + 1] = f.y;
         }
     }
+    if (tid == kWalker && a.n_split == 0) sh_walk.next(a, kNarrowCols, sh_seg[~n_seg & 1]);
+    __syncwarp();
     // what column t sees, of this split's tiles
     const int limit = min(r.len, last * kKvSlab);
-    const int ti = a.by_group.div(ct * kNarrowCols + t);
+    const int ti = a.by_group.div(t);
     const int end = ti < r.n ? min(limit, max(0, r.len - (r.n - 1 - ti))) : limit;
     const int low = ti < r.n && a.window > 0 ? max(0, r.len - (r.n - 1 - ti) - a.window) : 0;
     const int end_min = __reduce_min_sync(0xffffffffu, end), low_max = __reduce_max_sync(0xffffffffu, low);
 
-    const uint32_t magic = lds32(smem_addr(&sh_magic));
-    const uint32_t pick = (g & 1) ? 0x7632u : 0x5410u;  // the token's half of two words of scales
     float m = -INFINITY, l = 0.0f;
     uint64_t o[2 * NB];  // column t, dimensions 4g and 4g + 1, or 4g + 2 and 4g + 3, of the block
 #pragma unroll
     for (int k = 0; k < 2 * NB; ++k) o[k] = 0;
     int sx = kAttnUnit;  // p is in units of 2^sx
-    bool dead = false;
 
-    int slot = 0;
-    uint32_t phase = 0;
-    for (int u = warp, j_next = 2; u < n_units; u += kWarps) {
-        if (!__all_sync(0xffffffffu, mbar_wait(&full[slot], phase))) {
+    for (int u = warp, j_next = 2; u < n_units && !dead; u += kWarps) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&full[slot], phases >> slot & 1u))) {
             if (lane == 0) atomicOr(a.fault, 1u);
             dead = true;
             break;
         }
+        phases ^= 1u << slot;
+        pending &= ~(1u << slot);
         const uint32_t tile = smem_addr(ring) + slot * kSlotBytes;
         const int t0 = (first + 2 * u) * kKvSlab;
         // ------------------------------------------------ scores of column t: tokens 8h + g
@@ -646,34 +874,28 @@ template <int NB> __global__ void __launch_bounds__(kAttnWarps * 32, attn_ctas_p
         if (u + 2 * kWarps < n_units) {  // the warp's unit after next takes the slot's place
             if (j_next == 16) {
                 j_next = 0;
-                const int next = first + 2 * (u + 2 * kWarps + (lane >> 1) * kWarps) + (lane & 1);
-                feed.look(a, head, next < last ? feed.page_at(a, table, next) : 0, next, last, &sh_bad);
+                feed.start(a, seg, first + 2 * (u - warp + 2 * kWarps) + tile_off, &sh_bad[n_seg & 1]);
             }
             fence_proxy_async_smem();
             feed.copy(j_next++, lane, ring + slot * kSlotBytes, &full[slot], policy);
+            pending |= 1u << slot;
         }
-        phase ^= static_cast<uint32_t>(slot);
         slot ^= 1;
     }
-    if (dead) {
-        // leave only when the warp's copies have landed: the one that failed and the one behind it
-        (void)mbar_wait(&full[slot], phase);
-        if (warp + kWarps < n_units) (void)mbar_wait(&full[slot ^ 1], phase ^ static_cast<uint32_t>(slot));
-    }
-
     // ------------------------------------------------ join the warps
     l += __shfl_xor_sync(0xffffffffu, l, 4);
     l += __shfl_xor_sync(0xffffffffu, l, 8);
     l += __shfl_xor_sync(0xffffffffu, l, 16);
     m -= static_cast<float>(sx);  // the maximum in p's unit
     if (g == 0) sh_m[warp][t] = m;
-    __syncthreads();  // every warp is done with its ring
+    __syncthreads();
+    // the next segment's first tiles come while this one's sums are joined
+    if (ahead.some && !dead) begin(ahead, &sh_bad[(n_seg + 1) & 1]);
     float top = -INFINITY;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sh_m[w][t]);
     const float f0 = top == -INFINITY ? 0.0f : exp2_approx(m - top), f1 = f0 * 0.0625f;
     if (g == 0) sh_l[warp][t] = dead ? __int_as_float(0x7fffffff) : l * f0;
-    float *sum = reinterpret_cast<float *>(smem + kAttnBarBytes);  // [warp][column][D]
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
         const float2 x = f2_parts(o[2 * j]), y = f2_parts(o[2 * j + 1]);
@@ -682,21 +904,32 @@ template <int NB> __global__ void __launch_bounds__(kAttnWarps * 32, attn_ctas_p
             make_float4(x.x * f0, x.y * f1, y.x * f0, y.y * f1);
     }
     __syncthreads();
-    attn_store<D, kNarrowCols, kWarps>(a, r, item, split, n_splits, kNarrowCols, 1, sum, &sh_m[0][0], &sh_l[0][0],
-                                       r.bad || sh_bad, &sh_last);
+    attn_store<D, kNarrowCols>(a, seg, kNarrowCols, 1, sum, &sh_m[0][0], &sh_l[0][0], r.bad || sh_bad[n_seg & 1], &sh_last);
+    if (!ahead.some) break;
+    load_q<NB>(a, ahead.r, ahead.kvh, g / 2, t, v);
+    __syncthreads();  // the sums are read
+    if (tid == 0) sh_bad[n_seg & 1] = 0;
+    }
+    // leave only when the warp's copies have landed (after a wait that gave up: as far as they will)
+    for (int k = 0; k < 2; ++k)
+        if (pending >> k & 1u) (void)mbar_wait(&full[k], phases >> k & 1u);
 }
 
+// The wide form: each warp 8 * NT columns. SHARED: prompts; the warps split the columns (a.wc of them; the others the
+// ring's slots), warp 0 feeds the ring half a ring ahead of itself.
 template <int NB, int NT, bool SHARED>
-__global__ void __launch_bounds__(AttnForm<NB, SHARED>::kThreads, SHARED ? 1 : attn_ctas_per_sm(NB, NT)) attn_kernel(AttnArgs a) {
+__global__ void __launch_bounds__(kAttnThreads, SHARED ? 1 : attn_ctas_per_sm(NB, NT)) attn_kernel(AttnArgs a) {
     using G = KvGeom<NB>;
-    using F = AttnForm<NB, SHARED>;
-    constexpr int kWarps = kAttnWarps, kSlots = F::kSlots;
+    constexpr int kWarps = kAttnWarps, kSlots = attn_slots<NB, SHARED>();
     constexpr int D = G::kDim;
     constexpr int kSlotBytes = 2 * G::kTileBytes;
+    constexpr bool kApart = attn_sums_apart(NB, NT, SHARED);
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float sh_m[kWarps][NT * 8], sh_l[kWarps][NT * 8], sh_qs[kWarps][NT * 8];
-    __shared__ int sh_bad, sh_last;
+    __shared__ int sh_bad[2], sh_last, sh_scan[kWarps + 3];
     __shared__ uint32_t sh_magic;
+    __shared__ AttnSeg sh_seg[2];
+    __shared__ AttnWalk sh_walk;
     uint64_t *full = reinterpret_cast<uint64_t *>(smem);
     uint64_t *empty = full + kSlots;
     uint8_t *ring = smem + kAttnBarBytes;
@@ -708,7 +941,7 @@ __global__ void __launch_bounds__(AttnForm<NB, SHARED>::kThreads, SHARED ? 1 : a
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], a.wc);
         }
-        sh_bad = 0;
+        sh_bad[0] = sh_bad[1] = 0;
         sh_magic = kCodeMagic;
         fence_barrier_init();
     }
@@ -716,58 +949,73 @@ __global__ void __launch_bounds__(AttnForm<NB, SHARED>::kThreads, SHARED ? 1 : a
     block_op_wait();
     block_op_release();
 
-    const int item = blockIdx.x, split = blockIdx.y;
-    const int sh = a.by_ct.div(item), ct = a.by_ct.mod(item, sh);
-    const int seq = a.by_heads.div(sh), kvh = a.by_heads.mod(sh, seq);
-    const AttnRange r = attn_range(a, seq, ct, cols);
-    if (ct * cols >= r.n * a.group) return;
-    const int n_splits = r.splits(a.chunk);
-    if (split >= n_splits) return;
-    const int first = r.slab0 + split * a.chunk;  // tiles first .. last-1
-    const int last = min(r.slab0 + r.slabs, first + a.chunk);
-    const int n_units = (last - first + 1) / 2;   // pairs of tiles, a ring slot each
-
-    const uint8_t *head = a.c.pages + static_cast<int64_t>(kvh) * (a.c.page_tokens / kKvSlab) * G::kTileBytes;
-    const int32_t *table = a.c.table + static_cast<int64_t>(seq) * a.c.max_pages;
+    const int tile_off = SHARED ? lane : 2 * (warp + (lane >> 1) * kWarps) + (lane & 1);
+    int early_tile = -1, early_page = 0;
+    if (SHARED || a.n_split > 0) {
+        AttnSeg seg;
+        if (a.window == 0) {
+            early_tile = blockIdx.y * a.chunk + tile_off;
+            const int seq = a.by_heads.div(a.by_ct.div(blockIdx.x));
+            early_page = TileFeed<NB>::page_at(a, a.c.table + static_cast<int64_t>(seq) * a.c.max_pages, early_tile);
+        }
+        if (!attn_grid_seg(a, cols, seg)) return;
+        if (tid == kWalker) {
+            sh_seg[0] = seg;
+            sh_seg[1].some = false;
+        }
+    } else {
+        AttnWalk walk;
+        if (!walk.begin(a, cols, sh_scan)) return;
+        if (tid == kWalker) {
+            walk.next(a, cols, sh_seg[0]);
+            sh_walk = walk;
+        }
+    }
+    __syncthreads();
     const uint64_t policy = l2_evict_first_policy();
     TileFeed<NB> feed;
-
-    if (SHARED && warp == kWarps) {
-        // ------------------------------------------------------- producer
-        bool ok = true;
-        int u = 0;
-        for (int u0 = 0; u0 < n_units && ok; u0 += 16) {
-            const int tile = first + 2 * u0 + lane;
-            feed.look(a, head, tile < last ? feed.page_at(a, table, tile) : 0, tile, last, &sh_bad);
-            for (; u < min(n_units, u0 + 16); ++u) {
-                const int s = u % kSlots;
-                if (u >= kSlots) {
-                    if (!__all_sync(0xffffffffu, mbar_wait(&empty[s], static_cast<uint32_t>(u / kSlots - 1) & 1u))) {
-                        ok = false;
-                        break;
-                    }
+    int slot = SHARED ? warp / a.wc : warp;
+    uint32_t phases = 0, pending = 0;  // by slot: the parity to wait for, own copies not yet waited for
+    bool dead = false;
+    // the first units of a segment on their way: the warp's two, or all that the shared ring takes
+    const auto begin = [&](const AttnSeg &s, int *bad) {
+        if constexpr (SHARED) {
+            if (warp != 0) return;
+            feed.start(a, s, s.first + tile_off, bad, early_tile, early_page);
+            for (int k = 0; k < kSlots && s.first + 2 * k < s.last; ++k) feed.copy(k, lane, ring + k * kSlotBytes, &full[k], policy);
+        } else {
+            feed.start(a, s, s.first + tile_off, bad, early_tile, early_page);
+            early_tile = -1;
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                if (s.first + 2 * (warp + k * kWarps) < s.last) {
+                    const int to = slot ^ (k * kWarps);
                     fence_proxy_async_smem();
+                    feed.copy(k, lane, ring + to * kSlotBytes, &full[to], policy);
+                    pending |= 1u << to;
                 }
-                feed.copy(u - u0, lane, ring + s * kSlotBytes, &full[s], policy);
-            }
         }
-        if (!ok && lane == 0) atomicOr(a.fault, 1u);
-        // leave only when the copies into this CTA's shared memory have landed
-        for (int k = max(0, u - kSlots); k < u; ++k)
-            (void)mbar_wait(&full[k % kSlots], static_cast<uint32_t>(k / kSlots) & 1u);
-        return;
-    }
-
-    // ---------------------------------------------------------- consumers
+    };
     const int g = lane >> 2, t = lane & 3;
     const int wc = warp % a.wc, wt = warp / a.wc, n_wt = kWarps / a.wc;
-    const int col0 = ct * cols + wc * 8 * NT;  // the warp's first column
     uint4 *q_sm = reinterpret_cast<uint4 *>(ring + kSlots * kSlotBytes) + wc * (NT * 2 * NB * 32) + lane;
+    // the warps' sums [warp][column of the warp][D], behind q's fragments or over the ring
+    float *sum = reinterpret_cast<float *>(kApart ? ring + kSlots * kSlotBytes + NT * 2 * NB * 512 : ring);
+    const uint32_t magic = lds32(smem_addr(&sh_magic));
+    const uint32_t q_at = smem_addr(q_sm);
+    if (!SHARED) begin(sh_seg[0], &sh_bad[0]);
+
+    for (int n_seg = 0;; ++n_seg) {
+    const AttnSeg &seg = sh_seg[n_seg & 1], &ahead = sh_seg[~n_seg & 1];
+    const AttnRange &r = seg.r;
+    const int first = seg.first, last = seg.last;
+    const int n_units = (last - first + 1) / 2;   // pairs of tiles, a ring slot each
+    const int col0 = seg.ct * cols + wc * 8 * NT;  // the warp's first column
     // q's fragments: column g of each group of 8, this lane's 8 dimensions 8t.. of every block
 #pragma unroll 1
     for (int nt = wt; nt < NT; nt += n_wt) {
         float v[NB][8];
-        load_q<NB>(a, r, kvh, col0 + 8 * nt + g, t, v);
+        load_q<NB>(a, r, seg.kvh, col0 + 8 * nt + g, t, v);
         float top = 0.0f;
 #pragma unroll
         for (int b = 0; b < NB; ++b)
@@ -790,14 +1038,7 @@ __global__ void __launch_bounds__(AttnForm<NB, SHARED>::kThreads, SHARED ? 1 : a
             }
         }
     }
-    if constexpr (!SHARED) {
-        const int tile = first + 2 * (warp + (lane >> 1) * kWarps) + (lane & 1);
-        feed.look(a, head, tile < last ? feed.page_at(a, table, tile) : 0, tile, last, &sh_bad);
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-            if (warp + j * kWarps < n_units)
-                feed.copy(j, lane, ring + (warp + j * kWarps) * kSlotBytes, &full[warp + j * kWarps], policy);
-    }
+    if (SHARED) begin(seg, &sh_bad[0]);
     // what each column sees, of this split's tiles
     int end[NT], low[NT];
     const int limit = min(r.len, last * kKvSlab);
@@ -814,7 +1055,10 @@ __global__ void __launch_bounds__(AttnForm<NB, SHARED>::kThreads, SHARED ? 1 : a
     // units outside low_max .. end_min need masks (warp-uniform)
     end_min = __reduce_min_sync(0xffffffffu, end_min);
     low_max = __reduce_max_sync(0xffffffffu, low_max);
-    attn_consumer_barrier<kWarps>();
+    __syncthreads();
+
+    if (!SHARED && tid == kWalker && a.n_split == 0) sh_walk.next(a, cols, sh_seg[~n_seg & 1]);
+    __syncwarp();
 
     float m[NT], l[NT], qs[NT];
     uint64_t o[NT][2 * NB][2];  // columns 2t, 2t+1: dimension pairs' first and second
@@ -827,18 +1071,30 @@ __global__ void __launch_bounds__(AttnForm<NB, SHARED>::kThreads, SHARED ? 1 : a
         for (int k = 0; k < 2 * NB; ++k) o[nt][k][0] = o[nt][k][1] = 0;
     }
     int sx = kAttnUnit;  // p is in units of 2^sx
-    bool dead = false;
-    const uint32_t magic = lds32(smem_addr(&sh_magic));
-    const uint32_t q_at = smem_addr(q_sm);
 
-    int slot = wt;
-    uint32_t phase = 0;
-    for (int u = wt, j_next = 2; u < n_units; u += n_wt) {
-        if (!__all_sync(0xffffffffu, mbar_wait(&full[slot], phase))) {
+    int fed = kSlots;  // SHARED: units that warp 0 has asked for
+    for (int u = wt, j_next = 2; u < n_units && !dead; u += n_wt) {
+        if (SHARED && warp == 0) {
+            for (; fed < n_units && fed <= u + kSlots / 2; ++fed) {
+                const int s = fed % kSlots;
+                // unit fed - kSlots, before u: every warp that needs it has it, so this ends
+                if (!__all_sync(0xffffffffu, mbar_wait(&empty[s], static_cast<uint32_t>(fed / kSlots - 1) & 1u))) {
+                    if (lane == 0) atomicOr(a.fault, 1u);
+                    dead = true;
+                    break;
+                }
+                if (fed % 16 == 0) feed.start(a, seg, first + 2 * fed + tile_off, &sh_bad[0]);
+                fence_proxy_async_smem();
+                feed.copy(fed % 16, lane, ring + s * kSlotBytes, &full[s], policy);
+            }
+        }
+        if (!__all_sync(0xffffffffu, mbar_wait(&full[slot], phases >> slot & 1u))) {
             if (lane == 0) atomicOr(a.fault, 1u);
             dead = true;
             break;
         }
+        phases ^= 1u << slot;
+        pending &= ~(1u << slot);
         const uint32_t tile = smem_addr(ring) + slot * kSlotBytes;
         const int t0 = (first + 2 * u) * kKvSlab;
         // ------------------------------------------------ scores: column g, tokens 8h + 2t, 8h + 2t + 1
@@ -1016,26 +1272,25 @@ __global__ void __launch_bounds__(AttnForm<NB, SHARED>::kThreads, SHARED ? 1 : a
         __syncwarp();
         if constexpr (SHARED) {
             if (lane == 0) mbar_arrive(&empty[slot]);
-        } else if (u + 2 * kWarps < n_units) {  // the warp's unit after next takes the slot's place
-            if (j_next == 16) {
-                j_next = 0;
-                const int next = first + 2 * (u + 2 * kWarps + (lane >> 1) * kWarps) + (lane & 1);
-                feed.look(a, head, next < last ? feed.page_at(a, table, next) : 0, next, last, &sh_bad);
+            slot += n_wt;
+            if (slot >= kSlots) slot -= kSlots;
+        } else {
+            if (u + 2 * kWarps < n_units) {  // the warp's unit after next takes the slot's place
+                if (j_next == 16) {
+                    j_next = 0;
+                    feed.start(a, seg, first + 2 * (u - warp + 2 * kWarps) + tile_off, &sh_bad[n_seg & 1]);
+                }
+                fence_proxy_async_smem();
+                feed.copy(j_next++, lane, ring + slot * kSlotBytes, &full[slot], policy);
+                pending |= 1u << slot;
             }
-            fence_proxy_async_smem();
-            feed.copy(j_next++, lane, ring + slot * kSlotBytes, &full[slot], policy);
-        }
-        slot += n_wt;
-        if (slot >= kSlots) {
-            slot -= kSlots;
-            phase ^= 1;
+            slot ^= kWarps;
         }
     }
-
-    if (!SHARED && dead) {
-        // leave only when the warp's copies have landed (both slots: the one that failed, the one behind it)
-        for (int k = 0; k < 2; ++k)
-            if (warp + k * kWarps < n_units) (void)mbar_wait(&full[warp + k * kWarps], slot == warp + k * kWarps ? phase : phase ^ (k == 0));
+    if (SHARED && dead && warp == 0) {
+        // leave only when the copies have landed, as far as they will
+        for (int k = max(0, min(fed, n_units) - kSlots); k < min(fed, n_units); ++k)
+            (void)mbar_wait(&full[k % kSlots], static_cast<uint32_t>(k / kSlots) & 1u);
     }
 
     // ------------------------------------------------ join the warps
@@ -1046,8 +1301,9 @@ __global__ void __launch_bounds__(AttnForm<NB, SHARED>::kThreads, SHARED ? 1 : a
         m[nt] -= static_cast<float>(sx);  // the maximum in p's unit
         if (t == 0) sh_m[warp][8 * nt + g] = m[nt];
     }
-    attn_consumer_barrier<kWarps>();  // every warp is done with the ring
-    float *sum = reinterpret_cast<float *>(ring);  // [warp][column of the warp][D]
+    __syncthreads();  // every warp is done with the ring
+    // the next segment's first tiles come while this one's sums are joined, where these lie apart from the ring
+    if (!SHARED && kApart && ahead.some && !dead) begin(ahead, &sh_bad[(n_seg + 1) & 1]);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         // this warp's sums in the unit of the warps' common maximum: the lane's column g, columns 2t and 2t + 1 of o
@@ -1066,9 +1322,18 @@ __global__ void __launch_bounds__(AttnForm<NB, SHARED>::kThreads, SHARED ? 1 : a
             *reinterpret_cast<float4 *>(dst + D) = make_float4(x0.y * f[1], x1.y * s1, x2.y * f[1], x3.y * s1);
         }
     }
-    attn_consumer_barrier<kWarps>();
-    attn_store<D, 8 * NT, kWarps>(a, r, item, split, n_splits, cols, a.wc, sum, &sh_m[0][0], &sh_l[0][0], r.bad || sh_bad,
-                                  &sh_last);
+    __syncthreads();
+    attn_store<D, 8 * NT>(a, seg, cols, a.wc, sum, &sh_m[0][0], &sh_l[0][0], r.bad || sh_bad[n_seg & 1], &sh_last);
+    if (!ahead.some) break;
+    __syncthreads();  // the sums and q's fragments are read
+    if (tid == 0) sh_bad[n_seg & 1] = 0;
+    if (!kApart && !dead) begin(ahead, &sh_bad[(n_seg + 1) & 1]);
+    }
+    // leave only when the warp's copies have landed (after a wait that gave up: as far as they will)
+    for (uint32_t left = pending; left != 0; left &= left - 1) {
+        const int k = __ffs(left) - 1;
+        (void)mbar_wait(&full[k], phases >> k & 1u);
+    }
 }
 
 // ------------------------------------------------------------------ host side
@@ -1076,8 +1341,9 @@ struct AttnPlan {
     int nt, wc;           // column groups of 8 a warp, warps that split the columns
     int n_ct, cols;       // column tiles, columns of a tile
     int64_t items;        // kv heads of sequences x column tiles
-    int chunk, n_split;   // tiles of a split, most splits
-    int max_split;        // an upper bound of n_split that only grows with max_kv_len (the workspace's)
+    int chunk, n_split;   // the grid's form: tiles of a split, most splits; else 0
+    int ctas;             // ... CTAs of the grid
+    int64_t parts;        // parts that the workspace holds
 };
 
 template <int NB> cudaError_t launch_attn(AttnArgs a, const AttnPlan &p, cudaStream_t st);
@@ -1088,24 +1354,23 @@ extern template cudaError_t launch_attn<6>(AttnArgs, const AttnPlan &, cudaStrea
 extern template cudaError_t launch_attn<8>(AttnArgs, const AttnPlan &, cudaStream_t);
 
 #ifdef ZDMMV_ATTN_INSTANTIATE
-template <auto KERNEL>
-cudaError_t launch_attn_kernel(int threads, size_t smem, const AttnArgs &a, const AttnPlan &p, cudaStream_t st) {
+template <auto KERNEL> cudaError_t launch_attn_kernel(const AttnPlan &p, size_t smem, const AttnArgs &a, cudaStream_t st) {
     const cudaError_t e = smem_limit_raised<KERNEL>();
     if (e != cudaSuccess) return e;
-    return launch_block_op(KERNEL, dim3(static_cast<unsigned>(p.items), p.n_split), threads, smem, st, a);
+    const dim3 grid = p.n_split > 0 ? dim3(static_cast<unsigned>(p.items), p.n_split) : dim3(p.ctas);
+    return launch_block_op(KERNEL, grid, dim3(kAttnThreads), kAttnBarBytes + smem, st, a);
 }
 template <int NB, int NT, bool SHARED> cudaError_t launch_attn_form(const AttnArgs &a, const AttnPlan &p, cudaStream_t st) {
-    using F = AttnForm<NB, SHARED>;
-    // the join's sums lie over the ring
-    const size_t ring = F::kSlots * 2 * KvGeom<NB>::kTileBytes + static_cast<size_t>(p.wc) * NT * 2 * NB * 512;
-    const size_t join = static_cast<size_t>(kAttnWarps) * NT * 8 * NB * kQK * 4;
-    return launch_attn_kernel<&attn_kernel<NB, NT, SHARED>>(F::kThreads, kAttnBarBytes + (ring > join ? ring : join), a, p, st);
+    const size_t ring = attn_slots<NB, SHARED>() * 2 * KvGeom<NB>::kTileBytes + static_cast<size_t>(p.wc) * NT * 2 * NB * 512;
+    const size_t sums = static_cast<size_t>(kAttnWarps) * NT * 8 * NB * kQK * 4;
+    const size_t smem = attn_sums_apart(NB, NT, SHARED) ? ring + sums : (ring > sums ? ring : sums);
+    return launch_attn_kernel<&attn_kernel<NB, NT, SHARED>>(p, smem, a, st);
 }
 template <int NB> cudaError_t launch_attn(AttnArgs a, const AttnPlan &p, cudaStream_t st) {
     if (p.cols == kNarrowCols) {
-        constexpr size_t kRing = 2 * kAttnWarps * 2 * KvGeom<NB>::kTileBytes, kQ = 2 * NB * 256;
-        static_assert(kRing >= kAttnWarps * kNarrowCols * NB * kQK * 4, "the warps' sums lie over the ring");
-        return launch_attn_kernel<&attn_narrow_kernel<NB>>(kAttnWarps * 32, kAttnBarBytes + kRing + kQ, a, p, st);
+        constexpr size_t kRing = attn_slots<NB, false>() * 2 * KvGeom<NB>::kTileBytes, kQ = 2 * NB * 256;
+        constexpr size_t kSums = kAttnWarps * kNarrowCols * NB * kQK * 4;
+        return launch_attn_kernel<&attn_narrow_kernel<NB>>(p, kRing + kQ + kSums, a, st);
     }
     if (p.wc > 1) return launch_attn_form<NB, 2, true>(a, p, st);
     return p.nt == 1 ? launch_attn_form<NB, 1, false>(a, p, st) : launch_attn_form<NB, 2, false>(a, p, st);
