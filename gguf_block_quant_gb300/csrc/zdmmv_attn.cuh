@@ -107,6 +107,8 @@ struct AttnSeg {
     int mine, part0, part_step;  // this CTA's part; part s of the item is part0 (s = 0) or rest + s * part_step
     int rest;
     bool some;           // false: there is no such segment
+    bool whole;          // the CTA has all of the item ...
+    int base, steps;     // ... whose steps these are
     __device__ int part(int s) const { return s == 0 ? part0 : rest + s * part_step; }
 };
 
@@ -135,7 +137,7 @@ __device__ __forceinline__ bool attn_grid_seg(const AttnArgs &a, int cols, AttnS
 }
 
 // Decoding of several sequences: the CTA's stretch of the row of steps. It lies in shared memory, as the segments do (the main loop has no
-// registers to spare): begin() is for all threads, next() for one, between two barriers.
+// registers to spare).
 struct AttnWalk {
     int ctas, each, more;  // CTAs that have steps; `each` and in all `more` besides, evenly spread
     float per_step;        // ctas / steps
@@ -158,105 +160,85 @@ struct AttnWalk {
         return c;
     }
 
-    // False where the CTA has nothing to do. scan: shared memory for kAttnWarps + 3 ints.
-    __device__ bool begin(const AttnArgs &a, int cols, int *scan) {
-        const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, me = blockIdx.x;
-        const int heads = a.c.n_kv_heads, n_seq = a.c.n_seq;
-        int total = 0;
-        seq = base = 0;
-        if (n_seq == 1) {
-            r = attn_range(a, 0, 0, cols);
-            steps = steps_of(r);
-            total = steps * heads;
-        } else {
-            int mine = 0;
-            for (int s = tid; s < n_seq; s += kAttnThreads) mine += steps_of(attn_range(a, s, 0, cols)) * heads;
-            mine = __reduce_add_sync(0xffffffffu, mine);
-            if (lane == 0) scan[warp] = mine;
-            __syncthreads();
+    // Steps up to and with this thread's, of one value a thread of the CTA; `all` those of the whole CTA. scan: shared
+    // memory for kAttnWarps ints, free again after the next barrier.
+    __device__ static int upto(int w, int *scan, int &all) {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
-            for (int w = 0; w < kAttnWarps; ++w) total += scan[w];
+        for (int k = 1; k < 32; k <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, w, k);
+            if (lane >= k) w += o;
         }
-        ctas = min(static_cast<int>(gridDim.x), total);
-        if (me >= ctas) return false;
-        each = total / ctas;
-        more = total - each * ctas;
-        per_step = static_cast<float>(ctas) / static_cast<float>(total);
-        snap = min(3, each / 3);
-        at = cut(me);
-        end = cut(me + 1);
-        if (n_seq == 1) {
-            const int k0 = at / steps, k1 = (end - 1) / steps;
-            at = snapped(at, k0 * steps, steps);
-            end = snapped(end, k1 * steps, steps);
-        } else {
-            // the sequences whose steps hold both ends; each is snapped by the thread that finds it
-            for (int s0 = 0, before = 0;; s0 += kAttnThreads) {
-                const int s = s0 + tid;
-                const int n = s < n_seq ? steps_of(attn_range(a, s, 0, cols)) : 0, w = n * heads;
-                int upto = w;
+        if (lane == 31) scan[warp] = w;
+        __syncthreads();
+        all = 0;
 #pragma unroll
-                for (int k = 1; k < 32; k <<= 1) {
-                    const int o = __shfl_up_sync(0xffffffffu, upto, k);
-                    if (lane >= k) upto += o;
-                }
-                __syncthreads();
-                if (lane == 31) scan[warp] = upto;
-                __syncthreads();
-                int all = before;
-#pragma unroll
-                for (int k = 0; k < kAttnWarps; ++k) {
-                    if (k < warp) upto += scan[k];
-                    all += scan[k];
-                }
-                upto += before;
-                const int from = upto - w;
-                if (at >= from && at < upto) scan[kAttnWarps] = snapped(at, from + (at - from) / n * n, n);
-                if (end > from && end <= upto) scan[kAttnWarps + 1] = snapped(end, from + (end - 1 - from) / n * n, n);
-                if (end <= all) break;
-                before = all;
-            }
-            __syncthreads();
-            at = scan[kAttnWarps];
-            end = scan[kAttnWarps + 1];
-            if (at >= end) return false;
-            // the item that `at` begins or lies in
-            for (int s0 = 0, before = 0;; s0 += kAttnThreads) {
-                const int s = s0 + tid;
-                const int w = s < n_seq ? steps_of(attn_range(a, s, 0, cols)) * heads : 0;
-                int upto = w;
-#pragma unroll
-                for (int k = 1; k < 32; k <<= 1) {
-                    const int o = __shfl_up_sync(0xffffffffu, upto, k);
-                    if (lane >= k) upto += o;
-                }
-                __syncthreads();
-                if (lane == 31) scan[warp] = upto;
-                __syncthreads();
-                int all = before;
-#pragma unroll
-                for (int k = 0; k < kAttnWarps; ++k) {
-                    if (k < warp) upto += scan[k];
-                    all += scan[k];
-                }
-                upto += before;
-                if (at >= upto - w && at < upto) {
-                    scan[kAttnWarps] = s;
-                    scan[kAttnWarps + 1] = upto - w;
-                }
-                if (at < all) break;
-                before = all;
-            }
-            __syncthreads();
-            seq = scan[kAttnWarps];
-            base = scan[kAttnWarps + 1];
-            r = attn_range(a, seq, 0, cols);
-            steps = steps_of(r);
+        for (int k = 0; k < kAttnWarps; ++k) {
+            if (k < warp) w += scan[k];
+            all += scan[k];
         }
-        kvh = (at - base) / steps;
-        base += kvh * steps;
-        return at < end;
+        return w;
     }
+    // For all threads: fills *to, in shared memory, and is false in all where the CTA has nothing to do. scan: shared memory
+    // for kAttnWarps ints.
+    __device__ static bool begin(const AttnArgs &a, int cols, int *scan, AttnWalk *to) {
+        const int tid = threadIdx.x, me = blockIdx.x, heads = a.c.n_kv_heads, n_seq = a.c.n_seq;
+        // the sequences 256 at a time, one a thread; the first 256 are kept (beyond, they are looked at once more)
+        AttnRange r{};
+        int n = 0, all = 0;
+        if (tid < n_seq) {
+            r = attn_range(a, tid, 0, cols);
+            n = steps_of(r);
+        }
+        int last = upto(n * heads, scan, all), total = all;
+        for (int s0 = kAttnThreads; s0 < n_seq; s0 += kAttnThreads) {
+            int more_all;
+            __syncthreads();
+            (void)upto(s0 + tid < n_seq ? steps_of(attn_range(a, s0 + tid, 0, cols)) * heads : 0, scan, more_all);
+            total += more_all;
+        }
+        AttnWalk w;
+        w.ctas = min(static_cast<int>(gridDim.x), total);
+        if (me >= w.ctas) return false;
+        w.each = total / w.ctas;
+        w.more = total - w.each * w.ctas;
+        w.per_step = static_cast<float>(w.ctas) / static_cast<float>(total);
+        // a part costs its CTA about as much as a step and a half
+        w.snap = w.each >= 12 ? 1 : w.each / 3;
+        const int at = w.cut(me), end = w.cut(me + 1);
+        // the threads whose sequences hold the stretch's ends snap them
+        for (int s0 = 0, before = 0;;) {
+            const int from = before + last - n * heads;
+            if (n > 0 && end > from && end <= from + n * heads) {
+                const int k = (end - 1 - from) / n;
+                to->end = w.snapped(end, from + k * n, n);
+            }
+            if (n > 0 && at >= from && at < from + n * heads) {
+                const int k = (at - from) / n;
+                w.at = w.snapped(at, from + k * n, n);
+                w.seq = s0 + tid;
+                w.kvh = k;
+                w.base = from + k * n;
+                w.steps = n;
+                to->ctas = w.ctas; to->each = w.each; to->more = w.more; to->snap = w.snap; to->per_step = w.per_step;
+                to->at = w.at; to->seq = w.seq; to->kvh = w.kvh; to->base = w.base; to->steps = w.steps; to->r = r;
+            }
+            before += all;
+            if (end <= before) break;
+            s0 += kAttnThreads;
+            r = AttnRange{};
+            n = 0;
+            if (s0 + tid < n_seq) {
+                r = attn_range(a, s0 + tid, 0, cols);
+                n = steps_of(r);
+            }
+            __syncthreads();
+            last = upto(n * heads, scan, all);
+        }
+        __syncthreads();
+        return to->at < to->end;
+    }
+    // For one thread: the next segment, but for share()'s fields.
     __device__ void next(const AttnArgs &a, int cols, AttnSeg &g) {
         g.some = at < end;
         if (!g.some) return;
@@ -278,7 +260,15 @@ struct AttnWalk {
         g.first = r.slab0 + k0 * kStepTiles;
         g.last = min(r.slab0 + r.slabs, r.slab0 + k1 * kStepTiles);
         g.parts = 1;
-        if (k0 > 0 || k1 < steps) {
+        g.base = base;
+        g.steps = steps;
+        g.whole = k0 == 0 && k1 == steps;
+        at += k1 - k0;
+    }
+    // ... and these: who else has parts of the segment's item.
+    __device__ void share(AttnSeg &g) const {
+        if (!g.whole) {
+            const int base = g.base, steps = g.steps;
             // the first and the last CTA that have a step of the item
             int c0 = holder(base), c1 = holder(base + steps - 1);
             while (snapped(cut(c0 + 1), base, steps) <= base) ++c0;
@@ -291,7 +281,6 @@ struct AttnWalk {
             g.part_step = 2;
             g.mine = g.part(static_cast<int>(blockIdx.x) - c0);
         }
-        at += k1 - k0;
     }
 };
 
@@ -619,7 +608,7 @@ template <int NB> __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_
     constexpr int kSlotBytes = 2 * G::kTileBytes;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float sh_m[kWarps][kNarrowCols], sh_l[kWarps][kNarrowCols];
-    __shared__ int sh_bad[2], sh_last, sh_scan[kWarps + 3];
+    __shared__ int sh_bad[2], sh_last, sh_scan[kWarps];
     __shared__ uint32_t sh_magic;
     __shared__ AttnSeg sh_seg[2];
     __shared__ AttnWalk sh_walk;
@@ -657,12 +646,8 @@ template <int NB> __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_
             sh_seg[1].some = false;
         }
     } else {
-        AttnWalk walk;
-        if (!walk.begin(a, kNarrowCols, sh_scan)) return;
-        if (tid == kWalker) {
-            walk.next(a, kNarrowCols, sh_seg[0]);
-            sh_walk = walk;
-        }
+        if (!AttnWalk::begin(a, kNarrowCols, sh_scan, &sh_walk)) return;
+        if (tid == kWalker) sh_walk.next(a, kNarrowCols, sh_seg[0]);
     }
     __syncthreads();
     const uint64_t policy = l2_evict_first_policy();
@@ -728,7 +713,10 @@ template <int NB> __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_
             qf[k / 2][2 * (k % 2) + 1] = f.y;
         }
     }
-    if (tid == kWalker && a.n_split == 0) sh_walk.next(a, kNarrowCols, sh_seg[~n_seg & 1]);
+    if (tid == kWalker && a.n_split == 0) {
+        sh_walk.share(sh_seg[n_seg & 1]);
+        sh_walk.next(a, kNarrowCols, sh_seg[~n_seg & 1]);
+    }
     __syncwarp();
     // what column t sees, of this split's tiles
     const int limit = min(r.len, last * kKvSlab);
@@ -926,7 +914,7 @@ __global__ void __launch_bounds__(kAttnThreads, SHARED ? 1 : attn_ctas_per_sm(NB
     constexpr bool kApart = attn_sums_apart(NB, NT, SHARED);
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float sh_m[kWarps][NT * 8], sh_l[kWarps][NT * 8], sh_qs[kWarps][NT * 8];
-    __shared__ int sh_bad[2], sh_last, sh_scan[kWarps + 3];
+    __shared__ int sh_bad[2], sh_last, sh_scan[kWarps];
     __shared__ uint32_t sh_magic;
     __shared__ AttnSeg sh_seg[2];
     __shared__ AttnWalk sh_walk;
@@ -964,12 +952,8 @@ __global__ void __launch_bounds__(kAttnThreads, SHARED ? 1 : attn_ctas_per_sm(NB
             sh_seg[1].some = false;
         }
     } else {
-        AttnWalk walk;
-        if (!walk.begin(a, cols, sh_scan)) return;
-        if (tid == kWalker) {
-            walk.next(a, cols, sh_seg[0]);
-            sh_walk = walk;
-        }
+        if (!AttnWalk::begin(a, cols, sh_scan, &sh_walk)) return;
+        if (tid == kWalker) sh_walk.next(a, cols, sh_seg[0]);
     }
     __syncthreads();
     const uint64_t policy = l2_evict_first_policy();
@@ -1057,7 +1041,10 @@ __global__ void __launch_bounds__(kAttnThreads, SHARED ? 1 : attn_ctas_per_sm(NB
     low_max = __reduce_max_sync(0xffffffffu, low_max);
     __syncthreads();
 
-    if (!SHARED && tid == kWalker && a.n_split == 0) sh_walk.next(a, cols, sh_seg[~n_seg & 1]);
+    if (!SHARED && tid == kWalker && a.n_split == 0) {
+        sh_walk.share(sh_seg[n_seg & 1]);
+        sh_walk.next(a, cols, sh_seg[~n_seg & 1]);
+    }
     __syncwarp();
 
     float m[NT], l[NT], qs[NT];
