@@ -14,6 +14,7 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // Up to four columns a kv head of a sequence take the narrow form, up to 16 the wide one, more a shared ring. The grid is
 // (items) x (splits of their tokens), as many as run at once -- but for several sequences' decoding with more steps than
 // CTAs, whose lengths decide (AttnWalk; 64 sequences of up to 16384 tokens: 109 us with the grid, WALK_US so).
+constexpr int kEnds = 8;
 constexpr int kCounters = ZDMMV_ATTN_COUNTER_BYTES / 4;
 
 bool attn_plan(const KvView &c, int head_dim, int n_q_heads, int max_q_len, int64_t max_tokens, AttnPlan *out) {
@@ -26,8 +27,9 @@ bool attn_plan(const KvView &c, int head_dim, int n_q_heads, int max_q_len, int6
     }();
     AttnPlan p{};
     const int64_t columns = static_cast<int64_t>(max_q_len) * (n_q_heads / c.n_kv_heads);
-    p.nt = columns <= 8 ? 1 : 2;
+    const int nb = kv_blocks(head_dim);
     p.wc = columns <= 16 ? 1 : (columns <= 32 ? 2 : (columns <= 64 ? 4 : 8));
+    p.nt = p.wc == 8 ? attn_prompt_nt(nb) : (columns <= 8 ? 1 : 2);
     p.cols = columns <= kNarrowCols ? kNarrowCols : 8 * p.nt * p.wc;
     const int64_t n_ct = ceil_div(columns, p.cols);
     p.items = static_cast<int64_t>(c.n_seq) * c.n_kv_heads * n_ct;
@@ -35,16 +37,26 @@ bool attn_plan(const KvView &c, int head_dim, int n_q_heads, int max_q_len, int6
     const int64_t steps = p.items * ceil_div(tiles, kStepTiles);
     if (steps > 0x7fffffff || columns > 0x7fffff00) return false;
     p.n_ct = static_cast<int>(n_ct);
-    const int64_t slots = static_cast<int64_t>(sms) * (p.wc > 1 ? 1 : attn_ctas_per_sm(kv_blocks(head_dim), p.nt));
+    const int64_t slots = static_cast<int64_t>(sms) * (p.wc > 1 ? 1 : attn_ctas_per_sm(nb, p.nt));
     if (p.wc == 1 && c.n_seq > 1 && steps > slots) {
         p.ctas = static_cast<int>(std::min<int64_t>(slots, kCounters));
         p.parts = steps > p.items ? 2 * p.ctas : 0;  // an item of one step is never shared
     } else {
         const int64_t splits = p.items > kCounters ? 1 : std::max<int64_t>(1, slots / p.items);
-        const int64_t most = std::min(splits, ceil_div(tiles, kMinChunk));
+        int64_t most = std::min(splits, ceil_div(tiles, kMinChunk));
+        p.parts = most;
+        if (p.wc > 1 && p.items <= kCounters) {
+            // whole waves of CTAs: the split whose waves cost least, a CTA's start and end as much as kEnds tiles
+            p.parts = std::min(4 * splits, ceil_div(tiles, kMinChunk));
+            const auto cost = [&](int64_t n) { return ceil_div(p.items * n, slots) * (ceil_div(tiles, n) + kEnds); };
+            for (int waves = 1; waves <= 4; ++waves) {
+                const int64_t n = std::min(std::max<int64_t>(1, waves * slots / p.items), p.parts);
+                if (cost(n) < cost(most)) most = n;
+            }
+        }
         p.chunk = static_cast<int>(std::max<int64_t>(kMinChunk, ceil_div(ceil_div(tiles, most), 2) * 2));  // whole ring slots
         p.n_split = static_cast<int>(most);
-        p.parts = most > 1 ? p.items * most : 0;
+        p.parts = p.parts > 1 ? p.items * p.parts : 0;
     }
     *out = p;
     return true;

@@ -64,12 +64,17 @@ struct AttnArgs {
 constexpr int kAttnWarps = 8, kAttnThreads = kAttnWarps * 32;
 constexpr int kWalker = kAttnThreads - 1;    // the thread that finds the CTA's next segment
 constexpr int kStepTiles = 2 * kAttnWarps;  // tiles of a step: a ring slot for each warp
-// Ring slots (a pair of tiles) of a CTA: two a warp; the shared ring's, as many where they fit.
-template <int NB, bool SHARED> __host__ __device__ constexpr int attn_slots() { return SHARED && NB >= 8 ? 8 : 16; }
+// The wide kernel's forms: own rings (up to 16 columns), a shared ring (17 to 64), a shared ring whose codes the CTA turns
+// into fragments once for all its warps (more: prompts).
+enum AttnForm { kOwn = 0, kShared = 1, kPrompt = 2 };
+// Ring slots (a pair of tiles) of a CTA: two a warp; of the shared rings as many where they fit.
+__host__ __device__ constexpr int attn_slots(int nb, int form) { return form == kOwn || (form == kShared && nb < 8) ? 16 : 8; }
+// Groups of 8 columns a warp of the prompt form: two, one where the shared memory does not hold q and the fragments of two.
+__host__ __device__ constexpr int attn_prompt_nt(int nb) { return nb < 8 ? 2 : 1; }
 // CTAs of the forms without a shared ring that run on an SM at once.
 __host__ __device__ constexpr int attn_ctas_per_sm(int nb, int nt) { return nb * nt <= 4 ? 2 : 1; }
 // Whether the warps' sums have shared memory of their own, so that the next item's tiles can come while they are joined.
-__host__ __device__ constexpr bool attn_sums_apart(int nb, int nt, bool shared) { return !shared && nb * nt < 16; }
+__host__ __device__ constexpr bool attn_sums_apart(int nb, int nt, int form) { return form == kOwn && nb * nt < 16; }
 constexpr int kAttnBarBytes = 256;  // two barriers a slot
 constexpr int kAttnUnit = 13;
 constexpr int kJoinAhead = 16;
@@ -295,6 +300,9 @@ __device__ __forceinline__ void mma_first(float (&d)[4], const uint32_t (&a)[4],
         "{%10, %10, %10, %10};"
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+}
+__device__ __forceinline__ void sts128(uint32_t at, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 __device__ __forceinline__ uint32_t h2_add(uint32_t a, uint32_t b) {
     uint32_t d;
@@ -903,15 +911,20 @@ template <int NB> __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_
         if (pending >> k & 1u) (void)mbar_wait(&full[k], phases >> k & 1u);
 }
 
-// The wide form: each warp 8 * NT columns. SHARED: prompts; the warps split the columns (a.wc of them; the others the
-// ring's slots), warp 0 feeds the ring half a ring ahead of itself.
-template <int NB, int NT, bool SHARED>
-__global__ void __launch_bounds__(kAttnThreads, SHARED ? 1 : attn_ctas_per_sm(NB, NT)) attn_kernel(AttnArgs a) {
+// The wide form: each warp 8 * NT columns. With a shared ring the warps split the columns (a.wc of them; the others the
+// ring's slots), and warp 0 feeds it half a ring ahead of itself. The prompt form (a.wc = 8): every unit's codes become
+// fp16 fragments in shared memory once, an eighth by each warp, a unit ahead of their use (one barrier a unit; converting
+// in every warp costs 144 of its 480 instructions a tile), and q's fragments stay in registers. Bound by the tensor cores'
+// mma.sync rate (8 cycles an m16n8k16), twice the products of 16-bit inputs for the two parts of q and p.
+template <int NB, int NT, int FORM>
+__global__ void __launch_bounds__(kAttnThreads, FORM != kOwn ? 1 : attn_ctas_per_sm(NB, NT)) attn_kernel(AttnArgs a) {
+    constexpr bool SHARED = FORM != kOwn, PROMPT = FORM == kPrompt;
+    constexpr bool kQReg = PROMPT && NB * NT <= 8;  // q's fragments in registers
     using G = KvGeom<NB>;
-    constexpr int kWarps = kAttnWarps, kSlots = attn_slots<NB, SHARED>();
+    constexpr int kWarps = kAttnWarps, kSlots = attn_slots(NB, FORM);
     constexpr int D = G::kDim;
     constexpr int kSlotBytes = 2 * G::kTileBytes;
-    constexpr bool kApart = attn_sums_apart(NB, NT, SHARED);
+    constexpr bool kApart = attn_sums_apart(NB, NT, FORM);
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float sh_m[kWarps][NT * 8], sh_l[kWarps][NT * 8], sh_qs[kWarps][NT * 8];
     __shared__ int sh_bad[2], sh_last, sh_scan[kWarps];
@@ -987,6 +1000,35 @@ __global__ void __launch_bounds__(kAttnThreads, SHARED ? 1 : attn_ctas_per_sm(NB
     float *sum = reinterpret_cast<float *>(kApart ? ring + kSlots * kSlotBytes + NT * 2 * NB * 512 : ring);
     const uint32_t magic = lds32(smem_addr(&sh_magic));
     const uint32_t q_at = smem_addr(q_sm);
+    // PROMPT: the fragments of two units, [octet][block][lane] of K, then [tile][block][half][lane] of V
+    constexpr uint32_t kFragV = 4 * NB * 512, kFragBytes = 8 * NB * 512;
+    const uint32_t frag0 = smem_addr(ring) + kSlots * kSlotBytes + a.wc * (NT * 2 * NB * 512);
+    const auto convert = [&](uint32_t tile, uint32_t to) {
+        const auto word = [&](int s, int at, int plane, int b) {
+            return lds32(tile + s * G::kTileBytes + at + (((plane * (NB / G::kVec) + b / G::kVec) * 32 + lane) * G::kVec + b % G::kVec) * 4);
+        };
+        for (int k = warp; k < 4 * NB; k += kWarps) {
+            const int h = k / NB, b = k % NB;
+            uint32_t c[4];
+            code_pairs(word(h >> 1, 0, h & 1, b), magic, c);
+            sts128(to + k * 512 + lane * 16, c[0], c[1], c[2], c[3]);
+        }
+        for (int k = warp; k < 2 * NB; k += kWarps) {
+            const int s = k / NB, j = k % NB;
+            uint32_t c[4], d[4];
+            code_pairs(word(s, G::kVAt, 0, j), magic, c);
+            code_pairs(word(s, G::kVAt, 1, j), magic, d);
+            sts128(to + kFragV + 2 * k * 512 + lane * 16, c[0], c[1], d[0], d[1]);
+            sts128(to + kFragV + (2 * k + 1) * 512 + lane * 16, c[2], c[3], d[2], d[3]);
+        }
+    };
+    const auto wait_full = [&](int s) {  // PROMPT: a wait that gave up ends no loop, so that every barrier is met
+        if (!dead && !__all_sync(0xffffffffu, mbar_wait(&full[s], phases >> s & 1u))) {
+            if (lane == 0) atomicOr(a.fault, 1u);
+            dead = true;
+        }
+        phases ^= 1u << s;
+    };
     if (!SHARED) begin(sh_seg[0], &sh_bad[0]);
 
     for (int n_seg = 0;; ++n_seg) {
@@ -1059,9 +1101,33 @@ __global__ void __launch_bounds__(kAttnThreads, SHARED ? 1 : attn_ctas_per_sm(NB
     }
     int sx = kAttnUnit;  // p is in units of 2^sx
 
+    uint32_t qreg[kQReg ? NT : 1][kQReg ? 2 * NB : 1][4];
+    if constexpr (kQReg) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int k = 0; k < 2 * NB; ++k) {
+                const uint4 f = lds128(q_at + (nt * 2 * NB + k) * 512);
+                qreg[nt][k][0] = f.x; qreg[nt][k][1] = f.y; qreg[nt][k][2] = f.z; qreg[nt][k][3] = f.w;
+            }
+    }
+    if (PROMPT && n_units > 0) {
+        wait_full(0);
+        convert(smem_addr(ring), frag0);
+        __syncthreads();
+    }
+
     int fed = kSlots;  // SHARED: units that warp 0 has asked for
-    for (int u = wt, j_next = 2; u < n_units && !dead; u += n_wt) {
-        if (SHARED && warp == 0) {
+    for (int u = wt, j_next = 2; u < n_units && (PROMPT || !dead); u += n_wt) {
+        if (PROMPT) {
+            const int s = (u + 1) % kSlots;
+            if (u + 1 < n_units) {
+                wait_full(s);
+                convert(smem_addr(ring) + s * kSlotBytes, frag0 + (~u & 1) * kFragBytes);
+            }
+        }
+        const uint32_t frag = frag0 + (u & 1) * kFragBytes + lane * 16;
+        if (SHARED && !PROMPT && warp == 0) {
             for (; fed < n_units && fed <= u + kSlots / 2; ++fed) {
                 const int s = fed % kSlots;
                 // unit fed - kSlots, before u: every warp that needs it has it, so this ends
@@ -1075,13 +1141,15 @@ __global__ void __launch_bounds__(kAttnThreads, SHARED ? 1 : attn_ctas_per_sm(NB
                 feed.copy(fed % 16, lane, ring + s * kSlotBytes, &full[s], policy);
             }
         }
-        if (!__all_sync(0xffffffffu, mbar_wait(&full[slot], phases >> slot & 1u))) {
-            if (lane == 0) atomicOr(a.fault, 1u);
-            dead = true;
-            break;
+        if constexpr (!PROMPT) {
+            if (!__all_sync(0xffffffffu, mbar_wait(&full[slot], phases >> slot & 1u))) {
+                if (lane == 0) atomicOr(a.fault, 1u);
+                dead = true;
+                break;
+            }
+            phases ^= 1u << slot;
+            pending &= ~(1u << slot);
         }
-        phases ^= 1u << slot;
-        pending &= ~(1u << slot);
         const uint32_t tile = smem_addr(ring) + slot * kSlotBytes;
         const int t0 = (first + 2 * u) * kKvSlab;
         // ------------------------------------------------ scores: column g, tokens 8h + 2t, 8h + 2t + 1
@@ -1095,7 +1163,8 @@ __global__ void __launch_bounds__(kAttnThreads, SHARED ? 1 : attn_ctas_per_sm(NB
             uint32_t kw[2][NB], dk[2][NB];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                lds_words<NB, G::kVec>(tile + s * G::kTileBytes + (h * NB * 32 + lane * G::kVec) * 4, 128 * G::kVec, kw[h]);
+                if constexpr (!PROMPT)
+                    lds_words<NB, G::kVec>(tile + s * G::kTileBytes + (h * NB * 32 + lane * G::kVec) * 4, 128 * G::kVec, kw[h]);
                 lds_words<NB, G::kVec>(tile + s * G::kTileBytes + G::kKScaleAt + (t + 4 * h) * NB * 4, 4 * G::kVec, dk[h]);
             }
 #pragma unroll
@@ -1105,13 +1174,23 @@ __global__ void __launch_bounds__(kAttnThreads, SHARED ? 1 : attn_ctas_per_sm(NB
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        const uint4 f = lds128(q_at + (nt * 2 * NB + 2 * b + k) * 512);
-                        qa[nt][k][0] = f.x; qa[nt][k][1] = f.y; qa[nt][k][2] = f.z; qa[nt][k][3] = f.w;
+                        if constexpr (kQReg) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) qa[nt][k][i] = qreg[nt][2 * b + k][i];
+                        } else {
+                            const uint4 f = lds128(q_at + (nt * 2 * NB + 2 * b + k) * 512);
+                            qa[nt][k][0] = f.x; qa[nt][k][1] = f.y; qa[nt][k][2] = f.z; qa[nt][k][3] = f.w;
+                        }
                     }
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     uint32_t kc[4];
-                    code_pairs(kw[h][b], magic, kc);
+                    if constexpr (PROMPT) {
+                        const uint4 f = lds128(frag + ((2 * s + h) * NB + b) * 512);
+                        kc[0] = f.x; kc[1] = f.y; kc[2] = f.z; kc[3] = f.w;
+                    } else {
+                        code_pairs(kw[h][b], magic, kc);
+                    }
                     const uint64_t d = f2_half2(dk[h][b]);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
@@ -1221,19 +1300,29 @@ __global__ void __launch_bounds__(kAttnThreads, SHARED ? 1 : attn_ctas_per_sm(NB
         }
         // ------------------------------------------------ product with V
         uint32_t vw[4][NB];
+        if constexpr (!PROMPT) {
 #pragma unroll
-        for (int h = 0; h < 4; ++h)
-            lds_words<NB, G::kVec>(tile + (h >> 1) * G::kTileBytes + G::kVAt + ((h & 1) * NB * 32 + lane * G::kVec) * 4,
-                                   128 * G::kVec, vw[h]);
+            for (int h = 0; h < 4; ++h)
+                lds_words<NB, G::kVec>(tile + (h >> 1) * G::kTileBytes + G::kVAt + ((h & 1) * NB * 32 + lane * G::kVec) * 4,
+                                       128 * G::kVec, vw[h]);
+        }
 #pragma unroll
         for (int j = 0; j < NB; ++j) {
             uint32_t f[2][2][4];  // [tile][dimensions 4g, 4g+1 / 4g+2, 4g+3 of the block]
+            if constexpr (PROMPT) {
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {
-                uint32_t vc[4];
-                code_pairs(vw[h][j], magic, vc);
-                f[h >> 1][0][2 * (h & 1)] = vc[0]; f[h >> 1][0][2 * (h & 1) + 1] = vc[1];
-                f[h >> 1][1][2 * (h & 1)] = vc[2]; f[h >> 1][1][2 * (h & 1) + 1] = vc[3];
+                for (int k = 0; k < 4; ++k) {
+                    const uint4 x = lds128(frag + kFragV + (2 * ((k >> 1) * NB + j) + (k & 1)) * 512);
+                    f[k >> 1][k & 1][0] = x.x; f[k >> 1][k & 1][1] = x.y; f[k >> 1][k & 1][2] = x.z; f[k >> 1][k & 1][3] = x.w;
+                }
+            } else {
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    uint32_t vc[4];
+                    code_pairs(vw[h][j], magic, vc);
+                    f[h >> 1][0][2 * (h & 1)] = vc[0]; f[h >> 1][0][2 * (h & 1) + 1] = vc[1];
+                    f[h >> 1][1][2 * (h & 1)] = vc[2]; f[h >> 1][1][2 * (h & 1) + 1] = vc[3];
+                }
             }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
@@ -1257,7 +1346,16 @@ __global__ void __launch_bounds__(kAttnThreads, SHARED ? 1 : attn_ctas_per_sm(NB
             }
         }
         __syncwarp();
-        if constexpr (SHARED) {
+        if constexpr (PROMPT) {
+            __syncthreads();  // the unit's slot and fragments are free, the next one's fragments are there
+            if (warp == 0 && u + kSlots < n_units && !dead) {
+                if ((u + kSlots) % 16 == 0) feed.start(a, seg, first + 2 * (u + kSlots) + tile_off, &sh_bad[0]);
+                fence_proxy_async_smem();
+                feed.copy((u + kSlots) % 16, lane, ring + slot * kSlotBytes, &full[slot], policy);
+                fed = u + kSlots + 1;
+            }
+            if (++slot == kSlots) slot = 0;
+        } else if constexpr (SHARED) {
             if (lane == 0) mbar_arrive(&empty[slot]);
             slot += n_wt;
             if (slot >= kSlots) slot -= kSlots;
@@ -1347,20 +1445,22 @@ template <auto KERNEL> cudaError_t launch_attn_kernel(const AttnPlan &p, size_t 
     const dim3 grid = p.n_split > 0 ? dim3(static_cast<unsigned>(p.items), p.n_split) : dim3(p.ctas);
     return launch_block_op(KERNEL, grid, dim3(kAttnThreads), kAttnBarBytes + smem, st, a);
 }
-template <int NB, int NT, bool SHARED> cudaError_t launch_attn_form(const AttnArgs &a, const AttnPlan &p, cudaStream_t st) {
-    const size_t ring = attn_slots<NB, SHARED>() * 2 * KvGeom<NB>::kTileBytes + static_cast<size_t>(p.wc) * NT * 2 * NB * 512;
+template <int NB, int NT, int FORM> cudaError_t launch_attn_form(const AttnArgs &a, const AttnPlan &p, cudaStream_t st) {
+    const size_t ring = attn_slots(NB, FORM) * 2 * KvGeom<NB>::kTileBytes + static_cast<size_t>(p.wc) * NT * 2 * NB * 512 +
+                        (FORM == kPrompt ? 2 * 8 * NB * 512 : 0);
     const size_t sums = static_cast<size_t>(kAttnWarps) * NT * 8 * NB * kQK * 4;
-    const size_t smem = attn_sums_apart(NB, NT, SHARED) ? ring + sums : (ring > sums ? ring : sums);
-    return launch_attn_kernel<&attn_kernel<NB, NT, SHARED>>(p, smem, a, st);
+    const size_t smem = attn_sums_apart(NB, NT, FORM) ? ring + sums : (ring > sums ? ring : sums);
+    return launch_attn_kernel<&attn_kernel<NB, NT, FORM>>(p, smem, a, st);
 }
 template <int NB> cudaError_t launch_attn(AttnArgs a, const AttnPlan &p, cudaStream_t st) {
     if (p.cols == kNarrowCols) {
-        constexpr size_t kRing = attn_slots<NB, false>() * 2 * KvGeom<NB>::kTileBytes, kQ = 2 * NB * 256;
+        constexpr size_t kRing = attn_slots(NB, kOwn) * 2 * KvGeom<NB>::kTileBytes, kQ = 2 * NB * 256;
         constexpr size_t kSums = kAttnWarps * kNarrowCols * NB * kQK * 4;
         return launch_attn_kernel<&attn_narrow_kernel<NB>>(p, kRing + kQ + kSums, a, st);
     }
-    if (p.wc > 1) return launch_attn_form<NB, 2, true>(a, p, st);
-    return p.nt == 1 ? launch_attn_form<NB, 1, false>(a, p, st) : launch_attn_form<NB, 2, false>(a, p, st);
+    if (p.wc == 8) return launch_attn_form<NB, attn_prompt_nt(NB), kPrompt>(a, p, st);
+    if (p.wc > 1) return launch_attn_form<NB, 2, kShared>(a, p, st);
+    return p.nt == 1 ? launch_attn_form<NB, 1, kOwn>(a, p, st) : launch_attn_form<NB, 2, kOwn>(a, p, st);
 }
 #endif
 
