@@ -12,8 +12,12 @@ namespace {
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Up to four columns a kv head of a sequence take the narrow form, up to 16 the wide one, more a shared ring. The grid is
-// (items) x (splits of their tokens), as many as run at once -- but for several sequences' decoding with more steps than
-// CTAs, whose lengths decide (AttnWalk; 64 sequences of up to 16384 tokens: 109 us with the grid, WALK_US so).
+// (items) x (splits of their tokens): as many as run at once; up to four times that for several sequences, whose lengths may
+// differ, while a split has kRaggedChunk tiles; whole waves of prompts' CTAs. Long sequences' decoding, from kWalkSteps steps
+// a CTA on, goes by the lengths instead (AttnWalk): 64 of up to 16384 tokens 109 us with the grid and 96 so, 64 of 4096 71
+// and 68, but 64 of 1000 22.4 and 24.6.
+constexpr int kWalkSteps = 12;
+constexpr int kRaggedChunk = 128;
 constexpr int kEnds = 8;
 constexpr int kCounters = ZDMMV_ATTN_COUNTER_BYTES / 4;
 
@@ -38,11 +42,13 @@ bool attn_plan(const KvView &c, int head_dim, int n_q_heads, int max_q_len, int6
     if (steps > 0x7fffffff || columns > 0x7fffff00) return false;
     p.n_ct = static_cast<int>(n_ct);
     const int64_t slots = static_cast<int64_t>(sms) * (p.wc > 1 ? 1 : attn_ctas_per_sm(nb, p.nt));
-    if (p.wc == 1 && c.n_seq > 1 && steps > slots) {
+    if (p.wc == 1 && c.n_seq > 1 && steps > kWalkSteps * slots) {
         p.ctas = static_cast<int>(std::min<int64_t>(slots, kCounters));
         p.parts = steps > p.items ? 2 * p.ctas : 0;  // an item of one step is never shared
     } else {
-        const int64_t splits = p.items > kCounters ? 1 : std::max<int64_t>(1, slots / p.items);
+        int64_t splits = p.items > kCounters ? 1 : std::max<int64_t>(1, slots / p.items);
+        if (p.wc == 1 && c.n_seq > 1 && p.items <= kCounters)
+            splits = std::max(splits, std::min(ceil_div(4 * slots, p.items), ceil_div(tiles, kRaggedChunk)));
         int64_t most = std::min(splits, ceil_div(tiles, kMinChunk));
         p.parts = most;
         if (p.wc > 1 && p.items <= kCounters) {

@@ -118,7 +118,8 @@ struct AttnSeg {
 };
 
 // The grid's form, (item) x (split): the CTA's part of its item, tiles in equal stretches of kMinChunk or more; false where
-// there is none.
+// there is none. (Splitting each of several sequences by its own length cuts the short ones up for nothing: 22.4 instead of
+// 15 us for 8 sequences of 3 to 8191 tokens and 16 heads.)
 constexpr int kMinChunk = kStepTiles;
 __device__ __forceinline__ bool attn_grid_seg(const AttnArgs &a, int cols, AttnSeg &g) {
     const int item = blockIdx.x, split = blockIdx.y;
@@ -128,8 +129,8 @@ __device__ __forceinline__ bool attn_grid_seg(const AttnArgs &a, int cols, AttnS
     g.kvh = a.by_heads.mod(sh, g.seq);
     g.r = attn_range(a, g.seq, g.ct, cols);
     if (g.ct * cols >= g.r.n * a.group) return false;
-    // the host's chunk is for the longest sequence that the call allows
-    const int chunk = max(kMinChunk, (a.by_split.div(g.r.slabs + a.n_split - 1) + 1) & ~1);
+    // the host's chunk is for the longest sequence that the call allows; a single one is split by its own length
+    const int chunk = a.c.n_seq > 1 ? a.chunk : max(kMinChunk, (a.by_split.div(g.r.slabs + a.n_split - 1) + 1) & ~1);
     g.parts = max(1, (g.r.slabs + chunk - 1) / chunk);
     if (split >= g.parts) return false;
     g.first = g.r.slab0 + split * chunk;
@@ -209,7 +210,7 @@ struct AttnWalk {
         w.more = total - w.each * w.ctas;
         w.per_step = static_cast<float>(w.ctas) / static_cast<float>(total);
         // a part costs its CTA about as much as a step and a half
-        w.snap = w.each >= 12 ? 1 : w.each / 3;
+        w.snap = min(2, w.each / 3);
         const int at = w.cut(me), end = w.cut(me + 1);
         // the threads whose sequences hold the stretch's ends snap them
         for (int s0 = 0, before = 0;;) {
@@ -914,12 +915,13 @@ template <int NB> __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_
 // The wide form: each warp 8 * NT columns. With a shared ring the warps split the columns (a.wc of them; the others the
 // ring's slots), and warp 0 feeds it half a ring ahead of itself. The prompt form (a.wc = 8): every unit's codes become
 // fp16 fragments in shared memory once, an eighth by each warp, a unit ahead of their use (one barrier a unit; converting
-// in every warp costs 144 of its 480 instructions a tile), and q's fragments stay in registers. Bound by the tensor cores'
-// mma.sync rate (8 cycles an m16n8k16), twice the products of 16-bit inputs for the two parts of q and p.
+// in every warp costs 144 of its 480 instructions a tile). Two warps a scheduler (O's and the products' registers allow no
+// more) keep the tensor cores 40% busy (8 cycles an m16n8k16): a 256-token chunk over 8192 takes 294 us, 114 at their rate.
+// Measured and not kept: q's fragments in registers (295), a product's sums put off behind the next block's products (295),
+// the warps drifting apart by up to two units (317), 8 columns a warp with 16 warps (445).
 template <int NB, int NT, int FORM>
 __global__ void __launch_bounds__(kAttnThreads, FORM != kOwn ? 1 : attn_ctas_per_sm(NB, NT)) attn_kernel(AttnArgs a) {
     constexpr bool SHARED = FORM != kOwn, PROMPT = FORM == kPrompt;
-    constexpr bool kQReg = PROMPT && NB * NT <= 8;  // q's fragments in registers
     using G = KvGeom<NB>;
     constexpr int kWarps = kAttnWarps, kSlots = attn_slots(NB, FORM);
     constexpr int D = G::kDim;
@@ -1101,16 +1103,6 @@ __global__ void __launch_bounds__(kAttnThreads, FORM != kOwn ? 1 : attn_ctas_per
     }
     int sx = kAttnUnit;  // p is in units of 2^sx
 
-    uint32_t qreg[kQReg ? NT : 1][kQReg ? 2 * NB : 1][4];
-    if constexpr (kQReg) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int k = 0; k < 2 * NB; ++k) {
-                const uint4 f = lds128(q_at + (nt * 2 * NB + k) * 512);
-                qreg[nt][k][0] = f.x; qreg[nt][k][1] = f.y; qreg[nt][k][2] = f.z; qreg[nt][k][3] = f.w;
-            }
-    }
     if (PROMPT && n_units > 0) {
         wait_full(0);
         convert(smem_addr(ring), frag0);
@@ -1174,31 +1166,34 @@ __global__ void __launch_bounds__(kAttnThreads, FORM != kOwn ? 1 : attn_ctas_per
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        if constexpr (kQReg) {
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) qa[nt][k][i] = qreg[nt][2 * b + k][i];
-                        } else {
-                            const uint4 f = lds128(q_at + (nt * 2 * NB + 2 * b + k) * 512);
-                            qa[nt][k][0] = f.x; qa[nt][k][1] = f.y; qa[nt][k][2] = f.z; qa[nt][k][3] = f.w;
-                        }
+                        const uint4 f = lds128(q_at + (nt * 2 * NB + 2 * b + k) * 512);
+                        qa[nt][k][0] = f.x; qa[nt][k][1] = f.y; qa[nt][k][2] = f.z; qa[nt][k][3] = f.w;
                     }
+                float c[2][NT][4];
+                uint32_t kc[2][4];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    uint32_t kc[4];
                     if constexpr (PROMPT) {
                         const uint4 f = lds128(frag + ((2 * s + h) * NB + b) * 512);
-                        kc[0] = f.x; kc[1] = f.y; kc[2] = f.z; kc[3] = f.w;
+                        kc[h][0] = f.x; kc[h][1] = f.y; kc[h][2] = f.z; kc[h][3] = f.w;
                     } else {
-                        code_pairs(kw[h][b], magic, kc);
+                        code_pairs(kw[h][b], magic, kc[h]);
                     }
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) mma_first(c[h][nt], qa[nt][0], kc[h][0], kc[h][1]);
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) mma_acc(c[h][nt], qa[nt][1], kc[h][2], kc[h][3]);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
                     const uint64_t d = f2_half2(dk[h][b]);
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        float c[4];
-                        mma_first(c, qa[nt][0], kc[0], kc[1]);
-                        mma_acc(c, qa[nt][1], kc[2], kc[3]);
-                        acc[nt][2 * s + h] = f2_fma(d, f2_add(f2(c[0], c[1]), f2(c[2], c[3])), acc[nt][2 * s + h]);
-                    }
+                    for (int nt = 0; nt < NT; ++nt)
+                        acc[nt][2 * s + h] = f2_fma(d, f2_add(f2(c[h][nt][0], c[h][nt][1]), f2(c[h][nt][2], c[h][nt][3])), acc[nt][2 * s + h]);
                 }
             }
         }
@@ -1324,26 +1319,39 @@ __global__ void __launch_bounds__(kAttnThreads, FORM != kOwn ? 1 : attn_ctas_per
                     f[h >> 1][1][2 * (h & 1)] = vc[2]; f[h >> 1][1][2 * (h & 1) + 1] = vc[3];
                 }
             }
+            uint32_t hi[NT][4], lo[NT][4];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                uint32_t hi[4], lo[4];
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int h = 0; h < 4; ++h) {
-                    hi[h] = h2_mul(ph[nt][h], dv[h][j]);
-                    lo[h] = h2_fma(pl[nt][h], dv[h][j], h2_fma(ph[nt][h], dv[h][j], h2_neg(hi[h])));
+                    hi[nt][h] = h2_mul(ph[nt][h], dv[h][j]);
+                    lo[nt][h] = h2_fma(pl[nt][h], dv[h][j], h2_fma(ph[nt][h], dv[h][j], h2_neg(hi[nt][h])));
                 }
-                // summed over the unit by the tensor cores (they truncate), over the units in fp32
+            // summed over the unit by the tensor cores (they truncate), over the units in fp32
+            float c[NT][2][4];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int s = 0; s < 2; ++s) mma_first(c[nt][s], f[0][s], lo[nt][0], lo[nt][1]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int s = 0; s < 2; ++s) mma_acc(c[nt][s], f[1][s], lo[nt][2], lo[nt][3]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int s = 0; s < 2; ++s) mma_acc(c[nt][s], f[0][s], hi[nt][0], hi[nt][1]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int s = 0; s < 2; ++s) mma_acc(c[nt][s], f[1][s], hi[nt][2], hi[nt][3]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {
-                    float c[4];
-                    mma_first(c, f[0][s], lo[0], lo[1]);
-                    mma_acc(c, f[1][s], lo[2], lo[3]);
-                    mma_acc(c, f[0][s], hi[0], hi[1]);
-                    mma_acc(c, f[1][s], hi[2], hi[3]);
-                    o[nt][2 * j + s][0] = f2_add(o[nt][2 * j + s][0], f2(c[0], c[1]));
-                    o[nt][2 * j + s][1] = f2_add(o[nt][2 * j + s][1], f2(c[2], c[3]));
+                    o[nt][2 * j + s][0] = f2_add(o[nt][2 * j + s][0], f2(c[nt][s][0], c[nt][s][1]));
+                    o[nt][2 * j + s][1] = f2_add(o[nt][2 * j + s][1], f2(c[nt][s][2], c[nt][s][3]));
                 }
-            }
         }
         __syncwarp();
         if constexpr (PROMPT) {
