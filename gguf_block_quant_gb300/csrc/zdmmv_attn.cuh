@@ -451,6 +451,13 @@ template <int NB> struct TileFeed {
         const int slot = a.by_page_tiles.div(tile);
         return slot < a.c.max_pages ? table[slot] : 0;
     }
+    // the same, now: a plain load may be put off to its use, behind the loads that it should run beside
+    __device__ static int page_early(const AttnArgs &a, const int32_t *table, int tile) {
+        const int slot = min(a.by_page_tiles.div(tile), a.c.max_pages - 1);
+        int page;
+        asm volatile("ld.global.b32 %0, [%1];" : "=r"(page) : "l"(table + slot));
+        return page;
+    }
     __device__ void look(const AttnArgs &a, const uint8_t *head, int page, int tile, int last, int *sh_bad) {
         in = tile < last;
         const bool wrong = in && (page < 0 || page >= a.c.n_pages);
@@ -639,26 +646,8 @@ template <int NB> __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_
     block_op_wait();
     block_op_release();
 
-    // without a window a sequence of the full length has its split's pages here: looked up beside the lengths
     const int tile_off = 2 * (warp + (lane >> 1) * kWarps) + (lane & 1);
     int early_tile = -1, early_page = 0;
-    if (a.n_split > 0) {
-        AttnSeg seg;
-        if (a.window == 0) {
-            early_tile = blockIdx.y * a.chunk + tile_off;
-            const int seq = a.by_heads.div(a.by_ct.div(blockIdx.x));
-            early_page = TileFeed<NB>::page_at(a, a.c.table + static_cast<int64_t>(seq) * a.c.max_pages, early_tile);
-        }
-        if (!attn_grid_seg(a, kNarrowCols, seg)) return;
-        if (tid == kWalker) {
-            sh_seg[0] = seg;
-            sh_seg[1].some = false;
-        }
-    } else {
-        if (!AttnWalk::begin(a, kNarrowCols, sh_scan, &sh_walk)) return;
-        if (tid == kWalker) sh_walk.next(a, kNarrowCols, sh_seg[0]);
-    }
-    __syncthreads();
     const uint64_t policy = l2_evict_first_policy();
     TileFeed<NB> feed;
     int slot = 0;
@@ -681,8 +670,29 @@ template <int NB> __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_
     // q: column g / 2, this lane's dimensions 8t .. 8t+7 of every block; asked for before the tiles' copies, which it
     // would otherwise wait behind
     float v[NB][8];
-    load_q<NB>(a, sh_seg[0].r, sh_seg[0].kvh, g / 2, t, v);
-    begin(sh_seg[0], &sh_bad[0]);
+    if (a.n_split > 0) {
+        // without a window a sequence of the full length has its split's pages here: looked up beside the lengths
+        if (a.window == 0) {
+            early_tile = blockIdx.y * a.chunk + tile_off;
+            const int seq = a.by_heads.div(a.by_ct.div(blockIdx.x));
+            early_page = TileFeed<NB>::page_early(a, a.c.table + static_cast<int64_t>(seq) * a.c.max_pages, early_tile);
+        }
+        AttnSeg seg;
+        if (!attn_grid_seg(a, kNarrowCols, seg)) return;
+        load_q<NB>(a, seg.r, seg.kvh, g / 2, t, v);
+        begin(seg, &sh_bad[0]);
+        if (tid == kWalker) {
+            sh_seg[0] = seg;
+            sh_seg[1].some = false;
+        }
+        __syncthreads();
+    } else {
+        if (!AttnWalk::begin(a, kNarrowCols, sh_scan, &sh_walk)) return;
+        if (tid == kWalker) sh_walk.next(a, kNarrowCols, sh_seg[0]);
+        __syncthreads();
+        load_q<NB>(a, sh_seg[0].r, sh_seg[0].kvh, g / 2, t, v);
+        begin(sh_seg[0], &sh_bad[0]);
+    }
     const uint32_t magic = lds32(smem_addr(&sh_magic));
     const uint32_t pick = (g & 1) ? 0x7632u : 0x5410u;  // the token's half of two words of scales
 
@@ -959,7 +969,7 @@ __global__ void __launch_bounds__(kAttnThreads, FORM != kOwn ? 1 : attn_ctas_per
         if (a.window == 0) {
             early_tile = blockIdx.y * a.chunk + tile_off;
             const int seq = a.by_heads.div(a.by_ct.div(blockIdx.x));
-            early_page = TileFeed<NB>::page_at(a, a.c.table + static_cast<int64_t>(seq) * a.c.max_pages, early_tile);
+            early_page = TileFeed<NB>::page_early(a, a.c.table + static_cast<int64_t>(seq) * a.c.max_pages, early_tile);
         }
         if (!attn_grid_seg(a, cols, seg)) return;
         if (tid == kWalker) {
