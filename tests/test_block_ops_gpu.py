@@ -288,6 +288,56 @@ def test_attention_new_tokens(lens, new, window, heads, group, dim):
     run_attention(np.random.default_rng(sum(lens) + sum(new) + window), lens, new, 32, heads, group, dim, window=window)
 
 
+def ragged(rng, n, most):
+    """Lengths from 0 and 1 to `most`, most of them short."""
+    lens = np.exp(rng.uniform(0, np.log(most), n)).astype(int)
+    lens[:3] = most, 0, 1
+    return rng.permutation(lens).tolist()
+
+
+@pytest.mark.parametrize("n_seq, most, heads, group, dim, window", [
+    (40, 4000, 8, 4, 128, 0), (40, 4000, 8, 1, 128, 900), (24, 5000, 8, 8, 128, 0), (90, 3000, 4, 16, 64, 0),
+    (28, 3500, 6, 12, 256, 0), (60, 2000, 6, 3, 96, 0), (40, 3000, 4, 8, 192, 0)])
+def test_attention_many_long_sequences(n_seq, most, heads, group, dim, window):
+    """Enough steps that the CTAs take stretches of all sequences' steps: shared items, whole ones, empty ones."""
+    rng = np.random.default_rng(n_seq + most)
+    lens = ragged(rng, n_seq, most)
+    cache, q, q_start, out = run_attention(rng, lens, [1] * n_seq, 64, heads, group, dim, window=window)
+    for _ in range(3):  # the same bits again
+        again = Z.attn_q4_0(cache, dev(q), dev(q_start), dev(np.array(lens, np.int32)), 1, most, window=window)
+        assert torch.equal(again, out)
+
+
+def test_attention_more_sequences_than_threads():
+    """More than 256 sequences, some with two new tokens, some with none, a bad one among them."""
+    rng = np.random.default_rng(21)
+    n_seq, heads, group, dim, page = 700, 2, 2, 128, 32
+    lens = ragged(rng, n_seq, 760)
+    new = [int(min(n, rng.integers(0, 3))) for n in lens]
+    cache, pages, table = random_cache(rng, lens, page, heads, dim)
+    q_start = np.concatenate(([0], np.cumsum(new))).astype(np.int32)
+    q = rng.standard_normal((q_start[-1], heads * group, dim)).astype(np.float32)
+    bad = next(s for s in range(300, n_seq) if new[s])
+    now = np.array(lens, np.int32)
+    now[bad] = -5
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = Z.attn_q4_0(cache, dev(q), dev(q_start), dev(now), 2, 760, status=status)
+    rows = slice(q_start[bad], q_start[bad + 1])
+    assert status.item() == 1 and out[rows].isnan().all()
+    keep = np.setdiff1d(np.arange(q_start[-1]), np.arange(rows.start, rows.stop))
+    k, v = R.values(pages, page, heads, dim)
+    want, tp, tv = R.attention(q, q_start, lens, table, k, v, page, dim ** -0.5)
+    got = out.double().cpu().numpy()
+    tol = tv * (2 * 2.0 ** -19 * tp + 2.0 ** -17)[..., None]
+    assert (np.abs(got - want) <= tol)[keep].all()
+
+
+@pytest.mark.parametrize("dim", [64, 96, 128, 192, 256])
+@pytest.mark.parametrize("new, lens, window", [([40, 3], [1200, 300], 0), ([150], [4000], 0), ([64], [64], 20)])
+def test_attention_prompts(dim, new, lens, window):
+    run_attention(np.random.default_rng(dim + sum(new)), lens, new, 48, 2, 4, dim, window=window)
+
+
 def test_attention_windows_read_no_older_page():
     """Pages wholly before the window may be gone."""
     rng = np.random.default_rng(9)
