@@ -48,6 +48,7 @@ struct AppendArgs {
     __half *k_val, *v_val;
     int32_t *status;
     uint32_t *fault;
+    int32_t head_bytes;  // of a page's head
     int64_t k_stride, v_stride, q_stride, rope_rows;
     int32_t n_tok, n_q_heads, rot_dim, halves;
 };
@@ -151,17 +152,36 @@ __device__ __forceinline__ void place_check(const AppendArgs &a, Place &w, int l
 }
 __device__ __forceinline__ float place_fill(const Place &w) { return w.bad ? __int_as_float(0x7fffffff) : 0.0f; }
 
+// Where a token's results go, found once a token: its rows of q_out, k_val and v_val, and of the cache its tile of head 0
+// (nullptr where it is not written) with its places in it.
+struct Rows {
+    float *q;
+    __half *k, *v;
+    uint8_t *tile;
+    int r;  // token of the tile
+};
+template <int NB> __device__ __forceinline__ Rows rows_of(const AppendArgs &a, const Place &w, int tok) {
+    using G = KvGeom<NB>;
+    const int64_t kv = static_cast<int64_t>(tok) * a.c.n_kv_heads * G::kDim;
+    Rows y;
+    y.q = a.q_out + static_cast<int64_t>(tok) * a.n_q_heads * G::kDim;
+    y.k = a.k_val ? a.k_val + kv : nullptr;
+    y.v = a.v_val ? a.v_val + kv : nullptr;
+    y.tile = w.ok ? a.c.pages + w.page * a.c.page_bytes + static_cast<int64_t>(w.in / kKvSlab) * G::kTileBytes : nullptr;
+    y.r = w.in % kKvSlab;
+    return y;
+}
+
 // Four dimensions e0 .. e0+3 of a (rotated) head: q's are stored; k's and v's are quantized and stored in the cache and as
 // values. The whole warp calls it: a block's 8 lanes exchange its maximum.
 template <int NB>
-__device__ __forceinline__ void put_head(const AppendArgs &a, const Place &w, int tok, int head, int e0, int lane, const float (&x)[4]) {
+__device__ __forceinline__ void put_head(const AppendArgs &a, const Rows &to, int head, int e0, int lane, const float (&x)[4]) {
     using G = KvGeom<NB>;
     const bool inside = e0 < G::kDim;
     const int kvh = head - a.n_q_heads;
     if (kvh < 0) {
         if (inside)
-            *reinterpret_cast<float4 *>(a.q_out + (static_cast<int64_t>(tok) * a.n_q_heads + head) * G::kDim + e0) =
-                make_float4(x[0], x[1], x[2], x[3]);
+            *reinterpret_cast<float4 *>(to.q + head * G::kDim + e0) = make_float4(x[0], x[1], x[2], x[3]);
         return;
     }
     const bool is_k = kvh < a.c.n_kv_heads;
@@ -188,10 +208,9 @@ __device__ __forceinline__ void put_head(const AppendArgs &a, const Place &w, in
     }
     const uint32_t upper = __shfl_down_sync(0xffffffffu, packed, 1);
     if (!inside) return;
-    const int b = e0 / kQK, g = (e0 % kQK) / 4, r = w.in % kKvSlab;
-    if (w.ok) {
-        uint8_t *tile = a.c.pages + w.page * a.c.page_bytes +
-                        static_cast<int64_t>(h * (a.c.page_tokens / kKvSlab) + w.in / kKvSlab) * G::kTileBytes;
+    const int b = e0 / kQK, g = (e0 % kQK) / 4, r = to.r;
+    if (to.tile) {
+        uint8_t *tile = to.tile + static_cast<int64_t>(h) * a.head_bytes;
         __half *scales = reinterpret_cast<__half *>(tile + (is_k ? G::kKScaleAt : G::kVScaleAt));
         if (g == 0) scales[G::scale_half(r, b)] = dh;
         if (is_k) {
@@ -200,14 +219,14 @@ __device__ __forceinline__ void put_head(const AppendArgs &a, const Place &w, in
             reinterpret_cast<uint16_t *>(tile + G::kVAt)[G::v_half(r, b, g)] = static_cast<uint16_t>(packed);
         }
     }
-    __half *val = is_k ? a.k_val : a.v_val;
+    __half *val = is_k ? to.k : to.v;
     if (!val) return;
     const float df = __half2float(dh);
     __half2 y[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i)
         y[i] = __floats2half2_rn(df * (static_cast<float>(code[2 * i]) - 8.0f), df * (static_cast<float>(code[2 * i + 1]) - 8.0f));
-    *reinterpret_cast<uint2 *>(val + (static_cast<int64_t>(tok) * a.c.n_kv_heads + h) * G::kDim + e0) = *reinterpret_cast<uint2 *>(y);
+    *reinterpret_cast<uint2 *>(val + h * G::kDim + e0) = *reinterpret_cast<uint2 *>(y);
 }
 
 // Few tokens: one warp per token and head. Lane l holds the four dimensions 4l .. 4l+3 of each pass of 128 and loads all
@@ -238,13 +257,14 @@ template <int NB, bool FAST> __global__ void __launch_bounds__(kAppendWarps * 32
     for (int p = 0; p < kPass; ++p)
         if (w.ok && turned && p * 128 + 4 * lane < a.rot_dim) turn[p] = load_turn<FAST>(a, pos, p * 128 + 4 * lane);
     place_check(a, w, lane);
+    const Rows to = rows_of<NB>(a, w, tok);
     __syncwarp();
 #pragma unroll
     for (int p = 0; p < kPass; ++p) {
         const int e0 = p * 128 + 4 * lane;
         if (!w.ok) v[p][0] = v[p][1] = v[p][2] = v[p][3] = place_fill(w);
         else if (turned && e0 < a.rot_dim) turn_head<FAST>(a, e0, turn[p], o[p], v[p]);
-        put_head<NB>(a, w, tok, head, e0, lane, v[p]);
+        put_head<NB>(a, to, head, e0, lane, v[p]);
     }
 }
 
@@ -252,7 +272,8 @@ template <int NB, bool FAST> __global__ void __launch_bounds__(kAppendWarps * 32
 // the next kStreamSlots of them on their way into its own ring in shared memory (a bulk copy a head), so that the loads
 // wait neither for the token's look-up nor for the quantization; a token's place, cosines and sines are read once and
 // kept for all its heads. 4093 tokens of 48 heads of 128: one warp a head without the ring 49 us at best (48 warps an
-// SM, each with its loads in flight for half of its life), with it 38 us (74% of the copy rate).
+// SM, each with its loads in flight for half of its life), with it 37.6 us (75% of the copy rate), then bound by issue (68%
+// active; 41 us of 154 instructions a head before the token's row addresses were found once).
 constexpr int kStreamWarps = 8, kStreamHeads = 4, kStreamSlots = 3;
 template <int NB, bool FAST> __global__ void __launch_bounds__(kStreamWarps * 32, NB <= 4 ? 3 : 2) kv_append_stream_kernel(AppendArgs a, int n_jobs) {
     using G = KvGeom<NB>;
@@ -285,10 +306,15 @@ template <int NB, bool FAST> __global__ void __launch_bounds__(kStreamWarps * 32
     int at = -1, s = 0;
     uint32_t phase = 0;
     Place w{};
+    Rows to{};
     Turn turn[kPass];
     bool ok = true;
-    for (int job = first; job < last; ++job) {
-        const int tok = a.by_groups.div(job), h0 = a.by_groups.mod(job, tok) * kStreamHeads;
+    int tok = a.by_groups.div(first), h0 = a.by_groups.mod(first, tok) * kStreamHeads;
+    for (int job = first; job < last; ++job, h0 += kStreamHeads) {
+        if (h0 >= heads) {
+            h0 = 0;
+            ++tok;
+        }
         if (tok != at) {
             at = tok;
             const int pos = a.pos[tok];
@@ -297,15 +323,17 @@ template <int NB, bool FAST> __global__ void __launch_bounds__(kStreamWarps * 32
             for (int p = 0; p < kPass; ++p)
                 if (w.ok && p * 128 + 4 * lane < a.rot_dim) turn[p] = load_turn<FAST>(a, pos, p * 128 + 4 * lane);
             place_check(a, w, lane);
+            to = rows_of<NB>(a, w, tok);
         }
         if (!__all_sync(0xffffffffu, mbar_wait(&full[s], phase))) {
             if (lane == 0) atomicOr(a.fault, 1u);
             ok = false;
         }
         const float *rows = reinterpret_cast<const float *>(ring + s * kSlotBytes);
-#pragma unroll 2
-        for (int u = 0; u < min(kStreamHeads, heads - h0); ++u) {
+#pragma unroll
+        for (int u = 0; u < kStreamHeads; ++u) {
             const int head = h0 + u;
+            if (head >= heads) break;
             const bool turned = head < a.n_q_heads + a.c.n_kv_heads;
 #pragma unroll
             for (int p = 0; p < kPass; ++p) {
@@ -318,7 +346,7 @@ template <int NB, bool FAST> __global__ void __launch_bounds__(kStreamWarps * 32
                     load_head<FAST>(a, rows + u * G::kDim, e0, turn_it, v, o);
                     if (turn_it) turn_head<FAST>(a, e0, turn[p], o, v);
                 }
-                put_head<NB>(a, w, tok, head, e0, lane, v);
+                put_head<NB>(a, to, head, e0, lane, v);
             }
         }
         __syncwarp();
@@ -397,6 +425,7 @@ zdmmv_status zdmmv_kv_append_q4_0(const zdmmv_kv_cache *cache, const zdmmv_kv_ap
         (g.q && g.q_stride % 4))
         return ZDMMV_ERR_ALIGN;
     a.by_page = FastDiv::of(cache->page_tokens);
+    a.head_bytes = cache->page_tokens / kKvSlab * 18 * cache->head_dim;
     a.k = g.k; a.v = g.v; a.q = g.q;
     a.seq = g.seq; a.pos = g.pos; a.rope = g.rope;
     a.q_out = g.q_out;
