@@ -32,8 +32,14 @@ bool attn_plan(const KvView &c, int head_dim, int n_q_heads, int max_q_len, int6
     AttnPlan p{};
     const int64_t columns = static_cast<int64_t>(max_q_len) * (n_q_heads / c.n_kv_heads);
     const int nb = kv_blocks(head_dim);
-    p.wc = columns <= 16 ? 1 : (columns <= 32 ? 2 : (columns <= 64 ? 4 : 8));
-    p.nt = p.wc == 8 ? attn_prompt_nt(nb) : (columns <= 8 ? 1 : 2);
+    p.wc = columns <= 16 ? 1 : (columns <= 32 ? 2 : (columns <= 64 ? 4 : attn_prompt_warps(nb)));
+    p.nt = p.wc > 4 ? attn_prompt_nt(nb) : (columns <= 8 ? 1 : 2);
+    if (p.wc > 4) {
+        // the fewest column tiles, the columns evenly over them
+        const int64_t tiles_of = ceil_div(columns, 8 * p.nt * p.wc);
+        p.wc = static_cast<int>(ceil_div(ceil_div(columns, tiles_of), 8 * p.nt));
+        p.prompt = true;
+    }
     p.cols = columns <= kNarrowCols ? kNarrowCols : 8 * p.nt * p.wc;
     const int64_t n_ct = ceil_div(columns, p.cols);
     p.items = static_cast<int64_t>(c.n_seq) * c.n_kv_heads * n_ct;

@@ -4,7 +4,7 @@
 //
 // A COLUMN c is one query row: a new token's head. The columns of one kv head (the
 // heads of its group times the sequence's new tokens) read the same K and V, so a
-// CTA takes 8, 16, 32 or 64 of them and streams the kv head's tiles once.
+// CTA takes 4 to 64 of them (of a prompt up to 192) and streams the kv head's tiles once.
 //
 // The arithmetic, on mma.sync m16n8k16 (fp16 in, fp32 sums):
 //  * A code n (0..15) under the bits of 1024 is the fp16 number 1024 + n, or
@@ -36,6 +36,10 @@
 // are joined at the item's end through shared memory, and an item's parts by the CTA that finishes last (through the
 // workspace). More columns (prompts): the grid is (column tile of an item) x (split of its tokens), the warps split the
 // columns and share a ring.
+//
+// What it reaches. One sequence of 130975 tokens, 8 kv heads of 128, 4 columns (the narrow kernel): 35.8 us, 62% of the
+// copy rate, of which some 12 us are the kernel's ends; at 2^20 tokens 217 us, 82%. 64 sequences of up to 16384 tokens:
+// 96.8 us (65%). The narrow kernel is bound by its instructions as much as by memory (issue 60%, ALU 46% at 131K tokens).
 #pragma once
 
 #include "zdmmv_kv.cuh"
@@ -69,6 +73,9 @@ constexpr int kStepTiles = 2 * kAttnWarps;  // tiles of a step: a ring slot for 
 enum AttnForm { kOwn = 0, kShared = 1, kPrompt = 2 };
 // Ring slots (a pair of tiles) of a CTA: two a warp; of the shared rings as many where they fit.
 __host__ __device__ constexpr int attn_slots(int nb, int form) { return form == kOwn || (form == kShared && nb < 8) ? 16 : 8; }
+// Warps of the prompt form, which are its column splits too: as many as q's fragments leave shared memory for.
+__host__ __device__ constexpr int attn_prompt_warps(int nb) { return nb <= 4 ? 12 : 8; }
+__host__ __device__ constexpr int attn_form_warps(int nb, int form) { return form == kPrompt ? attn_prompt_warps(nb) : kAttnWarps; }
 // Groups of 8 columns a warp of the prompt form: two, one where the shared memory does not hold q and the fragments of two.
 __host__ __device__ constexpr int attn_prompt_nt(int nb) { return nb < 8 ? 2 : 1; }
 // CTAs of the forms without a shared ring that run on an SM at once.
@@ -490,14 +497,13 @@ template <int NB> struct TileFeed {
 // where CTAs share the item, as a part; the CTA that comes last joins the parts, in their
 // order: out = sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s. `sum`: [warp][WCOLS][D]; m, l: [warp][WCOLS], l in the
 // common unit too.
-template <int D, int WCOLS>
-__device__ __forceinline__ void attn_store(const AttnArgs &a, const AttnSeg &seg, int cols, int wc, float *sum, const float *m,
+template <int D, int WCOLS, int WARPS>
+__device__ __forceinline__ void attn_store(const AttnArgs &a, const AttnSeg &seg, int cols, int wc, int n_wt, float *sum, const float *m,
                                            const float *l, bool bad, int *sh_last) {
-    constexpr int kThreads = kAttnThreads, kQuads = D / 4;
+    constexpr int kThreads = WARPS * 32, kQuads = D / 4;
     const int tid = threadIdx.x;
     const AttnRange &r = seg.r;
     const int ct = seg.ct, kvh = seg.kvh, n_splits = seg.parts;
-    const int n_wt = kAttnWarps / wc;
     const int live = min(cols, r.n * a.group - ct * cols);  // columns that are query rows
     if (r.bad && tid == 0 && a.status) *a.status = 1;
     const auto row = [&](int col) {
@@ -701,7 +707,7 @@ template <int NB> __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_
     const AttnRange &r = seg.r;
     const int first = seg.first, last = seg.last;
     const int n_units = (last - first + 1) / 2;   // pairs of tiles
-    // its B fragments, the upper (g even) or lower part: each warp makes an eighth of them for all
+    // its B fragments, the upper (g even) or lower part
     uint32_t qf[NB][4];
     float qs;
     {
@@ -911,7 +917,7 @@ template <int NB> __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_
             make_float4(x.x * f0, x.y * f1, y.x * f0, y.y * f1);
     }
     __syncthreads();
-    attn_store<D, kNarrowCols>(a, seg, kNarrowCols, 1, sum, &sh_m[0][0], &sh_l[0][0], r.bad || sh_bad[n_seg & 1], &sh_last);
+    attn_store<D, kNarrowCols, kWarps>(a, seg, kNarrowCols, 1, kWarps, sum, &sh_m[0][0], &sh_l[0][0], r.bad || sh_bad[n_seg & 1], &sh_last);
     if (!ahead.some) break;
     load_q<NB>(a, ahead.r, ahead.kvh, g / 2, t, v);
     __syncthreads();  // the sums are read
@@ -923,17 +929,19 @@ template <int NB> __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_
 }
 
 // The wide form: each warp 8 * NT columns. With a shared ring the warps split the columns (a.wc of them; the others the
-// ring's slots), and warp 0 feeds it half a ring ahead of itself. The prompt form (a.wc = 8): every unit's codes become
-// fp16 fragments in shared memory once, an eighth by each warp, a unit ahead of their use (one barrier a unit; converting
-// in every warp costs 144 of its 480 instructions a tile). Two warps a scheduler (O's and the products' registers allow no
-// more) keep the tensor cores 40% busy (8 cycles an m16n8k16): a 256-token chunk over 8192 takes 294 us, 114 at their rate.
-// Measured and not kept: q's fragments in registers (295), a product's sums put off behind the next block's products (295),
-// the warps drifting apart by up to two units (317), 8 columns a warp with 16 warps (445).
+// ring's slots), and warp 0 feeds it half a ring ahead of itself. The prompt form (all warps of a CTA split the columns, as
+// evenly as the fewest column tiles allow): every unit's codes become fp16 fragments in shared memory once, by all warps, a
+// unit ahead of their use (one barrier a unit; converting in every warp costs 144 of its 480 instructions a tile). Three
+// warps a scheduler up to 128 dimensions (168 registers) keep the tensor cores 43% busy (8 cycles an m16n8k16; a product
+// that waits for another 22): a 256-token chunk over 8192, 32 heads of 128, takes 292 us, 114 at their rate. Two warps with
+// 252 registers: 40%, 297 us. Measured with two and not kept: q's fragments in registers (295), a product's sums put off
+// behind the next block's products (295), the warps drifting apart by up to two units (317), 8 columns a warp with 16 warps
+// (445); with three, a block's q fragments read once for both of a unit's tiles (293).
 template <int NB, int NT, int FORM>
-__global__ void __launch_bounds__(kAttnThreads, FORM != kOwn ? 1 : attn_ctas_per_sm(NB, NT)) attn_kernel(AttnArgs a) {
+__global__ void __launch_bounds__(attn_form_warps(NB, FORM) * 32, FORM != kOwn ? 1 : attn_ctas_per_sm(NB, NT)) attn_kernel(AttnArgs a) {
     constexpr bool SHARED = FORM != kOwn, PROMPT = FORM == kPrompt;
     using G = KvGeom<NB>;
-    constexpr int kWarps = kAttnWarps, kSlots = attn_slots(NB, FORM);
+    constexpr int kWarps = attn_form_warps(NB, FORM), kSlots = attn_slots(NB, FORM);
     constexpr int D = G::kDim;
     constexpr int kSlotBytes = 2 * G::kTileBytes;
     constexpr bool kApart = attn_sums_apart(NB, NT, FORM);
@@ -972,13 +980,13 @@ __global__ void __launch_bounds__(kAttnThreads, FORM != kOwn ? 1 : attn_ctas_per
             early_page = TileFeed<NB>::page_early(a, a.c.table + static_cast<int64_t>(seq) * a.c.max_pages, early_tile);
         }
         if (!attn_grid_seg(a, cols, seg)) return;
-        if (tid == kWalker) {
+        if (tid == kWarps * 32 - 1) {
             sh_seg[0] = seg;
             sh_seg[1].some = false;
         }
     } else {
         if (!AttnWalk::begin(a, cols, sh_scan, &sh_walk)) return;
-        if (tid == kWalker) sh_walk.next(a, cols, sh_seg[0]);
+        if (tid == kWarps * 32 - 1) sh_walk.next(a, cols, sh_seg[0]);
     }
     __syncthreads();
     const uint64_t policy = l2_evict_first_policy();
@@ -1006,7 +1014,7 @@ __global__ void __launch_bounds__(kAttnThreads, FORM != kOwn ? 1 : attn_ctas_per
         }
     };
     const int g = lane >> 2, t = lane & 3;
-    const int wc = warp % a.wc, wt = warp / a.wc, n_wt = kWarps / a.wc;
+    const int wc = PROMPT ? warp : warp % a.wc, wt = PROMPT ? 0 : warp / a.wc, n_wt = PROMPT ? 1 : kWarps / a.wc;
     uint4 *q_sm = reinterpret_cast<uint4 *>(ring + kSlots * kSlotBytes) + wc * (NT * 2 * NB * 32) + lane;
     // the warps' sums [warp][column of the warp][D], behind q's fragments or over the ring
     float *sum = reinterpret_cast<float *>(kApart ? ring + kSlots * kSlotBytes + NT * 2 * NB * 512 : ring);
@@ -1049,9 +1057,10 @@ __global__ void __launch_bounds__(kAttnThreads, FORM != kOwn ? 1 : attn_ctas_per
     const int first = seg.first, last = seg.last;
     const int n_units = (last - first + 1) / 2;   // pairs of tiles, a ring slot each
     const int col0 = seg.ct * cols + wc * 8 * NT;  // the warp's first column
+    const bool idle = PROMPT && (warp >= a.wc || col0 >= r.n * a.group);  // no columns: the warp converts, and that is all
     // q's fragments: column g of each group of 8, this lane's 8 dimensions 8t.. of every block
 #pragma unroll 1
-    for (int nt = wt; nt < NT; nt += n_wt) {
+    for (int nt = wt; nt < NT && !idle; nt += n_wt) {
         float v[NB][8];
         load_q<NB>(a, r, seg.kvh, col0 + 8 * nt + g, t, v);
         float top = 0.0f;
@@ -1095,7 +1104,7 @@ __global__ void __launch_bounds__(kAttnThreads, FORM != kOwn ? 1 : attn_ctas_per
     low_max = __reduce_max_sync(0xffffffffu, low_max);
     __syncthreads();
 
-    if (!SHARED && tid == kWalker && a.n_split == 0) {
+    if (!SHARED && tid == kWarps * 32 - 1 && a.n_split == 0) {
         sh_walk.share(sh_seg[n_seg & 1]);
         sh_walk.next(a, cols, sh_seg[~n_seg & 1]);
     }
@@ -1129,6 +1138,7 @@ __global__ void __launch_bounds__(kAttnThreads, FORM != kOwn ? 1 : attn_ctas_per
             }
         }
         const uint32_t frag = frag0 + (u & 1) * kFragBytes + lane * 16;
+        if (!idle) {
         if (SHARED && !PROMPT && warp == 0) {
             for (; fed < n_units && fed <= u + kSlots / 2; ++fed) {
                 const int s = fed % kSlots;
@@ -1363,6 +1373,7 @@ __global__ void __launch_bounds__(kAttnThreads, FORM != kOwn ? 1 : attn_ctas_per
                     o[nt][2 * j + s][1] = f2_add(o[nt][2 * j + s][1], f2(c[nt][s][2], c[nt][s][3]));
                 }
         }
+        }
         __syncwarp();
         if constexpr (PROMPT) {
             __syncthreads();  // the unit's slot and fragments are free, the next one's fragments are there
@@ -1426,7 +1437,7 @@ __global__ void __launch_bounds__(kAttnThreads, FORM != kOwn ? 1 : attn_ctas_per
         }
     }
     __syncthreads();
-    attn_store<D, 8 * NT>(a, seg, cols, a.wc, sum, &sh_m[0][0], &sh_l[0][0], r.bad || sh_bad[n_seg & 1], &sh_last);
+    attn_store<D, 8 * NT, kWarps>(a, seg, cols, a.wc, n_wt, sum, &sh_m[0][0], &sh_l[0][0], r.bad || sh_bad[n_seg & 1], &sh_last);
     if (!ahead.some) break;
     __syncthreads();  // the sums and q's fragments are read
     if (tid == 0) sh_bad[n_seg & 1] = 0;
@@ -1442,6 +1453,7 @@ __global__ void __launch_bounds__(kAttnThreads, FORM != kOwn ? 1 : attn_ctas_per
 // ------------------------------------------------------------------ host side
 struct AttnPlan {
     int nt, wc;           // column groups of 8 a warp, warps that split the columns
+    bool prompt;          // the prompt form
     int n_ct, cols;       // column tiles, columns of a tile
     int64_t items;        // kv heads of sequences x column tiles
     int chunk, n_split;   // the grid's form: tiles of a split, most splits; else 0
@@ -1457,18 +1469,18 @@ extern template cudaError_t launch_attn<6>(AttnArgs, const AttnPlan &, cudaStrea
 extern template cudaError_t launch_attn<8>(AttnArgs, const AttnPlan &, cudaStream_t);
 
 #ifdef ZDMMV_ATTN_INSTANTIATE
-template <auto KERNEL> cudaError_t launch_attn_kernel(const AttnPlan &p, size_t smem, const AttnArgs &a, cudaStream_t st) {
+template <auto KERNEL, int WARPS = kAttnWarps> cudaError_t launch_attn_kernel(const AttnPlan &p, size_t smem, const AttnArgs &a, cudaStream_t st) {
     const cudaError_t e = smem_limit_raised<KERNEL>();
     if (e != cudaSuccess) return e;
     const dim3 grid = p.n_split > 0 ? dim3(static_cast<unsigned>(p.items), p.n_split) : dim3(p.ctas);
-    return launch_block_op(KERNEL, grid, dim3(kAttnThreads), kAttnBarBytes + smem, st, a);
+    return launch_block_op(KERNEL, grid, dim3(WARPS * 32), kAttnBarBytes + smem, st, a);
 }
 template <int NB, int NT, int FORM> cudaError_t launch_attn_form(const AttnArgs &a, const AttnPlan &p, cudaStream_t st) {
     const size_t ring = attn_slots(NB, FORM) * 2 * KvGeom<NB>::kTileBytes + static_cast<size_t>(p.wc) * NT * 2 * NB * 512 +
                         (FORM == kPrompt ? 2 * 8 * NB * 512 : 0);
-    const size_t sums = static_cast<size_t>(kAttnWarps) * NT * 8 * NB * kQK * 4;
+    const size_t sums = static_cast<size_t>(attn_form_warps(NB, FORM)) * NT * 8 * NB * kQK * 4;
     const size_t smem = attn_sums_apart(NB, NT, FORM) ? ring + sums : (ring > sums ? ring : sums);
-    return launch_attn_kernel<&attn_kernel<NB, NT, FORM>>(p, smem, a, st);
+    return launch_attn_kernel<&attn_kernel<NB, NT, FORM>, attn_form_warps(NB, FORM)>(p, smem, a, st);
 }
 template <int NB> cudaError_t launch_attn(AttnArgs a, const AttnPlan &p, cudaStream_t st) {
     if (p.cols == kNarrowCols) {
@@ -1476,7 +1488,7 @@ template <int NB> cudaError_t launch_attn(AttnArgs a, const AttnPlan &p, cudaStr
         constexpr size_t kSums = kAttnWarps * kNarrowCols * NB * kQK * 4;
         return launch_attn_kernel<&attn_narrow_kernel<NB>>(p, kRing + kQ + kSums, a, st);
     }
-    if (p.wc == 8) return launch_attn_form<NB, attn_prompt_nt(NB), kPrompt>(a, p, st);
+    if (p.prompt) return launch_attn_form<NB, attn_prompt_nt(NB), kPrompt>(a, p, st);
     if (p.wc > 1) return launch_attn_form<NB, 2, kShared>(a, p, st);
     return p.nt == 1 ? launch_attn_form<NB, 1, kOwn>(a, p, st) : launch_attn_form<NB, 2, kOwn>(a, p, st);
 }

@@ -668,8 +668,10 @@ typedef struct {
  * kv_len < 0, kv_len > max_kv_len or past its max_pages pages, with a page
  * number outside 0..n_pages-1 where it would read, or with more new tokens than
  * max_q_len is bad: the rows of it that the grid covers are NaN, nothing is read
- * out of range. Tokens at and past kv_len may hold anything. Deterministic from
- * call to call with the same max_q_len and max_kv_len.
+ * out of range. Tokens at and past kv_len may hold anything. The same
+ * inputs, all sequences' lengths among them, with the same max_q_len and
+ * max_kv_len give the same bits; how the work is split, and so the last bits of
+ * one sequence's result, may depend on the other sequences' lengths.
  * Errors: ERR_NULL, ERR_SHAPE, ERR_ALIGN, ERR_SIZE, ERR_CUDA. */
 #define ZDMMV_ATTN_COUNTER_BYTES 8192
 size_t zdmmv_attn_q4_0_workspace_bytes(const zdmmv_kv_cache *cache, int n_q_heads, int max_q_len,
