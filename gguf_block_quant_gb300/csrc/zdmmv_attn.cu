@@ -34,7 +34,10 @@ bool attn_plan(const KvView &c, int head_dim, int n_q_heads, int max_q_len, int6
     const int nb = kv_blocks(head_dim);
     p.wc = columns <= 16 ? 1 : (columns <= 32 ? 2 : (columns <= 64 ? 4 : attn_prompt_warps(nb)));
     p.nt = p.wc > 4 ? attn_prompt_nt(nb) : (columns <= 8 ? 1 : 2);
-    if (p.wc > 4) {
+    if (p.wc > 4 && nb <= 4) {
+        p.prompt = true;
+        p.wc = 8;
+    } else if (p.wc > 4) {
         // the fewest column tiles, the columns evenly over them
         const int64_t tiles_of = ceil_div(columns, 8 * p.nt * p.wc);
         p.wc = static_cast<int>(ceil_div(ceil_div(columns, tiles_of), 8 * p.nt));
@@ -47,6 +50,7 @@ bool attn_plan(const KvView &c, int head_dim, int n_q_heads, int max_q_len, int6
     const int64_t steps = p.items * ceil_div(tiles, kStepTiles);
     if (steps > 0x7fffffff || columns > 0x7fffff00) return false;
     p.n_ct = static_cast<int>(n_ct);
+    p.round = p.prompt && nb <= 4 ? 8 : 2;  // whole tiles of 128 tokens, whole ring slots
     const int64_t slots = static_cast<int64_t>(sms) * (p.wc > 1 ? 1 : attn_ctas_per_sm(nb, p.nt));
     if (p.wc == 1 && c.n_seq > 1 && steps > kWalkSteps * slots) {
         p.ctas = static_cast<int>(std::min<int64_t>(slots, kCounters));
@@ -60,13 +64,14 @@ bool attn_plan(const KvView &c, int head_dim, int n_q_heads, int max_q_len, int6
         if (p.wc > 1 && p.items <= kCounters) {
             // whole waves of CTAs: the split whose waves cost least, a CTA's start and end as much as kEnds tiles
             p.parts = std::min(4 * splits, ceil_div(tiles, kMinChunk));
-            const auto cost = [&](int64_t n) { return ceil_div(p.items * n, slots) * (ceil_div(tiles, n) + kEnds); };
+            const int ends = p.round == 8 ? 32 : kEnds;
+            const auto cost = [&](int64_t n) { return ceil_div(p.items * n, slots) * (ceil_div(tiles, n) + ends); };
             for (int waves = 1; waves <= 4; ++waves) {
                 const int64_t n = std::min(std::max<int64_t>(1, waves * slots / p.items), p.parts);
                 if (cost(n) < cost(most)) most = n;
             }
         }
-        p.chunk = static_cast<int>(std::max<int64_t>(kMinChunk, ceil_div(ceil_div(tiles, most), 2) * 2));  // whole ring slots
+        p.chunk = static_cast<int>(std::max<int64_t>(kMinChunk, ceil_div(ceil_div(tiles, most), p.round) * p.round));
         p.n_split = static_cast<int>(most);
         p.parts = p.parts > 1 ? p.items * p.parts : 0;
     }
@@ -132,7 +137,7 @@ zdmmv_status zdmmv_attn_q4_0(const zdmmv_kv_cache *cache, const zdmmv_attn_args 
     a.by_group = FastDiv::of(a.group);
     a.by_page_tiles = FastDiv::of(cache->page_tokens / kKvSlab);
     a.by_split = FastDiv::of(std::max(1, p.n_split));
-    a.n_ct = p.n_ct; a.n_split = p.n_split; a.chunk = p.chunk; a.wc = p.wc;
+    a.n_ct = p.n_ct; a.n_split = p.n_split; a.chunk = p.chunk; a.round = p.round; a.wc = p.wc;
     a.count = static_cast<uint32_t *>(g.workspace);
     a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(g.workspace) + ZDMMV_ATTN_COUNTER_BYTES);
     a.part_ml = reinterpret_cast<float2 *>(a.part + p.parts * p.cols * cache->head_dim);

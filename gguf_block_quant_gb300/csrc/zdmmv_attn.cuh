@@ -61,6 +61,7 @@ struct AttnArgs {
     int32_t n_tok, n_q_heads, group, max_q_len, max_kv_len, window;
     int32_t n_ct;       // column tiles of a kv head of a sequence
     int32_t n_split, chunk;  // the grid's form: most splits, tiles of a split of the longest sequence; else 0
+    int32_t round;      // ... whose length is a multiple of this power of two
     int32_t wc;         // warps that split the columns (the others split the tokens)
     float scale_log2;
 };
@@ -137,7 +138,7 @@ __device__ __forceinline__ bool attn_grid_seg(const AttnArgs &a, int cols, AttnS
     g.r = attn_range(a, g.seq, g.ct, cols);
     if (g.ct * cols >= g.r.n * a.group) return false;
     // the host's chunk is for the longest sequence that the call allows; a single one is split by its own length
-    const int chunk = a.c.n_seq > 1 ? a.chunk : max(kMinChunk, (a.by_split.div(g.r.slabs + a.n_split - 1) + 1) & ~1);
+    const int chunk = a.c.n_seq > 1 ? a.chunk : max(kMinChunk, (a.by_split.div(g.r.slabs + a.n_split - 1) + a.round - 1) & -a.round);
     g.parts = max(1, (g.r.slabs + chunk - 1) / chunk);
     if (split >= g.parts) return false;
     g.first = g.r.slab0 + split * chunk;
@@ -496,11 +497,11 @@ template <int NB> struct TileFeed {
 // The CTA's end: the warps' sums (already in the unit of their common maximum) added up, and stored as the result or,
 // where CTAs share the item, as a part; the CTA that comes last joins the parts, in their
 // order: out = sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s. `sum`: [warp][WCOLS][D]; m, l: [warp][WCOLS], l in the
-// common unit too.
-template <int D, int WCOLS, int WARPS>
+// common unit too; TURNED: column c's quads lie exchanged by c & 7.
+template <int D, int WCOLS, int WARPS, bool TURNED = false>
 __device__ __forceinline__ void attn_store(const AttnArgs &a, const AttnSeg &seg, int cols, int wc, int n_wt, float *sum, const float *m,
                                            const float *l, bool bad, int *sh_last) {
-    constexpr int kThreads = WARPS * 32, kQuads = D / 4;
+    constexpr int kThreads = WARPS * 32, kQuads = D / 4, kAhead = WARPS > 12 ? 4 : kJoinAhead;  // as registers allow
     const int tid = threadIdx.x;
     const AttnRange &r = seg.r;
     const int ct = seg.ct, kvh = seg.kvh, n_splits = seg.parts;
@@ -518,7 +519,7 @@ __device__ __forceinline__ void attn_store(const AttnArgs &a, const AttnSeg &seg
         for (int w = 0; w < n_wt; ++w) {
             const int at = (w * wc + w0) * WCOLS + wcol;
             ls += l[at];
-            const float4 x = *reinterpret_cast<const float4 *>(sum + at * D + e);
+            const float4 x = *reinterpret_cast<const float4 *>(sum + at * D + (TURNED ? e ^ 4 * (c & 7) : e));
             acc.x += x.x; acc.y += x.y; acc.z += x.z; acc.w += x.w;
         }
         if (bad) ls = __int_as_float(0x7fffffff);
@@ -547,7 +548,7 @@ __device__ __forceinline__ void attn_store(const AttnArgs &a, const AttnSeg &seg
     }
     __syncthreads();
     if (!*sh_last) return;
-    // a thread for four dimensions of a column, kJoinAhead splits' loads in flight; where that leaves threads over, groups of
+    // a thread for four dimensions of a column, kAhead splits' loads in flight; where that leaves threads over, groups of
     // them share the splits
     const int quads = live * kQuads, groups = max(1, kThreads / quads);
     float4 *grp_sum = reinterpret_cast<float4 *>(sum);  // [group][quads], then their maxima and sums of p
@@ -558,25 +559,25 @@ __device__ __forceinline__ void attn_store(const AttnArgs &a, const AttnSeg &seg
         float top = -INFINITY, ls = 0.0f;
         const int c = k / kQuads, e = 4 * (k % kQuads);
         if (k < quads && grp < groups) {
-            for (int s0 = grp; s0 < n_splits; s0 += kJoinAhead * groups) {
-                float2 ml[kJoinAhead];
-                float4 x[kJoinAhead];
+            for (int s0 = grp; s0 < n_splits; s0 += kAhead * groups) {
+                float2 ml[kAhead];
+                float4 x[kAhead];
                 float to = top;
 #pragma unroll
-                for (int i = 0; i < kJoinAhead; ++i) {
+                for (int i = 0; i < kAhead; ++i) {
                     const int s = s0 + i * groups;
                     const int64_t p = static_cast<int64_t>(seg.part(s)) * cols + c;
                     ml[i] = s < n_splits ? __ldcg(&a.part_ml[p]) : make_float2(-INFINITY, 0.0f);
                     x[i] = s < n_splits ? __ldcg(reinterpret_cast<const float4 *>(a.part + p * D + e)) : make_float4(0.f, 0.f, 0.f, 0.f);
                 }
 #pragma unroll
-                for (int i = 0; i < kJoinAhead; ++i) to = fmaxf(to, ml[i].x);
+                for (int i = 0; i < kAhead; ++i) to = fmaxf(to, ml[i].x);
                 const float keep = top == -INFINITY ? 0.0f : exp2_approx(top - to);
                 top = to;
                 ls *= keep;
                 acc.x *= keep; acc.y *= keep; acc.z *= keep; acc.w *= keep;
 #pragma unroll
-                for (int i = 0; i < kJoinAhead; ++i) {
+                for (int i = 0; i < kAhead; ++i) {
                     const float f = ml[i].x == -INFINITY ? 0.0f : exp2_approx(ml[i].x - top);
                     ls += f * ml[i].y;  // NaN where a split is bad, whatever its weight
                     acc.x += f * x[i].x; acc.y += f * x[i].y; acc.z += f * x[i].z; acc.w += f * x[i].w;
@@ -1458,10 +1459,12 @@ struct AttnPlan {
     int64_t items;        // kv heads of sequences x column tiles
     int chunk, n_split;   // the grid's form: tiles of a split, most splits; else 0
     int ctas;             // ... CTAs of the grid
+    int round;            // ... and what these are a multiple of
     int64_t parts;        // parts that the workspace holds
 };
 
 template <int NB> cudaError_t launch_attn(AttnArgs a, const AttnPlan &p, cudaStream_t st);
+template <int NB> cudaError_t launch_attn_prompt(const AttnArgs &a, const AttnPlan &p, cudaStream_t st);  // NB <= 4
 extern template cudaError_t launch_attn<2>(AttnArgs, const AttnPlan &, cudaStream_t);
 extern template cudaError_t launch_attn<3>(AttnArgs, const AttnPlan &, cudaStream_t);
 extern template cudaError_t launch_attn<4>(AttnArgs, const AttnPlan &, cudaStream_t);
@@ -1488,7 +1491,11 @@ template <int NB> cudaError_t launch_attn(AttnArgs a, const AttnPlan &p, cudaStr
         constexpr size_t kSums = kAttnWarps * kNarrowCols * NB * kQK * 4;
         return launch_attn_kernel<&attn_narrow_kernel<NB>>(p, kRing + kQ + kSums, a, st);
     }
-    if (p.prompt) return launch_attn_form<NB, attn_prompt_nt(NB), kPrompt>(a, p, st);
+    if constexpr (NB <= 4) {
+        if (p.prompt) return launch_attn_prompt<NB>(a, p, st);
+    } else {
+        if (p.prompt) return launch_attn_form<NB, attn_prompt_nt(NB), kPrompt>(a, p, st);
+    }
     if (p.wc > 1) return launch_attn_form<NB, 2, kShared>(a, p, st);
     return p.nt == 1 ? launch_attn_form<NB, 1, kOwn>(a, p, st) : launch_attn_form<NB, 2, kOwn>(a, p, st);
 }

@@ -1,0 +1,508 @@
+// zdmmv_attn_prompt.cuh -- attention of many columns (prompts) over the paged 4-bit
+// cache, heads of up to 128 dimensions, on the fifth-generation tensor cores
+// (zdmmv_attn.cuh has the formula, the columns and the join of parts).
+//
+// A CTA takes 128 columns of a kv head (the 128 rows of tcgen05.mma's D) and runs
+// over its split's tokens in tiles of 128:
+//   S = Q K^T, p = exp2(S - max) in registers, O = P V, out += O
+//  * Operands are fp16, each in two parts that hold it to 22 bits (q, p) or exactly
+//    (k = d (n - 8): 11 + 4 bits): three products hi hi + lo hi + hi lo, the fourth
+//    being below 2^-22 of the first.
+//  * Q and P are A operands in tensor memory, K and V B operands in shared memory
+//    (128-byte swizzle; K by rows of its dimensions, V transposed by the hardware).
+//    Tensor memory's 512 columns: Q 128, two tiles of S 256 (P takes S's place, 16
+//    tokens' two parts over their 16 sums), O 128.
+//  * O leaves tensor memory after every tile and is added up in fp32 registers: the
+//    tensor cores truncate where they add, which 24 additions a tile do not show,
+//    but those of thousands of tokens would.
+//
+// Warps 0-7 take the softmax and the sums: a thread has 64 of a tile's tokens of a row, whose maximum the row's two threads
+// exchange, and half of the row's output. Warps 8-15 turn the cache's codes into operands, three of which fit shared memory,
+// in the order S0 S1 O0 S2 O1 S3 ..., and a thread of warp 16 starts the products S, one of warp 19 the products O
+// (two, for one that waits and starts in turn leaves the tensor cores idle for a third of the time: starting blocks while
+// they are a few products behind). Warp 17 copies the cache's
+// tiles three operands ahead, warp 18 looks over their scales.
+#pragma once
+
+#include "zdmmv_attn.cuh"
+
+namespace zdmmv {
+
+constexpr int kPromptThreads = 640, kPromptRows = 128, kPromptTokens = 128, kPromptSlots = 3, kPromptRaw = 3;
+constexpr int kPromptSlabs = kPromptTokens / kKvSlab;
+// Registers a thread: what the kernel is launched with (20 warps share 65536) is shared out again, 8 warps of softmax, 8 that
+// feed, 4 of which one starts the products.
+constexpr int kRegsLaunch = 96, kRegsSoft = 160, kRegsFeed = 56, kRegsStart = 48;
+static_assert(8 * kRegsSoft + 8 * kRegsFeed + 4 * kRegsStart <= 20 * kRegsLaunch, "more would wait for ever");
+// tensor memory columns
+constexpr uint32_t kTmCols = 512, kTmS = 128, kTmO = 384;
+// barriers: Q is in tensor memory; by half (tile & 1): S is made, P is stored, O is made; O is read; by slot: the operand is
+// converted, its products are done; by place of the cache's tiles: copied, looked over, converted; all products are done
+constexpr int kWaitQ = 0, kWaitS = 1, kWaitP = 3, kWaitO = 5, kWaitFree = 7, kWaitFull = 8, kWaitSlot = 11, kWaitCopy = 14,
+              kWaitRaw = 17, kWaitRawFree = 20, kWaitEnd = 23, kPromptBars = 24;
+
+template <int NB> struct PromptGeom {
+    static constexpr int kChunks = (NB + 1) / 2;                          // of 64 dimensions
+    static constexpr uint32_t kChunkBytes = kPromptTokens * 128;          // 64 dimensions of a tile
+    static constexpr uint32_t kPartBytes = kChunks * kChunkBytes;         // upper or lower parts
+    static constexpr uint32_t kSlotBytes = 2 * kPartBytes;
+    static constexpr size_t kSmem = kPromptSlots * kSlotBytes + kPromptRaw * 8 * 9 * NB * kQK + 1024;  // aligned to 1024
+    static_assert(kPromptRows * NB * kQK * 4 <= kPromptSlots * kSlotBytes, "the sums lie over the slots");
+};
+
+// ------------------------------------------------------------------ tensor memory
+__device__ __forceinline__ void tm_alloc(uint32_t *to) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(to)), "n"(kTmCols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+}
+__device__ __forceinline__ void tm_free(uint32_t at) {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(at), "n"(kTmCols));
+}
+__device__ __forceinline__ void tm_before_sync() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tm_after_sync() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tm_stored() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// 16 columns of the warp's 32 rows: word i of a lane is its row's column i. The words are there after tm_loaded().
+__device__ __forceinline__ void tm_load(uint32_t at, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+          "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(at)
+        : "memory");
+}
+// ... (each array's words depend on it, so that none is used before)
+template <int N> __device__ __forceinline__ void tm_loaded(uint32_t (&r)[N][16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+        asm volatile("" : "+r"(r[k][0]), "+r"(r[k][1]), "+r"(r[k][2]), "+r"(r[k][3]), "+r"(r[k][4]), "+r"(r[k][5]), "+r"(r[k][6]),
+                          "+r"(r[k][7]), "+r"(r[k][8]), "+r"(r[k][9]), "+r"(r[k][10]), "+r"(r[k][11]), "+r"(r[k][12]), "+r"(r[k][13]),
+                          "+r"(r[k][14]), "+r"(r[k][15]));
+}
+__device__ __forceinline__ void tm_store(uint32_t at, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(
+            r[0]),
+        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
+        "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(at)
+        : "memory");
+}
+__device__ __forceinline__ void tm_store4(uint32_t at, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%4], {%0, %1, %2, %3};" ::"r"(x), "r"(y), "r"(z), "r"(w), "r"(at) : "memory");
+}
+// D (128 x N, tensor memory) = A (128 x 16 fp16, tensor memory) B (16 x N fp16, shared memory), plus D if `more`
+__device__ __forceinline__ void tm_mma(uint32_t d, uint32_t a, uint64_t b, uint32_t kind, uint32_t more) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a),
+        "l"(b), "r"(kind), "r"(more)
+        : "memory");
+}
+// an arrival on `bar` when the products started so far are done
+__device__ __forceinline__ void tm_commit(uint64_t *bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+// A B operand in rows of 128 bytes, swizzled by 128 bytes, 8 rows a group of 1024 bytes; for one that is transposed, `lead`
+// is the distance of its chunks of 64 columns.
+__device__ __forceinline__ uint64_t tm_operand(uint32_t at, uint32_t lead) {
+    return static_cast<uint64_t>((at >> 4) & 0x3FFFu) | static_cast<uint64_t>(lead >> 4) << 16 | 64ull << 32 | 1ull << 46 | 2ull << 61;
+}
+// fp16 operands, fp32 sums, 128 rows, n columns; transposed: B's rows are the summed index
+__host__ __device__ constexpr uint32_t tm_kind(int n, bool transposed) {
+    return 1u << 4 | (transposed ? 1u << 16 : 0u) | static_cast<uint32_t>(n / 8) << 17 | (kPromptRows / 16) << 24;
+}
+
+// ------------------------------------------------------------------ the cache's operands
+// Operand i of n tiles' 2 n: K0 K1 V0 K2 V1 ... K(n-1) V(n-2) V(n-1). A warp of 8-15 has a cache tile (16 tokens) of each.
+template <int NB> struct PromptFeed {
+    using G = KvGeom<NB>;
+    static constexpr uint32_t kRawBytes = G::kCodeBytes + G::kScaleBytes;  // a cache tile's K or V
+    static_assert(kPromptRaw == kPromptSlots && kPromptRaw * 2 == 6, "operand i's place is its slot; its unit lives for two turns");
+
+    __device__ static bool is_v(int i, int n) { return i == 2 * n - 1 || (i > 0 && !(i & 1)); }
+    __device__ static int tile(int i, int n) { return i == 2 * n - 1 ? n - 1 : (i == 0 ? 0 : ((i & 1) ? (i + 1) / 2 : i / 2 - 1)); }
+    // the token of an octet that this lane's words become a row of
+    __device__ static int token(int lane, bool v) { return v ? 2 * (lane & 3) + (lane >> 2 & 1) : lane >> 2; }
+    // 8 codes times d: the upper parts to `at`, the lower ones behind them. Order: dimensions 0 4 1 5 2 6 3 7.
+    __device__ static void put(uint32_t w, uint32_t d, uint32_t magic, uint32_t at) {
+        constexpr uint32_t kM1032 = 0xE408E408u, kM72 = 0xD480D480u, k16th = 0x2C002C00u;
+        const uint32_t w8 = w >> 8;
+        uint32_t n[4], lo[4];
+        n[0] = h2_add((w & 0x000F000Fu) | magic, kM1032);
+        n[1] = h2_fma((w & 0x00F000F0u) | magic, k16th, kM72);
+        n[2] = h2_add((w8 & 0x000F000Fu) | magic, kM1032);
+        n[3] = h2_fma((w8 & 0x00F000F0u) | magic, k16th, kM72);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t hi = h2_mul(n[k], d);
+            lo[k] = h2_fma(n[k], d, h2_neg(hi));
+            n[k] = hi;
+        }
+        sts128(at, n[0], n[1], n[2], n[3]);
+        sts128(at + PromptGeom<NB>::kPartBytes, lo[0], lo[1], lo[2], lo[3]);
+    }
+    // Octet u of the cache tile at `raw` becomes rows row0 .. row0+7 of the operand at `slot`; rows from `live` on are no
+    // tokens and become zeros, whatever the cache holds there.
+    template <bool V> __device__ static void convert(uint32_t raw, int u, uint32_t slot, int row0, int live, bool shrink, uint32_t magic, int lane) {
+        const int tok = token(lane, V), row = row0 + tok, t8 = V ? lane >> 3 : lane & 3;
+        const uint32_t pick = row >= live ? 0x4444u : ((tok & 1) ? 0x3232u : 0x1010u);
+        uint32_t w[NB], d[NB];
+        lds_words<NB, G::kVec>(raw + (u * NB * 32 + lane * G::kVec) * 4, 128 * G::kVec, w);
+        lds_words<NB, G::kVec>(raw + G::kCodeBytes + (4 * u + (tok >> 1)) * NB * 4, 4 * G::kVec, d);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            d[b] = __byte_perm(d[b], 0, pick);
+            if (V) {  // two tokens of 4 dimensions: the neighbour's for one token of 8
+                const uint32_t o = __shfl_xor_sync(0xffffffffu, w[b], 4);
+                w[b] = __byte_perm(w[b], o, (lane & 4) ? 0x3276 : 0x5410);
+            }
+        }
+        if (shrink)
+#pragma unroll
+            for (int b = 0; b < NB; ++b) d[b] = h2_mul(d[b], 0x2C002C00u);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            // K: odd rows begin with the other block of a chunk, so that 8 lanes' stores meet 8 different banks
+            const int o = (b ^ 1) < NB ? b ^ 1 : b;
+            const bool other = !V && o != b && (row & 1);
+            const uint32_t x = other ? w[o] : w[b], y = other ? d[o] : d[b];
+            const int c = (((b & 1) ^ (other ? 1 : 0)) * 4 + t8) ^ (row & 7);
+            put(x, y, magic, slot + (b >> 1) * PromptGeom<NB>::kChunkBytes + row * 128 + c * 16);
+        }
+    }
+    // Whether a scale of a live token of the 8 cache tiles at `raw` is 2^13 or more, so that 8 d is no fp16 number: its
+    // exponent's upper three bits are set.
+    __device__ static bool large(uint32_t raw, int live, int lane) {
+        uint32_t any = 0;
+#pragma unroll
+        for (int w = 0; w < 8; ++w)
+            for (int k = lane; k < 8 * NB; k += 32) {
+                const uint32_t d = lds32(raw + w * kRawBytes + G::kCodeBytes + k * 4);
+                const int tok = 16 * w + 2 * (k / NB);
+                any |= d & d << 1 & d << 2 & ((tok < live ? 0x4000u : 0u) | (tok + 1 < live ? 0x40000000u : 0u));
+            }
+        return __any_sync(0xffffffffu, any != 0);
+    }
+};
+
+template <int NB> __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(AttnArgs a) {
+    using G = KvGeom<NB>;
+    using P = PromptGeom<NB>;
+    constexpr int D = G::kDim;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ __align__(8) uint64_t bar[kPromptBars];
+    __shared__ float sh_top[2][2][kPromptRows], sh_m[kPromptRows], sh_l[2][kPromptRows], sh_unit[6], sh_made[2][4];
+    __shared__ int sh_bad, sh_last;
+    __shared__ uint32_t sh_tm, sh_magic;
+    __shared__ AttnSeg sh_seg;
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, half = warp >> 2;
+    if (tid == 0) {
+        for (int k = 0; k < kPromptBars; ++k) {
+            const bool rows = k == kWaitQ || k == kWaitP || k == kWaitP + 1 || k == kWaitFree;  // warps 0-7
+            const bool each = (k >= kWaitFull && k < kWaitSlot) || (k >= kWaitRawFree && k < kWaitEnd);  // warps 8-15
+            // the products and their unit; both kinds of products
+            const bool both = k == kWaitS || k == kWaitS + 1 || k == kWaitO || k == kWaitO + 1 || k == kWaitEnd;
+            mbar_init(&bar[k], rows ? 2 * kPromptRows : (each ? 8 : (both ? 2 : 1)));
+        }
+        sh_bad = 0;
+        sh_magic = kCodeMagic;
+        fence_barrier_init();
+    }
+    block_op_wait();
+    block_op_release();
+    {
+        AttnSeg seg;
+        if (!attn_grid_seg(a, kPromptRows, seg)) return;
+        if (tid == 0) sh_seg = seg;
+    }
+    if (warp == 16) tm_alloc(&sh_tm);
+    tm_before_sync();
+    __syncthreads();
+    tm_after_sync();
+    const AttnSeg &seg = sh_seg;
+    const AttnRange &r = seg.r;
+    const uint32_t tm = sh_tm;
+    const uint32_t slots = (smem_addr(smem) + 1023u) & ~1023u;
+    float *sum = reinterpret_cast<float *>(smem + (slots - smem_addr(smem)));
+    uint8_t *raws = reinterpret_cast<uint8_t *>(sum) + kPromptSlots * P::kSlotBytes;  // [place][8] cache tiles' K or V
+    const int first = seg.first, last = seg.last, limit = min(r.len, last * kKvSlab);
+    const int n = (last - first + kPromptSlabs - 1) / kPromptSlabs;
+    bool dead = false;  // a wait gave up: no more waits, but every barrier of threads is met
+    const auto wait = [&](int which, uint32_t parity) {
+        if (!dead && !mbar_wait(&bar[which], parity)) {
+            atomicOr(a.fault, 1u);
+            dead = true;
+        }
+    };
+
+    if (warp >= 16) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsStart));
+        if ((warp == 16 || warp == 19) && lane == 0) {
+            const bool v = warp == 19;
+            const uint32_t kind = v ? tm_kind(D, true) : tm_kind(kPromptTokens, false);
+            const int steps = (v ? kPromptTokens : D) / 16;
+            if (!v) wait(kWaitQ, 0);
+#pragma unroll 1
+            for (int tile = 0; tile < n; ++tile) {
+                const int i = v ? (tile == n - 1 ? 2 * n - 1 : 2 * tile + 2) : (tile == 0 ? 0 : 2 * tile - 1);
+                const int s = i % kPromptSlots, b = tile & 1;
+                if (v) {
+                    wait(kWaitP + b, tile >> 1 & 1);
+                    if (tile > 0) wait(kWaitFree, (tile - 1) & 1);
+                } else if (tile > 1) {
+                    wait(kWaitO + b, (tile - 2) >> 1 & 1);  // S takes the place of P two tiles before
+                }
+                wait(kWaitFull + s, i / kPromptSlots & 1);
+                if (dead) break;
+                tm_after_sync();
+                uint64_t *made = &bar[(v ? kWaitO : kWaitS) + b];
+                sh_made[v][tile & 3] = sh_unit[i % 6];
+                mbar_arrive(made);
+                const uint32_t half_at = tm + kTmS + b * kPromptTokens, from = v ? half_at : tm, to = v ? tm + kTmO : half_at;
+                const uint64_t b0 = tm_operand(slots + s * P::kSlotBytes, P::kChunkBytes);
+#pragma unroll 1
+                for (int k = 0; k < steps; ++k) {
+                    const uint64_t at = b0 + ((v ? k * 2048u : (k >> 2) * P::kChunkBytes + (k & 3) * 32u) >> 4);
+                    tm_mma(to, from + 16 * k, at, kind, k > 0);
+                    tm_mma(to, from + 16 * k + 8, at, kind, 1);
+                    tm_mma(to, from + 16 * k, at + (P::kPartBytes >> 4), kind, 1);
+                }
+                tm_commit(made);
+                tm_commit(&bar[kWaitSlot + s]);
+            }
+            // the products that were started are done before their operands' and sums' memory is another's
+            tm_commit(&bar[kWaitEnd]);
+            if (!mbar_wait(&bar[kWaitEnd], 0)) atomicOr(a.fault, 1u);
+        }
+        if (warp == 17) {  // the cache's tiles, a lane each of an operand's 8
+            const int32_t *table = a.c.table + static_cast<int64_t>(seg.seq) * a.c.max_pages;
+            const uint8_t *head = a.c.pages + static_cast<int64_t>(seg.kvh) * static_cast<int>(a.by_page_tiles.d) * G::kTileBytes;
+            const uint64_t policy = l2_evict_first_policy();
+            int i = 0;
+#pragma unroll 1
+            for (; i < 2 * n; ++i) {
+                const int s = i % kPromptRaw, slab = first + PromptFeed<NB>::tile(i, n) * kPromptSlabs + lane;
+                const bool v = PromptFeed<NB>::is_v(i, n), in = lane < kPromptSlabs && slab < last;
+                int page = in ? TileFeed<NB>::page_at(a, table, slab) : 0;
+                if (in && (page < 0 || page >= a.c.n_pages)) {
+                    sh_bad = 1;
+                    if (a.status) *a.status = 1;
+                    page = 0;
+                }
+                const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, in)) * PromptFeed<NB>::kRawBytes;
+                if (i >= kPromptRaw) wait(kWaitRawFree + s, (i / kPromptRaw - 1) & 1);
+                if (__any_sync(0xffffffffu, dead)) break;
+                if (lane == 0) mbar_arrive_expect_tx(&bar[kWaitCopy + s], bytes);
+                __syncwarp();
+                if (in) {
+                    const uint8_t *src = head + page * a.c.page_bytes +
+                                         static_cast<int64_t>(a.by_page_tiles.mod(slab, a.by_page_tiles.div(slab))) * G::kTileBytes;
+                    uint8_t *to = raws + (s * 8 + lane) * PromptFeed<NB>::kRawBytes;
+                    bulk_copy_g2s(to, src + (v ? G::kVAt : 0), G::kCodeBytes, &bar[kWaitCopy + s], policy);
+                    bulk_copy_g2s(to + G::kCodeBytes, src + (v ? G::kVScaleAt : G::kKScaleAt), G::kScaleBytes, &bar[kWaitCopy + s], policy);
+                }
+            }
+            // leave only when the copies have landed (after a wait that gave up: as far as they will)
+            for (int k = max(0, i - kPromptRaw); k < i; ++k) (void)mbar_wait(&bar[kWaitCopy + k % kPromptRaw], k / kPromptRaw & 1);
+        }
+        if (warp == 18) {  // ... and their unit: 1, or 16 where a scale is too large
+#pragma unroll 1
+            for (int i = 0; i < 2 * n; ++i) {
+                const int s = i % kPromptRaw, tile = PromptFeed<NB>::tile(i, n);
+                wait(kWaitCopy + s, i / kPromptRaw & 1);
+                __syncwarp();
+                const bool large = PromptFeed<NB>::large(smem_addr(raws) + s * 8 * PromptFeed<NB>::kRawBytes,
+                                                         limit - first * kKvSlab - tile * kPromptTokens, lane);
+                if (lane == 0) {
+                    sh_unit[i % 6] = large ? 16.0f : 1.0f;
+                    mbar_arrive(&bar[kWaitRaw + s]);
+                }
+            }
+        }
+        __syncwarp();
+        __syncthreads();
+    } else if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFeed));
+        const int w = warp - 8;
+        const uint32_t magic = lds32(smem_addr(&sh_magic));
+        using F = PromptFeed<NB>;
+#pragma unroll 1
+        for (int i = 0; i < 2 * n; ++i) {
+            const int s = i % kPromptSlots, tile = F::tile(i, n), live = limit - first * kKvSlab - tile * kPromptTokens;
+            const uint32_t slot = slots + s * P::kSlotBytes, raw = smem_addr(raws) + (s * 8 + w) * F::kRawBytes;
+            wait(kWaitRaw + s, i / kPromptRaw & 1);
+            if (i >= kPromptSlots) wait(kWaitSlot + s, (i / kPromptSlots - 1) & 1);
+            __syncwarp();
+            const bool shrink = sh_unit[i % 6] != 1.0f;
+            if (F::is_v(i, n)) {
+#pragma unroll
+                for (int u = 0; u < 2; ++u) F::template convert<true>(raw, u, slot, 16 * w + 8 * u, live, shrink, magic, lane);
+            } else {
+#pragma unroll
+                for (int u = 0; u < 2; ++u) F::template convert<false>(raw, u, slot, 16 * w + 8 * u, live, shrink, magic, lane);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&bar[kWaitFull + s]);
+                mbar_arrive(&bar[kWaitRawFree + s]);
+            }
+        }
+        __syncthreads();
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
+        const int row = tid & (kPromptRows - 1), col = seg.ct * kPromptRows + row;
+        const uint32_t rows = tm + (static_cast<uint32_t>(warp & 3) << 21);  // the warp's 32 rows
+        const int i = a.by_group.div(col);
+        const bool valid = i < r.n;
+        float qs;
+        {  // half of the row of Q
+            const float *q = a.q + static_cast<int64_t>(r.q0 + (valid ? i : 0)) * a.q_stride +
+                             static_cast<int64_t>(seg.kvh * a.group + (valid ? col - i * a.group : 0)) * D + half * (D / 2);
+            float4 x[D / 8];
+#pragma unroll
+            for (int e = 0; e < D / 8; ++e)
+                x[e] = valid ? *reinterpret_cast<const float4 *>(q + 4 * e) : make_float4(0.f, 0.f, 0.f, 0.f);
+            float top = 0.0f;
+#pragma unroll
+            for (int e = 0; e < D / 8; ++e)
+                top = fmaxf(fmaxf(fmaxf(top, fabsf(x[e].x)), fmaxf(fabsf(x[e].y), fabsf(x[e].z))), fabsf(x[e].w));
+            sh_top[1][half][row] = top;
+            asm volatile("barrier.cta.sync 2, 256;" ::: "memory");
+            top = fmaxf(top, sh_top[1][half ^ 1][row]);
+            float up, down;
+            q_unit(top, a.scale_log2, up, down);
+            qs = fmaxf(fabsf(a.scale_log2) * down, 1e-37f);
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {  // 8 dimensions
+                uint32_t f[8];
+                const float4 y = x[2 * k], z = x[2 * k + 1];
+                split_h2(y.x * up, z.x * up, f[0], f[4]);
+                split_h2(y.y * up, z.y * up, f[1], f[5]);
+                split_h2(y.z * up, z.z * up, f[2], f[6]);
+                split_h2(y.w * up, z.w * up, f[3], f[7]);
+                const int e = half * (D / 16) + k;  // of the row's D / 8
+                tm_store4(rows + 16 * (e >> 1) + 4 * (e & 1), f[0], f[1], f[2], f[3]);
+                tm_store4(rows + 16 * (e >> 1) + 8 + 4 * (e & 1), f[4], f[5], f[6], f[7]);
+            }
+            tm_stored();
+            tm_before_sync();
+            mbar_arrive(&bar[kWaitQ]);
+        }
+        const int seen = max(0, r.len - (r.n - 1 - i));
+        const int end = valid ? min(limit, seen) : limit, low = valid && a.window > 0 ? max(0, seen - a.window) : 0;
+        float m = -INFINITY, keep = 0.0f;
+        constexpr int kLoads = D / 32;  // of 16 of the thread's D / 2 dimensions
+        uint64_t l2 = 0, acc[D / 4];    // acc[4 g + k]: dimensions 8 g + k and 8 g + 4 + k of its half
+#pragma unroll
+        for (int k = 0; k < D / 4; ++k) acc[k] = 0;
+        const auto drain = [&](int tile) {  // the sums of a tile
+            wait(kWaitO + (tile & 1), tile >> 1 & 1);
+            __syncwarp();
+            tm_after_sync();
+            const float unit = sh_made[1][tile & 3];
+            uint32_t o[kLoads][16];
+#pragma unroll
+            for (int c = 0; c < kLoads; ++c) tm_load(rows + kTmO + half * (D / 2) + 16 * c, o[c]);
+            tm_loaded(o);
+            tm_before_sync();
+            mbar_arrive(&bar[kWaitFree]);
+            const uint64_t keep2 = f2(keep, keep), unit2 = f2(unit, unit);
+#pragma unroll
+            for (int c = 0; c < kLoads; ++c)
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    acc[8 * c + k] = f2_fma(acc[8 * c + k], keep2, f2_mul(f2(__uint_as_float(o[c][2 * k]), __uint_as_float(o[c][2 * k + 1])), unit2));
+        };
+#pragma unroll 1
+        for (int tile = 0; tile < n; ++tile) {
+            const uint32_t at = rows + kTmS + (tile & 1) * kPromptTokens + half * (kPromptTokens / 2);
+            const int t0 = first * kKvSlab + tile * kPromptTokens + half * (kPromptTokens / 2);
+            wait(kWaitS + (tile & 1), tile >> 1 & 1);
+            __syncwarp();
+            tm_after_sync();
+            const float unit = qs * sh_made[0][tile & 3];
+            uint32_t s[4][16];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tm_load(at + 16 * c, s[c]);
+            tm_loaded(s);
+            if (__any_sync(0xffffffffu, t0 < low || t0 + kPromptTokens / 2 > end)) {
+#pragma unroll
+                for (int k = 0; k < 64; ++k)
+                    if (t0 + k < low || t0 + k >= end) s[k / 16][k % 16] = 0xff800000u;
+            }
+            float top = -INFINITY, top1 = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < 64; k += 4) {
+                top = fmaxf(fmaxf(top, __uint_as_float(s[k / 16][k % 16])), __uint_as_float(s[k / 16][k % 16 + 1]));
+                top1 = fmaxf(fmaxf(top1, __uint_as_float(s[k / 16][k % 16 + 2])), __uint_as_float(s[k / 16][k % 16 + 3]));
+            }
+            top = fmaxf(top, top1) * unit;
+            sh_top[tile & 1][half][row] = top;
+            asm volatile("barrier.cta.sync 2, 256;" ::: "memory");
+            const float to = fmaxf(m, fmaxf(top, sh_top[tile & 1][half ^ 1][row]));
+            const float then = m == -INFINITY ? 0.0f : exp2_approx(m - to);
+            m = to;
+            const float shift = to == -INFINITY ? 0.0f : kAttnUnit - to;
+            const uint64_t unit2 = f2(unit, unit), shift2 = f2(shift, shift);
+            l2 = f2_mul(l2, f2(then, then));
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint32_t f[16];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const uint64_t x = f2_fma(f2(__uint_as_float(s[c][2 * k]), __uint_as_float(s[c][2 * k + 1])), unit2, shift2);
+                    const float2 v = f2_parts(x);
+                    const uint64_t p = f2(exp2_approx(v.x), exp2_approx(v.y));
+                    l2 = f2_add(l2, p);
+                    split_f2(p, f[k], f[8 + k]);
+                }
+                tm_store(at + 16 * c, f);
+            }
+            tm_stored();
+            tm_before_sync();
+            mbar_arrive(&bar[kWaitP + (tile & 1)]);
+            if (tile > 0) drain(tile - 1);
+            keep = then;
+        }
+        if (n > 0) drain(n - 1);
+        const float2 ls = f2_parts(l2);
+        sh_l[half][row] = ls.x + ls.y;
+        __syncthreads();  // the products are done; their operands' memory takes the sums
+        if (half == 0) {
+            sh_m[row] = m;
+            sh_l[0][row] += sh_l[1][row];
+        }
+        float *mine = sum + row * D;
+#pragma unroll
+        for (int g = 0; g < D / 16; ++g) {
+            float2 x[4];
+            const int quad = half * (D / 8) + 2 * g;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) x[k] = f2_parts(acc[4 * g + k]);
+            *reinterpret_cast<float4 *>(mine + 4 * (quad ^ (row & 7))) = make_float4(x[0].x, x[1].x, x[2].x, x[3].x);
+            *reinterpret_cast<float4 *>(mine + 4 * ((quad + 1) ^ (row & 7))) = make_float4(x[0].y, x[1].y, x[2].y, x[3].y);
+        }
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLaunch));
+    }
+    if (warp >= 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsLaunch));  // waits for warps 0-7 to give theirs back, which wait for nothing
+    tm_before_sync();
+    __syncthreads();
+    tm_after_sync();
+    if (warp == 16) tm_free(tm);
+    attn_store<D, kPromptRows, kPromptThreads / 32, true>(a, seg, kPromptRows, 1, 1, sum, sh_m, &sh_l[0][0], r.bad || sh_bad, &sh_last);
+}
+
+template <int NB> cudaError_t launch_attn_prompt(const AttnArgs &a, const AttnPlan &p, cudaStream_t st) {
+    const cudaError_t e = smem_limit_raised<&attn_prompt_kernel<NB>>();
+    if (e != cudaSuccess) return e;
+    static const bool shares_fit = [] {  // the compiler may have launched it with fewer registers than are shared out
+        cudaFuncAttributes f{};
+        return cudaFuncGetAttributes(&f, attn_prompt_kernel<NB>) == cudaSuccess && f.numRegs == kRegsLaunch;
+    }();
+    if (!shares_fit) return cudaErrorLaunchOutOfResources;
+    return launch_block_op(&attn_prompt_kernel<NB>, dim3(static_cast<unsigned>(p.items), p.n_split), dim3(kPromptThreads),
+                           PromptGeom<NB>::kSmem, st, a);
+}
+
+}  // namespace zdmmv
