@@ -19,6 +19,7 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 constexpr int kWalkSteps = 12;
 constexpr int kRaggedChunk = 128;
 constexpr int kEnds = 8;
+constexpr int kTallEnds = 32, kTallJoin = 1;  // ... of the form on tcgen05: its start, and the join's loads of four parts for 2560 values
 constexpr int kCounters = ZDMMV_ATTN_COUNTER_BYTES / 4;
 
 bool attn_plan(const KvView &c, int head_dim, int n_q_heads, int max_q_len, int64_t max_tokens, AttnPlan *out) {
@@ -32,16 +33,16 @@ bool attn_plan(const KvView &c, int head_dim, int n_q_heads, int max_q_len, int6
     AttnPlan p{};
     const int64_t columns = static_cast<int64_t>(max_q_len) * (n_q_heads / c.n_kv_heads);
     const int nb = kv_blocks(head_dim);
-    p.wc = columns <= 16 ? 1 : (columns <= 32 ? 2 : (columns <= 64 ? 4 : attn_prompt_warps(nb)));
+    p.wc = columns <= 16 ? 1 : (columns <= 32 ? 2 : (columns <= 64 ? 4 : 8));
     p.nt = p.wc > 4 ? attn_prompt_nt(nb) : (columns <= 8 ? 1 : 2);
-    if (p.wc > 4 && nb <= 4) {
-        p.prompt = true;
+    p.tall = columns > kTallColumns && nb <= kTallBlocks;
+    if (p.tall) {  // 128 columns
         p.wc = 8;
+        p.nt = 2;
     } else if (p.wc > 4) {
         // the fewest column tiles, the columns evenly over them
         const int64_t tiles_of = ceil_div(columns, 8 * p.nt * p.wc);
         p.wc = static_cast<int>(ceil_div(ceil_div(columns, tiles_of), 8 * p.nt));
-        p.prompt = true;
     }
     p.cols = columns <= kNarrowCols ? kNarrowCols : 8 * p.nt * p.wc;
     const int64_t n_ct = ceil_div(columns, p.cols);
@@ -50,7 +51,7 @@ bool attn_plan(const KvView &c, int head_dim, int n_q_heads, int max_q_len, int6
     const int64_t steps = p.items * ceil_div(tiles, kStepTiles);
     if (steps > 0x7fffffff || columns > 0x7fffff00) return false;
     p.n_ct = static_cast<int>(n_ct);
-    p.round = p.prompt && nb <= 4 ? 8 : 2;  // whole tiles of 128 tokens, whole ring slots
+    p.round = p.tall ? 8 : 2;  // whole tiles of 128 tokens, whole ring slots
     const int64_t slots = static_cast<int64_t>(sms) * (p.wc > 1 ? 1 : attn_ctas_per_sm(nb, p.nt));
     if (p.wc == 1 && c.n_seq > 1 && steps > kWalkSteps * slots) {
         p.ctas = static_cast<int>(std::min<int64_t>(slots, kCounters));
@@ -64,8 +65,13 @@ bool attn_plan(const KvView &c, int head_dim, int n_q_heads, int max_q_len, int6
         if (p.wc > 1 && p.items <= kCounters) {
             // whole waves of CTAs: the split whose waves cost least, a CTA's start and end as much as kEnds tiles
             p.parts = std::min(4 * splits, ceil_div(tiles, kMinChunk));
-            const int ends = p.round == 8 ? 32 : kEnds;
-            const auto cost = [&](int64_t n) { return ceil_div(p.items * n, slots) * (ceil_div(tiles, n) + ends); };
+            const int64_t cols = std::min<int64_t>(columns, p.cols);
+            const auto cost = [&](int64_t n) {
+                const int64_t ends = p.tall ? kTallEnds + kTallJoin * ceil_div(cols * head_dim, 2560) * ceil_div(n, 4) : kEnds;
+                return ceil_div(p.items * n, slots) * (ceil_div(tiles, n) + ends);
+            };
+            for (int64_t n = most / 2; p.tall && n > 1; n /= 2)
+                if (cost(n) < cost(most)) most = n;
             for (int waves = 1; waves <= 4; ++waves) {
                 const int64_t n = std::min(std::max<int64_t>(1, waves * slots / p.items), p.parts);
                 if (cost(n) < cost(most)) most = n;

@@ -74,9 +74,10 @@ constexpr int kStepTiles = 2 * kAttnWarps;  // tiles of a step: a ring slot for 
 enum AttnForm { kOwn = 0, kShared = 1, kPrompt = 2 };
 // Ring slots (a pair of tiles) of a CTA: two a warp; of the shared rings as many where they fit.
 __host__ __device__ constexpr int attn_slots(int nb, int form) { return form == kOwn || (form == kShared && nb < 8) ? 16 : 8; }
-// Warps of the prompt form, which are its column splits too: as many as q's fragments leave shared memory for.
-__host__ __device__ constexpr int attn_prompt_warps(int nb) { return nb <= 4 ? 12 : 8; }
-__host__ __device__ constexpr int attn_form_warps(int nb, int form) { return form == kPrompt ? attn_prompt_warps(nb) : kAttnWarps; }
+// Heads of up to kTallBlocks blocks with more than kTallColumns columns take the form on tcgen05 (zdmmv_attn_prompt.cuh)
+// instead of the shared and the prompt form: 8 sequences of 4000 tokens with 64 columns, 8 heads of 128, 99 us with the
+// shared form and 52 with that; one of 60000 with 24 columns 88 and 77; 20 columns over 2000 16.5 and 14.6.
+constexpr int kTallBlocks = 4, kTallColumns = 16;
 // Groups of 8 columns a warp of the prompt form: two, one where the shared memory does not hold q and the fragments of two.
 __host__ __device__ constexpr int attn_prompt_nt(int nb) { return nb < 8 ? 2 : 1; }
 // CTAs of the forms without a shared ring that run on an SM at once.
@@ -931,18 +932,17 @@ template <int NB> __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_
 
 // The wide form: each warp 8 * NT columns. With a shared ring the warps split the columns (a.wc of them; the others the
 // ring's slots), and warp 0 feeds it half a ring ahead of itself. The prompt form (all warps of a CTA split the columns, as
-// evenly as the fewest column tiles allow): every unit's codes become fp16 fragments in shared memory once, by all warps, a
-// unit ahead of their use (one barrier a unit; converting in every warp costs 144 of its 480 instructions a tile). Three
-// warps a scheduler up to 128 dimensions (168 registers) keep the tensor cores 43% busy (8 cycles an m16n8k16; a product
-// that waits for another 22): a 256-token chunk over 8192, 32 heads of 128, takes 292 us, 114 at their rate. Two warps with
-// 252 registers: 40%, 297 us. Measured with two and not kept: q's fragments in registers (295), a product's sums put off
-// behind the next block's products (295), the warps drifting apart by up to two units (317), 8 columns a warp with 16 warps
-// (445); with three, a block's q fragments read once for both of a unit's tiles (293).
+// evenly as the fewest column tiles allow): every unit's codes become fp16 fragments in shared memory once, an eighth by each
+// warp, a unit ahead of their use (one barrier a unit; converting in every warp costs 144 of its 480 instructions a tile). Two
+// warps a scheduler (the output's and the products' registers allow no more) wait for each other's products (8 cycles an
+// m16n8k16, 22 one that needs the one before): with heads of 128 they kept the tensor cores 40% busy, and q's fragments in
+// registers, a product's sums put off behind the next block's products or warps that drift apart gained nothing. Heads of up
+// to 128 dimensions have a form of their own (zdmmv_attn_prompt.cuh), three times as fast.
 template <int NB, int NT, int FORM>
-__global__ void __launch_bounds__(attn_form_warps(NB, FORM) * 32, FORM != kOwn ? 1 : attn_ctas_per_sm(NB, NT)) attn_kernel(AttnArgs a) {
+__global__ void __launch_bounds__(kAttnWarps * 32, FORM != kOwn ? 1 : attn_ctas_per_sm(NB, NT)) attn_kernel(AttnArgs a) {
     constexpr bool SHARED = FORM != kOwn, PROMPT = FORM == kPrompt;
     using G = KvGeom<NB>;
-    constexpr int kWarps = attn_form_warps(NB, FORM), kSlots = attn_slots(NB, FORM);
+    constexpr int kWarps = kAttnWarps, kSlots = attn_slots(NB, FORM);
     constexpr int D = G::kDim;
     constexpr int kSlotBytes = 2 * G::kTileBytes;
     constexpr bool kApart = attn_sums_apart(NB, NT, FORM);
@@ -1454,7 +1454,7 @@ __global__ void __launch_bounds__(attn_form_warps(NB, FORM) * 32, FORM != kOwn ?
 // ------------------------------------------------------------------ host side
 struct AttnPlan {
     int nt, wc;           // column groups of 8 a warp, warps that split the columns
-    bool prompt;          // the prompt form
+    bool tall;            // the form on tcgen05
     int n_ct, cols;       // column tiles, columns of a tile
     int64_t items;        // kv heads of sequences x column tiles
     int chunk, n_split;   // the grid's form: tiles of a split, most splits; else 0
@@ -1464,7 +1464,7 @@ struct AttnPlan {
 };
 
 template <int NB> cudaError_t launch_attn(AttnArgs a, const AttnPlan &p, cudaStream_t st);
-template <int NB> cudaError_t launch_attn_prompt(const AttnArgs &a, const AttnPlan &p, cudaStream_t st);  // NB <= 4
+template <int NB> cudaError_t launch_attn_tall(const AttnArgs &a, const AttnPlan &p, cudaStream_t st);  // NB <= kTallBlocks
 extern template cudaError_t launch_attn<2>(AttnArgs, const AttnPlan &, cudaStream_t);
 extern template cudaError_t launch_attn<3>(AttnArgs, const AttnPlan &, cudaStream_t);
 extern template cudaError_t launch_attn<4>(AttnArgs, const AttnPlan &, cudaStream_t);
@@ -1472,18 +1472,18 @@ extern template cudaError_t launch_attn<6>(AttnArgs, const AttnPlan &, cudaStrea
 extern template cudaError_t launch_attn<8>(AttnArgs, const AttnPlan &, cudaStream_t);
 
 #ifdef ZDMMV_ATTN_INSTANTIATE
-template <auto KERNEL, int WARPS = kAttnWarps> cudaError_t launch_attn_kernel(const AttnPlan &p, size_t smem, const AttnArgs &a, cudaStream_t st) {
+template <auto KERNEL> cudaError_t launch_attn_kernel(const AttnPlan &p, size_t smem, const AttnArgs &a, cudaStream_t st) {
     const cudaError_t e = smem_limit_raised<KERNEL>();
     if (e != cudaSuccess) return e;
     const dim3 grid = p.n_split > 0 ? dim3(static_cast<unsigned>(p.items), p.n_split) : dim3(p.ctas);
-    return launch_block_op(KERNEL, grid, dim3(WARPS * 32), kAttnBarBytes + smem, st, a);
+    return launch_block_op(KERNEL, grid, dim3(kAttnThreads), kAttnBarBytes + smem, st, a);
 }
 template <int NB, int NT, int FORM> cudaError_t launch_attn_form(const AttnArgs &a, const AttnPlan &p, cudaStream_t st) {
     const size_t ring = attn_slots(NB, FORM) * 2 * KvGeom<NB>::kTileBytes + static_cast<size_t>(p.wc) * NT * 2 * NB * 512 +
                         (FORM == kPrompt ? 2 * 8 * NB * 512 : 0);
-    const size_t sums = static_cast<size_t>(attn_form_warps(NB, FORM)) * NT * 8 * NB * kQK * 4;
+    const size_t sums = static_cast<size_t>(kAttnWarps) * NT * 8 * NB * kQK * 4;
     const size_t smem = attn_sums_apart(NB, NT, FORM) ? ring + sums : (ring > sums ? ring : sums);
-    return launch_attn_kernel<&attn_kernel<NB, NT, FORM>, attn_form_warps(NB, FORM)>(p, smem, a, st);
+    return launch_attn_kernel<&attn_kernel<NB, NT, FORM>>(p, smem, a, st);
 }
 template <int NB> cudaError_t launch_attn(AttnArgs a, const AttnPlan &p, cudaStream_t st) {
     if (p.cols == kNarrowCols) {
@@ -1491,12 +1491,12 @@ template <int NB> cudaError_t launch_attn(AttnArgs a, const AttnPlan &p, cudaStr
         constexpr size_t kSums = kAttnWarps * kNarrowCols * NB * kQK * 4;
         return launch_attn_kernel<&attn_narrow_kernel<NB>>(p, kRing + kQ + kSums, a, st);
     }
-    if constexpr (NB <= 4) {
-        if (p.prompt) return launch_attn_prompt<NB>(a, p, st);
+    if constexpr (NB <= kTallBlocks) {
+        if (p.tall) return launch_attn_tall<NB>(a, p, st);
     } else {
-        if (p.prompt) return launch_attn_form<NB, attn_prompt_nt(NB), kPrompt>(a, p, st);
+        if (p.wc > 4) return launch_attn_form<NB, attn_prompt_nt(NB), kPrompt>(a, p, st);
+        if (p.wc > 1) return launch_attn_form<NB, 2, kShared>(a, p, st);
     }
-    if (p.wc > 1) return launch_attn_form<NB, 2, kShared>(a, p, st);
     return p.nt == 1 ? launch_attn_form<NB, 1, kOwn>(a, p, st) : launch_attn_form<NB, 2, kOwn>(a, p, st);
 }
 #endif

@@ -493,7 +493,7 @@ template <int NB> __global__ void __launch_bounds__(kPromptThreads, 1) attn_prom
     attn_store<D, kPromptRows, kPromptThreads / 32, true>(a, seg, kPromptRows, 1, 1, sum, sh_m, &sh_l[0][0], r.bad || sh_bad, &sh_last);
 }
 
-template <int NB> cudaError_t launch_attn_prompt(const AttnArgs &a, const AttnPlan &p, cudaStream_t st) {
+template <int NB> cudaError_t launch_attn_tall(const AttnArgs &a, const AttnPlan &p, cudaStream_t st) {
     const cudaError_t e = smem_limit_raised<&attn_prompt_kernel<NB>>();
     if (e != cudaSuccess) return e;
     static const bool shares_fit = [] {  // the compiler may have launched it with fewer registers than are shared out
