@@ -18,9 +18,9 @@
 //
 // Warps 0-7 take the softmax and the sums: a thread has 64 of a tile's tokens of a row, whose maximum the row's two threads
 // exchange, and half of the row's output. Warps 8-15 turn the cache's codes into operands, three of which fit shared memory,
-// in the order S0 S1 O0 S2 O1 S3 ..., and a thread of warp 16 starts the products S, one of warp 19 the products O
-// (two, for one that waits and starts in turn leaves the tensor cores idle for a third of the time: starting blocks while
-// they are a few products behind). Warp 17 copies the cache's
+// in the order S0 S1 O0 S2 O1 S3 ..., and a thread of warp 16 starts the products in that order, as soon as one
+// of warp 19 says so (starting blocks while the tensor cores are a product or two behind, and one thread that waits for all
+// of it leaves them idle for a third of the time): each softmax has the time of two operands' products. Warp 17 copies the cache's
 // tiles three operands ahead, warp 18 looks over their scales.
 #pragma once
 
@@ -37,9 +37,10 @@ static_assert(8 * kRegsSoft + 8 * kRegsFeed + 4 * kRegsStart <= 20 * kRegsLaunch
 // tensor memory columns
 constexpr uint32_t kTmCols = 512, kTmS = 128, kTmO = 384;
 // barriers: Q is in tensor memory; by half (tile & 1): S is made, P is stored, O is made; O is read; by slot: the operand is
-// converted, its products are done; by place of the cache's tiles: copied, looked over, converted; all products are done
+// converted, its products are done; by place of the cache's tiles: copied, looked over, converted; by slot:
+// its products may start; all products are done
 constexpr int kWaitQ = 0, kWaitS = 1, kWaitP = 3, kWaitO = 5, kWaitFree = 7, kWaitFull = 8, kWaitSlot = 11, kWaitCopy = 14,
-              kWaitRaw = 17, kWaitRawFree = 20, kWaitEnd = 23, kPromptBars = 24;
+              kWaitRaw = 17, kWaitRawFree = 20, kWaitGo = 23, kWaitEnd = 26, kPromptBars = 27;
 
 template <int NB> struct PromptGeom {
     static constexpr int kChunks = (NB + 1) / 2;                          // of 64 dimensions
@@ -90,12 +91,21 @@ __device__ __forceinline__ void tm_store(uint32_t at, const uint32_t (&r)[16]) {
 __device__ __forceinline__ void tm_store4(uint32_t at, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%4], {%0, %1, %2, %3};" ::"r"(x), "r"(y), "r"(z), "r"(w), "r"(at) : "memory");
 }
-// D (128 x N, tensor memory) = A (128 x 16 fp16, tensor memory) B (16 x N fp16, shared memory), plus D if `more`
-__device__ __forceinline__ void tm_mma(uint32_t d, uint32_t a, uint64_t b, uint32_t kind, uint32_t more) {
+// D (128 x N, tensor memory) = (or, if `more`, +=) the three products of A's parts (128 x 16 fp16 each, tensor memory, the
+// lower one 8 columns on) and B's (16 x N fp16 each, shared memory, the lower one `lower` on)
+template <uint32_t KIND> __device__ __forceinline__ void tm_mma3(uint32_t d, uint32_t a, uint64_t b, uint32_t lower, bool more) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a),
-        "l"(b), "r"(kind), "r"(more)
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %6, 0;\n\tsetp.eq.u32 q, %6, %6;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %3, %5, p;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%2], %3, %5, q;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %4, %5, q;\n\t}" ::"r"(d),
+        "r"(a), "r"(a + 8), "l"(b), "l"(b + lower), "r"(KIND), "r"(static_cast<uint32_t>(more))
         : "memory");
+}
+__device__ __forceinline__ bool one_lane() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
 }
 // an arrival on `bar` when the products started so far are done
 __device__ __forceinline__ void tm_commit(uint64_t *bar) {
@@ -199,9 +209,9 @@ template <int NB> __global__ void __launch_bounds__(kPromptThreads, 1) attn_prom
     if (tid == 0) {
         for (int k = 0; k < kPromptBars; ++k) {
             const bool rows = k == kWaitQ || k == kWaitP || k == kWaitP + 1 || k == kWaitFree;  // warps 0-7
-            const bool each = (k >= kWaitFull && k < kWaitSlot) || (k >= kWaitRawFree && k < kWaitEnd);  // warps 8-15
-            // the products and their unit; both kinds of products
-            const bool both = k == kWaitS || k == kWaitS + 1 || k == kWaitO || k == kWaitO + 1 || k == kWaitEnd;
+            const bool each = (k >= kWaitFull && k < kWaitSlot) || (k >= kWaitRawFree && k < kWaitGo);  // warps 8-15
+            // the products and their unit
+            const bool both = k == kWaitS || k == kWaitS + 1 || k == kWaitO || k == kWaitO + 1;
             mbar_init(&bar[k], rows ? 2 * kPromptRows : (each ? 8 : (both ? 2 : 1)));
         }
         sh_bad = 0;
@@ -237,41 +247,60 @@ template <int NB> __global__ void __launch_bounds__(kPromptThreads, 1) attn_prom
 
     if (warp >= 16) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsStart));
-        if ((warp == 16 || warp == 19) && lane == 0) {
-            const bool v = warp == 19;
-            const uint32_t kind = v ? tm_kind(D, true) : tm_kind(kPromptTokens, false);
-            const int steps = (v ? kPromptTokens : D) / 16;
-            if (!v) wait(kWaitQ, 0);
+        if (warp == 19 && lane == 0) {  // says when the products may start
+            wait(kWaitQ, 0);
 #pragma unroll 1
-            for (int tile = 0; tile < n; ++tile) {
-                const int i = v ? (tile == n - 1 ? 2 * n - 1 : 2 * tile + 2) : (tile == 0 ? 0 : 2 * tile - 1);
-                const int s = i % kPromptSlots, b = tile & 1;
+            for (int i = 0; i < 2 * n; ++i) {
+                const int s = i % kPromptSlots, tile = PromptFeed<NB>::tile(i, n), b = tile & 1;
+                const bool v = PromptFeed<NB>::is_v(i, n);
                 if (v) {
                     wait(kWaitP + b, tile >> 1 & 1);
                     if (tile > 0) wait(kWaitFree, (tile - 1) & 1);
-                } else if (tile > 1) {
-                    wait(kWaitO + b, (tile - 2) >> 1 & 1);  // S takes the place of P two tiles before
                 }
                 wait(kWaitFull + s, i / kPromptSlots & 1);
                 if (dead) break;
                 tm_after_sync();
-                uint64_t *made = &bar[(v ? kWaitO : kWaitS) + b];
                 sh_made[v][tile & 3] = sh_unit[i % 6];
-                mbar_arrive(made);
-                const uint32_t half_at = tm + kTmS + b * kPromptTokens, from = v ? half_at : tm, to = v ? tm + kTmO : half_at;
-                const uint64_t b0 = tm_operand(slots + s * P::kSlotBytes, P::kChunkBytes);
+                mbar_arrive(&bar[(v ? kWaitO : kWaitS) + b]);
+                tm_before_sync();
+                mbar_arrive(&bar[kWaitGo + s]);
+            }
+        }
+        if (warp == 16) {  // starts them: by one lane, but with addresses that the compiler sees to be the warp's
+            const int todo = __shfl_sync(0xffffffffu, 2 * n, 0);
+            const uint32_t tm0 = __shfl_sync(0xffffffffu, tm, 0);
+            int s = 0, phase = 0;
 #pragma unroll 1
-                for (int k = 0; k < steps; ++k) {
-                    const uint64_t at = b0 + ((v ? k * 2048u : (k >> 2) * P::kChunkBytes + (k & 3) * 32u) >> 4);
-                    tm_mma(to, from + 16 * k, at, kind, k > 0);
-                    tm_mma(to, from + 16 * k + 8, at, kind, 1);
-                    tm_mma(to, from + 16 * k, at + (P::kPartBytes >> 4), kind, 1);
+            for (int i = 0; i < todo; ++i) {
+                const bool v = PromptFeed<NB>::is_v(i, todo / 2);
+                const int b = PromptFeed<NB>::tile(i, todo / 2) & 1;
+                const uint32_t half_at = tm0 + kTmS + b * kPromptTokens;
+                const uint64_t operand = tm_operand(slots + s * P::kSlotBytes, P::kChunkBytes);
+                wait(kWaitGo + s, phase);
+                if (__any_sync(0xffffffffu, dead)) break;
+                tm_after_sync();
+                if (one_lane()) {
+                    if (v) {
+#pragma unroll
+                        for (int k = 0; k < kPromptTokens / 16; ++k)
+                            tm_mma3<tm_kind(D, true)>(tm0 + kTmO, half_at + 16 * k, operand + (k * 2048 >> 4), P::kPartBytes >> 4, k > 0);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < D / 16; ++k)
+                            tm_mma3<tm_kind(kPromptTokens, false)>(half_at, tm0 + 16 * k, operand + ((k >> 2) * P::kChunkBytes + (k & 3) * 32 >> 4),
+                                                                   P::kPartBytes >> 4, k > 0);
+                    }
+                    tm_commit(&bar[(v ? kWaitO : kWaitS) + b]);
+                    tm_commit(&bar[kWaitSlot + s]);
                 }
-                tm_commit(made);
-                tm_commit(&bar[kWaitSlot + s]);
+                __syncwarp();
+                if (++s == kPromptSlots) {
+                    s = 0;
+                    phase ^= 1;
+                }
             }
             // the products that were started are done before their operands' and sums' memory is another's
-            tm_commit(&bar[kWaitEnd]);
+            if (one_lane()) tm_commit(&bar[kWaitEnd]);
             if (!mbar_wait(&bar[kWaitEnd], 0)) atomicOr(a.fault, 1u);
         }
         if (warp == 17) {  // the cache's tiles, a lane each of an operand's 8
