@@ -1,6 +1,7 @@
-// zdmmv_attn_prompt.cuh -- attention of many columns (prompts) over the paged 4-bit
-// cache, heads of up to 128 dimensions, on the fifth-generation tensor cores
-// (zdmmv_attn.cuh has the formula, the columns and the join of parts).
+// zdmmv_attn_prompt.cuh -- attention of more than 16 columns (prompts, drafted tokens of
+// grouped heads) over the paged 4-bit cache, heads of up to 128 dimensions, on the
+// fifth-generation tensor cores (zdmmv_attn.cuh has the formula, the columns and the
+// join of parts).
 //
 // A CTA takes 128 columns of a kv head (the 128 rows of tcgen05.mma's D) and runs
 // over its split's tokens in tiles of 128:
@@ -20,8 +21,15 @@
 // exchange, and half of the row's output. Warps 8-15 turn the cache's codes into operands, three of which fit shared memory,
 // in the order S0 S1 O0 S2 O1 S3 ..., and a thread of warp 16 starts the products in that order, as soon as one
 // of warp 19 says so (starting blocks while the tensor cores are a product or two behind, and one thread that waits for all
-// of it leaves them idle for a third of the time): each softmax has the time of two operands' products. Warp 17 copies the cache's
-// tiles three operands ahead, warp 18 looks over their scales.
+// of it leaves them idle for a third of the time): each softmax has the time of two operands' products. Warps 17 and 18
+// copy the cache's tiles three operands ahead.
+//
+// Bound: 24 products of 64 cycles an operand, 3072 cycles a tile, 42 us for 256 tokens over 8192 (32 heads of 128, 152 SMs),
+// which takes 83: 128 CTAs of 32 tiles of some 4000 cycles each, and 10 us of starts and ends. A tile's time goes by the
+// conversion (1250 to 1500 cycles an operand, 8 warps that share the schedulers with the softmax) and by how soon the next
+// tiles' bytes are there. Measured and not kept, each with what was there then: warp 8 starting the products between its
+// conversions (230), one thread both waiting and starting (105), a thread for each kind of product (96), operands converted
+// and waited for in halves (106 against 97), the tiles' copies by one warp (93), by cp.async (108), and by one lane (123).
 #pragma once
 
 #include "zdmmv_attn.cuh"
@@ -212,7 +220,7 @@ template <int NB> __global__ void __launch_bounds__(kPromptThreads, 1) attn_prom
             const bool each = (k >= kWaitFull && k < kWaitSlot) || (k >= kWaitRawFree && k < kWaitGo);  // warps 8-15
             // the products and their unit
             const bool both = k == kWaitS || k == kWaitS + 1 || k == kWaitO || k == kWaitO + 1;
-            mbar_init(&bar[k], rows ? 2 * kPromptRows : (each ? 8 : (both ? 2 : 1)));
+            mbar_init(&bar[k], rows ? 2 * kPromptRows : (each ? 8 : (both || (k >= kWaitCopy && k < kWaitRaw) ? 2 : 1)));
         }
         sh_bad = 0;
         sh_magic = kCodeMagic;
@@ -247,23 +255,38 @@ template <int NB> __global__ void __launch_bounds__(kPromptThreads, 1) attn_prom
 
     if (warp >= 16) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsStart));
-        if (warp == 19 && lane == 0) {  // says when the products may start
+        if (warp == 19) {  // finds the operands' unit, two ahead, and says when the products may start
+            const auto scan = [&](int i) {
+                const int s = i % kPromptRaw, tile = PromptFeed<NB>::tile(i, n);
+                wait(kWaitCopy + s, i / kPromptRaw & 1);
+                __syncwarp();
+                const bool large = PromptFeed<NB>::large(smem_addr(raws) + s * 8 * PromptFeed<NB>::kRawBytes,
+                                                         limit - first * kKvSlab - tile * kPromptTokens, lane);
+                if (lane == 0) {
+                    sh_unit[i % 6] = large ? 16.0f : 1.0f;
+                    mbar_arrive(&bar[kWaitRaw + s]);
+                }
+            };
+            for (int i = 0; i < min(2, 2 * n); ++i) scan(i);
             wait(kWaitQ, 0);
 #pragma unroll 1
             for (int i = 0; i < 2 * n; ++i) {
                 const int s = i % kPromptSlots, tile = PromptFeed<NB>::tile(i, n), b = tile & 1;
                 const bool v = PromptFeed<NB>::is_v(i, n);
+                if (i + 2 < 2 * n) scan(i + 2);
                 if (v) {
                     wait(kWaitP + b, tile >> 1 & 1);
                     if (tile > 0) wait(kWaitFree, (tile - 1) & 1);
                 }
                 wait(kWaitFull + s, i / kPromptSlots & 1);
-                if (dead) break;
                 tm_after_sync();
-                sh_made[v][tile & 3] = sh_unit[i % 6];
-                mbar_arrive(&bar[(v ? kWaitO : kWaitS) + b]);
-                tm_before_sync();
-                mbar_arrive(&bar[kWaitGo + s]);
+                if (lane == 0 && !dead) {
+                    sh_made[v][tile & 3] = sh_unit[i % 6];
+                    mbar_arrive(&bar[(v ? kWaitO : kWaitS) + b]);
+                    tm_before_sync();
+                    mbar_arrive(&bar[kWaitGo + s]);
+                }
+                __syncwarp();
             }
         }
         if (warp == 16) {  // starts them: by one lane, but with addresses that the compiler sees to be the warp's
@@ -303,15 +326,15 @@ template <int NB> __global__ void __launch_bounds__(kPromptThreads, 1) attn_prom
             if (one_lane()) tm_commit(&bar[kWaitEnd]);
             if (!mbar_wait(&bar[kWaitEnd], 0)) atomicOr(a.fault, 1u);
         }
-        if (warp == 17) {  // the cache's tiles, a lane each of an operand's 8
+        if (warp == 17 || warp == 18) {  // the cache's tiles, a lane each of half an operand's 8 (one warp's take 90 cycles a copy)
             const int32_t *table = a.c.table + static_cast<int64_t>(seg.seq) * a.c.max_pages;
             const uint8_t *head = a.c.pages + static_cast<int64_t>(seg.kvh) * static_cast<int>(a.by_page_tiles.d) * G::kTileBytes;
             const uint64_t policy = l2_evict_first_policy();
             int i = 0;
 #pragma unroll 1
             for (; i < 2 * n; ++i) {
-                const int s = i % kPromptRaw, slab = first + PromptFeed<NB>::tile(i, n) * kPromptSlabs + lane;
-                const bool v = PromptFeed<NB>::is_v(i, n), in = lane < kPromptSlabs && slab < last;
+                const int s = i % kPromptRaw, mine = 4 * (warp - 17) + lane, slab = first + PromptFeed<NB>::tile(i, n) * kPromptSlabs + mine;
+                const bool v = PromptFeed<NB>::is_v(i, n), in = lane < kPromptSlabs / 2 && slab < last;
                 int page = in ? TileFeed<NB>::page_at(a, table, slab) : 0;
                 if (in && (page < 0 || page >= a.c.n_pages)) {
                     sh_bad = 1;
@@ -326,27 +349,13 @@ template <int NB> __global__ void __launch_bounds__(kPromptThreads, 1) attn_prom
                 if (in) {
                     const uint8_t *src = head + page * a.c.page_bytes +
                                          static_cast<int64_t>(a.by_page_tiles.mod(slab, a.by_page_tiles.div(slab))) * G::kTileBytes;
-                    uint8_t *to = raws + (s * 8 + lane) * PromptFeed<NB>::kRawBytes;
+                    uint8_t *to = raws + (s * 8 + mine) * PromptFeed<NB>::kRawBytes;
                     bulk_copy_g2s(to, src + (v ? G::kVAt : 0), G::kCodeBytes, &bar[kWaitCopy + s], policy);
                     bulk_copy_g2s(to + G::kCodeBytes, src + (v ? G::kVScaleAt : G::kKScaleAt), G::kScaleBytes, &bar[kWaitCopy + s], policy);
                 }
             }
             // leave only when the copies have landed (after a wait that gave up: as far as they will)
             for (int k = max(0, i - kPromptRaw); k < i; ++k) (void)mbar_wait(&bar[kWaitCopy + k % kPromptRaw], k / kPromptRaw & 1);
-        }
-        if (warp == 18) {  // ... and their unit: 1, or 16 where a scale is too large
-#pragma unroll 1
-            for (int i = 0; i < 2 * n; ++i) {
-                const int s = i % kPromptRaw, tile = PromptFeed<NB>::tile(i, n);
-                wait(kWaitCopy + s, i / kPromptRaw & 1);
-                __syncwarp();
-                const bool large = PromptFeed<NB>::large(smem_addr(raws) + s * 8 * PromptFeed<NB>::kRawBytes,
-                                                         limit - first * kKvSlab - tile * kPromptTokens, lane);
-                if (lane == 0) {
-                    sh_unit[i % 6] = large ? 16.0f : 1.0f;
-                    mbar_arrive(&bar[kWaitRaw + s]);
-                }
-            }
         }
         __syncwarp();
         __syncthreads();
