@@ -11,9 +11,10 @@ namespace {
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Up to four columns a kv head of a sequence take the narrow form, up to 16 the wide one, more a shared ring. The grid is
-// (items) x (splits of their tokens): as many as run at once; up to four times that for several sequences, whose lengths may
-// differ, while a split has kRaggedChunk tiles; whole waves of prompts' CTAs. Long sequences' decoding, from kWalkSteps steps
+// Up to four columns a kv head of a sequence take the narrow form, up to 16 the wide one, more the form on tcgen05 or (heads
+// past 128 dimensions) a shared ring. The grid is (items) x (splits of their tokens): as many as run at once; up to four times that for several sequences, whose lengths may
+// differ, while a split has kRaggedChunk tiles; whole waves of
+// CTAs for more than 16 columns. Long sequences' decoding, from kWalkSteps steps
 // a CTA on, goes by the lengths instead (AttnWalk): 64 of up to 16384 tokens 109 us with the grid and 96 so, 64 of 4096 71
 // and 68, but 64 of 1000 22.4 and 24.6.
 constexpr int kWalkSteps = 12;

@@ -4,7 +4,8 @@
 //
 // A COLUMN c is one query row: a new token's head. The columns of one kv head (the
 // heads of its group times the sequence's new tokens) read the same K and V, so a
-// CTA takes 4 to 64 of them (of a prompt up to 192) and streams the kv head's tiles once.
+// CTA takes 4 to 128 of them and streams the kv head's tiles once. More than 16 columns
+// with heads of up to 128 dimensions: zdmmv_attn_prompt.cuh. Else:
 //
 // The arithmetic, on mma.sync m16n8k16 (fp16 in, fp32 sums):
 //  * A code n (0..15) under the bits of 1024 is the fp16 number 1024 + n, or
@@ -34,7 +35,7 @@
 // equal stretch of them, whatever the lengths: parts of an item at the stretch's ends, whole items between. Each warp has
 // its own ring of two slots (a pair of tiles each, one bulk copy a tile), its own running maximum and its own sums; they
 // are joined at the item's end through shared memory, and an item's parts by the CTA that finishes last (through the
-// workspace). More columns (prompts): the grid is (column tile of an item) x (split of its tokens), the warps split the
+// workspace). More columns: the grid is (column tile of an item) x (split of its tokens), the warps split the
 // columns and share a ring.
 //
 // What it reaches. One sequence of 130975 tokens, 8 kv heads of 128, 4 columns (the narrow kernel): 35.8 us, 62% of the
@@ -76,7 +77,8 @@ enum AttnForm { kOwn = 0, kShared = 1, kPrompt = 2 };
 __host__ __device__ constexpr int attn_slots(int nb, int form) { return form == kOwn || (form == kShared && nb < 8) ? 16 : 8; }
 // Heads of up to kTallBlocks blocks with more than kTallColumns columns take the form on tcgen05 (zdmmv_attn_prompt.cuh)
 // instead of the shared and the prompt form: 8 sequences of 4000 tokens with 64 columns, 8 heads of 128, 99 us with the
-// shared form and 52 with that; one of 60000 with 24 columns 88 and 77; 20 columns over 2000 16.5 and 14.6.
+// shared form and 46 with that; one of 60000 with 24 columns 88 and 66; 20 columns over 2000 16.5 and 14.1; 1024 columns over
+// 8192 292 with the prompt form and 82.
 constexpr int kTallBlocks = 4, kTallColumns = 16;
 // Groups of 8 columns a warp of the prompt form: two, one where the shared memory does not hold q and the fragments of two.
 __host__ __device__ constexpr int attn_prompt_nt(int nb) { return nb < 8 ? 2 : 1; }
@@ -937,7 +939,7 @@ template <int NB> __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_
 // warps a scheduler (the output's and the products' registers allow no more) wait for each other's products (8 cycles an
 // m16n8k16, 22 one that needs the one before): with heads of 128 they kept the tensor cores 40% busy, and q's fragments in
 // registers, a product's sums put off behind the next block's products or warps that drift apart gained nothing. Heads of up
-// to 128 dimensions have a form of their own (zdmmv_attn_prompt.cuh), three times as fast.
+// to 128 dimensions have a form of their own (zdmmv_attn_prompt.cuh).
 template <int NB, int NT, int FORM>
 __global__ void __launch_bounds__(kAttnWarps * 32, FORM != kOwn ? 1 : attn_ctas_per_sm(NB, NT)) attn_kernel(AttnArgs a) {
     constexpr bool SHARED = FORM != kOwn, PROMPT = FORM == kPrompt;
