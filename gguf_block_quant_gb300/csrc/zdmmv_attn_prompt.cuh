@@ -14,7 +14,7 @@
 //    Tensor memory's 512 columns: Q 128, two tiles of S 256 (P takes S's place, 16
 //    tokens' two parts over their 16 sums), O 128.
 //  * O leaves tensor memory after every tile and is added up in fp32 registers: the
-//    tensor cores truncate where they add, which 24 additions a tile do not show,
+//    tensor cores truncate where they add, which a tile's additions do not show,
 //    but those of thousands of tokens would.
 //
 // Warps 0-7 take the softmax and the sums: a thread has 64 of a tile's tokens of a row, whose maximum the row's two threads
@@ -25,7 +25,7 @@
 // copy the cache's tiles three operands ahead.
 //
 // Bound: 24 products of 64 cycles an operand, 3072 cycles a tile, 42 us for 256 tokens over 8192 (32 heads of 128, 152 SMs),
-// which takes 83: 128 CTAs of 32 tiles of some 4000 cycles each, and 10 us of starts and ends. A tile's time goes by the
+// which takes 82: 128 CTAs of 32 tiles of some 4000 cycles each, and 8 us of starts and ends. A tile's time goes by the
 // conversion (1250 to 1500 cycles an operand, 8 warps that share the schedulers with the softmax) and by how soon the next
 // tiles' bytes are there. Measured and not kept, each with what was there then: warp 8 starting the products between its
 // conversions (230), one thread both waiting and starting (105), a thread for each kind of product (96), operands converted
@@ -99,16 +99,25 @@ __device__ __forceinline__ void tm_store(uint32_t at, const uint32_t (&r)[16]) {
 __device__ __forceinline__ void tm_store4(uint32_t at, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%4], {%0, %1, %2, %3};" ::"r"(x), "r"(y), "r"(z), "r"(w), "r"(at) : "memory");
 }
-// D (128 x N, tensor memory) = (or, if `more`, +=) the three products of A's parts (128 x 16 fp16 each, tensor memory, the
-// lower one 8 columns on) and B's (16 x N fp16 each, shared memory, the lower one `lower` on)
-template <uint32_t KIND> __device__ __forceinline__ void tm_mma3(uint32_t d, uint32_t a, uint64_t b, uint32_t lower, bool more) {
+// D (128 x N, tensor memory) = (or, if `more`, +=) A (128 x 16 fp16, tensor memory) B (16 x N fp16, shared memory)
+template <uint32_t KIND> __device__ __forceinline__ void tm_mma(uint32_t d, uint32_t a, uint64_t b, bool more) {
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %6, 0;\n\tsetp.eq.u32 q, %6, %6;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %3, %5, p;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%2], %3, %5, q;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %4, %5, q;\n\t}" ::"r"(d),
-        "r"(a), "r"(a + 8), "l"(b), "l"(b + lower), "r"(KIND), "r"(static_cast<uint32_t>(more))
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a),
+        "l"(b), "r"(KIND), "r"(static_cast<uint32_t>(more))
         : "memory");
+}
+// D = the sum of STEPS products of 16, of A's parts (a step's lower one 8 columns on) and B's (the lower one LOWER on; step k
+// is at(k) on). The two products with a lower part come first: their sums are small, so that D is truncated in its full size
+// STEPS times only (2.2e-6 of the result against 64 bits for 8192 tokens with all three in turn).
+template <uint32_t KIND, int STEPS, uint32_t LOWER, typename At>
+__device__ __forceinline__ void tm_mma_parts(uint32_t d, uint32_t a, uint64_t b, At at) {
+#pragma unroll
+    for (int k = 0; k < STEPS; ++k) {
+        tm_mma<KIND>(d, a + 16 * k + 8, b + (at(k) >> 4), k > 0);
+        tm_mma<KIND>(d, a + 16 * k, b + ((at(k) + LOWER) >> 4), true);
+    }
+#pragma unroll
+    for (int k = 0; k < STEPS; ++k) tm_mma<KIND>(d, a + 16 * k, b + (at(k) >> 4), true);
 }
 __device__ __forceinline__ bool one_lane() {
     uint32_t r;
@@ -303,16 +312,12 @@ template <int NB> __global__ void __launch_bounds__(kPromptThreads, 1) attn_prom
                 if (__any_sync(0xffffffffu, dead)) break;
                 tm_after_sync();
                 if (one_lane()) {
-                    if (v) {
-#pragma unroll
-                        for (int k = 0; k < kPromptTokens / 16; ++k)
-                            tm_mma3<tm_kind(D, true)>(tm0 + kTmO, half_at + 16 * k, operand + (k * 2048 >> 4), P::kPartBytes >> 4, k > 0);
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < D / 16; ++k)
-                            tm_mma3<tm_kind(kPromptTokens, false)>(half_at, tm0 + 16 * k, operand + ((k >> 2) * P::kChunkBytes + (k & 3) * 32 >> 4),
-                                                                   P::kPartBytes >> 4, k > 0);
-                    }
+                    if (v)
+                        tm_mma_parts<tm_kind(D, true), kPromptTokens / 16, P::kPartBytes>(tm0 + kTmO, half_at, operand,
+                                                                                          [](int k) { return k * 2048u; });
+                    else
+                        tm_mma_parts<tm_kind(kPromptTokens, false), D / 16, P::kPartBytes>(
+                            half_at, tm0, operand, [](int k) { return (k >> 2) * P::kChunkBytes + (k & 3) * 32u; });
                     tm_commit(&bar[(v ? kWaitO : kWaitS) + b]);
                     tm_commit(&bar[kWaitSlot + s]);
                 }
@@ -369,6 +374,7 @@ template <int NB> __global__ void __launch_bounds__(kPromptThreads, 1) attn_prom
             const int s = i % kPromptSlots, tile = F::tile(i, n), live = limit - first * kKvSlab - tile * kPromptTokens;
             const uint32_t slot = slots + s * P::kSlotBytes, raw = smem_addr(raws) + (s * 8 + w) * F::kRawBytes;
             wait(kWaitRaw + s, i / kPromptRaw & 1);
+            if (i == kPromptSlots - 1) wait(kWaitQ, 0);  // Q has left the slot
             if (i >= kPromptSlots) wait(kWaitSlot + s, (i / kPromptSlots - 1) & 1);
             __syncwarp();
             const bool shrink = sh_unit[i % 6] != 1.0f;
@@ -394,13 +400,26 @@ template <int NB> __global__ void __launch_bounds__(kPromptThreads, 1) attn_prom
         const int i = a.by_group.div(col);
         const bool valid = i < r.n;
         float qs;
-        {  // half of the row of Q
-            const float *q = a.q + static_cast<int64_t>(r.q0 + (valid ? i : 0)) * a.q_stride +
-                             static_cast<int64_t>(seg.kvh * a.group + (valid ? col - i * a.group : 0)) * D + half * (D / 2);
+        {  // Q: whole rows by a warp (a lane's own row at once costs 4096 cycles of cache lines), through the last slot
+            constexpr int kQuads = D / 4;
             float4 x[D / 8];
+            float4 *stage = reinterpret_cast<float4 *>(reinterpret_cast<uint8_t *>(sum) + (kPromptSlots - 1) * P::kSlotBytes);
 #pragma unroll
-            for (int e = 0; e < D / 8; ++e)
-                x[e] = valid ? *reinterpret_cast<const float4 *>(q + 4 * e) : make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int k = 0; k < D / 8; ++k) {
+                const int at = 32 * k + lane, to = 16 * warp + at / kQuads, c = seg.ct * kPromptRows + to, token = a.by_group.div(c);
+                x[k] = token < r.n ? *reinterpret_cast<const float4 *>(a.q + static_cast<int64_t>(r.q0 + token) * a.q_stride +
+                                                                       static_cast<int64_t>(seg.kvh * a.group + c - token * a.group) * D +
+                                                                       4 * (at % kQuads))
+                                   : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+#pragma unroll
+            for (int k = 0; k < D / 8; ++k) {
+                const int at = 32 * k + lane, to = 16 * warp + at / kQuads;
+                stage[to * kQuads + (at % kQuads ^ (to & 7))] = x[k];
+            }
+            asm volatile("barrier.cta.sync 2, 256;" ::: "memory");
+#pragma unroll
+            for (int e = 0; e < D / 8; ++e) x[e] = stage[row * kQuads + ((half * (D / 8) + e) ^ (row & 7))];
             float top = 0.0f;
 #pragma unroll
             for (int e = 0; e < D / 8; ++e)
