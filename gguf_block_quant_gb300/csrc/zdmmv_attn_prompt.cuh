@@ -19,9 +19,9 @@
 //
 // Warps 0-7 take the softmax and the sums: a thread has 64 of a tile's tokens of a row, whose maximum the row's two threads
 // exchange, and half of the row's output. Warps 8-15 turn the cache's codes into operands, three of which fit shared memory,
-// in the order S0 S1 O0 S2 O1 S3 ..., and a thread of warp 16 starts the products in that order, as soon as one
-// of warp 19 says so (starting blocks while the tensor cores are a product or two behind, and one thread that waits for all
-// of it leaves them idle for a third of the time): each softmax has the time of two operands' products. Warps 17 and 18
+// in the order S0 S1 O0 S2 O1 S3 ..., and warp 16 starts the products in that order, as soon as warp 19
+// says so, which also finds out whether an operand must be made in units of 16 (starting blocks while the tensor cores are a product or two behind, and a thread that waits for all
+// of it too leaves them idle for a third of the time): each softmax has the time of two operands' products. Warps 17 and 18
 // copy the cache's tiles three operands ahead.
 //
 // Bound: 24 products of 64 cycles an operand, 3072 cycles a tile, 42 us for 256 tokens over 8192 (32 heads of 128, 152 SMs),
@@ -39,7 +39,7 @@ namespace zdmmv {
 constexpr int kPromptThreads = 640, kPromptRows = 128, kPromptTokens = 128, kPromptSlots = 3, kPromptRaw = 3;
 constexpr int kPromptSlabs = kPromptTokens / kKvSlab;
 // Registers a thread: what the kernel is launched with (20 warps share 65536) is shared out again, 8 warps of softmax, 8 that
-// feed, 4 of which one starts the products.
+// convert, 4 that copy, look over and start the products.
 constexpr int kRegsLaunch = 96, kRegsSoft = 160, kRegsFeed = 56, kRegsStart = 48;
 static_assert(8 * kRegsSoft + 8 * kRegsFeed + 4 * kRegsStart <= 20 * kRegsLaunch, "more would wait for ever");
 // tensor memory columns
@@ -331,7 +331,7 @@ template <int NB> __global__ void __launch_bounds__(kPromptThreads, 1) attn_prom
             if (one_lane()) tm_commit(&bar[kWaitEnd]);
             if (!mbar_wait(&bar[kWaitEnd], 0)) atomicOr(a.fault, 1u);
         }
-        if (warp == 17 || warp == 18) {  // the cache's tiles, a lane each of half an operand's 8 (one warp's take 90 cycles a copy)
+        if (warp == 17 || warp == 18) {  // the cache's tiles, a lane each of half an operand's 8 (a lane's copy takes 90 cycles, one after another)
             const int32_t *table = a.c.table + static_cast<int64_t>(seg.seq) * a.c.max_pages;
             const uint8_t *head = a.c.pages + static_cast<int64_t>(seg.kvh) * static_cast<int>(a.by_page_tiles.d) * G::kTileBytes;
             const uint64_t policy = l2_evict_first_policy();
