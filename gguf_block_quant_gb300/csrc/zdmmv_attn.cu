@@ -12,18 +12,18 @@ namespace {
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Up to four columns a kv head of a sequence take the narrow form, up to 16 the wide one, more the form on tcgen05 or (heads
-// past 128 dimensions) a shared ring. The grid is (items) x (splits of their tokens): as many as run at once; up to four times that for several sequences, whose lengths may
-// differ, while a split has kRaggedChunk tiles; whole waves of
-// CTAs for more than 16 columns. Long sequences' decoding, from kWalkSteps steps
-// a CTA on, goes by the lengths instead (AttnWalk): 64 of up to 16384 tokens 109 us with the grid and 96 so, 64 of 4096 71
-// and 68, but 64 of 1000 22.4 and 24.6.
+// past 128 dimensions) a shared ring. The grid is (items) x (splits of their tokens): as many as run at once; up to four
+// times that for several sequences, whose lengths may differ, while a split has kRaggedChunk tiles; whole waves of CTAs for
+// more than 16 columns. Long sequences' decoding, from kWalkSteps steps a CTA on, goes by the lengths instead (AttnWalk): 64
+// of up to 16384 tokens 109 us with the grid and 96 so, 64 of 4096 71 and 68, but 64 of 1000 22.4 and 24.6.
+// The plan is made for what a window leaves to see of the longest sequence, and the workspace is checked for that plan.
 constexpr int kWalkSteps = 12;
 constexpr int kRaggedChunk = 128;
 constexpr int kEnds = 8;
 constexpr int kTallEnds = 32, kTallJoin = 1;  // ... of the form on tcgen05: its start, and the join's loads of four parts for 2560 values
 constexpr int kCounters = ZDMMV_ATTN_COUNTER_BYTES / 4;
 
-bool attn_plan(const KvView &c, int head_dim, int n_q_heads, int max_q_len, int64_t max_tokens, AttnPlan *out) {
+int device_sms() {
     static const int sms = [] {
         int dev = 0, n = 0;
         if (cudaGetDevice(&dev) != cudaSuccess ||
@@ -31,64 +31,122 @@ bool attn_plan(const KvView &c, int head_dim, int n_q_heads, int max_q_len, int6
             return 152;
         return n;
     }();
+    return sms;
+}
+
+// How the columns of a kv head of a sequence lie over CTAs: the kernel's form, the columns of a CTA, its column tiles, and
+// the CTAs that the device runs at once.
+struct AttnLayout {
+    int nt, wc, cols;
+    bool tall;
+    int64_t n_ct, slots;
+};
+AttnLayout attn_layout(int64_t columns, int head_dim) {
+    AttnLayout f{};
+    const int nb = kv_blocks(head_dim);
+    f.wc = columns <= 16 ? 1 : (columns <= 32 ? 2 : (columns <= 64 ? 4 : 8));
+    f.nt = f.wc > 4 ? attn_prompt_nt(nb) : (columns <= 8 ? 1 : 2);
+    f.tall = columns > kTallColumns && nb <= kTallBlocks;
+    if (f.tall) {  // 128 columns
+        f.wc = 8;
+        f.nt = 2;
+    } else if (f.wc > 4) {
+        // the fewest column tiles, the columns evenly over them
+        const int64_t tiles_of = ceil_div(columns, 8 * f.nt * f.wc);
+        f.wc = static_cast<int>(ceil_div(ceil_div(columns, tiles_of), 8 * f.nt));
+    }
+    f.cols = columns <= kNarrowCols ? kNarrowCols : 8 * f.nt * f.wc;
+    f.n_ct = ceil_div(columns, f.cols);
+    f.slots = static_cast<int64_t>(device_sms()) * (f.wc > 1 ? 1 : attn_ctas_per_sm(nb, f.nt));
+    return f;
+}
+
+int64_t attn_tiles(int64_t tokens) { return std::max<int64_t>(1, ceil_div(tokens, kKvSlab)); }
+
+// Whether `items` of `tiles` tiles each are walked by equal stretches, and the parts that this takes (an item of one step is
+// never shared).
+bool attn_walks(const AttnLayout &f, int n_seq, int64_t items, int64_t tiles) {
+    return f.wc == 1 && n_seq > 1 && items * ceil_div(tiles, kStepTiles) > kWalkSteps * f.slots;
+}
+int64_t attn_walk_ctas(const AttnLayout &f) { return std::min<int64_t>(f.slots, kCounters); }
+int64_t attn_walk_parts(const AttnLayout &f, int64_t tiles) { return tiles > kStepTiles ? 2 * attn_walk_ctas(f) : 0; }
+
+// The grid's splits of an item: the number taken, or the most that is taken for this many tiles or fewer. Both rise with the
+// tiles.
+int64_t attn_own_splits(const AttnLayout &f, int n_seq, int64_t items, int64_t tiles) {
+    if (items > kCounters) return 1;
+    int64_t splits = std::max<int64_t>(1, f.slots / items);
+    if (n_seq > 1) splits = std::max(splits, std::min(ceil_div(4 * f.slots, items), ceil_div(tiles, kRaggedChunk)));
+    return std::min(splits, ceil_div(tiles, kMinChunk));
+}
+int64_t attn_most_shared_splits(const AttnLayout &f, int64_t items, int64_t tiles) {
+    if (items > kCounters) return 1;
+    return std::min(std::max<int64_t>(1, 4 * f.slots / items), ceil_div(tiles, kMinChunk));
+}
+// Whole waves of CTAs: the split whose waves cost least, a CTA's start and end as much as kEnds tiles.
+int64_t attn_shared_splits(const AttnLayout &f, int64_t items, int64_t tiles, int64_t columns, int head_dim) {
+    if (items > kCounters) return 1;
+    const int64_t splits = std::max<int64_t>(1, f.slots / items), most = std::min(4 * splits, ceil_div(tiles, kMinChunk));
+    const int64_t cols = std::min<int64_t>(columns, f.cols);
+    const auto cost = [&](int64_t n) {
+        const int64_t ends = f.tall ? kTallEnds + kTallJoin * ceil_div(cols * head_dim, 2560) * ceil_div(n, 4) : kEnds;
+        return ceil_div(items * n, f.slots) * (ceil_div(tiles, n) + ends);
+    };
+    int64_t best = std::min(splits, ceil_div(tiles, kMinChunk));
+    for (int64_t n = best / 2; f.tall && n > 1; n /= 2)
+        if (cost(n) < cost(best)) best = n;
+    for (int waves = 1; waves <= 4; ++waves) {
+        const int64_t n = std::min(std::max<int64_t>(1, waves * f.slots / items), most);
+        if (cost(n) < cost(best)) best = n;
+    }
+    return best;
+}
+
+bool attn_plan(const KvView &c, int head_dim, int n_q_heads, int max_q_len, int64_t max_tokens, AttnPlan *out) {
     AttnPlan p{};
     const int64_t columns = static_cast<int64_t>(max_q_len) * (n_q_heads / c.n_kv_heads);
-    const int nb = kv_blocks(head_dim);
-    p.wc = columns <= 16 ? 1 : (columns <= 32 ? 2 : (columns <= 64 ? 4 : 8));
-    p.nt = p.wc > 4 ? attn_prompt_nt(nb) : (columns <= 8 ? 1 : 2);
-    p.tall = columns > kTallColumns && nb <= kTallBlocks;
-    if (p.tall) {  // 128 columns
-        p.wc = 8;
-        p.nt = 2;
-    } else if (p.wc > 4) {
-        // the fewest column tiles, the columns evenly over them
-        const int64_t tiles_of = ceil_div(columns, 8 * p.nt * p.wc);
-        p.wc = static_cast<int>(ceil_div(ceil_div(columns, tiles_of), 8 * p.nt));
-    }
-    p.cols = columns <= kNarrowCols ? kNarrowCols : 8 * p.nt * p.wc;
-    const int64_t n_ct = ceil_div(columns, p.cols);
-    p.items = static_cast<int64_t>(c.n_seq) * c.n_kv_heads * n_ct;
-    const int64_t tiles = std::max<int64_t>(1, ceil_div(max_tokens, kKvSlab));
-    const int64_t steps = p.items * ceil_div(tiles, kStepTiles);
-    if (steps > 0x7fffffff || columns > 0x7fffff00) return false;
-    p.n_ct = static_cast<int>(n_ct);
+    if (columns > 0x7fffff00) return false;
+    const AttnLayout f = attn_layout(columns, head_dim);
+    p.nt = f.nt;
+    p.wc = f.wc;
+    p.cols = f.cols;
+    p.tall = f.tall;
+    p.items = static_cast<int64_t>(c.n_seq) * c.n_kv_heads * f.n_ct;
+    const int64_t tiles = attn_tiles(max_tokens);
+    if (p.items * ceil_div(tiles, kStepTiles) > 0x7fffffff) return false;
+    p.n_ct = static_cast<int>(f.n_ct);
     p.round = p.tall ? 8 : 2;  // whole tiles of 128 tokens, whole ring slots
-    const int64_t slots = static_cast<int64_t>(sms) * (p.wc > 1 ? 1 : attn_ctas_per_sm(nb, p.nt));
-    if (p.wc == 1 && c.n_seq > 1 && steps > kWalkSteps * slots) {
-        p.ctas = static_cast<int>(std::min<int64_t>(slots, kCounters));
-        p.parts = steps > p.items ? 2 * p.ctas : 0;  // an item of one step is never shared
+    if (attn_walks(f, c.n_seq, p.items, tiles)) {
+        p.ctas = static_cast<int>(attn_walk_ctas(f));
+        p.parts = attn_walk_parts(f, tiles);
     } else {
-        int64_t splits = p.items > kCounters ? 1 : std::max<int64_t>(1, slots / p.items);
-        if (p.wc == 1 && c.n_seq > 1 && p.items <= kCounters)
-            splits = std::max(splits, std::min(ceil_div(4 * slots, p.items), ceil_div(tiles, kRaggedChunk)));
-        int64_t most = std::min(splits, ceil_div(tiles, kMinChunk));
-        p.parts = most;
-        if (p.wc > 1 && p.items <= kCounters) {
-            // whole waves of CTAs: the split whose waves cost least, a CTA's start and end as much as kEnds tiles
-            p.parts = std::min(4 * splits, ceil_div(tiles, kMinChunk));
-            const int64_t cols = std::min<int64_t>(columns, p.cols);
-            const auto cost = [&](int64_t n) {
-                const int64_t ends = p.tall ? kTallEnds + kTallJoin * ceil_div(cols * head_dim, 2560) * ceil_div(n, 4) : kEnds;
-                return ceil_div(p.items * n, slots) * (ceil_div(tiles, n) + ends);
-            };
-            for (int64_t n = most / 2; p.tall && n > 1; n /= 2)
-                if (cost(n) < cost(most)) most = n;
-            for (int waves = 1; waves <= 4; ++waves) {
-                const int64_t n = std::min(std::max<int64_t>(1, waves * slots / p.items), p.parts);
-                if (cost(n) < cost(most)) most = n;
-            }
-        }
-        p.chunk = static_cast<int>(std::max<int64_t>(kMinChunk, ceil_div(ceil_div(tiles, most), p.round) * p.round));
-        p.n_split = static_cast<int>(most);
-        p.parts = p.parts > 1 ? p.items * p.parts : 0;
+        const int64_t splits = f.wc == 1 ? attn_own_splits(f, c.n_seq, p.items, tiles)
+                                         : attn_shared_splits(f, p.items, tiles, columns, head_dim);
+        p.chunk = static_cast<int>(std::max<int64_t>(kMinChunk, ceil_div(ceil_div(tiles, splits), p.round) * p.round));
+        p.n_split = static_cast<int>(splits);
+        p.parts = splits > 1 ? p.items * splits : 0;
     }
     *out = p;
     return true;
 }
 
-size_t attn_workspace(const AttnPlan &p, int head_dim) {
-    if (p.parts == 0) return 0;
-    return ZDMMV_ATTN_COUNTER_BYTES + static_cast<size_t>(p.parts) * p.cols * (head_dim + 2) * 4;
+size_t attn_parts_bytes(int64_t parts, int64_t cols, int head_dim) {
+    return parts == 0 ? 0 : ZDMMV_ATTN_COUNTER_BYTES + static_cast<size_t>(parts * cols) * (head_dim + 2) * 4;
+}
+
+// What any call with this layout and up to `tokens` tokens (all of a sequence, or what a window leaves of it) needs. The need
+// does not rise with the length by itself: 384 items are cut into 768 parts of the grid at 2100 tokens, and walked in 608 at
+// 16384. Each way's does, so the most is the longest grid's or the walk's.
+size_t attn_layout_bytes(const AttnLayout &f, const KvView &c, int head_dim, int64_t tokens) {
+    const int64_t items = static_cast<int64_t>(c.n_seq) * c.n_kv_heads * f.n_ct;
+    int64_t tiles = attn_tiles(tokens), parts = 0;
+    if (attn_walks(f, c.n_seq, items, tiles)) {
+        parts = attn_walk_parts(f, tiles);
+        tiles = kWalkSteps * f.slots / items * kStepTiles;  // the longest that are not walked
+    }
+    const int64_t splits = tiles == 0 ? 1 : (f.wc == 1 ? attn_own_splits(f, c.n_seq, items, tiles) : attn_most_shared_splits(f, items, tiles));
+    if (splits > 1) parts = std::max(parts, items * splits);
+    return attn_parts_bytes(parts, f.cols, head_dim);
 }
 
 }  // namespace
@@ -104,7 +162,8 @@ size_t zdmmv_attn_q4_0_workspace_bytes(const zdmmv_kv_cache *cache, int n_q_head
     if (kv_check(cache, &c) != ZDMMV_OK || n_q_heads < 1 || n_q_heads > 65535 || n_q_heads % c.n_kv_heads ||
         max_q_len < 1 || max_kv_len < 0 || !attn_plan(c, cache->head_dim, n_q_heads, max_q_len, max_kv_len, &p))
         return 0;
-    return attn_workspace(p, cache->head_dim);
+    return attn_layout_bytes(attn_layout(static_cast<int64_t>(max_q_len) * (n_q_heads / c.n_kv_heads), cache->head_dim), c,
+                             cache->head_dim, max_kv_len);
 }
 
 zdmmv_status zdmmv_attn_q4_0(const zdmmv_kv_cache *cache, const zdmmv_attn_args *args, zdmmv_stream_t stream) {
@@ -113,23 +172,21 @@ zdmmv_status zdmmv_attn_q4_0(const zdmmv_kv_cache *cache, const zdmmv_attn_args 
     const zdmmv_status st = kv_check(cache, &a.c);
     if (st != ZDMMV_OK) return st;
     const zdmmv_attn_args &g = *args;
-    AttnPlan p{}, whole{};
+    AttnPlan p{};
     if (g.n_tok < 0 || g.n_q_heads < 1 || g.n_q_heads > 65535 || g.n_q_heads % cache->n_kv_heads || g.max_q_len < 1 ||
         g.max_kv_len < 0 || g.window < 0 || !std::isfinite(g.scale))
         return ZDMMV_ERR_SHAPE;
     // with a window, no column tile sees more than the window and its own new tokens
     const int64_t seen = g.window > 0 ? std::min<int64_t>(g.max_kv_len, static_cast<int64_t>(g.window) + g.max_q_len + kKvSlab)
                                       : g.max_kv_len;
-    if (!attn_plan(a.c, cache->head_dim, g.n_q_heads, g.max_q_len, g.max_kv_len, &whole) ||
-        !attn_plan(a.c, cache->head_dim, g.n_q_heads, g.max_q_len, seen, &p))
-        return ZDMMV_ERR_SHAPE;
+    if (!attn_plan(a.c, cache->head_dim, g.n_q_heads, g.max_q_len, seen, &p)) return ZDMMV_ERR_SHAPE;
     if (g.n_tok == 0) return ZDMMV_OK;
     if (!g.q || !g.q_start || !g.kv_len || !g.out) return ZDMMV_ERR_NULL;
     if (g.q_stride < static_cast<int64_t>(g.n_q_heads) * cache->head_dim) return ZDMMV_ERR_SHAPE;
     if (kv_misaligned(g.q, 16) || kv_misaligned(g.out, 16) || kv_misaligned(g.workspace, 16) ||
         kv_misaligned(g.q_start, 4) || kv_misaligned(g.kv_len, 4) || kv_misaligned(g.status_dev, 4) || g.q_stride % 4)
         return ZDMMV_ERR_ALIGN;
-    const size_t need = attn_workspace(whole, cache->head_dim);
+    const size_t need = attn_parts_bytes(p.parts, p.cols, cache->head_dim);  // of the plan that is launched
     if (need && !g.workspace) return ZDMMV_ERR_NULL;
     if (g.workspace_bytes < need) return ZDMMV_ERR_SIZE;
     a.q = g.q; a.q_start = g.q_start; a.kv_len = g.kv_len; a.out = g.out; a.status = g.status_dev;
