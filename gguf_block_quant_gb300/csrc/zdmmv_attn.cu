@@ -20,6 +20,7 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 constexpr int kWalkSteps = 12;
 constexpr int kRaggedChunk = 128;
 constexpr int kEnds = 8;
+constexpr int kPromptCols = 128;  // of a CTA of the form on tcgen05
 constexpr int kTallEnds = 32, kTallJoin = 1;  // ... of the form on tcgen05: its start, and the join's loads of four parts for 2560 values
 constexpr int kCounters = ZDMMV_ATTN_COUNTER_BYTES / 4;
 
@@ -47,7 +48,7 @@ AttnLayout attn_layout(int64_t columns, int head_dim) {
     f.wc = columns <= 16 ? 1 : (columns <= 32 ? 2 : (columns <= 64 ? 4 : 8));
     f.nt = f.wc > 4 ? attn_prompt_nt(nb) : (columns <= 8 ? 1 : 2);
     f.tall = columns > kTallColumns && nb <= kTallBlocks;
-    if (f.tall) {  // 128 columns
+    if (f.tall) {  // kPromptCols
         f.wc = 8;
         f.nt = 2;
     } else if (f.wc > 4) {
@@ -149,6 +150,23 @@ size_t attn_layout_bytes(const AttnLayout &f, const KvView &c, int head_dim, int
     return attn_parts_bytes(parts, f.cols, head_dim);
 }
 
+// ... and with `columns` or fewer, which may take any other form. Those of up to 16 columns have one column tile and are taken
+// one by one; of the others, CTAs of `top` columns or fewer, at most four times as many as run at once, and no more than there
+// are steps.
+size_t attn_bounds_bytes(const KvView &c, int head_dim, int group, int64_t columns, int64_t tokens) {
+    size_t most = 0;
+    for (int64_t form = kNarrowCols, below = 0; form <= 16; below = form, form *= 2) {
+        const int64_t last = std::min(columns, form) / group * group;  // the most columns that take it
+        if (last > below) most = std::max(most, attn_layout_bytes(attn_layout(last, head_dim), c, head_dim, tokens));
+    }
+    const int64_t heads = static_cast<int64_t>(c.n_seq) * c.n_kv_heads, steps = ceil_div(attn_tiles(tokens), kMinChunk);
+    const AttnLayout f = attn_layout(columns, head_dim);
+    if (f.wc == 1 || heads > kCounters || steps == 1 || 4 * f.slots / heads < 2) return most;
+    columns = std::min<int64_t>(columns, 0x7fffff00);  // more are refused
+    const int64_t top = f.tall ? kPromptCols : (columns <= 32 ? 32 : (columns <= 64 ? 64 : 64 * attn_prompt_nt(kv_blocks(head_dim))));
+    return std::max(most, attn_parts_bytes(std::min(4 * f.slots, heads * ceil_div(columns, top) * steps), top, head_dim));
+}
+
 }  // namespace
 }  // namespace zdmmv
 
@@ -158,12 +176,11 @@ extern "C" {
 
 size_t zdmmv_attn_q4_0_workspace_bytes(const zdmmv_kv_cache *cache, int n_q_heads, int max_q_len, int max_kv_len) {
     KvView c{};
-    AttnPlan p{};
-    if (kv_check(cache, &c) != ZDMMV_OK || n_q_heads < 1 || n_q_heads > 65535 || n_q_heads % c.n_kv_heads ||
-        max_q_len < 1 || max_kv_len < 0 || !attn_plan(c, cache->head_dim, n_q_heads, max_q_len, max_kv_len, &p))
+    if (kv_check(cache, &c) != ZDMMV_OK || n_q_heads < 1 || n_q_heads > 65535 || n_q_heads % c.n_kv_heads || max_q_len < 1 ||
+        max_kv_len < 0)
         return 0;
-    return attn_layout_bytes(attn_layout(static_cast<int64_t>(max_q_len) * (n_q_heads / c.n_kv_heads), cache->head_dim), c,
-                             cache->head_dim, max_kv_len);
+    const int group = n_q_heads / c.n_kv_heads;
+    return attn_bounds_bytes(c, cache->head_dim, group, static_cast<int64_t>(max_q_len) * group, max_kv_len);
 }
 
 zdmmv_status zdmmv_attn_q4_0(const zdmmv_kv_cache *cache, const zdmmv_attn_args *args, zdmmv_stream_t stream) {

@@ -674,8 +674,8 @@ typedef struct {
  * one sequence's result, may depend on the other sequences' lengths.
  * Errors: ERR_NULL, ERR_SHAPE, ERR_ALIGN, ERR_SIZE, ERR_CUDA. */
 #define ZDMMV_ATTN_COUNTER_BYTES 8192
-/* What a workspace has to hold for every call with max_q_len new tokens, lengths
- * of max_kv_len or less and any window. */
+/* What a workspace has to hold for every call with max_q_len new tokens a
+ * sequence or fewer, lengths of max_kv_len or less, and any window. */
 size_t zdmmv_attn_q4_0_workspace_bytes(const zdmmv_kv_cache *cache, int n_q_heads, int max_q_len,
                                        int max_kv_len);
 zdmmv_status zdmmv_attn_q4_0(const zdmmv_kv_cache *cache, const zdmmv_attn_args *args,

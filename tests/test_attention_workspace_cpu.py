@@ -47,3 +47,29 @@ def test_a_call_checks_what_it_launches():
     assert call(workspace_bytes=need - 1) == 6
     assert call(workspace=None) == 1
     assert call(workspace_bytes=need) not in (1, 6)
+
+
+@pytest.mark.parametrize("head_dim", [64, 96, 128, 192, 256])
+@pytest.mark.parametrize("kv_heads", [1, 4, 8, 16])
+def test_more_new_tokens_never_need_less(kv_heads, head_dim):
+    """A workspace made for a prompt's chunk is one for decoding."""
+    for n_seq, group, most in itertools.product(SEQS, (1, 3, 4, 5, 8), LENGTHS[::3]):
+        size = sizer(n_seq, kv_heads, head_dim, kv_heads * group)
+        last = 0
+        for new in (1, 2, 3, 4, 5, 6, 7, 8, 9, 12, 13, 16, 17, 24, 33, 40, 65, 100, 128, 129, 200, 300, 600, 2000):
+            now = size(new, most)
+            assert now >= last, (n_seq, group, new, most)
+            last = now
+
+
+def test_the_workspace_of_300_sequences_serves_eight_new_tokens_and_one():
+    """Eight new tokens of four heads make more items than there are counters, which are not split; one is walked."""
+    size = sizer(300, 8, 128, 32)
+    assert size(8, 4096) >= size(1, 4096) >= 8192 + 608 * 4 * 130 * 4
+
+
+def test_sizes_stay_within_reason():
+    """Twice as many parts as run at once, or four times as many CTAs of 128 columns as the device has SMs."""
+    for head_dim, kv_heads, n_seq, new in itertools.product((64, 128, 256), (1, 8), (1, 40, 300), (1, 8, 4096)):
+        size = sizer(n_seq, kv_heads, head_dim, 4 * kv_heads)(new, 1 << 20)
+        assert size <= 8192 + 4 * 152 * 128 * (head_dim + 2) * 4

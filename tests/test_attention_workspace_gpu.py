@@ -49,3 +49,24 @@ def test_windows_over_many_sequences(n_seq, heads, group, dim, new, window, long
         rows = slice(s * new, (s + 1) * new)
         check_attention(out[rows], q[rows], [0, new], lens[s:s + 1], np.arange(held)[None], whole[table[s, :held]], page, heads,
                         dim, window=window)
+
+
+def test_a_prompts_workspace_serves_decoding():
+    """One workspace for up to eight new tokens of 300 sequences, then calls of eight, three and one new tokens on it."""
+    rng = np.random.default_rng(300)
+    n_seq, heads, group, dim, page, bound = 300, 8, 4, 128, 64, 4096
+    lens = [max(8, n) for n in ragged(rng, n_seq, 700)]
+    cache, _, table = random_cache(rng, lens, page, heads, dim)
+    wide = np.full((n_seq, bound // page), -1, np.int32)
+    wide[:, :table.shape[1]] = table
+    cache = Z.KVCache(cache.pages, page, heads, dim, dev(wide))
+    size = Z.attn_q4_0_workspace_bytes(cache, heads * group, 8, bound)
+    ws, behind = guarded(size)
+    ws[:8192] = 0
+    kv_len = dev(np.array(lens, np.int32))
+    for new in (8, 1, 3, 1):
+        q_start = dev(np.arange(n_seq + 1, dtype=np.int32) * new)
+        q = torch.randn(n_seq * new, heads * group, dim, device="cuda", generator=torch.Generator("cuda").manual_seed(new))
+        out = Z.attn_q4_0(cache, q, q_start, kv_len, new, bound, workspace=ws)
+        assert torch.equal(Z.attn_q4_0(cache, q, q_start, kv_len, new, bound), out)
+        assert (behind == 0xA5).all() and not ws[:8192].any()
