@@ -254,10 +254,11 @@ template <int NB> __global__ void __launch_bounds__(kPromptThreads, 1) attn_prom
     uint8_t *raws = reinterpret_cast<uint8_t *>(sum) + kPromptSlots * P::kSlotBytes;  // [place][8] cache tiles' K or V
     const int first = seg.first, last = seg.last, limit = min(r.len, last * kKvSlab);
     const int n = (last - first + kPromptSlabs - 1) / kPromptSlabs;
-    bool dead = false;  // a wait gave up: no more waits, but every barrier of threads is met
+    bool dead = false;  // a wait gave up: no more waits, but every barrier of threads is met; the result is NaN
     const auto wait = [&](int which, uint32_t parity) {
         if (!dead && !mbar_wait(&bar[which], parity)) {
             atomicOr(a.fault, 1u);
+            sh_bad = 1;
             dead = true;
         }
     };
@@ -329,7 +330,10 @@ template <int NB> __global__ void __launch_bounds__(kPromptThreads, 1) attn_prom
             }
             // the products that were started are done before their operands' and sums' memory is another's
             if (one_lane()) tm_commit(&bar[kWaitEnd]);
-            if (!mbar_wait(&bar[kWaitEnd], 0)) atomicOr(a.fault, 1u);
+            if (!mbar_wait(&bar[kWaitEnd], 0)) {
+                atomicOr(a.fault, 1u);
+                sh_bad = 1;
+            }
         }
         if (warp == 17 || warp == 18) {  // the cache's tiles, a lane each of half an operand's 8 (a lane's copy takes 90 cycles, one after another)
             const int32_t *table = a.c.table + static_cast<int64_t>(seg.seq) * a.c.max_pages;
