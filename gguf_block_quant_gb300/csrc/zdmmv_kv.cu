@@ -308,7 +308,8 @@ template <int NB, bool FAST> __global__ void __launch_bounds__(kStreamWarps * 32
     Place w{};
     Rows to{};
     Turn turn[kPass];
-    bool ok = true;
+    bool ok = true;  // no wait gave up
+    int lost = 0;    // ... else the job whose did: no more waits and copies, and the rows from it on are NaN
     int tok = a.by_groups.div(first), h0 = a.by_groups.mod(first, tok) * kStreamHeads;
     for (int job = first; job < last; ++job, h0 += kStreamHeads) {
         if (h0 >= heads) {
@@ -325,9 +326,10 @@ template <int NB, bool FAST> __global__ void __launch_bounds__(kStreamWarps * 32
             place_check(a, w, lane);
             to = rows_of<NB>(a, w, tok);
         }
-        if (!__all_sync(0xffffffffu, mbar_wait(&full[s], phase))) {
+        if (ok && !__all_sync(0xffffffffu, mbar_wait(&full[s], phase))) {
             if (lane == 0) atomicOr(a.fault, 1u);
             ok = false;
+            lost = job;
         }
         const float *rows = reinterpret_cast<const float *>(ring + s * kSlotBytes);
 #pragma unroll
@@ -360,7 +362,7 @@ template <int NB, bool FAST> __global__ void __launch_bounds__(kStreamWarps * 32
         }
     }
     if (!ok) {  // leave only when the copies have landed, as far as they will
-        for (int k = 0; k < kStreamSlots; ++k) (void)mbar_wait(&full[k], 0);
+        for (int k = lost; k < min(lost + kStreamSlots, last); ++k) (void)mbar_wait(&full[(k - first) % kStreamSlots], (k - first) / kStreamSlots & 1);
     }
 }
 
