@@ -25,10 +25,11 @@
 //  * Product with V: A = the codes' dimensions x 16 tokens, B = x = p * d_v (V's
 //    scales are per token and block) in two fp16 parts, formed in fp16: with p =
 //    ph + pl, xh = ph * d_v rounded, xl = pl * d_v + (ph * d_v - xh), whose bracket
-//    one fma gives exactly. p is kept in units of 2^sx, sx such that p and x stay
-//    below 2^15 for the largest |d_v| met: fp16's lowest unit of 2^-24 is then
-//    below 2^-38 of the largest p, and below 2^-26 of the largest x while d_v is a
-//    normal fp16 number.
+//    one fma gives exactly. p is in units of 2^-13, so that p and x stay below 2^15
+//    while |d_v| < 2: fp16's lowest unit of 2^-24 is then 2^-38 of the largest p.
+//    32 tokens of which one has a larger scale take x = p * d_v in fp32 instead,
+//    split in the unit of each column's and block's largest x, so that large values
+//    cost neither other blocks nor other tokens their precision.
 //
 // Work. Up to 16 columns a kv head of a sequence (decoding): the ITEMS (sequence, kv head) one after another are a row of
 // STEPS of 16 tiles (a pair for each of a CTA's 8 warps), and every CTA of a grid that fills the device once takes an
@@ -42,6 +43,8 @@
 // copy rate, of which some 12 us are the kernel's ends; at 2^20 tokens 217 us, 82%. 64 sequences of up to 16384 tokens:
 // 96.8 us (65%). The narrow kernel is bound by its instructions as much as by memory (issue 60%, ALU 46% at 131K tokens).
 #pragma once
+
+#include <type_traits>
 
 #include "zdmmv_kv.cuh"
 
@@ -87,7 +90,7 @@ __host__ __device__ constexpr int attn_ctas_per_sm(int nb, int nt) { return nb *
 // Whether the warps' sums have shared memory of their own, so that the next item's tiles can come while they are joined.
 __host__ __device__ constexpr bool attn_sums_apart(int nb, int nt, int form) { return form == kOwn && nb * nt < 16; }
 constexpr int kAttnBarBytes = 256;  // two barriers a slot
-constexpr int kAttnUnit = 13;
+constexpr float kAttnUnit = 13.0f;  // p is in units of 2^-kAttnUnit
 constexpr int kJoinAhead = 16;
 
 // What a CTA (and the join) works on, from the lengths on the device.
@@ -450,8 +453,30 @@ __device__ __forceinline__ void q_unit(float top, float scale, float &up, float 
     up = __uint_as_float((static_cast<uint32_t>(e + 127) << 23) | (scale < 0.0f ? 0x80000000u : 0u));
     down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
 }
-// The unit of p for a largest |d_v| (fp16 bits) of 2 or more: 2^(unit - kAttnUnit) |d_v| < 2.
-__device__ __forceinline__ int unit_for(uint32_t bits) { return kAttnUnit + 15 - static_cast<int>(bits >> 10); }
+// Whether a scale of the warp's tokens is 2 or more (bit 14 of an fp16 number).
+template <int NB> __device__ __forceinline__ bool scales_large(const uint32_t (&dv)[4][NB]) {
+    uint32_t any = 0;
+#pragma unroll
+    for (int h = 0; h < 4; ++h)
+#pragma unroll
+        for (int b = 0; b < NB; ++b) any |= dv[h][b];
+    return __any_sync(0xffffffffu, (any & 0x40004000u) != 0);
+}
+// x = p d_v of a unit's tokens (a lane's pairs; the lanes of a column are t = 0 .. 3) in two fp16 parts whose unit is 2^-e for
+// the column's largest x: x = down * (hi + lo).
+__device__ __forceinline__ void split_x(const uint64_t (&x)[4], uint32_t (&hi)[4], uint32_t (&lo)[4], float &down) {
+    float top = 0.0f, up;
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+        const float2 v = f2_parts(x[h]);
+        top = fmaxf(fmaxf(top, fabsf(v.x)), fabsf(v.y));
+    }
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    q_unit(top, 1.0f, up, down);
+#pragma unroll
+    for (int h = 0; h < 4; ++h) split_f2(f2_mul(x[h], f2(up, up)), hi[h], lo[h]);
+}
 
 // The copies of a stretch of units (pairs of tiles, a ring slot each): unit first_unit + k * step, k = 0, 1, ...; a warp's
 // lanes look up the pages of 16 units at a time, lanes 2j and 2j + 1 copy unit j's tiles.
@@ -758,7 +783,6 @@ template <int NB> __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_
     uint64_t o[2 * NB];  // column t, dimensions 4g and 4g + 1, or 4g + 2 and 4g + 3, of the block
 #pragma unroll
     for (int k = 0; k < 2 * NB; ++k) o[k] = 0;
-    int sx = kAttnUnit;  // p is in units of 2^sx
 
     for (int u = warp, j_next = 2; u < n_units && !dead; u += kWarps) {
         if (!__all_sync(0xffffffffu, mbar_wait(&full[slot], phases >> slot & 1u))) {
@@ -814,29 +838,7 @@ template <int NB> __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_
                 }
             }
         }
-        // ------------------------------------------------ the unit of p: 2^kAttnUnit while every |d_v| < 2
-        {
-            uint32_t any = 0;
-#pragma unroll
-            for (int h = 0; h < 4; ++h)
-#pragma unroll
-                for (int b = 0; b < NB; ++b) any |= dv[h][b];
-            if (__any_sync(0xffffffffu, (any & 0x40004000u) != 0)) {
-                uint32_t big = 0;
-#pragma unroll
-                for (int h = 0; h < 4; ++h)
-#pragma unroll
-                    for (int b = 0; b < NB; ++b) big = max(big, max(dv[h][b] & 0x7fffu, (dv[h][b] >> 16) & 0x7fffu));
-                const int to = unit_for(__reduce_max_sync(0xffffffffu, big));
-                if (to < sx) {
-                    const float keep = __uint_as_float(static_cast<uint32_t>(to - sx + 127) << 23);
-                    sx = to;
-                    l *= keep;
-#pragma unroll
-                    for (int k = 0; k < 2 * NB; ++k) o[k] = f2_mul(o[k], f2(keep, keep));
-                }
-            }
-        }
+        const bool large = scales_large(dv);
         // ------------------------------------------------ softmax
         float top = fmaxf(fmaxf(sc[0], sc[1]), fmaxf(sc[2], sc[3]));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
@@ -851,7 +853,7 @@ template <int NB> __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_
 #pragma unroll
             for (int k = 0; k < 2 * NB; ++k) o[k] = f2_mul(o[k], f2(keep, keep));
         }
-        const float base = m == -INFINITY ? 0.0f : m - static_cast<float>(sx);
+        const float base = m == -INFINITY ? 0.0f : m - kAttnUnit;
         uint32_t p0[4], p1[4];  // rows 0 or ph, and ph or pl, of tokens 8h + 2t, + 1
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
@@ -867,26 +869,50 @@ template <int NB> __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_
         for (int h = 0; h < 4; ++h)
             lds_words<NB, G::kVec>(tile + (h >> 1) * G::kTileBytes + G::kVAt + ((h & 1) * NB * 32 + lane * G::kVec) * 4,
                                    128 * G::kVec, vw[h]);
+        const auto product = [&](auto wide_range) {
 #pragma unroll
-        for (int j = 0; j < NB; ++j) {
-            uint32_t f[2][2][4], x[4];
+            for (int j = 0; j < NB; ++j) {
+                uint32_t f[2][2][4], x[4];
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {
-                uint32_t vc[4];
-                code_pairs(vw[h][j], magic, vc);
-                f[h >> 1][0][2 * (h & 1)] = vc[0]; f[h >> 1][0][2 * (h & 1) + 1] = vc[1];
-                f[h >> 1][1][2 * (h & 1)] = vc[2]; f[h >> 1][1][2 * (h & 1) + 1] = vc[3];
-                x[h] = h2_fma(p1[h], dv[h][j], h2_fma(p0[h], dv[h][j], h2_neg(h2_mul(p0[h], dv[h][j]))));
+                for (int h = 0; h < 4; ++h) {
+                    uint32_t vc[4];
+                    code_pairs(vw[h][j], magic, vc);
+                    f[h >> 1][0][2 * (h & 1)] = vc[0]; f[h >> 1][0][2 * (h & 1) + 1] = vc[1];
+                    f[h >> 1][1][2 * (h & 1)] = vc[2]; f[h >> 1][1][2 * (h & 1) + 1] = vc[3];
+                }
+                float down = 1.0f;
+                if constexpr (decltype(wide_range)::value) {
+                    // the rows of pl have p itself; those of ph get x's upper part from them
+                    uint64_t px[4];
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) px[h] = f2_mul(f2_add(f2_half2(p0[h]), f2_half2(p1[h])), f2_half2(dv[h][j]));
+                    uint32_t lo[4];
+                    split_x(px, x, lo, down);
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+                        const uint32_t hi = __shfl_xor_sync(0xffffffffu, x[h], 4);
+                        x[h] = (g & 1) ? lo[h] : hi;
+                    }
+                    down = __shfl_sync(0xffffffffu, down, 8 * t + 4);
+                } else {
+#pragma unroll
+                    for (int h = 0; h < 4; ++h)
+                        x[h] = h2_fma(p1[h], dv[h][j], h2_fma(p0[h], dv[h][j], h2_neg(h2_mul(p0[h], dv[h][j]))));
+                }
+                // summed over the unit by the tensor cores (they truncate), over the units in fp32
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    float c[4];
+                    mma_first(c, f[0][i], x[0], x[1]);
+                    mma_acc(c, f[1][i], x[2], x[3]);
+                    const uint64_t y = f2(c[0] + c[1], c[2] + c[3]);
+                    if constexpr (decltype(wide_range)::value) o[2 * j + i] = f2_fma(y, f2(down, down), o[2 * j + i]);
+                    else o[2 * j + i] = f2_add(o[2 * j + i], y);
+                }
             }
-            // summed over the unit by the tensor cores (they truncate), over the units in fp32
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                float c[4];
-                mma_first(c, f[0][i], x[0], x[1]);
-                mma_acc(c, f[1][i], x[2], x[3]);
-                o[2 * j + i] = f2_add(o[2 * j + i], f2(c[0] + c[1], c[2] + c[3]));
-            }
-        }
+        };
+        if (large) product(std::true_type{});
+        else product(std::false_type{});
         __syncwarp();
         if (u + 2 * kWarps < n_units) {  // the warp's unit after next takes the slot's place
             if (j_next == 16) {
@@ -903,7 +929,6 @@ template <int NB> __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_
     l += __shfl_xor_sync(0xffffffffu, l, 4);
     l += __shfl_xor_sync(0xffffffffu, l, 8);
     l += __shfl_xor_sync(0xffffffffu, l, 16);
-    m -= static_cast<float>(sx);  // the maximum in p's unit
     if (g == 0) sh_m[warp][t] = m;
     __syncthreads();
     // the next segment's first tiles come while this one's sums are joined
@@ -1123,7 +1148,6 @@ __global__ void __launch_bounds__(kAttnWarps * 32, FORM != kOwn ? 1 : attn_ctas_
 #pragma unroll
         for (int k = 0; k < 2 * NB; ++k) o[nt][k][0] = o[nt][k][1] = 0;
     }
-    int sx = kAttnUnit;  // p is in units of 2^sx
 
     if (PROMPT && n_units > 0) {
         wait_full(0);
@@ -1248,35 +1272,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, FORM != kOwn ? 1 : attn_ctas_
                 }
             }
         }
-        // ------------------------------------------------ the unit of p: 2^kAttnUnit while every |d_v| < 2
-        {
-            uint32_t any = 0;
-#pragma unroll
-            for (int h = 0; h < 4; ++h)
-#pragma unroll
-                for (int b = 0; b < NB; ++b) any |= dv[h][b];
-            if (__any_sync(0xffffffffu, (any & 0x40004000u) != 0)) {  // bit 14 of an fp16 number: 2 and above
-                uint32_t big = 0;
-#pragma unroll
-                for (int h = 0; h < 4; ++h)
-#pragma unroll
-                    for (int b = 0; b < NB; ++b) big = max(big, max(dv[h][b] & 0x7fffu, (dv[h][b] >> 16) & 0x7fffu));
-                big = __reduce_max_sync(0xffffffffu, big);
-                const int to = unit_for(big);
-                if (to < sx) {
-                    const float keep = __uint_as_float(static_cast<uint32_t>(to - sx + 127) << 23);
-                    sx = to;
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        l[nt] *= keep;
-#pragma unroll
-                        for (int j = 0; j < 2 * NB; ++j)
-#pragma unroll
-                            for (int i = 0; i < 2; ++i) o[nt][j][i] = f2_mul(o[nt][j][i], f2(keep, keep));
-                    }
-                }
-            }
-        }
+        const bool large = scales_large(dv);
         // ------------------------------------------------ softmax
         bool grow = false;
         float top[NT];
@@ -1308,7 +1304,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, FORM != kOwn ? 1 : attn_ctas_
         uint32_t ph[NT][4], pl[NT][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const float base = m[nt] == -INFINITY ? 0.0f : m[nt] - static_cast<float>(sx);
+            const float base = m[nt] == -INFINITY ? 0.0f : m[nt] - kAttnUnit;
             float e[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) e[i] = exp2_approx(fmaf(sc[nt][i], qs[nt], -base));
@@ -1324,6 +1320,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, FORM != kOwn ? 1 : attn_ctas_
                 lds_words<NB, G::kVec>(tile + (h >> 1) * G::kTileBytes + G::kVAt + ((h & 1) * NB * 32 + lane * G::kVec) * 4,
                                        128 * G::kVec, vw[h]);
         }
+        const auto product = [&](auto wide_range) {
 #pragma unroll
         for (int j = 0; j < NB; ++j) {
             uint32_t f[2][2][4];  // [tile][dimensions 4g, 4g+1 / 4g+2, 4g+3 of the block]
@@ -1343,13 +1340,22 @@ __global__ void __launch_bounds__(kAttnWarps * 32, FORM != kOwn ? 1 : attn_ctas_
                 }
             }
             uint32_t hi[NT][4], lo[NT][4];
+            float down[NT];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt) {
+                if constexpr (decltype(wide_range)::value) {
+                    uint64_t px[4];
 #pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    hi[nt][h] = h2_mul(ph[nt][h], dv[h][j]);
-                    lo[nt][h] = h2_fma(pl[nt][h], dv[h][j], h2_fma(ph[nt][h], dv[h][j], h2_neg(hi[nt][h])));
+                    for (int h = 0; h < 4; ++h) px[h] = f2_mul(f2_add(f2_half2(ph[nt][h]), f2_half2(pl[nt][h])), f2_half2(dv[h][j]));
+                    split_x(px, hi[nt], lo[nt], down[nt]);
+                } else {
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+                        hi[nt][h] = h2_mul(ph[nt][h], dv[h][j]);
+                        lo[nt][h] = h2_fma(pl[nt][h], dv[h][j], h2_fma(ph[nt][h], dv[h][j], h2_neg(hi[nt][h])));
+                    }
                 }
+            }
             // summed over the unit by the tensor cores (they truncate), over the units in fp32
             float c[NT][2][4];
 #pragma unroll
@@ -1369,13 +1375,24 @@ __global__ void __launch_bounds__(kAttnWarps * 32, FORM != kOwn ? 1 : attn_ctas_
 #pragma unroll
                 for (int s = 0; s < 2; ++s) mma_acc(c[nt][s], f[1][s], hi[nt][2], hi[nt][3]);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt) {
+                uint64_t unit = 0;
+                if constexpr (decltype(wide_range)::value)
+                    unit = f2(__shfl_sync(0xffffffffu, down[nt], 8 * t), __shfl_sync(0xffffffffu, down[nt], 8 * t + 4));
 #pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    o[nt][2 * j + s][0] = f2_add(o[nt][2 * j + s][0], f2(c[nt][s][0], c[nt][s][1]));
-                    o[nt][2 * j + s][1] = f2_add(o[nt][2 * j + s][1], f2(c[nt][s][2], c[nt][s][3]));
-                }
+                for (int s = 0; s < 2; ++s)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        uint64_t &to = o[nt][2 * j + s][i];
+                        const uint64_t y = f2(c[nt][s][2 * i], c[nt][s][2 * i + 1]);
+                        if constexpr (decltype(wide_range)::value) to = f2_fma(y, unit, to);
+                        else to = f2_add(to, y);
+                    }
+            }
         }
+        };
+        if (large) product(std::true_type{});
+        else product(std::false_type{});
         }
         __syncwarp();
         if constexpr (PROMPT) {
@@ -1415,7 +1432,6 @@ __global__ void __launch_bounds__(kAttnWarps * 32, FORM != kOwn ? 1 : attn_ctas_
     for (int nt = 0; nt < NT; ++nt) {
         l[nt] += __shfl_xor_sync(0xffffffffu, l[nt], 1);
         l[nt] += __shfl_xor_sync(0xffffffffu, l[nt], 2);
-        m[nt] -= static_cast<float>(sx);  // the maximum in p's unit
         if (t == 0) sh_m[warp][8 * nt + g] = m[nt];
     }
     __syncthreads();  // every warp is done with the ring
