@@ -258,7 +258,6 @@ template <int NB> __global__ void __launch_bounds__(kPromptThreads, 1) attn_prom
     const auto wait = [&](int which, uint32_t parity) {
         if (!dead && !mbar_wait(&bar[which], parity)) {
             atomicOr(a.fault, 1u);
-            sh_bad = 1;
             dead = true;
         }
     };
@@ -332,7 +331,7 @@ template <int NB> __global__ void __launch_bounds__(kPromptThreads, 1) attn_prom
             if (one_lane()) tm_commit(&bar[kWaitEnd]);
             if (!mbar_wait(&bar[kWaitEnd], 0)) {
                 atomicOr(a.fault, 1u);
-                sh_bad = 1;
+                dead = true;
             }
         }
         if (warp == 17 || warp == 18) {  // the cache's tiles, a lane each of half an operand's 8 (a lane's copy takes 90 cycles, one after another)
@@ -366,6 +365,7 @@ template <int NB> __global__ void __launch_bounds__(kPromptThreads, 1) attn_prom
             // leave only when the copies have landed (after a wait that gave up: as far as they will)
             for (int k = max(0, i - kPromptRaw); k < i; ++k) (void)mbar_wait(&bar[kWaitCopy + k % kPromptRaw], k / kPromptRaw & 1);
         }
+        if (dead) sh_bad = 1;
         __syncwarp();
         __syncthreads();
     } else if (warp >= 8) {
@@ -396,6 +396,7 @@ template <int NB> __global__ void __launch_bounds__(kPromptThreads, 1) attn_prom
                 mbar_arrive(&bar[kWaitRawFree + s]);
             }
         }
+        if (dead) sh_bad = 1;
         __syncthreads();
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
@@ -527,6 +528,7 @@ template <int NB> __global__ void __launch_bounds__(kPromptThreads, 1) attn_prom
             keep = then;
         }
         if (n > 0) drain(n - 1);
+        if (dead) sh_bad = 1;
         const float2 ls = f2_parts(l2);
         sh_l[half][row] = ls.x + ls.y;
         __syncthreads();  // the products are done; their operands' memory takes the sums

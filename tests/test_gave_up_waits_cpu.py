@@ -27,11 +27,17 @@ def waits_that_report(text):
 
 
 def test_the_prompt_kernel_poisons_its_result():
-    """attn_store stores NaN where sh_bad is set: every wait that reports a fault sets it."""
+    """attn_store stores NaN where sh_bad is set: every wait that reports a fault marks its thread, and all three kinds of warps
+    set sh_bad for a marked thread before the barrier in front of attn_store."""
     text = source("zdmmv_attn_prompt.cuh")
     reports = text.count("atomicOr(a.fault")
     assert reports >= 2
-    assert sum("atomicOr(a.fault" in b and "sh_bad = 1" in b for b in waits_that_report(text)) == reports
+    assert sum("atomicOr(a.fault" in b and "dead = true" in b for b in waits_that_report(text)) == reports
+    kernel = block(text, text.index("attn_prompt_kernel(AttnArgs a)"))
+    roles = kernel.split("asm volatile(\"setmaxnreg.")[1:4]
+    assert [r.count("if (dead) sh_bad = 1;") for r in roles] == [1, 1, 1]
+    for r in roles:
+        assert "wait(" not in r[r.index("if (dead) sh_bad = 1;"):].replace("tm_", "")
 
 
 def test_the_append_rings_last_waits():
