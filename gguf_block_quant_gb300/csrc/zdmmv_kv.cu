@@ -308,8 +308,7 @@ template <int NB, bool FAST> __global__ void __launch_bounds__(kStreamWarps * 32
     Place w{};
     Rows to{};
     Turn turn[kPass];
-    bool ok = true;  // no wait gave up
-    int lost = 0;    // ... else the job whose did: no more waits and copies, and the rows from it on are NaN
+    int lost = -1;  // the job whose wait gave up: the rows from it on are NaN
     int tok = a.by_groups.div(first), h0 = a.by_groups.mod(first, tok) * kStreamHeads;
     for (int job = first; job < last; ++job, h0 += kStreamHeads) {
         if (h0 >= heads) {
@@ -326,10 +325,10 @@ template <int NB, bool FAST> __global__ void __launch_bounds__(kStreamWarps * 32
             place_check(a, w, lane);
             to = rows_of<NB>(a, w, tok);
         }
-        if (ok && !__all_sync(0xffffffffu, mbar_wait(&full[s], phase))) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&full[s], phase))) {
             if (lane == 0) atomicOr(a.fault, 1u);
-            ok = false;
             lost = job;
+            break;
         }
         const float *rows = reinterpret_cast<const float *>(ring + s * kSlotBytes);
 #pragma unroll
@@ -341,8 +340,8 @@ template <int NB, bool FAST> __global__ void __launch_bounds__(kStreamWarps * 32
             for (int p = 0; p < kPass; ++p) {
                 const int e0 = p * 128 + 4 * lane;
                 float v[4] = {0.0f, 0.0f, 0.0f, 0.0f}, o[4];
-                if (!w.ok || !ok) {
-                    v[0] = v[1] = v[2] = v[3] = ok ? place_fill(w) : __int_as_float(0x7fffffff);
+                if (!w.ok) {
+                    v[0] = v[1] = v[2] = v[3] = place_fill(w);
                 } else if (e0 < G::kDim) {
                     const bool turn_it = turned && e0 < a.rot_dim;
                     load_head<FAST>(a, rows + u * G::kDim, e0, turn_it, v, o);
@@ -352,7 +351,7 @@ template <int NB, bool FAST> __global__ void __launch_bounds__(kStreamWarps * 32
             }
         }
         __syncwarp();
-        if (ok && job + kStreamSlots < last) {
+        if (job + kStreamSlots < last) {
             fence_proxy_async_smem();
             copy(job + kStreamSlots, s);
         }
@@ -361,8 +360,17 @@ template <int NB, bool FAST> __global__ void __launch_bounds__(kStreamWarps * 32
             phase ^= 1;
         }
     }
-    if (!ok) {  // leave only when the copies have landed, as far as they will
-        for (int k = lost; k < min(lost + kStreamSlots, last); ++k) (void)mbar_wait(&full[(k - first) % kStreamSlots], (k - first) / kStreamSlots & 1);
+    if (lost < 0) return;
+    // leave only when the copies have landed, as far as they will
+    for (int k = lost; k < min(lost + kStreamSlots, last); ++k) (void)mbar_wait(&full[(k - first) % kStreamSlots], (k - first) / kStreamSlots & 1);
+    const float nan = __int_as_float(0x7fffffff), row[4] = {nan, nan, nan, nan};
+    for (int job = lost; job < last; ++job) {
+        const int t = a.by_groups.div(job), from = a.by_groups.mod(job, t) * kStreamHeads;
+        Place where = place_of(a, a.pos[t], a.seq[t]);
+        place_check(a, where, lane);
+        const Rows dst = rows_of<NB>(a, where, t);
+        for (int head = from; head < min(from + kStreamHeads, heads); ++head)
+            for (int p = 0; p < kPass; ++p) put_head<NB>(a, dst, head, p * 128 + 4 * lane, lane, row);
     }
 }
 
