@@ -17,12 +17,16 @@
 //    tensor cores truncate where they add, which a tile's additions do not show,
 //    but those of thousands of tokens would.
 //
+//  * 8 d has to be an fp16 number: where a tile has a scale of 2^13 or more (values past 65000), V's operand takes that
+//    block's dimensions in units of 16, K's all of the tile, whose scales then count to 2^-21. A unit for each token of K
+//    (its sums put right before the softmax) cost every tile of any call 10% of its time.
+//
 // Warps 0-7 take the softmax and the sums: a thread has 64 of a tile's tokens of a row, whose maximum the row's two threads
 // exchange, and half of the row's output. Warps 8-15 turn the cache's codes into operands, three of which fit shared memory,
-// in the order S0 S1 O0 S2 O1 S3 ..., and warp 16 starts the products in that order, as soon as warp 19
-// says so, which also finds out whether an operand must be made in units of 16 (starting blocks while the tensor cores are a product or two behind, and a thread that waits for all
-// of it too leaves them idle for a third of the time): each softmax has the time of two operands' products. Warps 17 and 18
-// copy the cache's tiles three operands ahead.
+// in the order S0 S1 O0 S2 O1 S3 ..., and warp 16 starts the products in that order, as soon as warp 19 says so, which also
+// finds out what must be made in units of 16: each softmax has the time of two operands' products. (Starting blocks while the
+// tensor cores are a product or two behind, and a thread that waits for all of it too leaves them idle for a third of the
+// time.) Warps 17 and 18 copy the cache's tiles three operands ahead.
 //
 // Bound: 24 products of 64 cycles an operand, 3072 cycles a tile, 42 us for 256 tokens over 8192 (32 heads of 128, 152 SMs),
 // which takes 82: 128 CTAs of 32 tiles of some 4000 cycles each, and 8 us of starts and ends. A tile's time goes by the
@@ -169,7 +173,7 @@ template <int NB> struct PromptFeed {
     }
     // Octet u of the cache tile at `raw` becomes rows row0 .. row0+7 of the operand at `slot`; rows from `live` on are no
     // tokens and become zeros, whatever the cache holds there.
-    template <bool V> __device__ static void convert(uint32_t raw, int u, uint32_t slot, int row0, int live, bool shrink, uint32_t magic, int lane) {
+    template <bool V> __device__ static void convert(uint32_t raw, int u, uint32_t slot, int row0, int live, uint32_t units, uint32_t magic, int lane) {
         const int tok = token(lane, V), row = row0 + tok, t8 = V ? lane >> 3 : lane & 3;
         const uint32_t pick = row >= live ? 0x4444u : ((tok & 1) ? 0x3232u : 0x1010u);
         uint32_t w[NB], d[NB];
@@ -183,9 +187,10 @@ template <int NB> struct PromptFeed {
                 w[b] = __byte_perm(w[b], o, (lane & 4) ? 0x3276 : 0x5410);
             }
         }
-        if (shrink)
+        if (units != 0)
 #pragma unroll
-            for (int b = 0; b < NB; ++b) d[b] = h2_mul(d[b], 0x2C002C00u);
+            for (int b = 0; b < NB; ++b)
+                if (units >> b & 1u) d[b] = h2_mul(d[b], 0x2C002C00u);
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
             // K: odd rows begin with the other block of a chunk, so that 8 lanes' stores meet 8 different banks
@@ -196,9 +201,10 @@ template <int NB> struct PromptFeed {
             put(x, y, magic, slot + (b >> 1) * PromptGeom<NB>::kChunkBytes + row * 128 + c * 16);
         }
     }
-    // Whether a scale of a live token of the 8 cache tiles at `raw` is 2^13 or more, so that 8 d is no fp16 number: its
-    // exponent's upper three bits are set.
-    __device__ static bool large(uint32_t raw, int live, int lane) {
+    // The blocks that are made in units of 16, a bit each: those with a scale of a live token of the 8 cache tiles at `raw` that
+    // is 2^13 or more (its exponent's upper three bits are set), so that 8 d is no fp16 number; of K all or none, whose blocks
+    // are one sum.
+    __device__ static uint32_t units(uint32_t raw, int live, bool v, int lane) {
         uint32_t any = 0;
 #pragma unroll
         for (int w = 0; w < 8; ++w)
@@ -207,7 +213,16 @@ template <int NB> struct PromptFeed {
                 const int tok = 16 * w + 2 * (k / NB);
                 any |= d & d << 1 & d << 2 & ((tok < live ? 0x4000u : 0u) | (tok + 1 < live ? 0x40000000u : 0u));
             }
-        return __any_sync(0xffffffffu, any != 0);
+        if (!__any_sync(0xffffffffu, any != 0)) return 0;
+        if (!v) return ~0u;
+        uint32_t blocks = 0;
+#pragma unroll 1
+        for (int i = lane; i < 64 * NB; i += 32) {
+            const int w = i / (8 * NB), k = i % (8 * NB), tok = 16 * w + 2 * (k / NB);
+            const uint32_t d = lds32(raw + w * kRawBytes + G::kCodeBytes + k * 4);
+            if (d & d << 1 & d << 2 & ((tok < live ? 0x4000u : 0u) | (tok + 1 < live ? 0x40000000u : 0u))) blocks |= 1u << k % NB;
+        }
+        return __reduce_or_sync(0xffffffffu, blocks);
     }
 };
 
@@ -217,9 +232,9 @@ template <int NB> __global__ void __launch_bounds__(kPromptThreads, 1) attn_prom
     constexpr int D = G::kDim;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(8) uint64_t bar[kPromptBars];
-    __shared__ float sh_top[2][2][kPromptRows], sh_m[kPromptRows], sh_l[2][kPromptRows], sh_unit[6], sh_made[2][4];
+    __shared__ float sh_top[2][2][kPromptRows], sh_m[kPromptRows], sh_l[2][kPromptRows], sh_made_k[4];
     __shared__ int sh_bad, sh_last;
-    __shared__ uint32_t sh_tm, sh_magic;
+    __shared__ uint32_t sh_tm, sh_magic, sh_unit[6], sh_made_v[4];
     __shared__ AttnSeg sh_seg;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, half = warp >> 2;
@@ -269,10 +284,10 @@ template <int NB> __global__ void __launch_bounds__(kPromptThreads, 1) attn_prom
                 const int s = i % kPromptRaw, tile = PromptFeed<NB>::tile(i, n);
                 wait(kWaitCopy + s, i / kPromptRaw & 1);
                 __syncwarp();
-                const bool large = PromptFeed<NB>::large(smem_addr(raws) + s * 8 * PromptFeed<NB>::kRawBytes,
-                                                         limit - first * kKvSlab - tile * kPromptTokens, lane);
+                const uint32_t units = PromptFeed<NB>::units(smem_addr(raws) + s * 8 * PromptFeed<NB>::kRawBytes,
+                                                             limit - first * kKvSlab - tile * kPromptTokens, PromptFeed<NB>::is_v(i, n), lane);
                 if (lane == 0) {
-                    sh_unit[i % 6] = large ? 16.0f : 1.0f;
+                    sh_unit[i % 6] = units;
                     mbar_arrive(&bar[kWaitRaw + s]);
                 }
             };
@@ -290,7 +305,8 @@ template <int NB> __global__ void __launch_bounds__(kPromptThreads, 1) attn_prom
                 wait(kWaitFull + s, i / kPromptSlots & 1);
                 tm_after_sync();
                 if (lane == 0 && !dead) {
-                    sh_made[v][tile & 3] = sh_unit[i % 6];
+                    if (v) sh_made_v[tile & 3] = sh_unit[i % 6];
+                    else sh_made_k[tile & 3] = sh_unit[i % 6] ? 16.0f : 1.0f;
                     mbar_arrive(&bar[(v ? kWaitO : kWaitS) + b]);
                     tm_before_sync();
                     mbar_arrive(&bar[kWaitGo + s]);
@@ -381,13 +397,13 @@ template <int NB> __global__ void __launch_bounds__(kPromptThreads, 1) attn_prom
             if (i == kPromptSlots - 1) wait(kWaitQ, 0);  // Q has left the slot
             if (i >= kPromptSlots) wait(kWaitSlot + s, (i / kPromptSlots - 1) & 1);
             __syncwarp();
-            const bool shrink = sh_unit[i % 6] != 1.0f;
+            const uint32_t units = sh_unit[i % 6];
             if (F::is_v(i, n)) {
 #pragma unroll
-                for (int u = 0; u < 2; ++u) F::template convert<true>(raw, u, slot, 16 * w + 8 * u, live, shrink, magic, lane);
+                for (int u = 0; u < 2; ++u) F::template convert<true>(raw, u, slot, 16 * w + 8 * u, live, units, magic, lane);
             } else {
 #pragma unroll
-                for (int u = 0; u < 2; ++u) F::template convert<false>(raw, u, slot, 16 * w + 8 * u, live, shrink, magic, lane);
+                for (int u = 0; u < 2; ++u) F::template convert<false>(raw, u, slot, 16 * w + 8 * u, live, units, magic, lane);
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -462,19 +478,26 @@ template <int NB> __global__ void __launch_bounds__(kPromptThreads, 1) attn_prom
             wait(kWaitO + (tile & 1), tile >> 1 & 1);
             __syncwarp();
             tm_after_sync();
-            const float unit = sh_made[1][tile & 3];
+            const uint32_t units = sh_made_v[tile & 3];
             uint32_t o[kLoads][16];
 #pragma unroll
             for (int c = 0; c < kLoads; ++c) tm_load(rows + kTmO + half * (D / 2) + 16 * c, o[c]);
             tm_loaded(o);
             tm_before_sync();
             mbar_arrive(&bar[kWaitFree]);
-            const uint64_t keep2 = f2(keep, keep), unit2 = f2(unit, unit);
+            if (units != 0) {
+#pragma unroll
+                for (int c = 0; c < kLoads; ++c)
+                    if (units >> ((half * (D / 2) + 16 * c) / kQK) & 1u)
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) o[c][k] = __float_as_uint(16.0f * __uint_as_float(o[c][k]));
+            }
+            const uint64_t keep2 = f2(keep, keep);
 #pragma unroll
             for (int c = 0; c < kLoads; ++c)
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
-                    acc[8 * c + k] = f2_fma(acc[8 * c + k], keep2, f2_mul(f2(__uint_as_float(o[c][2 * k]), __uint_as_float(o[c][2 * k + 1])), unit2));
+                    acc[8 * c + k] = f2_fma(acc[8 * c + k], keep2, f2(__uint_as_float(o[c][2 * k]), __uint_as_float(o[c][2 * k + 1])));
         };
 #pragma unroll 1
         for (int tile = 0; tile < n; ++tile) {
@@ -483,7 +506,7 @@ template <int NB> __global__ void __launch_bounds__(kPromptThreads, 1) attn_prom
             wait(kWaitS + (tile & 1), tile >> 1 & 1);
             __syncwarp();
             tm_after_sync();
-            const float unit = qs * sh_made[0][tile & 3];
+            const float unit = qs * sh_made_k[tile & 3];
             uint32_t s[4][16];
 #pragma unroll
             for (int c = 0; c < 4; ++c) tm_load(at + 16 * c, s[c]);

@@ -640,7 +640,13 @@ zdmmv_status zdmmv_kv_append_q4_0(const zdmmv_kv_cache *cache, const zdmmv_kv_ap
  * over the tokens seen; a row that sees none is zero. q and every p are split
  * into two fp16 parts for the tensor cores (22 bits), the codes of K and V are
  * exact there, the blocks' scales, all sums and the softmax's statistics are
- * fp32: the result is that of fp32 arithmetic on the cache's values. */
+ * fp32: the result is that of fp32 arithmetic on the cache's values, with these
+ * limits. q counts to 2^-34 of its row's largest, and p times a scale of V below
+ * 2 to 2^-38 of the row's largest p. With more than 16 query rows (new tokens
+ * times the heads of a kv head) and heads of up to 128 dimensions, p counts to
+ * 2^-38 of the row's largest whatever V is; and where one of 128 tokens has a
+ * scale of 2^13 or more (a value past 65000 in its block of 32), the scales of
+ * all 128 count to 2^-21 (of V those of the same block alone). */
 typedef struct {
     const float *q;          /* device fp32 [n_tok][n_q_heads][head_dim], tokens q_stride apart (rotated) */
     const int32_t *q_start;  /* device int32 [n_seq+1], rising from 0 to n_tok */

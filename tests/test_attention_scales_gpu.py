@@ -1,12 +1,13 @@
 """Attention over blocks whose scales differ by up to fp16's whole range, in every form of the kernel. The bounds are those of
-tests/test_block_ops_gpu.py, which are each block's own: large values in one block of 32 dimensions do not excuse errors in
-another."""
+tests/test_block_ops_gpu.py and (tcgen05) tests/test_attention_columns_gpu.py, which are each block's own: large values in one
+block of 32 dimensions do not excuse errors in another."""
 import numpy as np
 import pytest
 import torch
 
 from gguf_block_quant_gb300 import zdmmv as Z
 from tests import block_ref as R
+from tests import test_attention_columns_gpu as C
 from tests.test_block_ops_gpu import check_attention, dev, random_cache
 
 pytestmark = pytest.mark.gpu
@@ -15,6 +16,8 @@ pytestmark = pytest.mark.gpu
 FORMS = [(64, 4, 1), (128, 4, 1), (256, 2, 1), (96, 1, 3), (192, 4, 1), (64, 8, 1), (128, 8, 1), (96, 8, 1), (256, 7, 1),
          (192, 5, 1), (128, 16, 1), (64, 5, 3), (96, 12, 1), (192, 16, 1), (256, 16, 1), (192, 24, 1), (256, 8, 6),
          (192, 20, 5), (256, 10, 9)]
+# ... and on tcgen05
+TALL = [(64, 17, 1), (96, 8, 5), (128, 8, 16), (128, 40, 4)]
 
 
 def setup(rng, lens, heads, dim, k_scales, v_scales, page=32):
@@ -43,7 +46,14 @@ def attend(cache, q, lens, new, **kw):
     return out, q_start
 
 
-@pytest.mark.parametrize("dim, group, new", FORMS)
+def check(dim, group, new, *args):
+    if (dim, group, new) in TALL:
+        C.check(*args, dim ** -0.5, 0)
+    else:
+        check_attention(*args)
+
+
+@pytest.mark.parametrize("dim, group, new", FORMS + TALL)
 @pytest.mark.parametrize("large", [2.0 ** 3, 2.0 ** 12, 2.0 ** 14.9])
 def test_large_and_small_blocks_of_v(dim, group, new, large):
     """Every other block's scales are `large`, the others' 2^-12."""
@@ -56,10 +66,10 @@ def test_large_and_small_blocks_of_v(dim, group, new, large):
     cache, pages, table = setup(rng, lens, heads, dim, None, scales)
     q = (0.1 * rng.standard_normal((2 * new, heads * group, dim))).astype(np.float32)
     out, q_start = attend(cache, q, lens, [new, new])
-    check_attention(out, q, q_start, lens, table, pages, 32, heads, dim)
+    check(dim, group, new, out, q, q_start, lens, table, pages, 32, heads, dim)
 
 
-@pytest.mark.parametrize("dim, group, new", FORMS)
+@pytest.mark.parametrize("dim, group, new", FORMS + TALL)
 def test_large_and_small_tokens_of_v(dim, group, new):
     """Some tokens' scales are 2^14, the others' 2^-2 (a block's scales 2^16 apart)."""
     rng = np.random.default_rng(dim + group)
@@ -71,7 +81,7 @@ def test_large_and_small_tokens_of_v(dim, group, new):
     cache, pages, table = setup(rng, lens, heads, dim, None, scales)
     q = (0.1 * rng.standard_normal((2 * new, heads * group, dim))).astype(np.float32)
     out, q_start = attend(cache, q, lens, [new, new])
-    check_attention(out, q, q_start, lens, table, pages, 32, heads, dim)
+    check(dim, group, new, out, q, q_start, lens, table, pages, 32, heads, dim)
 
 
 @pytest.mark.parametrize("dim, group, new", FORMS)
