@@ -29,7 +29,8 @@
 //    while |d_v| < 2: fp16's lowest unit of 2^-24 is then 2^-38 of the largest p.
 //    32 tokens of which one has a larger scale take x = p * d_v in fp32 instead,
 //    split in the unit of each column's and block's largest x, so that large values
-//    cost neither other blocks nor other tokens their precision.
+//    cost neither other blocks nor other tokens their precision, and infinities and
+//    NaN no column that does not see them.
 //
 // Work. Up to 16 columns a kv head of a sequence (decoding): the ITEMS (sequence, kv head) one after another are a row of
 // STEPS of 16 tiles (a pair for each of a CTA's 8 warps), and every CTA of a grid that fills the device once takes an
@@ -462,13 +463,24 @@ template <int NB> __device__ __forceinline__ bool scales_large(const uint32_t (&
         for (int b = 0; b < NB; ++b) any |= dv[h][b];
     return __any_sync(0xffffffffu, (any & 0x40004000u) != 0);
 }
+// Which of a lane's tokens tok, tok + 1, tok + 8, ... of a unit are in low .. end - 1, a bit each.
+__device__ __forceinline__ uint32_t seen_tokens(int tok, int low, int end) {
+    uint32_t seen = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int a = tok + 8 * (i >> 1) + (i & 1);
+        seen |= (a >= low && a < end ? 1u : 0u) << i;
+    }
+    return seen;
+}
 // x = p d_v of a unit's tokens (a lane's pairs; the lanes of a column are t = 0 .. 3) in two fp16 parts whose unit is 2^-e for
-// the column's largest x: x = down * (hi + lo).
-__device__ __forceinline__ void split_x(const uint64_t (&x)[4], uint32_t (&hi)[4], uint32_t (&lo)[4], float &down) {
+// the column's largest x: x = down * (hi + lo). V of what the column does not see may be no number, and x is 0 there.
+__device__ __forceinline__ void split_x(uint64_t (&x)[4], uint32_t seen, uint32_t (&hi)[4], uint32_t (&lo)[4], float &down) {
     float top = 0.0f, up;
 #pragma unroll
     for (int h = 0; h < 4; ++h) {
-        const float2 v = f2_parts(x[h]);
+        const float2 y = f2_parts(x[h]), v = make_float2((seen >> 2 * h & 1u) ? y.x : 0.0f, (seen >> (2 * h + 1) & 1u) ? y.y : 0.0f);
+        x[h] = f2(v.x, v.y);
         top = fmaxf(fmaxf(top, fabsf(v.x)), fabsf(v.y));
     }
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
@@ -870,6 +882,9 @@ template <int NB> __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_
             lds_words<NB, G::kVec>(tile + (h >> 1) * G::kTileBytes + G::kVAt + ((h & 1) * NB * 32 + lane * G::kVec) * 4,
                                    128 * G::kVec, vw[h]);
         const auto product = [&](auto wide_range) {
+            uint32_t seen = 0;  // by column g / 2
+            if constexpr (decltype(wide_range)::value)
+                seen = seen_tokens(t0 + 2 * t, __shfl_sync(0xffffffffu, low, g >> 1), __shfl_sync(0xffffffffu, end, g >> 1));
 #pragma unroll
             for (int j = 0; j < NB; ++j) {
                 uint32_t f[2][2][4], x[4];
@@ -887,7 +902,7 @@ template <int NB> __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_
 #pragma unroll
                     for (int h = 0; h < 4; ++h) px[h] = f2_mul(f2_add(f2_half2(p0[h]), f2_half2(p1[h])), f2_half2(dv[h][j]));
                     uint32_t lo[4];
-                    split_x(px, x, lo, down);
+                    split_x(px, seen, x, lo, down);
 #pragma unroll
                     for (int h = 0; h < 4; ++h) {
                         const uint32_t hi = __shfl_xor_sync(0xffffffffu, x[h], 4);
@@ -1321,6 +1336,9 @@ __global__ void __launch_bounds__(kAttnWarps * 32, FORM != kOwn ? 1 : attn_ctas_
                                        128 * G::kVec, vw[h]);
         }
         const auto product = [&](auto wide_range) {
+            uint32_t seen[NT];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) seen[nt] = decltype(wide_range)::value ? seen_tokens(t0 + 2 * t, low[nt], end[nt]) : 0;
 #pragma unroll
         for (int j = 0; j < NB; ++j) {
             uint32_t f[2][2][4];  // [tile][dimensions 4g, 4g+1 / 4g+2, 4g+3 of the block]
@@ -1347,7 +1365,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, FORM != kOwn ? 1 : attn_ctas_
                     uint64_t px[4];
 #pragma unroll
                     for (int h = 0; h < 4; ++h) px[h] = f2_mul(f2_add(f2_half2(ph[nt][h]), f2_half2(pl[nt][h])), f2_half2(dv[h][j]));
-                    split_x(px, hi[nt], lo[nt], down[nt]);
+                    split_x(px, seen[nt], hi[nt], lo[nt], down[nt]);
                 } else {
 #pragma unroll
                     for (int h = 0; h < 4; ++h) {

@@ -226,6 +226,49 @@ template <int NB> struct PromptFeed {
     }
 };
 
+// Where V's scales are infinities or NaN the products make NaN of rows that do not see them (0 times NaN). The sums of such a row
+// and block once more, by a warp with a lane for a dimension, over the tokens that the row sees of the split: a scalar loop,
+// since this is no ordinary call, and NaN at once where the row sees one. (Zeros in their place while the operands are made, and a
+// record of the tokens, cost every call 2 to 10% of its time.)
+template <int NB>
+__device__ __forceinline__ float attn_redo(const AttnArgs &a, const AttnSeg &seg, int col, int b, float m, int lane) {
+    using G = KvGeom<NB>;
+    const AttnRange &r = seg.r;
+    const int i = a.by_group.div(col), seen = max(0, r.len - (r.n - 1 - i));
+    const int end = min(min(r.len, seg.last * kKvSlab), seen);
+    const int low = max(seg.first * kKvSlab, a.window > 0 ? seen - a.window : 0);
+    const int32_t *table = a.c.table + static_cast<int64_t>(seg.seq) * a.c.max_pages;
+    const uint8_t *head = a.c.pages + static_cast<int64_t>(seg.kvh) * static_cast<int>(a.by_page_tiles.d) * G::kTileBytes;
+    const auto tile_of = [&](int slab) {
+        const int slot = a.by_page_tiles.div(slab);
+        return head + table[slot] * a.c.page_bytes + static_cast<int64_t>(a.by_page_tiles.mod(slab, slot)) * G::kTileBytes;
+    };
+    const auto scale_of = [&](const uint8_t *tile, int at, int tok, int block) {
+        return __half2float(reinterpret_cast<const __half *>(tile + at)[G::scale_half(tok, block)]);
+    };
+    for (int t0 = low; t0 < end; t0 += 32) {
+        const int t = t0 + lane;
+        const bool no = t < end && !isfinite(scale_of(tile_of(t / kKvSlab), G::kVScaleAt, t % kKvSlab, b));
+        if (__any_sync(0xffffffffu, no)) return __int_as_float(0x7fffffff);
+    }
+    const float *q = a.q + static_cast<int64_t>(r.q0 + i) * a.q_stride + static_cast<int64_t>(seg.kvh * a.group + col - i * a.group) * G::kDim + lane;
+    float sum = 0.0f;
+    for (int t = low; t < end; ++t) {
+        const uint8_t *tile = tile_of(t / kKvSlab);
+        const int tok = t % kKvSlab;
+        float s = 0.0f;
+        for (int k = 0; k < NB; ++k) {
+            const uint32_t code = reinterpret_cast<const uint32_t *>(tile)[G::k_word(tok, k, lane / 8)] >> 4 * (lane % 8) & 15u;
+            s = fmaf(q[k * kQK], scale_of(tile, G::kKScaleAt, tok, k) * (static_cast<float>(code) - 8.0f), s);
+        }
+#pragma unroll
+        for (int k = 16; k > 0; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
+        const uint32_t code = reinterpret_cast<const uint16_t *>(tile + G::kVAt)[G::v_half(tok, b, lane / 4)] >> 4 * (lane % 4) & 15u;
+        sum = fmaf(exp2_approx(fmaf(s, a.scale_log2, kAttnUnit - m)), scale_of(tile, G::kVScaleAt, tok, b) * (static_cast<float>(code) - 8.0f), sum);
+    }
+    return sum;
+}
+
 template <int NB> __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(AttnArgs a) {
     using G = KvGeom<NB>;
     using P = PromptGeom<NB>;
@@ -233,7 +276,7 @@ template <int NB> __global__ void __launch_bounds__(kPromptThreads, 1) attn_prom
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(8) uint64_t bar[kPromptBars];
     __shared__ float sh_top[2][2][kPromptRows], sh_m[kPromptRows], sh_l[2][kPromptRows], sh_made_k[4];
-    __shared__ int sh_bad, sh_last;
+    __shared__ int sh_bad, sh_last, sh_redo;
     __shared__ uint32_t sh_tm, sh_magic, sh_unit[6], sh_made_v[4];
     __shared__ AttnSeg sh_seg;
 
@@ -246,7 +289,7 @@ template <int NB> __global__ void __launch_bounds__(kPromptThreads, 1) attn_prom
             const bool both = k == kWaitS || k == kWaitS + 1 || k == kWaitO || k == kWaitO + 1;
             mbar_init(&bar[k], rows ? 2 * kPromptRows : (each ? 8 : (both || (k >= kWaitCopy && k < kWaitRaw) ? 2 : 1)));
         }
-        sh_bad = 0;
+        sh_bad = sh_redo = 0;
         sh_magic = kCodeMagic;
         fence_barrier_init();
     }
@@ -552,6 +595,10 @@ template <int NB> __global__ void __launch_bounds__(kPromptThreads, 1) attn_prom
         }
         if (n > 0) drain(n - 1);
         if (dead) sh_bad = 1;
+        uint64_t no = 0;  // 0 times a sum that is no number
+#pragma unroll
+        for (int k = 0; k < D / 4; ++k) no = f2_fma(acc[k], 0, no);
+        if (!(f2_parts(no).x + f2_parts(no).y == 0.0f)) sh_redo = 1;
         const float2 ls = f2_parts(l2);
         sh_l[half][row] = ls.x + ls.y;
         __syncthreads();  // the products are done; their operands' memory takes the sums
@@ -576,6 +623,15 @@ template <int NB> __global__ void __launch_bounds__(kPromptThreads, 1) attn_prom
     __syncthreads();
     tm_after_sync();
     if (warp == 16) tm_free(tm);
+    if (sh_redo && !sh_bad && !r.bad) {
+        for (int k = warp; k < kPromptRows * NB; k += kPromptThreads / 32) {
+            const int row = k / NB, b = k % NB, col = seg.ct * kPromptRows + row;
+            float *at = sum + row * D + 4 * ((8 * b + lane / 4) ^ (row & 7)) + lane % 4;
+            const bool no = col < r.n * a.group && isfinite(sh_l[0][row]) && !isfinite(*at);
+            if (__any_sync(0xffffffffu, no)) *at = attn_redo<NB>(a, seg, col, b, sh_m[row], lane);
+        }
+        __syncthreads();
+    }
     attn_store<D, kPromptRows, kPromptThreads / 32, true>(a, seg, kPromptRows, 1, 1, sum, sh_m, &sh_l[0][0], r.bad || sh_bad, &sh_last);
 }
 

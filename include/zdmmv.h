@@ -674,7 +674,9 @@ typedef struct {
  * kv_len < 0, kv_len > max_kv_len or past its max_pages pages, with a page
  * number outside 0..n_pages-1 where it would read, or with more new tokens than
  * max_q_len is bad: the rows of it that the grid covers are NaN, nothing is read
- * out of range. Tokens at and past kv_len may hold anything. The same
+ * out of range. Tokens at and past kv_len may hold anything, and so may, for a
+ * row, those that it does not see: infinities and NaN there (v past 524000 is
+ * stored as infinity) have no part in its result. The same
  * inputs, all sequences' lengths among them, with the same max_q_len and
  * max_kv_len give the same bits; how the work is split, and so the last bits of
  * one sequence's result, may depend on the other sequences' lengths.
