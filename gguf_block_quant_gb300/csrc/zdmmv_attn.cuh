@@ -92,6 +92,11 @@ __host__ __device__ constexpr int attn_ctas_per_sm(int nb, int nt) { return nb *
 __host__ __device__ constexpr bool attn_sums_apart(int nb, int nt, int form) { return form == kOwn && nb * nt < 16; }
 constexpr int kAttnBarBytes = 256;  // two barriers a slot
 constexpr float kAttnUnit = 13.0f;  // p is in units of 2^-kAttnUnit
+// From scores of this size on (in powers of two) a float's step is a part of p that counts: p is then of the rounded score less
+// the maximum, not of both in one fma, which would leave the largest score's own rounding in the exponent of every p (2^64 of
+// it at 2^30).
+constexpr float kHugeScore = 8388608.0f;
+__device__ __forceinline__ bool score_huge(float m) { return fabsf(m) >= kHugeScore && m != -INFINITY; }
 constexpr int kJoinAhead = 16;
 
 // What a CTA (and the join) works on, from the lengths on the device.
@@ -385,7 +390,8 @@ template <int NB, int W> __device__ __forceinline__ void lds_words(uint32_t at, 
     }
 }
 
-// Two fp32 operations in one instruction (each half rounded as the scalar one).
+// Two fp32 operations in one instruction (each half rounded as the scalar one; but a product that an f2_add takes may become one
+// fma with it, .rn or not: where that matters, the scalar intrinsics).
 __device__ __forceinline__ uint64_t f2(float x, float y) {
     uint64_t d;
     asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(x), "f"(y));
@@ -450,7 +456,7 @@ __device__ __forceinline__ void load_q(const AttnArgs &a, const AttnRange &r, in
 // 2^e that brings a column's largest magnitude into [2^13, 2^14), with the scale's sign (up), and 2^-e (down).
 __device__ __forceinline__ void q_unit(float top, float scale, float &up, float &down) {
     int e = 13 - (static_cast<int>(__float_as_uint(top) >> 23) - 127);
-    e = min(100, max(-100, e));
+    e = min(100, e);  // -114 at least
     up = __uint_as_float((static_cast<uint32_t>(e + 127) << 23) | (scale < 0.0f ? 0x80000000u : 0u));
     down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
 }
@@ -792,6 +798,7 @@ template <int NB> __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_
     const int end_min = __reduce_min_sync(0xffffffffu, end), low_max = __reduce_max_sync(0xffffffffu, low);
 
     float m = -INFINITY, l = 0.0f;
+    bool huge = false;
     uint64_t o[2 * NB];  // column t, dimensions 4g and 4g + 1, or 4g + 2 and 4g + 3, of the block
 #pragma unroll
     for (int k = 0; k < 2 * NB; ++k) o[k] = 0;
@@ -864,12 +871,19 @@ template <int NB> __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_
             l *= keep;
 #pragma unroll
             for (int k = 0; k < 2 * NB; ++k) o[k] = f2_mul(o[k], f2(keep, keep));
+            huge = __any_sync(0xffffffffu, score_huge(m));
         }
-        const float base = m == -INFINITY ? 0.0f : m - kAttnUnit;
+        float base = m == -INFINITY ? 0.0f : m - kAttnUnit, unit = qs;
+        if (huge) {
+#pragma unroll
+            for (int h = 0; h < 4; ++h) sc[h] = __fadd_rn(__fmul_rn(sc[h], qs), m == -INFINITY ? 0.0f : -m);
+            base = -kAttnUnit;
+            unit = 1.0f;
+        }
         uint32_t p0[4], p1[4];  // rows 0 or ph, and ph or pl, of tokens 8h + 2t, + 1
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
-            const float p = exp2_approx(fmaf(sc[h], qs, -base));
+            const float p = exp2_approx(fmaf(sc[h], unit, -base));
             l += p;
             const uint32_t w = pack_h2(0.0f, p);
             p0[h] = transpose_8x8(w);
@@ -1154,6 +1168,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, FORM != kOwn ? 1 : attn_ctas_
     __syncwarp();
 
     float m[NT], l[NT], qs[NT];
+    bool huge = false;
     uint64_t o[NT][2 * NB][2];  // columns 2t, 2t+1: dimension pairs' first and second
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -1315,14 +1330,24 @@ __global__ void __launch_bounds__(kAttnWarps * 32, FORM != kOwn ? 1 : attn_ctas_
                     o[nt][j][1] = f2_mul(o[nt][j][1], k01);
                 }
             }
+            bool any = false;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) any |= score_huge(m[nt]);
+            huge = __any_sync(0xffffffffu, any);
         }
         uint32_t ph[NT][4], pl[NT][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const float base = m[nt] == -INFINITY ? 0.0f : m[nt] - kAttnUnit;
+            float base = m[nt] == -INFINITY ? 0.0f : m[nt] - kAttnUnit, unit = qs[nt];
+            if (huge) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) sc[nt][i] = __fadd_rn(__fmul_rn(sc[nt][i], unit), m[nt] == -INFINITY ? 0.0f : -m[nt]);
+                base = -kAttnUnit;
+                unit = 1.0f;
+            }
             float e[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) e[i] = exp2_approx(fmaf(sc[nt][i], qs[nt], -base));
+            for (int i = 0; i < 8; ++i) e[i] = exp2_approx(fmaf(sc[nt][i], unit, -base));
             l[nt] += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
 #pragma unroll
             for (int h = 0; h < 4; ++h) split_f2(f2(e[2 * h], e[2 * h + 1]), ph[nt][h], pl[nt][h]);

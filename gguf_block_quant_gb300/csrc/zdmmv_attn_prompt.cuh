@@ -226,12 +226,13 @@ template <int NB> struct PromptFeed {
     }
 };
 
-// Where V's scales are infinities or NaN the products make NaN of rows that do not see them (0 times NaN). The sums of such a row
-// and block once more, by a warp with a lane for a dimension, over the tokens that the row sees of the split: a scalar loop,
-// since this is no ordinary call, and NaN at once where the row sees one. (Zeros in their place while the operands are made, and a
-// record of the tokens, cost every call 2 to 10% of its time.)
+// A row once more, token by token, by a warp with a lane for a dimension of each block: what the row sees of the split, its sums
+// to `sum` (column's quads exchanged as the kernel has them), its maximum and sum of p. Two kinds of rows need it, neither of
+// ordinary calls: where V is an infinity or NaN the products are NaN for rows that do not see it (0 times NaN); and from scores
+// of kHugeScore on the fma of p's exponent does not do. (In the tiles' loops the one cost every call 2 to 10% of its time, the
+// other 2.)
 template <int NB>
-__device__ __forceinline__ float attn_redo(const AttnArgs &a, const AttnSeg &seg, int col, int b, float m, int lane) {
+__device__ __forceinline__ void attn_redo(const AttnArgs &a, const AttnSeg &seg, int col, int row, float *sum, float &row_m, float &row_l, int lane) {
     using G = KvGeom<NB>;
     const AttnRange &r = seg.r;
     const int i = a.by_group.div(col), seen = max(0, r.len - (r.n - 1 - i));
@@ -239,34 +240,43 @@ __device__ __forceinline__ float attn_redo(const AttnArgs &a, const AttnSeg &seg
     const int low = max(seg.first * kKvSlab, a.window > 0 ? seen - a.window : 0);
     const int32_t *table = a.c.table + static_cast<int64_t>(seg.seq) * a.c.max_pages;
     const uint8_t *head = a.c.pages + static_cast<int64_t>(seg.kvh) * static_cast<int>(a.by_page_tiles.d) * G::kTileBytes;
-    const auto tile_of = [&](int slab) {
-        const int slot = a.by_page_tiles.div(slab);
-        return head + table[slot] * a.c.page_bytes + static_cast<int64_t>(a.by_page_tiles.mod(slab, slot)) * G::kTileBytes;
-    };
-    const auto scale_of = [&](const uint8_t *tile, int at, int tok, int block) {
-        return __half2float(reinterpret_cast<const __half *>(tile + at)[G::scale_half(tok, block)]);
-    };
-    for (int t0 = low; t0 < end; t0 += 32) {
-        const int t = t0 + lane;
-        const bool no = t < end && !isfinite(scale_of(tile_of(t / kKvSlab), G::kVScaleAt, t % kKvSlab, b));
-        if (__any_sync(0xffffffffu, no)) return __int_as_float(0x7fffffff);
+    const float *src = a.q + static_cast<int64_t>(r.q0 + i) * a.q_stride + static_cast<int64_t>(seg.kvh * a.group + col - i * a.group) * G::kDim + lane;
+    float q[NB], o[NB], m = -INFINITY, l = 0.0f;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        q[b] = src[b * kQK];
+        o[b] = 0.0f;
     }
-    const float *q = a.q + static_cast<int64_t>(r.q0 + i) * a.q_stride + static_cast<int64_t>(seg.kvh * a.group + col - i * a.group) * G::kDim + lane;
-    float sum = 0.0f;
+#pragma unroll 1
     for (int t = low; t < end; ++t) {
-        const uint8_t *tile = tile_of(t / kKvSlab);
-        const int tok = t % kKvSlab;
+        const int slab = t / kKvSlab, tok = t % kKvSlab, slot = a.by_page_tiles.div(slab);
+        const uint8_t *tile = head + table[slot] * a.c.page_bytes + static_cast<int64_t>(a.by_page_tiles.mod(slab, slot)) * G::kTileBytes;
+        const __half *scales = reinterpret_cast<const __half *>(tile + G::kKScaleAt);  // then V's
         float s = 0.0f;
-        for (int k = 0; k < NB; ++k) {
-            const uint32_t code = reinterpret_cast<const uint32_t *>(tile)[G::k_word(tok, k, lane / 8)] >> 4 * (lane % 8) & 15u;
-            s = fmaf(q[k * kQK], scale_of(tile, G::kKScaleAt, tok, k) * (static_cast<float>(code) - 8.0f), s);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            const uint32_t code = reinterpret_cast<const uint32_t *>(tile)[G::k_word(tok, b, lane / 8)] >> 4 * (lane % 8) & 15u;
+            s = fmaf(q[b], __half2float(scales[G::scale_half(tok, b)]) * (static_cast<float>(code) - 8.0f), s);
         }
 #pragma unroll
         for (int k = 16; k > 0; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
-        const uint32_t code = reinterpret_cast<const uint16_t *>(tile + G::kVAt)[G::v_half(tok, b, lane / 4)] >> 4 * (lane % 4) & 15u;
-        sum = fmaf(exp2_approx(fmaf(s, a.scale_log2, kAttnUnit - m)), scale_of(tile, G::kVScaleAt, tok, b) * (static_cast<float>(code) - 8.0f), sum);
+        s *= a.scale_log2;
+        const float to = fmaxf(m, s), keep = m == -INFINITY ? 0.0f : exp2_approx(m - to), p = exp2_approx(__fadd_rn(s, -to) + kAttnUnit);
+        m = to;
+        l = fmaf(l, keep, p);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            const uint32_t code = reinterpret_cast<const uint16_t *>(tile + G::kVAt)[G::v_half(tok, b, lane / 4)] >> 4 * (lane % 4) & 15u;
+            const float v = __half2float(scales[G::kScaleBytes / 2 + G::scale_half(tok, b)]) * (static_cast<float>(code) - 8.0f);
+            o[b] = fmaf(o[b], keep, p * v);
+        }
     }
-    return sum;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) sum[row * G::kDim + 4 * ((8 * b + lane / 4) ^ (row & 7)) + lane % 4] = o[b];
+    if (lane == 0) {
+        row_m = m;
+        row_l = l;
+    }
 }
 
 template <int NB> __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(AttnArgs a) {
@@ -598,7 +608,7 @@ template <int NB> __global__ void __launch_bounds__(kPromptThreads, 1) attn_prom
         uint64_t no = 0;  // 0 times a sum that is no number
 #pragma unroll
         for (int k = 0; k < D / 4; ++k) no = f2_fma(acc[k], 0, no);
-        if (!(f2_parts(no).x + f2_parts(no).y == 0.0f)) sh_redo = 1;
+        if (!(f2_parts(no).x + f2_parts(no).y == 0.0f) || score_huge(m)) sh_redo = 1;
         const float2 ls = f2_parts(l2);
         sh_l[half][row] = ls.x + ls.y;
         __syncthreads();  // the products are done; their operands' memory takes the sums
@@ -624,11 +634,13 @@ template <int NB> __global__ void __launch_bounds__(kPromptThreads, 1) attn_prom
     tm_after_sync();
     if (warp == 16) tm_free(tm);
     if (sh_redo && !sh_bad && !r.bad) {
-        for (int k = warp; k < kPromptRows * NB; k += kPromptThreads / 32) {
-            const int row = k / NB, b = k % NB, col = seg.ct * kPromptRows + row;
-            float *at = sum + row * D + 4 * ((8 * b + lane / 4) ^ (row & 7)) + lane % 4;
-            const bool no = col < r.n * a.group && isfinite(sh_l[0][row]) && !isfinite(*at);
-            if (__any_sync(0xffffffffu, no)) *at = attn_redo<NB>(a, seg, col, b, sh_m[row], lane);
+        for (int row = warp; row < kPromptRows; row += kPromptThreads / 32) {
+            const int col = seg.ct * kPromptRows + row;
+            if (col >= r.n * a.group) break;
+            bool no = false;
+            for (int e = lane; e < D; e += 32) no |= !isfinite(sum[row * D + e]);
+            if (score_huge(sh_m[row]) || (__any_sync(0xffffffffu, no) && isfinite(sh_l[0][row])))
+                attn_redo<NB>(a, seg, col, row, sum, sh_m[row], sh_l[0][row], lane);
         }
         __syncthreads();
     }
