@@ -22,6 +22,7 @@ constexpr int kRaggedChunk = 128;
 constexpr int kEnds = 8;
 constexpr int kPromptCols = 128;  // of a CTA of the form on tcgen05
 constexpr int kTallEnds = 32, kTallJoin = 1;  // ... of the form on tcgen05: its start, and the join's loads of four parts for 2560 values
+constexpr int kMostTokens = 0x7fffff00;  // so that a tile's end past the last token is a number too
 constexpr int kCounters = ZDMMV_ATTN_COUNTER_BYTES / 4;
 
 int device_sms() {
@@ -211,7 +212,7 @@ zdmmv_status zdmmv_attn_q4_0(const zdmmv_kv_cache *cache, const zdmmv_attn_args 
     if (!a.fault) return ZDMMV_ERR_CUDA;
     a.q_stride = g.q_stride;
     a.n_tok = g.n_tok; a.n_q_heads = g.n_q_heads; a.group = g.n_q_heads / cache->n_kv_heads;
-    a.max_q_len = g.max_q_len; a.max_kv_len = g.max_kv_len; a.window = g.window;
+    a.max_q_len = g.max_q_len; a.max_kv_len = std::min(g.max_kv_len, kMostTokens); a.window = g.window;
     a.scale_log2 = g.scale * 1.44269504088896340736f;
     a.by_ct = FastDiv::of(p.n_ct);
     a.by_heads = FastDiv::of(cache->n_kv_heads);

@@ -671,7 +671,7 @@ typedef struct {
 
 /* The lengths and the page table are read on the device (a captured graph
  * replays with new ones, within max_q_len and max_kv_len). A sequence with
- * kv_len < 0, kv_len > max_kv_len or past its max_pages pages, with a page
+ * kv_len < 0, kv_len > max_kv_len (or 2^31 - 256) or past its max_pages pages, with a page
  * number outside 0..n_pages-1 where it would read, or with more new tokens than
  * max_q_len is bad: the rows of it that the grid covers are NaN, nothing is read
  * out of range. Tokens at and past kv_len may hold anything, and so may, for a
