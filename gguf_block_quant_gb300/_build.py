@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import os
+import re
 import shutil
 import subprocess
 
@@ -21,6 +22,16 @@ LIB = os.path.join(OUT_DIR, "libzdmmv.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
               "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]
+
+
+# Kernels that share their registers out again among their warps, and the registers a thread that their shares add up to: compiled
+# with any other number they are refused at their first launch, which is late to hear of it.
+REGISTERS = {"zdmmv_attn_prompt.cu": ("attn_prompt_kernel", 96)}
+
+
+def registers_of(log: str, kernel: str) -> list[int]:
+    """The registers that ptxas -v reports for a kernel's instances."""
+    return [int(n) for n in re.findall(r"Compiling entry function '[^']*" + kernel + r"[^']*'.*?Used (\d+) registers", log, re.S)]
 
 
 def nvcc() -> str:
@@ -60,7 +71,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
         obj = os.path.join(OUT_DIR, os.path.basename(src)[:-3] + ".o")
         objs.append(obj)
         cmd = [cc, *ARCH, *NVCC_FLAGS, "-c", src, "-o", obj]
-        if ptxas_verbose:
+        if ptxas_verbose or os.path.basename(src) in REGISTERS:
             cmd += ["-Xptxas", "-v"]
         jobs.append(cmd)
 
@@ -74,7 +85,10 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
                 print(" ".join(cmd))
                 print(r.stdout, r.stderr)
             if r.returncode != 0:
-                raise RuntimeError(f"nvcc failed on {cmd[-3]}")
+                raise RuntimeError(f"nvcc failed on {cmd[cmd.index('-c') + 1]}")
+            kernel, want = REGISTERS.get(os.path.basename(cmd[cmd.index("-c") + 1]), (None, 0))
+            if kernel and set(registers_of(r.stdout + r.stderr, kernel)) != {want}:
+                raise RuntimeError(f"{kernel}: {registers_of(r.stdout + r.stderr, kernel)} registers a thread, its warps' shares are of {want}")
     tmp = LIB + f".tmp{os.getpid()}"
     link = [cc, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(link, capture_output=True, text=True)
