@@ -272,8 +272,8 @@ template <int NB, bool FAST> __global__ void __launch_bounds__(kAppendWarps * 32
 // the next kStreamSlots of them on their way into its own ring in shared memory (a bulk copy a head), so that the loads
 // wait neither for the token's look-up nor for the quantization; a token's place, cosines and sines are read once and
 // kept for all its heads. 4093 tokens of 48 heads of 128: one warp a head without the ring 49 us at best (48 warps an
-// SM, each with its loads in flight for half of its life), with it 37.6 us (75% of the copy rate), then bound by issue (68%
-// active; 41 us of 154 instructions a head before the token's row addresses were found once).
+// SM, each with its loads in flight for half of its life), with it 37.0 us (76% of the copy rate), then bound by issue (67%
+// active, 135 instructions a head; 41 us with 154 before the token's row addresses were found once).
 constexpr int kStreamWarps = 8, kStreamHeads = 4, kStreamSlots = 3;
 template <int NB, bool FAST> __global__ void __launch_bounds__(kStreamWarps * 32, NB <= 4 ? 3 : 2) kv_append_stream_kernel(AppendArgs a, int n_jobs) {
     using G = KvGeom<NB>;
