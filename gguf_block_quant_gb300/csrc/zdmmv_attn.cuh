@@ -41,8 +41,8 @@
 // columns and share a ring.
 //
 // What it reaches. One sequence of 130975 tokens, 8 kv heads of 128, 4 columns (the narrow kernel): 35.7 us, 62% of the
-// copy rate, of which some 12 us are the kernel's ends; at 2^20 tokens 217 us, 82%. 64 sequences of up to 16384 tokens:
-// 96.8 us (65%). The narrow kernel is bound by its instructions as much as by memory (issue 60%, ALU 46% at 131K tokens).
+// copy rate, of which some 12 us are the kernel's ends; at 2^20 tokens 218 us, 82%. 64 sequences of up to 16384 tokens:
+// 97.2 us (65%). The narrow kernel is bound by its instructions as much as by memory (issue 61%, ALU 47% at 131K tokens).
 #pragma once
 
 #include <type_traits>

@@ -8,7 +8,7 @@
 // neighbouring threads a block. Bound by memory with many rows (4 + 4 bytes in,
 // 4 + 34/32 out, 2 with y, a value): 4096 x 4096 takes 40.2 us, 93% of the copy rate.
 // By latency with few: then V = 1, as many
-// threads as the row has float4 (8 x 4096: 2.7 us, 1 x 2048: 2.0 us).
+// threads as the row has float4 (8 x 4096: 2.8 us, 1 x 2048: 2.1 us).
 #include <cmath>
 
 #include "zdmmv_kv.cuh"
