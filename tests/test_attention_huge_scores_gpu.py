@@ -30,13 +30,28 @@ def put_k(tile, dim, tok, codes, scale):
 def test_the_largest_score_takes_all(dim, group, new, size):
     """Every token's K is the same direction u, of a length of its own, and q is size times u: scores of one sign, whose
     neighbours are 1 / 100 of their size apart or more."""
+    takes_all(dim, group, new, size, [90, 37], 2, lambda n: np.linspace(0.05, 0.3, n))
+
+
+@pytest.mark.parametrize("dim, group, new", [(128, 4, 1), (64, 8, 1), (192, 20, 5), (64, 8, 8), (128, 8, 16)])
+@pytest.mark.parametrize("size", [1e7, 1e22, -1e22])
+def test_the_largest_score_of_many_parts(dim, group, new, size):
+    """The same over a length whose parts are joined; all but a few tokens are as long as one another."""
+    def lengths(n):
+        d = np.full(n, 0.2)
+        d[:4] = 0.31, 0.3, 0.05, 0.06
+        return d
+    takes_all(dim, group, new, size, [4000], 1, lengths)
+
+
+def takes_all(dim, group, new, size, lens, heads, lengths):
     rng = np.random.default_rng(dim + group)
-    lens, heads, page = [90, 37], 2, 32
+    page = 32
     cache, pages, table = random_cache(rng, lens, page, heads, dim)
     u = np.where(rng.random((heads, dim)) < 0.5, 1, -1)
     d = np.zeros((len(lens), max(lens)))
     for s, n in enumerate(lens):
-        d[s, :n] = rng.permutation(np.linspace(0.05, 0.3, n))
+        d[s, :n] = rng.permutation(lengths(n))
         for tok in range(n):
             for h in range(heads):
                 put_k(pages.reshape(-1, heads, page // 16, 18 * dim)[table[s, tok // page], h, tok % page // 16], dim, tok % 16,

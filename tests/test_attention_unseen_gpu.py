@@ -71,3 +71,31 @@ def test_a_value_that_the_append_stores_as_infinity():
         outs.append(Z.attn_q4_0(cache, q[:new].contiguous(), dev(np.array([0, new], np.int32)), dev(np.array([last], np.int32)), new, n))
     assert torch.isfinite(outs[1]).all() and not torch.isfinite(outs[0][3, :, :32]).any()
     assert torch.allclose(outs[0][:3], outs[1], rtol=1e-4, atol=1e-5)
+
+
+@pytest.mark.parametrize("dim, group, new", [(128, 4, 1), (64, 4, 3), (128, 8, 2), (192, 8, 5), (256, 16, 5), (64, 8, 8), (96, 8, 5),
+                                             (128, 8, 16)])
+@pytest.mark.parametrize("window", [0, 2000])
+def test_non_finite_tokens_in_long_sequences(dim, group, new, window):
+    """The same where a row's sums are joined from parts, some of which have such a token."""
+    rng = np.random.default_rng(dim + group + new)
+    lens, heads, page = [5003], 1, 64
+    cache, pages, table = random_cache(rng, lens, page, heads, dim)
+    spoilt, n, nb = pages.copy(), lens[0], dim // 32
+    if window:
+        spoil(spoilt, table, page, heads, dim, 0, n - new - window, 1, np.nan, np.arange(nb))
+    if new > 1:
+        spoil(spoilt, table, page, heads, dim, 0, n - 1, 1, np.inf, np.array([0]))
+    cache.pages.copy_(dev(spoilt))
+    q = rng.standard_normal((new, heads * group, dim)).astype(np.float32)
+    out, q_start = attend(cache, q, lens, [new], window=window)
+    if new > 1:
+        assert not torch.isfinite(out[-1, :, :32]).any() and torch.isfinite(out[-1, :, 32:]).all()
+        k, v = R.values(pages, page, heads, dim)
+        want = R.attention(q, q_start, lens, table, k, v, page, dim ** -0.5, window)[0]
+        out[-1, :, :32] = dev(want[-1, :, :32].astype(np.float32))
+    args = (out, q, q_start, lens, table, pages, page, heads, dim)
+    if dim <= 128 and group * new > 16:
+        C.check(*args, dim ** -0.5, window)
+    else:
+        check_attention(*args, window=window)
