@@ -25,8 +25,8 @@
 //  * Product with V: A = the codes' dimensions x 16 tokens, B = x = p * d_v (V's
 //    scales are per token and block) in two fp16 parts, formed in fp16: with p =
 //    ph + pl, xh = ph * d_v rounded, xl = pl * d_v + (ph * d_v - xh), whose bracket
-//    one fma gives exactly. p is in units of 2^-13, so that p and x stay below 2^15
-//    while |d_v| < 2: fp16's lowest unit of 2^-24 is then 2^-38 of the largest p.
+//    one fma gives exactly. p is in units of 2^-13, so that x is an fp16
+//    number while |d_v| < 7: fp16's lowest unit of 2^-24 is then 2^-38 of the largest p.
 //    32 tokens of which one has a larger scale take x = p * d_v in fp32 instead,
 //    split in the unit of each column's and block's largest x, so that large values
 //    cost neither other blocks nor other tokens their precision, and infinities and
@@ -92,11 +92,11 @@ __host__ __device__ constexpr int attn_ctas_per_sm(int nb, int nt) { return nb *
 __host__ __device__ constexpr bool attn_sums_apart(int nb, int nt, int form) { return form == kOwn && nb * nt < 16; }
 constexpr int kAttnBarBytes = 256;  // two barriers a slot
 constexpr float kAttnUnit = 13.0f;  // p is in units of 2^-kAttnUnit
-// From scores of this size on (in powers of two) a float's step is a part of p that counts: p is then of the rounded score less
-// the maximum, not of both in one fma, which would leave the largest score's own rounding in the exponent of every p (2^64 of
-// it at 2^30).
-constexpr float kHugeScore = 8388608.0f;
-__device__ __forceinline__ bool score_huge(float m) { return fabsf(m) >= kHugeScore && m != -INFINITY; }
+// From scores of some size on (in powers of two) a float's step is a part of p that counts: p is then of the rounded score less
+// the maximum, not of both in one fma, which would leave the largest score's own rounding in the exponent of every p: below
+// 2^(1/32) of it at 2^20 (of the products here), below 2^(1/4) at 2^23 (tcgen05), 2^64 at 2^30.
+constexpr float kHugeScore = 1048576.0f, kHugeScoreTall = 8388608.0f;
+__device__ __forceinline__ bool score_huge(float m, float from) { return fabsf(m) >= from && m != -INFINITY; }
 constexpr int kJoinAhead = 16;
 
 // What a CTA (and the join) works on, from the lengths on the device.
@@ -460,14 +460,21 @@ __device__ __forceinline__ void q_unit(float top, float scale, float &up, float 
     up = __uint_as_float((static_cast<uint32_t>(e + 127) << 23) | (scale < 0.0f ? 0x80000000u : 0u));
     down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
 }
-// Whether a scale of the warp's tokens is 2 or more (bit 14 of an fp16 number).
+// Whether a scale of the warp's tokens is 7 or more, so that p times it may be no fp16 number. Bit 14 says 2 or more: the others
+// are looked at only then.
 template <int NB> __device__ __forceinline__ bool scales_large(const uint32_t (&dv)[4][NB]) {
     uint32_t any = 0;
 #pragma unroll
     for (int h = 0; h < 4; ++h)
 #pragma unroll
         for (int b = 0; b < NB; ++b) any |= dv[h][b];
-    return __any_sync(0xffffffffu, (any & 0x40004000u) != 0);
+    if (!__any_sync(0xffffffffu, (any & 0x40004000u) != 0)) return false;
+    uint32_t top = 0;
+#pragma unroll
+    for (int h = 0; h < 4; ++h)
+#pragma unroll
+        for (int b = 0; b < NB; ++b) top = max(top, max(dv[h][b] & 0x7fffu, dv[h][b] >> 16 & 0x7fffu));
+    return __any_sync(0xffffffffu, top >= 0x4700u);
 }
 // Which of a lane's tokens tok, tok + 1, tok + 8, ... of a unit are in low .. end - 1, a bit each.
 __device__ __forceinline__ uint32_t seen_tokens(int tok, int low, int end) {
@@ -871,7 +878,7 @@ template <int NB> __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_
             l *= keep;
 #pragma unroll
             for (int k = 0; k < 2 * NB; ++k) o[k] = f2_mul(o[k], f2(keep, keep));
-            huge = __any_sync(0xffffffffu, score_huge(m));
+            huge = __any_sync(0xffffffffu, score_huge(m, kHugeScore));
         }
         float base = m == -INFINITY ? 0.0f : m - kAttnUnit, unit = qs;
         if (huge) {
@@ -1332,7 +1339,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, FORM != kOwn ? 1 : attn_ctas_
             }
             bool any = false;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) any |= score_huge(m[nt]);
+            for (int nt = 0; nt < NT; ++nt) any |= score_huge(m[nt], kHugeScore);
             huge = __any_sync(0xffffffffu, any);
         }
         uint32_t ph[NT][4], pl[NT][4];

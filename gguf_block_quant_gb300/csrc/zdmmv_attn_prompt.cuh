@@ -229,7 +229,7 @@ template <int NB> struct PromptFeed {
 // A row once more, token by token, by a warp with a lane for a dimension of each block: what the row sees of the split, its sums
 // to `sum` (column's quads exchanged as the kernel has them), its maximum and sum of p. Two kinds of rows need it, neither of
 // ordinary calls: where V is an infinity or NaN the products are NaN for rows that do not see it (0 times NaN); and from scores
-// of kHugeScore on the fma of p's exponent does not do. (In the tiles' loops the one cost every call 2 to 10% of its time, the
+// of kHugeScoreTall on the fma of p's exponent does not do. (In the tiles' loops the one cost every call 2 to 10% of its time, the
 // other 2.)
 template <int NB>
 __device__ __forceinline__ void attn_redo(const AttnArgs &a, const AttnSeg &seg, int col, int row, float *sum, float &row_m, float &row_l, int lane) {
@@ -608,7 +608,7 @@ template <int NB> __global__ void __launch_bounds__(kPromptThreads, 1) attn_prom
         uint64_t no = 0;  // 0 times a sum that is no number
 #pragma unroll
         for (int k = 0; k < D / 4; ++k) no = f2_fma(acc[k], 0, no);
-        if (!(f2_parts(no).x + f2_parts(no).y == 0.0f) || score_huge(m)) sh_redo = 1;
+        if (!(f2_parts(no).x + f2_parts(no).y == 0.0f) || score_huge(m, kHugeScoreTall)) sh_redo = 1;
         const float2 ls = f2_parts(l2);
         sh_l[half][row] = ls.x + ls.y;
         __syncthreads();  // the products are done; their operands' memory takes the sums
@@ -639,7 +639,7 @@ template <int NB> __global__ void __launch_bounds__(kPromptThreads, 1) attn_prom
             if (col >= r.n * a.group) break;
             bool no = false;
             for (int e = lane; e < D; e += 32) no |= !isfinite(sum[row * D + e]);
-            if (score_huge(sh_m[row]) || (__any_sync(0xffffffffu, no) && isfinite(sh_l[0][row])))
+            if (score_huge(sh_m[row], kHugeScoreTall) || (__any_sync(0xffffffffu, no) && isfinite(sh_l[0][row])))
                 attn_redo<NB>(a, seg, col, row, sum, sh_m[row], sh_l[0][row], lane);
         }
         __syncthreads();

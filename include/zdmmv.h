@@ -642,7 +642,7 @@ zdmmv_status zdmmv_kv_append_q4_0(const zdmmv_kv_cache *cache, const zdmmv_kv_ap
  * exact there, the blocks' scales, all sums and the softmax's statistics are
  * fp32: the result is that of fp32 arithmetic on the cache's values, with these
  * limits. q counts to 2^-34 of its row's largest, and p times a scale of V below
- * 2 to 2^-38 of the row's largest p. With more than 16 query rows (new tokens
+ * 7 to 2^-38 of the row's largest p. With more than 16 query rows (new tokens
  * times the heads of a kv head) and heads of up to 128 dimensions, p counts to
  * 2^-38 of the row's largest whatever V is; and where one of 128 tokens has a
  * scale of 2^13 or more (a value past 65000 in its block of 32), the scales of
