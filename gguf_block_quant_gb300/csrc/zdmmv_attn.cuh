@@ -25,8 +25,8 @@
 //  * Product with V: A = the codes' dimensions x 16 tokens, B = x = p * d_v (V's
 //    scales are per token and block) in two fp16 parts, formed in fp16: with p =
 //    ph + pl, xh = ph * d_v rounded, xl = pl * d_v + (ph * d_v - xh), whose bracket
-//    one fma gives exactly. p is in units of 2^-13, so that x is an fp16
-//    number while |d_v| < 7: fp16's lowest unit of 2^-24 is then 2^-38 of the largest p.
+//    one fma gives exactly. p is in units of 2^-13, so that x is an fp16 number while
+//    |d_v| < 7: half of fp16's lowest unit, 2^-24, is then 2^-38 of the largest p.
 //    32 tokens of which one has a larger scale take x = p * d_v in fp32 instead,
 //    split in the unit of each column's and block's largest x, so that large values
 //    cost neither other blocks nor other tokens their precision, and infinities and
@@ -40,9 +40,9 @@
 // workspace). More columns: the grid is (column tile of an item) x (split of its tokens), the warps split the
 // columns and share a ring.
 //
-// What it reaches. One sequence of 130975 tokens, 8 kv heads of 128, 4 columns (the narrow kernel): 35.7 us, 62% of the
-// copy rate, of which some 12 us are the kernel's ends; at 2^20 tokens 218 us, 82%. 64 sequences of up to 16384 tokens:
-// 97.2 us (65%). The narrow kernel is bound by its instructions as much as by memory (issue 61%, ALU 47% at 131K tokens).
+// What it reaches. One sequence of 130975 tokens, 8 kv heads of 128, 4 columns (the narrow kernel): 36.2 us, 61% of the
+// copy rate, of which some 12 us are the kernel's ends; at 2^20 tokens 220 us, 81%. 64 sequences of up to 16384 tokens:
+// 98.0 us (64%). The narrow kernel is bound by its instructions as much as by memory (issue 61%, ALU 47% at 131K tokens).
 #pragma once
 
 #include <type_traits>
