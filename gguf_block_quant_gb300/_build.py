@@ -26,7 +26,7 @@ NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompil
 
 # Kernels that share their registers out again among their warps, and the registers a thread that their shares add up to: compiled
 # with any other number they are refused at their first launch, which is late to hear of it.
-REGISTERS = {"zdmmv_attn_prompt.cu": ("attn_prompt_kernel", 96)}
+REGISTERS = {"zdmmv_attn_prompt.cu": ("attn_prompt_kernel", 96), "zdmmv_attn_prompt_tree.cu": ("attn_prompt_kernel", 96)}
 
 
 def registers_of(log: str, kernel: str) -> list[int]:

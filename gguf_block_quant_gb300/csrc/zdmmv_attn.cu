@@ -1,4 +1,4 @@
-// zdmmv_attn.cu -- zdmmv_attn_q4_0: argument checks and the plan of the launch
+// zdmmv_attn.cu -- zdmmv_attn_q4_0 and zdmmv_attn_tree_q4_0: argument checks and the plan of the launch
 // (the kernels: zdmmv_attn.cuh).
 #include <algorithm>
 #include <cmath>
@@ -24,6 +24,7 @@ constexpr int kPromptCols = 128;  // of a CTA of the form on tcgen05
 constexpr int kTallEnds = 32, kTallJoin = 1;  // ... of the form on tcgen05: its start, and the join's loads of four parts for 2560 values
 constexpr int kMostTokens = 0x7fffff00;  // so that a tile's end past the last token is a number too
 constexpr int kCounters = ZDMMV_ATTN_COUNTER_BYTES / 4;
+constexpr int kMostWords = 1 << 20;  // of a row of bits, so that 32 times their number is a number too
 
 int device_sms() {
     static const int sms = [] {
@@ -168,23 +169,8 @@ size_t attn_bounds_bytes(const KvView &c, int head_dim, int group, int64_t colum
     return std::max(most, attn_parts_bytes(std::min(4 * f.slots, heads * ceil_div(columns, top) * steps), top, head_dim));
 }
 
-}  // namespace
-}  // namespace zdmmv
-
-using namespace zdmmv;
-
-extern "C" {
-
-size_t zdmmv_attn_q4_0_workspace_bytes(const zdmmv_kv_cache *cache, int n_q_heads, int max_q_len, int max_kv_len) {
-    KvView c{};
-    if (kv_check(cache, &c) != ZDMMV_OK || n_q_heads < 1 || n_q_heads > 65535 || n_q_heads % c.n_kv_heads || max_q_len < 1 ||
-        max_kv_len < 0)
-        return 0;
-    const int group = n_q_heads / c.n_kv_heads;
-    return attn_bounds_bytes(c, cache->head_dim, group, static_cast<int64_t>(max_q_len) * group, max_kv_len);
-}
-
-zdmmv_status zdmmv_attn_q4_0(const zdmmv_kv_cache *cache, const zdmmv_attn_args *args, zdmmv_stream_t stream) {
+// `tree`: nullptr, or its checked fields
+zdmmv_status attn_call(const zdmmv_kv_cache *cache, const zdmmv_attn_args *args, const zdmmv_attn_tree *tree, zdmmv_stream_t stream) {
     if (!args) return ZDMMV_ERR_NULL;
     AttnArgs a{};
     const zdmmv_status st = kv_check(cache, &a.c);
@@ -194,15 +180,19 @@ zdmmv_status zdmmv_attn_q4_0(const zdmmv_kv_cache *cache, const zdmmv_attn_args 
     if (g.n_tok < 0 || g.n_q_heads < 1 || g.n_q_heads > 65535 || g.n_q_heads % cache->n_kv_heads || g.max_q_len < 1 ||
         g.max_kv_len < 0 || g.window < 0 || !std::isfinite(g.scale))
         return ZDMMV_ERR_SHAPE;
+    const bool seen = tree && tree->seen;
+    if (seen && (tree->seen_words < 1 || tree->seen_words > kMostWords || static_cast<int64_t>(tree->seen_words) * 32 < g.max_q_len))
+        return ZDMMV_ERR_SHAPE;
     // with a window, no column tile sees more than the window and its own new tokens
-    const int64_t seen = g.window > 0 ? std::min<int64_t>(g.max_kv_len, static_cast<int64_t>(g.window) + g.max_q_len + kKvSlab)
+    const int64_t most = g.window > 0 ? std::min<int64_t>(g.max_kv_len, static_cast<int64_t>(g.window) + g.max_q_len + kKvSlab)
                                       : g.max_kv_len;
-    if (!attn_plan(a.c, cache->head_dim, g.n_q_heads, g.max_q_len, seen, &p)) return ZDMMV_ERR_SHAPE;
+    if (!attn_plan(a.c, cache->head_dim, g.n_q_heads, g.max_q_len, most, &p)) return ZDMMV_ERR_SHAPE;
     if (g.n_tok == 0) return ZDMMV_OK;
     if (!g.q || !g.q_start || !g.kv_len || !g.out) return ZDMMV_ERR_NULL;
     if (g.q_stride < static_cast<int64_t>(g.n_q_heads) * cache->head_dim) return ZDMMV_ERR_SHAPE;
     if (kv_misaligned(g.q, 16) || kv_misaligned(g.out, 16) || kv_misaligned(g.workspace, 16) ||
-        kv_misaligned(g.q_start, 4) || kv_misaligned(g.kv_len, 4) || kv_misaligned(g.status_dev, 4) || g.q_stride % 4)
+        kv_misaligned(g.q_start, 4) || kv_misaligned(g.kv_len, 4) || kv_misaligned(g.status_dev, 4) || g.q_stride % 4 ||
+        (tree && (kv_misaligned(tree->seen, 4) || kv_misaligned(tree->lse, 4))))
         return ZDMMV_ERR_ALIGN;
     const size_t need = attn_parts_bytes(p.parts, p.cols, cache->head_dim);  // of the plan that is launched
     if (need && !g.workspace) return ZDMMV_ERR_NULL;
@@ -223,16 +213,47 @@ zdmmv_status zdmmv_attn_q4_0(const zdmmv_kv_cache *cache, const zdmmv_attn_args 
     a.count = static_cast<uint32_t *>(g.workspace);
     a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(g.workspace) + ZDMMV_ATTN_COUNTER_BYTES);
     a.part_ml = reinterpret_cast<float2 *>(a.part + p.parts * p.cols * cache->head_dim);
+    const bool more = tree && (tree->seen || tree->lse);
+    if (more) {
+        a.seen = tree->seen;
+        a.lse = tree->lse;
+        a.seen_words = tree->seen_words;
+    }
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e = cudaErrorInvalidValue;
     switch (kv_blocks(cache->head_dim)) {
-    case 2: e = launch_attn<2>(a, p, s); break;
-    case 3: e = launch_attn<3>(a, p, s); break;
-    case 4: e = launch_attn<4>(a, p, s); break;
-    case 6: e = launch_attn<6>(a, p, s); break;
-    case 8: e = launch_attn<8>(a, p, s); break;
+    case 2: e = more ? launch_attn<2, true>(a, p, s) : launch_attn<2, false>(a, p, s); break;
+    case 3: e = more ? launch_attn<3, true>(a, p, s) : launch_attn<3, false>(a, p, s); break;
+    case 4: e = more ? launch_attn<4, true>(a, p, s) : launch_attn<4, false>(a, p, s); break;
+    case 6: e = more ? launch_attn<6, true>(a, p, s) : launch_attn<6, false>(a, p, s); break;
+    case 8: e = more ? launch_attn<8, true>(a, p, s) : launch_attn<8, false>(a, p, s); break;
     }
     return e == cudaSuccess ? ZDMMV_OK : ZDMMV_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace zdmmv
+
+using namespace zdmmv;
+
+extern "C" {
+
+size_t zdmmv_attn_q4_0_workspace_bytes(const zdmmv_kv_cache *cache, int n_q_heads, int max_q_len, int max_kv_len) {
+    KvView c{};
+    if (kv_check(cache, &c) != ZDMMV_OK || n_q_heads < 1 || n_q_heads > 65535 || n_q_heads % c.n_kv_heads || max_q_len < 1 ||
+        max_kv_len < 0)
+        return 0;
+    const int group = n_q_heads / c.n_kv_heads;
+    return attn_bounds_bytes(c, cache->head_dim, group, static_cast<int64_t>(max_q_len) * group, max_kv_len);
+}
+
+zdmmv_status zdmmv_attn_q4_0(const zdmmv_kv_cache *cache, const zdmmv_attn_args *args, zdmmv_stream_t stream) {
+    return attn_call(cache, args, nullptr, stream);
+}
+
+zdmmv_status zdmmv_attn_tree_q4_0(const zdmmv_kv_cache *cache, const zdmmv_attn_args *args, const zdmmv_attn_tree *tree,
+                                  zdmmv_stream_t stream) {
+    return tree ? attn_call(cache, args, tree, stream) : ZDMMV_ERR_NULL;
 }
 
 }  // extern "C"

@@ -69,6 +69,10 @@ struct AttnArgs {
     int32_t round;      // ... whose length is a multiple of this power of two
     int32_t wc;         // warps that split the columns (the others split the tokens)
     float scale_log2;
+    // of the TREE instances alone
+    const uint32_t *seen;  // nullable: the new tokens' rows of bits, `seen_words` words each
+    float *lse;            // nullable: [n_tok][n_q_heads]
+    int32_t seen_words;
 };
 
 constexpr int kAttnWarps = 8, kAttnThreads = kAttnWarps * 32;
@@ -106,7 +110,7 @@ struct AttnRange {
     bool bad;
     int slab0, slabs;  // tiles that any column of the column tile sees
 };
-__device__ __forceinline__ AttnRange attn_range(const AttnArgs &a, int seq, int ct, int cols) {
+template <bool TREE> __device__ __forceinline__ AttnRange attn_range(const AttnArgs &a, int seq, int ct, int cols) {
     AttnRange r;
     const int q0 = a.q_start[seq], q1 = a.q_start[seq + 1];
     r.len = a.kv_len[seq];
@@ -115,11 +119,47 @@ __device__ __forceinline__ AttnRange attn_range(const AttnArgs &a, int seq, int 
     r.q0 = min(max(q0, 0), a.n_tok);
     r.n = max(0, min(q1, a.n_tok) - r.q0);
     const int i0 = a.by_group.div(ct * cols), i1 = min(r.n - 1, a.by_group.div(ct * cols + cols - 1));
-    const int end = max(0, r.len - (r.n - 1 - i1));
-    const int low = a.window > 0 ? max(0, r.len - (r.n - 1 - i0) - a.window) : 0;
+    int end = max(0, r.len - (r.n - 1 - i1));
+    int low = a.window > 0 ? max(0, r.len - (r.n - 1 - i0) - a.window) : 0;
+    if constexpr (TREE) {
+        if (a.seen) {
+            end = r.len;
+            low = a.window > 0 ? max(0, max(0, r.len - r.n) - a.window) : 0;
+        }
+    }
     r.slab0 = low / kKvSlab;
     r.slabs = r.bad ? 0 : max(0, (end + kKvSlab - 1) / kKvSlab - r.slab0);
     return r;
+}
+
+// The order of a tree of new tokens (the TREE instances, where a.seen is not null). The sequence's new tokens are the last n of
+// its cache; new token i sees the tokens before them, with a window the last of those that its own ones leave of it, and of the
+// new ones those that its row of bits names. The kernels test the bits in the tiles from the first new token on, which are the
+// last of a sequence: a row's 32 bits of a unit are two words that come from the cache, shifted together; nothing is kept in
+// registers over the tiles before, so that the instances for a tree cost what the others do.
+__device__ __forceinline__ uint32_t tree_word(const AttnArgs &a, const AttnRange &r, const uint32_t *row, int k) {
+    if (k < 0) return ~0u;  // before the new tokens
+    const int left = min(r.n, 32 * a.seen_words) - 32 * k;
+    if (left <= 0) return 0u;
+    const uint32_t w = __ldg(row + k);
+    return left >= 32 ? w : w & ((1u << left) - 1u);
+}
+__device__ __forceinline__ const uint32_t *tree_row(const AttnArgs &a, const AttnRange &r, int i) {
+    return a.seen + static_cast<int64_t>(r.q0 + i) * a.seen_words;
+}
+// Which of the cache's tokens tok .. tok + 31 new token i (0 .. n - 1) sees, the window left out of account.
+__device__ __forceinline__ uint32_t tree_bits(const AttnArgs &a, const AttnRange &r, int i, int tok) {
+    const int j = tok - (r.len - r.n);
+    const uint32_t *row = tree_row(a, r, i);
+    return __funnelshift_r(tree_word(a, r, row, j >> 5), tree_word(a, r, row, (j >> 5) + 1), j & 31);
+}
+// The first token that it sees.
+__device__ __forceinline__ int tree_low(const AttnArgs &a, const AttnRange &r, int i) {
+    if (a.window == 0) return 0;
+    const uint32_t *row = tree_row(a, r, i);
+    int own = 0;
+    for (int k = 0; k < a.seen_words; ++k) own += __popc(tree_word(a, r, row, k));
+    return max(0, r.len - r.n - max(0, a.window - own));
 }
 
 // One CTA's share of an item: tiles first .. last-1, and where its sums go where others share the item.
@@ -141,13 +181,13 @@ struct AttnSeg {
 // there is none. (Splitting each of several sequences by its own length cuts the short ones up for nothing: 22.4 instead of
 // 15 us for 8 sequences of 3 to 8191 tokens and 16 heads.)
 constexpr int kMinChunk = kStepTiles;
-__device__ __forceinline__ bool attn_grid_seg(const AttnArgs &a, int cols, AttnSeg &g) {
+template <bool TREE> __device__ __forceinline__ bool attn_grid_seg(const AttnArgs &a, int cols, AttnSeg &g) {
     const int item = blockIdx.x, split = blockIdx.y;
     const int sh = a.by_ct.div(item);
     g.ct = a.by_ct.mod(item, sh);
     g.seq = a.by_heads.div(sh);
     g.kvh = a.by_heads.mod(sh, g.seq);
-    g.r = attn_range(a, g.seq, g.ct, cols);
+    g.r = attn_range<TREE>(a, g.seq, g.ct, cols);
     if (g.ct * cols >= g.r.n * a.group) return false;
     // the host's chunk is for the longest sequence that the call allows; a single one is split by its own length
     const int chunk = a.c.n_seq > 1 ? a.chunk : max(kMinChunk, (a.by_split.div(g.r.slabs + a.n_split - 1) + a.round - 1) & -a.round);
@@ -207,20 +247,20 @@ struct AttnWalk {
     }
     // For all threads: fills *to, in shared memory, and is false in all where the CTA has nothing to do. scan: shared memory
     // for kAttnWarps ints.
-    __device__ static bool begin(const AttnArgs &a, int cols, int *scan, AttnWalk *to) {
+    template <bool TREE> __device__ static bool begin(const AttnArgs &a, int cols, int *scan, AttnWalk *to) {
         const int tid = threadIdx.x, me = blockIdx.x, heads = a.c.n_kv_heads, n_seq = a.c.n_seq;
         // the sequences 256 at a time, one a thread; the first 256 are kept (beyond, they are looked at once more)
         AttnRange r{};
         int n = 0, all = 0;
         if (tid < n_seq) {
-            r = attn_range(a, tid, 0, cols);
+            r = attn_range<TREE>(a, tid, 0, cols);
             n = steps_of(r);
         }
         int last = upto(n * heads, scan, all), total = all;
         for (int s0 = kAttnThreads; s0 < n_seq; s0 += kAttnThreads) {
             int more_all;
             __syncthreads();
-            (void)upto(s0 + tid < n_seq ? steps_of(attn_range(a, s0 + tid, 0, cols)) * heads : 0, scan, more_all);
+            (void)upto(s0 + tid < n_seq ? steps_of(attn_range<TREE>(a, s0 + tid, 0, cols)) * heads : 0, scan, more_all);
             total += more_all;
         }
         AttnWalk w;
@@ -255,7 +295,7 @@ struct AttnWalk {
             r = AttnRange{};
             n = 0;
             if (s0 + tid < n_seq) {
-                r = attn_range(a, s0 + tid, 0, cols);
+                r = attn_range<TREE>(a, s0 + tid, 0, cols);
                 n = steps_of(r);
             }
             __syncthreads();
@@ -265,7 +305,7 @@ struct AttnWalk {
         return to->at < to->end;
     }
     // For one thread: the next segment, but for share()'s fields.
-    __device__ void next(const AttnArgs &a, int cols, AttnSeg &g) {
+    template <bool TREE> __device__ void next(const AttnArgs &a, int cols, AttnSeg &g) {
         g.some = at < end;
         if (!g.some) return;
         if (at == base + steps) {
@@ -273,7 +313,7 @@ struct AttnWalk {
             if (++kvh == a.c.n_kv_heads) {
                 kvh = 0;
                 do {
-                    r = attn_range(a, ++seq, 0, cols);
+                    r = attn_range<TREE>(a, ++seq, 0, cols);
                     steps = steps_of(r);
                 } while (steps == 0);  // `end` is within the steps of all, so a sequence with some follows
             }
@@ -486,6 +526,13 @@ __device__ __forceinline__ uint32_t seen_tokens(int tok, int low, int end) {
     }
     return seen;
 }
+// ... of the unit's 32 tokens, a bit each.
+__device__ __forceinline__ uint32_t lane_bits(uint32_t bits, int t) {
+    uint32_t seen = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) seen |= (bits >> (2 * t + 8 * (i >> 1) + (i & 1)) & 1u) << i;
+    return seen;
+}
 // x = p d_v of a unit's tokens (a lane's pairs; the lanes of a column are t = 0 .. 3) in two fp16 parts whose unit is 2^-e for
 // the column's largest x: x = down * (hi + lo). V of what the column does not see may be no number, and x is 0 there.
 __device__ __forceinline__ void split_x(uint64_t (&x)[4], uint32_t seen, uint32_t (&hi)[4], uint32_t (&lo)[4], float &down) {
@@ -551,7 +598,7 @@ template <int NB> struct TileFeed {
 // where CTAs share the item, as a part; the CTA that comes last joins the parts, in their
 // order: out = sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s. `sum`: [warp][WCOLS][D]; m, l: [warp][WCOLS], l in the
 // common unit too; TURNED: column c's quads lie exchanged by c & 7.
-template <int D, int WCOLS, int WARPS, bool TURNED = false>
+template <int D, int WCOLS, int WARPS, bool TREE, bool TURNED = false>
 __device__ __forceinline__ void attn_store(const AttnArgs &a, const AttnSeg &seg, int cols, int wc, int n_wt, float *sum, const float *m,
                                            const float *l, bool bad, int *sh_last) {
     constexpr int kThreads = WARPS * 32, kQuads = D / 4, kAhead = WARPS > 12 ? 4 : kJoinAhead;  // as registers allow
@@ -563,6 +610,20 @@ __device__ __forceinline__ void attn_store(const AttnArgs &a, const AttnSeg &seg
     const auto row = [&](int col) {
         const int i = a.by_group.div(col);
         return a.out + (static_cast<int64_t>(r.q0 + i) * a.n_q_heads + kvh * a.group + (col - i * a.group)) * D;
+    };
+    // the logarithm of the sum of exp(score): p is in units of 2^-kAttnUnit of the maximum's
+    const auto put_lse = [&](int col, float top, float ls) {
+        if constexpr (TREE) {
+            const int i = a.by_group.div(col);
+            if (a.lse)
+                a.lse[static_cast<int64_t>(r.q0 + i) * a.n_q_heads + kvh * a.group + (col - i * a.group)] =
+                    ls == 0.0f ? -INFINITY : (top + (log2f(ls) - kAttnUnit)) * 0.693147180559945309f;
+        }
+    };
+    const auto warps_top = [&](int w0, int wcol) {
+        float top = -INFINITY;
+        for (int w = 0; w < n_wt; ++w) top = fmaxf(top, m[(w * wc + w0) * WCOLS + wcol]);
+        return top;
     };
     for (int k = tid; k < live * kQuads; k += kThreads) {
         const int c = k / kQuads, e = 4 * (k % kQuads);
@@ -579,12 +640,14 @@ __device__ __forceinline__ void attn_store(const AttnArgs &a, const AttnSeg &seg
         if (n_splits == 1) {
             const float inv = ls == 0.0f ? 0.0f : 1.0f / ls;
             *reinterpret_cast<float4 *>(row(ct * cols + c) + e) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+            if constexpr (TREE) {
+                if (e == 0) put_lse(ct * cols + c, warps_top(w0, wcol), ls);
+            }
         } else {
             const int64_t at = static_cast<int64_t>(seg.mine) * cols + c;
             __stcg(reinterpret_cast<float4 *>(a.part + at * D + e), acc);
             if (e == 0) {
-                float top = -INFINITY;
-                for (int w = 0; w < n_wt; ++w) top = fmaxf(top, m[(w * wc + w0) * WCOLS + wcol]);
+                const float top = warps_top(w0, wcol);
                 __stcg(&a.part_ml[at], make_float2(top, ls));
             }
         }
@@ -647,6 +710,7 @@ __device__ __forceinline__ void attn_store(const AttnArgs &a, const AttnSeg &seg
             float to = top;
             for (int q = 1; q < groups; ++q) to = fmaxf(to, grp_ml[q * quads + k].x);
             const float keep = top == -INFINITY ? 0.0f : exp2_approx(top - to);
+            if constexpr (TREE) top = to;
             ls *= keep;
             acc.x *= keep; acc.y *= keep; acc.z *= keep; acc.w *= keep;
             for (int q = 1; q < groups; ++q) {
@@ -660,6 +724,7 @@ __device__ __forceinline__ void attn_store(const AttnArgs &a, const AttnSeg &seg
         if (k < quads) {
             const float inv = ls == 0.0f ? 0.0f : 1.0f / ls;
             *reinterpret_cast<float4 *>(row(ct * cols + c) + e) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+            if (TREE && e == 0) put_lse(ct * cols + c, top, ls);
         }
     }
 }
@@ -678,7 +743,7 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
     return y;
 }
 constexpr int kNarrowCols = 4;
-template <int NB> __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(NB, 1)) attn_narrow_kernel(AttnArgs a) {
+template <int NB, bool TREE> __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(NB, 1)) attn_narrow_kernel(AttnArgs a) {
     using G = KvGeom<NB>;
     constexpr int D = G::kDim, kWarps = kAttnWarps;
     constexpr int kSlotBytes = 2 * G::kTileBytes;
@@ -738,7 +803,7 @@ template <int NB> __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_
             early_page = TileFeed<NB>::page_early(a, a.c.table + static_cast<int64_t>(seq) * a.c.max_pages, early_tile);
         }
         AttnSeg seg;
-        if (!attn_grid_seg(a, kNarrowCols, seg)) return;
+        if (!attn_grid_seg<TREE>(a, kNarrowCols, seg)) return;
         load_q<NB>(a, seg.r, seg.kvh, g / 2, t, v);
         begin(seg, &sh_bad[0]);
         if (tid == kWalker) {
@@ -747,8 +812,8 @@ template <int NB> __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_
         }
         __syncthreads();
     } else {
-        if (!AttnWalk::begin(a, kNarrowCols, sh_scan, &sh_walk)) return;
-        if (tid == kWalker) sh_walk.next(a, kNarrowCols, sh_seg[0]);
+        if (!AttnWalk::begin<TREE>(a, kNarrowCols, sh_scan, &sh_walk)) return;
+        if (tid == kWalker) sh_walk.next<TREE>(a, kNarrowCols, sh_seg[0]);
         __syncthreads();
         load_q<NB>(a, sh_seg[0].r, sh_seg[0].kvh, g / 2, t, v);
         begin(sh_seg[0], &sh_bad[0]);
@@ -794,15 +859,20 @@ template <int NB> __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_
     }
     if (tid == kWalker && a.n_split == 0) {
         sh_walk.share(sh_seg[n_seg & 1]);
-        sh_walk.next(a, kNarrowCols, sh_seg[~n_seg & 1]);
+        sh_walk.next<TREE>(a, kNarrowCols, sh_seg[~n_seg & 1]);
     }
     __syncwarp();
     // what column t sees, of this split's tiles
     const int limit = min(r.len, last * kKvSlab);
     const int ti = a.by_group.div(t);
-    const int end = ti < r.n ? min(limit, max(0, r.len - (r.n - 1 - ti))) : limit;
-    const int low = ti < r.n && a.window > 0 ? max(0, r.len - (r.n - 1 - ti) - a.window) : 0;
-    const int end_min = __reduce_min_sync(0xffffffffu, end), low_max = __reduce_max_sync(0xffffffffu, low);
+    int end = ti < r.n ? min(limit, max(0, r.len - (r.n - 1 - ti))) : limit;
+    int low = ti < r.n && a.window > 0 ? max(0, r.len - (r.n - 1 - ti) - a.window) : 0;
+    const bool tree = TREE && a.seen != nullptr;
+    if (tree) {
+        end = limit;
+        low = ti < r.n ? tree_low(a, r, ti) : 0;
+    }
+    const int end_min = __reduce_min_sync(0xffffffffu, tree ? min(end, r.len - r.n) : end), low_max = __reduce_max_sync(0xffffffffu, low);
 
     float m = -INFINITY, l = 0.0f;
     bool huge = false;
@@ -854,6 +924,7 @@ template <int NB> __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_
             for (int h = 0; h < 4; ++h) {
                 const int tok = t0 + 8 * h + g;
                 if (tok < low || tok >= end) sc[h] = -INFINITY;
+                if (tree && ti < r.n && !(tree_bits(a, r, ti, t0) >> (8 * h + g) & 1u)) sc[h] = -INFINITY;
                 // a token past the sequence's (or a stale half slot) may hold anything, NaN among it: its V
                 // counts for nothing
                 const int pair = t0 + 8 * h + 2 * t;
@@ -906,6 +977,10 @@ template <int NB> __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_
             uint32_t seen = 0;  // by column g / 2
             if constexpr (decltype(wide_range)::value)
                 seen = seen_tokens(t0 + 2 * t, __shfl_sync(0xffffffffu, low, g >> 1), __shfl_sync(0xffffffffu, end, g >> 1));
+            if constexpr (decltype(wide_range)::value && TREE) {
+                const int i = a.by_group.div(g >> 1);
+                if (tree && i < r.n) seen &= lane_bits(tree_bits(a, r, i, t0), t);
+            }
 #pragma unroll
             for (int j = 0; j < NB; ++j) {
                 uint32_t f[2][2][4], x[4];
@@ -982,7 +1057,7 @@ template <int NB> __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_
             make_float4(x.x * f0, x.y * f1, y.x * f0, y.y * f1);
     }
     __syncthreads();
-    attn_store<D, kNarrowCols, kWarps>(a, seg, kNarrowCols, 1, kWarps, sum, &sh_m[0][0], &sh_l[0][0], r.bad || sh_bad[n_seg & 1], &sh_last);
+    attn_store<D, kNarrowCols, kWarps, TREE>(a, seg, kNarrowCols, 1, kWarps, sum, &sh_m[0][0], &sh_l[0][0], r.bad || sh_bad[n_seg & 1], &sh_last);
     if (!ahead.some) break;
     load_q<NB>(a, ahead.r, ahead.kvh, g / 2, t, v);
     __syncthreads();  // the sums are read
@@ -1001,7 +1076,7 @@ template <int NB> __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_
 // m16n8k16, 22 one that needs the one before): with heads of 128 they kept the tensor cores 40% busy, and q's fragments in
 // registers, a product's sums put off behind the next block's products or warps that drift apart gained nothing. Heads of up
 // to 128 dimensions have a form of their own (zdmmv_attn_prompt.cuh).
-template <int NB, int NT, int FORM>
+template <int NB, int NT, int FORM, bool TREE>
 __global__ void __launch_bounds__(kAttnWarps * 32, FORM != kOwn ? 1 : attn_ctas_per_sm(NB, NT)) attn_kernel(AttnArgs a) {
     constexpr bool SHARED = FORM != kOwn, PROMPT = FORM == kPrompt;
     using G = KvGeom<NB>;
@@ -1043,14 +1118,14 @@ __global__ void __launch_bounds__(kAttnWarps * 32, FORM != kOwn ? 1 : attn_ctas_
             const int seq = a.by_heads.div(a.by_ct.div(blockIdx.x));
             early_page = TileFeed<NB>::page_early(a, a.c.table + static_cast<int64_t>(seq) * a.c.max_pages, early_tile);
         }
-        if (!attn_grid_seg(a, cols, seg)) return;
+        if (!attn_grid_seg<TREE>(a, cols, seg)) return;
         if (tid == kWarps * 32 - 1) {
             sh_seg[0] = seg;
             sh_seg[1].some = false;
         }
     } else {
-        if (!AttnWalk::begin(a, cols, sh_scan, &sh_walk)) return;
-        if (tid == kWarps * 32 - 1) sh_walk.next(a, cols, sh_seg[0]);
+        if (!AttnWalk::begin<TREE>(a, cols, sh_scan, &sh_walk)) return;
+        if (tid == kWarps * 32 - 1) sh_walk.next<TREE>(a, cols, sh_seg[0]);
     }
     __syncthreads();
     const uint64_t policy = l2_evict_first_policy();
@@ -1154,12 +1229,18 @@ __global__ void __launch_bounds__(kAttnWarps * 32, FORM != kOwn ? 1 : attn_ctas_
     int end[NT], low[NT];
     const int limit = min(r.len, last * kKvSlab);
     int end_min = limit, low_max = 0;
+    const bool tree = TREE && a.seen != nullptr;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         const int i = a.by_group.div(col0 + 8 * nt + g);
         const bool valid = i < r.n;
         end[nt] = valid ? min(limit, max(0, r.len - (r.n - 1 - i))) : limit;
         low[nt] = valid && a.window > 0 ? max(0, r.len - (r.n - 1 - i) - a.window) : 0;
+        if (tree) {
+            end[nt] = limit;
+            low[nt] = valid ? tree_low(a, r, i) : 0;
+            end_min = min(end_min, r.len - r.n);
+        }
         end_min = min(end_min, end[nt]);
         low_max = max(low_max, low[nt]);
     }
@@ -1170,7 +1251,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, FORM != kOwn ? 1 : attn_ctas_
 
     if (!SHARED && tid == kWarps * 32 - 1 && a.n_split == 0) {
         sh_walk.share(sh_seg[n_seg & 1]);
-        sh_walk.next(a, cols, sh_seg[~n_seg & 1]);
+        sh_walk.next<TREE>(a, cols, sh_seg[~n_seg & 1]);
     }
     __syncwarp();
 
@@ -1295,6 +1376,16 @@ __global__ void __launch_bounds__(kAttnWarps * 32, FORM != kOwn ? 1 : attn_ctas_
                 sc[nt][2 * h + 1] = v.y;
             }
         if (t0 + 2 * kKvSlab > end_min || t0 < low_max) {
+            if (tree) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const int k = a.by_group.div(col0 + 8 * nt + g);
+                    const uint32_t bits = k < r.n ? lane_bits(tree_bits(a, r, k, t0), t) : 0xffu;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (!(bits >> i & 1u)) sc[nt][i] = -INFINITY;
+                }
+            }
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const int tok = t0 + 2 * t + (i & 1) + 8 * (i >> 1);
@@ -1370,7 +1461,13 @@ __global__ void __launch_bounds__(kAttnWarps * 32, FORM != kOwn ? 1 : attn_ctas_
         const auto product = [&](auto wide_range) {
             uint32_t seen[NT];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) seen[nt] = decltype(wide_range)::value ? seen_tokens(t0 + 2 * t, low[nt], end[nt]) : 0;
+            for (int nt = 0; nt < NT; ++nt) {
+                seen[nt] = decltype(wide_range)::value ? seen_tokens(t0 + 2 * t, low[nt], end[nt]) : 0;
+                if constexpr (decltype(wide_range)::value && TREE) {
+                    const int k = a.by_group.div(col0 + 8 * nt + g);
+                    if (tree && k < r.n) seen[nt] &= lane_bits(tree_bits(a, r, k, t0), t);
+                }
+            }
 #pragma unroll
         for (int j = 0; j < NB; ++j) {
             uint32_t f[2][2][4];  // [tile][dimensions 4g, 4g+1 / 4g+2, 4g+3 of the block]
@@ -1506,7 +1603,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, FORM != kOwn ? 1 : attn_ctas_
         }
     }
     __syncthreads();
-    attn_store<D, 8 * NT, kWarps>(a, seg, cols, a.wc, n_wt, sum, &sh_m[0][0], &sh_l[0][0], r.bad || sh_bad[n_seg & 1], &sh_last);
+    attn_store<D, 8 * NT, kWarps, TREE>(a, seg, cols, a.wc, n_wt, sum, &sh_m[0][0], &sh_l[0][0], r.bad || sh_bad[n_seg & 1], &sh_last);
     if (!ahead.some) break;
     __syncthreads();  // the sums and q's fragments are read
     if (tid == 0) sh_bad[n_seg & 1] = 0;
@@ -1531,13 +1628,18 @@ struct AttnPlan {
     int64_t parts;        // parts that the workspace holds
 };
 
-template <int NB> cudaError_t launch_attn(AttnArgs a, const AttnPlan &p, cudaStream_t st);
-template <int NB> cudaError_t launch_attn_tall(const AttnArgs &a, const AttnPlan &p, cudaStream_t st);  // NB <= kTallBlocks
-extern template cudaError_t launch_attn<2>(AttnArgs, const AttnPlan &, cudaStream_t);
-extern template cudaError_t launch_attn<3>(AttnArgs, const AttnPlan &, cudaStream_t);
-extern template cudaError_t launch_attn<4>(AttnArgs, const AttnPlan &, cudaStream_t);
-extern template cudaError_t launch_attn<6>(AttnArgs, const AttnPlan &, cudaStream_t);
-extern template cudaError_t launch_attn<8>(AttnArgs, const AttnPlan &, cudaStream_t);
+template <int NB, bool TREE> cudaError_t launch_attn(AttnArgs a, const AttnPlan &p, cudaStream_t st);
+template <int NB, bool TREE> cudaError_t launch_attn_tall(const AttnArgs &a, const AttnPlan &p, cudaStream_t st);  // NB <= kTallBlocks
+extern template cudaError_t launch_attn<2, false>(AttnArgs, const AttnPlan &, cudaStream_t);
+extern template cudaError_t launch_attn<2, true>(AttnArgs, const AttnPlan &, cudaStream_t);
+extern template cudaError_t launch_attn<3, false>(AttnArgs, const AttnPlan &, cudaStream_t);
+extern template cudaError_t launch_attn<3, true>(AttnArgs, const AttnPlan &, cudaStream_t);
+extern template cudaError_t launch_attn<4, false>(AttnArgs, const AttnPlan &, cudaStream_t);
+extern template cudaError_t launch_attn<4, true>(AttnArgs, const AttnPlan &, cudaStream_t);
+extern template cudaError_t launch_attn<6, false>(AttnArgs, const AttnPlan &, cudaStream_t);
+extern template cudaError_t launch_attn<6, true>(AttnArgs, const AttnPlan &, cudaStream_t);
+extern template cudaError_t launch_attn<8, false>(AttnArgs, const AttnPlan &, cudaStream_t);
+extern template cudaError_t launch_attn<8, true>(AttnArgs, const AttnPlan &, cudaStream_t);
 
 #ifdef ZDMMV_ATTN_INSTANTIATE
 template <auto KERNEL> cudaError_t launch_attn_kernel(const AttnPlan &p, size_t smem, const AttnArgs &a, cudaStream_t st) {
@@ -1546,26 +1648,26 @@ template <auto KERNEL> cudaError_t launch_attn_kernel(const AttnPlan &p, size_t 
     const dim3 grid = p.n_split > 0 ? dim3(static_cast<unsigned>(p.items), p.n_split) : dim3(p.ctas);
     return launch_block_op(KERNEL, grid, dim3(kAttnThreads), kAttnBarBytes + smem, st, a);
 }
-template <int NB, int NT, int FORM> cudaError_t launch_attn_form(const AttnArgs &a, const AttnPlan &p, cudaStream_t st) {
+template <int NB, int NT, int FORM, bool TREE> cudaError_t launch_attn_form(const AttnArgs &a, const AttnPlan &p, cudaStream_t st) {
     const size_t ring = attn_slots(NB, FORM) * 2 * KvGeom<NB>::kTileBytes + static_cast<size_t>(p.wc) * NT * 2 * NB * 512 +
                         (FORM == kPrompt ? 2 * 8 * NB * 512 : 0);
     const size_t sums = static_cast<size_t>(kAttnWarps) * NT * 8 * NB * kQK * 4;
     const size_t smem = attn_sums_apart(NB, NT, FORM) ? ring + sums : (ring > sums ? ring : sums);
-    return launch_attn_kernel<&attn_kernel<NB, NT, FORM>>(p, smem, a, st);
+    return launch_attn_kernel<&attn_kernel<NB, NT, FORM, TREE>>(p, smem, a, st);
 }
-template <int NB> cudaError_t launch_attn(AttnArgs a, const AttnPlan &p, cudaStream_t st) {
+template <int NB, bool TREE> cudaError_t launch_attn(AttnArgs a, const AttnPlan &p, cudaStream_t st) {
     if (p.cols == kNarrowCols) {
         constexpr size_t kRing = attn_slots(NB, kOwn) * 2 * KvGeom<NB>::kTileBytes, kQ = 2 * NB * 256;
         constexpr size_t kSums = kAttnWarps * kNarrowCols * NB * kQK * 4;
-        return launch_attn_kernel<&attn_narrow_kernel<NB>>(p, kRing + kQ + kSums, a, st);
+        return launch_attn_kernel<&attn_narrow_kernel<NB, TREE>>(p, kRing + kQ + kSums, a, st);
     }
     if constexpr (NB <= kTallBlocks) {
-        if (p.tall) return launch_attn_tall<NB>(a, p, st);
+        if (p.tall) return launch_attn_tall<NB, TREE>(a, p, st);
     } else {
-        if (p.wc > 4) return launch_attn_form<NB, attn_prompt_nt(NB), kPrompt>(a, p, st);
-        if (p.wc > 1) return launch_attn_form<NB, 2, kShared>(a, p, st);
+        if (p.wc > 4) return launch_attn_form<NB, attn_prompt_nt(NB), kPrompt, TREE>(a, p, st);
+        if (p.wc > 1) return launch_attn_form<NB, 2, kShared, TREE>(a, p, st);
     }
-    return p.nt == 1 ? launch_attn_form<NB, 1, kOwn>(a, p, st) : launch_attn_form<NB, 2, kOwn>(a, p, st);
+    return p.nt == 1 ? launch_attn_form<NB, 1, kOwn, TREE>(a, p, st) : launch_attn_form<NB, 2, kOwn, TREE>(a, p, st);
 }
 #endif
 

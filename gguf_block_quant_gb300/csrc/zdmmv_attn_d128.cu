@@ -3,5 +3,5 @@
 #include "zdmmv_attn.cuh"
 
 namespace zdmmv {
-template cudaError_t launch_attn<4>(AttnArgs, const AttnPlan &, cudaStream_t);
+template cudaError_t launch_attn<4, false>(AttnArgs, const AttnPlan &, cudaStream_t);
 }  // namespace zdmmv

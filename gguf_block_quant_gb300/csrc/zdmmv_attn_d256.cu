@@ -3,5 +3,5 @@
 #include "zdmmv_attn.cuh"
 
 namespace zdmmv {
-template cudaError_t launch_attn<8>(AttnArgs, const AttnPlan &, cudaStream_t);
+template cudaError_t launch_attn<8, false>(AttnArgs, const AttnPlan &, cudaStream_t);
 }  // namespace zdmmv

@@ -2,7 +2,7 @@
 #include "zdmmv_attn_prompt.cuh"
 
 namespace zdmmv {
-template cudaError_t launch_attn_tall<2>(const AttnArgs &, const AttnPlan &, cudaStream_t);
-template cudaError_t launch_attn_tall<3>(const AttnArgs &, const AttnPlan &, cudaStream_t);
-template cudaError_t launch_attn_tall<4>(const AttnArgs &, const AttnPlan &, cudaStream_t);
+template cudaError_t launch_attn_tall<2, false>(const AttnArgs &, const AttnPlan &, cudaStream_t);
+template cudaError_t launch_attn_tall<3, false>(const AttnArgs &, const AttnPlan &, cudaStream_t);
+template cudaError_t launch_attn_tall<4, false>(const AttnArgs &, const AttnPlan &, cudaStream_t);
 }  // namespace zdmmv

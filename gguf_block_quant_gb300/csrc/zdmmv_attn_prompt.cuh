@@ -231,13 +231,14 @@ template <int NB> struct PromptFeed {
 // ordinary calls: where V is an infinity or NaN the products are NaN for rows that do not see it (0 times NaN); and from scores
 // of kHugeScoreTall on the fma of p's exponent does not do. (In the tiles' loops the one cost every call 2 to 10% of its time, the
 // other 2.)
-template <int NB>
+template <int NB, bool TREE>
 __device__ __forceinline__ void attn_redo(const AttnArgs &a, const AttnSeg &seg, int col, int row, float *sum, float &row_m, float &row_l, int lane) {
     using G = KvGeom<NB>;
     const AttnRange &r = seg.r;
-    const int i = a.by_group.div(col), seen = max(0, r.len - (r.n - 1 - i));
+    const bool tree = TREE && a.seen != nullptr;
+    const int i = a.by_group.div(col), seen = tree ? r.len : max(0, r.len - (r.n - 1 - i));
     const int end = min(min(r.len, seg.last * kKvSlab), seen);
-    const int low = max(seg.first * kKvSlab, a.window > 0 ? seen - a.window : 0);
+    const int low = max(seg.first * kKvSlab, tree ? tree_low(a, r, i) : (a.window > 0 ? seen - a.window : 0));
     const int32_t *table = a.c.table + static_cast<int64_t>(seg.seq) * a.c.max_pages;
     const uint8_t *head = a.c.pages + static_cast<int64_t>(seg.kvh) * static_cast<int>(a.by_page_tiles.d) * G::kTileBytes;
     const float *src = a.q + static_cast<int64_t>(r.q0 + i) * a.q_stride + static_cast<int64_t>(seg.kvh * a.group + col - i * a.group) * G::kDim + lane;
@@ -249,6 +250,7 @@ __device__ __forceinline__ void attn_redo(const AttnArgs &a, const AttnSeg &seg,
     }
 #pragma unroll 1
     for (int t = low; t < end; ++t) {
+        if (tree && !(tree_bits(a, r, i, t) & 1u)) continue;
         const int slab = t / kKvSlab, tok = t % kKvSlab, slot = a.by_page_tiles.div(slab);
         const uint8_t *tile = head + table[slot] * a.c.page_bytes + static_cast<int64_t>(a.by_page_tiles.mod(slab, slot)) * G::kTileBytes;
         const __half *scales = reinterpret_cast<const __half *>(tile + G::kKScaleAt);  // then V's
@@ -279,7 +281,7 @@ __device__ __forceinline__ void attn_redo(const AttnArgs &a, const AttnSeg &seg,
     }
 }
 
-template <int NB> __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(AttnArgs a) {
+template <int NB, bool TREE> __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(AttnArgs a) {
     using G = KvGeom<NB>;
     using P = PromptGeom<NB>;
     constexpr int D = G::kDim;
@@ -307,7 +309,7 @@ template <int NB> __global__ void __launch_bounds__(kPromptThreads, 1) attn_prom
     block_op_release();
     {
         AttnSeg seg;
-        if (!attn_grid_seg(a, kPromptRows, seg)) return;
+        if (!attn_grid_seg<TREE>(a, kPromptRows, seg)) return;
         if (tid == 0) sh_seg = seg;
     }
     if (warp == 16) tm_alloc(&sh_tm);
@@ -521,7 +523,12 @@ template <int NB> __global__ void __launch_bounds__(kPromptThreads, 1) attn_prom
             mbar_arrive(&bar[kWaitQ]);
         }
         const int seen = max(0, r.len - (r.n - 1 - i));
-        const int end = valid ? min(limit, seen) : limit, low = valid && a.window > 0 ? max(0, seen - a.window) : 0;
+        int end = valid ? min(limit, seen) : limit, low = valid && a.window > 0 ? max(0, seen - a.window) : 0;
+        const bool tree = TREE && a.seen != nullptr;
+        if (tree) {
+            low = valid ? tree_low(a, r, i) : 0;
+            end = min(limit, r.len - r.n);  // ... and what its bits name
+        }
         float m = -INFINITY, keep = 0.0f;
         constexpr int kLoads = D / 32;  // of 16 of the thread's D / 2 dimensions
         uint64_t l2 = 0, acc[D / 4];    // acc[4 g + k]: dimensions 8 g + k and 8 g + 4 + k of its half
@@ -565,9 +572,20 @@ template <int NB> __global__ void __launch_bounds__(kPromptThreads, 1) attn_prom
             for (int c = 0; c < 4; ++c) tm_load(at + 16 * c, s[c]);
             tm_loaded(s);
             if (__any_sync(0xffffffffu, t0 < low || t0 + kPromptTokens / 2 > end)) {
+                if (tree) {
+                    uint32_t bits[2] = {~0u, ~0u};
+                    if (valid) {
+                        bits[0] = tree_bits(a, r, i, t0);
+                        bits[1] = tree_bits(a, r, i, t0 + 32);
+                    }
 #pragma unroll
-                for (int k = 0; k < 64; ++k)
-                    if (t0 + k < low || t0 + k >= end) s[k / 16][k % 16] = 0xff800000u;
+                    for (int k = 0; k < 64; ++k)
+                        if (t0 + k < low || t0 + k >= limit || !(bits[k / 32] >> (k % 32) & 1u)) s[k / 16][k % 16] = 0xff800000u;
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 64; ++k)
+                        if (t0 + k < low || t0 + k >= end) s[k / 16][k % 16] = 0xff800000u;
+                }
             }
             float top = -INFINITY, top1 = -INFINITY;
 #pragma unroll
@@ -640,22 +658,22 @@ template <int NB> __global__ void __launch_bounds__(kPromptThreads, 1) attn_prom
             bool no = false;
             for (int e = lane; e < D; e += 32) no |= !isfinite(sum[row * D + e]);
             if (score_huge(sh_m[row], kHugeScoreTall) || (__any_sync(0xffffffffu, no) && isfinite(sh_l[0][row])))
-                attn_redo<NB>(a, seg, col, row, sum, sh_m[row], sh_l[0][row], lane);
+                attn_redo<NB, TREE>(a, seg, col, row, sum, sh_m[row], sh_l[0][row], lane);
         }
         __syncthreads();
     }
-    attn_store<D, kPromptRows, kPromptThreads / 32, true>(a, seg, kPromptRows, 1, 1, sum, sh_m, &sh_l[0][0], r.bad || sh_bad, &sh_last);
+    attn_store<D, kPromptRows, kPromptThreads / 32, TREE, true>(a, seg, kPromptRows, 1, 1, sum, sh_m, &sh_l[0][0], r.bad || sh_bad, &sh_last);
 }
 
-template <int NB> cudaError_t launch_attn_tall(const AttnArgs &a, const AttnPlan &p, cudaStream_t st) {
-    const cudaError_t e = smem_limit_raised<&attn_prompt_kernel<NB>>();
+template <int NB, bool TREE> cudaError_t launch_attn_tall(const AttnArgs &a, const AttnPlan &p, cudaStream_t st) {
+    const cudaError_t e = smem_limit_raised<&attn_prompt_kernel<NB, TREE>>();
     if (e != cudaSuccess) return e;
     static const bool shares_fit = [] {  // the compiler may have launched it with fewer registers than are shared out
         cudaFuncAttributes f{};
-        return cudaFuncGetAttributes(&f, attn_prompt_kernel<NB>) == cudaSuccess && f.numRegs == kRegsLaunch;
+        return cudaFuncGetAttributes(&f, attn_prompt_kernel<NB, TREE>) == cudaSuccess && f.numRegs == kRegsLaunch;
     }();
     if (!shares_fit) return cudaErrorLaunchOutOfResources;
-    return launch_block_op(&attn_prompt_kernel<NB>, dim3(static_cast<unsigned>(p.items), p.n_split), dim3(kPromptThreads),
+    return launch_block_op(&attn_prompt_kernel<NB, TREE>, dim3(static_cast<unsigned>(p.items), p.n_split), dim3(kPromptThreads),
                            PromptGeom<NB>::kSmem, st, a);
 }
 

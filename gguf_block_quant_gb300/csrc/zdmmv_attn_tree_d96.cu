@@ -1,0 +1,7 @@
+// zdmmv_attn_tree_d96.cu -- the attention kernels with a tree's order and lse for heads of 96 dimensions.
+#define ZDMMV_ATTN_INSTANTIATE
+#include "zdmmv_attn.cuh"
+
+namespace zdmmv {
+template cudaError_t launch_attn<3, true>(AttnArgs, const AttnPlan &, cudaStream_t);
+}  // namespace zdmmv

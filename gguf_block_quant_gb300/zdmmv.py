@@ -57,6 +57,7 @@ _RMSNORM_ARGS = struct.Struct("@6P4qf4x")
 _KV_CACHE = struct.Struct("@2Pq5i4x")
 _KV_APPEND_ARGS = struct.Struct("@10P4q4i")
 _ATTN_ARGS = struct.Struct("@6PNq5if")
+_ATTN_TREE = struct.Struct("@2Pi4x")
 _SIGS = {
     "zdmmv_status_str": ([_int], ctypes.c_char_p),
     "zdmmv_version": ([], ctypes.c_char_p),
@@ -97,6 +98,7 @@ _SIGS = {
     "zdmmv_kv_append_q4_0": ([_vp, _vp, _vp], _int),
     "zdmmv_attn_q4_0_workspace_bytes": ([_vp, _int, _int, _int], ctypes.c_size_t),
     "zdmmv_attn_q4_0": ([_vp, _vp, _vp], _int),
+    "zdmmv_attn_tree_q4_0": ([_vp, _vp, _vp, _vp], _int),
 }
 
 
@@ -548,11 +550,19 @@ def attn_q4_0(cache: KVCache, q, q_start, kv_len, max_q_len: int, max_kv_len: in
     """Attention of the new tokens q (fp32 [n_tok][heads][head_dim] or [n_tok][heads * head_dim]) over the cache;
     sequence s has the rows q_start[s] .. q_start[s+1]-1 and kv_len[s] tokens in the cache. scale: default
     1/sqrt(head_dim). Returns out, fp32 [n_tok][heads][head_dim]."""
+    args, out, _, _ = _attn_args("attn_q4_0", cache, q, q_start, kv_len, max_q_len, max_kv_len, scale, window, out, workspace,
+                                 status, stream)
+    _enter("zdmmv_attn_q4_0", cache.c, args, _raw_stream(stream))
+    return out
+
+
+def _attn_args(who, cache, q, q_start, kv_len, max_q_len, max_kv_len, scale, window, out, workspace, status, stream):
+    """(packed zdmmv_attn_args, out, tokens, query heads)."""
     dim, n_seq = cache.head_dim, cache.n_seq
     pq, n_tok, width, sq = _rows(q, "q")
     heads = width // dim
     if heads * dim != width:
-        _bad("attn_q4_0: q must be [n_tok][heads * head_dim]")
+        _bad(f"{who}: q must be [n_tok][heads * head_dim]")
     if out is None:
         out = _make((n_tok, heads, dim), _F32, q.device, stream)
     if workspace is None:
@@ -561,5 +571,26 @@ def attn_q4_0(cache: KVCache, q, q_start, kv_len, max_q_len: int, max_kv_len: in
                            _whole(out, _F32, n_tok * width, "out"), _whole(workspace, _U8, 0, "workspace"),
                            0 if status is None else _whole(status, _I32, 1, "status"), workspace.numel(), sq, n_tok, heads,
                            max_q_len, max_kv_len, window, dim ** -0.5 if scale is None else scale)
-    _enter("zdmmv_attn_q4_0", cache.c, args, _raw_stream(stream))
+    return args, out, n_tok, heads
+
+
+def attn_tree_q4_0(cache: KVCache, q, q_start, kv_len, max_q_len: int, max_kv_len: int, seen=None, lse=None,
+                   scale: float | None = None, window: int = 0, out=None, workspace=None, status=None, stream=None):
+    """attn_q4_0 where the new tokens see one another as `seen` says (int32 [n_tok][words], bit j%32 of word j/32 of token
+    i's row: it sees the sequence's new token j; None: those before it and itself). lse: fp32 [n_tok][heads], filled
+    with the logarithms of the rows' sums of exp(score), for attn_weights_q4_0 or to join parts. Returns out."""
+    args, out, n_tok, heads = _attn_args("attn_tree_q4_0", cache, q, q_start, kv_len, max_q_len, max_kv_len, scale, window, out,
+                                         workspace, status, stream)
+    ps, words = _seen(seen, n_tok)
+    tree = _ATTN_TREE.pack(ps, 0 if lse is None else _whole(lse, _F32, n_tok * heads, "lse"), words)
+    _enter("zdmmv_attn_tree_q4_0", cache.c, args, tree, _raw_stream(stream))
     return out
+
+
+def _seen(seen, n_tok: int) -> tuple[int, int]:
+    """(data pointer, words of a row) of a tree's bits; (0, 0) for none."""
+    if seen is None:
+        return 0, 0
+    if seen.dim() != 2 or seen.shape[0] < n_tok:
+        _bad(f"seen: expected int32 [n_tok][words] with {n_tok} rows")
+    return _whole(seen, _I32, 0, "seen"), seen.shape[1]

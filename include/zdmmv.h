@@ -689,6 +689,36 @@ size_t zdmmv_attn_q4_0_workspace_bytes(const zdmmv_kv_cache *cache, int n_q_head
 zdmmv_status zdmmv_attn_q4_0(const zdmmv_kv_cache *cache, const zdmmv_attn_args *args,
                              zdmmv_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Drafted trees and a cache that forgets. A step that verifies drafted tokens
+ * appends a whole tree of them (zdmmv_kv_append_at_q4_0: the tokens of one depth
+ * share a position), attends with each token seeing its ancestors
+ * (zdmmv_attn_tree_q4_0) and keeps the path that was accepted
+ * (zdmmv_kv_accept_q4_0). A cache that grew too long is cut back to the tokens
+ * that attention looked at (zdmmv_attn_weights_q4_0 every step,
+ * zdmmv_kv_evict_q4_0 now and then); its slots then are no positions any more,
+ * which zdmmv_kv_append_at_q4_0 takes apart.
+ * ------------------------------------------------------------------------ */
+
+/* zdmmv_attn_q4_0 with an order of the caller's among the new tokens. Of a
+ * sequence with kv_len tokens in the cache and n new ones, new token i sees the
+ * kv_len - n tokens before them and the new tokens j whose bit j of its row of
+ * `seen` is set, itself only if bit i is (bits from n on are not looked at). With
+ * a window it sees at most the last max(0, window - c) of those before, c being
+ * its set bits: `window` tokens in all, as a chain's token does, but all that its
+ * bits name. All else is zdmmv_attn_q4_0's, its workspace too. */
+typedef struct {
+    const uint32_t *seen;  /* nullable: the order of zdmmv_attn_q4_0; device uint32 [n_tok][seen_words], bit
+                              j%32 of word j/32 */
+    float *lse;            /* nullable; device fp32 [n_tok][n_q_heads]: ln sum_t exp(scale * (q . k_t)) over
+                              the tokens seen, -infinity for a row that sees none, NaN for one of a bad sequence */
+    int32_t seen_words;    /* words of a row, 32*seen_words >= max_q_len, at most 2^20 (ignored where seen is NULL) */
+} zdmmv_attn_tree;
+
+/* Errors: as zdmmv_attn_q4_0 (ERR_NULL for a NULL tree, ERR_SHAPE for too few words). */
+zdmmv_status zdmmv_attn_tree_q4_0(const zdmmv_kv_cache *cache, const zdmmv_attn_args *args,
+                                  const zdmmv_attn_tree *tree, zdmmv_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
