@@ -22,9 +22,7 @@ constexpr int kRaggedChunk = 128;
 constexpr int kEnds = 8;
 constexpr int kPromptCols = 128;  // of a CTA of the form on tcgen05
 constexpr int kTallEnds = 32, kTallJoin = 1;  // ... of the form on tcgen05: its start, and the join's loads of four parts for 2560 values
-constexpr int kMostTokens = 0x7fffff00;  // so that a tile's end past the last token is a number too
 constexpr int kCounters = ZDMMV_ATTN_COUNTER_BYTES / 4;
-constexpr int kMostWords = 1 << 20;  // of a row of bits, so that 32 times their number is a number too
 
 int device_sms() {
     static const int sms = [] {
@@ -181,7 +179,7 @@ zdmmv_status attn_call(const zdmmv_kv_cache *cache, const zdmmv_attn_args *args,
         g.max_kv_len < 0 || g.window < 0 || !std::isfinite(g.scale))
         return ZDMMV_ERR_SHAPE;
     const bool seen = tree && tree->seen;
-    if (seen && (tree->seen_words < 1 || tree->seen_words > kMostWords || static_cast<int64_t>(tree->seen_words) * 32 < g.max_q_len))
+    if (seen && (tree->seen_words < 1 || tree->seen_words > kMostSeenWords || static_cast<int64_t>(tree->seen_words) * 32 < g.max_q_len))
         return ZDMMV_ERR_SHAPE;
     // with a window, no column tile sees more than the window and its own new tokens
     const int64_t most = g.window > 0 ? std::min<int64_t>(g.max_kv_len, static_cast<int64_t>(g.window) + g.max_q_len + kKvSlab)
@@ -202,7 +200,8 @@ zdmmv_status attn_call(const zdmmv_kv_cache *cache, const zdmmv_attn_args *args,
     if (!a.fault) return ZDMMV_ERR_CUDA;
     a.q_stride = g.q_stride;
     a.n_tok = g.n_tok; a.n_q_heads = g.n_q_heads; a.group = g.n_q_heads / cache->n_kv_heads;
-    a.max_q_len = g.max_q_len; a.max_kv_len = std::min(g.max_kv_len, kMostTokens); a.window = g.window;
+    a.max_q_len = g.max_q_len; a.max_kv_len = std::min(g.max_kv_len, kMostAttnTokens);
+    a.window = attn_window(g.window, g.max_kv_len);
     a.scale_log2 = g.scale * 1.44269504088896340736f;
     a.by_ct = FastDiv::of(p.n_ct);
     a.by_heads = FastDiv::of(cache->n_kv_heads);

@@ -75,6 +75,12 @@ struct AttnArgs {
     int32_t seen_words;
 };
 
+constexpr int kMostAttnTokens = 0x7fffff00;  // so that a tile's end past the last token is a number too
+// A window past the longest sequence is one of its length (and leaves no sum of it and a length past 32 bits).
+inline int32_t attn_window(int32_t window, int32_t max_kv_len) {
+    return window > max_kv_len && window > 0 ? (max_kv_len > 0 ? max_kv_len : 1) : window;
+}
+constexpr int kMostSeenWords = 1 << 20;      // of a row of bits, so that 32 times their number is a number too
 constexpr int kAttnWarps = 8, kAttnThreads = kAttnWarps * 32;
 constexpr int kWalker = kAttnThreads - 1;    // the thread that finds the CTA's next segment
 constexpr int kStepTiles = 2 * kAttnWarps;  // tiles of a step: a ring slot for each warp

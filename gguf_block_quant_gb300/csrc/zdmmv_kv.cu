@@ -1,4 +1,4 @@
-// zdmmv_kv.cu -- the paged 4-bit cache's geometry and zdmmv_kv_append_q4_0: the
+// zdmmv_kv.cu -- the paged 4-bit cache's geometry and zdmmv_kv_append[_at]_q4_0: the
 // position rotation of q and k, and k and v quantized to Q4_0 into their pages.
 #include "zdmmv_kv.cuh"
 
@@ -43,6 +43,7 @@ struct AppendArgs {
     FastDiv by_groups, by_page;
     const float *k, *v, *q;
     const int32_t *seq, *pos;
+    const int32_t *turn_pos;  // the rotation's positions; pos itself where they are the same
     const float *rope;
     float *q_out;
     __half *k_val, *v_val;
@@ -133,12 +134,12 @@ struct Place {
     bool ok, bad;   // written to the cache; outside what the cache and the rotation table have
 };
 // The page's look-up is the one load: place_check looks at what it brought.
-__device__ __forceinline__ Place place_of(const AppendArgs &a, int pos, int seq) {
+__device__ __forceinline__ Place place_of(const AppendArgs &a, int pos, int seq, int turn_pos) {
     Place w;
     const bool pad = pos < 0;
     const int slot = pad ? 0 : a.by_page.div(pos);
     w.in = pad ? 0 : a.by_page.mod(pos, slot);
-    w.bad = !pad && (seq < 0 || seq >= a.c.n_seq || slot >= a.c.max_pages || (a.rot_dim > 0 && pos >= a.rope_rows));
+    w.bad = !pad && (seq < 0 || seq >= a.c.n_seq || slot >= a.c.max_pages || (a.rot_dim > 0 && (turn_pos < 0 || turn_pos >= a.rope_rows)));
     w.ok = !pad && !w.bad;
     w.page = w.ok ? a.c.table[static_cast<int64_t>(seq) * a.c.max_pages + slot] : 0;
     return w;
@@ -243,7 +244,7 @@ template <int NB, bool FAST> __global__ void __launch_bounds__(kAppendWarps * 32
     block_op_release();
     if (tok >= a.n_tok) return;
     const bool turned = head < a.n_q_heads + a.c.n_kv_heads;
-    const int pos = a.pos[tok], seq = a.seq[tok];
+    const int pos = a.pos[tok], seq = a.seq[tok], turn_pos = a.turn_pos[tok];
     float v[kPass][4], o[kPass][4];
 #pragma unroll
     for (int p = 0; p < kPass; ++p) {
@@ -251,11 +252,11 @@ template <int NB, bool FAST> __global__ void __launch_bounds__(kAppendWarps * 32
         v[p][0] = v[p][1] = v[p][2] = v[p][3] = 0.0f;
         if (e0 < G::kDim) load_head<FAST>(a, head_row(a, tok, head, G::kDim), e0, turned && e0 < a.rot_dim, v[p], o[p]);
     }
-    Place w = place_of(a, pos, seq);
+    Place w = place_of(a, pos, seq, turn_pos);
     Turn turn[kPass];
 #pragma unroll
     for (int p = 0; p < kPass; ++p)
-        if (w.ok && turned && p * 128 + 4 * lane < a.rot_dim) turn[p] = load_turn<FAST>(a, pos, p * 128 + 4 * lane);
+        if (w.ok && turned && p * 128 + 4 * lane < a.rot_dim) turn[p] = load_turn<FAST>(a, turn_pos, p * 128 + 4 * lane);
     place_check(a, w, lane);
     const Rows to = rows_of<NB>(a, w, tok);
     __syncwarp();
@@ -317,11 +318,11 @@ template <int NB, bool FAST> __global__ void __launch_bounds__(kStreamWarps * 32
         }
         if (tok != at) {
             at = tok;
-            const int pos = a.pos[tok];
-            w = place_of(a, pos, a.seq[tok]);
+            const int turn_pos = a.turn_pos[tok];
+            w = place_of(a, a.pos[tok], a.seq[tok], turn_pos);
 #pragma unroll
             for (int p = 0; p < kPass; ++p)
-                if (w.ok && p * 128 + 4 * lane < a.rot_dim) turn[p] = load_turn<FAST>(a, pos, p * 128 + 4 * lane);
+                if (w.ok && p * 128 + 4 * lane < a.rot_dim) turn[p] = load_turn<FAST>(a, turn_pos, p * 128 + 4 * lane);
             place_check(a, w, lane);
             to = rows_of<NB>(a, w, tok);
         }
@@ -366,7 +367,7 @@ template <int NB, bool FAST> __global__ void __launch_bounds__(kStreamWarps * 32
     const float nan = __int_as_float(0x7fffffff), row[4] = {nan, nan, nan, nan};
     for (int job = lost; job < last; ++job) {
         const int t = a.by_groups.div(job), from = a.by_groups.mod(job, t) * kStreamHeads;
-        Place where = place_of(a, a.pos[t], a.seq[t]);
+        Place where = place_of(a, a.pos[t], a.seq[t], a.turn_pos[t]);
         place_check(a, where, lane);
         const Rows dst = rows_of<NB>(a, where, t);
         for (int head = from; head < min(from + kStreamHeads, heads); ++head)
@@ -400,20 +401,8 @@ template <int NB> cudaError_t launch_append(const AppendArgs &a, cudaStream_t st
     return a.rot_dim % (a.halves ? 8 : 4) == 0 ? launch_append_as<NB, true>(a, st) : launch_append_as<NB, false>(a, st);
 }
 
-}  // namespace
-}  // namespace zdmmv
-
-using namespace zdmmv;
-
-extern "C" {
-
-size_t zdmmv_kv_page_bytes(int page_tokens, int n_kv_heads, int head_dim) {
-    if (!kv_geometry_ok(page_tokens, n_kv_heads, head_dim)) return 0;
-    return static_cast<size_t>(page_tokens / kKvSlab) * n_kv_heads * 18 * head_dim;
-}
-
-zdmmv_status zdmmv_kv_append_q4_0(const zdmmv_kv_cache *cache, const zdmmv_kv_append_args *args,
-                                  zdmmv_stream_t stream) {
+zdmmv_status append_call(const zdmmv_kv_cache *cache, const zdmmv_kv_append_args *args, const int32_t *rope_pos,
+                         zdmmv_stream_t stream) {
     if (!args) return ZDMMV_ERR_NULL;
     AppendArgs a{};
     const zdmmv_status st = kv_check(cache, &a.c);
@@ -431,13 +420,14 @@ zdmmv_status zdmmv_kv_append_q4_0(const zdmmv_kv_cache *cache, const zdmmv_kv_ap
     if (g.q && g.q_out == g.q && g.q_stride != qn) return ZDMMV_ERR_SHAPE;
     if (kv_misaligned(g.k, 16) || kv_misaligned(g.v, 16) || kv_misaligned(g.q, 16) || kv_misaligned(g.q_out, 16) ||
         kv_misaligned(g.rope, 16) || kv_misaligned(g.k_val, 8) || kv_misaligned(g.v_val, 8) || kv_misaligned(g.seq, 4) ||
-        kv_misaligned(g.pos, 4) || kv_misaligned(g.status_dev, 4) || g.k_stride % 4 || g.v_stride % 4 ||
+        kv_misaligned(g.pos, 4) || kv_misaligned(g.status_dev, 4) || kv_misaligned(rope_pos, 4) || g.k_stride % 4 || g.v_stride % 4 ||
         (g.q && g.q_stride % 4))
         return ZDMMV_ERR_ALIGN;
     a.by_page = FastDiv::of(cache->page_tokens);
     a.head_bytes = cache->page_tokens / kKvSlab * 18 * cache->head_dim;
     a.k = g.k; a.v = g.v; a.q = g.q;
     a.seq = g.seq; a.pos = g.pos; a.rope = g.rope;
+    a.turn_pos = rope_pos ? rope_pos : g.pos;
     a.q_out = g.q_out;
     a.k_val = static_cast<__half *>(g.k_val);
     a.v_val = static_cast<__half *>(g.v_val);
@@ -456,6 +446,28 @@ zdmmv_status zdmmv_kv_append_q4_0(const zdmmv_kv_cache *cache, const zdmmv_kv_ap
     case 8: e = launch_append<8>(a, s); break;
     }
     return e == cudaSuccess ? ZDMMV_OK : ZDMMV_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace zdmmv
+
+using namespace zdmmv;
+
+extern "C" {
+
+size_t zdmmv_kv_page_bytes(int page_tokens, int n_kv_heads, int head_dim) {
+    if (!kv_geometry_ok(page_tokens, n_kv_heads, head_dim)) return 0;
+    return static_cast<size_t>(page_tokens / kKvSlab) * n_kv_heads * 18 * head_dim;
+}
+
+zdmmv_status zdmmv_kv_append_q4_0(const zdmmv_kv_cache *cache, const zdmmv_kv_append_args *args,
+                                  zdmmv_stream_t stream) {
+    return append_call(cache, args, nullptr, stream);
+}
+
+zdmmv_status zdmmv_kv_append_at_q4_0(const zdmmv_kv_cache *cache, const zdmmv_kv_append_args *args, const int32_t *rope_pos,
+                                     zdmmv_stream_t stream) {
+    return append_call(cache, args, rope_pos, stream);
 }
 
 }  // extern "C"

@@ -1,0 +1,482 @@
+// zdmmv_kv_keep.cu -- what stays in the paged 4-bit cache: zdmmv_kv_evict_q4_0 (the tokens with the largest sums of attention
+// weights, to other pages) and zdmmv_kv_accept_q4_0 (the accepted path of a drafted tree, in place).
+#include <cooperative_groups.h>
+
+#include <algorithm>
+
+#include "zdmmv_kv.cuh"
+#include "zdmmv_internal.h"
+
+namespace zdmmv {
+namespace {
+
+namespace cg = cooperative_groups;
+
+struct KeepArgs {
+    KvView from, to;
+    FastDiv by_heads, from_page_tiles, to_page_tiles, by_tiles;
+    const int32_t *kv_len;
+    const float *sums;
+    int32_t *index;
+    float *sums_out;
+    int32_t *len_out, *status;
+    int64_t sums_stride, sums_out_stride;
+    int32_t max_kv_len, budget, sinks, recent;
+    int32_t n_tiles;  // of the budget
+    int32_t held;     // sums of a CTA that its shared memory holds
+};
+
+// A sum as a whole number that rises with it: -0 is 0, a NaN is below all.
+__device__ __forceinline__ uint32_t sum_key(float x) {
+    if (x != x) x = -INFINITY;
+    const uint32_t u = __float_as_uint(x + 0.0f);
+    return u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
+}
+
+// ------------------------------------------------------------------ which tokens stay
+// A cluster of CTAs for a kv head of a sequence (one CTA for short ones), each with an equal stretch of the tokens between the
+// first and the latest ones, whose sums it reads once into shared memory. The smallest sum that stays is found digit by digit,
+// 11 bits at a time from the top: every CTA counts its sums by digit, and adds up the cluster's counts. Then each CTA knows how
+// many tokens stay before its own, and writes its own in their order: of sums equal to the smallest, the first ones.
+constexpr int kPickThreads = 512, kPickWarps = kPickThreads / 32, kDigit = 2048, kPickCluster = 8;
+constexpr int kPickOne = 8192;      // tokens up to which one CTA does it
+constexpr int kPickHeld = 32 * 1024;  // most sums that a CTA holds; those beyond it are read again
+
+__global__ void __launch_bounds__(kPickThreads) kv_pick_kernel(KeepArgs a) {
+    extern __shared__ float held[];
+    __shared__ __align__(16) uint32_t sh_count[3][kDigit];  // of this CTA's sums, by digit
+    __shared__ uint32_t sh_scan[kPickWarps], sh_above[kPickWarps], sh_equal[kPickWarps];
+    __shared__ uint32_t sh_found, sh_want, sh_mine[2];
+    cg::cluster_group cluster = cg::this_cluster();
+    const int ranks = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    block_op_wait();
+    block_op_release();
+    const int item = blockIdx.x / ranks, seq = a.by_heads.div(item);
+    const float *sums = a.sums + static_cast<int64_t>(item) * a.sums_stride;
+    int32_t *index = a.index + static_cast<int64_t>(item) * a.budget;
+    float *sums_out = a.sums_out ? a.sums_out + static_cast<int64_t>(item) * a.sums_out_stride : nullptr;
+    const int n = a.kv_len[seq];
+    const bool bad = n < 0 || n > a.max_kv_len || n > static_cast<int64_t>(a.from.max_pages) * a.from.page_tokens;
+    if (rank == 0 && tid == 0) {
+        if (bad && a.status) *a.status = 1;
+        if (a.len_out && a.by_heads.mod(item, seq) == 0) a.len_out[seq] = bad ? -1 : min(n, a.budget);
+    }
+    const int me = rank * kPickThreads + tid, all = ranks * kPickThreads;
+    if (bad || n <= a.budget) {  // the whole cluster takes this way
+        for (int j = me; j < a.budget; j += all) {
+            const bool in = !bad && j < n;
+            index[j] = in ? j : -1;
+            if (sums_out) sums_out[j] = in ? sums[j] : 0.0f;
+        }
+        return;
+    }
+    const auto keep = [&](int at, int t, float x) {
+        index[at] = t;
+        if (sums_out) sums_out[at] = x;
+    };
+    for (int j = me; j < a.sinks; j += all) keep(j, j, sums[j]);
+    for (int j = me; j < a.recent; j += all) keep(a.budget - a.recent + j, n - a.recent + j, sums[n - a.recent + j]);
+    const int between = n - a.sinks - a.recent;                 // more than are wanted of them
+    uint32_t want = static_cast<uint32_t>(a.budget - a.sinks - a.recent);
+    if (want == 0) return;
+    const int each = (between + ranks - 1) / ranks, first = min(between, rank * each), mine = min(each, between - first);
+    const float *src = sums + a.sinks + first;
+    const auto value = [&](int i) { return i < a.held ? held[i] : src[i]; };
+    for (int i = tid; i < min(mine, a.held); i += kPickThreads) held[i] = src[i];
+    for (int i = tid; i < 3 * kDigit; i += kPickThreads) (&sh_count[0][0])[i] = 0;
+    __syncthreads();
+
+    uint32_t known = 0;  // the smallest sum's digits so far
+#pragma unroll 1
+    for (int pass = 0; pass < 3; ++pass) {
+        const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), above = shift + (pass == 2 ? 10 : 11);
+        const uint32_t mask = pass == 2 ? 1023u : 2047u;
+        for (int i = tid; i < mine; i += kPickThreads) {
+            const uint32_t k = sum_key(value(i));
+            if (pass == 0 || k >> above == known >> above) atomicAdd(&sh_count[pass][k >> shift & mask], 1u);
+        }
+        cluster.sync();
+        // four digits a thread, the largest first; `want` of the cluster's sums with the known digits stay
+        uint32_t c[4] = {0, 0, 0, 0}, sum = 0;
+        for (int q = 0; q < ranks; ++q) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(cluster.map_shared_rank(&sh_count[pass][kDigit - 4 - 4 * tid], q));
+            c[0] += x.w; c[1] += x.z; c[2] += x.y; c[3] += x.x;
+        }
+        sum = c[0] + c[1] + c[2] + c[3];
+        uint32_t upto = sum;
+#pragma unroll
+        for (int k = 1; k < 32; k <<= 1) {
+            const uint32_t o = __shfl_up_sync(0xffffffffu, upto, k);
+            if (lane >= k) upto += o;
+        }
+        if (lane == 31) sh_scan[warp] = upto;
+        __syncthreads();
+        for (int w = 0; w < warp; ++w) upto += sh_scan[w];
+        uint32_t over = upto - sum;  // sums of larger digits than this thread's
+        if (over < want && want <= upto) {
+            for (int k = 0; k < 4; ++k) {
+                if (want <= over + c[k]) {
+                    sh_found = static_cast<uint32_t>(kDigit - 1 - 4 * tid - k);
+                    sh_want = want - over;
+                    break;
+                }
+                over += c[k];
+            }
+        }
+        __syncthreads();
+        known |= sh_found << shift;
+        want = sh_want;
+    }
+    // `want` of the sums equal to `known` stay, and all above it: a warp's stretch of the CTA's
+    const int per_warp = (mine + 32 * kPickWarps - 1) / (32 * kPickWarps) * 32;
+    const int from = min(mine, warp * per_warp), to = min(mine, from + per_warp);
+    uint32_t more = 0, same = 0;
+    for (int i = from + lane; i < to; i += 32) {
+        const uint32_t k = sum_key(value(i));
+        more += k > known;
+        same += k == known;
+    }
+    more = __reduce_add_sync(0xffffffffu, more);
+    same = __reduce_add_sync(0xffffffffu, same);
+    if (lane == 0) {
+        sh_above[warp] = more;
+        sh_equal[warp] = same;
+    }
+    __syncthreads();
+    if (tid == 0) {
+        uint32_t m = 0, s = 0;
+        for (int w = 0; w < kPickWarps; ++w) {
+            m += sh_above[w];
+            s += sh_equal[w];
+        }
+        sh_mine[0] = m;
+        sh_mine[1] = s;
+    }
+    cluster.sync();
+    more = same = 0;
+    for (int q = 0; q < rank; ++q) {
+        const uint32_t *o = cluster.map_shared_rank(&sh_mine[0], q);
+        more += o[0];
+        same += o[1];
+    }
+    for (int w = 0; w < warp; ++w) {
+        more += sh_above[w];
+        same += sh_equal[w];
+    }
+    const uint32_t before = (1u << lane) - 1u;
+    for (int i0 = from; i0 < to; i0 += 32) {
+        const int i = i0 + lane;
+        const float x = i < to ? value(i) : 0.0f;
+        const uint32_t k = sum_key(x);
+        const uint32_t ups = __ballot_sync(0xffffffffu, i < to && k > known), eqs = __ballot_sync(0xffffffffu, i < to && k == known);
+        const uint32_t m = more + __popc(ups & before), s = same + __popc(eqs & before);
+        if (i < to && (k > known || (k == known && s < want)))
+            keep(a.sinks + static_cast<int>(m + min(s, want)), a.sinks + first + i, x);
+        more += __popc(ups);
+        same += __popc(eqs);
+    }
+    cluster.sync();  // no CTA leaves while another may read its counts
+}
+
+// ------------------------------------------------------------------ their move
+// A warp makes a tile of 16 tokens of one head: a lane brings the words of the new tile that it stores, from wherever their
+// tokens lie. A token's K words are the same there and here; a V word holds two tokens' halves.
+constexpr int kGatherWarps = 8;
+template <int NB> __global__ void __launch_bounds__(kGatherWarps * 32) kv_gather_kernel(KeepArgs a, int64_t n_jobs) {
+    using G = KvGeom<NB>;
+    constexpr int V = G::kVec;
+    struct __align__(4 * V) Words {
+        uint32_t w[V];
+    };
+    const int lane = threadIdx.x & 31;
+    const int64_t job = static_cast<int64_t>(blockIdx.x) * kGatherWarps + (threadIdx.x >> 5);
+    block_op_wait();
+    block_op_release();
+    if (job >= n_jobs) return;
+    const int item = a.by_tiles.div(static_cast<int>(job)), tile = a.by_tiles.mod(static_cast<int>(job), item);
+    const int seq = a.by_heads.div(item), kvh = a.by_heads.mod(item, seq);
+    const int t0 = tile * kKvSlab;
+    // lanes 0 .. 15: where the tile's tokens are
+    const uint8_t *src = nullptr;
+    int r = 0;
+    bool some = false, wrong = false;
+    if (lane < kKvSlab && t0 + lane < a.budget) {
+        const int t = a.index[static_cast<int64_t>(item) * a.budget + t0 + lane];
+        some = t >= 0;
+        if (some) {
+            const int slab = t / kKvSlab, slot = a.from_page_tiles.div(slab);
+            const int page = a.from.table[static_cast<int64_t>(seq) * a.from.max_pages + slot];
+            wrong = page < 0 || page >= a.from.n_pages;
+            r = t % kKvSlab;
+            if (!wrong)
+                src = a.from.pages + page * a.from.page_bytes +
+                      (static_cast<int64_t>(kvh) * static_cast<int>(a.from_page_tiles.d) + a.from_page_tiles.mod(slab, slot)) * G::kTileBytes;
+        }
+    }
+    if (!__any_sync(0xffffffffu, some)) return;
+    const int slot = a.to_page_tiles.div(tile), page = a.to.table[static_cast<int64_t>(seq) * a.to.max_pages + slot];
+    const bool lost = page < 0 || page >= a.to.n_pages;
+    if ((wrong || (lost && lane == 0)) && a.status) *a.status = 1;
+    if (lost) return;
+    uint8_t *dst = a.to.pages + page * a.to.page_bytes +
+                   (static_cast<int64_t>(kvh) * static_cast<int>(a.to_page_tiles.d) + a.to_page_tiles.mod(tile, slot)) * G::kTileBytes;
+    const uint32_t nans = __ballot_sync(0xffffffffu, wrong);
+    const auto tile_of = [&](int tok) {
+        return reinterpret_cast<const uint8_t *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), tok));
+    };
+    Words k[2][NB / V], v[2][NB / V][2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int tok = 8 * h + (lane >> 2);
+        const uint8_t *p = tile_of(tok);
+        const int at = __shfl_sync(0xffffffffu, r, tok);
+#pragma unroll
+        for (int b = 0; b < NB / V; ++b) {
+            k[h][b] = Words{};
+            if (p) k[h][b] = *reinterpret_cast<const Words *>(p + G::k_word(at, b * V, lane & 3) * 4);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int two = 8 * h + 2 * (lane & 3) + i;
+            const uint8_t *q = tile_of(two);
+            const int to = __shfl_sync(0xffffffffu, r, two);
+#pragma unroll
+            for (int b = 0; b < NB / V; ++b) {
+                v[h][b][i] = Words{};
+                if (q) {
+                    v[h][b][i] = *reinterpret_cast<const Words *>(q + G::kVAt + (G::v_half(to, b * V, lane >> 2) >> 1) * 4);
+#pragma unroll
+                    for (int x = 0; x < V; ++x) v[h][b][i].w[x] = (v[h][b][i].w[x] >> (16 * (to & 1)) & 0xffffu) << (16 * i);
+                }
+            }
+        }
+    }
+    // scales: word (pair of tokens, block), K's then V's
+    constexpr int kScaleWords = 16 * NB, kPer = (kScaleWords + 31) / 32;
+    uint32_t d[kPer];
+#pragma unroll
+    for (int c = 0; c < kPer; ++c) {
+        const int word = 32 * c + lane, which = word / (8 * NB), pair = word % (8 * NB) / NB, b = word % NB;
+        d[c] = 0;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint8_t *p = tile_of(2 * pair + i);
+            const int at = __shfl_sync(0xffffffffu, r, 2 * pair + i);
+            uint32_t x = nans >> (2 * pair + i) & 1u ? 0x7fffu : 0u;
+            if (p && word < kScaleWords) x = reinterpret_cast<const uint16_t *>(p + G::kKScaleAt + which * G::kScaleBytes)[G::scale_half(at, b)];
+            d[c] |= x << (16 * i);
+        }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int b = 0; b < NB / V; ++b) {
+            const int at = (h * (NB / V) + b) * 32 * V + lane * V;
+            Words x;
+#pragma unroll
+            for (int w = 0; w < V; ++w) x.w[w] = v[h][b][0].w[w] | v[h][b][1].w[w];
+            *reinterpret_cast<Words *>(dst + at * 4) = k[h][b];
+            *reinterpret_cast<Words *>(dst + G::kVAt + at * 4) = x;
+        }
+#pragma unroll
+    for (int c = 0; c < kPer; ++c)
+        if (32 * c + lane < kScaleWords) reinterpret_cast<uint32_t *>(dst + G::kKScaleAt)[32 * c + lane] = d[c];
+}
+
+// ------------------------------------------------------------------ the accepted path
+// A CTA for a kv head of a sequence. The path rises, so number j of it is j or more: 16 tokens at a time are read before they
+// are written, and none that is still to be read is written over.
+struct AcceptArgs {
+    KvView c;
+    FastDiv by_heads, by_page;
+    const int32_t *base, *path, *n_path;
+    int32_t *len_out, *status;
+    float *sums;
+    int64_t sums_stride;
+    int64_t room;  // tokens that the sums have room for, and that a place is a number of
+    int32_t max_path;
+};
+constexpr int kAcceptWarps = 8, kAcceptThreads = kAcceptWarps * 32, kMostPath = 1024;
+template <int NB> __global__ void __launch_bounds__(kAcceptThreads) kv_accept_kernel(AcceptArgs a) {
+    using G = KvGeom<NB>;
+    __shared__ int sh_path[kMostPath], sh_from[kMostPath], sh_to[kMostPath];  // the path, and the pages from and to which it moves
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    block_op_wait();
+    block_op_release();
+    const int seq = a.by_heads.div(blockIdx.x), kvh = a.by_heads.mod(blockIdx.x, seq);
+    const int base = a.base[seq], n = a.n_path[seq];
+    const int32_t *path = a.path + static_cast<int64_t>(seq) * a.max_path;
+    const int64_t room = min(static_cast<int64_t>(a.c.max_pages) * a.c.page_tokens, a.room);
+    bool bad = base < 0 || n < 0 || n > a.max_path;
+    const int32_t *table = a.c.table + static_cast<int64_t>(seq) * a.c.max_pages;
+    if (!bad) {
+        for (int j = tid; j < n; j += kAcceptThreads) {
+            const int p = path[j], prev = j > 0 ? path[j - 1] : -1;
+            sh_path[j] = p;
+            if (p <= prev || prev < -1 || static_cast<int64_t>(base) + p >= room) {
+                bad = true;
+                break;
+            }
+            const int from = a.by_page.div(base + p), to = a.by_page.div(base + j);
+            sh_from[j] = table[from];
+            sh_to[j] = table[to];
+            if (p != j) bad |= sh_from[j] < 0 || sh_from[j] >= a.c.n_pages || sh_to[j] < 0 || sh_to[j] >= a.c.n_pages;
+        }
+    }
+    bad = __syncthreads_or(bad);
+    if (kvh == 0 && tid == 0) {
+        if (a.len_out) a.len_out[seq] = bad ? -1 : base + n;
+        if (bad && a.status) *a.status = 1;
+    }
+    if (bad) return;
+    const int64_t head = static_cast<int64_t>(kvh) * (a.c.page_tokens / kKvSlab);
+    const auto tile_of = [&](int page, int tok) {
+        return a.c.pages + page * a.c.page_bytes + (head + tok / kKvSlab) * G::kTileBytes;
+    };
+    float *sums = a.sums ? a.sums + static_cast<int64_t>(blockIdx.x) * a.sums_stride + base : nullptr;
+    constexpr int kAtOnce = 2 * kAcceptWarps;
+    for (int j0 = 0; j0 < n; j0 += kAtOnce) {
+        uint32_t k[2];
+        uint16_t v[2][(8 * NB + 31) / 32], d[2];
+        float sum[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int j = j0 + warp + i * kAcceptWarps;
+            if (j >= n || sh_path[j] == j) continue;
+            const int at = a.by_page.mod(base + sh_path[j], a.by_page.div(base + sh_path[j])), r = at % kKvSlab;
+            const uint8_t *src = tile_of(sh_from[j], at);
+            if (sums) sum[i] = sums[sh_path[j]];
+            if (lane < 4 * NB) k[i] = reinterpret_cast<const uint32_t *>(src)[G::k_word(r, lane >> 2, lane & 3)];
+#pragma unroll
+            for (int c = 0; c < (8 * NB + 31) / 32; ++c)
+                if (32 * c + lane < 8 * NB) v[i][c] = reinterpret_cast<const uint16_t *>(src + G::kVAt)[G::v_half(r, (32 * c + lane) >> 3, lane & 7)];
+            if (lane < 2 * NB)
+                d[i] = reinterpret_cast<const uint16_t *>(src + (lane < NB ? G::kKScaleAt : G::kVScaleAt))[G::scale_half(r, lane % NB)];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int j = j0 + warp + i * kAcceptWarps;
+            if (j >= n || sh_path[j] == j) continue;
+            const int at = a.by_page.mod(base + j, a.by_page.div(base + j)), r = at % kKvSlab;
+            uint8_t *dst = tile_of(sh_to[j], at);
+            if (sums && lane == 0) sums[j] = sum[i];
+            if (lane < 4 * NB) reinterpret_cast<uint32_t *>(dst)[G::k_word(r, lane >> 2, lane & 3)] = k[i];
+#pragma unroll
+            for (int c = 0; c < (8 * NB + 31) / 32; ++c)
+                if (32 * c + lane < 8 * NB) reinterpret_cast<uint16_t *>(dst + G::kVAt)[G::v_half(r, (32 * c + lane) >> 3, lane & 7)] = v[i][c];
+            if (lane < 2 * NB)
+                reinterpret_cast<uint16_t *>(dst + (lane < NB ? G::kKScaleAt : G::kVScaleAt))[G::scale_half(r, lane % NB)] = d[i];
+        }
+        __syncthreads();
+    }
+}
+
+template <int NB> cudaError_t launch_gather(const KeepArgs &a, int64_t jobs, cudaStream_t st) {
+    return launch_block_op(kv_gather_kernel<NB>, dim3(static_cast<unsigned>((jobs + kGatherWarps - 1) / kGatherWarps)), dim3(kGatherWarps * 32),
+                           0, st, a, jobs);
+}
+template <int NB> cudaError_t launch_accept(const AcceptArgs &a, cudaStream_t st) {
+    return launch_block_op(kv_accept_kernel<NB>, dim3(static_cast<unsigned>(a.c.n_seq) * a.c.n_kv_heads), dim3(kAcceptThreads), 0, st, a);
+}
+cudaError_t launch_pick(KeepArgs a, int64_t items, cudaStream_t st) {
+    cudaError_t e = smem_limit_raised<&kv_pick_kernel>();
+    if (e != cudaSuccess) return e;
+    const int ranks = a.max_kv_len <= kPickOne ? 1 : kPickCluster;
+    a.held = std::min((a.max_kv_len + ranks - 1) / ranks, kPickHeld);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(items * ranks));
+    cfg.blockDim = dim3(kPickThreads);
+    cfg.dynamicSmemBytes = static_cast<size_t>(a.held) * 4;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(ranks);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl_enabled() ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kv_pick_kernel, a);
+}
+
+}  // namespace
+}  // namespace zdmmv
+
+using namespace zdmmv;
+
+extern "C" {
+
+zdmmv_status zdmmv_kv_evict_q4_0(const zdmmv_kv_cache *from, const zdmmv_kv_cache *to, const zdmmv_kv_evict_args *args,
+                                 zdmmv_stream_t stream) {
+    if (!args) return ZDMMV_ERR_NULL;
+    KeepArgs a{};
+    zdmmv_status st = kv_check(from, &a.from);
+    if (st == ZDMMV_OK) st = kv_check(to, &a.to);
+    if (st != ZDMMV_OK) return st;
+    const zdmmv_kv_evict_args &g = *args;
+    const int64_t items = static_cast<int64_t>(a.from.n_seq) * a.from.n_kv_heads;
+    const int64_t tiles = (static_cast<int64_t>(g.budget) + kKvSlab - 1) / kKvSlab, jobs = items * tiles;
+    if (from->n_seq != to->n_seq || from->n_kv_heads != to->n_kv_heads || from->head_dim != to->head_dim || g.max_kv_len < 0 ||
+        g.max_kv_len > 0x7fffff00 || g.budget < 1 || g.sinks < 0 || g.recent < 0 || static_cast<int64_t>(g.sinks) + g.recent > g.budget ||
+        g.budget > static_cast<int64_t>(a.to.max_pages) * a.to.page_tokens || jobs > 0x7fffff00 || items * kPickCluster > 0x7fffff00)
+        return ZDMMV_ERR_SHAPE;
+    if (!g.kv_len || !g.sums || !g.index) return ZDMMV_ERR_NULL;
+    if (g.sums_stride < g.max_kv_len || (g.sums_out && (g.sums_out_stride < g.budget || g.sums_out == g.sums))) return ZDMMV_ERR_SHAPE;
+    if (kv_misaligned(g.kv_len, 4) || kv_misaligned(g.sums, 4) || kv_misaligned(g.index, 4) || kv_misaligned(g.sums_out, 4) ||
+        kv_misaligned(g.len_out, 4) || kv_misaligned(g.status_dev, 4))
+        return ZDMMV_ERR_ALIGN;
+    a.by_heads = FastDiv::of(from->n_kv_heads);
+    a.from_page_tiles = FastDiv::of(from->page_tokens / kKvSlab);
+    a.to_page_tiles = FastDiv::of(to->page_tokens / kKvSlab);
+    a.by_tiles = FastDiv::of(static_cast<int32_t>(tiles));
+    a.kv_len = g.kv_len; a.sums = g.sums; a.index = g.index; a.sums_out = g.sums_out; a.len_out = g.len_out; a.status = g.status_dev;
+    a.sums_stride = g.sums_stride; a.sums_out_stride = g.sums_out_stride;
+    a.max_kv_len = g.max_kv_len; a.budget = g.budget; a.sinks = g.sinks; a.recent = g.recent;
+    a.n_tiles = static_cast<int32_t>(tiles);
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t e = launch_pick(a, items, s);
+    if (e != cudaSuccess) return ZDMMV_ERR_CUDA;
+    e = cudaErrorInvalidValue;
+    switch (kv_blocks(from->head_dim)) {
+    case 2: e = launch_gather<2>(a, jobs, s); break;
+    case 3: e = launch_gather<3>(a, jobs, s); break;
+    case 4: e = launch_gather<4>(a, jobs, s); break;
+    case 6: e = launch_gather<6>(a, jobs, s); break;
+    case 8: e = launch_gather<8>(a, jobs, s); break;
+    }
+    return e == cudaSuccess ? ZDMMV_OK : ZDMMV_ERR_CUDA;
+}
+
+zdmmv_status zdmmv_kv_accept_q4_0(const zdmmv_kv_cache *cache, const zdmmv_kv_accept_args *args, zdmmv_stream_t stream) {
+    if (!args) return ZDMMV_ERR_NULL;
+    AcceptArgs a{};
+    const zdmmv_status st = kv_check(cache, &a.c);
+    if (st != ZDMMV_OK) return st;
+    const zdmmv_kv_accept_args &g = *args;
+    if (g.max_path < 1 || g.max_path > kMostPath || static_cast<int64_t>(a.c.n_seq) * a.c.n_kv_heads > 0x7fffff00) return ZDMMV_ERR_SHAPE;
+    if (!g.base || !g.path || !g.n_path) return ZDMMV_ERR_NULL;
+    if (g.sums && (g.sums_stride < g.max_path || g.sums_len < g.max_path || g.sums_stride < g.sums_len)) return ZDMMV_ERR_SHAPE;
+    if (kv_misaligned(g.base, 4) || kv_misaligned(g.path, 4) || kv_misaligned(g.n_path, 4) || kv_misaligned(g.len_out, 4) ||
+        kv_misaligned(g.status_dev, 4) || kv_misaligned(g.sums, 4))
+        return ZDMMV_ERR_ALIGN;
+    a.by_heads = FastDiv::of(cache->n_kv_heads);
+    a.by_page = FastDiv::of(cache->page_tokens);
+    a.base = g.base; a.path = g.path; a.n_path = g.n_path; a.len_out = g.len_out; a.status = g.status_dev;
+    a.max_path = g.max_path;
+    a.sums = g.sums; a.sums_stride = g.sums_stride;
+    a.room = g.sums ? std::min<int64_t>(0x7fffff00, g.sums_len) : 0x7fffff00;
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t e = cudaErrorInvalidValue;
+    switch (kv_blocks(cache->head_dim)) {
+    case 2: e = launch_accept<2>(a, s); break;
+    case 3: e = launch_accept<3>(a, s); break;
+    case 4: e = launch_accept<4>(a, s); break;
+    case 6: e = launch_accept<6>(a, s); break;
+    case 8: e = launch_accept<8>(a, s); break;
+    }
+    return e == cudaSuccess ? ZDMMV_OK : ZDMMV_ERR_CUDA;
+}
+
+}  // extern "C"

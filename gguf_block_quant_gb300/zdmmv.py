@@ -58,6 +58,9 @@ _KV_CACHE = struct.Struct("@2Pq5i4x")
 _KV_APPEND_ARGS = struct.Struct("@10P4q4i")
 _ATTN_ARGS = struct.Struct("@6PNq5if")
 _ATTN_TREE = struct.Struct("@2Pi4x")
+_ATTN_WEIGHTS_ARGS = struct.Struct("@8P3q6i2f")
+_KV_EVICT_ARGS = struct.Struct("@6P2q4i")
+_KV_ACCEPT_ARGS = struct.Struct("@6P2qi4x")
 _SIGS = {
     "zdmmv_status_str": ([_int], ctypes.c_char_p),
     "zdmmv_version": ([], ctypes.c_char_p),
@@ -98,7 +101,11 @@ _SIGS = {
     "zdmmv_kv_append_q4_0": ([_vp, _vp, _vp], _int),
     "zdmmv_attn_q4_0_workspace_bytes": ([_vp, _int, _int, _int], ctypes.c_size_t),
     "zdmmv_attn_q4_0": ([_vp, _vp, _vp], _int),
+    "zdmmv_kv_append_at_q4_0": ([_vp, _vp, _vp, _vp], _int),
     "zdmmv_attn_tree_q4_0": ([_vp, _vp, _vp, _vp], _int),
+    "zdmmv_attn_weights_q4_0": ([_vp, _vp, _vp], _int),
+    "zdmmv_kv_evict_q4_0": ([_vp, _vp, _vp, _vp], _int),
+    "zdmmv_kv_accept_q4_0": ([_vp, _vp, _vp], _int),
 }
 
 
@@ -500,10 +507,11 @@ class KVCache:
 
 
 def kv_append_q4_0(cache: KVCache, k, v, seq, pos, q=None, q_out=None, rope=None, rope_style: int = ROPE_HALVES,
-                   k_val=None, v_val=None, status=None, stream=None):
+                   k_val=None, v_val=None, status=None, stream=None, rope_pos=None):
     """Append tokens (fp32 k and v, [n_tok][heads * head_dim] or [n_tok][heads][head_dim], tokens may be strided) to
     their sequences' pages, rotated by rope (fp32 [positions][rot_dim]: cosines, then sines) and quantized to Q4_0.
-    With q, returns it rotated (q_out). k_val, v_val: fp16, the values the cache then holds."""
+    With q, returns it rotated (q_out). k_val, v_val: fp16, the values the cache then holds. rope_pos: int32 [n_tok], the
+    rows of rope where they are not pos (drafted trees, a cache that was cut back)."""
     dim = cache.head_dim
     kv = cache.n_kv_heads * dim
     pk, n_tok, wk, sk = _rows(k, "k")
@@ -530,7 +538,10 @@ def kv_append_q4_0(cache: KVCache, k, v, seq, pos, q=None, q_out=None, rope=None
         ps = _whole(status, _I32, 1, "status")
     args = _KV_APPEND_ARGS.pack(pk, pv, pq, _whole(seq, _I32, n_tok, "seq"), _whole(pos, _I32, n_tok, "pos"), pr, po, pkv,
                                 pvv, ps, sk, sv, sq, positions, n_tok, heads, rot, rope_style)
-    _enter("zdmmv_kv_append_q4_0", cache.c, args, _raw_stream(stream))
+    if rope_pos is None:
+        _enter("zdmmv_kv_append_q4_0", cache.c, args, _raw_stream(stream))
+    else:
+        _enter("zdmmv_kv_append_at_q4_0", cache.c, args, _whole(rope_pos, _I32, n_tok, "rope_pos"), _raw_stream(stream))
     return q_out
 
 
@@ -594,3 +605,73 @@ def _seen(seen, n_tok: int) -> tuple[int, int]:
     if seen.dim() != 2 or seen.shape[0] < n_tok:
         _bad(f"seen: expected int32 [n_tok][words] with {n_tok} rows")
     return _whole(seen, _I32, 0, "seen"), seen.shape[1]
+
+
+def _per_head(t: torch.Tensor, cache: KVCache, n: int, what: str) -> tuple[int, int]:
+    """(data pointer, floats between kv heads) of a float32 CUDA tensor [n_seq][n_kv_heads][n or more]."""
+    if t.dtype is not _F32 or not t.is_cuda or t.dim() != 3 or t.shape[0] != cache.n_seq or t.shape[1] != cache.n_kv_heads or t.shape[2] < n:
+        _bad(f"{what}: expected float32 CUDA [{cache.n_seq}][{cache.n_kv_heads}][{n} or more]")
+    s0, s1, s2 = t.stride()
+    if cache.n_kv_heads == 1:
+        s1 = s0 if cache.n_seq > 1 else t.shape[2]
+    if s2 != 1 and t.shape[2] > 1 or cache.n_seq > 1 and s0 != s1 * cache.n_kv_heads:
+        _bad(f"{what}: kv heads have to lie evenly apart, their values side by side")
+    return t.data_ptr(), s1
+
+
+def attn_weights_q4_0(cache: KVCache, q, q_start, kv_len, lse, max_q_len: int, max_kv_len: int, seen=None,
+                      scale: float | None = None, window: int = 0, sums=None, out=None, keep: float = 1.0, status=None, stream=None):
+    """What the rows of an attention call gave each cached token: keep * sums + the sum of exp(score - lse) over the rows
+    of a kv head that see it (without sums for the new tokens), fp32 [n_seq][n_kv_heads][max_kv_len or more]. lse: as
+    attn_tree_q4_0 wrote it for the same q, seen, scale and window. out: where it goes (may be sums; None: a new tensor
+    of zeros behind the sequences' ends). Returns out."""
+    dim, n_seq = cache.head_dim, cache.n_seq
+    pq, n_tok, width, sq = _rows(q, "q")
+    heads = width // dim
+    if heads * dim != width:
+        _bad("attn_weights_q4_0: q must be [n_tok][heads * head_dim]")
+    if out is None:
+        out = _make((n_seq, cache.n_kv_heads, max_kv_len), _F32, q.device, stream, torch.zeros)
+    po, so = _per_head(out, cache, max_kv_len, "out")
+    pb, sb = (0, 0) if sums is None else _per_head(sums, cache, max_kv_len, "sums")
+    ps, words = _seen(seen, n_tok)
+    args = _ATTN_WEIGHTS_ARGS.pack(pq, _whole(q_start, _I32, n_seq + 1, "q_start"), _whole(kv_len, _I32, n_seq, "kv_len"),
+                                   _whole(lse, _F32, n_tok * heads, "lse"), ps, pb, po,
+                                   0 if status is None else _whole(status, _I32, 1, "status"), sq, sb, so, n_tok, heads, max_q_len,
+                                   max_kv_len, window, words, dim ** -0.5 if scale is None else scale, keep)
+    _enter("zdmmv_attn_weights_q4_0", cache.c, args, _raw_stream(stream))
+    return out
+
+
+def kv_evict_q4_0(cache: KVCache, to: KVCache, kv_len, sums, budget: int, max_kv_len: int, sinks: int = 0, recent: int = 0, index=None,
+                  sums_out=None, len_out=None, status=None, stream=None):
+    """Keep `budget` tokens of each kv head of a longer sequence: the first `sinks`, the last `recent` and those with the
+    largest sums (fp32 [n_seq][n_kv_heads][max_kv_len or more]), in their order in the pages of `to`, which are no pages
+    of `cache`. Returns index, int32 [n_seq][n_kv_heads][budget]: the kept tokens' positions, -1 behind the last.
+    sums_out: the kept tokens' sums; len_out: int32 [n_seq], the new lengths."""
+    n_seq, kv = cache.n_seq, cache.n_kv_heads
+    if index is None:
+        index = _make((n_seq, kv, budget), _I32, cache.pages.device, stream)
+    ps, ss = _per_head(sums, cache, max_kv_len, "sums")
+    po, so = (0, 0) if sums_out is None else _per_head(sums_out, cache, budget, "sums_out")
+    args = _KV_EVICT_ARGS.pack(_whole(kv_len, _I32, n_seq, "kv_len"), ps, _whole(index, _I32, n_seq * kv * budget, "index"), po,
+                               0 if len_out is None else _whole(len_out, _I32, n_seq, "len_out"),
+                               0 if status is None else _whole(status, _I32, 1, "status"), ss, so, max_kv_len, budget, sinks, recent)
+    _enter("zdmmv_kv_evict_q4_0", cache.c, to.c, args, _raw_stream(stream))
+    return index
+
+
+def kv_accept_q4_0(cache: KVCache, base, path, n_path, sums=None, len_out=None, status=None, stream=None):
+    """The accepted path of a drafted tree: of the tokens behind the first base[s] of sequence s, number path[s][j] moves to
+    position base[s] + j (j < n_path[s], path rising), and so do sums (fp32 [n_seq][n_kv_heads][tokens], nullable).
+    Returns len_out, int32 [n_seq]: the new lengths."""
+    n_seq = cache.n_seq
+    if path.dim() != 2 or path.shape[0] != n_seq:
+        _bad("kv_accept_q4_0: path must be int32 [n_seq][max_path]")
+    if len_out is None:
+        len_out = _make((n_seq,), _I32, path.device, stream)
+    args = _KV_ACCEPT_ARGS.pack(_whole(base, _I32, n_seq, "base"), _whole(path, _I32, 0, "path"), _whole(n_path, _I32, n_seq, "n_path"),
+                                _whole(len_out, _I32, n_seq, "len_out"), 0 if status is None else _whole(status, _I32, 1, "status"),
+                                *((0, 0, 0) if sums is None else (*_per_head(sums, cache, 0, "sums"), sums.shape[2])), path.shape[1])
+    _enter("zdmmv_kv_accept_q4_0", cache.c, args, _raw_stream(stream))
+    return len_out

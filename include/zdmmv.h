@@ -700,6 +700,14 @@ zdmmv_status zdmmv_attn_q4_0(const zdmmv_kv_cache *cache, const zdmmv_attn_args 
  * which zdmmv_kv_append_at_q4_0 takes apart.
  * ------------------------------------------------------------------------ */
 
+/* zdmmv_kv_append_q4_0 with positions of the rotation's own: token i goes to
+ * position pos[i] of its sequence's pages and is rotated by row rope_pos[i] of
+ * rope, a device int32 [n_tok], 4-byte aligned (NULL: pos itself). A token of
+ * which rope_pos is negative or past rope_rows is bad, unless rot_dim is 0 or pos
+ * is negative. */
+zdmmv_status zdmmv_kv_append_at_q4_0(const zdmmv_kv_cache *cache, const zdmmv_kv_append_args *args,
+                                     const int32_t *rope_pos, zdmmv_stream_t stream);
+
 /* zdmmv_attn_q4_0 with an order of the caller's among the new tokens. Of a
  * sequence with kv_len tokens in the cache and n new ones, new token i sees the
  * kv_len - n tokens before them and the new tokens j whose bit j of its row of
@@ -718,6 +726,103 @@ typedef struct {
 /* Errors: as zdmmv_attn_q4_0 (ERR_NULL for a NULL tree, ERR_SHAPE for too few words). */
 zdmmv_status zdmmv_attn_tree_q4_0(const zdmmv_kv_cache *cache, const zdmmv_attn_args *args,
                                   const zdmmv_attn_tree *tree, zdmmv_stream_t stream);
+
+/* What the query rows of an attention call gave each cached token. For token t of
+ * sequence s, kv head h, with n new tokens among kv_len:
+ *   out[s][h][t] = keep * before[s][h][t] + sum exp(scale * (q . k_t) - lse)
+ * over the new tokens and the heads of h's group that see t (the order of
+ * zdmmv_attn_q4_0, or that of `seen`), without the first part for the new tokens
+ * themselves (t >= kv_len - n): what stood there was of tokens that are gone. lse
+ * is what zdmmv_attn_tree_q4_0 wrote for the same rows, so a row's weights add up
+ * to one. Entries at and past kv_len are left as they are. Sums and scores are
+ * fp32 (scores as zdmmv_attn_q4_0 forms them; keep * before is one fma with the
+ * sum of the rest), in an order that does not depend on other sequences. */
+typedef struct {
+    const float *q;          /* device fp32 [n_tok][n_q_heads][head_dim], tokens q_stride apart (rotated) */
+    const int32_t *q_start;  /* device int32 [n_seq+1], rising from 0 to n_tok */
+    const int32_t *kv_len;   /* device int32 [n_seq], the new tokens included */
+    const float *lse;        /* device fp32 [n_tok][n_q_heads] */
+    const uint32_t *seen;    /* nullable; as zdmmv_attn_tree's */
+    const float *before;     /* nullable (zeros); device fp32 [n_seq][n_kv_heads], before_stride apart */
+    float *out;              /* device fp32 [n_seq][n_kv_heads], out_stride apart; may be `before` itself
+                                with the same stride, but overlaps no input otherwise */
+    int32_t *status_dev;     /* nullable device int32: 1 is stored for a bad sequence (as zdmmv_attn_q4_0's),
+                                whose entries are left as they are, or a bad page, whose tokens' are */
+    int64_t q_stride;        /* floats, a multiple of 4, >= n_q_heads*head_dim */
+    int64_t before_stride;   /* floats between kv heads, >= max_kv_len (ignored where before is NULL) */
+    int64_t out_stride;      /* the same for out */
+    int32_t n_tok;           /* rows of q and lse, >= 0 (0: out = keep * before) */
+    int32_t n_q_heads;       /* a multiple of n_kv_heads, at most 65535 */
+    int32_t max_q_len;       /* the most new tokens of a sequence, >= 1 */
+    int32_t max_kv_len;      /* the longest kv_len (an upper bound will do), >= 0 (0 is a no-op) */
+    int32_t window;          /* 0: no window; as the attention's */
+    int32_t seen_words;
+    float scale;             /* as the attention's */
+    float keep;              /* finite; 1 adds up, less forgets */
+} zdmmv_attn_weights_args;
+
+/* Errors: ERR_NULL, ERR_SHAPE, ERR_ALIGN, ERR_CUDA. */
+zdmmv_status zdmmv_attn_weights_q4_0(const zdmmv_kv_cache *cache, const zdmmv_attn_weights_args *args,
+                                     zdmmv_stream_t stream);
+
+/* Cuts a cache back. Of each kv head of a sequence longer than `budget` tokens
+ * the first `sinks`, the last `recent` and, of those between, the ones with the
+ * largest sums are kept, budget in all (of equal sums the earlier token; a NaN
+ * counts as -infinity). They go, in their order, to positions 0, 1, ... of the
+ * same sequence in the cache `to`, every head its own tokens; shorter sequences
+ * are copied whole. `to` has pages of its own: none of its pages is one that
+ * `from` reads (they may lie in the same buffer), so pages that several sequences
+ * share in `from` are safe. The bytes of a token are moved as they are; the
+ * places behind the last token of a tile of 16 become zeros. */
+typedef struct {
+    const int32_t *kv_len;   /* device int32 [n_seq]: the sequences' lengths in `from` */
+    const float *sums;       /* device fp32 [n_seq][n_kv_heads], sums_stride apart */
+    int32_t *index;          /* device int32 [n_seq][n_kv_heads][budget]: the kept tokens' positions in `from`,
+                                rising; -1 behind the last one */
+    float *sums_out;         /* nullable; device fp32 [n_seq][n_kv_heads], sums_out_stride apart: the kept tokens'
+                                sums, 0 behind the last one up to budget; overlaps no input */
+    int32_t *len_out;        /* nullable; device int32 [n_seq]: min(kv_len, budget); -1 for a bad sequence */
+    int32_t *status_dev;     /* nullable device int32: 1 is stored for a bad sequence or page */
+    int64_t sums_stride;     /* floats between kv heads, >= max_kv_len */
+    int64_t sums_out_stride; /* ... >= budget (ignored where sums_out is NULL) */
+    int32_t max_kv_len;      /* the longest kv_len (an upper bound will do), >= 0 */
+    int32_t budget;          /* >= 1, at most what max_pages of `to` hold */
+    int32_t sinks, recent;   /* >= 0, sinks + recent <= budget */
+} zdmmv_kv_evict_args;
+
+/* `from` and `to` have the same n_seq, n_kv_heads and head_dim; page_tokens may
+ * differ. A sequence with kv_len < 0, > max_kv_len or past its max_pages pages is
+ * bad: its index is all -1, its sums_out all 0, no page of it is written. A token
+ * of a page outside 0..n_pages-1 of `from` becomes NaN; a tile of such a page of
+ * `to` is not written. Two launches.
+ * Errors: ERR_NULL, ERR_SHAPE (sums_out as sums itself too), ERR_ALIGN, ERR_CUDA. */
+zdmmv_status zdmmv_kv_evict_q4_0(const zdmmv_kv_cache *from, const zdmmv_kv_cache *to, const zdmmv_kv_evict_args *args,
+                                 zdmmv_stream_t stream);
+
+/* Keeps the accepted path of a drafted tree: of the tokens that were appended
+ * behind the first base[s] ones of sequence s, number path[s][j] (from 0, in
+ * their order in the cache) moves to position base[s] + j, for all kv heads. The
+ * path rises: path[s][j] < path[s][j+1]. What lies behind it is no token any
+ * more (its bytes are left as they are). */
+typedef struct {
+    const int32_t *base;     /* device int32 [n_seq] */
+    const int32_t *path;     /* device int32 [n_seq][max_path] */
+    const int32_t *n_path;   /* device int32 [n_seq], 0 .. max_path: entries of path that count */
+    int32_t *len_out;        /* nullable; device int32 [n_seq]: base + n_path; -1 for a bad sequence. Neither base,
+                                path nor n_path */
+    int32_t *status_dev;     /* nullable device int32: 1 is stored for a bad sequence */
+    float *sums;             /* nullable; device fp32 [n_seq][n_kv_heads], sums_stride apart: the tokens' sums of
+                                attention weight, which move with them */
+    int64_t sums_stride;     /* floats between kv heads, >= sums_len (ignored, as sums_len, where sums is NULL) */
+    int64_t sums_len;        /* tokens of a kv head that sums has room for, >= max_path */
+    int32_t max_path;        /* 1 .. 1024 */
+} zdmmv_kv_accept_args;
+
+/* A sequence with base < 0, n_path outside 0..max_path, a path that does not
+ * rise from 0 or more or passes the sequence's max_pages pages (or sums_len, or 2^31 - 256), or with a page
+ * number outside 0..n_pages-1 where it would read or write, is bad: nothing of
+ * it moves. Errors: ERR_NULL, ERR_SHAPE, ERR_ALIGN, ERR_CUDA. */
+zdmmv_status zdmmv_kv_accept_q4_0(const zdmmv_kv_cache *cache, const zdmmv_kv_accept_args *args, zdmmv_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -13,7 +13,27 @@ class _AttnTree(ctypes.Structure):
     _fields_ = [("seen", ctypes.c_void_p), ("lse", ctypes.c_void_p), ("seen_words", ctypes.c_int32)]
 
 
-@pytest.mark.parametrize("name, c, packed", [("zdmmv_attn_tree", _AttnTree, Z._ATTN_TREE)])
+class _AttnWeightsArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("q", "q_start", "kv_len", "lse", "seen", "before", "out", "status_dev")] + [
+        (n, ctypes.c_int64) for n in ("q_stride", "before_stride", "out_stride")] + [
+        (n, ctypes.c_int32) for n in ("n_tok", "n_q_heads", "max_q_len", "max_kv_len", "window", "seen_words")] + [
+        (n, ctypes.c_float) for n in ("scale", "keep")]
+
+
+class _KvEvictArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("kv_len", "sums", "index", "sums_out", "len_out", "status_dev")] + [
+        (n, ctypes.c_int64) for n in ("sums_stride", "sums_out_stride")] + [
+        (n, ctypes.c_int32) for n in ("max_kv_len", "budget", "sinks", "recent")]
+
+
+class _KvAcceptArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("base", "path", "n_path", "len_out", "status_dev", "sums")] + [
+        (n, ctypes.c_int64) for n in ("sums_stride", "sums_len")] + [("max_path", ctypes.c_int32)]
+
+
+@pytest.mark.parametrize("name, c, packed", [
+    ("zdmmv_attn_tree", _AttnTree, Z._ATTN_TREE), ("zdmmv_attn_weights_args", _AttnWeightsArgs, Z._ATTN_WEIGHTS_ARGS),
+    ("zdmmv_kv_evict_args", _KvEvictArgs, Z._KV_EVICT_ARGS), ("zdmmv_kv_accept_args", _KvAcceptArgs, Z._KV_ACCEPT_ARGS)])
 def test_packed_structs_match_the_header(name, c, packed):
     B.test_packed_structs_match_the_header(name, c, packed)
 
@@ -54,3 +74,73 @@ def test_binding_refuses_bad_bits():
     with pytest.raises(ValueError):
         Z._seen(torch.zeros(3, 1, dtype=torch.int32), 3)     # a host tensor
     assert Z._seen(None, 3) == (0, 0)
+
+
+def _weights(**k):
+    d = dict(q=FAKE, q_start=FAKE, kv_len=FAKE, lse=FAKE, seen=FAKE, before=FAKE, out=2 * FAKE, status_dev=FAKE, q_stride=1024,
+             before_stride=100, out_stride=100, n_tok=3, n_q_heads=8, max_q_len=2, max_kv_len=100, window=0, seen_words=1, scale=0.1,
+             keep=1.0)
+    return _AttnWeightsArgs(**{**d, **k})
+
+
+@pytest.mark.parametrize("code, change", [
+    (2, dict(n_tok=-1)), (2, dict(n_q_heads=7)), (2, dict(n_q_heads=0)), (2, dict(n_q_heads=65536)), (2, dict(max_q_len=0)),
+    (2, dict(max_kv_len=-1)), (2, dict(window=-1)), (2, dict(scale=float("nan"))), (2, dict(keep=float("inf"))),
+    (2, dict(seen_words=0)), (2, dict(seen_words=(1 << 20) + 1)), (2, dict(max_q_len=33)), (2, dict(q_stride=1000)),
+    (2, dict(out_stride=99)), (2, dict(before_stride=99)), (2, dict(before=2 * FAKE, before_stride=104)),
+    (1, dict(q=None)), (1, dict(q_start=None)), (1, dict(kv_len=None)), (1, dict(lse=None)), (1, dict(out=None)),
+    (3, dict(q=FAKE + 4)), (3, dict(q_stride=1026)), (3, dict(q_start=FAKE + 1)), (3, dict(kv_len=FAKE + 2)), (3, dict(lse=FAKE + 2)),
+    (3, dict(seen=FAKE + 2)), (3, dict(before=FAKE + 1)), (3, dict(out=FAKE + 2)), (3, dict(status_dev=FAKE + 2)),
+    (0, dict(max_kv_len=0, q=None, out=None))])
+def test_weights_checks(L, code, change):  # noqa: F811
+    assert L.zdmmv_attn_weights_q4_0(ctypes.byref(_cache()), ctypes.byref(_weights(**change)), None) == code
+
+
+def _evict(**k):
+    d = dict(kv_len=FAKE, sums=FAKE, index=FAKE, sums_out=2 * FAKE, len_out=FAKE, status_dev=FAKE, sums_stride=100, sums_out_stride=64,
+             max_kv_len=100, budget=64, sinks=4, recent=16)
+    return _KvEvictArgs(**{**d, **k})
+
+
+@pytest.mark.parametrize("code, change", [
+    (2, dict(max_kv_len=-1)), (2, dict(max_kv_len=0x7fffffff, sums_stride=1 << 40)), (2, dict(budget=0)), (2, dict(budget=129, sums_out_stride=200)),
+    (2, dict(sinks=-1)), (2, dict(recent=-1)), (2, dict(sinks=49)), (2, dict(sinks=0x7fffffff, recent=0x7fffffff)),
+    (2, dict(sums_stride=99)), (2, dict(sums_out_stride=63)), (2, dict(sums_out=FAKE)),
+    (1, dict(kv_len=None)), (1, dict(sums=None)), (1, dict(index=None)),
+    (3, dict(kv_len=FAKE + 2)), (3, dict(sums=FAKE + 1)), (3, dict(index=FAKE + 2)), (3, dict(sums_out=FAKE + 2)), (3, dict(len_out=FAKE + 1)),
+    (3, dict(status_dev=FAKE + 2))])
+def test_evict_checks(L, code, change):  # noqa: F811
+    assert L.zdmmv_kv_evict_q4_0(ctypes.byref(_cache()), ctypes.byref(_cache()), ctypes.byref(_evict(**change)), None) == code
+
+
+@pytest.mark.parametrize("code, change", [(2, dict(n_seq=3)), (2, dict(n_kv_heads=1)), (2, dict(head_dim=64)), (2, dict(page_tokens=20)),
+                                          (1, dict(pages=None)), (3, dict(pages=FAKE + 8))])
+def test_evict_checks_both_caches(L, code, change):  # noqa: F811
+    call = L.zdmmv_kv_evict_q4_0
+    assert call(ctypes.byref(_cache()), ctypes.byref(_cache(**change)), ctypes.byref(_evict()), None) == code
+    assert call(ctypes.byref(_cache(**change)), ctypes.byref(_cache()), ctypes.byref(_evict()), None) == code
+
+
+def _accept(**k):
+    return _KvAcceptArgs(**{**dict(base=FAKE, path=FAKE, n_path=FAKE, len_out=FAKE, status_dev=FAKE, sums=FAKE, sums_stride=128, sums_len=100, max_path=8), **k})
+
+
+@pytest.mark.parametrize("code, change", [
+    (2, dict(max_path=0)), (2, dict(max_path=1025)), (2, dict(sums_stride=99)), (2, dict(sums_len=7)), (3, dict(sums=FAKE + 2)), (1, dict(base=None)), (1, dict(path=None)), (1, dict(n_path=None)),
+    (3, dict(base=FAKE + 1)), (3, dict(path=FAKE + 2)), (3, dict(n_path=FAKE + 2)), (3, dict(len_out=FAKE + 2)), (3, dict(status_dev=FAKE + 2))])
+def test_accept_checks(L, code, change):  # noqa: F811
+    assert L.zdmmv_kv_accept_q4_0(ctypes.byref(_cache()), ctypes.byref(_accept(**change)), None) == code
+
+
+def test_append_at_checks(L):  # noqa: F811
+    assert L.zdmmv_kv_append_at_q4_0(ctypes.byref(_cache()), ctypes.byref(B._append()), FAKE + 2, None) == 3
+    assert L.zdmmv_kv_append_at_q4_0(ctypes.byref(_cache()), ctypes.byref(B._append(n_tok=0)), FAKE, None) == 0
+    assert L.zdmmv_kv_append_at_q4_0(ctypes.byref(_cache()), ctypes.byref(B._append(rot_dim=3)), FAKE, None) == 2
+
+
+def test_null_structs(L):  # noqa: F811
+    c = ctypes.byref(_cache())
+    assert L.zdmmv_attn_weights_q4_0(c, None, None) == 1 and L.zdmmv_attn_weights_q4_0(None, ctypes.byref(_weights()), None) == 1
+    assert L.zdmmv_kv_accept_q4_0(c, None, None) == 1 and L.zdmmv_kv_accept_q4_0(None, ctypes.byref(_accept()), None) == 1
+    assert L.zdmmv_kv_evict_q4_0(c, c, None, None) == 1 and L.zdmmv_kv_evict_q4_0(c, None, ctypes.byref(_evict()), None) == 1
+    assert L.zdmmv_kv_append_at_q4_0(c, None, FAKE, None) == 1
