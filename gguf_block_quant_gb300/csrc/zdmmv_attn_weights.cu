@@ -2,19 +2,15 @@
 //
 //   out_t = keep before_t + sum_c exp(scale (q_c . k_t) - lse_c)      over the columns c (query rows of the kv head) that see t,
 //
-// from the keys alone: half of the cache's bytes, and no product with V.
+// from the keys alone: half of the cache's bytes, and no product with V. A token belongs to one warp (or thread), which goes over
+// all columns in a fixed order: nothing is joined, no atomics on sums.
 //
-// The scores are formed as in the narrow kernel of zdmmv_attn.cuh (A = a tile's 16 tokens of codes, B = four columns' upper and
-// lower parts; a product's C holds a column's two sums side by side), so that they agree with those that lse was made of. Every
-// tile belongs to one warp, which goes over all columns, four at a time, and adds up its tokens' weights in a fixed order:
-// nothing is joined, no atomics. Up to kBlockCols columns the parts of q lie in shared memory once; more columns come in blocks
-// of as many, between which the weights wait in shared memory.
-// The keys go from the cache to registers (they lie there in the order of the fragments): a lane's 128-bit loads of a tile run a
-// tile ahead of the products.
+// Few columns (decoding, small trees): attn_weights_kernel, on mma.sync. Many (prompts, drafted tokens of grouped heads):
+// attn_weights_tall_kernel, on tcgen05.
 #include <algorithm>
 #include <cmath>
 
-#include "zdmmv_attn.cuh"
+#include "zdmmv_attn_prompt.cuh"
 #include "zdmmv_internal.h"
 
 namespace zdmmv {
@@ -22,7 +18,6 @@ namespace {
 
 constexpr int kWeightWarps = 8, kWeightThreads = kWeightWarps * 32;
 constexpr int kBlockCols = 64;       // columns whose parts of q lie in shared memory at once
-constexpr int kMostChunk = 512;      // tiles of a CTA with several blocks of columns: their weights take 32 KB
 constexpr int kAllCols = 0x7fffff00; // a column tile of all columns
 
 struct WeightArgs {
@@ -31,9 +26,45 @@ struct WeightArgs {
     const float *lse_in, *before;
     float *out;
     int64_t before_stride, out_stride;  // between kv heads
-    int32_t chunks, chunk;              // CTAs of an item, tiles of one
+    uint8_t *images;                    // the tall kernel's blocks of q
+    FastDiv by_blocks;                  // ... of an item, at most
+    int32_t chunks;                     // the tall kernel's CTAs of an item
     float keep;
 };
+
+// How a column's product with a key becomes its weight, p = exp2(x * product + y), and which tokens it sees.
+struct Column {
+    float x, y;
+    int low, end;
+};
+__device__ __forceinline__ Column column_of(const WeightArgs &w, const AttnRange &r, int kvh, int col, float lse, float down) {
+    const AttnArgs &a = w.a;
+    const int i = a.by_group.div(col);
+    // one that is none adds 2^-infinity, and where tokens are masked at all it sees none: a key may be no number
+    if (i >= r.n) return {0.0f, -INFINITY, 0, 0};
+    Column c;
+    c.x = fmaxf(fabsf(a.scale_log2) * down, 1e-37f);
+    c.y = -1.44269504088896340736f * lse;
+    if (a.seen) {
+        c.low = tree_low(a, r, i);
+        c.end = r.len;
+    } else {
+        c.end = max(0, r.len - (r.n - 1 - i));
+        c.low = a.window > 0 ? max(0, c.end - a.window) : 0;
+    }
+    return c;
+}
+__device__ __forceinline__ const float *column_lse(const WeightArgs &w, const AttnRange &r, int kvh, int col) {
+    const int i = w.a.by_group.div(col);
+    return w.lse_in + static_cast<int64_t>(r.q0 + i) * w.a.n_q_heads + kvh * w.a.group + (col - i * w.a.group);
+}
+// The cache tiles low .. end-1 of a sequence whose tokens' sums a call has to write: all, or, where sums stay in place and
+// unscaled, those that a row sees.
+__device__ __forceinline__ void tiles_of(const WeightArgs &w, const AttnRange &r, int &low, int &end) {
+    low = 0;
+    end = r.bad ? 0 : (r.len + kKvSlab - 1) / kKvSlab;
+    if (w.keep == 1.0f && w.before == w.out) low = min(r.slab0, end);
+}
 
 template <int N, int W> __device__ __forceinline__ void ldg_words(const uint8_t *at, int step, uint32_t (&w)[N]) {
 #pragma unroll
@@ -50,60 +81,151 @@ template <int N, int W> __device__ __forceinline__ void ldg_words(const uint8_t 
         }
     }
 }
-// A lane's part of a tile's keys: of the tokens g and g + 8 the codes of 8 dimensions of every block, and the scales.
-template <int NB> struct Keys {
-    uint32_t code[2][NB], scale[2][NB];
-    __device__ void load(const uint8_t *tile, int lane) {
-        using G = KvGeom<NB>;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            ldg_words<NB, G::kVec>(tile + (h * NB * 32 + lane * G::kVec) * 4, 128 * G::kVec, code[h]);
-            ldg_words<NB, G::kVec>(tile + G::kKScaleAt + ((lane >> 3) + 4 * h) * NB * 4, 4 * G::kVec, scale[h]);
-        }
-    }
-};
+
+__device__ __forceinline__ void cp_async_16(uint32_t to, const void *from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void cp_async_4(uint32_t to, const void *from) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// ------------------------------------------------------------------ up to kBlockCols columns
+// The scores are formed as in the narrow kernel of zdmmv_attn.cuh (A = a tile's 16 tokens of codes, B = four columns' upper and
+// lower parts; a product's C holds a column's two sums side by side), so that they agree with those that lse was made of. The
+// steps (8 tiles, one a warp) of all kv heads of all sequences one after another are a row, of which every CTA of a grid that
+// fills the device takes an equal stretch, whatever the lengths. A warp keeps the next tiles' keys, and their tokens' earlier
+// sums, on their way into its own ring in shared memory.
+constexpr int kWeightStages = 4;
+template <int NB> constexpr int kStageBytes = 9 * NB * kQK + kKvSlab * 4;
+template <int NB> constexpr size_t kWeightRing = static_cast<size_t>(kWeightWarps) * kWeightStages * kStageBytes<NB>;
 
 template <int NB> __global__ void __launch_bounds__(kWeightThreads, 2) attn_weights_kernel(WeightArgs w) {
     using G = KvGeom<NB>;
     const AttnArgs &a = w.a;
-    extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ float2 sh_exp[kBlockCols];  // p = exp2(x * score + y)
-    __shared__ int2 sh_see[kBlockCols];    // first token that a column sees, and the one after the last
-    __shared__ int sh_low, sh_end;
-    uint2 *q_sm = reinterpret_cast<uint2 *>(smem);                                     // [group of 4][2 NB][lane]
-    float *wait_sm = reinterpret_cast<float *>(smem + kBlockCols / 4 * 2 * NB * 256);  // weights between blocks of columns
+    constexpr int kKeyBytes = 9 * G::kDim;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ Column sh_col[kBlockCols];
+    __shared__ int sh_low, sh_end, sh_scan[kWeightWarps], sh_seq, sh_from;
+    __shared__ uint32_t sh_magic;
+    uint2 *q_sm = reinterpret_cast<uint2 *>(smem + kWeightRing<NB>);  // [group of 4][2 NB][lane]
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+    const uint32_t ring = smem_addr(smem) + warp * (kWeightStages * kStageBytes<NB>);
+    if (tid == 0) sh_magic = kCodeMagic;
     block_op_wait();
     block_op_release();
-    const int item = w.by_chunks.div(blockIdx.x), chunk = w.by_chunks.mod(blockIdx.x, item);
-    const int seq = a.by_heads.div(item), kvh = a.by_heads.mod(item, seq);
-    const AttnRange r = attn_range<true>(a, seq, 0, kAllCols);
-    if (r.bad) {
-        if (tid == 0 && a.status) *a.status = 1;
-        return;
+    const int heads = a.c.n_kv_heads, n_seq = a.c.n_seq;
+    const auto steps_of = [&](int seq) {
+        const AttnRange r = attn_range<true>(a, seq, 0, kAllCols);
+        int low, end;
+        tiles_of(w, r, low, end);
+        if (r.bad && blockIdx.x == 0 && a.status) *a.status = 1;
+        return (end - low + kWeightWarps - 1) / kWeightWarps;
+    };
+    // this CTA's stretch of the row, and the sequence that it begins in
+    int64_t at, last;
+    {
+        int64_t total = 0;
+        int kept = 0;
+        for (int s0 = 0; s0 < n_seq; s0 += kWeightThreads) {
+            const int n = s0 + tid < n_seq ? steps_of(s0 + tid) * heads : 0;
+            if (s0 == 0) kept = n;
+            int all;
+            (void)AttnWalk::upto(n, sh_scan, all);
+            total += all;
+            __syncthreads();
+        }
+        const int64_t ctas = min(static_cast<int64_t>(gridDim.x), total);
+        if (blockIdx.x >= ctas) return;
+        at = total * blockIdx.x / ctas;
+        last = total * (blockIdx.x + 1) / ctas;
+        for (int64_t s0 = 0, before = 0;; s0 += kWeightThreads) {
+            const int seq = static_cast<int>(s0) + tid, n = s0 == 0 ? kept : (seq < n_seq ? steps_of(seq) * heads : 0);
+            int all;
+            const int64_t from = before + AttnWalk::upto(n, sh_scan, all) - n;
+            if (n > 0 && at >= from && at < from + n) {
+                sh_seq = seq;
+                sh_from = static_cast<int>(at - from);
+            }
+            before += all;
+            __syncthreads();
+            if (at < before) break;
+        }
     }
-    const int tiles = (r.len + kKvSlab - 1) / kKvSlab, first = chunk * w.chunk, last = min(tiles, first + w.chunk);
-    if (first >= last) return;
-    const int base = r.len - r.n, columns = r.n * a.group;
-    const bool tree = a.seen != nullptr;
-    const float *before = w.before ? w.before + static_cast<int64_t>(item) * w.before_stride : nullptr;
-    float *out = w.out + static_cast<int64_t>(item) * w.out_stride;
-    const int32_t *table = a.c.table + static_cast<int64_t>(seq) * a.c.max_pages;
-    const uint8_t *head = a.c.pages + static_cast<int64_t>(kvh) * static_cast<int>(a.by_page_tiles.d) * G::kTileBytes;
+    int seq = sh_seq, inside = sh_from;  // the step of the sequence's steps
+    const uint32_t magic = lds32(smem_addr(&sh_magic));
     const uint32_t pick = (g & 1) ? 0x7632u : 0x5410u;  // the token's half of two words of scales
 
-    for (int col0 = 0;; col0 += kBlockCols) {
-        const int cols = max(0, min(kBlockCols, columns - col0)), groups = (cols + 3) / 4;
-        const bool last_block = col0 + kBlockCols >= columns;
-        if (col0 > 0) __syncthreads();  // the block before is done with
+    while (true) {
+        const AttnRange r = attn_range<true>(a, seq, 0, kAllCols);
+        int low, end;
+        tiles_of(w, r, low, end);
+        const int steps = (end - low + kWeightWarps - 1) / kWeightWarps;
+        if (inside >= steps * heads) {  // the next sequence, as long as the stretch has steps of one
+            ++seq;
+            inside = 0;
+            continue;
+        }
+        const int kvh = inside / steps, step = inside - kvh * steps;
+        const int n_steps = static_cast<int>(min(static_cast<int64_t>(steps - step), last - at));
+        const int first = low + step * kWeightWarps, stop = min(end, first + n_steps * kWeightWarps);
+        const int base = r.len - r.n, columns = r.n * a.group, groups = (columns + 3) / 4;
+        const bool tree = a.seen != nullptr;
+        const int64_t item = static_cast<int64_t>(seq) * heads + kvh;
+        const float *before = w.before ? w.before + item * w.before_stride : nullptr;
+        float *out = w.out + item * w.out_stride;
+        const int32_t *table = a.c.table + static_cast<int64_t>(seq) * a.c.max_pages;
+        const uint8_t *head = a.c.pages + static_cast<int64_t>(kvh) * static_cast<int>(a.by_page_tiles.d) * G::kTileBytes;
+
+        // the warp's tiles are first + warp + 8 k; a lane looks up every 32nd one's page
+        const uint8_t *src = nullptr;
+        bool wrong = false;
+        uint32_t have = 0, skip = 0;  // by k % 32: the tile's keys are (asked for); its page is bad
+        const auto ask = [&](int k) {
+            const int tile = first + warp + kWeightWarps * k;
+            if (tile < stop) {
+                if ((k & 31) == 0) {
+                    const int mine = tile + kWeightWarps * lane;
+                    src = nullptr;
+                    wrong = false;
+                    if (mine < stop && mine >= r.slab0 && mine < r.slab0 + r.slabs && columns > 0) {
+                        const int slot = a.by_page_tiles.div(mine), page = table[slot];
+                        wrong = page < 0 || page >= a.c.n_pages;
+                        if (wrong && a.status) *a.status = 1;
+                        if (!wrong)
+                            src = head + page * a.c.page_bytes + static_cast<int64_t>(a.by_page_tiles.mod(mine, slot)) * G::kTileBytes;
+                    }
+                }
+                const uint8_t *from =
+                    reinterpret_cast<const uint8_t *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), k & 31));
+                const uint32_t bit = 1u << (k & 31);
+                have = from ? have | bit : have & ~bit;
+                skip = __shfl_sync(0xffffffffu, wrong ? 1 : 0, k & 31) ? skip | bit : skip & ~bit;
+                const uint32_t to = ring + (k % kWeightStages) * kStageBytes<NB>;
+                if (from) {
+#pragma unroll
+                    for (int c = lane; c < 18 * NB; c += 32) cp_async_16(to + 16 * c, from + 16 * c + (c < 16 * NB ? 0 : G::kCodeBytes));
+                }
+                const int tok = tile * kKvSlab + lane;
+                if (before && lane < kKvSlab && tok < base) cp_async_4(to + kKeyBytes + 4 * lane, before + tok);
+            }
+            cp_async_commit();
+        };
+#pragma unroll
+        for (int k = 0; k < kWeightStages - 1; ++k) ask(k);
+
+        __syncthreads();  // the segment before is done with q and its columns
         if (tid == 0) {
             sh_low = 0;
-            sh_end = r.len;
+            sh_end = tree ? base : r.len;
         }
         __syncthreads();
         for (int grp = warp; grp < groups; grp += kWeightWarps) {
             float v[NB][8], top = 0.0f, up, down;
-            const int col = col0 + 4 * grp + g / 2, i = a.by_group.div(col);
+            const int col = 4 * grp + g / 2;
+            const bool lead = t == 0 && (g & 1) == 0;
+            const float lse = lead && col < columns ? *column_lse(w, r, kvh, col) : 0.0f;
             load_q<NB>(a, r, kvh, col, t, v);
 #pragma unroll
             for (int b = 0; b < NB; ++b)
@@ -121,80 +243,45 @@ template <int NB> __global__ void __launch_bounds__(kWeightThreads, 2) attn_weig
                     split_h2(v[b][2 * h + 1] * up * 0.0625f, v[b][2 * h + 5] * up * 0.0625f, f[2], f[3]);
                     q_sm[(grp * 2 * NB + 2 * b + h) * 32 + lane] = (g & 1) ? make_uint2(f[1], f[3]) : make_uint2(f[0], f[2]);
                 }
-            if (t == 0 && (g & 1) == 0) {
-                const int at = 4 * grp + g / 2;
-                // a column that is none adds 2^-infinity
-                float2 e = make_float2(0.0f, -INFINITY);
-                int2 see = make_int2(0, r.len);
-                if (i < r.n) {
-                    const float lse = w.lse_in[static_cast<int64_t>(r.q0 + i) * a.n_q_heads + kvh * a.group + (col - i * a.group)];
-                    e = make_float2(fmaxf(fabsf(a.scale_log2) * down, 1e-37f), -1.44269504088896340736f * lse);
-                    if (tree) {
-                        see.x = tree_low(a, r, i);
-                        atomicMin(&sh_end, base);
-                    } else {
-                        see.y = max(0, r.len - (r.n - 1 - i));
-                        see.x = a.window > 0 ? max(0, see.y - a.window) : 0;
-                        atomicMin(&sh_end, see.y);
-                    }
-                    atomicMax(&sh_low, see.x);
+            if (lead) {
+                const Column c = column_of(w, r, kvh, col, lse, down);
+                if (col < columns) {
+                    atomicMin(&sh_end, c.end);
+                    atomicMax(&sh_low, c.low);
                 }
-                sh_exp[at] = e;
-                sh_see[at] = see;
+                sh_col[col] = c;
             }
         }
         __syncthreads();
         const int low_max = sh_low, end_min = sh_end;
 
-        // the warp's tiles are first + warp + 8 k; a lane looks up every 32nd one's page
-        const uint8_t *src = nullptr;
-        bool wrong = false;
-        const auto look = [&](int k0) {
-            const int tile = first + warp + kWeightWarps * (k0 + lane);
-            src = nullptr;
-            wrong = false;
-            if (tile < last && tile >= r.slab0 && tile < r.slab0 + r.slabs && columns > 0) {
-                const int slot = a.by_page_tiles.div(tile), page = table[slot];
-                wrong = page < 0 || page >= a.c.n_pages;
-                if (wrong && a.status) *a.status = 1;
-                if (!wrong)
-                    src = head + page * a.c.page_bytes + static_cast<int64_t>(a.by_page_tiles.mod(tile, slot)) * G::kTileBytes;
-            }
-        };
-        const auto source = [&](int k) {
-            return reinterpret_cast<const uint8_t *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), k & 31));
-        };
-        Keys<NB> keys;
-        look(0);
-        const uint8_t *now = source(0);
-        bool skip = __shfl_sync(0xffffffffu, wrong ? 1 : 0, 0) != 0;
-        if (now) keys.load(now, lane);
-        for (int k = 0, tile = first + warp; tile < last; ++k, tile += kWeightWarps) {
-            const int t0 = tile * kKvSlab, tok = t0 + g + ((t & 1) ? 8 : 0);  // the token that lanes t = 0 and 1 store
-            uint32_t f[NB][8];
-            float dd[NB][2];
-            const bool some = now != nullptr, left = skip;
-            if (some) {
+        for (int k = 0, tile = first + warp; tile < stop; ++k, tile += kWeightWarps) {
+            cp_async_wait<kWeightStages - 2>();
+            __syncwarp();  // all lanes' copies of tile k are there, and all are done with the slot before
+            ask(k + kWeightStages - 1);
+            const uint32_t stage = ring + (k % kWeightStages) * kStageBytes<NB>;
+            const int t0 = tile * kKvSlab;
+            float s0 = 0.0f, s1 = 0.0f;  // tokens t0 + g and t0 + g + 8
+            if (have >> (k & 31) & 1u) {
+                uint32_t f[NB][8];
+                float dd[NB][2];
+                uint32_t kw[2][NB], dk[2][NB];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    lds_words<NB, G::kVec>(stage + (h * NB * 32 + lane * G::kVec) * 4, 128 * G::kVec, kw[h]);
+                    lds_words<NB, G::kVec>(stage + G::kCodeBytes + ((lane >> 3) + 4 * h) * NB * 4, 4 * G::kVec, dk[h]);
+                }
 #pragma unroll
                 for (int b = 0; b < NB; ++b) {
                     uint32_t k0[4], k1[4];
-                    code_pairs(keys.code[0][b], kCodeMagic, k0);
-                    code_pairs(keys.code[1][b], kCodeMagic, k1);
+                    code_pairs(kw[0][b], magic, k0);
+                    code_pairs(kw[1][b], magic, k1);
                     f[b][0] = k0[0]; f[b][1] = k1[0]; f[b][2] = k0[1]; f[b][3] = k1[1];
                     f[b][4] = k0[2]; f[b][5] = k1[2]; f[b][6] = k0[3]; f[b][7] = k1[3];
-                    const float2 d = f2_parts(f2_half2(__byte_perm(keys.scale[0][b], keys.scale[1][b], pick)));
+                    const float2 d = f2_parts(f2_half2(__byte_perm(dk[0][b], dk[1][b], pick)));
                     dd[b][0] = d.x;
                     dd[b][1] = d.y;
                 }
-            }
-            if (tile + kWeightWarps < last) {
-                if (((k + 1) & 31) == 0) look(k + 1);
-                now = source(k + 1);
-                skip = __shfl_sync(0xffffffffu, wrong ? 1 : 0, (k + 1) & 31) != 0;
-                if (now) keys.load(now, lane);
-            }
-            float s0 = 0.0f, s1 = 0.0f;  // tokens t0 + g and t0 + g + 8
-            if (some) {
                 const bool masked = t0 < low_max || t0 + kKvSlab > end_min;
                 for (int grp = 0; grp < groups; ++grp) {
                     float x0 = 0.0f, x1 = 0.0f;
@@ -208,14 +295,13 @@ template <int NB> __global__ void __launch_bounds__(kWeightThreads, 2) attn_weig
                         x0 = fmaf(dd[b][0], c[0] + c[1], x0);
                         x1 = fmaf(dd[b][1], c[2] + c[3], x1);
                     }
-                    const float2 e = sh_exp[4 * grp + t];
-                    float p0 = exp2_approx(fmaf(x0, e.x, e.y)), p1 = exp2_approx(fmaf(x1, e.x, e.y));
+                    const Column c = sh_col[4 * grp + t];
+                    float p0 = exp2_approx(fmaf(x0, c.x, c.y)), p1 = exp2_approx(fmaf(x1, c.x, c.y));
                     if (masked) {
-                        const int2 see = sh_see[4 * grp + t];
-                        const int i = a.by_group.div(col0 + 4 * grp + t);
+                        const int i = a.by_group.div(4 * grp + t);
                         const uint32_t bits = tree && i < r.n ? tree_bits(a, r, i, t0) : ~0u;
-                        if (t0 + g < see.x || t0 + g >= see.y || !(bits >> g & 1u)) p0 = 0.0f;
-                        if (t0 + g + 8 < see.x || t0 + g + 8 >= see.y || !(bits >> (g + 8) & 1u)) p1 = 0.0f;
+                        if (t0 + g < c.low || t0 + g >= c.end || !(bits >> g & 1u)) p0 = 0.0f;
+                        if (t0 + g + 8 < c.low || t0 + g + 8 >= c.end || !(bits >> (g + 8) & 1u)) p1 = 0.0f;
                     }
                     s0 += p0;
                     s1 += p1;
@@ -225,24 +311,375 @@ template <int NB> __global__ void __launch_bounds__(kWeightThreads, 2) attn_weig
                 s0 += __shfl_xor_sync(0xffffffffu, s0, 2);
                 s1 += __shfl_xor_sync(0xffffffffu, s1, 2);
             }
-            if (t < 2 && tok < r.len && !left) {
-                float s = t == 0 ? s0 : s1;
-                float *rest = wait_sm + (tile - first) * kKvSlab + (tok - t0);
-                if (col0 > 0) s += *rest;
-                if (!last_block) *rest = s;
-                else out[tok] = before && tok < base ? fmaf(w.keep, before[tok], s) : s;
+            const int own = g + (t == 1 ? 8 : 0), tok = t0 + own;  // the token that lanes t = 0 and 1 store
+            if (t < 2 && tok < r.len && !(skip >> (k & 31) & 1u)) {
+                const float s = t == 0 ? s0 : s1;
+                out[tok] = before && tok < base ? fmaf(w.keep, __uint_as_float(lds32(stage + kKeyBytes + 4 * own)), s) : s;
             }
         }
-        if (last_block) break;
+        cp_async_wait<0>();
+        at += n_steps;
+        inside += n_steps;
+        if (at >= last) break;
     }
 }
 
-template <int NB> cudaError_t launch_weights(const WeightArgs &w, int64_t items, int64_t columns, cudaStream_t st) {
+// ------------------------------------------------------------------ more columns
+// S = K Q^T on tcgen05: a CTA takes 128 tokens of a kv head, the 128 rows of D, and goes over all columns, 64 at a time, so that
+// a thread has one token's products with 32 columns in registers and adds their weights up by itself.
+//  * K is the A operand, in tensor memory for the CTA's life, Q the B operand, in shared memory (rows of 128 bytes swizzled by
+//    128 bytes), each in two fp16 parts (k exactly, q to 22 bits; zdmmv_attn_prompt.cuh): 3 D/16 products a block.
+//  * Every CTA of a kv head needs all of its q: weights_q_kernel makes the operands (and what each column needs to become a
+//    weight) once, in the workspace, as they lie in shared memory, and the CTAs bring them with one bulk copy a block, two
+//    blocks ahead. (Each CTA turning q into operands by itself: 141 us for 256 tokens over 8192 instead of the present time at
+//    the end of this comment, 700 of 1000 instructions a block.)
+//  * One lane starts a block's products while all threads take the weights of the block before; D is double. Two CTAs an SM
+//    (heads of up to 128 dimensions) fill each other's gaps.
+// Where a token has a scale of 2^13 or more, the 128 tokens' operand is in units of 16, as there.
+constexpr int kTallTokens = 128, kTallSlots = 3;
+template <int NB> struct TallGeom {
+    static constexpr int kDim = NB * kQK, kChunks = (NB + 1) / 2;  // of 64 dimensions
+    static constexpr uint32_t kKChunk = kTallTokens * 128, kQChunk = kBlockCols * 128;
+    static constexpr uint32_t kKPart = kChunks * kKChunk, kQPart = kChunks * kQChunk;
+    // a block of q in the workspace: the operand's parts, the columns' (x, y) by two, what they see, and of it the latest first
+    // token and the earliest end
+    static constexpr uint32_t kExpAt = 2 * kQPart, kSeeAt = kExpAt + kBlockCols * 8, kBothAt = kSeeAt + kBlockCols * 8;
+    static constexpr uint32_t kImage = kBothAt + 16, kSlot = (kImage + 1023) / 1024 * 1024;
+    static constexpr size_t kSmem = kTallSlots * kSlot + 1024;  // aligned to 1024; before the blocks of q, K
+    static_assert(2 * kKPart <= kTallSlots * kSlot, "K's rows");
+    static constexpr int kCtas = NB <= 4 ? 2 : 1;
+    static constexpr uint32_t kTm = NB <= 4 ? 256 : 512, kTmD = kDim;  // K's columns, then twice 64 of D
+    static_assert(kTmD + 2 * kBlockCols <= kTm, "tensor memory");
+};
+// Blocks of a call's q: sequence s's first is number q0 group / 64 + s, which leaves room for all of those before it.
+__device__ __forceinline__ int64_t first_block(const WeightArgs &w, const AttnRange &r, int seq) {
+    return static_cast<int64_t>(r.q0) * w.a.group / kBlockCols + seq;
+}
+int64_t weight_blocks(int n_seq, int n_tok, int group) { return static_cast<int64_t>(n_tok) * group / kBlockCols + n_seq; }
+template <int NB> __device__ __forceinline__ uint8_t *block_image(const WeightArgs &w, int64_t block, int kvh) {
+    return w.images + (block * w.a.c.n_kv_heads + kvh) * TallGeom<NB>::kImage;
+}
+
+// A CTA makes a block: whole rows by a warp, four dimensions a lane of each 128.
+template <int NB> __global__ void __launch_bounds__(kWeightThreads) weights_q_kernel(WeightArgs w) {
+    using T = TallGeom<NB>;
+    constexpr int D = T::kDim, kPasses = (D + 127) / 128, kPerWarp = kBlockCols / kWeightWarps;
+    const AttnArgs &a = w.a;
+    __shared__ int sh_low, sh_end;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    block_op_wait();
+    block_op_release();
+    const int item = w.by_blocks.div(blockIdx.x), block = w.by_blocks.mod(blockIdx.x, item);
+    const int seq = a.by_heads.div(item), kvh = a.by_heads.mod(item, seq);
+    const AttnRange r = attn_range<true>(a, seq, 0, kAllCols);
+    const int columns = r.n * a.group, col0 = block * kBlockCols + warp * kPerWarp;
+    if (r.bad || block * kBlockCols >= columns) return;
+    float4 x[kPerWarp][kPasses];
+#pragma unroll
+    for (int j = 0; j < kPerWarp; ++j) {
+        const int col = col0 + j, i = a.by_group.div(col);
+        const float *q = a.q + static_cast<int64_t>(r.q0 + (i < r.n ? i : 0)) * a.q_stride +
+                         static_cast<int64_t>(kvh * a.group + (i < r.n ? col - i * a.group : 0)) * D + 4 * lane;
+#pragma unroll
+        for (int p = 0; p < kPasses; ++p)
+            x[j][p] = i < r.n && 128 * p + 4 * lane < D ? __ldg(reinterpret_cast<const float4 *>(q + 128 * p)) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    const float lse = lane < kPerWarp && col0 + lane < columns ? __ldg(column_lse(w, r, kvh, col0 + lane)) : 0.0f;
+    if (tid == 0) {
+        sh_low = 0;
+        sh_end = a.seen ? r.len - r.n : r.len;
+    }
+    __syncthreads();
+    uint8_t *image = block_image<NB>(w, first_block(w, r, seq) + block, kvh);
+    float up[kPerWarp], mine = 0.0f;
+#pragma unroll
+    for (int j = 0; j < kPerWarp; ++j) {
+        float top = 0.0f, down;
+#pragma unroll
+        for (int p = 0; p < kPasses; ++p)
+            top = fmaxf(fmaxf(fmaxf(top, fabsf(x[j][p].x)), fmaxf(fabsf(x[j][p].y), fabsf(x[j][p].z))), fabsf(x[j][p].w));
+#pragma unroll
+        for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+        q_unit(top, a.scale_log2, up[j], down);
+        if (lane == j) mine = down;
+    }
+    if (lane < kPerWarp) {
+        const int at = warp * kPerWarp + lane;
+        const Column c = column_of(w, r, kvh, col0 + lane, lse, mine);
+        float *e = reinterpret_cast<float *>(image + T::kExpAt) + 4 * (at / 2) + (at & 1);  // two columns' x, then their y
+        e[0] = c.x;
+        e[2] = c.y;
+        reinterpret_cast<int2 *>(image + T::kSeeAt)[at] = make_int2(c.low, c.end);
+        if (col0 + lane < columns) {
+            atomicMax(&sh_low, c.low);
+            atomicMin(&sh_end, c.end);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < kPerWarp; ++j) {
+        const int to = warp * kPerWarp + j;  // the operand's row
+#pragma unroll
+        for (int p = 0; p < kPasses; ++p) {
+            const float4 v = x[j][p];
+            const bool odd = lane & 1;
+            const float o0 = __shfl_xor_sync(0xffffffffu, odd ? v.x : v.z, 1), o1 = __shfl_xor_sync(0xffffffffu, odd ? v.y : v.w, 1);
+            uint2 hi, lo;  // dimensions 0 4 1 5, or 2 6 3 7, of 8
+            split_h2((odd ? o0 : v.x) * up[j], (odd ? v.z : o0) * up[j], hi.x, lo.x);
+            split_h2((odd ? o1 : v.y) * up[j], (odd ? v.w : o1) * up[j], hi.y, lo.y);
+            if (128 * p + 4 * lane < D) {
+                const int t8 = 16 * p + (lane >> 1);
+                uint8_t *at = image + (t8 >> 3) * T::kQChunk + to * 128 + (((t8 & 7) ^ (to & 7)) << 4) + (lane & 1) * 8;
+                *reinterpret_cast<uint2 *>(at) = hi;
+                *reinterpret_cast<uint2 *>(at + T::kQPart) = lo;
+            }
+        }
+    }
+    __syncthreads();
+    if (tid == 0) *reinterpret_cast<int2 *>(image + T::kBothAt) = make_int2(sh_low, sh_end);
+}
+
+template <int NB> __global__ void __launch_bounds__(kWeightThreads, TallGeom<NB>::kCtas) attn_weights_tall_kernel(WeightArgs w) {
+    using G = KvGeom<NB>;
+    using T = TallGeom<NB>;
+    constexpr int D = G::kDim;
+    const AttnArgs &a = w.a;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ int sh_skip[kWeightWarps], sh_dead;
+    __shared__ float sh_sum[kTallTokens];
+    __shared__ __align__(8) uint64_t bar[kTallSlots + 2];  // by slot: its block of q has come; by block % 2: its products are done
+    __shared__ uint32_t sh_tm;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, half = warp >> 2;
+    block_op_release();
+    // until its wait below the kernel reads only what was there before weights_q_kernel, which began after all that was
+    // complete, and writes nothing but the status
+    const int item = w.by_chunks.div(blockIdx.x), chunk = w.by_chunks.mod(blockIdx.x, item);
+    const int seq = a.by_heads.div(item), kvh = a.by_heads.mod(item, seq);
+    const AttnRange r = attn_range<true>(a, seq, 0, kAllCols);
+    const int first = chunk * kTallTokens, live = r.bad ? 0 : r.len - first;  // tokens from `live` on are none
+    if (r.bad && tid == 0 && a.status) *a.status = 1;
+    if (live <= 0) {
+        block_op_wait();
+        return;
+    }
+    const int base = r.len - r.n, columns = r.n * a.group, blocks = (columns + kBlockCols - 1) / kBlockCols;
+    const bool tree = a.seen != nullptr;
+    const int row = (warp & 3) * 32 + lane, tok = first + row;  // this thread's token, with half of a block's columns
+    float *out = w.out + static_cast<int64_t>(item) * w.out_stride + tok;
+    const bool had = w.before != nullptr && tok < base && half == 0;
+    const float earlier = had ? w.before[static_cast<int64_t>(item) * w.before_stride + tok] : 0.0f;
+    constexpr int kSlabs = kTallTokens / kKvSlab;
+    if (columns == 0 || chunk * kSlabs >= r.slab0 + r.slabs || (chunk + 1) * kSlabs <= r.slab0) {  // nobody sees them
+        block_op_wait();
+        if (half == 0 && row < live) *out = had ? w.keep * earlier : 0.0f;
+        return;
+    }
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&sh_tm)), "n"(T::kTm) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    if (tid == 0) {
+        for (int k = 0; k < kTallSlots + 2; ++k) mbar_init(&bar[k], 1);
+        fence_barrier_init();
+        sh_dead = 0;
+    }
+    const uint32_t slots = (smem_addr(smem) + 1023u) & ~1023u;
+    uint8_t *slot_mem = smem + (slots - smem_addr(smem));
+
+    // K: a cache tile a warp, as rows in shared memory, whence each thread puts half of its token's row into tensor memory
+    float unit;
+    {
+        const int slab = chunk * kSlabs + warp;
+        const uint8_t *src = nullptr;
+        if (slab * kKvSlab < r.len) {
+            const int slot = a.by_page_tiles.div(slab), page = a.c.table[static_cast<int64_t>(seq) * a.c.max_pages + slot];
+            if (page >= 0 && page < a.c.n_pages)
+                src = a.c.pages + page * a.c.page_bytes +
+                      (static_cast<int64_t>(kvh) * static_cast<int>(a.by_page_tiles.d) + a.by_page_tiles.mod(slab, slot)) * G::kTileBytes;
+            else if (lane == 0 && a.status) *a.status = 1;
+        }
+        if (lane == 0) sh_skip[warp] = src == nullptr;
+        uint32_t code[2][NB], scale[2][NB], any = 0;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+#pragma unroll
+            for (int b = 0; b < NB; ++b) code[u][b] = scale[u][b] = 0;
+            if (src) {
+                ldg_words<NB, G::kVec>(src + (u * NB * 32 + lane * G::kVec) * 4, 128 * G::kVec, code[u]);
+                ldg_words<NB, G::kVec>(src + G::kKScaleAt + ((lane >> 3) + 4 * u) * NB * 4, 4 * G::kVec, scale[u]);
+            }
+            const int tok0 = 16 * warp + 8 * u + 2 * (lane >> 3);
+            const uint32_t alive = (tok0 < live ? 0x4000u : 0u) | (tok0 + 1 < live ? 0x40000000u : 0u);
+#pragma unroll
+            for (int b = 0; b < NB; ++b) any |= scale[u][b] & scale[u][b] << 1 & scale[u][b] << 2 & alive;
+        }
+        const bool units = __syncthreads_or(any != 0);
+        unit = units ? 16.0f : 1.0f;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int mine = 16 * warp + 8 * u + (lane >> 2);
+            const uint32_t pick = mine >= live ? 0x4444u : ((lane & 4) ? 0x3232u : 0x1010u);
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                scale[u][b] = __byte_perm(scale[u][b], 0, pick);
+                if (units) scale[u][b] = h2_mul(scale[u][b], 0x2C002C00u);
+            }
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                // odd rows begin with the other block of a chunk, so that 8 lanes' stores meet 8 different banks
+                const int o = (b ^ 1) < NB ? b ^ 1 : b;
+                const bool other = o != b && (mine & 1);
+                const int c = (((b & 1) ^ (other ? 1 : 0)) * 4 + (lane & 3)) ^ (mine & 7);
+                PromptFeed<NB>::put(other ? code[u][o] : code[u][b], other ? scale[u][o] : scale[u][b], kCodeMagic,
+                                    slots + (b >> 1) * T::kKChunk + mine * 128 + c * 16);
+            }
+        }
+    }
+    tm_before_sync();
+    __syncthreads();
+    tm_after_sync();
+    const uint32_t tm = sh_tm, rows = tm + (static_cast<uint32_t>(warp & 3) << 21);  // the warp's 32 rows
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) {
+        const int e = half * (D / 16) + k;  // 8 dimensions
+        const uint32_t from = slots + (e >> 3) * T::kKChunk + row * 128 + (((e & 7) ^ (row & 7)) << 4);
+        const uint4 hi = lds128(from), lo = lds128(from + T::kKPart);
+        tm_store4(rows + 16 * (e >> 1) + 4 * (e & 1), hi.x, hi.y, hi.z, hi.w);
+        tm_store4(rows + 16 * (e >> 1) + 8 + 4 * (e & 1), lo.x, lo.y, lo.z, lo.w);
+    }
+    tm_stored();
+    tm_before_sync();
+    fence_proxy_async_smem();
+    __syncthreads();
+    tm_after_sync();
+    block_op_wait();
+
+    const int64_t block0 = first_block(w, r, seq);
+    const uint64_t policy = l2_evict_last_policy();
+    const auto ask = [&](int block) {
+        const int s = block % kTallSlots;
+        fence_proxy_async_smem();
+        mbar_arrive_expect_tx(&bar[s], T::kImage);
+        bulk_copy_g2s(slot_mem + s * T::kSlot, block_image<NB>(w, block0 + block, kvh), T::kImage, &bar[s], policy);
+    };
+    bool dead = false;  // a wait gave up: no more waits, but every barrier of threads is met; the result is NaN
+    int asked = 0;      // tid 0: blocks that were asked for
+    const auto wait = [&](int which, int parity) {
+        if (!dead && !mbar_wait(&bar[which], parity)) {
+            atomicOr(a.fault, 1u);
+            dead = true;
+        }
+        __syncwarp();
+    };
+    uint64_t total2 = 0;
+    const auto weigh = [&](int block) {
+        const uint8_t *image = slot_mem + block % kTallSlots * T::kSlot;
+        const float4 *exps = reinterpret_cast<const float4 *>(image + T::kExpAt) + half * (kBlockCols / 4);
+        const int2 both = *reinterpret_cast<const int2 *>(image + T::kBothAt);
+        uint32_t s[2][16];
+        const uint32_t at = rows + T::kTmD + (block & 1) * kBlockCols + half * (kBlockCols / 2);
+        tm_load(at, s[0]);
+        tm_load(at + 16, s[1]);
+        tm_loaded(s);
+        const bool masked = first < both.x || first + kTallTokens > both.y;
+        const uint64_t unit2 = f2(unit, unit);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            const float4 e = exps[k];
+            const float2 y = f2_parts(f2_fma(f2_mul(f2(__uint_as_float(s[k / 8][2 * k % 16]), __uint_as_float(s[k / 8][2 * k % 16 + 1])), unit2),
+                                             f2(e.x, e.y), f2(e.z, e.w)));
+            s[k / 8][2 * k % 16] = __float_as_uint(exp2_approx(y.x));
+            s[k / 8][2 * k % 16 + 1] = __float_as_uint(exp2_approx(y.y));
+        }
+        if (masked) {
+            const int2 *see = reinterpret_cast<const int2 *>(image + T::kSeeAt) + half * (kBlockCols / 2);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+                const int2 c = see[k];
+                bool in = tok >= c.x && tok < c.y;
+                const int i = a.by_group.div(block * kBlockCols + half * (kBlockCols / 2) + k);
+                if (tree && in && tok >= base && i < r.n) in = tree_bits(a, r, i, tok) & 1u;
+                if (!in) s[k / 16][k % 16] = 0;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 16; ++k) total2 = f2_add(total2, f2(__uint_as_float(s[k / 8][2 * k % 16]), __uint_as_float(s[k / 8][2 * k % 16 + 1])));
+    };
+    if (tid == 0)
+        for (; asked < min(kTallSlots, blocks); ++asked) ask(asked);
+#pragma unroll 1
+    for (int block = 0; block <= blocks; ++block) {
+        if (block < blocks && warp == 0) {
+            wait(block % kTallSlots, block / kTallSlots & 1);
+            if (one_lane() && !dead) {
+                const uint64_t q = tm_operand(slots + block % kTallSlots * T::kSlot, T::kQChunk);
+                tm_mma_parts<tm_kind(kBlockCols, false), D / 16, T::kQPart>(tm + T::kTmD + (block & 1) * kBlockCols, tm, q,
+                                                                            [](int k) { return (k >> 2) * T::kQChunk + (k & 3) * 32u; });
+                tm_commit(&bar[kTallSlots + (block & 1)]);
+            }
+            __syncwarp();
+        }
+        if (block > 0) {
+            // a barrier for each half of D: the next block's products may be done before a slow warp looks
+            wait(kTallSlots + (block - 1 & 1), block - 1 >> 1 & 1);
+            tm_after_sync();
+            weigh(block - 1);
+            tm_before_sync();
+        }
+        __syncthreads();  // D of the block before is read, and so is its slot
+        tm_after_sync();
+        if (tid == 0 && block > 0 && asked < blocks && !dead) ask(asked++);
+    }
+    // leave only when the copies have landed (after a wait that gave up: as far as they will)
+    if (dead && tid == 0)
+        for (int k = max(0, asked - kTallSlots); k < asked; ++k) (void)mbar_wait(&bar[k % kTallSlots], k / kTallSlots & 1);
+    if (dead) sh_dead = 1;
+    const float2 both = f2_parts(total2);
+    if (half == 1) sh_sum[row] = both.x + both.y;
+    __syncthreads();
+    if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "n"(T::kTm));
+    if (half == 0 && row < live && !sh_skip[row / kKvSlab]) {
+        float sum = both.x + both.y + sh_sum[row];
+        if (sh_dead) sum = __int_as_float(0x7fffffff);
+        *out = had ? fmaf(w.keep, earlier, sum) : sum;
+    }
+}
+
+// More columns than these take the tall kernel (all that the other one takes, and what that does not).
+constexpr int kTallWeightCols = 32;
+static_assert(kTallWeightCols <= kBlockCols, "the other kernel's columns");
+size_t weights_bytes(int head_dim, int n_seq, int n_kv_heads, int group, int n_tok, int max_q_len) {
+    if (static_cast<int64_t>(std::min(max_q_len, n_tok)) * group <= kTallWeightCols) return 0;
+    const int64_t images = weight_blocks(n_seq, n_tok, group) * n_kv_heads;
+    switch (kv_blocks(head_dim)) {
+    case 2: return images * TallGeom<2>::kImage;
+    case 3: return images * TallGeom<3>::kImage;
+    case 4: return images * TallGeom<4>::kImage;
+    case 6: return images * TallGeom<6>::kImage;
+    default: return images * TallGeom<8>::kImage;
+    }
+}
+
+template <int NB> cudaError_t launch_weights(WeightArgs w, int64_t items, int64_t columns, int sms, cudaStream_t st) {
+    const int64_t most = w.a.max_kv_len;
+    if (columns > kTallWeightCols) {
+        cudaError_t e = smem_limit_raised<&attn_weights_tall_kernel<NB>>();
+        if (e != cudaSuccess) return e;
+        const int64_t blocks = (columns + kBlockCols - 1) / kBlockCols;
+        w.by_blocks = FastDiv::of(static_cast<int32_t>(blocks));
+        e = launch_block_op(&weights_q_kernel<NB>, dim3(static_cast<unsigned>(items * blocks)), dim3(kWeightThreads), 0, st, w);
+        if (e != cudaSuccess) return e;
+        const int64_t chunks = (most + kTallTokens - 1) / kTallTokens;
+        w.chunks = static_cast<int32_t>(chunks);
+        w.by_chunks = FastDiv::of(w.chunks);
+        return launch_block_op(&attn_weights_tall_kernel<NB>, dim3(static_cast<unsigned>(items * chunks)), dim3(kWeightThreads),
+                               TallGeom<NB>::kSmem, st, w);
+    }
     const cudaError_t e = smem_limit_raised<&attn_weights_kernel<NB>>();
     if (e != cudaSuccess) return e;
-    const size_t smem = static_cast<size_t>(std::min<int64_t>(kBlockCols, columns + 3) / 4) * 2 * NB * 256 +
-                        (columns > kBlockCols ? static_cast<size_t>(w.chunk) * kKvSlab * 4 : 0);
-    return launch_block_op(&attn_weights_kernel<NB>, dim3(static_cast<unsigned>(items * w.chunks)), dim3(kWeightThreads), smem, st, w);
+    const int64_t steps = items * ((most + kWeightWarps * kKvSlab - 1) / (kWeightWarps * kKvSlab));
+    const size_t smem = kWeightRing<NB> + static_cast<size_t>((columns + 3) / 4) * 2 * NB * 256;
+    return launch_block_op(&attn_weights_kernel<NB>, dim3(static_cast<unsigned>(std::min<int64_t>(steps, 2 * sms))), dim3(kWeightThreads),
+                           smem, st, w);
 }
 
 }  // namespace
@@ -251,6 +688,13 @@ template <int NB> cudaError_t launch_weights(const WeightArgs &w, int64_t items,
 using namespace zdmmv;
 
 extern "C" {
+
+size_t zdmmv_attn_weights_q4_0_workspace_bytes(const zdmmv_kv_cache *cache, int n_q_heads, int n_tok, int max_q_len) {
+    KvView c{};
+    if (kv_check(cache, &c) != ZDMMV_OK || n_q_heads < 1 || n_q_heads > 65535 || n_q_heads % c.n_kv_heads || n_tok < 0 || max_q_len < 1)
+        return 0;
+    return weights_bytes(cache->head_dim, c.n_seq, c.n_kv_heads, n_q_heads / c.n_kv_heads, n_tok, max_q_len);
+}
 
 zdmmv_status zdmmv_attn_weights_q4_0(const zdmmv_kv_cache *cache, const zdmmv_attn_weights_args *args, zdmmv_stream_t stream) {
     if (!args) return ZDMMV_ERR_NULL;
@@ -267,16 +711,23 @@ zdmmv_status zdmmv_attn_weights_q4_0(const zdmmv_kv_cache *cache, const zdmmv_at
     const int group = g.n_q_heads / cache->n_kv_heads;
     const int64_t columns = static_cast<int64_t>(std::min(g.max_q_len, std::max(1, g.n_tok))) * group;
     const int64_t items = static_cast<int64_t>(a.c.n_seq) * a.c.n_kv_heads;
-    const int64_t tiles = (static_cast<int64_t>(std::min(g.max_kv_len, kMostAttnTokens)) + kKvSlab - 1) / kKvSlab;
-    if (columns > kAllCols || items > 0x7fffff00) return ZDMMV_ERR_SHAPE;
+    // 128 tokens of a kv head are a step of the one kernel and a CTA of the other
+    const int64_t steps = items * ((static_cast<int64_t>(g.max_kv_len) + kTallTokens - 1) / kTallTokens);
+    if (columns > kAllCols || steps > 0x7fffff00 || items * ((columns + kBlockCols - 1) / kBlockCols) > 0x7fffff00) return ZDMMV_ERR_SHAPE;
     if (g.max_kv_len == 0) return ZDMMV_OK;
     if (!g.q_start || !g.kv_len || !g.out || (g.n_tok > 0 && (!g.q || !g.lse))) return ZDMMV_ERR_NULL;
     if ((g.n_tok > 0 && g.q_stride < static_cast<int64_t>(g.n_q_heads) * cache->head_dim) || g.out_stride < g.max_kv_len ||
         (g.before && g.before_stride < g.max_kv_len) || (g.before == g.out && g.before_stride != g.out_stride))
         return ZDMMV_ERR_SHAPE;
     if (kv_misaligned(g.q, 16) || g.q_stride % 4 || kv_misaligned(g.q_start, 4) || kv_misaligned(g.kv_len, 4) || kv_misaligned(g.lse, 4) ||
-        kv_misaligned(g.seen, 4) || kv_misaligned(g.before, 4) || kv_misaligned(g.out, 4) || kv_misaligned(g.status_dev, 4))
+        kv_misaligned(g.seen, 4) || kv_misaligned(g.before, 4) || kv_misaligned(g.out, 4) || kv_misaligned(g.status_dev, 4) || kv_misaligned(g.workspace, 16))
         return ZDMMV_ERR_ALIGN;
+    const size_t need = weights_bytes(cache->head_dim, a.c.n_seq, a.c.n_kv_heads, group, g.n_tok, g.max_q_len);
+    if (need && !g.workspace) return ZDMMV_ERR_NULL;
+    if (g.workspace_bytes < need) return ZDMMV_ERR_SIZE;
+    w.images = static_cast<uint8_t *>(g.workspace);
+    a.fault = current_fault_word();
+    if (!a.fault) return ZDMMV_ERR_CUDA;
     a.q = g.q; a.q_start = g.q_start; a.kv_len = g.kv_len; a.status = g.status_dev;
     a.q_stride = g.q_stride;
     a.n_tok = g.n_tok; a.n_q_heads = g.n_q_heads; a.group = group;
@@ -292,24 +743,14 @@ zdmmv_status zdmmv_attn_weights_q4_0(const zdmmv_kv_cache *cache, const zdmmv_at
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return ZDMMV_ERR_CUDA;
-    // as many CTAs as run at once, or four times that for several sequences, whose lengths may differ
-    const int64_t want = static_cast<int64_t>(sms) * 2 * (a.c.n_seq > 1 ? 4 : 1);
-    int64_t chunk = std::max<int64_t>(kWeightWarps, (items * tiles + want - 1) / want);
-    chunk = (chunk + kWeightWarps - 1) / kWeightWarps * kWeightWarps;
-    if (columns > kBlockCols) chunk = std::min<int64_t>(chunk, kMostChunk);
-    const int64_t chunks = (tiles + chunk - 1) / chunk;
-    if (items * chunks > 0x7fffff00) return ZDMMV_ERR_SHAPE;
-    w.chunk = static_cast<int32_t>(chunk);
-    w.chunks = static_cast<int32_t>(chunks);
-    w.by_chunks = FastDiv::of(w.chunks);
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e = cudaErrorInvalidValue;
     switch (kv_blocks(cache->head_dim)) {
-    case 2: e = launch_weights<2>(w, items, columns, s); break;
-    case 3: e = launch_weights<3>(w, items, columns, s); break;
-    case 4: e = launch_weights<4>(w, items, columns, s); break;
-    case 6: e = launch_weights<6>(w, items, columns, s); break;
-    case 8: e = launch_weights<8>(w, items, columns, s); break;
+    case 2: e = launch_weights<2>(w, items, columns, sms, s); break;
+    case 3: e = launch_weights<3>(w, items, columns, sms, s); break;
+    case 4: e = launch_weights<4>(w, items, columns, sms, s); break;
+    case 6: e = launch_weights<6>(w, items, columns, sms, s); break;
+    case 8: e = launch_weights<8>(w, items, columns, sms, s); break;
     }
     return e == cudaSuccess ? ZDMMV_OK : ZDMMV_ERR_CUDA;
 }

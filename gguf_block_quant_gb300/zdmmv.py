@@ -58,7 +58,7 @@ _KV_CACHE = struct.Struct("@2Pq5i4x")
 _KV_APPEND_ARGS = struct.Struct("@10P4q4i")
 _ATTN_ARGS = struct.Struct("@6PNq5if")
 _ATTN_TREE = struct.Struct("@2Pi4x")
-_ATTN_WEIGHTS_ARGS = struct.Struct("@8P3q6i2f")
+_ATTN_WEIGHTS_ARGS = struct.Struct("@9PN3q6i2f")
 _KV_EVICT_ARGS = struct.Struct("@6P2q4i")
 _KV_ACCEPT_ARGS = struct.Struct("@6P2qi4x")
 _SIGS = {
@@ -103,6 +103,7 @@ _SIGS = {
     "zdmmv_attn_q4_0": ([_vp, _vp, _vp], _int),
     "zdmmv_kv_append_at_q4_0": ([_vp, _vp, _vp, _vp], _int),
     "zdmmv_attn_tree_q4_0": ([_vp, _vp, _vp, _vp], _int),
+    "zdmmv_attn_weights_q4_0_workspace_bytes": ([_vp, _int, _int, _int], ctypes.c_size_t),
     "zdmmv_attn_weights_q4_0": ([_vp, _vp, _vp], _int),
     "zdmmv_kv_evict_q4_0": ([_vp, _vp, _vp, _vp], _int),
     "zdmmv_kv_accept_q4_0": ([_vp, _vp, _vp], _int),
@@ -619,12 +620,18 @@ def _per_head(t: torch.Tensor, cache: KVCache, n: int, what: str) -> tuple[int, 
     return t.data_ptr(), s1
 
 
+def attn_weights_q4_0_workspace_bytes(cache: KVCache, n_q_heads: int, n_tok: int, max_q_len: int) -> int:
+    return int(lib().zdmmv_attn_weights_q4_0_workspace_bytes(cache.c, n_q_heads, n_tok, max_q_len))
+
+
 def attn_weights_q4_0(cache: KVCache, q, q_start, kv_len, lse, max_q_len: int, max_kv_len: int, seen=None,
-                      scale: float | None = None, window: int = 0, sums=None, out=None, keep: float = 1.0, status=None, stream=None):
+                      scale: float | None = None, window: int = 0, sums=None, out=None, keep: float = 1.0, workspace=None, status=None,
+                      stream=None):
     """What the rows of an attention call gave each cached token: keep * sums + the sum of exp(score - lse) over the rows
     of a kv head that see it (without sums for the new tokens), fp32 [n_seq][n_kv_heads][max_kv_len or more]. lse: as
     attn_tree_q4_0 wrote it for the same q, seen, scale and window. out: where it goes (may be sums; None: a new tensor
-    of zeros behind the sequences' ends). Returns out."""
+    of zeros behind the sequences' ends). workspace: uint8, of attn_weights_q4_0_workspace_bytes (None: a new one where
+    one is needed). Returns out."""
     dim, n_seq = cache.head_dim, cache.n_seq
     pq, n_tok, width, sq = _rows(q, "q")
     heads = width // dim
@@ -635,9 +642,14 @@ def attn_weights_q4_0(cache: KVCache, q, q_start, kv_len, lse, max_q_len: int, m
     po, so = _per_head(out, cache, max_kv_len, "out")
     pb, sb = (0, 0) if sums is None else _per_head(sums, cache, max_kv_len, "sums")
     ps, words = _seen(seen, n_tok)
+    pw = nw = 0
+    if workspace is None and heads * min(n_tok, max_q_len) > 32 * cache.n_kv_heads:  # with fewer columns none is needed
+        workspace = _make(attn_weights_q4_0_workspace_bytes(cache, heads, n_tok, max_q_len), _U8, q.device, stream)
+    if workspace is not None:
+        pw, nw = _whole(workspace, _U8, 0, "workspace"), workspace.numel()
     args = _ATTN_WEIGHTS_ARGS.pack(pq, _whole(q_start, _I32, n_seq + 1, "q_start"), _whole(kv_len, _I32, n_seq, "kv_len"),
-                                   _whole(lse, _F32, n_tok * heads, "lse"), ps, pb, po,
-                                   0 if status is None else _whole(status, _I32, 1, "status"), sq, sb, so, n_tok, heads, max_q_len,
+                                   _whole(lse, _F32, n_tok * heads, "lse"), ps, pb, po, pw,
+                                   0 if status is None else _whole(status, _I32, 1, "status"), nw, sq, sb, so, n_tok, heads, max_q_len,
                                    max_kv_len, window, words, dim ** -0.5 if scale is None else scale, keep)
     _enter("zdmmv_attn_weights_q4_0", cache.c, args, _raw_stream(stream))
     return out

@@ -746,8 +746,11 @@ typedef struct {
     const float *before;     /* nullable (zeros); device fp32 [n_seq][n_kv_heads], before_stride apart */
     float *out;              /* device fp32 [n_seq][n_kv_heads], out_stride apart; may be `before` itself
                                 with the same stride, but overlaps no input otherwise */
+    void *workspace;         /* device, 16-byte aligned, >= zdmmv_attn_weights_q4_0_workspace_bytes, of any
+                                contents; NULL where that size is 0. One workspace per call in flight */
     int32_t *status_dev;     /* nullable device int32: 1 is stored for a bad sequence (as zdmmv_attn_q4_0's),
                                 whose entries are left as they are, or a bad page, whose tokens' are */
+    size_t workspace_bytes;
     int64_t q_stride;        /* floats, a multiple of 4, >= n_q_heads*head_dim */
     int64_t before_stride;   /* floats between kv heads, >= max_kv_len (ignored where before is NULL) */
     int64_t out_stride;      /* the same for out */
@@ -761,7 +764,12 @@ typedef struct {
     float keep;              /* finite; 1 adds up, less forgets */
 } zdmmv_attn_weights_args;
 
-/* Errors: ERR_NULL, ERR_SHAPE, ERR_ALIGN, ERR_CUDA. */
+/* What a workspace has to hold for a call with n_tok rows, max_q_len of them a
+ * sequence: q as the tensor cores take it, from 33 columns (rows times the heads of a
+ * kv head) on; 0 with fewer. Rises with both. */
+size_t zdmmv_attn_weights_q4_0_workspace_bytes(const zdmmv_kv_cache *cache, int n_q_heads, int n_tok, int max_q_len);
+/* After a wait that gave up (ZDMMV_FAULT_WAIT_TIMEOUT) the entries concerned are
+ * NaN. Errors: ERR_NULL, ERR_SHAPE, ERR_ALIGN, ERR_SIZE, ERR_CUDA. */
 zdmmv_status zdmmv_attn_weights_q4_0(const zdmmv_kv_cache *cache, const zdmmv_attn_weights_args *args,
                                      zdmmv_stream_t stream);
 

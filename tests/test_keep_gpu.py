@@ -568,3 +568,42 @@ def test_they_run_as_a_graph():
         assert torch.equal(alone.pages, cache.pages) and torch.equal(to2.pages, to.pages)
         for name in want:
             assert torch.equal(got[name], want[name]), name
+
+
+@pytest.mark.parametrize("dim", [64, 96, 128, 192, 256])
+@pytest.mark.parametrize("heads, group, new", [(2, 4, 9), (1, 1, 65), (2, 8, 16), (1, 5, 129)])
+def test_weights_many_columns(dim, heads, group, new):
+    """36 to 645 columns: blocks of 64 that are full, nearly empty or one more than full; lengths around 128 tokens."""
+    run_weights(np.random.default_rng(dim + new), [new, 127 + new, 128, 129, 700], [new, new, min(new, 128), 1, new - 1], 48, heads, group,
+                dim, masks="tree" if new != 65 else None, window=0 if new < 100 else 150)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_weights_of_large_scales(dim):
+    """Scales of 2^13 and more among 128 tokens (their operand in units of 16), small queries: the bound counts the keys' size."""
+    rng = np.random.default_rng(dim)
+    page, n, new, group = 32, 200, 12, 4
+    cache, pages, table = random_cache(rng, [n], page, 1, dim)
+    for at in (5, 130, 199):
+        R.put(pages, page, 1, dim, table[0, at // page], at % page, 0, 0, rng.integers(0, 16, dim),
+              np.linspace(8000, 60000, dim // 32).astype(np.float16))
+    cache = Z.KVCache(dev(pages), page, 1, dim, dev(table))
+    q = (2e-5 * rng.standard_normal((new, group, dim))).astype(np.float32)
+    starts, ld, lse = dev(np.array([0, new], np.int32)), dev(np.array([n], np.int32)), torch.empty(new, group, device="cuda")
+    Z.attn_tree_q4_0(cache, dev(q), starts, ld, new, n, lse=lse)
+    out = Z.attn_weights_q4_0(cache, dev(q), starts, ld, lse, new, n).double().cpu().numpy()
+    k, _ = R.values(pages, page, 1, dim)
+    want, tol = T.weights(q, [0, new], [n], table, k, page, dim ** -0.5, lse.double().cpu().numpy())
+    # the other tokens' scales count to 2^-21 of themselves where they share an operand: 2^-21 P, within 2^-18 P
+    assert np.all(np.abs(out - want) <= 2.0 ** -18 * tol + 1e-30)
+
+
+def test_weights_of_a_prompts_chunk():
+    """Two CTAs on some SMs, each with more blocks of columns than it has places for; the same bits again."""
+    rng = np.random.default_rng(77)
+    cache, q, starts, ld, lse, had, out = run_weights(rng, [3000], [256], 64, 8, 2, 128)
+    for _ in range(3):
+        again = torch.full_like(out, -7.0)
+        Z.attn_weights_q4_0(cache, dev(q), starts, ld, lse, 256, 3000, sums=had, out=again)
+        assert torch.equal(again, out)
+    assert Z.device_status() == 0

@@ -14,8 +14,8 @@ class _AttnTree(ctypes.Structure):
 
 
 class _AttnWeightsArgs(ctypes.Structure):
-    _fields_ = [(n, ctypes.c_void_p) for n in ("q", "q_start", "kv_len", "lse", "seen", "before", "out", "status_dev")] + [
-        (n, ctypes.c_int64) for n in ("q_stride", "before_stride", "out_stride")] + [
+    _fields_ = [(n, ctypes.c_void_p) for n in ("q", "q_start", "kv_len", "lse", "seen", "before", "out", "workspace", "status_dev")] + [
+        ("workspace_bytes", ctypes.c_size_t)] + [(n, ctypes.c_int64) for n in ("q_stride", "before_stride", "out_stride")] + [
         (n, ctypes.c_int32) for n in ("n_tok", "n_q_heads", "max_q_len", "max_kv_len", "window", "seen_words")] + [
         (n, ctypes.c_float) for n in ("scale", "keep")]
 
@@ -77,7 +77,7 @@ def test_binding_refuses_bad_bits():
 
 
 def _weights(**k):
-    d = dict(q=FAKE, q_start=FAKE, kv_len=FAKE, lse=FAKE, seen=FAKE, before=FAKE, out=2 * FAKE, status_dev=FAKE, q_stride=1024,
+    d = dict(q=FAKE, q_start=FAKE, kv_len=FAKE, lse=FAKE, seen=FAKE, before=FAKE, out=2 * FAKE, workspace=None, status_dev=FAKE, workspace_bytes=0, q_stride=1024,
              before_stride=100, out_stride=100, n_tok=3, n_q_heads=8, max_q_len=2, max_kv_len=100, window=0, seen_words=1, scale=0.1,
              keep=1.0)
     return _AttnWeightsArgs(**{**d, **k})
@@ -91,7 +91,8 @@ def _weights(**k):
     (1, dict(q=None)), (1, dict(q_start=None)), (1, dict(kv_len=None)), (1, dict(lse=None)), (1, dict(out=None)),
     (3, dict(q=FAKE + 4)), (3, dict(q_stride=1026)), (3, dict(q_start=FAKE + 1)), (3, dict(kv_len=FAKE + 2)), (3, dict(lse=FAKE + 2)),
     (3, dict(seen=FAKE + 2)), (3, dict(before=FAKE + 1)), (3, dict(out=FAKE + 2)), (3, dict(status_dev=FAKE + 2)),
-    (0, dict(max_kv_len=0, q=None, out=None))])
+    (1, dict(n_tok=40, max_q_len=32)), (6, dict(n_tok=40, max_q_len=32, workspace=FAKE, workspace_bytes=4096)),
+    (3, dict(workspace=FAKE + 8)), (0, dict(max_kv_len=0, q=None, out=None))])
 def test_weights_checks(L, code, change):  # noqa: F811
     assert L.zdmmv_attn_weights_q4_0(ctypes.byref(_cache()), ctypes.byref(_weights(**change)), None) == code
 
@@ -144,3 +145,27 @@ def test_null_structs(L):  # noqa: F811
     assert L.zdmmv_kv_accept_q4_0(c, None, None) == 1 and L.zdmmv_kv_accept_q4_0(None, ctypes.byref(_accept()), None) == 1
     assert L.zdmmv_kv_evict_q4_0(c, c, None, None) == 1 and L.zdmmv_kv_evict_q4_0(c, None, ctypes.byref(_evict()), None) == 1
     assert L.zdmmv_kv_append_at_q4_0(c, None, FAKE, None) == 1
+
+
+def test_weights_workspace(L):  # noqa: F811
+    size = lambda heads, tok, new, **k: L.zdmmv_attn_weights_q4_0_workspace_bytes(ctypes.byref(_cache(**k)), heads, tok, new)  # noqa: E731
+    assert size(8, 8, 8) == 0 and size(8, 100, 8) == 0 and size(8, 8, 100) == 0      # 32 columns
+    assert size(8, 9, 9) > 0 and size(16, 5, 5) > 0
+    assert size(7, 9, 9) == 0 and size(8, -1, 9) == 0 and size(8, 9, 0) == 0         # refused shapes
+    last = 0
+    for tok in (9, 10, 16, 17, 100, 101, 1000):
+        assert size(8, tok, 9) >= last
+        last = size(8, tok, 9)
+    # blocks of 64 columns of q in two fp16 parts and 16 bytes a column: those of the rows, and one a sequence
+    assert size(8, 1000, 9) == (1000 * 4 // 64 + 2) * 2 * (64 * (128 * 4 + 16) + 16)
+
+
+def test_weights_waits_that_gave_up():
+    """Every wait of the tall kernel that reports a fault marks its thread, and a marked thread makes the result NaN."""
+    from tests.test_gave_up_waits_cpu import block, source, waits_that_report
+    text = source("zdmmv_attn_weights.cu")
+    assert text.count("atomicOr(a.fault") == 1
+    assert ["dead = true" in b for b in waits_that_report(text)] == [True]
+    kernel = block(text, text.index("attn_weights_tall_kernel(WeightArgs w)"))
+    after = kernel[kernel.index("if (dead) sh_dead = 1;"):]
+    assert "wait(" not in after and after.index("__syncthreads()") < after.index("if (sh_dead) sum = ")
