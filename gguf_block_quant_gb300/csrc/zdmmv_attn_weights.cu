@@ -342,7 +342,7 @@ template <int NB> struct TallGeom {
     static constexpr uint32_t kKChunk = kTallTokens * 128, kQChunk = kBlockCols * 128;
     static constexpr uint32_t kKPart = kChunks * kKChunk, kQPart = kChunks * kQChunk;
     // a block of q in the workspace: the operand's parts, the columns' (x, y) by two, what they see, and of it the latest first
-    // token and the earliest end
+    // token, the earliest end, the earliest first token and the latest end
     static constexpr uint32_t kExpAt = 2 * kQPart, kSeeAt = kExpAt + kBlockCols * 8, kBothAt = kSeeAt + kBlockCols * 8;
     static constexpr uint32_t kImage = kBothAt + 16, kSlot = (kImage + 1023) / 1024 * 1024;
     static constexpr size_t kSmem = kTallSlots * kSlot + 1024;  // aligned to 1024; before the blocks of q, K
@@ -365,7 +365,7 @@ template <int NB> __global__ void __launch_bounds__(kWeightThreads) weights_q_ke
     using T = TallGeom<NB>;
     constexpr int D = T::kDim, kPasses = (D + 127) / 128, kPerWarp = kBlockCols / kWeightWarps;
     const AttnArgs &a = w.a;
-    __shared__ int sh_low, sh_end;
+    __shared__ int4 sh_both;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     block_op_wait();
     block_op_release();
@@ -386,8 +386,7 @@ template <int NB> __global__ void __launch_bounds__(kWeightThreads) weights_q_ke
     }
     const float lse = lane < kPerWarp && col0 + lane < columns ? __ldg(column_lse(w, r, kvh, col0 + lane)) : 0.0f;
     if (tid == 0) {
-        sh_low = 0;
-        sh_end = a.seen ? r.len - r.n : r.len;
+        sh_both = make_int4(0, a.seen ? r.len - r.n : r.len, r.len, 0);
     }
     __syncthreads();
     uint8_t *image = block_image<NB>(w, first_block(w, r, seq) + block, kvh);
@@ -411,8 +410,10 @@ template <int NB> __global__ void __launch_bounds__(kWeightThreads) weights_q_ke
         e[2] = c.y;
         reinterpret_cast<int2 *>(image + T::kSeeAt)[at] = make_int2(c.low, c.end);
         if (col0 + lane < columns) {
-            atomicMax(&sh_low, c.low);
-            atomicMin(&sh_end, c.end);
+            atomicMax(&sh_both.x, c.low);
+            atomicMin(&sh_both.y, c.end);
+            atomicMin(&sh_both.z, c.low);
+            atomicMax(&sh_both.w, c.end);
         }
     }
 #pragma unroll
@@ -435,7 +436,7 @@ template <int NB> __global__ void __launch_bounds__(kWeightThreads) weights_q_ke
         }
     }
     __syncthreads();
-    if (tid == 0) *reinterpret_cast<int2 *>(image + T::kBothAt) = make_int2(sh_low, sh_end);
+    if (tid == 0) *reinterpret_cast<int4 *>(image + T::kBothAt) = sh_both;
 }
 
 template <int NB> __global__ void __launch_bounds__(kWeightThreads, TallGeom<NB>::kCtas) attn_weights_tall_kernel(WeightArgs w) {
@@ -452,7 +453,8 @@ template <int NB> __global__ void __launch_bounds__(kWeightThreads, TallGeom<NB>
     block_op_release();
     // until its wait below the kernel reads only what was there before weights_q_kernel, which began after all that was
     // complete, and writes nothing but the status
-    const int item = w.by_chunks.div(blockIdx.x), chunk = w.by_chunks.mod(blockIdx.x, item);
+    // the last tokens of a sequence, whose columns are masked, first
+    const int item = w.by_chunks.div(blockIdx.x), chunk = w.chunks - 1 - w.by_chunks.mod(blockIdx.x, item);
     const int seq = a.by_heads.div(item), kvh = a.by_heads.mod(item, seq);
     const AttnRange r = attn_range<true>(a, seq, 0, kAllCols);
     const int first = chunk * kTallTokens, live = r.bad ? 0 : r.len - first;  // tokens from `live` on are none
@@ -574,7 +576,8 @@ template <int NB> __global__ void __launch_bounds__(kWeightThreads, TallGeom<NB>
     const auto weigh = [&](int block) {
         const uint8_t *image = slot_mem + block % kTallSlots * T::kSlot;
         const float4 *exps = reinterpret_cast<const float4 *>(image + T::kExpAt) + half * (kBlockCols / 4);
-        const int2 both = *reinterpret_cast<const int2 *>(image + T::kBothAt);
+        const int4 both = *reinterpret_cast<const int4 *>(image + T::kBothAt);
+        if (first >= both.w || first + kTallTokens <= both.z) return;  // no column sees a token of the CTA's
         uint32_t s[2][16];
         const uint32_t at = rows + T::kTmD + (block & 1) * kBlockCols + half * (kBlockCols / 2);
         tm_load(at, s[0]);
@@ -592,13 +595,24 @@ template <int NB> __global__ void __launch_bounds__(kWeightThreads, TallGeom<NB>
         }
         if (masked) {
             const int2 *see = reinterpret_cast<const int2 *>(image + T::kSeeAt) + half * (kBlockCols / 2);
+            if (tree) {
+                const int col0 = block * kBlockCols + half * (kBlockCols / 2);
+                int was = -1;
+                bool bit = true;
 #pragma unroll
-            for (int k = 0; k < 32; ++k) {
-                const int2 c = see[k];
-                bool in = tok >= c.x && tok < c.y;
-                const int i = a.by_group.div(block * kBlockCols + half * (kBlockCols / 2) + k);
-                if (tree && in && tok >= base && i < r.n) in = tree_bits(a, r, i, tok) & 1u;
-                if (!in) s[k / 16][k % 16] = 0;
+                for (int k = 0; k < 32; ++k) {
+                    const int i = a.by_group.div(col0 + k);
+                    if (i != was) bit = tok < base || (i < r.n && tok < r.len && (tree_bits(a, r, i, tok) & 1u));
+                    was = i;
+                    const int2 c = see[k];
+                    if (tok < c.x || tok >= c.y || !bit) s[k / 16][k % 16] = 0;
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < 32; ++k) {
+                    const int2 c = see[k];
+                    if (tok < c.x || tok >= c.y) s[k / 16][k % 16] = 0;
+                }
             }
         }
 #pragma unroll
