@@ -17,7 +17,7 @@ namespace zdmmv {
 namespace {
 
 constexpr int kWeightWarps = 8, kWeightThreads = kWeightWarps * 32;
-constexpr int kBlockCols = 64;       // columns whose parts of q lie in shared memory at once
+constexpr int kBlockCols = 64;       // columns of a block of q
 constexpr int kAllCols = 0x7fffff00; // a column tile of all columns
 
 struct WeightArgs {
@@ -91,17 +91,19 @@ __device__ __forceinline__ void cp_async_4(uint32_t to, const void *from) {
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// ------------------------------------------------------------------ up to kBlockCols columns
+// ------------------------------------------------------------------ few columns
 // The scores are formed as in the narrow kernel of zdmmv_attn.cuh (A = a tile's 16 tokens of codes, B = four columns' upper and
 // lower parts; a product's C holds a column's two sums side by side), so that they agree with those that lse was made of. The
-// steps (8 tiles, one a warp) of all kv heads of all sequences one after another are a row, of which every CTA of a grid that
-// fills the device takes an equal stretch, whatever the lengths. A warp keeps the next tiles' keys, and their tokens' earlier
-// sums, on their way into its own ring in shared memory.
-constexpr int kWeightStages = 4;
-template <int NB> constexpr int kStageBytes = 9 * NB * kQK + kKvSlab * 4;
-template <int NB> constexpr size_t kWeightRing = static_cast<size_t>(kWeightWarps) * kWeightStages * kStageBytes<NB>;
+// steps (16 tiles, a pair for each warp) of all kv heads of all sequences one after another are a row, of which every CTA of a
+// grid that fills the device takes an equal stretch, whatever the lengths. A warp keeps the next pairs' keys, and their tokens'
+// earlier sums, on their way into its own ring in shared memory; a pair's 32 sums end up one in each lane.
+// ONE: up to four columns, whose parts of q stay in registers.
+constexpr int kWeightStages = 3;
+template <int NB> constexpr int kPairBytes = 2 * 9 * NB * kQK + 2 * kKvSlab * 4;
+template <int NB> constexpr size_t kWeightRing = static_cast<size_t>(kWeightWarps) * kWeightStages * kPairBytes<NB>;
+__host__ __device__ constexpr int weight_ctas(int nb, bool one) { return one && nb <= 4 ? 3 : 2; }
 
-template <int NB> __global__ void __launch_bounds__(kWeightThreads, 2) attn_weights_kernel(WeightArgs w) {
+template <int NB, bool ONE> __global__ void __launch_bounds__(kWeightThreads, weight_ctas(NB, ONE)) attn_weights_kernel(WeightArgs w) {
     using G = KvGeom<NB>;
     const AttnArgs &a = w.a;
     constexpr int kKeyBytes = 9 * G::kDim;
@@ -111,7 +113,7 @@ template <int NB> __global__ void __launch_bounds__(kWeightThreads, 2) attn_weig
     __shared__ uint32_t sh_magic;
     uint2 *q_sm = reinterpret_cast<uint2 *>(smem + kWeightRing<NB>);  // [group of 4][2 NB][lane]
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-    const uint32_t ring = smem_addr(smem) + warp * (kWeightStages * kStageBytes<NB>);
+    const uint32_t ring = smem_addr(smem) + warp * (kWeightStages * kPairBytes<NB>);
     if (tid == 0) sh_magic = kCodeMagic;
     block_op_wait();
     block_op_release();
@@ -121,7 +123,7 @@ template <int NB> __global__ void __launch_bounds__(kWeightThreads, 2) attn_weig
         int low, end;
         tiles_of(w, r, low, end);
         if (r.bad && blockIdx.x == 0 && a.status) *a.status = 1;
-        return (end - low + kWeightWarps - 1) / kWeightWarps;
+        return (end - low + kStepTiles - 1) / kStepTiles;
     };
     // this CTA's stretch of the row, and the sequence that it begins in
     int64_t at, last;
@@ -161,7 +163,7 @@ template <int NB> __global__ void __launch_bounds__(kWeightThreads, 2) attn_weig
         const AttnRange r = attn_range<true>(a, seq, 0, kAllCols);
         int low, end;
         tiles_of(w, r, low, end);
-        const int steps = (end - low + kWeightWarps - 1) / kWeightWarps;
+        const int steps = (end - low + kStepTiles - 1) / kStepTiles;
         if (inside >= steps * heads) {  // the next sequence, as long as the stretch has steps of one
             ++seq;
             inside = 0;
@@ -169,8 +171,9 @@ template <int NB> __global__ void __launch_bounds__(kWeightThreads, 2) attn_weig
         }
         const int kvh = inside / steps, step = inside - kvh * steps;
         const int n_steps = static_cast<int>(min(static_cast<int64_t>(steps - step), last - at));
-        const int first = low + step * kWeightWarps, stop = min(end, first + n_steps * kWeightWarps);
+        const int first = low + step * kStepTiles, stop = min(end, first + n_steps * kStepTiles);
         const int base = r.len - r.n, columns = r.n * a.group, groups = (columns + 3) / 4;
+        const int seen0 = r.slab0, seen1 = columns > 0 ? r.slab0 + r.slabs : 0;  // tiles that a column sees
         const bool tree = a.seen != nullptr;
         const int64_t item = static_cast<int64_t>(seq) * heads + kvh;
         const float *before = w.before ? w.before + item * w.before_stride : nullptr;
@@ -178,37 +181,36 @@ template <int NB> __global__ void __launch_bounds__(kWeightThreads, 2) attn_weig
         const int32_t *table = a.c.table + static_cast<int64_t>(seq) * a.c.max_pages;
         const uint8_t *head = a.c.pages + static_cast<int64_t>(kvh) * static_cast<int>(a.by_page_tiles.d) * G::kTileBytes;
 
-        // the warp's tiles are first + warp + 8 k; a lane looks up every 32nd one's page
+        // the warp's pairs are tiles first + 2 (warp + 8 k); lanes 2 j and 2 j + 1 look up every 16th one's pages
         const uint8_t *src = nullptr;
-        bool wrong = false;
-        uint32_t have = 0, skip = 0;  // by k % 32: the tile's keys are (asked for); its page is bad
+        uint32_t bad_now = 0, bad_next = 0;  // bad pages of 16 pairs, those in use and those asked for
         const auto ask = [&](int k) {
-            const int tile = first + warp + kWeightWarps * k;
+            const int tile = first + 2 * (warp + kWeightWarps * k);
             if (tile < stop) {
-                if ((k & 31) == 0) {
-                    const int mine = tile + kWeightWarps * lane;
+                if ((k & 15) == 0) {
+                    const int mine = tile + 2 * kWeightWarps * (lane >> 1) + (lane & 1);
                     src = nullptr;
-                    wrong = false;
-                    if (mine < stop && mine >= r.slab0 && mine < r.slab0 + r.slabs && columns > 0) {
+                    bool wrong = false;
+                    if (mine < stop && mine >= seen0 && mine < seen1) {
                         const int slot = a.by_page_tiles.div(mine), page = table[slot];
                         wrong = page < 0 || page >= a.c.n_pages;
                         if (wrong && a.status) *a.status = 1;
                         if (!wrong)
                             src = head + page * a.c.page_bytes + static_cast<int64_t>(a.by_page_tiles.mod(mine, slot)) * G::kTileBytes;
                     }
+                    bad_next = __ballot_sync(0xffffffffu, wrong);
                 }
-                const uint8_t *from =
-                    reinterpret_cast<const uint8_t *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), k & 31));
-                const uint32_t bit = 1u << (k & 31);
-                have = from ? have | bit : have & ~bit;
-                skip = __shfl_sync(0xffffffffu, wrong ? 1 : 0, k & 31) ? skip | bit : skip & ~bit;
-                const uint32_t to = ring + (k % kWeightStages) * kStageBytes<NB>;
+                const int s = lane >> 4, l = lane & 15;  // half a warp for a tile
+                const uint8_t *from = reinterpret_cast<const uint8_t *>(
+                    __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), 2 * (k & 15) + s));
+                const uint32_t stage = ring + (k % kWeightStages) * kPairBytes<NB>, to = stage + s * kKeyBytes + 16 * l;
                 if (from) {
 #pragma unroll
-                    for (int c = lane; c < 18 * NB; c += 32) cp_async_16(to + 16 * c, from + 16 * c + (c < 16 * NB ? 0 : G::kCodeBytes));
+                    for (int c = 0; c < NB; ++c) cp_async_16(to + 256 * c, from + 16 * l + 256 * c);
+                    if (l < 2 * NB) cp_async_16(to + G::kCodeBytes, from + 16 * l + G::kKScaleAt);
                 }
                 const int tok = tile * kKvSlab + lane;
-                if (before && lane < kKvSlab && tok < base) cp_async_4(to + kKeyBytes + 4 * lane, before + tok);
+                if (before && tok < base) cp_async_4(stage + 2 * kKeyBytes + 4 * lane, before + tok);
             }
             cp_async_commit();
         };
@@ -254,68 +256,92 @@ template <int NB> __global__ void __launch_bounds__(kWeightThreads, 2) attn_weig
         }
         __syncthreads();
         const int low_max = sh_low, end_min = sh_end;
+        uint2 qf[ONE ? 2 * NB : 1];
+        Column mine{0.0f, -INFINITY, 0, 0};
+        if constexpr (ONE) {
+            if (groups > 0) mine = sh_col[t];
+#pragma unroll
+            for (int k = 0; k < 2 * NB; ++k) qf[k] = groups > 0 ? q_sm[k * 32 + lane] : make_uint2(0, 0);
+        }
 
-        for (int k = 0, tile = first + warp; tile < stop; ++k, tile += kWeightWarps) {
+        for (int k = 0, tile = first + 2 * warp; tile < stop; ++k, tile += kStepTiles) {
             cp_async_wait<kWeightStages - 2>();
-            __syncwarp();  // all lanes' copies of tile k are there, and all are done with the slot before
+            __syncwarp();  // all lanes' copies of pair k are there, and all are done with the place before
             ask(k + kWeightStages - 1);
-            const uint32_t stage = ring + (k % kWeightStages) * kStageBytes<NB>;
+            if ((k & 15) == 0) bad_now = bad_next;
+            const uint32_t stage = ring + (k % kWeightStages) * kPairBytes<NB>;
             const int t0 = tile * kKvSlab;
-            float s0 = 0.0f, s1 = 0.0f;  // tokens t0 + g and t0 + g + 8
-            if (have >> (k & 31) & 1u) {
-                uint32_t f[NB][8];
-                float dd[NB][2];
-                uint32_t kw[2][NB], dk[2][NB];
+            float p[2][2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};  // by tile: tokens g and g + 8
+            if (tile + 1 >= seen0 && tile < seen1) {
+                const bool masked = t0 < low_max || t0 + 2 * kKvSlab > end_min;
+                // ... of one column of a group of four
+                const auto weigh = [&](int s, int grp, const Column &c, float x0, float x1) {
+                    float p0 = exp2_approx(fmaf(x0, c.x, c.y)), p1 = exp2_approx(fmaf(x1, c.x, c.y));
+                    if (masked) {
+                        const int i = a.by_group.div(4 * grp + t), tok = t0 + kKvSlab * s + g;
+                        const uint32_t bits = tree && i < r.n ? tree_bits(a, r, i, t0 + kKvSlab * s) : ~0u;
+                        if (tok < c.low || tok >= c.end || !(bits >> g & 1u)) p0 = 0.0f;
+                        if (tok + 8 < c.low || tok + 8 >= c.end || !(bits >> (g + 8) & 1u)) p1 = 0.0f;
+                    }
+                    p[s][0] += p0;
+                    p[s][1] += p1;
+                };
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    lds_words<NB, G::kVec>(stage + (h * NB * 32 + lane * G::kVec) * 4, 128 * G::kVec, kw[h]);
-                    lds_words<NB, G::kVec>(stage + G::kCodeBytes + ((lane >> 3) + 4 * h) * NB * 4, 4 * G::kVec, dk[h]);
-                }
+                for (int s = 0; s < 2; ++s) {
+                    const uint32_t keys = stage + s * kKeyBytes;
+                    uint32_t kw[2][NB], dk[2][NB];
 #pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    uint32_t k0[4], k1[4];
-                    code_pairs(kw[0][b], magic, k0);
-                    code_pairs(kw[1][b], magic, k1);
-                    f[b][0] = k0[0]; f[b][1] = k1[0]; f[b][2] = k0[1]; f[b][3] = k1[1];
-                    f[b][4] = k0[2]; f[b][5] = k1[2]; f[b][6] = k0[3]; f[b][7] = k1[3];
-                    const float2 d = f2_parts(f2_half2(__byte_perm(dk[0][b], dk[1][b], pick)));
-                    dd[b][0] = d.x;
-                    dd[b][1] = d.y;
-                }
-                const bool masked = t0 < low_max || t0 + kKvSlab > end_min;
-                for (int grp = 0; grp < groups; ++grp) {
-                    float x0 = 0.0f, x1 = 0.0f;
-#pragma unroll
-                    for (int b = 0; b < NB; ++b) {
-                        const uint2 q0 = q_sm[(grp * 2 * NB + 2 * b) * 32 + lane], q1 = q_sm[(grp * 2 * NB + 2 * b + 1) * 32 + lane];
-                        const uint32_t a0[4] = {f[b][0], f[b][1], f[b][2], f[b][3]}, a1[4] = {f[b][4], f[b][5], f[b][6], f[b][7]};
+                    for (int h = 0; h < 2; ++h) {
+                        lds_words<NB, G::kVec>(keys + (h * NB * 32 + lane * G::kVec) * 4, 128 * G::kVec, kw[h]);
+                        lds_words<NB, G::kVec>(keys + G::kCodeBytes + ((lane >> 3) + 4 * h) * NB * 4, 4 * G::kVec, dk[h]);
+                    }
+                    uint32_t f[ONE ? 1 : NB][8];
+                    float2 dd[ONE ? 1 : NB];
+                    const auto block = [&](int b, uint32_t (&x)[8], float2 &d) {
+                        uint32_t k0[4], k1[4];
+                        code_pairs(kw[0][b], magic, k0);
+                        code_pairs(kw[1][b], magic, k1);
+                        x[0] = k0[0]; x[1] = k1[0]; x[2] = k0[1]; x[3] = k1[1];
+                        x[4] = k0[2]; x[5] = k1[2]; x[6] = k0[3]; x[7] = k1[3];
+                        d = f2_parts(f2_half2(__byte_perm(dk[0][b], dk[1][b], pick)));
+                    };
+                    const auto score = [&](const uint32_t (&x)[8], float2 d, uint2 q0, uint2 q1, float &x0, float &x1) {
+                        const uint32_t a0[4] = {x[0], x[1], x[2], x[3]}, a1[4] = {x[4], x[5], x[6], x[7]};
                         float c[4];
                         mma_first(c, a0, q0.x, q0.y);
                         mma_acc(c, a1, q1.x, q1.y);
-                        x0 = fmaf(dd[b][0], c[0] + c[1], x0);
-                        x1 = fmaf(dd[b][1], c[2] + c[3], x1);
+                        x0 = fmaf(d.x, c[0] + c[1], x0);
+                        x1 = fmaf(d.y, c[2] + c[3], x1);
+                    };
+                    if constexpr (ONE) {
+                        float x0 = 0.0f, x1 = 0.0f;
+#pragma unroll
+                        for (int b = 0; b < NB; ++b) {
+                            block(b, f[0], dd[0]);
+                            score(f[0], dd[0], qf[2 * b], qf[2 * b + 1], x0, x1);
+                        }
+                        weigh(s, 0, mine, x0, x1);
+                    } else {
+#pragma unroll
+                        for (int b = 0; b < NB; ++b) block(b, f[b], dd[b]);
+                        for (int grp = 0; grp < groups; ++grp) {
+                            float x0 = 0.0f, x1 = 0.0f;
+#pragma unroll
+                            for (int b = 0; b < NB; ++b)
+                                score(f[b], dd[b], q_sm[(grp * 2 * NB + 2 * b) * 32 + lane], q_sm[(grp * 2 * NB + 2 * b + 1) * 32 + lane], x0, x1);
+                            weigh(s, grp, sh_col[4 * grp + t], x0, x1);
+                        }
                     }
-                    const Column c = sh_col[4 * grp + t];
-                    float p0 = exp2_approx(fmaf(x0, c.x, c.y)), p1 = exp2_approx(fmaf(x1, c.x, c.y));
-                    if (masked) {
-                        const int i = a.by_group.div(4 * grp + t);
-                        const uint32_t bits = tree && i < r.n ? tree_bits(a, r, i, t0) : ~0u;
-                        if (t0 + g < c.low || t0 + g >= c.end || !(bits >> g & 1u)) p0 = 0.0f;
-                        if (t0 + g + 8 < c.low || t0 + g + 8 >= c.end || !(bits >> (g + 8) & 1u)) p1 = 0.0f;
-                    }
-                    s0 += p0;
-                    s1 += p1;
                 }
-                s0 += __shfl_xor_sync(0xffffffffu, s0, 1);
-                s1 += __shfl_xor_sync(0xffffffffu, s1, 1);
-                s0 += __shfl_xor_sync(0xffffffffu, s0, 2);
-                s1 += __shfl_xor_sync(0xffffffffu, s1, 2);
             }
-            const int own = g + (t == 1 ? 8 : 0), tok = t0 + own;  // the token that lanes t = 0 and 1 store
-            if (t < 2 && tok < r.len && !(skip >> (k & 31) & 1u)) {
-                const float s = t == 0 ? s0 : s1;
-                out[tok] = before && tok < base ? fmaf(w.keep, __uint_as_float(lds32(stage + kKeyBytes + 4 * own)), s) : s;
-            }
+            // over the four columns' lanes: lane t has tile t / 2, tokens g and g + 8 by t % 2
+            const bool upper = t & 2, odd = t & 1;
+            const float r0 = (upper ? p[1][0] : p[0][0]) + __shfl_xor_sync(0xffffffffu, upper ? p[0][0] : p[1][0], 2);
+            const float r1 = (upper ? p[1][1] : p[0][1]) + __shfl_xor_sync(0xffffffffu, upper ? p[0][1] : p[1][1], 2);
+            const float sum = (odd ? r1 : r0) + __shfl_xor_sync(0xffffffffu, odd ? r0 : r1, 1);
+            const int own = (upper ? kKvSlab : 0) + (odd ? 8 : 0) + g, tok = t0 + own;
+            if (tok < r.len && !(bad_now >> (2 * (k & 15) + (upper ? 1 : 0)) & 1u))
+                out[tok] = before && tok < base ? fmaf(w.keep, __uint_as_float(lds32(stage + 2 * kKeyBytes + 4 * own)), sum) : sum;
         }
         cp_async_wait<0>();
         at += n_steps;
@@ -673,6 +699,14 @@ size_t weights_bytes(int head_dim, int n_seq, int n_kv_heads, int group, int n_t
     }
 }
 
+template <int NB, bool ONE> cudaError_t launch_few(const WeightArgs &w, int64_t items, int64_t columns, int sms, cudaStream_t st) {
+    const cudaError_t e = smem_limit_raised<&attn_weights_kernel<NB, ONE>>();
+    if (e != cudaSuccess) return e;
+    constexpr int kStep = kStepTiles * kKvSlab;
+    const int64_t steps = items * ((w.a.max_kv_len + kStep - 1) / kStep), ctas = static_cast<int64_t>(weight_ctas(NB, ONE)) * sms;
+    const size_t smem = kWeightRing<NB> + static_cast<size_t>((columns + 3) / 4) * 2 * NB * 256;
+    return launch_block_op(&attn_weights_kernel<NB, ONE>, dim3(static_cast<unsigned>(std::min(steps, ctas))), dim3(kWeightThreads), smem, st, w);
+}
 template <int NB> cudaError_t launch_weights(WeightArgs w, int64_t items, int64_t columns, int sms, cudaStream_t st) {
     const int64_t most = w.a.max_kv_len;
     if (columns > kTallWeightCols) {
@@ -688,12 +722,7 @@ template <int NB> cudaError_t launch_weights(WeightArgs w, int64_t items, int64_
         return launch_block_op(&attn_weights_tall_kernel<NB>, dim3(static_cast<unsigned>(items * chunks)), dim3(kWeightThreads),
                                TallGeom<NB>::kSmem, st, w);
     }
-    const cudaError_t e = smem_limit_raised<&attn_weights_kernel<NB>>();
-    if (e != cudaSuccess) return e;
-    const int64_t steps = items * ((most + kWeightWarps * kKvSlab - 1) / (kWeightWarps * kKvSlab));
-    const size_t smem = kWeightRing<NB> + static_cast<size_t>((columns + 3) / 4) * 2 * NB * 256;
-    return launch_block_op(&attn_weights_kernel<NB>, dim3(static_cast<unsigned>(std::min<int64_t>(steps, 2 * sms))), dim3(kWeightThreads),
-                           smem, st, w);
+    return columns <= 4 ? launch_few<NB, true>(w, items, columns, sms, st) : launch_few<NB, false>(w, items, columns, sms, st);
 }
 
 }  // namespace
