@@ -38,9 +38,9 @@ __device__ __forceinline__ uint32_t sum_key(float x) {
 // first and the latest ones, whose sums it reads once into shared memory. The smallest sum that stays is found digit by digit,
 // 11 bits at a time from the top: every CTA counts its sums by digit, and adds up the cluster's counts. Then each CTA knows how
 // many tokens stay before its own, and writes its own in their order: of sums equal to the smallest, the first ones.
-constexpr int kPickThreads = 512, kPickWarps = kPickThreads / 32, kDigit = 2048, kPickCluster = 8;
+constexpr int kPickThreads = 1024, kPickWarps = kPickThreads / 32, kDigit = 2048, kPickCluster = 8;
 constexpr int kPickOne = 8192;      // tokens up to which one CTA does it
-constexpr int kPickHeld = 32 * 1024;  // most sums that a CTA holds; those beyond it are read again
+constexpr int kPickHeld = 48 * 1024;  // most sums that a CTA holds; those beyond it are read again
 
 __global__ void __launch_bounds__(kPickThreads) kv_pick_kernel(KeepArgs a) {
     extern __shared__ float held[];
@@ -82,28 +82,54 @@ __global__ void __launch_bounds__(kPickThreads) kv_pick_kernel(KeepArgs a) {
     if (want == 0) return;
     const int each = (between + ranks - 1) / ranks, first = min(between, rank * each), mine = min(each, between - first);
     const float *src = sums + a.sinks + first;
-    const auto value = [&](int i) { return i < a.held ? held[i] : src[i]; };
-    for (int i = tid; i < min(mine, a.held); i += kPickThreads) held[i] = src[i];
+    const int here = min(mine, a.held);
+    // eight loads at a time in flight
+    constexpr int kAhead = 8;
+    for (int i0 = tid; i0 < here; i0 += kAhead * kPickThreads) {
+        float x[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) x[k] = i0 + k * kPickThreads < here ? src[i0 + k * kPickThreads] : 0.0f;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+            if (i0 + k * kPickThreads < here) held[i0 + k * kPickThreads] = x[k];
+    }
     for (int i = tid; i < 3 * kDigit; i += kPickThreads) (&sh_count[0][0])[i] = 0;
     __syncthreads();
+    // for every sum of from .. to - 1, a lane's turn each, whole warps at a time: at(i, sum, whether there is one)
+    const auto each_sum = [&](int from, int to, int step, auto at) {
+        int i = from;
+        for (; i - lane < min(to, here); i += step) at(i, i < to ? (i < here ? held[i] : src[i]) : 0.0f, i < to);
+        for (; i - lane < to; i += step) at(i, i < to ? src[i] : 0.0f, i < to);
+    };
 
     uint32_t known = 0;  // the smallest sum's digits so far
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
         const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), above = shift + (pass == 2 ? 10 : 11);
         const uint32_t mask = pass == 2 ? 1023u : 2047u;
-        for (int i = tid; i < mine; i += kPickThreads) {
-            const uint32_t k = sum_key(value(i));
-            if (pass == 0 || k >> above == known >> above) atomicAdd(&sh_count[pass][k >> shift & mask], 1u);
-        }
+        each_sum(tid, mine, kPickThreads, [&](int, float x, bool in) {
+            const uint32_t k = sum_key(x), digit = k >> shift & mask;
+            const bool counts = in && (pass == 0 || k >> above == known >> above);
+            // the lanes that have the first one's digit (sums that never counted are all zero) add it at once
+            const uint32_t who = __ballot_sync(0xffffffffu, counts);
+            if (who == 0) return;
+            const int lead = __ffs(who) - 1;
+            const uint32_t theirs = __shfl_sync(0xffffffffu, digit, lead);
+            const bool same = counts && digit == theirs;
+            const uint32_t group = __ballot_sync(0xffffffffu, same);
+            if (lane == lead) atomicAdd(&sh_count[pass][digit], static_cast<uint32_t>(__popc(group)));
+            else if (counts && !same) atomicAdd(&sh_count[pass][digit], 1u);
+        });
         cluster.sync();
-        // four digits a thread, the largest first; `want` of the cluster's sums with the known digits stay
-        uint32_t c[4] = {0, 0, 0, 0}, sum = 0;
+        // two digits a thread, the largest first; `want` of the cluster's sums with the known digits stay
+        static_assert(kDigit == 2 * kPickThreads, "two digits a thread");
+        uint32_t c0 = 0, c1 = 0;
         for (int q = 0; q < ranks; ++q) {
-            const uint4 x = *reinterpret_cast<const uint4 *>(cluster.map_shared_rank(&sh_count[pass][kDigit - 4 - 4 * tid], q));
-            c[0] += x.w; c[1] += x.z; c[2] += x.y; c[3] += x.x;
+            const uint2 x = *reinterpret_cast<const uint2 *>(cluster.map_shared_rank(&sh_count[pass][kDigit - 2 - 2 * tid], q));
+            c0 += x.y;
+            c1 += x.x;
         }
-        sum = c[0] + c[1] + c[2] + c[3];
+        const uint32_t sum = c0 + c1;
         uint32_t upto = sum;
 #pragma unroll
         for (int k = 1; k < 32; k <<= 1) {
@@ -112,17 +138,13 @@ __global__ void __launch_bounds__(kPickThreads) kv_pick_kernel(KeepArgs a) {
         }
         if (lane == 31) sh_scan[warp] = upto;
         __syncthreads();
-        for (int w = 0; w < warp; ++w) upto += sh_scan[w];
-        uint32_t over = upto - sum;  // sums of larger digits than this thread's
+        uint32_t front = lane < warp ? sh_scan[lane] : 0;  // the warps before
+        upto += __reduce_add_sync(0xffffffffu, front);
+        const uint32_t over = upto - sum;  // sums of larger digits than this thread's
         if (over < want && want <= upto) {
-            for (int k = 0; k < 4; ++k) {
-                if (want <= over + c[k]) {
-                    sh_found = static_cast<uint32_t>(kDigit - 1 - 4 * tid - k);
-                    sh_want = want - over;
-                    break;
-                }
-                over += c[k];
-            }
+            const bool second = want > over + c0;
+            sh_found = static_cast<uint32_t>(kDigit - 1 - 2 * tid - (second ? 1 : 0));
+            sh_want = want - over - (second ? c0 : 0);
         }
         __syncthreads();
         known |= sh_found << shift;
@@ -132,11 +154,11 @@ __global__ void __launch_bounds__(kPickThreads) kv_pick_kernel(KeepArgs a) {
     const int per_warp = (mine + 32 * kPickWarps - 1) / (32 * kPickWarps) * 32;
     const int from = min(mine, warp * per_warp), to = min(mine, from + per_warp);
     uint32_t more = 0, same = 0;
-    for (int i = from + lane; i < to; i += 32) {
-        const uint32_t k = sum_key(value(i));
-        more += k > known;
-        same += k == known;
-    }
+    each_sum(from + lane, to, 32, [&](int, float x, bool in) {
+        const uint32_t k = sum_key(x);
+        more += in && k > known;
+        same += in && k == known;
+    });
     more = __reduce_add_sync(0xffffffffu, more);
     same = __reduce_add_sync(0xffffffffu, same);
     if (lane == 0) {
@@ -144,14 +166,13 @@ __global__ void __launch_bounds__(kPickThreads) kv_pick_kernel(KeepArgs a) {
         sh_equal[warp] = same;
     }
     __syncthreads();
-    if (tid == 0) {
-        uint32_t m = 0, s = 0;
-        for (int w = 0; w < kPickWarps; ++w) {
-            m += sh_above[w];
-            s += sh_equal[w];
+    static_assert(kPickWarps == 32, "a lane for each warp");
+    if (warp == 0) {
+        const uint32_t m = __reduce_add_sync(0xffffffffu, sh_above[lane]), e = __reduce_add_sync(0xffffffffu, sh_equal[lane]);
+        if (lane == 0) {
+            sh_mine[0] = m;
+            sh_mine[1] = e;
         }
-        sh_mine[0] = m;
-        sh_mine[1] = s;
     }
     cluster.sync();
     more = same = 0;
@@ -160,22 +181,17 @@ __global__ void __launch_bounds__(kPickThreads) kv_pick_kernel(KeepArgs a) {
         more += o[0];
         same += o[1];
     }
-    for (int w = 0; w < warp; ++w) {
-        more += sh_above[w];
-        same += sh_equal[w];
-    }
+    more += __reduce_add_sync(0xffffffffu, lane < warp ? sh_above[lane] : 0u);
+    same += __reduce_add_sync(0xffffffffu, lane < warp ? sh_equal[lane] : 0u);
     const uint32_t before = (1u << lane) - 1u;
-    for (int i0 = from; i0 < to; i0 += 32) {
-        const int i = i0 + lane;
-        const float x = i < to ? value(i) : 0.0f;
+    each_sum(from + lane, to, 32, [&](int i, float x, bool in) {
         const uint32_t k = sum_key(x);
-        const uint32_t ups = __ballot_sync(0xffffffffu, i < to && k > known), eqs = __ballot_sync(0xffffffffu, i < to && k == known);
+        const uint32_t ups = __ballot_sync(0xffffffffu, in && k > known), eqs = __ballot_sync(0xffffffffu, in && k == known);
         const uint32_t m = more + __popc(ups & before), s = same + __popc(eqs & before);
-        if (i < to && (k > known || (k == known && s < want)))
-            keep(a.sinks + static_cast<int>(m + min(s, want)), a.sinks + first + i, x);
+        if (in && (k > known || (k == known && s < want))) keep(a.sinks + static_cast<int>(m + min(s, want)), a.sinks + first + i, x);
         more += __popc(ups);
         same += __popc(eqs);
-    }
+    });
     cluster.sync();  // no CTA leaves while another may read its counts
 }
 
@@ -383,7 +399,13 @@ template <int NB> cudaError_t launch_accept(const AcceptArgs &a, cudaStream_t st
 cudaError_t launch_pick(KeepArgs a, int64_t items, cudaStream_t st) {
     cudaError_t e = smem_limit_raised<&kv_pick_kernel>();
     if (e != cudaSuccess) return e;
-    const int ranks = a.max_kv_len <= kPickOne ? 1 : kPickCluster;
+    int dev = 0, sms = 0;
+    e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    // a CTA an SM (its registers), so clusters as large as fill the device once
+    int ranks = 1;
+    while (a.max_kv_len > kPickOne && ranks < kPickCluster && items * ranks * 2 <= sms) ranks *= 2;
     a.held = std::min((a.max_kv_len + ranks - 1) / ranks, kPickHeld);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(items * ranks));
