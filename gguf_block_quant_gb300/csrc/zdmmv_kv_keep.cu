@@ -23,7 +23,7 @@ struct KeepArgs {
     int64_t sums_stride, sums_out_stride;
     int32_t max_kv_len, budget, sinks, recent;
     int32_t n_tiles;  // of the budget
-    int32_t held;     // sums of a CTA that its shared memory holds
+    int32_t held;     // sums of a CTA that its shared memory holds, as keys
 };
 
 // A sum as a whole number that rises with it: -0 is 0, a NaN is below all.
@@ -42,13 +42,18 @@ constexpr int kPickThreads = 1024, kPickWarps = kPickThreads / 32, kDigit = 2048
 constexpr int kPickOne = 8192;      // tokens up to which one CTA does it
 constexpr int kPickHeld = 48 * 1024;  // most sums that a CTA holds; those beyond it are read again
 
-__global__ void __launch_bounds__(kPickThreads) kv_pick_kernel(KeepArgs a) {
-    extern __shared__ float held[];
+template <bool CLUSTER> __global__ void __launch_bounds__(kPickThreads) kv_pick_kernel(KeepArgs a) {
+    extern __shared__ uint32_t held[];
     __shared__ __align__(16) uint32_t sh_count[3][kDigit];  // of this CTA's sums, by digit
     __shared__ uint32_t sh_scan[kPickWarps], sh_above[kPickWarps], sh_equal[kPickWarps];
     __shared__ uint32_t sh_found, sh_want, sh_mine[2];
     cg::cluster_group cluster = cg::this_cluster();
-    const int ranks = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
+    const int ranks = CLUSTER ? static_cast<int>(cluster.num_blocks()) : 1, rank = CLUSTER ? static_cast<int>(cluster.block_rank()) : 0;
+    const auto sync_all = [&] {
+        if constexpr (CLUSTER) cluster.sync();
+        else __syncthreads();
+    };
+    const auto of_rank = [&](uint32_t *p, int q) { return CLUSTER ? cluster.map_shared_rank(p, q) : p; };
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     block_op_wait();
     block_op_release();
@@ -71,12 +76,12 @@ __global__ void __launch_bounds__(kPickThreads) kv_pick_kernel(KeepArgs a) {
         }
         return;
     }
-    const auto keep = [&](int at, int t, float x) {
+    const auto keep = [&](int at, int t) {
         index[at] = t;
-        if (sums_out) sums_out[at] = x;
+        if (sums_out) sums_out[at] = sums[t];
     };
-    for (int j = me; j < a.sinks; j += all) keep(j, j, sums[j]);
-    for (int j = me; j < a.recent; j += all) keep(a.budget - a.recent + j, n - a.recent + j, sums[n - a.recent + j]);
+    for (int j = me; j < a.sinks; j += all) keep(j, j);
+    for (int j = me; j < a.recent; j += all) keep(a.budget - a.recent + j, n - a.recent + j);
     const int between = n - a.sinks - a.recent;                 // more than are wanted of them
     uint32_t want = static_cast<uint32_t>(a.budget - a.sinks - a.recent);
     if (want == 0) return;
@@ -91,15 +96,16 @@ __global__ void __launch_bounds__(kPickThreads) kv_pick_kernel(KeepArgs a) {
         for (int k = 0; k < kAhead; ++k) x[k] = i0 + k * kPickThreads < here ? src[i0 + k * kPickThreads] : 0.0f;
 #pragma unroll
         for (int k = 0; k < kAhead; ++k)
-            if (i0 + k * kPickThreads < here) held[i0 + k * kPickThreads] = x[k];
+            if (i0 + k * kPickThreads < here) held[i0 + k * kPickThreads] = sum_key(x[k]);
     }
     for (int i = tid; i < 3 * kDigit; i += kPickThreads) (&sh_count[0][0])[i] = 0;
     __syncthreads();
-    // for every sum of from .. to - 1, a lane's turn each, whole warps at a time: at(i, sum, whether there is one)
-    const auto each_sum = [&](int from, int to, int step, auto at) {
+    // for every sum of from .. to - 1, a lane's turn each, whole warps at a time: at(i, key, whether there is one)
+    const auto each_key = [&](int from, int to, int step, auto at) {
         int i = from;
-        for (; i - lane < min(to, here); i += step) at(i, i < to ? (i < here ? held[i] : src[i]) : 0.0f, i < to);
-        for (; i - lane < to; i += step) at(i, i < to ? src[i] : 0.0f, i < to);
+#pragma unroll 4
+        for (; i - lane + 31 < min(to, here); i += step) at(i, held[i], true);
+        for (; i - lane < to; i += step) at(i, i < to ? (i < here ? held[i] : sum_key(src[i])) : 0u, i < to);
     };
 
     uint32_t known = 0;  // the smallest sum's digits so far
@@ -107,25 +113,15 @@ __global__ void __launch_bounds__(kPickThreads) kv_pick_kernel(KeepArgs a) {
     for (int pass = 0; pass < 3; ++pass) {
         const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), above = shift + (pass == 2 ? 10 : 11);
         const uint32_t mask = pass == 2 ? 1023u : 2047u;
-        each_sum(tid, mine, kPickThreads, [&](int, float x, bool in) {
-            const uint32_t k = sum_key(x), digit = k >> shift & mask;
-            const bool counts = in && (pass == 0 || k >> above == known >> above);
-            // the lanes that have the first one's digit (sums that never counted are all zero) add it at once
-            const uint32_t who = __ballot_sync(0xffffffffu, counts);
-            if (who == 0) return;
-            const int lead = __ffs(who) - 1;
-            const uint32_t theirs = __shfl_sync(0xffffffffu, digit, lead);
-            const bool same = counts && digit == theirs;
-            const uint32_t group = __ballot_sync(0xffffffffu, same);
-            if (lane == lead) atomicAdd(&sh_count[pass][digit], static_cast<uint32_t>(__popc(group)));
-            else if (counts && !same) atomicAdd(&sh_count[pass][digit], 1u);
+        each_key(tid, mine, kPickThreads, [&](int, uint32_t k, bool in) {
+            if (in && (pass == 0 || k >> above == known >> above)) atomicAdd(&sh_count[pass][k >> shift & mask], 1u);
         });
-        cluster.sync();
+        sync_all();
         // two digits a thread, the largest first; `want` of the cluster's sums with the known digits stay
         static_assert(kDigit == 2 * kPickThreads, "two digits a thread");
         uint32_t c0 = 0, c1 = 0;
         for (int q = 0; q < ranks; ++q) {
-            const uint2 x = *reinterpret_cast<const uint2 *>(cluster.map_shared_rank(&sh_count[pass][kDigit - 2 - 2 * tid], q));
+            const uint2 x = *reinterpret_cast<const uint2 *>(of_rank(&sh_count[pass][kDigit - 2 - 2 * tid], q));
             c0 += x.y;
             c1 += x.x;
         }
@@ -154,8 +150,7 @@ __global__ void __launch_bounds__(kPickThreads) kv_pick_kernel(KeepArgs a) {
     const int per_warp = (mine + 32 * kPickWarps - 1) / (32 * kPickWarps) * 32;
     const int from = min(mine, warp * per_warp), to = min(mine, from + per_warp);
     uint32_t more = 0, same = 0;
-    each_sum(from + lane, to, 32, [&](int, float x, bool in) {
-        const uint32_t k = sum_key(x);
+    each_key(from + lane, to, 32, [&](int, uint32_t k, bool in) {
         more += in && k > known;
         same += in && k == known;
     });
@@ -174,25 +169,24 @@ __global__ void __launch_bounds__(kPickThreads) kv_pick_kernel(KeepArgs a) {
             sh_mine[1] = e;
         }
     }
-    cluster.sync();
+    sync_all();
     more = same = 0;
     for (int q = 0; q < rank; ++q) {
-        const uint32_t *o = cluster.map_shared_rank(&sh_mine[0], q);
+        const uint32_t *o = of_rank(&sh_mine[0], q);
         more += o[0];
         same += o[1];
     }
     more += __reduce_add_sync(0xffffffffu, lane < warp ? sh_above[lane] : 0u);
     same += __reduce_add_sync(0xffffffffu, lane < warp ? sh_equal[lane] : 0u);
     const uint32_t before = (1u << lane) - 1u;
-    each_sum(from + lane, to, 32, [&](int i, float x, bool in) {
-        const uint32_t k = sum_key(x);
+    each_key(from + lane, to, 32, [&](int i, uint32_t k, bool in) {
         const uint32_t ups = __ballot_sync(0xffffffffu, in && k > known), eqs = __ballot_sync(0xffffffffu, in && k == known);
         const uint32_t m = more + __popc(ups & before), s = same + __popc(eqs & before);
-        if (in && (k > known || (k == known && s < want))) keep(a.sinks + static_cast<int>(m + min(s, want)), a.sinks + first + i, x);
+        if (in && (k > known || (k == known && s < want))) keep(a.sinks + static_cast<int>(m + min(s, want)), a.sinks + first + i);
         more += __popc(ups);
         same += __popc(eqs);
     });
-    cluster.sync();  // no CTA leaves while another may read its counts
+    if constexpr (CLUSTER) cluster.sync();  // no CTA leaves while another may read its counts
 }
 
 // ------------------------------------------------------------------ their move
@@ -397,20 +391,26 @@ template <int NB> cudaError_t launch_accept(const AcceptArgs &a, cudaStream_t st
     return launch_block_op(kv_accept_kernel<NB>, dim3(static_cast<unsigned>(a.c.n_seq) * a.c.n_kv_heads), dim3(kAcceptThreads), 0, st, a);
 }
 cudaError_t launch_pick(KeepArgs a, int64_t items, cudaStream_t st) {
-    cudaError_t e = smem_limit_raised<&kv_pick_kernel>();
-    if (e != cudaSuccess) return e;
     int dev = 0, sms = 0;
-    e = cudaGetDevice(&dev);
+    cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
     // a CTA an SM (its registers), so clusters as large as fill the device once
     int ranks = 1;
     while (a.max_kv_len > kPickOne && ranks < kPickCluster && items * ranks * 2 <= sms) ranks *= 2;
-    a.held = std::min((a.max_kv_len + ranks - 1) / ranks, kPickHeld);
+    a.held = std::min(a.max_kv_len / ranks + 1, kPickHeld);
+    const size_t smem = static_cast<size_t>(a.held) * 4;
+    if (ranks == 1) {
+        e = smem_limit_raised<&kv_pick_kernel<false>>();
+        if (e != cudaSuccess) return e;
+        return launch_block_op(&kv_pick_kernel<false>, dim3(static_cast<unsigned>(items)), dim3(kPickThreads), smem, st, a);
+    }
+    e = smem_limit_raised<&kv_pick_kernel<true>>();
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(items * ranks));
     cfg.blockDim = dim3(kPickThreads);
-    cfg.dynamicSmemBytes = static_cast<size_t>(a.held) * 4;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -420,7 +420,7 @@ cudaError_t launch_pick(KeepArgs a, int64_t items, cudaStream_t st) {
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = pdl_enabled() ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kv_pick_kernel, a);
+    return cudaLaunchKernelEx(&cfg, kv_pick_kernel<true>, a);
 }
 
 }  // namespace
