@@ -62,6 +62,29 @@ AttnLayout attn_layout(int64_t columns, int head_dim) {
     return f;
 }
 
+// A tree's columns past 16 by 16 a CTA, on own rings: each CTA reads the cache's tiles again, but its eight warps share them,
+// and nothing is converted first. With heads past 128 dimensions always (96 columns over 2011 tokens of 2 heads of 256: 19.9 us,
+// with a shared ring 52.4; 512 columns over 8192 of 8 heads of 256: 310 and 341); else while a place on an SM has no more than
+// kOwnTiles tiles to go over (8 heads of 128: 64 columns over 8000 tokens, 105 tiles a place, 28.4 and 31.6 on tcgen05; over
+// 16000 46.5 and 40.1; 100 columns over 1000 14.2 and 20.4).
+constexpr int kOwnTiles = 120;
+AttnLayout attn_own_layout(int64_t columns, int head_dim) {
+    AttnLayout f{};
+    f.wc = 1;
+    f.nt = 2;
+    f.cols = 16;
+    f.n_ct = ceil_div(columns, 16);
+    f.slots = static_cast<int64_t>(device_sms()) * attn_ctas_per_sm(kv_blocks(head_dim), f.nt);
+    return f;
+}
+AttnLayout attn_tree_layout(int64_t columns, int head_dim, int64_t heads, int64_t tiles) {
+    if (columns > 16) {
+        const AttnLayout own = attn_own_layout(columns, head_dim);
+        if (kv_blocks(head_dim) > kTallBlocks || heads * own.n_ct * tiles <= kOwnTiles * own.slots) return own;
+    }
+    return attn_layout(columns, head_dim);
+}
+
 int64_t attn_tiles(int64_t tokens) { return std::max<int64_t>(1, ceil_div(tokens, kKvSlab)); }
 
 // Whether `items` of `tiles` tiles each are walked by equal stretches, and the parts that this takes (an item of one step is
@@ -85,54 +108,60 @@ int64_t attn_most_shared_splits(const AttnLayout &f, int64_t items, int64_t tile
     return std::min(std::max<int64_t>(1, 4 * f.slots / items), ceil_div(tiles, kMinChunk));
 }
 // Whole waves of CTAs: the split whose waves cost least, a CTA's start and end as much as kEnds tiles.
-int64_t attn_shared_splits(const AttnLayout &f, int64_t items, int64_t tiles, int64_t columns, int head_dim) {
+// `full`: items of that many are taken to be as long as the longest.
+int64_t attn_shared_splits(const AttnLayout &f, int64_t items, int64_t full, int64_t tiles, int64_t columns, int head_dim) {
     if (items > kCounters) return 1;
     const int64_t splits = std::max<int64_t>(1, f.slots / items), most = std::min(4 * splits, ceil_div(tiles, kMinChunk));
     const int64_t cols = std::min<int64_t>(columns, f.cols);
     const auto cost = [&](int64_t n) {
         const int64_t ends = f.tall ? kTallEnds + kTallJoin * ceil_div(cols * head_dim, 2560) * ceil_div(n, 4) : kEnds;
-        return ceil_div(items * n, f.slots) * (ceil_div(tiles, n) + ends);
+        return ceil_div(full * n, f.slots) * (ceil_div(tiles, n) + ends);
     };
     int64_t best = std::min(splits, ceil_div(tiles, kMinChunk));
     for (int64_t n = best / 2; f.tall && n > 1; n /= 2)
         if (cost(n) < cost(best)) best = n;
     for (int waves = 1; waves <= 4; ++waves) {
-        const int64_t n = std::min(std::max<int64_t>(1, waves * f.slots / items), most);
+        const int64_t n = std::min(std::max<int64_t>(1, waves * f.slots / full), most);
         if (cost(n) < cost(best)) best = n;
     }
     return best;
 }
 
-bool attn_plan(const KvView &c, int head_dim, int n_q_heads, int max_q_len, int64_t max_tokens, AttnPlan *out) {
+size_t attn_parts_bytes(int64_t parts, int64_t cols, int head_dim) {
+    return parts == 0 ? 0 : ZDMMV_ATTN_COUNTER_BYTES + static_cast<size_t>(parts * cols) * (head_dim + 2) * 4;
+}
+
+// `room`: of a tree, what a workspace for calls without one holds, which its plan does with; else 0.
+bool attn_plan(const KvView &c, int head_dim, int n_q_heads, int max_q_len, int64_t max_tokens, size_t room, AttnPlan *out) {
     AttnPlan p{};
     const int64_t columns = static_cast<int64_t>(max_q_len) * (n_q_heads / c.n_kv_heads);
     if (columns > 0x7fffff00) return false;
-    const AttnLayout f = attn_layout(columns, head_dim);
+    const int64_t tiles = attn_tiles(max_tokens), heads = static_cast<int64_t>(c.n_seq) * c.n_kv_heads;
+    const AttnLayout f = room ? attn_tree_layout(columns, head_dim, heads, tiles) : attn_layout(columns, head_dim);
     p.nt = f.nt;
     p.wc = f.wc;
     p.cols = f.cols;
     p.tall = f.tall;
-    p.items = static_cast<int64_t>(c.n_seq) * c.n_kv_heads * f.n_ct;
-    const int64_t tiles = attn_tiles(max_tokens);
+    p.items = heads * f.n_ct;
     if (p.items * ceil_div(tiles, kStepTiles) > 0x7fffffff) return false;
     p.n_ct = static_cast<int>(f.n_ct);
     p.round = p.tall ? 8 : 2;  // whole tiles of 128 tokens, whole ring slots
-    if (attn_walks(f, c.n_seq, p.items, tiles)) {
+    if (f.n_ct == 1 && attn_walks(f, c.n_seq, p.items, tiles)) {
         p.ctas = static_cast<int>(attn_walk_ctas(f));
         p.parts = attn_walk_parts(f, tiles);
     } else {
-        const int64_t splits = f.wc == 1 ? attn_own_splits(f, c.n_seq, p.items, tiles)
-                                         : attn_shared_splits(f, p.items, tiles, columns, head_dim);
+        // several trees' lengths differ: half of their items are taken to be long (eight of 25 tokens over up to 8191, 64 items:
+        // 39.5 us in four parts, 50.6 in two)
+        const int64_t full = room && c.n_seq > 1 ? ceil_div(p.items, 2) : p.items;
+        int64_t splits = f.wc == 1 ? attn_own_splits(f, c.n_seq, p.items, tiles)
+                                   : attn_shared_splits(f, p.items, full, tiles, columns, head_dim);
+        while (room && splits > 1 && attn_parts_bytes(p.items * splits, p.cols, head_dim) > room) --splits;
         p.chunk = static_cast<int>(std::max<int64_t>(kMinChunk, ceil_div(ceil_div(tiles, splits), p.round) * p.round));
         p.n_split = static_cast<int>(splits);
         p.parts = splits > 1 ? p.items * splits : 0;
     }
     *out = p;
     return true;
-}
-
-size_t attn_parts_bytes(int64_t parts, int64_t cols, int head_dim) {
-    return parts == 0 ? 0 : ZDMMV_ATTN_COUNTER_BYTES + static_cast<size_t>(parts * cols) * (head_dim + 2) * 4;
 }
 
 // What any call with this layout and up to `tokens` tokens (all of a sequence, or what a window leaves of it) needs. The need
@@ -184,7 +213,10 @@ zdmmv_status attn_call(const zdmmv_kv_cache *cache, const zdmmv_attn_args *args,
     // with a window, no column tile sees more than the window and its own new tokens
     const int64_t most = g.window > 0 ? std::min<int64_t>(g.max_kv_len, static_cast<int64_t>(g.window) + g.max_q_len + kKvSlab)
                                       : g.max_kv_len;
-    if (!attn_plan(a.c, cache->head_dim, g.n_q_heads, g.max_q_len, most, &p)) return ZDMMV_ERR_SHAPE;
+    const int group = g.n_q_heads / cache->n_kv_heads;
+    const bool more = tree && (tree->seen || tree->lse);
+    const size_t room = more ? std::max<size_t>(1, attn_bounds_bytes(a.c, cache->head_dim, group, static_cast<int64_t>(g.max_q_len) * group, most)) : 0;
+    if (!attn_plan(a.c, cache->head_dim, g.n_q_heads, g.max_q_len, most, room, &p)) return ZDMMV_ERR_SHAPE;
     if (g.n_tok == 0) return ZDMMV_OK;
     if (!g.q || !g.q_start || !g.kv_len || !g.out) return ZDMMV_ERR_NULL;
     if (g.q_stride < static_cast<int64_t>(g.n_q_heads) * cache->head_dim) return ZDMMV_ERR_SHAPE;
@@ -199,7 +231,7 @@ zdmmv_status attn_call(const zdmmv_kv_cache *cache, const zdmmv_attn_args *args,
     a.fault = current_fault_word();
     if (!a.fault) return ZDMMV_ERR_CUDA;
     a.q_stride = g.q_stride;
-    a.n_tok = g.n_tok; a.n_q_heads = g.n_q_heads; a.group = g.n_q_heads / cache->n_kv_heads;
+    a.n_tok = g.n_tok; a.n_q_heads = g.n_q_heads; a.group = group;
     a.max_q_len = g.max_q_len; a.max_kv_len = std::min(g.max_kv_len, kMostAttnTokens);
     a.window = attn_window(g.window, g.max_kv_len);
     a.scale_log2 = g.scale * 1.44269504088896340736f;
@@ -212,7 +244,6 @@ zdmmv_status attn_call(const zdmmv_kv_cache *cache, const zdmmv_attn_args *args,
     a.count = static_cast<uint32_t *>(g.workspace);
     a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(g.workspace) + ZDMMV_ATTN_COUNTER_BYTES);
     a.part_ml = reinterpret_cast<float2 *>(a.part + p.parts * p.cols * cache->head_dim);
-    const bool more = tree && (tree->seen || tree->lse);
     if (more) {
         a.seen = tree->seen;
         a.lse = tree->lse;

@@ -1669,7 +1669,7 @@ template <int NB, bool TREE> cudaError_t launch_attn(AttnArgs a, const AttnPlan 
     }
     if constexpr (NB <= kTallBlocks) {
         if (p.tall) return launch_attn_tall<NB, TREE>(a, p, st);
-    } else {
+    } else if constexpr (!TREE) {
         if (p.wc > 4) return launch_attn_form<NB, attn_prompt_nt(NB), kPrompt, TREE>(a, p, st);
         if (p.wc > 1) return launch_attn_form<NB, 2, kShared, TREE>(a, p, st);
     }

@@ -169,3 +169,18 @@ def test_weights_waits_that_gave_up():
     kernel = block(text, text.index("attn_weights_tall_kernel(WeightArgs w)"))
     after = kernel[kernel.index("if (dead) sh_dead = 1;"):]
     assert "wait(" not in after and after.index("__syncthreads()") < after.index("if (sh_dead) sum = ")
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="what is not refused would run")
+@pytest.mark.parametrize("head_dim", [64, 128, 256])
+def test_attentions_workspace_is_one_for_trees(L, head_dim):  # noqa: F811
+    """A tree's plan does with what zdmmv_attn_q4_0_workspace_bytes asks for, whatever the shape."""
+    import itertools
+    for n_seq, heads, group, new, most, window in itertools.product((1, 2, 7, 40, 300, 700), (1, 4, 8), (1, 4, 5, 8), (1, 3, 5, 12, 25, 64, 300),
+                                                                   (1, 300, 2011, 9000, 65536), (0, 1000)):
+        c = _cache(n_seq=n_seq, n_kv_heads=heads, head_dim=head_dim, max_pages=1 << 16)
+        size = L.zdmmv_attn_q4_0_workspace_bytes(ctypes.byref(c), heads * group, new, most)
+        args = _attn(n_q_heads=heads * group, q_stride=heads * group * head_dim, max_q_len=new, max_kv_len=most, window=window,
+                     n_tok=new, workspace=FAKE if size else None, workspace_bytes=size)
+        got = L.zdmmv_attn_tree_q4_0(ctypes.byref(c), ctypes.byref(args), ctypes.byref(_tree(seen_words=10)), None)
+        assert got not in (1, 2, 6), (n_seq, heads, group, new, most, window, got)

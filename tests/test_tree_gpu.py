@@ -58,7 +58,7 @@ def run(rng, lens, new, page, heads, group, dim, masks="tree", window=0, scale=N
 @pytest.mark.parametrize("dim", [64, 96, 128, 192, 256])
 @pytest.mark.parametrize("heads, group, new", [(2, 1, 3), (1, 1, 8), (2, 4, 4), (1, 4, 7), (2, 3, 13), (1, 8, 17)])
 def test_tree(dim, heads, group, new):
-    """4, 8, 16, 28, 39 and 136 columns: every form of the kernel; lengths around a tile's and a page's ends."""
+    """4, 8, 16, 28, 39 and 136 columns; lengths around a tile's and a page's ends."""
     rng = np.random.default_rng(dim + heads + new)
     run(rng, [new, new + 1, 40, 300, 1029], [new, max(1, new - 1), new, 2, new], 32, heads, group, dim)
 
@@ -230,3 +230,53 @@ def test_streams_and_graphs():
             results.append(Z.attn_tree_q4_0(cache, qd, starts, ld, n, 900, seen=sd, stream=st))
     torch.cuda.synchronize()
     assert all(torch.equal(r, out) for r in results)
+
+
+# More columns times tiles than 16 columns a CTA are for: heads of up to 128 dimensions on tcgen05.
+@pytest.mark.parametrize("dim, heads, group, new, length, window, masks", [
+    (128, 8, 4, 16, 9300, 0, "tree"), (64, 16, 4, 24, 12500, 0, "tree"), (96, 8, 4, 33, 9500, 0, "any"), (128, 8, 4, 40, 9100, 6400, "tree"),
+    (128, 8, 4, 25, 9200, 0, None)])
+def test_many_columns_and_tokens(dim, heads, group, new, length, window, masks):
+    rng = np.random.default_rng(dim + new)
+    cache, _, _, q, q_start, _, seen, out, lse = run(rng, [length], [new], 64, heads, group, dim, masks=masks, window=window)
+    again = torch.empty_like(lse)
+    o = Z.attn_tree_q4_0(cache, dev(q), dev(q_start), dev(np.array([length], np.int32)), new, length, seen=seen, lse=again, window=window)
+    assert torch.equal(o, out) and torch.equal(again, lse)
+
+
+def test_many_columns_and_sequences():
+    rng = np.random.default_rng(31)
+    lens = [3000, 0, 1, 700, 2999, 25, 1800]
+    run(rng, lens, [25, 0, 1, 9, 25, 25, 13], 32, 8, 4, 128)
+    run(rng, lens, [25, 3, 2, 9, 25, 25, 13], 16, 8, 4, 96, masks="any", window=900)
+
+
+@pytest.mark.parametrize("what", ["v", "k", "scores"])
+def test_many_columns_with_rows_done_once_more(what):
+    """Infinities and NaN in drafted tokens that most rows do not see, and scores past 2^23, on tcgen05 (rows token by token)."""
+    rng = np.random.default_rng(5)
+    page, heads, group, dim, n, length = 64, 8, 4, 128, 16, 9300
+    cache, pages, table = random_cache(rng, [length], page, heads, dim)
+    masks = [T.tree_mask(n, rng)]
+    masks[0][:, 7] = False
+    masks[0][:, 12] = False
+    masks[0][7, 7] = masks[0][12, 12] = True
+    for j, worst in ((7, np.inf), (12, np.nan)) if what != "scores" else ():
+        at = length - n + j
+        for h in range(heads):
+            R.put(pages, page, heads, dim, table[0, at // page], at % page, h, 1 if what == "v" else 0, np.full(dim, 15),
+                  np.full(dim // 32, worst, np.float16))
+    cache = Z.KVCache(dev(pages), page, heads, dim, dev(table))
+    q = (rng.standard_normal((n, heads * group, dim)) * (3e7 if what == "scores" else 1)).astype(np.float32)
+    q_start, lse = np.array([0, n], np.int32), torch.empty(n, heads * group, device="cuda")
+    out = Z.attn_tree_q4_0(cache, dev(q), dev(q_start), dev(np.array([length], np.int32)), n, length, seen=dev(T.pack(masks, 1)), lse=lse)
+    rows = np.array([i for i in range(n) if i not in (7, 12)])
+    if what != "scores":
+        with np.errstate(invalid="ignore"):
+            check(out, lse, q, q_start, [length], table, pages, page, heads, dim, masks, rows=rows)
+        return
+    k, v = R.values(pages, page, heads, dim)
+    _, want_lse, tp, _ = T.attention(q, q_start, [length], table, k, v, page, dim ** -0.5, masks)
+    assert np.isfinite(out.cpu().numpy()).all()
+    # ln of at most 9300 equal terms above the largest score
+    assert np.all(np.abs(lse.double().cpu().numpy() - want_lse) <= 2.0 ** -19 * tp + 8 * 2.0 ** -24 * np.abs(want_lse) + 10)

@@ -43,27 +43,33 @@ def attention(q, q_start, lens, table, k, v, page_tokens, scale, masks=None, win
     """(out, lse, tol_p, tol_v) in 64 bits; the latter two as block_ref.attention's. masks: one a sequence."""
     n_tok, hq, dim = q.shape
     hk = k.shape[1]
+    group = hq // hk
     out, lse = np.zeros(q.shape), np.full((n_tok, hq), -np.inf)
     tol_p, tol_v = np.zeros((n_tok, hq)), np.zeros(q.shape)
     for s, length in enumerate(lens):
-        n = q_start[s + 1] - q_start[s]
-        for i in range(n):
-            row = q_start[s] + i
-            t = np.flatnonzero(visible(length, n, i, None if masks is None else masks[s], window))
-            if len(t) == 0:
-                continue
-            page, at = table[s][t // page_tokens], t % page_tokens
-            for h in range(hq):
-                kk, vv = k[page, h // (hq // hk), at], v[page, h // (hq // hk), at]
-                score = kk @ q[row, h].astype(np.float64) * scale
-                e = np.exp(score - score.max())
-                lse[row, h] = score.max() + np.log(e.sum())
-                p = e / e.sum()
-                out[row, h] = p @ vv
-                big_k = np.abs(kk).reshape(len(t), -1, R.QK).max(-1)
-                big_v = np.abs(vv).reshape(len(t), -1, R.QK).max(-1)
-                tol_p[row, h] = abs(scale) * (big_k @ np.abs(q[row, h]).reshape(-1, R.QK).sum(-1)).max()
-                tol_v[row, h] = np.repeat(p @ big_v, R.QK)
+        n, rows = q_start[s + 1] - q_start[s], slice(q_start[s], q_start[s + 1])
+        if n == 0 or length <= 0:
+            continue
+        see = np.array([visible(length, n, i, None if masks is None else masks[s], window) for i in range(n)])
+        some = see.any(1)
+        t = np.arange(length)
+        page, at = table[s][t // page_tokens], t % page_tokens
+        for h in range(hk):
+            heads = slice(h * group, (h + 1) * group)
+            kk, vv = k[page, h, at], v[page, h, at]
+            qq = q[rows, heads].astype(np.float64)
+            big_k, big_v = (np.abs(x).reshape(length, -1, R.QK).max(-1) for x in (kk, vv))
+            score = np.where(see[:, None], qq @ kk.T * scale, -np.inf)
+            top = np.where(some[:, None], score.max(-1, initial=-np.inf), 0)
+            e = np.exp(score - top[..., None])
+            total = np.where(some[:, None], e.sum(-1), 1)
+            lse[rows, heads] = np.where(some[:, None], top + np.log(total), -np.inf)
+            p = e / total[..., None]
+            # what a row does not see may be no number
+            out[rows, heads] = np.array([[pj[see[i]] @ vv[see[i]] for pj in p[i]] for i in range(n)])
+            reach = np.abs(qq).reshape(n, group, -1, R.QK).sum(-1) @ big_k.T
+            tol_p[rows, heads] = abs(scale) * np.where(see[:, None], reach, 0).max(-1, initial=0)
+            tol_v[rows, heads] = np.array([[np.repeat(pj[see[i]] @ big_v[see[i]], R.QK) for pj in p[i]] for i in range(n)])
     return out, lse, tol_p, tol_v
 
 
