@@ -17,7 +17,7 @@ namespace zdmmv {
 namespace {
 
 constexpr int kWeightWarps = 8, kWeightThreads = kWeightWarps * 32;
-constexpr int kBlockCols = 64;       // columns of a block of q
+constexpr int kBlockCols = 64;       // columns of a block of q, and most of the kernel for few
 constexpr int kAllCols = 0x7fffff00; // a column tile of all columns
 
 struct WeightArgs {
@@ -684,11 +684,15 @@ template <int NB> __global__ void __launch_bounds__(kWeightThreads, TallGeom<NB>
     }
 }
 
-// More columns than these take the tall kernel (all that the other one takes, and what that does not).
-constexpr int kTallWeightCols = 32;
-static_assert(kTallWeightCols <= kBlockCols, "the other kernel's columns");
+// More columns than kBlockCols take the tall kernel, and more than kFewCols where all its CTAs run at once (a CTA's start, its
+// keys turned into operands, costs it as much as two blocks of columns): 8 heads of 128, 48 columns over 1000 tokens 7.1 us and
+// 10.8 with the other kernel, over 64000 67.0 and 49.7; 24 columns over 1000 7.1 and 7.3; 64 over 64000 67.1 and 62.8.
+constexpr int kFewCols = 24;
+template <int NB> bool weights_tall(int64_t columns, int64_t items, int64_t max_kv_len, int sms) {
+    return columns > kBlockCols || (columns > kFewCols && items * ((max_kv_len + kTallTokens - 1) / kTallTokens) <= TallGeom<NB>::kCtas * sms);
+}
 size_t weights_bytes(int head_dim, int n_seq, int n_kv_heads, int group, int n_tok, int max_q_len) {
-    if (static_cast<int64_t>(std::min(max_q_len, n_tok)) * group <= kTallWeightCols) return 0;
+    if (static_cast<int64_t>(std::min(max_q_len, n_tok)) * group <= kFewCols) return 0;
     const int64_t images = weight_blocks(n_seq, n_tok, group) * n_kv_heads;
     switch (kv_blocks(head_dim)) {
     case 2: return images * TallGeom<2>::kImage;
@@ -709,7 +713,7 @@ template <int NB, bool ONE> cudaError_t launch_few(const WeightArgs &w, int64_t 
 }
 template <int NB> cudaError_t launch_weights(WeightArgs w, int64_t items, int64_t columns, int sms, cudaStream_t st) {
     const int64_t most = w.a.max_kv_len;
-    if (columns > kTallWeightCols) {
+    if (weights_tall<NB>(columns, items, most, sms)) {
         cudaError_t e = smem_limit_raised<&attn_weights_tall_kernel<NB>>();
         if (e != cudaSuccess) return e;
         const int64_t blocks = (columns + kBlockCols - 1) / kBlockCols;

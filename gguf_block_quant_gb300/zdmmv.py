@@ -643,7 +643,7 @@ def attn_weights_q4_0(cache: KVCache, q, q_start, kv_len, lse, max_q_len: int, m
     pb, sb = (0, 0) if sums is None else _per_head(sums, cache, max_kv_len, "sums")
     ps, words = _seen(seen, n_tok)
     pw = nw = 0
-    if workspace is None and heads * min(n_tok, max_q_len) > 32 * cache.n_kv_heads:  # with fewer columns none is needed
+    if workspace is None and heads * min(n_tok, max_q_len) > 24 * cache.n_kv_heads:  # with fewer columns none is needed
         workspace = _make(attn_weights_q4_0_workspace_bytes(cache, heads, n_tok, max_q_len), _U8, q.device, stream)
     if workspace is not None:
         pw, nw = _whole(workspace, _U8, 0, "workspace"), workspace.numel()

@@ -765,7 +765,7 @@ typedef struct {
 } zdmmv_attn_weights_args;
 
 /* What a workspace has to hold for a call with n_tok rows, max_q_len of them a
- * sequence: q as the tensor cores take it, from 33 columns (rows times the heads of a
+ * sequence: q as the tensor cores take it, from 25 columns (rows times the heads of a
  * kv head) on; 0 with fewer. Rises with both. */
 size_t zdmmv_attn_weights_q4_0_workspace_bytes(const zdmmv_kv_cache *cache, int n_q_heads, int n_tok, int max_q_len);
 /* After a wait that gave up (ZDMMV_FAULT_WAIT_TIMEOUT) the entries concerned are

@@ -607,3 +607,9 @@ def test_weights_of_a_prompts_chunk():
         Z.attn_weights_q4_0(cache, dev(q), starts, ld, lse, 256, 3000, sums=had, out=again)
         assert torch.equal(again, out)
     assert Z.device_status() == 0
+
+
+@pytest.mark.parametrize("heads, group, dim, new, length", [(8, 4, 128, 15, 5200), (8, 2, 64, 31, 5200), (8, 4, 256, 12, 2600)])
+def test_weights_of_a_middling_number_of_columns(heads, group, dim, new, length):
+    """25 to 64 columns over more tokens than the tall kernel's CTAs take at once: sixteen groups of four at most."""
+    run_weights(np.random.default_rng(dim), [length, 40], [new, new - 3], 64, heads, group, dim, masks="tree")

@@ -149,8 +149,8 @@ def test_null_structs(L):  # noqa: F811
 
 def test_weights_workspace(L):  # noqa: F811
     size = lambda heads, tok, new, **k: L.zdmmv_attn_weights_q4_0_workspace_bytes(ctypes.byref(_cache(**k)), heads, tok, new)  # noqa: E731
-    assert size(8, 8, 8) == 0 and size(8, 100, 8) == 0 and size(8, 8, 100) == 0      # 32 columns
-    assert size(8, 9, 9) > 0 and size(16, 5, 5) > 0
+    assert size(8, 6, 6) == 0 and size(8, 100, 6) == 0 and size(8, 6, 100) == 0      # 24 columns
+    assert size(8, 7, 7) > 0 and size(16, 4, 4) > 0
     assert size(7, 9, 9) == 0 and size(8, -1, 9) == 0 and size(8, 9, 0) == 0         # refused shapes
     last = 0
     for tok in (9, 10, 16, 17, 100, 101, 1000):
