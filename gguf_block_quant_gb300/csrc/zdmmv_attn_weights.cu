@@ -22,7 +22,7 @@ constexpr int kAllCols = 0x7fffff00; // a column tile of all columns
 
 struct WeightArgs {
     AttnArgs a;            // out, the workspace's and the split's fields unused
-    FastDiv by_chunks;
+    FastDiv by_items;      // kv heads of sequences
     const float *lse_in, *before;
     float *out;
     int64_t before_stride, out_stride;  // between kv heads
@@ -479,8 +479,8 @@ template <int NB> __global__ void __launch_bounds__(kWeightThreads, TallGeom<NB>
     block_op_release();
     // until its wait below the kernel reads only what was there before weights_q_kernel, which began after all that was
     // complete, and writes nothing but the status
-    // the last tokens of a sequence, whose columns are masked, first
-    const int item = w.by_chunks.div(blockIdx.x), chunk = w.chunks - 1 - w.by_chunks.mod(blockIdx.x, item);
+    // the last tokens of the sequences, whose columns are masked, first
+    const int back = w.by_items.div(blockIdx.x), item = w.by_items.mod(blockIdx.x, back), chunk = w.chunks - 1 - back;
     const int seq = a.by_heads.div(item), kvh = a.by_heads.mod(item, seq);
     const AttnRange r = attn_range<true>(a, seq, 0, kAllCols);
     const int first = chunk * kTallTokens, live = r.bad ? 0 : r.len - first;  // tokens from `live` on are none
@@ -722,7 +722,7 @@ template <int NB> cudaError_t launch_weights(WeightArgs w, int64_t items, int64_
         if (e != cudaSuccess) return e;
         const int64_t chunks = (most + kTallTokens - 1) / kTallTokens;
         w.chunks = static_cast<int32_t>(chunks);
-        w.by_chunks = FastDiv::of(w.chunks);
+        w.by_items = FastDiv::of(static_cast<int32_t>(items));
         return launch_block_op(&attn_weights_tall_kernel<NB>, dim3(static_cast<unsigned>(items * chunks)), dim3(kWeightThreads),
                                TallGeom<NB>::kSmem, st, w);
     }
