@@ -60,7 +60,6 @@ template <bool CLUSTER> __global__ void __launch_bounds__(kPickThreads) kv_pick_
     const int item = blockIdx.x / ranks, seq = a.by_heads.div(item);
     const float *sums = a.sums + static_cast<int64_t>(item) * a.sums_stride;
     int32_t *index = a.index + static_cast<int64_t>(item) * a.budget;
-    float *sums_out = a.sums_out ? a.sums_out + static_cast<int64_t>(item) * a.sums_out_stride : nullptr;
     const int n = a.kv_len[seq];
     const bool bad = n < 0 || n > a.max_kv_len || n > static_cast<int64_t>(a.from.max_pages) * a.from.page_tokens;
     if (rank == 0 && tid == 0) {
@@ -69,27 +68,18 @@ template <bool CLUSTER> __global__ void __launch_bounds__(kPickThreads) kv_pick_
     }
     const int me = rank * kPickThreads + tid, all = ranks * kPickThreads;
     if (bad || n <= a.budget) {  // the whole cluster takes this way
-        for (int j = me; j < a.budget; j += all) {
-            const bool in = !bad && j < n;
-            index[j] = in ? j : -1;
-            if (sums_out) sums_out[j] = in ? sums[j] : 0.0f;
-        }
+        for (int j = me; j < a.budget; j += all) index[j] = !bad && j < n ? j : -1;
         return;
     }
-    const auto keep = [&](int at, int t) {
-        index[at] = t;
-        if (sums_out) sums_out[at] = sums[t];
-    };
-    for (int j = me; j < a.sinks; j += all) keep(j, j);
-    for (int j = me; j < a.recent; j += all) keep(a.budget - a.recent + j, n - a.recent + j);
+    for (int j = me; j < a.sinks; j += all) index[j] = j;
+    for (int j = me; j < a.recent; j += all) index[a.budget - a.recent + j] = n - a.recent + j;
     const int between = n - a.sinks - a.recent;                 // more than are wanted of them
     uint32_t want = static_cast<uint32_t>(a.budget - a.sinks - a.recent);
     if (want == 0) return;
     const int each = (between + ranks - 1) / ranks, first = min(between, rank * each), mine = min(each, between - first);
     const float *src = sums + a.sinks + first;
     const int here = min(mine, a.held);
-    // eight loads at a time in flight
-    constexpr int kAhead = 8;
+    constexpr int kAhead = 16;  // loads at a time in flight
     for (int i0 = tid; i0 < here; i0 += kAhead * kPickThreads) {
         float x[kAhead];
 #pragma unroll
@@ -182,7 +172,7 @@ template <bool CLUSTER> __global__ void __launch_bounds__(kPickThreads) kv_pick_
     each_key(from + lane, to, 32, [&](int i, uint32_t k, bool in) {
         const uint32_t ups = __ballot_sync(0xffffffffu, in && k > known), eqs = __ballot_sync(0xffffffffu, in && k == known);
         const uint32_t m = more + __popc(ups & before), s = same + __popc(eqs & before);
-        if (in && (k > known || (k == known && s < want))) keep(a.sinks + static_cast<int>(m + min(s, want)), a.sinks + first + i);
+        if (in && (k > known || (k == known && s < want))) index[a.sinks + static_cast<int>(m + min(s, want))] = a.sinks + first + i;
         more += __popc(ups);
         same += __popc(eqs);
     });
@@ -191,7 +181,7 @@ template <bool CLUSTER> __global__ void __launch_bounds__(kPickThreads) kv_pick_
 
 // ------------------------------------------------------------------ their move
 // A warp makes a tile of 16 tokens of one head: a lane brings the words of the new tile that it stores, from wherever their
-// tokens lie. A token's K words are the same there and here; a V word holds two tokens' halves.
+// tokens lie. A token's K words are the same there and here; a V word holds two tokens' halves. The tokens' sums go along.
 constexpr int kGatherWarps = 8;
 template <int NB> __global__ void __launch_bounds__(kGatherWarps * 32) kv_gather_kernel(KeepArgs a, int64_t n_jobs) {
     using G = KvGeom<NB>;
@@ -211,9 +201,11 @@ template <int NB> __global__ void __launch_bounds__(kGatherWarps * 32) kv_gather
     const uint8_t *src = nullptr;
     int r = 0;
     bool some = false, wrong = false;
+    float sum = 0.0f;
     if (lane < kKvSlab && t0 + lane < a.budget) {
         const int t = a.index[static_cast<int64_t>(item) * a.budget + t0 + lane];
         some = t >= 0;
+        if (a.sums_out && some) sum = a.sums[static_cast<int64_t>(item) * a.sums_stride + t];
         if (some) {
             const int slab = t / kKvSlab, slot = a.from_page_tiles.div(slab);
             const int page = a.from.table[static_cast<int64_t>(seq) * a.from.max_pages + slot];
@@ -224,11 +216,19 @@ template <int NB> __global__ void __launch_bounds__(kGatherWarps * 32) kv_gather
                       (static_cast<int64_t>(kvh) * static_cast<int>(a.from_page_tiles.d) + a.from_page_tiles.mod(slab, slot)) * G::kTileBytes;
         }
     }
-    if (!__any_sync(0xffffffffu, some)) return;
+    const bool put_sum = a.sums_out && lane < kKvSlab && t0 + lane < a.budget;
+    float *sum_to = a.sums_out + static_cast<int64_t>(item) * a.sums_out_stride + t0 + lane;
+    if (!__any_sync(0xffffffffu, some)) {
+        if (put_sum) *sum_to = 0.0f;
+        return;
+    }
     const int slot = a.to_page_tiles.div(tile), page = a.to.table[static_cast<int64_t>(seq) * a.to.max_pages + slot];
     const bool lost = page < 0 || page >= a.to.n_pages;
     if ((wrong || (lost && lane == 0)) && a.status) *a.status = 1;
-    if (lost) return;
+    if (lost) {
+        if (put_sum) *sum_to = sum;
+        return;
+    }
     uint8_t *dst = a.to.pages + page * a.to.page_bytes +
                    (static_cast<int64_t>(kvh) * static_cast<int>(a.to_page_tiles.d) + a.to_page_tiles.mod(tile, slot)) * G::kTileBytes;
     const uint32_t nans = __ballot_sync(0xffffffffu, wrong);
@@ -292,6 +292,7 @@ template <int NB> __global__ void __launch_bounds__(kGatherWarps * 32) kv_gather
 #pragma unroll
     for (int c = 0; c < kPer; ++c)
         if (32 * c + lane < kScaleWords) reinterpret_cast<uint32_t *>(dst + G::kKScaleAt)[32 * c + lane] = d[c];
+    if (put_sum) *sum_to = sum;
 }
 
 // ------------------------------------------------------------------ the accepted path
