@@ -98,6 +98,10 @@ template <int N> __device__ __forceinline__ void cp_async_wait() { asm volatile(
 // grid that fills the device takes an equal stretch, whatever the lengths. A warp keeps the next pairs' keys, and their tokens'
 // earlier sums, on their way into its own ring in shared memory; a pair's 32 sums end up one in each lane.
 // ONE: up to four columns, whose parts of q stay in registers.
+// One token of 32 heads over 130975 tokens of 8 kv heads of 128: 21.5 us, 3.9 TB/s, 59% of the copy rate; 48 sequences of up to
+// 16384 46.0 us, 3.7 TB/s. Bound by issue (61% active; 244 instructions a tile, 72 of them the codes' conversion) and the start:
+// lengths, pages, the first keys and q are four latencies one after another, of some 4 us. Measured before, over 130975: loads
+// a tile ahead into registers, the earlier sums read where they are used, 33.2; rings of four single tiles 28.8.
 constexpr int kWeightStages = 3;
 template <int NB> constexpr int kPairBytes = 2 * 9 * NB * kQK + 2 * kKvSlab * 4;
 template <int NB> constexpr size_t kWeightRing = static_cast<size_t>(kWeightWarps) * kWeightStages * kPairBytes<NB>;
@@ -357,11 +361,14 @@ template <int NB, bool ONE> __global__ void __launch_bounds__(kWeightThreads, we
 //    128 bytes), each in two fp16 parts (k exactly, q to 22 bits; zdmmv_attn_prompt.cuh): 3 D/16 products a block.
 //  * Every CTA of a kv head needs all of its q: weights_q_kernel makes the operands (and what each column needs to become a
 //    weight) once, in the workspace, as they lie in shared memory, and the CTAs bring them with one bulk copy a block, two
-//    blocks ahead. (Each CTA turning q into operands by itself: 141 us for 256 tokens over 8192 instead of the present time at
-//    the end of this comment, 700 of 1000 instructions a block.)
+//    blocks ahead. (Each CTA turning q into operands by itself: 141 us where this takes 46, 700 of 1000 instructions a block.)
 //  * One lane starts a block's products while all threads take the weights of the block before; D is double. Two CTAs an SM
 //    (heads of up to 128 dimensions) fill each other's gaps.
 // Where a token has a scale of 2^13 or more, the 128 tokens' operand is in units of 16, as there.
+// 256 tokens of 32 heads over 8192 of 8 kv heads of 128 (1024 columns, 512 CTAs): 46.1 us, the tensor cores 45% busy, of which
+// weights_q_kernel and the start take 4. A block's 24 products are 816 cycles; two CTAs' blocks take 2200, as the next block's
+// products wait for the weights of the one before (D is double, not triple), and 512 CTAs are 1.7 rounds of 304 places. On
+// mma.sync 199 us.
 constexpr int kTallTokens = 128, kTallSlots = 3;
 template <int NB> struct TallGeom {
     static constexpr int kDim = NB * kQK, kChunks = (NB + 1) / 2;  // of 64 dimensions

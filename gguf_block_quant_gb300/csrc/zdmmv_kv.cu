@@ -43,7 +43,7 @@ struct AppendArgs {
     FastDiv by_groups, by_page;
     const float *k, *v, *q;
     const int32_t *seq, *pos;
-    const int32_t *turn_pos;  // the rotation's positions; pos itself where they are the same
+    const int32_t *turn_pos;  // the rotation's positions; nullptr: pos (the kernels' instances with AT false)
     const float *rope;
     float *q_out;
     __half *k_val, *v_val;
@@ -134,12 +134,12 @@ struct Place {
     bool ok, bad;   // written to the cache; outside what the cache and the rotation table have
 };
 // The page's look-up is the one load: place_check looks at what it brought.
-__device__ __forceinline__ Place place_of(const AppendArgs &a, int pos, int seq, int turn_pos) {
+template <bool AT> __device__ __forceinline__ Place place_of(const AppendArgs &a, int pos, int seq, int turn_pos) {
     Place w;
     const bool pad = pos < 0;
     const int slot = pad ? 0 : a.by_page.div(pos);
     w.in = pad ? 0 : a.by_page.mod(pos, slot);
-    w.bad = !pad && (seq < 0 || seq >= a.c.n_seq || slot >= a.c.max_pages || (a.rot_dim > 0 && (turn_pos < 0 || turn_pos >= a.rope_rows)));
+    w.bad = !pad && (seq < 0 || seq >= a.c.n_seq || slot >= a.c.max_pages || (a.rot_dim > 0 && ((AT && turn_pos < 0) || turn_pos >= a.rope_rows)));
     w.ok = !pad && !w.bad;
     w.page = w.ok ? a.c.table[static_cast<int64_t>(seq) * a.c.max_pages + slot] : 0;
     return w;
@@ -234,7 +234,7 @@ __device__ __forceinline__ void put_head(const AppendArgs &a, const Rows &to, in
 // of a head before it stores any (so q_out may be q); the look-up of the token's place runs beside the loads. Bound by
 // the latency of its three dependent loads (2.2 us for 48 tokens of 48 heads of 128).
 constexpr int kAppendWarps = 4;
-template <int NB, bool FAST> __global__ void __launch_bounds__(kAppendWarps * 32) kv_append_kernel(AppendArgs a) {
+template <int NB, bool FAST, bool AT> __global__ void __launch_bounds__(kAppendWarps * 32) kv_append_kernel(AppendArgs a) {
     using G = KvGeom<NB>;
     constexpr int kPass = (G::kDim + 127) / 128;
     const int lane = threadIdx.x & 31;
@@ -244,7 +244,7 @@ template <int NB, bool FAST> __global__ void __launch_bounds__(kAppendWarps * 32
     block_op_release();
     if (tok >= a.n_tok) return;
     const bool turned = head < a.n_q_heads + a.c.n_kv_heads;
-    const int pos = a.pos[tok], seq = a.seq[tok], turn_pos = a.turn_pos[tok];
+    const int pos = a.pos[tok], seq = a.seq[tok], turn_pos = AT ? a.turn_pos[tok] : pos;
     float v[kPass][4], o[kPass][4];
 #pragma unroll
     for (int p = 0; p < kPass; ++p) {
@@ -252,7 +252,7 @@ template <int NB, bool FAST> __global__ void __launch_bounds__(kAppendWarps * 32
         v[p][0] = v[p][1] = v[p][2] = v[p][3] = 0.0f;
         if (e0 < G::kDim) load_head<FAST>(a, head_row(a, tok, head, G::kDim), e0, turned && e0 < a.rot_dim, v[p], o[p]);
     }
-    Place w = place_of(a, pos, seq, turn_pos);
+    Place w = place_of<AT>(a, pos, seq, turn_pos);
     Turn turn[kPass];
 #pragma unroll
     for (int p = 0; p < kPass; ++p)
@@ -276,7 +276,7 @@ template <int NB, bool FAST> __global__ void __launch_bounds__(kAppendWarps * 32
 // SM, each with its loads in flight for half of its life), with it 37.0 us (76% of the copy rate), then bound by issue (67%
 // active, 135 instructions a head; 41 us with 154 before the token's row addresses were found once).
 constexpr int kStreamWarps = 8, kStreamHeads = 4, kStreamSlots = 3;
-template <int NB, bool FAST> __global__ void __launch_bounds__(kStreamWarps * 32, NB <= 4 ? 3 : 2) kv_append_stream_kernel(AppendArgs a, int n_jobs) {
+template <int NB, bool FAST, bool AT> __global__ void __launch_bounds__(kStreamWarps * 32, NB <= 4 ? 3 : 2) kv_append_stream_kernel(AppendArgs a, int n_jobs) {
     using G = KvGeom<NB>;
     constexpr int kPass = (G::kDim + 127) / 128, kHeadBytes = G::kDim * 4, kSlotBytes = kStreamHeads * kHeadBytes;
     extern __shared__ __align__(128) uint8_t smem[];
@@ -318,8 +318,8 @@ template <int NB, bool FAST> __global__ void __launch_bounds__(kStreamWarps * 32
         }
         if (tok != at) {
             at = tok;
-            const int turn_pos = a.turn_pos[tok];
-            w = place_of(a, a.pos[tok], a.seq[tok], turn_pos);
+            const int pos = a.pos[tok], turn_pos = AT ? a.turn_pos[tok] : pos;
+            w = place_of<AT>(a, pos, a.seq[tok], turn_pos);
 #pragma unroll
             for (int p = 0; p < kPass; ++p)
                 if (w.ok && p * 128 + 4 * lane < a.rot_dim) turn[p] = load_turn<FAST>(a, turn_pos, p * 128 + 4 * lane);
@@ -367,7 +367,7 @@ template <int NB, bool FAST> __global__ void __launch_bounds__(kStreamWarps * 32
     const float nan = __int_as_float(0x7fffffff), row[4] = {nan, nan, nan, nan};
     for (int job = lost; job < last; ++job) {
         const int t = a.by_groups.div(job), from = a.by_groups.mod(job, t) * kStreamHeads;
-        Place where = place_of(a, a.pos[t], a.seq[t], a.turn_pos[t]);
+        Place where = place_of<AT>(a, a.pos[t], a.seq[t], AT ? a.turn_pos[t] : a.pos[t]);
         place_check(a, where, lane);
         const Rows dst = rows_of<NB>(a, where, t);
         for (int head = from; head < min(from + kStreamHeads, heads); ++head)
@@ -375,7 +375,7 @@ template <int NB, bool FAST> __global__ void __launch_bounds__(kStreamWarps * 32
     }
 }
 
-template <int NB, bool FAST> cudaError_t launch_append_as(AppendArgs a, cudaStream_t st) {
+template <int NB, bool FAST, bool AT> cudaError_t launch_append_as(AppendArgs a, cudaStream_t st) {
     const int heads = a.n_q_heads + 2 * a.c.n_kv_heads;
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -385,7 +385,7 @@ template <int NB, bool FAST> cudaError_t launch_append_as(AppendArgs a, cudaStre
     const int64_t pairs = static_cast<int64_t>(a.n_tok) * heads;
     if (pairs <= static_cast<int64_t>(sms) * 64) {
         a.by_groups = FastDiv::of(heads);
-        return launch_block_op(kv_append_kernel<NB, FAST>, dim3(static_cast<unsigned>((pairs + kAppendWarps - 1) / kAppendWarps)),
+        return launch_block_op(kv_append_kernel<NB, FAST, AT>, dim3(static_cast<unsigned>((pairs + kAppendWarps - 1) / kAppendWarps)),
                                dim3(kAppendWarps * 32), 0, st, a);
     }
     const int groups = (heads + kStreamHeads - 1) / kStreamHeads;
@@ -393,12 +393,14 @@ template <int NB, bool FAST> cudaError_t launch_append_as(AppendArgs a, cudaStre
     const int n_jobs = a.n_tok * groups;
     constexpr size_t kSmem = 256 + static_cast<size_t>(kStreamWarps) * kStreamSlots * kStreamHeads * NB * kQK * 4;
     constexpr int kCtas = kSmem <= 55 * 1024 ? 3 : 2;  // per SM: as many as fit
-    e = smem_limit_raised<&kv_append_stream_kernel<NB, FAST>>();
+    e = smem_limit_raised<&kv_append_stream_kernel<NB, FAST, AT>>();
     if (e != cudaSuccess) return e;
-    return launch_block_op(kv_append_stream_kernel<NB, FAST>, dim3(sms * kCtas), dim3(kStreamWarps * 32), kSmem, st, a, n_jobs);
+    return launch_block_op(kv_append_stream_kernel<NB, FAST, AT>, dim3(sms * kCtas), dim3(kStreamWarps * 32), kSmem, st, a, n_jobs);
 }
 template <int NB> cudaError_t launch_append(const AppendArgs &a, cudaStream_t st) {
-    return a.rot_dim % (a.halves ? 8 : 4) == 0 ? launch_append_as<NB, true>(a, st) : launch_append_as<NB, false>(a, st);
+    const bool fast = a.rot_dim % (a.halves ? 8 : 4) == 0;
+    if (a.turn_pos) return fast ? launch_append_as<NB, true, true>(a, st) : launch_append_as<NB, false, true>(a, st);
+    return fast ? launch_append_as<NB, true, false>(a, st) : launch_append_as<NB, false, false>(a, st);
 }
 
 zdmmv_status append_call(const zdmmv_kv_cache *cache, const zdmmv_kv_append_args *args, const int32_t *rope_pos,
@@ -427,7 +429,7 @@ zdmmv_status append_call(const zdmmv_kv_cache *cache, const zdmmv_kv_append_args
     a.head_bytes = cache->page_tokens / kKvSlab * 18 * cache->head_dim;
     a.k = g.k; a.v = g.v; a.q = g.q;
     a.seq = g.seq; a.pos = g.pos; a.rope = g.rope;
-    a.turn_pos = rope_pos ? rope_pos : g.pos;
+    a.turn_pos = rope_pos;
     a.q_out = g.q_out;
     a.k_val = static_cast<__half *>(g.k_val);
     a.v_val = static_cast<__half *>(g.v_val);

@@ -104,7 +104,7 @@ def _evict(**k):
 
 
 @pytest.mark.parametrize("code, change", [
-    (2, dict(max_kv_len=-1)), (2, dict(max_kv_len=0x7fffffff, sums_stride=1 << 40)), (2, dict(budget=0)), (2, dict(budget=129, sums_out_stride=200)),
+    (2, dict(max_kv_len=-1)), (2, dict(max_kv_len=0x7fff0001, sums_stride=1 << 40)), (2, dict(budget=0)), (2, dict(budget=129, sums_out_stride=200)),
     (2, dict(sinks=-1)), (2, dict(recent=-1)), (2, dict(sinks=49)), (2, dict(sinks=0x7fffffff, recent=0x7fffffff)),
     (2, dict(sums_stride=99)), (2, dict(sums_out_stride=63)), (2, dict(sums_out=FAKE)),
     (1, dict(kv_len=None)), (1, dict(sums=None)), (1, dict(index=None)),
