@@ -525,14 +525,18 @@ template <int NB> __global__ void __launch_bounds__(kWeightThreads, TallGeom<NB>
     {
         const int slab = chunk * kSlabs + warp;
         const uint8_t *src = nullptr;
-        if (slab * kKvSlab < r.len) {
+        bool wrong = false;
+        if (slab >= r.slab0 && slab < r.slab0 + r.slabs) {  // of the others, which every column masks, the pages may be gone
             const int slot = a.by_page_tiles.div(slab), page = a.c.table[static_cast<int64_t>(seq) * a.c.max_pages + slot];
             if (page >= 0 && page < a.c.n_pages)
                 src = a.c.pages + page * a.c.page_bytes +
                       (static_cast<int64_t>(kvh) * static_cast<int>(a.by_page_tiles.d) + a.by_page_tiles.mod(slab, slot)) * G::kTileBytes;
-            else if (lane == 0 && a.status) *a.status = 1;
+            else wrong = true;
         }
-        if (lane == 0) sh_skip[warp] = src == nullptr;
+        if (lane == 0) {
+            sh_skip[warp] = wrong;
+            if (wrong && a.status) *a.status = 1;
+        }
         uint32_t code[2][NB], scale[2][NB], any = 0;
 #pragma unroll
         for (int u = 0; u < 2; ++u) {

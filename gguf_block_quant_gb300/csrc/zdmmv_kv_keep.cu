@@ -457,6 +457,7 @@ zdmmv_status zdmmv_kv_evict_q4_0(const zdmmv_kv_cache *from, const zdmmv_kv_cach
     if (kv_misaligned(g.kv_len, 4) || kv_misaligned(g.sums, 4) || kv_misaligned(g.index, 4) || kv_misaligned(g.sums_out, 4) ||
         kv_misaligned(g.len_out, 4) || kv_misaligned(g.status_dev, 4))
         return ZDMMV_ERR_ALIGN;
+    if (from->pages == to->pages && from->page_table == to->page_table) return ZDMMV_ERR_SHAPE;
     a.by_heads = FastDiv::of(from->n_kv_heads);
     a.from_page_tiles = FastDiv::of(from->page_tokens / kKvSlab);
     a.to_page_tiles = FastDiv::of(to->page_tokens / kKvSlab);

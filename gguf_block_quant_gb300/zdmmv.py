@@ -603,19 +603,21 @@ def _seen(seen, n_tok: int) -> tuple[int, int]:
     """(data pointer, words of a row) of a tree's bits; (0, 0) for none."""
     if seen is None:
         return 0, 0
-    if seen.dim() != 2 or seen.shape[0] < n_tok:
+    shape = seen.shape
+    if len(shape) != 2 or shape[0] < n_tok:
         _bad(f"seen: expected int32 [n_tok][words] with {n_tok} rows")
-    return _whole(seen, _I32, 0, "seen"), seen.shape[1]
+    return _whole(seen, _I32, 0, "seen"), shape[1]
 
 
 def _per_head(t: torch.Tensor, cache: KVCache, n: int, what: str) -> tuple[int, int]:
     """(data pointer, floats between kv heads) of a float32 CUDA tensor [n_seq][n_kv_heads][n or more]."""
-    if t.dtype is not _F32 or not t.is_cuda or t.dim() != 3 or t.shape[0] != cache.n_seq or t.shape[1] != cache.n_kv_heads or t.shape[2] < n:
-        _bad(f"{what}: expected float32 CUDA [{cache.n_seq}][{cache.n_kv_heads}][{n} or more]")
+    shape, n_seq, kv = t.shape, cache.n_seq, cache.n_kv_heads
+    if t.dtype is not _F32 or not t.is_cuda or len(shape) != 3 or shape[0] != n_seq or shape[1] != kv or shape[2] < n:
+        _bad(f"{what}: expected float32 CUDA [{n_seq}][{kv}][{n} or more]")
     s0, s1, s2 = t.stride()
-    if cache.n_kv_heads == 1:
-        s1 = s0 if cache.n_seq > 1 else t.shape[2]
-    if s2 != 1 and t.shape[2] > 1 or cache.n_seq > 1 and s0 != s1 * cache.n_kv_heads:
+    if kv == 1:
+        s1 = s0 if n_seq > 1 else shape[2]
+    if s2 != 1 and shape[2] > 1 or n_seq > 1 and s0 != s1 * kv:
         _bad(f"{what}: kv heads have to lie evenly apart, their values side by side")
     return t.data_ptr(), s1
 
@@ -677,13 +679,13 @@ def kv_accept_q4_0(cache: KVCache, base, path, n_path, sums=None, len_out=None, 
     """The accepted path of a drafted tree: of the tokens behind the first base[s] of sequence s, number path[s][j] moves to
     position base[s] + j (j < n_path[s], path rising), and so do sums (fp32 [n_seq][n_kv_heads][tokens], nullable).
     Returns len_out, int32 [n_seq]: the new lengths."""
-    n_seq = cache.n_seq
-    if path.dim() != 2 or path.shape[0] != n_seq:
+    n_seq, shape = cache.n_seq, path.shape
+    if len(shape) != 2 or shape[0] != n_seq:
         _bad("kv_accept_q4_0: path must be int32 [n_seq][max_path]")
     if len_out is None:
         len_out = _make((n_seq,), _I32, path.device, stream)
     args = _KV_ACCEPT_ARGS.pack(_whole(base, _I32, n_seq, "base"), _whole(path, _I32, 0, "path"), _whole(n_path, _I32, n_seq, "n_path"),
                                 _whole(len_out, _I32, n_seq, "len_out"), 0 if status is None else _whole(status, _I32, 1, "status"),
-                                *((0, 0, 0) if sums is None else (*_per_head(sums, cache, 0, "sums"), sums.shape[2])), path.shape[1])
+                                *((0, 0, 0) if sums is None else (*_per_head(sums, cache, 0, "sums"), sums.shape[2])), shape[1])
     _enter("zdmmv_kv_accept_q4_0", cache.c, args, _raw_stream(stream))
     return len_out

@@ -734,9 +734,10 @@ zdmmv_status zdmmv_attn_tree_q4_0(const zdmmv_kv_cache *cache, const zdmmv_attn_
  * zdmmv_attn_q4_0, or that of `seen`), without the first part for the new tokens
  * themselves (t >= kv_len - n): what stood there was of tokens that are gone. lse
  * is what zdmmv_attn_tree_q4_0 wrote for the same rows, so a row's weights add up
- * to one. Entries at and past kv_len are left as they are. Sums and scores are
- * fp32 (scores as zdmmv_attn_q4_0 forms them; keep * before is one fma with the
- * sum of the rest), in an order that does not depend on other sequences. */
+ * to one. Pages of which no row sees a token are not looked at. Entries at and
+ * past kv_len are left as they are. Sums and scores are fp32 (scores as
+ * zdmmv_attn_q4_0 forms them; keep * before is one fma with the sum of the rest),
+ * in an order that goes by the shapes and bounds of the call alone. */
 typedef struct {
     const float *q;          /* device fp32 [n_tok][n_q_heads][head_dim], tokens q_stride apart (rotated) */
     const int32_t *q_start;  /* device int32 [n_seq+1], rising from 0 to n_tok */
@@ -803,7 +804,7 @@ typedef struct {
  * bad: its index is all -1, its sums_out all 0, no page of it is written. A token
  * of a page outside 0..n_pages-1 of `from` becomes NaN; a tile of such a page of
  * `to` is not written. Two launches.
- * Errors: ERR_NULL, ERR_SHAPE (sums_out as sums itself too), ERR_ALIGN, ERR_CUDA. */
+ * Errors: ERR_NULL, ERR_SHAPE (sums_out as sums itself and `to` as `from` too), ERR_ALIGN, ERR_CUDA. */
 zdmmv_status zdmmv_kv_evict_q4_0(const zdmmv_kv_cache *from, const zdmmv_kv_cache *to, const zdmmv_kv_evict_args *args,
                                  zdmmv_stream_t stream);
 

@@ -145,6 +145,29 @@ def test_weights_bad_sequences_and_pages():
     assert Z.device_status() == 0
 
 
+@pytest.mark.parametrize("group, new", [(4, 1), (4, 3), (8, 20)])
+def test_pages_before_the_window_may_be_gone(group, new):
+    """A windowed sequence's first pages have no number any more: neither the attention nor the weights look at them (the first
+    page is in a tile of 128 tokens with some that are seen), and their tokens' sums are kept."""
+    rng = np.random.default_rng(new)
+    page, dim, n, window = 16, 128, 700, 230
+    cache, pages, table = random_cache(rng, [n], page, 1, dim)
+    masks = [T.tree_mask(new, rng)]
+    q, starts, ld = dev(rng.standard_normal((new, group, dim)).astype(np.float32)), dev(np.array([0, new], np.int32)), dev(np.array([n], np.int32))
+    seen, had = dev(T.pack(masks, 1)), torch.rand(1, 1, n, device="cuda")
+    gone = table.copy()
+    gone[0, :(n - new - window) // page] = -1
+    results = []
+    for t in (table, gone):
+        c, lse, status = Z.KVCache(cache.pages, page, 1, dim, dev(t)), torch.empty(new, group, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+        out = Z.attn_tree_q4_0(c, q, starts, ld, new, n, seen=seen, lse=lse, window=window, status=status)
+        w = Z.attn_weights_q4_0(c, q, starts, ld, lse, new, n, seen=seen, window=window, sums=had, keep=0.5, status=status)
+        assert status.item() == 0
+        results.append((out, lse, w))
+    assert all(torch.equal(a, b) for a, b in zip(*results))
+    assert torch.equal(w[0, 0, :n - new - window], 0.5 * had[0, 0, :n - new - window])
+
+
 # ------------------------------------------------------------------ eviction
 def gathered(pages, page, heads, dim, table, index, to_pages, to_page, to_table):
     """The bytes of `to` after the move, by plain numpy."""

@@ -122,6 +122,11 @@ def test_evict_checks_both_caches(L, code, change):  # noqa: F811
     assert call(ctypes.byref(_cache(**change)), ctypes.byref(_cache()), ctypes.byref(_evict()), None) == code
 
 
+def test_evict_refuses_the_cache_itself(L):  # noqa: F811
+    c, again = _cache(), _cache()
+    assert L.zdmmv_kv_evict_q4_0(ctypes.byref(c), ctypes.byref(again), ctypes.byref(_evict()), None) == 2
+
+
 def _accept(**k):
     return _KvAcceptArgs(**{**dict(base=FAKE, path=FAKE, n_path=FAKE, len_out=FAKE, status_dev=FAKE, sums=FAKE, sums_stride=128, sums_len=100, max_path=8), **k})
 
@@ -184,3 +189,28 @@ def test_attentions_workspace_is_one_for_trees(L, head_dim):  # noqa: F811
                      n_tok=new, workspace=FAKE if size else None, workspace_bytes=size)
         got = L.zdmmv_attn_tree_q4_0(ctypes.byref(c), ctypes.byref(args), ctypes.byref(_tree(seen_words=10)), None)
         assert got not in (1, 2, 6), (n_seq, heads, group, new, most, window, got)
+
+
+def test_binding_refuses_bad_sums():
+    """[n_seq][n_kv_heads][tokens] with kv heads evenly apart; views of a wider buffer pass."""
+    class Cache:
+        n_seq, n_kv_heads = 2, 3
+
+    class Tensor:  # a CUDA tensor's looks
+        dtype, is_cuda = torch.float32, True
+
+        def __init__(self, t):
+            self.shape, self.stride, self.data_ptr = t.shape, t.stride, lambda: 256
+    wide = torch.zeros(2, 3, 50)
+    assert Z._per_head(Tensor(wide), Cache, 50, "x") == (256, 50)
+    assert Z._per_head(Tensor(wide[:, :, :40]), Cache, 40, "x") == (256, 50)
+    for bad in (wide[:1], wide[:, :2], wide[:, :, :30], torch.zeros(2, 4, 50)[:, :3], wide.transpose(0, 1), torch.zeros(2, 3, 100)[:, :, ::2],
+                wide[0], torch.zeros(150)):
+        with pytest.raises(ValueError):
+            Z._per_head(Tensor(bad), Cache, 40, "x")
+    Cache.n_seq, Cache.n_kv_heads = 1, 1
+    assert Z._per_head(Tensor(torch.zeros(1, 1, 7)), Cache, 7, "x") == (256, 7)
+    Cache.n_seq = 2
+    assert Z._per_head(Tensor(torch.zeros(2, 9, 7)[:, :1]), Cache, 7, "x") == (256, 63)
+    with pytest.raises(ValueError):
+        Z._per_head(torch.zeros(2, 1, 7), Cache, 7, "x")  # a host tensor
