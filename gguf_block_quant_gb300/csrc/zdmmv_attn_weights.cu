@@ -98,16 +98,17 @@ template <int N> __device__ __forceinline__ void cp_async_wait() { asm volatile(
 // grid that fills the device takes an equal stretch, whatever the lengths. A warp keeps the next pairs' keys, and their tokens'
 // earlier sums, on their way into its own ring in shared memory; a pair's 32 sums end up one in each lane.
 // ONE: up to four columns, whose parts of q stay in registers.
-// One token of 32 heads over 130975 tokens of 8 kv heads of 128: 21.5 us, 3.9 TB/s, 59% of the copy rate; 48 sequences of up to
-// 16384 46.0 us, 3.7 TB/s. Bound by issue (61% active; 244 instructions a tile, 72 of them the codes' conversion) and the start:
-// lengths, pages, the first keys and q are four latencies one after another, of some 4 us. Measured before, over 130975: loads
-// a tile ahead into registers, the earlier sums read where they are used, 33.2; rings of four single tiles 28.8.
+// One token of 32 heads over 130975 tokens of 8 kv heads of 128: 19.9 us, 4.2 TB/s, 63% of the copy rate; 48 sequences of up to
+// 16384 44.8 us, 3.8 TB/s. Bound by issue (some 240 instructions a tile, 72 of them the codes' conversion) and the start:
+// lengths, pages, the first keys and q are four latencies one after another, of some 4 us. Measured, over 130975: loads a tile
+// ahead into registers, the earlier sums read where they are used, 33.2; rings of four single tiles 28.8; three CTAs an SM, with
+// 80 registers a thread, 21.6; four places a ring 19.8 (but 45.2), five 20.1; q asked for before the pages, which it costs spills, 32.6.
 constexpr int kWeightStages = 3;
 template <int NB> constexpr int kPairBytes = 2 * 9 * NB * kQK + 2 * kKvSlab * 4;
 template <int NB> constexpr size_t kWeightRing = static_cast<size_t>(kWeightWarps) * kWeightStages * kPairBytes<NB>;
-__host__ __device__ constexpr int weight_ctas(int nb, bool one) { return one && nb <= 4 ? 3 : 2; }
+constexpr int kWeightCtas = 2;  // an SM
 
-template <int NB, bool ONE> __global__ void __launch_bounds__(kWeightThreads, weight_ctas(NB, ONE)) attn_weights_kernel(WeightArgs w) {
+template <int NB, bool ONE> __global__ void __launch_bounds__(kWeightThreads, kWeightCtas) attn_weights_kernel(WeightArgs w) {
     using G = KvGeom<NB>;
     const AttnArgs &a = w.a;
     constexpr int kKeyBytes = 9 * G::kDim;
@@ -718,7 +719,7 @@ template <int NB, bool ONE> cudaError_t launch_few(const WeightArgs &w, int64_t 
     const cudaError_t e = smem_limit_raised<&attn_weights_kernel<NB, ONE>>();
     if (e != cudaSuccess) return e;
     constexpr int kStep = kStepTiles * kKvSlab;
-    const int64_t steps = items * ((w.a.max_kv_len + kStep - 1) / kStep), ctas = static_cast<int64_t>(weight_ctas(NB, ONE)) * sms;
+    const int64_t steps = items * ((w.a.max_kv_len + kStep - 1) / kStep), ctas = static_cast<int64_t>(kWeightCtas) * sms;
     const size_t smem = kWeightRing<NB> + static_cast<size_t>((columns + 3) / 4) * 2 * NB * 256;
     return launch_block_op(&attn_weights_kernel<NB, ONE>, dim3(static_cast<unsigned>(std::min(steps, ctas))), dim3(kWeightThreads), smem, st, w);
 }
