@@ -98,11 +98,11 @@ template <int N> __device__ __forceinline__ void cp_async_wait() { asm volatile(
 // grid that fills the device takes an equal stretch, whatever the lengths. A warp keeps the next pairs' keys, and their tokens'
 // earlier sums, on their way into its own ring in shared memory; a pair's 32 sums end up one in each lane.
 // ONE: up to four columns, whose parts of q stay in registers.
-// One token of 32 heads over 130975 tokens of 8 kv heads of 128: 19.9 us, 4.2 TB/s, 63% of the copy rate; 48 sequences of up to
-// 16384 44.8 us, 3.8 TB/s. Bound by issue (some 240 instructions a tile, 72 of them the codes' conversion) and the start:
+// One token of 32 heads over 130975 tokens of 8 kv heads of 128: 19.7 us, 4.3 TB/s, 64% of the copy rate; 48 sequences of up to
+// 16384 44.6 us, 3.8 TB/s. Bound by issue (58% active; 205 instructions a tile, 72 of them the codes' conversion) and the start:
 // lengths, pages, the first keys and q are four latencies one after another, of some 4 us. Measured, over 130975: loads a tile
 // ahead into registers, the earlier sums read where they are used, 33.2; rings of four single tiles 28.8; three CTAs an SM, with
-// 80 registers a thread, 21.6; four places a ring 19.8 (but 45.2), five 20.1; q asked for before the pages, which it costs spills, 32.6.
+// 80 registers a thread, 21.6; four places a ring 19.8 (and 45.2), five 20.1; q asked for before the pages, which it costs spills, 32.6.
 constexpr int kWeightStages = 3;
 template <int NB> constexpr int kPairBytes = 2 * 9 * NB * kQK + 2 * kKvSlab * 4;
 template <int NB> constexpr size_t kWeightRing = static_cast<size_t>(kWeightWarps) * kWeightStages * kPairBytes<NB>;
