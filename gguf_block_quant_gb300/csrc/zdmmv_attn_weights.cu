@@ -481,7 +481,7 @@ template <int NB> __global__ void __launch_bounds__(kWeightThreads, TallGeom<NB>
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int sh_skip[kWeightWarps], sh_dead;
     __shared__ float sh_sum[kTallTokens];
-    __shared__ __align__(8) uint64_t bar[kTallSlots + 2];  // by slot: its block of q has come; by block % 2: its products are done
+    __shared__ __align__(8) uint64_t bar[kTallSlots + 3];  // by slot: its block of q has come; by block % 2: its products are done; all are
     __shared__ uint32_t sh_tm;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, half = warp >> 2;
     block_op_release();
@@ -514,7 +514,7 @@ template <int NB> __global__ void __launch_bounds__(kWeightThreads, TallGeom<NB>
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
     if (tid == 0) {
-        for (int k = 0; k < kTallSlots + 2; ++k) mbar_init(&bar[k], 1);
+        for (int k = 0; k < kTallSlots + 3; ++k) mbar_init(&bar[k], 1);
         fence_barrier_init();
         sh_dead = 0;
     }
@@ -681,9 +681,14 @@ template <int NB> __global__ void __launch_bounds__(kWeightThreads, TallGeom<NB>
         tm_after_sync();
         if (tid == 0 && block > 0 && asked < blocks && !dead) ask(asked++);
     }
-    // leave only when the copies have landed (after a wait that gave up: as far as they will)
-    if (dead && tid == 0)
-        for (int k = max(0, asked - kTallSlots); k < asked; ++k) (void)mbar_wait(&bar[k % kTallSlots], k / kTallSlots & 1);
+    // after a wait that gave up: leave only when the products and the copies that were started are done, as far as they will be
+    if (warp == 0 && __any_sync(0xffffffffu, dead)) {
+        if (one_lane()) tm_commit(&bar[kTallSlots + 2]);
+        (void)mbar_wait(&bar[kTallSlots + 2], 0);
+        if (tid == 0)
+            for (int k = max(0, asked - kTallSlots); k < asked; ++k) (void)mbar_wait(&bar[k % kTallSlots], k / kTallSlots & 1);
+        __syncwarp();
+    }
     if (dead) sh_dead = 1;
     const float2 both = f2_parts(total2);
     if (half == 1) sh_sum[row] = both.x + both.y;
