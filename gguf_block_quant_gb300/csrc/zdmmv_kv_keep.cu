@@ -22,8 +22,7 @@ struct KeepArgs {
     int32_t *len_out, *status;
     int64_t sums_stride, sums_out_stride;
     int32_t max_kv_len, budget, sinks, recent;
-    int32_t n_tiles;  // of the budget
-    int32_t held;     // sums of a CTA that its shared memory holds, as keys
+    int32_t held;  // sums of a CTA that its shared memory holds, as keys
 };
 
 // A sum as a whole number that rises with it: -0 is 0, a NaN is below all.
@@ -465,7 +464,6 @@ zdmmv_status zdmmv_kv_evict_q4_0(const zdmmv_kv_cache *from, const zdmmv_kv_cach
     a.kv_len = g.kv_len; a.sums = g.sums; a.index = g.index; a.sums_out = g.sums_out; a.len_out = g.len_out; a.status = g.status_dev;
     a.sums_stride = g.sums_stride; a.sums_out_stride = g.sums_out_stride;
     a.max_kv_len = g.max_kv_len; a.budget = g.budget; a.sinks = g.sinks; a.recent = g.recent;
-    a.n_tiles = static_cast<int32_t>(tiles);
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e = launch_pick(a, items, s);
     if (e != cudaSuccess) return ZDMMV_ERR_CUDA;

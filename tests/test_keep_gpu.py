@@ -636,3 +636,77 @@ def test_weights_of_a_prompts_chunk():
 def test_weights_of_a_middling_number_of_columns(heads, group, dim, new, length):
     """25 to 64 columns over more tokens than the tall kernel's CTAs take at once: sixteen groups of four at most."""
     run_weights(np.random.default_rng(dim), [length, 40], [new, new - 3], 64, heads, group, dim, masks="tree")
+
+
+def test_pages_past_32_bits():
+    """A cache of more than 2^32 bytes whose sequences lie in its last pages: what the same pages give at its start."""
+    rng = np.random.default_rng(3)
+    page, heads, dim, lens = 1024, 8, 256, [1500, 100]
+    small, pages, table = random_cache(rng, lens, page, heads, dim, spare=0)
+    per = Z.kv_page_bytes(page, heads, dim)
+    n_pages, far = len(pages) // per, (1 << 32) // per + 3
+    big = torch.empty((far + n_pages + 4) * per, dtype=torch.uint8, device="cuda")
+    big[far * per:(far + n_pages) * per].copy_(small.pages)
+    there = Z.KVCache(big, page, heads, dim, dev(np.where(table >= 0, table + far, -1).astype(np.int32)))
+    i32 = lambda v: dev(np.array(v, np.int32))  # noqa: E731
+    n = 5
+    q, starts, ld = dev(rng.standard_normal((2 * n, 2 * heads, dim)).astype(np.float32)), i32([0, n, 2 * n]), i32(lens)
+    seen, had = dev(T.pack([T.tree_mask(n, rng) for _ in lens], 1)), torch.rand(2, heads, 1500, device="cuda")
+    base, path, count = i32([v - n for v in lens]), i32([[0, 2, 4], [1, 3, 0]]), i32([3, 2])
+    results = []
+    for cache, buffer, first in ((small, torch.zeros(2 * per, dtype=torch.uint8, device="cuda"), 0), (there, big, far + n_pages)):
+        buffer[first * per:(first + 2) * per] = 0
+        to = Z.KVCache(buffer, page, heads, dim, i32([[first + 1], [first]]))
+        lse = torch.empty(2 * n, 2 * heads, device="cuda")
+        out = Z.attn_tree_q4_0(cache, q, starts, ld, n, 1500, seen=seen, lse=lse)
+        w = Z.attn_weights_q4_0(cache, q, starts, ld, lse, n, 1500, seen=seen, sums=had)
+        new = Z.kv_accept_q4_0(cache, base, path, count, sums=w)
+        index = Z.kv_evict_q4_0(cache, to, new, w, 700, 1500, sinks=2, recent=9)
+        held = cache.pages if cache is small else big[far * per:(far + n_pages) * per]
+        results.append((out, lse, w, new, index, held.clone(), buffer[first * per:(first + 2) * per].clone()))
+    assert all(torch.equal(a, b) for a, b in zip(*results))
+    assert Z.device_status() == 0
+
+
+def test_several_streams_at_once():
+    """The same chain of calls on streams of their own, with buffers of their own, as alone."""
+    rng = np.random.default_rng(6)
+    jobs = []
+    for dim, heads, group, n, length in ((128, 8, 4, 16, 3000), (256, 2, 8, 12, 1500), (64, 4, 1, 1, 4000)):
+        cache, _, _ = random_cache(rng, [length, length // 2], 64, heads, dim)
+        e = lambda *s, t=torch.float32: torch.zeros(*s, dtype=t, device="cuda")  # noqa: E731
+        q = dev(rng.standard_normal((2 * n, heads * group, dim)).astype(np.float32))
+        size = Z.attn_weights_q4_0_workspace_bytes(cache, heads * group, 2 * n, n)
+        jobs.append(dict(cache=cache, n=n, length=length, q=q, starts=dev(np.array([0, n, 2 * n], np.int32)),
+                         ld=dev(np.array([length, length // 2], np.int32)), seen=dev(T.pack([T.tree_mask(n, rng) for _ in range(2)], 1)),
+                         had=torch.rand(2, heads, length, device="cuda"), lse=e(2 * n, heads * group), out=e(*q.shape), sums=e(2, heads, length),
+                         index=e(2, heads, 300, t=torch.int32), kept=e(2, heads, 300), ws=Z.attn_q4_0_workspace(cache, heads * group, n, length),
+                         ww=e(max(16, size), t=torch.uint8), to=make_cache(10, 64, heads, dim, np.arange(10).reshape(2, 5), fill=0)[0]))
+
+    def chain(j, stream):
+        for _ in range(8):
+            Z.attn_tree_q4_0(j["cache"], j["q"], j["starts"], j["ld"], j["n"], j["length"], seen=j["seen"], lse=j["lse"], out=j["out"],
+                             workspace=j["ws"], stream=stream)
+            Z.attn_weights_q4_0(j["cache"], j["q"], j["starts"], j["ld"], j["lse"], j["n"], j["length"], seen=j["seen"], sums=j["had"],
+                                out=j["sums"], workspace=j["ww"], stream=stream)
+            Z.kv_evict_q4_0(j["cache"], j["to"], j["ld"], j["sums"], 300, j["length"], sinks=3, recent=50, index=j["index"],
+                            sums_out=j["kept"], stream=stream)
+
+    names = ("lse", "out", "sums", "index", "kept")
+    alone = []
+    for j in jobs:
+        chain(j, torch.cuda.current_stream())
+        torch.cuda.synchronize()
+        alone.append([j[k].clone() for k in names] + [j["to"].pages.clone()])
+    streams = [torch.cuda.Stream() for _ in jobs]
+    for _ in range(4):
+        for j in jobs:
+            for k in names:
+                j[k].zero_()
+        torch.cuda.synchronize()
+        for j, stream in zip(jobs, streams):
+            chain(j, stream)
+        torch.cuda.synchronize()
+        for j, want in zip(jobs, alone):
+            assert all(torch.equal(a, b) for a, b in zip([j[k] for k in names] + [j["to"].pages], want))
+    assert Z.device_status() == 0
