@@ -33,16 +33,18 @@ __device__ __forceinline__ uint32_t sum_key(float x) {
 }
 
 // ------------------------------------------------------------------ which tokens stay
-// A cluster of CTAs for a kv head of a sequence (one CTA for short ones), each with an equal stretch of the tokens between the
+// A cluster of CTAs for a kv head of a sequence (one CTA for up to 20480 tokens), each with an equal stretch of the tokens between the
 // first and the latest ones, whose sums it reads once into shared memory. The smallest sum that stays is found digit by digit,
 // 11 bits at a time from the top: every CTA counts its sums by digit, and adds up the cluster's counts. Then each CTA knows how
 // many tokens stay before its own, and writes its own in their order: of sums equal to the smallest, the first ones.
 // 32 kv heads of up to 65536 tokens: 16 to 20 us, of which the sums' loads take 3, each of the three counts 3 (its additions in
 // shared memory, the cluster's barrier, the reading of four CTAs' counts), the rising places 3. Bound by these steps' latencies.
 constexpr int kPickThreads = 1024, kPickWarps = kPickThreads / 32, kDigit = 2048, kPickCluster = 8;
-constexpr int kPickOne = 8192;      // tokens up to which one CTA does it
+// Tokens up to which a CTA more costs more than it saves, the cluster's barriers above all (8 kv heads, one, two, four and eight
+// CTAs each: 16000 tokens 12.3 12.9 13.5 17.0 us with the move of 256, 32000 17.5 15.2 14.6 17.5, 131072 132 60 22.2 20.9).
+constexpr int kPickEach = 20 * 1024;
 constexpr int kPickMost = 0x7fff0000;  // so that a warp's step past the last sum is a number too
-constexpr int kPickHeld = 48 * 1024;  // most sums that a CTA holds; those beyond it are read again
+constexpr int kPickHeld = 48 * 1024;   // most sums that a CTA holds; those beyond it are read again (65536 by one CTA 56 us, by two 20)
 
 template <bool CLUSTER> __global__ void __launch_bounds__(kPickThreads) kv_pick_kernel(KeepArgs a) {
     extern __shared__ uint32_t held[];
@@ -402,9 +404,10 @@ cudaError_t launch_pick(KeepArgs a, int64_t items, cudaStream_t st) {
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
-    // a CTA an SM (its registers), so clusters as large as fill the device once
+    // a CTA an SM, so clusters of no more than fill the device once, unless their sums would be read again (32 kv heads of 65536
+    // tokens: eight CTAs each 33.6 us, four 18.0)
     int ranks = 1;
-    while (a.max_kv_len > kPickOne && ranks < kPickCluster && items * ranks * 2 <= sms) ranks *= 2;
+    while (ranks < kPickCluster && a.max_kv_len / ranks > kPickEach && (items * ranks * 2 <= sms || a.max_kv_len / ranks > kPickHeld)) ranks *= 2;
     a.held = std::min(a.max_kv_len / ranks + 1, kPickHeld);
     const size_t smem = static_cast<size_t>(a.held) * 4;
     if (ranks == 1) {

@@ -240,7 +240,8 @@ def test_evict_picks(kind, lens, budget, sinks, recent):
 
 
 @pytest.mark.parametrize("kind", ["spread", "ties", "equal"])
-@pytest.mark.parametrize("lens, budget", [([8193, 8192, 100], 4000), ([70001, 33333], 16000), ([300007], 150001)])
+@pytest.mark.parametrize("lens, budget", [([8193, 8192, 100], 4000), ([20481, 20480], 9000), ([50001], 1500), ([70001, 33333], 16000), ([180000, 9], 2000),
+                                          ([300007], 150001), ([420003], 1017)])
 def test_evict_long(kind, lens, budget):
     """Clusters of CTAs a kv head; sums past what their shared memory holds."""
     run_evict(np.random.default_rng(budget), lens, budget, 16, 1000, 1024, 1024, 1, 64, kind=kind, moved=False)
