@@ -37,7 +37,7 @@ __device__ __forceinline__ uint32_t sum_key(float x) {
 // first and the latest ones, whose sums it reads once into shared memory. The smallest sum that stays is found digit by digit,
 // 11 bits at a time from the top: every CTA counts its sums by digit, and adds up the cluster's counts. Then each CTA knows how
 // many tokens stay before its own, and writes its own in their order: of sums equal to the smallest, the first ones.
-// 32 kv heads of up to 65536 tokens: 16 to 20 us, of which the sums' loads take 3, each of the three counts 3 (its additions in
+// 32 kv heads of up to 65536 tokens: 16 to 20 us, of which the sums' loads take 3, each of the two or three counts 3 (its additions in
 // shared memory, the cluster's barrier, the reading of four CTAs' counts), the rising places 3. Bound by these steps' latencies.
 constexpr int kPickThreads = 1024, kPickWarps = kPickThreads / 32, kDigit = 2048, kPickCluster = 8;
 // Tokens up to which a CTA more costs more than it saves, the cluster's barriers above all (8 kv heads, one, two, four and eight
@@ -50,7 +50,7 @@ template <bool CLUSTER> __global__ void __launch_bounds__(kPickThreads) kv_pick_
     extern __shared__ uint32_t held[];
     __shared__ __align__(16) uint32_t sh_count[3][kDigit];  // of this CTA's sums, by digit
     __shared__ uint32_t sh_scan[kPickWarps], sh_above[kPickWarps], sh_equal[kPickWarps];
-    __shared__ uint32_t sh_found, sh_want, sh_mine[2];
+    __shared__ uint32_t sh_found, sh_want, sh_have, sh_mine[2];
     cg::cluster_group cluster = cg::this_cluster();
     const int ranks = CLUSTER ? static_cast<int>(cluster.num_blocks()) : 1, rank = CLUSTER ? static_cast<int>(cluster.block_rank()) : 0;
     const auto sync_all = [&] {
@@ -135,10 +135,16 @@ template <bool CLUSTER> __global__ void __launch_bounds__(kPickThreads) kv_pick_
             const bool second = want > over + c0;
             sh_found = static_cast<uint32_t>(kDigit - 1 - 2 * tid - (second ? 1 : 0));
             sh_want = want - over - (second ? c0 : 0);
+            sh_have = second ? c1 : c0;
         }
         __syncthreads();
         known |= sh_found << shift;
         want = sh_want;
+        if (want == sh_have) {  // all with these digits stay (mostly one after two counts): all above the number before
+            --known;            // no sum's digits are all 0
+            want = 0;
+            break;
+        }
     }
     // `want` of the sums equal to `known` stay, and all above it: a warp's stretch of the CTA's
     const int per_warp = (mine + 32 * kPickWarps - 1) / (32 * kPickWarps) * 32;
