@@ -405,10 +405,15 @@ _F32, _F16, _U8, _I32 = torch.float32, torch.float16, torch.uint8, torch.int32
 _entries: dict = {}
 
 
+def _entry(name: str):
+    fn = _entries.get(name)
+    return _entries.setdefault(name, getattr(lib(), name)) if fn is None else fn
+
+
 def _enter(name: str, *args):
     fn = _entries.get(name)
     if fn is None:
-        fn = _entries.setdefault(name, getattr(lib(), name))
+        fn = _entry(name)
     rc = fn(*args)
     if rc != 0:
         raise ZdmmvError(name, rc)
@@ -623,7 +628,7 @@ def _per_head(t: torch.Tensor, cache: KVCache, n: int, what: str) -> tuple[int, 
 
 
 def attn_weights_q4_0_workspace_bytes(cache: KVCache, n_q_heads: int, n_tok: int, max_q_len: int) -> int:
-    return int(lib().zdmmv_attn_weights_q4_0_workspace_bytes(cache.c, n_q_heads, n_tok, max_q_len))
+    return _entry("zdmmv_attn_weights_q4_0_workspace_bytes")(cache.c, n_q_heads, n_tok, max_q_len)
 
 
 def attn_weights_q4_0(cache: KVCache, q, q_start, kv_len, lse, max_q_len: int, max_kv_len: int, seen=None,
