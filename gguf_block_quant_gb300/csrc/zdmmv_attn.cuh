@@ -163,8 +163,9 @@ __device__ __forceinline__ uint32_t tree_bits(const AttnArgs &a, const AttnRange
 __device__ __forceinline__ int tree_low(const AttnArgs &a, const AttnRange &r, int i) {
     if (a.window == 0) return 0;
     const uint32_t *row = tree_row(a, r, i);
+    const int words = min(a.seen_words, (r.n + 31) / 32);
     int own = 0;
-    for (int k = 0; k < a.seen_words; ++k) own += __popc(tree_word(a, r, row, k));
+    for (int k = 0; k < words; ++k) own += __popc(tree_word(a, r, row, k));
     return max(0, r.len - r.n - max(0, a.window - own));
 }
 
