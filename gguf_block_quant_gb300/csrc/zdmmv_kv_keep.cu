@@ -25,6 +25,11 @@ struct KeepArgs {
     int32_t held;  // sums of a CTA that its shared memory holds, as keys
 };
 
+// Whether a sequence's length is none that a call takes.
+__device__ __forceinline__ bool keep_bad(const KeepArgs &a, int n) {
+    return n < 0 || n > a.max_kv_len || n > static_cast<int64_t>(a.from.max_pages) * a.from.page_tokens;
+}
+
 // A sum as a whole number that rises with it: -0 is 0, a NaN is below all.
 __device__ __forceinline__ uint32_t sum_key(float x) {
     if (x != x) x = -INFINITY;
@@ -65,11 +70,8 @@ template <bool CLUSTER> __global__ void __launch_bounds__(kPickThreads) kv_pick_
     const float *sums = a.sums + static_cast<int64_t>(item) * a.sums_stride;
     int32_t *index = a.index + static_cast<int64_t>(item) * a.budget;
     const int n = a.kv_len[seq];
-    const bool bad = n < 0 || n > a.max_kv_len || n > static_cast<int64_t>(a.from.max_pages) * a.from.page_tokens;
-    if (rank == 0 && tid == 0) {
-        if (bad && a.status) *a.status = 1;
-        if (a.len_out && a.by_heads.mod(item, seq) == 0) a.len_out[seq] = bad ? -1 : min(n, a.budget);
-    }
+    const bool bad = keep_bad(a, n);
+    if (bad && rank == 0 && tid == 0 && a.status) *a.status = 1;
     const int me = rank * kPickThreads + tid, all = ranks * kPickThreads;
     if (bad || n <= a.budget) {  // the whole cluster takes this way
         for (int j = me; j < a.budget; j += all) index[j] = !bad && j < n ? j : -1;
@@ -210,6 +212,11 @@ template <int NB> __global__ void __launch_bounds__(kGatherWarps * 32) kv_gather
     const int item = a.by_tiles.div(static_cast<int>(job)), tile = a.by_tiles.mod(static_cast<int>(job), item);
     const int seq = a.by_heads.div(item), kvh = a.by_heads.mod(item, seq);
     const int t0 = tile * kKvSlab;
+    // here, where one thread alone looks at a sequence's length any more: len_out may be kv_len
+    if (a.len_out && tile == 0 && kvh == 0 && lane == 0) {
+        const int n = a.kv_len[seq];
+        a.len_out[seq] = keep_bad(a, n) ? -1 : min(n, a.budget);
+    }
     // lanes 0 .. 15: where the tile's tokens are
     const uint8_t *src = nullptr;
     int r = 0;
@@ -398,6 +405,12 @@ template <int NB> __global__ void __launch_bounds__(kAcceptThreads) kv_accept_ke
     }
 }
 
+// Whether n ints at p and m at q share a byte (a null pointer has none).
+bool ints_overlap(const int32_t *p, int64_t n, const int32_t *q, int64_t m) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    return p && q && a < b + 4 * static_cast<uintptr_t>(m) && b < a + 4 * static_cast<uintptr_t>(n);
+}
+
 template <int NB> cudaError_t launch_gather(const KeepArgs &a, int64_t jobs, cudaStream_t st) {
     return launch_block_op(kv_gather_kernel<NB>, dim3(static_cast<unsigned>((jobs + kGatherWarps - 1) / kGatherWarps)), dim3(kGatherWarps * 32),
                            0, st, a, jobs);
@@ -466,6 +479,7 @@ zdmmv_status zdmmv_kv_evict_q4_0(const zdmmv_kv_cache *from, const zdmmv_kv_cach
         kv_misaligned(g.len_out, 4) || kv_misaligned(g.status_dev, 4))
         return ZDMMV_ERR_ALIGN;
     if (from->pages == to->pages && from->page_table == to->page_table) return ZDMMV_ERR_SHAPE;
+    if (g.len_out != g.kv_len && ints_overlap(g.len_out, from->n_seq, g.kv_len, from->n_seq)) return ZDMMV_ERR_SHAPE;
     a.by_heads = FastDiv::of(from->n_kv_heads);
     a.from_page_tiles = FastDiv::of(from->page_tokens / kKvSlab);
     a.to_page_tiles = FastDiv::of(to->page_tokens / kKvSlab);

@@ -667,7 +667,7 @@ def kv_evict_q4_0(cache: KVCache, to: KVCache, kv_len, sums, budget: int, max_kv
     """Keep `budget` tokens of each kv head of a longer sequence: the first `sinks`, the last `recent` and those with the
     largest sums (fp32 [n_seq][n_kv_heads][max_kv_len or more]), in their order in the pages of `to`, which are no pages
     of `cache`. Returns index, int32 [n_seq][n_kv_heads][budget]: the kept tokens' positions, -1 behind the last.
-    sums_out: the kept tokens' sums; len_out: int32 [n_seq], the new lengths."""
+    sums_out: the kept tokens' sums; len_out: int32 [n_seq], the new lengths (may be kv_len itself)."""
     n_seq, kv = cache.n_seq, cache.n_kv_heads
     if index is None:
         index = _make((n_seq, kv, budget), _I32, cache.pages.device, stream)

@@ -790,7 +790,8 @@ typedef struct {
                                 rising; -1 behind the last one */
     float *sums_out;         /* nullable; device fp32 [n_seq][n_kv_heads], sums_out_stride apart: the kept tokens'
                                 sums, 0 behind the last one up to budget; overlaps no input */
-    int32_t *len_out;        /* nullable; device int32 [n_seq]: min(kv_len, budget); -1 for a bad sequence */
+    int32_t *len_out;        /* nullable; device int32 [n_seq]: min(kv_len, budget); -1 for a bad sequence. May be
+                                kv_len itself, but overlaps it in no other way (ERR_SHAPE) */
     int32_t *status_dev;     /* nullable device int32: 1 is stored for a bad sequence or page */
     int64_t sums_stride;     /* floats between kv heads, >= max_kv_len */
     int64_t sums_out_stride; /* ... >= budget (ignored where sums_out is NULL) */
