@@ -513,6 +513,10 @@ zdmmv_status zdmmv_kv_accept_q4_0(const zdmmv_kv_cache *cache, const zdmmv_kv_ac
     if (kv_misaligned(g.base, 4) || kv_misaligned(g.path, 4) || kv_misaligned(g.n_path, 4) || kv_misaligned(g.len_out, 4) ||
         kv_misaligned(g.status_dev, 4) || kv_misaligned(g.sums, 4))
         return ZDMMV_ERR_ALIGN;
+    // a sequence's heads have a CTA each, which all read what the first one's would write over
+    if (ints_overlap(g.len_out, a.c.n_seq, g.base, a.c.n_seq) || ints_overlap(g.len_out, a.c.n_seq, g.n_path, a.c.n_seq) ||
+        ints_overlap(g.len_out, a.c.n_seq, g.path, static_cast<int64_t>(a.c.n_seq) * g.max_path))
+        return ZDMMV_ERR_SHAPE;
     a.by_heads = FastDiv::of(cache->n_kv_heads);
     a.by_page = FastDiv::of(cache->page_tokens);
     a.base = g.base; a.path = g.path; a.n_path = g.n_path; a.len_out = g.len_out; a.status = g.status_dev;

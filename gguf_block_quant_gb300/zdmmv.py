@@ -683,7 +683,7 @@ def kv_evict_q4_0(cache: KVCache, to: KVCache, kv_len, sums, budget: int, max_kv
 def kv_accept_q4_0(cache: KVCache, base, path, n_path, sums=None, len_out=None, status=None, stream=None):
     """The accepted path of a drafted tree: of the tokens behind the first base[s] of sequence s, number path[s][j] moves to
     position base[s] + j (j < n_path[s], path rising), and so do sums (fp32 [n_seq][n_kv_heads][tokens], nullable).
-    Returns len_out, int32 [n_seq]: the new lengths."""
+    Returns len_out, int32 [n_seq]: the new lengths (it may not be base: its old ones are read until the end)."""
     n_seq, shape = cache.n_seq, path.shape
     if len(shape) != 2 or shape[0] != n_seq:
         _bad("kv_accept_q4_0: path must be int32 [n_seq][max_path]")

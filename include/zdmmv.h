@@ -818,8 +818,8 @@ typedef struct {
     const int32_t *base;     /* device int32 [n_seq] */
     const int32_t *path;     /* device int32 [n_seq][max_path] */
     const int32_t *n_path;   /* device int32 [n_seq], 0 .. max_path: entries of path that count */
-    int32_t *len_out;        /* nullable; device int32 [n_seq]: base + n_path; -1 for a bad sequence. Neither base,
-                                path nor n_path */
+    int32_t *len_out;        /* nullable; device int32 [n_seq]: base + n_path; -1 for a bad sequence. Overlaps
+                                neither base, path nor n_path (ERR_SHAPE) */
     int32_t *status_dev;     /* nullable device int32: 1 is stored for a bad sequence */
     float *sums;             /* nullable; device fp32 [n_seq][n_kv_heads], sums_stride apart: the tokens' sums of
                                 attention weight, which move with them */

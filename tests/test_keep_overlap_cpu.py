@@ -6,7 +6,7 @@ import torch
 
 from tests.test_block_ops_cpu import FAKE, L, _cache  # noqa: F401
 from tests.test_gave_up_waits_cpu import block, source
-from tests.test_tree_cpu import _evict
+from tests.test_tree_cpu import _accept, _evict
 
 
 def _evict_call(L, **k):  # noqa: F811
@@ -37,3 +37,21 @@ def test_evict_writes_a_length_where_one_thread_alone_reads_it():
     own = block(move, move.index("if (a.len_out && tile == 0 && kvh == 0 && lane == 0)"))
     assert move.count("kv_len") == own.count("a.kv_len[seq]") == 1 and move.count("a.len_out[seq]") == own.count("a.len_out[seq]") == 1
     assert move.index("block_op_wait()") < move.index("a.kv_len[seq]") < move.index("a.len_out[seq]")
+
+
+def _accept_call(L, **k):  # noqa: F811
+    args = _accept(**{**dict(base=2 * FAKE, path=3 * FAKE, n_path=4 * FAKE, len_out=5 * FAKE, status_dev=6 * FAKE, sums=7 * FAKE), **k})
+    return L.zdmmv_kv_accept_q4_0(ctypes.byref(_cache()), ctypes.byref(args), None)
+
+
+@pytest.mark.parametrize("what, size", [(2 * FAKE, 8), (4 * FAKE, 8), (3 * FAKE, 2 * 8 * 4)])
+def test_accept_refuses_lengths_over_its_inputs(L, what, size):  # noqa: F811
+    """base, n_path (two sequences) and path (of eight places each), from the first byte to the last."""
+    for at in (what - 4, what, what + size - 4):
+        assert _accept_call(L, len_out=at) == 2
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="what is not refused would run")
+def test_accept_takes_lengths_beside_its_inputs(L):  # noqa: F811
+    for at in (None, 5 * FAKE, 2 * FAKE - 8, 2 * FAKE + 8, 3 * FAKE - 8, 3 * FAKE + 64, 4 * FAKE + 8):
+        assert _accept_call(L, len_out=at) not in (1, 2, 3)
