@@ -1,6 +1,6 @@
 // zdmmv_attn_weights.cu -- zdmmv_attn_weights_q4_0: what the query rows of a call give each cached token,
 //
-//   out_t = keep before_t + sum_c exp(scale (q_c . k_t) - lse_c)      over the columns c (query rows of the kv head) that see t,
+//   out_t = keep before_t + sum_c exp(min(0, scale (q_c . k_t) - lse_c))      over the columns c (query rows of the kv head) that see t,
 //
 // from the keys alone: half of the cache's bytes, and no product with V. A token belongs to one warp (or thread), which goes over
 // all columns in a fixed order: nothing is joined, no atomics on sums.
@@ -32,7 +32,11 @@ struct WeightArgs {
     float keep;
 };
 
-// How a column's product with a key becomes its weight, p = exp2(x * product + y), and which tokens it sees.
+// How a column's product with a key becomes its weight, p = exp2(min(0, x * product + y)), and which tokens it sees. The minimum
+// changes roundings alone while |lse| is small: a row's lse is no less than any of its scores. A large lse's own step is a part
+// of the exponent that counts (2^-24 of |lse|, four times over with the products by ln 2 and its inverse), and a score is off by up to 2^-19
+// of its size, here and in the kernel that made lse. From 2^20 on y is therefore raised by 2^-17 of what |y| has beyond that, more
+// than all of it together from 2^21 on: a token that has all of a row's weight then gets it, whichever way its score was rounded.
 struct Column {
     float x, y;
     int low, end;
@@ -45,6 +49,7 @@ __device__ __forceinline__ Column column_of(const WeightArgs &w, const AttnRange
     Column c;
     c.x = fmaxf(fabsf(a.scale_log2) * down, 1e-37f);
     c.y = -1.44269504088896340736f * lse;
+    c.y += fminf(fmaxf(0.0f, (fabsf(c.y) - 1048576.0f) * 0x1p-17f), 1e34f);  // what is no number or infinite stays so
     if (a.seen) {
         c.low = tree_low(a, r, i);
         c.end = r.len;
@@ -53,6 +58,11 @@ __device__ __forceinline__ Column column_of(const WeightArgs &w, const AttnRange
         c.low = a.window > 0 ? max(0, c.end - a.window) : 0;
     }
     return c;
+}
+__device__ __forceinline__ float weight_of(float e) {  // a key that is no number has a weight that is none
+    float x;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(x) : "f"(e), "f"(0.0f));
+    return exp2_approx(x);
 }
 __device__ __forceinline__ const float *column_lse(const WeightArgs &w, const AttnRange &r, int kvh, int col) {
     const int i = w.a.by_group.div(col);
@@ -281,7 +291,7 @@ template <int NB, bool ONE> __global__ void __launch_bounds__(kWeightThreads, kW
                 const bool masked = t0 < low_max || t0 + 2 * kKvSlab > end_min;
                 // ... of one column of a group of four
                 const auto weigh = [&](int s, int grp, const Column &c, float x0, float x1) {
-                    float p0 = exp2_approx(fmaf(x0, c.x, c.y)), p1 = exp2_approx(fmaf(x1, c.x, c.y));
+                    float p0 = weight_of(fmaf(x0, c.x, c.y)), p1 = weight_of(fmaf(x1, c.x, c.y));
                     if (masked) {
                         const int i = a.by_group.div(4 * grp + t), tok = t0 + kKvSlab * s + g;
                         const uint32_t bits = tree && i < r.n ? tree_bits(a, r, i, t0 + kKvSlab * s) : ~0u;
@@ -628,8 +638,8 @@ template <int NB> __global__ void __launch_bounds__(kWeightThreads, TallGeom<NB>
             const float4 e = exps[k];
             const float2 y = f2_parts(f2_fma(f2_mul(f2(__uint_as_float(s[k / 8][2 * k % 16]), __uint_as_float(s[k / 8][2 * k % 16 + 1])), unit2),
                                              f2(e.x, e.y), f2(e.z, e.w)));
-            s[k / 8][2 * k % 16] = __float_as_uint(exp2_approx(y.x));
-            s[k / 8][2 * k % 16 + 1] = __float_as_uint(exp2_approx(y.y));
+            s[k / 8][2 * k % 16] = __float_as_uint(weight_of(y.x));
+            s[k / 8][2 * k % 16 + 1] = __float_as_uint(weight_of(y.y));
         }
         if (masked) {
             const int2 *see = reinterpret_cast<const int2 *>(image + T::kSeeAt) + half * (kBlockCols / 2);

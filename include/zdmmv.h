@@ -734,7 +734,12 @@ zdmmv_status zdmmv_attn_tree_q4_0(const zdmmv_kv_cache *cache, const zdmmv_attn_
  * zdmmv_attn_q4_0, or that of `seen`), without the first part for the new tokens
  * themselves (t >= kv_len - n): what stood there was of tokens that are gone. lse
  * is what zdmmv_attn_tree_q4_0 wrote for the same rows, so a row's weights add up
- * to one. Pages of which no row sees a token are not looked at. Entries at and
+ * to one, and none is more: a positive exponent, which roundings alone bring about,
+ * counts as 0. From |lse| of 727000 on (2^20 as a power of two) score - lse, a
+ * difference of two fp32 numbers, says too little for a sum of one; the exponent is
+ * then taken at the upper end of its error, 2^-17 (|lse| - 727000) more: the token
+ * with all of a row's weight counts as 1, and so may others whose scores come that
+ * near to its. Pages of which no row sees a token are not looked at. Entries at and
  * past kv_len are left as they are. Sums and scores are fp32 (scores as
  * zdmmv_attn_q4_0 forms them; keep * before is one fma with the sum of the rest),
  * in an order that goes by the shapes and bounds of the call alone. */
