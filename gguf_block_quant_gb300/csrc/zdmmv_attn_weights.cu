@@ -494,19 +494,15 @@ template <int NB> __global__ void __launch_bounds__(kWeightThreads, TallGeom<NB>
     __shared__ __align__(8) uint64_t bar[kTallSlots + 3];  // by slot: its block of q has come; by block % 2: its products are done; all are
     __shared__ uint32_t sh_tm;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, half = warp >> 2;
+    block_op_wait();  // before any load: what an early start may look at of the kernels before weights_q_kernel is said nowhere
     block_op_release();
-    // until its wait below the kernel reads only what was there before weights_q_kernel, which began after all that was
-    // complete, and writes nothing but the status
     // the last tokens of the sequences, whose columns are masked, first
     const int back = w.by_items.div(blockIdx.x), item = w.by_items.mod(blockIdx.x, back), chunk = w.chunks - 1 - back;
     const int seq = a.by_heads.div(item), kvh = a.by_heads.mod(item, seq);
     const AttnRange r = attn_range<true>(a, seq, 0, kAllCols);
     const int first = chunk * kTallTokens, live = r.bad ? 0 : r.len - first;  // tokens from `live` on are none
     if (r.bad && tid == 0 && a.status) *a.status = 1;
-    if (live <= 0) {
-        block_op_wait();
-        return;
-    }
+    if (live <= 0) return;
     const int base = r.len - r.n, columns = r.n * a.group, blocks = (columns + kBlockCols - 1) / kBlockCols;
     const bool tree = a.seen != nullptr;
     const int row = (warp & 3) * 32 + lane, tok = first + row;  // this thread's token, with half of a block's columns
@@ -515,7 +511,6 @@ template <int NB> __global__ void __launch_bounds__(kWeightThreads, TallGeom<NB>
     const float earlier = had ? w.before[static_cast<int64_t>(item) * w.before_stride + tok] : 0.0f;
     constexpr int kSlabs = kTallTokens / kKvSlab;
     if (columns == 0 || chunk * kSlabs >= r.slab0 + r.slabs || (chunk + 1) * kSlabs <= r.slab0) {  // nobody sees them
-        block_op_wait();
         if (half == 0 && row < live) *out = had ? w.keep * earlier : 0.0f;
         return;
     }
@@ -601,7 +596,6 @@ template <int NB> __global__ void __launch_bounds__(kWeightThreads, TallGeom<NB>
     fence_proxy_async_smem();
     __syncthreads();
     tm_after_sync();
-    block_op_wait();
 
     const int64_t block0 = first_block(w, r, seq);
     const uint64_t policy = l2_evict_last_policy();
