@@ -44,8 +44,9 @@ struct Column {
 __device__ __forceinline__ Column column_of(const WeightArgs &w, const AttnRange &r, int kvh, int col, float lse, float down) {
     const AttnArgs &a = w.a;
     const int i = a.by_group.div(col);
-    // one that is none adds 2^-infinity, and where tokens are masked at all it sees none: a key may be no number
-    if (i >= r.n) return {0.0f, -INFINITY, 0, 0};
+    // one that is none adds 2^-infinity, and where tokens are masked at all it sees none: a key may be no number. (A product of
+    // -infinity is one here too.)
+    if (i >= r.n) return {1e-37f, -INFINITY, 0, 0};
     Column c;
     c.x = fmaxf(fabsf(a.scale_log2) * down, 1e-37f);
     c.y = -1.44269504088896340736f * lse;
@@ -243,7 +244,8 @@ template <int NB, bool ONE> __global__ void __launch_bounds__(kWeightThreads, kW
             const int col = 4 * grp + g / 2;
             const bool lead = t == 0 && (g & 1) == 0;
             const float lse = lead && col < columns ? *column_lse(w, r, kvh, col) : 0.0f;
-            load_q<NB>(a, r, kvh, col, t, v);
+            // a column that is none has another's q: its products with an infinite key are no NaN where that one's are none
+            load_q<NB>(a, r, kvh, col < columns ? col : 4 * grp, t, v);
 #pragma unroll
             for (int b = 0; b < NB; ++b)
 #pragma unroll

@@ -739,8 +739,10 @@ zdmmv_status zdmmv_attn_tree_q4_0(const zdmmv_kv_cache *cache, const zdmmv_attn_
  * difference of two fp32 numbers, says too little for a sum of one; the exponent is
  * then taken at the upper end of its error, 2^-17 (|lse| - 727000) more: the token
  * with all of a row's weight counts as 1, and so may others whose scores come that
- * near to its. Pages of which no row sees a token are not looked at. Entries at and
- * past kv_len are left as they are. Sums and scores are fp32 (scores as
+ * near to its. A seen key with an infinity or NaN in it has its scores' weights (0
+ * for one of -infinity) with up to 24 query rows a kv head, with more it may be NaN;
+ * the other tokens' weights are theirs alone. Pages of which no row sees a token are
+ * not looked at. Entries at and past kv_len are left as they are. Sums and scores are fp32 (scores as
  * zdmmv_attn_q4_0 forms them; keep * before is one fma with the sum of the rest),
  * in an order that goes by the shapes and bounds of the call alone. */
 typedef struct {
