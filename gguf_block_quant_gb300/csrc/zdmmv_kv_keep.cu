@@ -48,7 +48,7 @@ constexpr int kPickThreads = 1024, kPickWarps = kPickThreads / 32, kDigit = 2048
 // Tokens up to which a CTA more costs more than it saves, the cluster's barriers above all (8 kv heads, one, two, four and eight
 // CTAs each: 16000 tokens 12.3 12.9 13.5 17.0 us with the move of 256, 32000 17.5 15.2 14.6 17.5, 131072 132 60 22.2 20.9).
 constexpr int kPickEach = 20 * 1024;
-constexpr int kPickMost = 0x7fff0000;  // so that a warp's step past the last sum is a number too
+constexpr int kPickMost = 0x7fff0000;  // tokens, and places of index: so that a cluster's step past the last one is a number too
 constexpr int kPickHeld = 48 * 1024;   // most sums that a CTA holds; those beyond it are read again (65536 by one CTA 56 us, by two 20)
 
 template <bool CLUSTER> __global__ void __launch_bounds__(kPickThreads) kv_pick_kernel(KeepArgs a) {
@@ -470,7 +470,7 @@ zdmmv_status zdmmv_kv_evict_q4_0(const zdmmv_kv_cache *from, const zdmmv_kv_cach
     const int64_t items = static_cast<int64_t>(a.from.n_seq) * a.from.n_kv_heads;
     const int64_t tiles = (static_cast<int64_t>(g.budget) + kKvSlab - 1) / kKvSlab, jobs = items * tiles;
     if (from->n_seq != to->n_seq || from->n_kv_heads != to->n_kv_heads || from->head_dim != to->head_dim || g.max_kv_len < 0 ||
-        g.max_kv_len > kPickMost || g.budget < 1 || g.sinks < 0 || g.recent < 0 || static_cast<int64_t>(g.sinks) + g.recent > g.budget ||
+        g.max_kv_len > kPickMost || g.budget < 1 || g.budget > kPickMost || g.sinks < 0 || g.recent < 0 || static_cast<int64_t>(g.sinks) + g.recent > g.budget ||
         g.budget > static_cast<int64_t>(a.to.max_pages) * a.to.page_tokens || jobs > 0x7fffff00 || items * kPickCluster > 0x7fffff00)
         return ZDMMV_ERR_SHAPE;
     if (!g.kv_len || !g.sums || !g.index) return ZDMMV_ERR_NULL;

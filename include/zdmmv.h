@@ -803,7 +803,7 @@ typedef struct {
     int64_t sums_stride;     /* floats between kv heads, >= max_kv_len */
     int64_t sums_out_stride; /* ... >= budget (ignored where sums_out is NULL) */
     int32_t max_kv_len;      /* the longest kv_len (an upper bound will do), 0 .. 2^31 - 2^16 */
-    int32_t budget;          /* >= 1, at most what max_pages of `to` hold */
+    int32_t budget;          /* >= 1, at most what max_pages of `to` hold and 2^31 - 2^16 */
     int32_t sinks, recent;   /* >= 0, sinks + recent <= budget */
 } zdmmv_kv_evict_args;
 
