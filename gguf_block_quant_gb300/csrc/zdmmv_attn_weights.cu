@@ -34,9 +34,10 @@ struct WeightArgs {
 
 // How a column's product with a key becomes its weight, p = exp2(min(0, x * product + y)), and which tokens it sees. The minimum
 // changes roundings alone while |lse| is small: a row's lse is no less than any of its scores. A large lse's own step is a part
-// of the exponent that counts (2^-24 of |lse|, four times over with the products by ln 2 and its inverse), and a score is off by up to 2^-19
-// of its size, here and in the kernel that made lse. From 2^20 on y is therefore raised by 2^-17 of what |y| has beyond that, more
-// than all of it together from 2^21 on: a token that has all of a row's weight then gets it, whichever way its score was rounded.
+// of the exponent that counts (2^-24 of |lse|, four times over with the products by ln 2 and its inverse), and a score is off by up
+// to 2^-19 of its products' magnitudes, here and in the kernel that made lse. From 2^20 on y is therefore raised by 2^-17 of what
+// |y| has beyond that, from 2^21 on more than all of it together where the largest score's products hardly cancel (where they do, the
+// bound is far from what happens): a token that has all of a row's weight then gets it, whichever way its score was rounded.
 struct Column {
     float x, y;
     int low, end;

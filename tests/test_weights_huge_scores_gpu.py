@@ -10,6 +10,8 @@ import pytest
 import torch
 
 from gguf_block_quant_gb300 import zdmmv as Z
+from tests import block_ref as R
+from tests import tree_ref as T
 from tests.test_attention_huge_scores_gpu import put_k
 from tests.test_block_ops_gpu import dev, random_cache
 
@@ -89,3 +91,42 @@ def test_a_weight_is_one_at_most(dim, group, new):
     cache.pages.copy_(dev(pages))
     out = Z.attn_weights_q4_0(cache, q, starts, ld, torch.zeros_like(lse), new, n, seen=seen)
     assert torch.isnan(out[0, 0, 0]) and torch.isfinite(out[0, 1]).all() and not out[0, 0, 1:].any()
+
+
+@pytest.mark.parametrize("dim, group, new", FORMS)
+@pytest.mark.parametrize("size", [3e6, 3e7, 1e10, 1e30])
+def test_queries_along_a_key(dim, group, new, size):
+    """Random keys, each row's q along one that it sees: its products are positive, P within twice their sum. Where the raise is more than
+    both scores' 2^-19 P and lse's roundings, and the largest score is alone by more than all of these, its weight is the row's."""
+    rng = np.random.default_rng(dim + group)
+    heads, page, n = 2, 32, 150
+    cache, pages, table = random_cache(rng, [n], page, heads, dim)
+    masks = [T.tree_mask(new, rng)]
+    k, _ = R.values(pages, page, heads, dim)
+    keys = k[table[0][np.arange(n) // page], :, np.arange(n) % page]      # [token][head][dim]
+    q = np.zeros((new, heads, group, dim))
+    for i in range(new):
+        see = np.flatnonzero(T.visible(n, new, i, masks[0]))
+        for h in range(heads):
+            q[i, h] = size * keys[rng.choice(see, group), h]
+    q = q.reshape(new, heads * group, dim).astype(np.float32)
+    starts, ld, seen = dev(np.array([0, new], np.int32)), dev(np.array([n], np.int32)), dev(T.pack(masks, 1))
+    lse = torch.empty(new, heads * group, device="cuda")
+    Z.attn_tree_q4_0(cache, dev(q), starts, ld, new, n, seen=seen, lse=lse)
+    out = Z.attn_weights_q4_0(cache, dev(q), starts, ld, lse, new, n, seen=seen)[0].double().cpu().numpy()
+    assert Z.device_status() == 0
+    least, clear_rows = np.zeros((heads, n)), 0
+    for i in range(new):
+        see = T.visible(n, new, i, masks[0])
+        for c in range(heads * group):
+            h = c // group
+            score = np.where(see, keys[:, h] @ q[i, c].astype(np.float64), -np.inf) * dim ** -0.5 / np.log(2)
+            reach = (np.abs(keys[see, h]).reshape(-1, dim // 32, 32).max(-1) @ np.abs(q[i, c].astype(np.float64)).reshape(-1, 32).sum(-1)).max()
+            err = 2.0 ** -18 * reach * dim ** -0.5 / np.log(2) + 2.0 ** -21.9 * np.abs(score[see]).max()
+            best, raised = score.argmax(), 2.0 ** -17 * (score.max() - 2.0 ** 20)
+            others = np.delete(score, best).max()
+            if raised >= err and score.max() - others > err + raised + 160:   # 2^-160 is 0
+                least[h, best] += 1
+                clear_rows += 1
+    assert clear_rows > 0.1 * new * heads * group  # of the inputs alone: 4 of 30 to 2 of 2
+    assert np.all(out >= least) and np.all(out.sum(-1) >= least.sum(-1)) and np.all(out <= new * group)
