@@ -782,7 +782,7 @@ zdmmv_status zdmmv_attn_weights_q4_0(const zdmmv_kv_cache *cache, const zdmmv_at
     const int group = g.n_q_heads / cache->n_kv_heads;
     const int64_t columns = static_cast<int64_t>(std::min(g.max_q_len, std::max(1, g.n_tok))) * group;
     const int64_t items = static_cast<int64_t>(a.c.n_seq) * a.c.n_kv_heads;
-    // 128 tokens of a kv head are a step of the one kernel and a CTA of the other
+    // 128 tokens of a kv head are a CTA of the tall kernel; a step of the other is 256
     const int64_t steps = items * ((static_cast<int64_t>(g.max_kv_len) + kTallTokens - 1) / kTallTokens);
     if (columns > kAllCols || steps > 0x7fffff00 || items * ((columns + kBlockCols - 1) / kBlockCols) > 0x7fffff00) return ZDMMV_ERR_SHAPE;
     if (g.max_kv_len == 0) return ZDMMV_OK;

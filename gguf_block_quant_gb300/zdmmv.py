@@ -627,6 +627,9 @@ def _per_head(t: torch.Tensor, cache: KVCache, n: int, what: str) -> tuple[int, 
     return t.data_ptr(), s1
 
 
+_FEW_COLUMNS = 24  # rows times heads of a kv head up to which attn_weights_q4_0 needs no workspace (a call spared each step)
+
+
 def attn_weights_q4_0_workspace_bytes(cache: KVCache, n_q_heads: int, n_tok: int, max_q_len: int) -> int:
     return _entry("zdmmv_attn_weights_q4_0_workspace_bytes")(cache.c, n_q_heads, n_tok, max_q_len)
 
@@ -650,7 +653,7 @@ def attn_weights_q4_0(cache: KVCache, q, q_start, kv_len, lse, max_q_len: int, m
     pb, sb = (0, 0) if sums is None else _per_head(sums, cache, max_kv_len, "sums")
     ps, words = _seen(seen, n_tok)
     pw = nw = 0
-    if workspace is None and heads * min(n_tok, max_q_len) > 24 * cache.n_kv_heads:  # with fewer columns none is needed
+    if workspace is None and heads * min(n_tok, max_q_len) > _FEW_COLUMNS * cache.n_kv_heads:
         workspace = _make(attn_weights_q4_0_workspace_bytes(cache, heads, n_tok, max_q_len), _U8, q.device, stream)
     if workspace is not None:
         pw, nw = _whole(workspace, _U8, 0, "workspace"), workspace.numel()

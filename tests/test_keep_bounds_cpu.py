@@ -4,6 +4,7 @@ import ctypes
 import pytest
 import torch
 
+from gguf_block_quant_gb300 import zdmmv as Z
 from tests.test_block_ops_cpu import FAKE, L, _cache  # noqa: F401
 from tests.test_gave_up_waits_cpu import source
 from tests.test_tree_cpu import _evict
@@ -35,3 +36,11 @@ def test_the_largest_step():
     text = source("zdmmv_kv_keep.cu")
     value = lambda name: int(re.search(rf"\b{name} = (0x[0-9a-f]+|\d+)", text).group(1), 0)  # noqa: E731
     assert value("kPickMost") + value("kPickThreads") * value("kPickCluster") < 1 << 31
+
+
+def test_the_binding_makes_a_workspace_where_one_is_needed(L):  # noqa: F811
+    for kv, group, dim, n_tok, most in [(k, g, d, t, m) for k in (1, 2, 8) for g in (1, 3, 4, 8, 24, 25, 64) for d in (64, 128, 256)
+                                        for t in (0, 1, 5, 6, 24, 25, 100) for m in (1, 3, 6, 7, 24, 25, 200)]:
+        cache = _cache(n_kv_heads=kv, head_dim=dim)
+        need = L.zdmmv_attn_weights_q4_0_workspace_bytes(ctypes.byref(cache), kv * group, n_tok, most)
+        assert (need > 0) == (kv * group * min(n_tok, most) > Z._FEW_COLUMNS * kv), (kv, group, dim, n_tok, most)
