@@ -708,12 +708,14 @@ template <int NB> __global__ void __launch_bounds__(kWeightThreads, TallGeom<NB>
     }
 }
 
-// More columns than kBlockCols take the tall kernel, and more than kFewCols where all its CTAs run at once (a CTA's start, its
-// keys turned into operands, costs it as much as two blocks of columns): 8 heads of 128, 48 columns over 1000 tokens 7.1 us and
-// 10.8 with the other kernel, over 64000 67.0 and 49.7; 24 columns over 1000 7.1 and 7.3; 64 over 64000 67.1 and 62.8.
-constexpr int kFewCols = 24;
+// More columns than kBlockCols take the tall kernel, and more than kTallFrom where all its CTAs run at once (its second launch, and
+// a CTA's start, cost it as much as eight groups of four columns): 8 heads of 128 over 1000 tokens, tall and few, 28 columns 8.8 us and 7.9,
+// 32 8.9 and 8.4, 36 8.9 and 9.5, 48 8.6 and 11.0, and over 64000 48 columns 67.0 and 49.7, 64 67.1 and 62.8; of 192 dimensions 28
+// columns 10.2 and 9.5, 36 10.2 and 11.7; of 256, where the other kernel has one CTA an SM, 28 11.2 and 12.4.
+constexpr int kFewCols = 24;  // up to which no rule takes the tall kernel: no workspace
+template <int NB> constexpr int kTallFrom = NB < 8 ? 32 : kFewCols;
 template <int NB> bool weights_tall(int64_t columns, int64_t items, int64_t max_kv_len, int sms) {
-    return columns > kBlockCols || (columns > kFewCols && items * ((max_kv_len + kTallTokens - 1) / kTallTokens) <= TallGeom<NB>::kCtas * sms);
+    return columns > kBlockCols || (columns > kTallFrom<NB> && items * ((max_kv_len + kTallTokens - 1) / kTallTokens) <= TallGeom<NB>::kCtas * sms);
 }
 size_t weights_bytes(int head_dim, int n_seq, int n_kv_heads, int group, int n_tok, int max_q_len) {
     if (static_cast<int64_t>(std::min(max_q_len, n_tok)) * group <= kFewCols) return 0;
