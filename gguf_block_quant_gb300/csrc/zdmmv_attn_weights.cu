@@ -107,12 +107,15 @@ template <int N> __device__ __forceinline__ void cp_async_wait() { asm volatile(
 // The scores are formed as in the narrow kernel of zdmmv_attn.cuh (A = a tile's 16 tokens of codes, B = four columns' upper and
 // lower parts; a product's C holds a column's two sums side by side), so that they agree with those that lse was made of. The
 // steps (16 tiles, a pair for each warp) of all kv heads of all sequences one after another are a row, of which every CTA of a
-// grid that fills the device takes an equal stretch, whatever the lengths. A warp keeps the next pairs' keys, and their tokens'
+// grid that fills the device (two an SM; heads past 128 dimensions mostly have room for one, and the stretches then run in two rounds) takes
+// an equal stretch, whatever the lengths. A warp keeps the next pairs' keys, and their tokens'
 // earlier sums, on their way into its own ring in shared memory; a pair's 32 sums end up one in each lane.
 // ONE: up to four columns, whose parts of q stay in registers.
-// One token of 32 heads over 130975 tokens of 8 kv heads of 128: 19.7 us, 4.3 TB/s, 64% of the copy rate; 48 sequences of up to
-// 16384 44.6 us, 3.8 TB/s. Bound by issue (58% active; 205 instructions a tile, 72 of them the codes' conversion) and the start:
-// lengths, pages, the first keys and q are four latencies one after another, of some 4 us. Measured, over 130975: loads a tile
+// One token of 32 heads over 130975 tokens of 8 kv heads of 128: 20.0 us, 4.2 TB/s, 63% of the copy rate; 48 sequences of up to
+// 16384 45.6 us, 3.8 TB/s. Four warps a scheduler keep 57% of the issue slots busy (207 instructions a tile, 72 of them the codes'
+// conversion, two the weight's bound), and the start, lengths, pages, the first keys and q, is four latencies one after another, of some 4 us;
+// of several sequences each kv head is such a start, as the rings run empty there. Over 131072 tokens of heads of 256 41.5 us,
+// one CTA an SM. Measured, over 130975, against 19.7 before the bound: loads a tile
 // ahead into registers, the earlier sums read where they are used, 33.2; rings of four single tiles 28.8; three CTAs an SM, with
 // 80 registers a thread, 21.6; four places a ring 19.8 (and 45.2), five 20.1; q asked for before the pages, which it costs spills, 32.6.
 constexpr int kWeightStages = 3;
@@ -375,14 +378,15 @@ template <int NB, bool ONE> __global__ void __launch_bounds__(kWeightThreads, kW
 //    128 bytes), each in two fp16 parts (k exactly, q to 22 bits; zdmmv_attn_prompt.cuh): 3 D/16 products a block.
 //  * Every CTA of a kv head needs all of its q: weights_q_kernel makes the operands (and what each column needs to become a
 //    weight) once, in the workspace, as they lie in shared memory, and the CTAs bring them with one bulk copy a block, two
-//    blocks ahead. (Each CTA turning q into operands by itself: 141 us where this takes 46, 700 of 1000 instructions a block.)
+//    blocks ahead. (Each CTA turning q into operands by itself: 141 us where this took 46, 700 of 1000 instructions a block.)
 //  * One lane starts a block's products while all threads take the weights of the block before; D is double. Two CTAs an SM
 //    (heads of up to 128 dimensions) fill each other's gaps.
 // Where a token has a scale of 2^13 or more, the 128 tokens' operand is in units of 16, as there.
-// 256 tokens of 32 heads over 8192 of 8 kv heads of 128 (1024 columns, 512 CTAs): 46.1 us, the tensor cores 45% busy, of which
-// weights_q_kernel and the start take 4. A block's 24 products are 816 cycles; two CTAs' blocks take 2200, as the next block's
-// products wait for the weights of the one before (D is double, not triple), and 512 CTAs are 1.7 rounds of 304 places. On
-// mma.sync 199 us.
+// 256 tokens of 32 heads over 8192 of 8 kv heads of 128 (1024 columns, 512 CTAs): 49.1 us, the tensor cores 44% busy, of which
+// weights_q_kernel and the start take 6 (4 with lengths, pages and keys loaded before the wait for that kernel, where nothing says that
+// what the kernels before it wrote can be seen), the weights' bound 1. A block's 24 products are 816 cycles; two CTAs' blocks take 2200
+// and more, as the next block's products wait for the weights of the one before (D is double, not triple), and 512 CTAs are 1.7 rounds of
+// 304 places. On mma.sync 199 us.
 constexpr int kTallTokens = 128, kTallSlots = 3;
 template <int NB> struct TallGeom {
     static constexpr int kDim = NB * kQK, kChunks = (NB + 1) / 2;  // of 64 dimensions

@@ -42,7 +42,7 @@ __device__ __forceinline__ uint32_t sum_key(float x) {
 // first and the latest ones, whose sums it reads once into shared memory. The smallest sum that stays is found digit by digit,
 // 11 bits at a time from the top: every CTA counts its sums by digit, and adds up the cluster's counts. Then each CTA knows how
 // many tokens stay before its own, and writes its own in their order: of sums equal to the smallest, the first ones.
-// 32 kv heads of up to 65536 tokens: 16 to 20 us, of which the sums' loads take 3, each of the two or three counts 3 (its additions in
+// 32 kv heads of up to 65536 tokens: 16 to 19 us, of which the sums' loads take 3, each of the two or three counts 3 (its additions in
 // shared memory, the cluster's barrier, the reading of four CTAs' counts), the rising places 3. Bound by these steps' latencies.
 constexpr int kPickThreads = 1024, kPickWarps = kPickThreads / 32, kDigit = 2048, kPickCluster = 8;
 // Tokens up to which a CTA more costs more than it saves, the cluster's barriers above all (8 kv heads, one, two, four and eight
